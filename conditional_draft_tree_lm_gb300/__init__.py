@@ -9,3 +9,11 @@ from .dtree import (  # noqa: F401
     status_string,
     workspace_bytes,
 )
+from .kvcache import (  # noqa: F401
+    AttentionWorkspace,
+    KvCache,
+    cache_attention,
+    kv_append,
+    kv_plan,
+    prompt_attention,
+)

@@ -1,0 +1,65 @@
+// Shared by the kernels around the target model's key/value cache: argument
+// checks, the smallest power-of-two scale, e4m3 conversions.
+#pragma once
+
+#include <cstdarg>
+#include <cstdio>
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace dt {
+
+// Largest finite e4m3 magnitude: 1.75 * 2^8.
+constexpr float kE4m3Max = 448.0f;
+
+// Smallest power of two s in [2^-126, 2^120] with 448 s >= amax (amax finite,
+// >= 0).  448 = 1.75 * 2^8, so with amax = m 2^k (1 <= m < 2) s is 2^(k-8)
+// where m <= 1.75 and 2^(k-7) above: read off the bits, no logarithm.
+DT_DEVINL float kv_pow2_scale(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  int e = static_cast<int>(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  e = e < -126 ? -126 : (e > 120 ? 120 : e);
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Two e4m3 bytes (low byte first) to fp16, exact.
+DT_DEVINL uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+
+inline dt_status kv_fail(dt_status s, const char* fmt, ...) {
+  char msg[240];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(msg, sizeof(msg), fmt, ap);
+  va_end(ap);
+  set_last_error(msg);
+  return s;
+}
+
+inline dt_status kv_launched(const char* who, cudaError_t e) {
+  if (e == cudaSuccess) return DT_OK;
+  return kv_fail(DT_ERR_CUDA, "%s: launch failed: %s (%d)", who, cudaGetErrorString(e), static_cast<int>(e));
+}
+
+inline bool kv_page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+// Rows of heads: 16-byte aligned base, strides that keep every head 16-byte aligned.
+inline bool kv_rows_ok(const void* p, int64_t row_stride, int64_t head_stride) {
+  return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && row_stride >= 0 && head_stride >= 0 &&
+         row_stride % 8 == 0 && head_stride % 8 == 0;
+}
+
+dt_status kv_check_cache(const char* who, const dt_kv_cache* c);
+
+// SM count of the current device, and one-time raising of a kernel's dynamic
+// shared-memory limit per device.
+cudaError_t kv_num_sms(int* n);
+
+}  // namespace dt

@@ -1,0 +1,209 @@
+// dt_kv_append: bf16 keys and values of new tokens into the 8-bit cache.
+//
+// Per page touched, head and tensor ("run": the new tokens that go to one page):
+//   need  = smallest power of two with 448 need >= max |x| over the run's finite x
+//   scale' = need at a page's start, else max(scale, need)
+//   earlier codes of the page -> RNE(code * scale / scale') where scale' > scale
+//   new codes = RNE(x / scale')
+// Powers of two make x / scale' exact, so that each value is rounded once, and
+// move earlier codes without rounding until they become subnormal.
+//
+// What bounds it: bytes (4 read and 2 written per channel pair), or latency for
+// a few tokens.  A run belongs to one CTA, whose threads hold all of it in
+// registers (16-byte loads), so that it is read once: amax first, codes from the
+// same registers.  Runs are found from the slot map itself: a row leads a run
+// unless its slot is the previous row's plus one inside the same page, so no
+// list of pages is needed and no CTA waits for another.
+#include "kv.cuh"
+
+namespace dt {
+namespace {
+
+constexpr int kAppendThreads = 128;
+
+struct AppendParams {
+  const __nv_bfloat16* x[2];
+  int64_t row_stride[2], head_stride[2];
+  uint8_t* codes[2];
+  float* scale[2];
+  const int64_t* slot_map;
+  const int32_t* src_rows;
+  int* status;
+  int64_t n_rows, n_src, n_slots;
+  int n_kv, shift, window;
+};
+
+// Two bf16 in a word, as fp32.
+DT_DEVINL float2 bf16x2_f32(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+DT_DEVINL float finite_or(float x, float other) { return fabsf(x) <= 3.402823466e38f ? x : other; }
+
+// NV: 16-byte vectors per thread of a full page (page * HD / 8 / threads, at least 1).
+template <int HD, int NV>
+__global__ void __launch_bounds__(kAppendThreads) k_kv_append(const AppendParams p) {
+  constexpr int kVecs = HD / 8;  // vectors per row
+  __shared__ float warp_max_s[kAppendThreads / 32];
+  __shared__ int run_len_s;
+  const int tid = threadIdx.x, head = blockIdx.y, which = blockIdx.z;
+  const int page = 1 << p.shift;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.window;
+  const int64_t t1 = t0 + p.window < p.n_rows ? t0 + p.window : p.n_rows;
+
+  for (int64_t t = t0; t < t1;) {
+    const int64_t slot = p.slot_map[t];
+    const int64_t before = t > 0 ? p.slot_map[t - 1] : -1;
+    const int off = static_cast<int>(slot & (page - 1));
+    if (slot < 0 || slot >= p.n_slots) {
+      if (slot >= 0 && p.status && tid == 0) atomicOr(p.status, DT_KV_BAD_INDEX);
+      ++t;
+      continue;
+    }
+    if (before >= 0 && before + 1 == slot && off != 0) {  // inside a run that starts before this window
+      ++t;
+      continue;
+    }
+    // the run: rows whose slots count up inside the page
+    __syncthreads();
+    if (tid == 0) run_len_s = page - off;
+    __syncthreads();
+    if (tid < page - off && (t + tid >= p.n_rows || p.slot_map[t + tid] != slot + tid)) atomicMin(&run_len_s, tid);
+    __syncthreads();
+    const int len = run_len_s;
+
+    uint4 v[NV];
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int at = tid + i * kAppendThreads, r = at / kVecs, c = (at % kVecs) * 8;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (r < len) {
+        const int64_t src = p.src_rows ? p.src_rows[t + r] : t + r;
+        if (src >= 0 && src < p.n_src)
+          v[i] = __ldg(reinterpret_cast<const uint4*>(p.x[which] + src * p.row_stride[which] +
+                                                      head * p.head_stride[which] + c));
+        else if (p.status)
+          atomicOr(p.status, DT_KV_BAD_INDEX);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = bf16x2_f32(w[k]);
+        amax = fmaxf(amax, fmaxf(fabsf(finite_or(f.x, 0.0f)), fabsf(finite_or(f.y, 0.0f))));
+      }
+    }
+    const int64_t tile = (slot >> p.shift) * p.n_kv + head;  // the page's part of this head
+    float* scale_at = p.scale[which] + tile;
+    const float old = off > 0 ? *scale_at : 0.0f;  // (read by all before thread 0 may write it)
+    amax = warp_max(amax);
+    if ((tid & 31) == 0) warp_max_s[tid >> 5] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, warp_max_s[w]);
+
+    uint8_t* codes = p.codes[which] + tile * page * HD;
+    const float need = kv_pow2_scale(amax);
+    const float now = off > 0 && old > need ? old : need;
+    if (off > 0 && now > old) {
+      const float ratio = old / now;
+      for (int i = tid; i < off * kVecs; i += kAppendThreads) {
+        uint2* at = reinterpret_cast<uint2*>(codes + static_cast<size_t>(i) * 8);
+        const uint2 c = *at;
+        uint32_t r[2];
+        const uint32_t in[2] = {c.x, c.y};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t lo = e4m3x2_to_f16x2(in[k] & 0xFFFFu), hi = e4m3x2_to_f16x2(in[k] >> 16);
+          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+          const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+          r[k] = __nv_cvt_float2_to_fp8x2(make_float2(a.x * ratio, a.y * ratio), __NV_SATFINITE, __NV_E4M3) |
+                 static_cast<uint32_t>(
+                     __nv_cvt_float2_to_fp8x2(make_float2(b.x * ratio, b.y * ratio), __NV_SATFINITE, __NV_E4M3))
+                     << 16;
+        }
+        *at = make_uint2(r[0], r[1]);
+      }
+    }
+    // (1 / now is exact for a power of two; a scale that a caller set otherwise is divided by)
+    const float nan = __uint_as_float(0x7FC00000u);
+    const bool pow2 = (__float_as_uint(now) & 0x7FFFFFu) == 0;
+    const float inv = 1.0f / now;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int at = tid + i * kAppendThreads, r = at / kVecs, c = (at % kVecs) * 8;
+      if (r >= len) continue;
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t o[2] = {0, 0};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float2 f = bf16x2_f32(w[k]);
+        f.x = finite_or(f.x, nan);
+        f.y = finite_or(f.y, nan);
+        f = pow2 ? make_float2(f.x * inv, f.y * inv) : make_float2(f.x / now, f.y / now);
+        o[k >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3)) << ((k & 1) * 16);
+      }
+      *reinterpret_cast<uint2*>(codes + static_cast<size_t>(off + r) * HD + c) = make_uint2(o[0], o[1]);
+    }
+    if (tid == 0 && now != old) *scale_at = now;
+    t += len;
+  }
+}
+
+template <int HD>
+cudaError_t launch(const AppendParams& p, dim3 grid, cudaStream_t st) {
+  switch ((1 << p.shift) * HD / 8 / kAppendThreads) {
+    case 1: k_kv_append<HD, 1><<<grid, kAppendThreads, 0, st>>>(p); break;
+    case 2: k_kv_append<HD, 2><<<grid, kAppendThreads, 0, st>>>(p); break;
+    case 4: k_kv_append<HD, 4><<<grid, kAppendThreads, 0, st>>>(p); break;
+    case 8: k_kv_append<HD, 8><<<grid, kAppendThreads, 0, st>>>(p); break;
+    default: k_kv_append<HD, 16><<<grid, kAppendThreads, 0, st>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace dt
+
+extern "C" dt_status dt_kv_append(const dt_kv_cache* cache, const dt_kv_append_args* args, void* stream) {
+  using namespace dt;
+  const char* who = "dt_kv_append";
+  if (dt_status s = kv_check_cache(who, cache)) return s;
+  if (!args) return kv_fail(DT_ERR_INVALID_ARG, "%s: null arguments", who);
+  const dt_kv_append_args& a = *args;
+  if (a.n_rows < 0 || a.n_src < 0) return kv_fail(DT_ERR_INVALID_ARG, "%s: a negative row count", who);
+  if (a.n_rows > 0x7FFFFFFF) return kv_fail(DT_ERR_SHAPE, "%s: n_rows above 2^31-1", who);
+  if (cache->n_kv > 65535) return kv_fail(DT_ERR_SHAPE, "%s: n_kv above 65535", who);
+  if (a.n_rows == 0) return DT_OK;
+  if (!a.slot_map || !kv_rows_ok(a.k, a.k_row_stride, a.k_head_stride) || !kv_rows_ok(a.v, a.v_row_stride, a.v_head_stride))
+    return kv_fail(DT_ERR_INVALID_ARG, "%s: null or misaligned k, v or slot_map", who);
+  AppendParams p = {};
+  p.x[0] = static_cast<const __nv_bfloat16*>(a.k);
+  p.x[1] = static_cast<const __nv_bfloat16*>(a.v);
+  p.row_stride[0] = a.k_row_stride;
+  p.row_stride[1] = a.v_row_stride;
+  p.head_stride[0] = a.k_head_stride;
+  p.head_stride[1] = a.v_head_stride;
+  p.codes[0] = static_cast<uint8_t*>(cache->k);
+  p.codes[1] = static_cast<uint8_t*>(cache->v);
+  p.scale[0] = cache->k_scale;
+  p.scale[1] = cache->v_scale;
+  p.slot_map = a.slot_map;
+  p.src_rows = a.src_rows;
+  p.status = a.status;
+  p.n_rows = a.n_rows;
+  p.n_src = a.n_src;
+  p.n_kv = cache->n_kv;
+  while ((16 << p.shift) < cache->page) ++p.shift;
+  p.shift += 4;
+  p.n_slots = static_cast<int64_t>(cache->n_pages) << p.shift;
+  // Rows a CTA looks for runs in: one while the CTAs still fit the GPU a few times over
+  // (each row may be a run of its own, a token per request), up to a page for long prompts.
+  p.window = 1;
+  while (p.window < cache->page && (a.n_rows / p.window) * cache->n_kv * 2 > 16384) p.window *= 2;
+  const dim3 grid(static_cast<unsigned>((a.n_rows + p.window - 1) / p.window), static_cast<unsigned>(cache->n_kv), 2);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return kv_launched(who, cache->head_dim == 64 ? launch<64>(p, grid, st) : launch<128>(p, grid, st));
+}

@@ -1,0 +1,218 @@
+// dt_kv_plan: block tables and slot maps from request lengths.
+//
+// new = max(old + delta + extra, 0), blocks(x) = ceil(x / page); per request the
+// rows it adds, the pages it takes and the pages it gives back; their exclusive
+// sums over the requests say which page of the ring a block gets and where a
+// request's rows and returned pages go.  Everything after the sums is
+// independent per row and per page.
+//
+// What bounds it: latency at serving sizes (a few hundred rows), the row
+// arrays' writes (16 bytes a row) for prompts.  So it is one launch without any
+// exchange between CTAs: every CTA reads all lengths (8 bytes a request, at most
+// 32 KB, from L2) and forms the sums for itself in shared memory, then takes its
+// share of rows and of requests.  The ring makes that safe: pages leave at its
+// head and come back behind its last one, places that no CTA reads in this call,
+// and blocks that a request gains are found from the sums, not from table
+// entries that another CTA writes.
+#include "kv.cuh"
+
+namespace dt {
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanMaxReq = 4096;
+
+struct PlanReq {  // one request's place in the sums
+  int row, take, give, old, fresh;  // fresh: new length
+};
+
+// Exclusive sums over the block of three 64-bit counts; totals in tot.
+DT_DEVINL void block_scan3(int64_t (&v)[3], int64_t (*warp_tot)[3], int64_t (&tot)[3]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t own[3] = {v[0], v[1], v[2]};
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int64_t w = __shfl_up_sync(0xFFFFFFFFu, v[k], o);
+      if (lane >= o) v[k] += w;
+    }
+  }
+  if (lane == 31) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) warp_tot[warp][k] = v[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      const int64_t x = warp_tot[w][k];
+      before += w < warp ? x : 0;
+      all += x;
+    }
+    v[k] += before - own[k];
+    tot[k] = all;
+  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const dt_kv_plan_args a, int shift) {
+  extern __shared__ PlanReq req[];  // [n_req + 1]
+  __shared__ int64_t warp_tot[kPlanThreads / 32][3];
+  __shared__ int faults;
+  const int n = a.n_req, tid = threadIdx.x;
+  if (tid == 0) faults = 0;
+  const int head = a.ring_in[0], count = a.ring_in[1];
+  __syncthreads();
+
+  // each thread sums a stretch of requests; the block scan places the stretches
+  const int per = (n + kPlanThreads - 1) / kPlanThreads;
+  const int q0 = min(n, tid * per), q1 = min(n, q0 + per);
+  int64_t v[3] = {0, 0, 0}, tot[3];
+  int bad = 0;
+  for (int q = q0; q < q1; ++q) {
+    const int old = a.len_old[q];
+    int64_t fresh = static_cast<int64_t>(old) + (a.delta ? a.delta[q] : 0) + a.extra;
+    fresh = fresh < 0 ? 0 : fresh;
+    const int64_t b_old = (static_cast<int64_t>(old) + a.page - 1) >> shift, b_new = (fresh + a.page - 1) >> shift;
+    if (old < 0 || b_old > a.max_blocks || b_new > a.max_blocks || fresh > 0x7FFFFFFF) {
+      bad |= DT_KV_BAD_LENGTH;
+      continue;
+    }
+    const int64_t rows = fresh > old ? fresh - old : 0;
+    if (a.path && rows > 0) {
+      if (rows - 1 > a.path_len) {
+        bad |= DT_KV_BAD_PATH;
+      } else {
+        for (int j = 0; j < rows - 1; ++j) {
+          const int s = a.path[static_cast<size_t>(q) * a.path_len + j];
+          if (s < 0 || s >= a.path_rows) bad |= DT_KV_BAD_PATH;
+        }
+      }
+    }
+    v[0] += rows;
+    v[1] += b_new > b_old ? b_new - b_old : 0;
+    v[2] += b_old > b_new ? b_old - b_new : 0;
+  }
+  block_scan3(v, warp_tot, tot);
+  if (tot[0] > a.max_rows) bad |= DT_KV_SHORT_OF_ROWS;
+  if (tot[1] > count || count < 0 || count > a.n_pages || head < 0 || head >= a.n_pages) bad |= DT_KV_SHORT_OF_PAGES;
+  if (tot[2] > a.n_pages - count) bad |= DT_KV_BAD_INDEX;  // more given back than can be in use
+  if (bad) atomicOr(&faults, bad);
+  __syncthreads();
+  const bool ok = faults == 0;
+  // (offsets fit 32 bits where the call goes ahead: rows <= max_rows, pages <= n_pages)
+  for (int q = q0; q < q1; ++q) {
+    const int old = a.len_old[q];
+    int64_t fresh = static_cast<int64_t>(old) + (a.delta ? a.delta[q] : 0) + a.extra;
+    fresh = ok ? (fresh < 0 ? 0 : fresh) : old;
+    PlanReq r;
+    r.row = ok ? static_cast<int>(v[0]) : 0;
+    r.take = static_cast<int>(v[1]);
+    r.give = static_cast<int>(v[2]);
+    r.old = old;
+    r.fresh = static_cast<int>(fresh);
+    req[q] = r;
+    if (ok) {
+      const int64_t b_old = (static_cast<int64_t>(old) + a.page - 1) >> shift, b_new = (fresh + a.page - 1) >> shift;
+      v[0] += fresh > old ? fresh - old : 0;
+      v[1] += b_new > b_old ? b_new - b_old : 0;
+      v[2] += b_old > b_new ? b_old - b_new : 0;
+    }
+  }
+  if (tid == 0) req[n].row = ok ? static_cast<int>(tot[0]) : 0;
+  __syncthreads();
+
+  if (blockIdx.x == 0) {
+    for (int q = tid; q <= n; q += kPlanThreads) {
+      a.row_start[q] = req[q].row;
+      if (q < n) a.len_new[q] = req[q].fresh;
+    }
+    if (tid == 0) {
+      a.ring_out[0] = ok ? static_cast<int>((static_cast<int64_t>(head) + tot[1]) % a.n_pages) : head;
+      a.ring_out[1] = ok ? static_cast<int>(count - tot[1] + tot[2]) : count;
+      *a.status = faults;
+    }
+  }
+
+  // pages: a warp per request, a lane per block that comes or goes
+  if (ok) {
+    const int lane = tid & 31;
+    const int warps = gridDim.x * (kPlanThreads / 32);
+    for (int q = blockIdx.x * (kPlanThreads / 32) + (tid >> 5); q < n; q += warps) {
+      const PlanReq r = req[q];
+      const int b_old = static_cast<int>((static_cast<int64_t>(r.old) + a.page - 1) >> shift);
+      const int b_new = static_cast<int>((static_cast<int64_t>(r.fresh) + a.page - 1) >> shift);
+      int32_t* table = a.block_table + static_cast<size_t>(q) * a.max_blocks;
+      for (int b = b_old + lane; b < b_new; b += 32)
+        table[b] = a.free_pages[(static_cast<int64_t>(head) + r.take + (b - b_old)) % a.n_pages];
+      for (int b = b_new + lane; b < b_old; b += 32)
+        a.free_pages[(static_cast<int64_t>(head) + count + r.give + (b - b_new)) % a.n_pages] = table[b];
+    }
+  }
+
+  // rows
+  const int total = req[n].row;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid; t < a.max_rows;
+       t += static_cast<int64_t>(gridDim.x) * kPlanThreads) {
+    int64_t slot = -1;
+    int pos = -1, src = -1;
+    if (t < total) {
+      int lo = 0, hi = n;  // the last request whose first row is <= t (and that has rows)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (req[mid].row <= t) lo = mid; else hi = mid;
+      }
+      const PlanReq r = req[lo];
+      const int j = static_cast<int>(t) - r.row;
+      pos = r.old + j;
+      const int b = pos >> shift;
+      const int b_old = static_cast<int>((static_cast<int64_t>(r.old) + a.page - 1) >> shift);
+      const int page = b >= b_old ? a.free_pages[(static_cast<int64_t>(head) + r.take + (b - b_old)) % a.n_pages]
+                                  : a.block_table[static_cast<size_t>(lo) * a.max_blocks + b];
+      slot = (static_cast<int64_t>(page) << shift) + (pos & (a.page - 1));
+      if (a.src_rows)
+        src = a.path ? lo * a.path_rows + (j == 0 ? 0 : a.path[static_cast<size_t>(lo) * a.path_len + j - 1])
+                     : static_cast<int>(t);
+    }
+    a.slot_map[t] = slot;
+    if (a.positions) a.positions[t] = pos;
+    if (a.src_rows) a.src_rows[t] = src;
+  }
+}
+
+}  // namespace
+}  // namespace dt
+
+extern "C" dt_status dt_kv_plan(const dt_kv_plan_args* args, void* stream) {
+  using namespace dt;
+  const char* who = "dt_kv_plan";
+  if (!args) return kv_fail(DT_ERR_INVALID_ARG, "%s: null arguments", who);
+  const dt_kv_plan_args& a = *args;
+  if (!a.len_old || !a.ring_in || !a.block_table || !a.free_pages || !a.len_new || !a.ring_out || !a.row_start ||
+      !a.slot_map || !a.status)
+    return kv_fail(DT_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (a.len_new == a.len_old || a.ring_out == a.ring_in)
+    return kv_fail(DT_ERR_INVALID_ARG, "%s: len_new and ring_out must not be the inputs", who);
+  if (!kv_page_ok(a.page)) return kv_fail(DT_ERR_SHAPE, "%s: page %d is not 16, 32, 64 or 128", who, a.page);
+  if (a.n_req < 1 || a.max_blocks < 1 || a.n_pages < 1 || a.max_rows < 1)
+    return kv_fail(DT_ERR_INVALID_ARG, "%s: need n_req, max_blocks, n_pages, max_rows >= 1", who);
+  if (a.n_req > kPlanMaxReq) return kv_fail(DT_ERR_SHAPE, "%s: %d requests, at most %d", who, a.n_req, kPlanMaxReq);
+  if (a.max_rows > 0x7FFFFFFF) return kv_fail(DT_ERR_SHAPE, "%s: max_rows above 2^31-1", who);
+  if (a.path && (!a.src_rows || a.path_len < 0 || a.path_rows < 1 ||
+                 static_cast<int64_t>(a.n_req) * a.path_rows > 0x7FFFFFFF))
+    return kv_fail(DT_ERR_INVALID_ARG, "%s: a path needs src_rows, path_len >= 0 and path_rows >= 1", who);
+  int sms = 0;
+  cudaError_t e = kv_num_sms(&sms);
+  const size_t smem = (a.n_req + 1) * sizeof(PlanReq);
+  if (e == cudaSuccess && smem > 46 * 1024)
+    e = cudaFuncSetAttribute(k_kv_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return kv_launched(who, e);
+  int shift = 4;
+  while ((1 << shift) < a.page) ++shift;
+  // four rows a thread, so that the sums are formed by few CTAs, up to one CTA per SM
+  int64_t grid = (a.max_rows + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  grid = grid > sms ? sms : grid;
+  k_kv_plan<<<static_cast<int>(grid), kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(a, shift);
+  return kv_launched(who, cudaGetLastError());
+}

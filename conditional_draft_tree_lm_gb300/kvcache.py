@@ -1,0 +1,282 @@
+"""The target model's key/value cache around a round (argument marshalling only).
+
+Binding of the ``dt_kv_*``, ``dt_cache_attention`` and ``dt_prompt_attention``
+calls of ``include/dtree.h``, which state formulas, layouts and errors.  A round
+of a serving loop, per attention layer::
+
+    kv_plan(...)             # pages and slots for a prompt, a token or an accepted path
+    prompt_attention(...)    # causal attention of packed prompts
+    kv_append(...)           # their keys and values into the 8-bit cache
+    cache_attention(...)     # a token, or a drafted tree under its mask, over the cache
+
+``examples/serve_tree.py`` runs them around ``DraftTreeBuilder``.  Nothing here
+computes: tensors become pointers, a refused call raises ``DtreeError``.
+"""
+from __future__ import annotations
+
+import ctypes
+from ctypes import POINTER, byref, c_float, c_int, c_int64, c_size_t, c_void_p
+
+from .dtree import DtreeError, load_library
+
+# bits of the status words (DT_KV_*)
+KV_SHORT_OF_PAGES = 1
+KV_BAD_LENGTH = 2
+KV_SHORT_OF_ROWS = 4
+KV_BAD_PATH = 8
+KV_BAD_INDEX = 16
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+                ("n_pages", c_int), ("page", c_int), ("n_kv", c_int), ("head_dim", c_int)]
+
+
+class _Plan(ctypes.Structure):
+    _fields_ = [("n_req", c_int), ("max_blocks", c_int), ("page", c_int), ("n_pages", c_int), ("extra", c_int),
+                ("path_len", c_int), ("path_rows", c_int), ("max_rows", c_int64)] + \
+        [(n, c_void_p) for n in ("len_old", "delta", "path", "ring_in", "block_table", "free_pages", "len_new",
+                                 "ring_out", "row_start", "slot_map", "positions", "src_rows", "status")]
+
+
+class _Append(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_row_stride", c_int64), ("k_head_stride", c_int64),
+                ("v_row_stride", c_int64), ("v_head_stride", c_int64), ("n_src", c_int64), ("n_rows", c_int64),
+                ("slot_map", c_void_p), ("src_rows", c_void_p), ("status", c_void_p)]
+
+
+class _Attend(ctypes.Structure):
+    _fields_ = [("n_req", c_int), ("slots", c_int), ("n_q", c_int), ("max_blocks", c_int), ("scale", c_float),
+                ("q", c_void_p), ("q_row_stride", c_int64), ("q_head_stride", c_int64),
+                ("k_new", c_void_p), ("v_new", c_void_p), ("k_row_stride", c_int64), ("k_head_stride", c_int64),
+                ("v_row_stride", c_int64), ("v_head_stride", c_int64),
+                ("block_table", c_void_p), ("length", c_void_p), ("mask", c_void_p),
+                ("out", c_void_p), ("out_row_stride", c_int64), ("out_head_stride", c_int64), ("lse", c_void_p),
+                ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("status", c_void_p)]
+
+
+class _Prompt(ctypes.Structure):
+    _fields_ = [("n_seq", c_int), ("n_q", c_int), ("n_kv", c_int), ("head_dim", c_int), ("n_rows", c_int64),
+                ("scale", c_float), ("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("out", c_void_p),
+                ("q_row_stride", c_int64), ("q_head_stride", c_int64), ("k_row_stride", c_int64),
+                ("k_head_stride", c_int64), ("v_row_stride", c_int64), ("v_head_stride", c_int64),
+                ("out_row_stride", c_int64), ("out_head_stride", c_int64), ("row_start", c_void_p), ("lse", c_void_p)]
+
+
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        lib = load_library()
+        for name, res, args in (
+                ("dt_kv_plan", c_int, [POINTER(_Plan), c_void_p]),
+                ("dt_kv_append", c_int, [POINTER(_Cache), POINTER(_Append), c_void_p]),
+                ("dt_cache_attention", c_int, [POINTER(_Cache), POINTER(_Attend), c_void_p]),
+                ("dt_cache_attention_workspace", c_size_t, [c_int] * 5),
+                ("dt_prompt_attention", c_int, [POINTER(_Prompt), c_void_p])):
+            fn = getattr(lib, name)
+            fn.restype, fn.argtypes = res, args
+        _lib = lib
+    return _lib
+
+
+def _stream(stream, device):
+    import torch
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _call(status, where):
+    if status != 0:
+        raise DtreeError(status, where + ": " + _lib.dt_last_error().decode(errors="replace"))
+
+
+def _flat(t, dtype, numel, name, device):
+    """Pointer of a contiguous tensor of `numel` elements."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the others on {device}")
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of {numel} elements, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _heads(t, lead, heads, dim, name, device):
+    """Pointer, row stride and head stride of a bf16 tensor [*lead, heads, dim].
+    Only rows and heads may be strided: several leading dimensions must fold into
+    one row index, and channels must be adjacent."""
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the others on {device}")
+    if tuple(t.shape) != (*lead, heads, dim):
+        raise ValueError(f"{name}: expected {(*lead, heads, dim)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 or (len(lead) == 2 and lead[0] > 1 and st[0] != st[1] * lead[1]):
+        raise ValueError(f"{name}: strides {st}: channels must be adjacent and rows evenly spaced")
+    row, head = st[-3], st[-2]
+    return t.data_ptr(), (row if lead[-1] > 1 or len(lead) == 1 else st[0]), (head if heads > 1 else 0)
+
+
+def _on_device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    return t.device
+
+
+class KvCache:
+    """One layer's cache: ``k``, ``v`` [n_pages, n_kv, page, head_dim] torch.float8_e4m3fn and
+    ``k_scale``, ``v_scale`` [n_pages, n_kv] fp32, caller tensors that are kept alive here."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        if k.dim() != 4:
+            raise ValueError("k: expected [n_pages, n_kv, page, head_dim]")
+        self.device = _on_device(k, "k")
+        self.n_pages, self.n_kv, self.page, self.head_dim = k.shape
+        n, s = k.numel(), self.n_pages * self.n_kv
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.c = _Cache(_flat(k, torch.float8_e4m3fn, n, "k", self.device),
+                        _flat(v, torch.float8_e4m3fn, n, "v", self.device),
+                        _flat(k_scale, torch.float32, s, "k_scale", self.device),
+                        _flat(v_scale, torch.float32, s, "v_scale", self.device),
+                        self.n_pages, self.page, self.n_kv, self.head_dim)
+
+    @classmethod
+    def empty(cls, n_pages, page, n_kv, head_dim, device="cuda"):
+        """A cache of unwritten pages."""
+        import torch
+        k = torch.empty(n_pages, n_kv, page, head_dim, dtype=torch.float8_e4m3fn, device=device)
+        scale = torch.ones(n_pages, n_kv, dtype=torch.float32, device=device)
+        return cls(k, torch.empty_like(k), scale, torch.ones_like(scale))
+
+
+class AttentionWorkspace:
+    """Device memory that ``cache_attention`` calls use one after the other (calls that may
+    overlap, on several streams, need one each).  It grows with the largest call so far;
+    grow it before a stream capture by a call of the captured sizes or by ``reserve``."""
+
+    def __init__(self):
+        self.buffer, self.sizes = None, None
+
+    def reserve(self, n_req, slots, n_q, n_kv, head_dim, device="cuda"):
+        import torch
+        sizes = (n_req, slots, n_q, n_kv, head_dim)
+        if sizes != self.sizes:
+            need = _library().dt_cache_attention_workspace(*sizes)
+            if self.buffer is None or self.buffer.numel() < need or self.buffer.device != torch.device(device):
+                self.buffer = torch.zeros(max(need, 256), dtype=torch.uint8, device=device)
+            self.sizes = sizes
+        return self.buffer
+
+
+def kv_plan(len_old, len_new, block_table, free_pages, ring_in, ring_out, row_start, slot_map, status, *, page,
+            delta=None, extra=0, positions=None, path=None, path_rows=0, src_rows=None, stream=None):
+    """Block tables and slot maps from request lengths (``dt_kv_plan``).  int32 CUDA tensors but for
+    ``slot_map`` (int64): len_old, delta, len_new [n_req], block_table [n_req, max_blocks], free_pages
+    [n_pages], ring_in, ring_out [2], row_start [n_req + 1], slot_map, positions, src_rows [max_rows],
+    path [n_req, path_len], status [1] (KV_* bits, read it when convenient)."""
+    import torch
+    lib = _library()
+    i32, dev = torch.int32, _on_device(len_old, "len_old")
+    n, rows = len_old.numel(), slot_map.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table: expected [n_req, max_blocks]")
+    path_len = 0
+    if path is not None:
+        if path.dim() != 2:
+            raise ValueError("path: expected [n_req, path_len]")
+        path_len = path.shape[1]
+    width = block_table.shape[1]
+    a = _Plan(n, width, page, free_pages.numel(), extra, path_len, path_rows, rows,
+              _flat(len_old, i32, n, "len_old", dev),
+              None if delta is None else _flat(delta, i32, n, "delta", dev),
+              None if path is None else _flat(path, i32, n * path_len, "path", dev),
+              _flat(ring_in, i32, 2, "ring_in", dev), _flat(block_table, i32, n * width, "block_table", dev),
+              _flat(free_pages, i32, free_pages.numel(), "free_pages", dev), _flat(len_new, i32, n, "len_new", dev),
+              _flat(ring_out, i32, 2, "ring_out", dev), _flat(row_start, i32, n + 1, "row_start", dev),
+              _flat(slot_map, torch.int64, rows, "slot_map", dev),
+              None if positions is None else _flat(positions, i32, rows, "positions", dev),
+              None if src_rows is None else _flat(src_rows, i32, rows, "src_rows", dev),
+              _flat(status, i32, 1, "status", dev))
+    _call(lib.dt_kv_plan(byref(a), _stream(stream, dev)), "dt_kv_plan")
+
+
+def kv_append(cache, k, v, slot_map, *, src_rows=None, status=None, stream=None):
+    """Keys and values of new tokens into the cache (``dt_kv_append``).  k, v: bf16
+    [rows, n_kv, head_dim] or [n_req, rows, n_kv, head_dim], rows and heads may be strided."""
+    import torch
+    lib = _library()
+    dev, n = cache.device, slot_map.numel()
+    lead = tuple(k.shape[:-2])
+    kp, kr, kh = _heads(k, lead, cache.n_kv, cache.head_dim, "k", dev)
+    vp, vr, vh = _heads(v, lead, cache.n_kv, cache.head_dim, "v", dev)
+    a = _Append(kp, vp, kr, kh, vr, vh, lead[0] if len(lead) == 1 else lead[0] * lead[1], n,
+                _flat(slot_map, torch.int64, n, "slot_map", dev),
+                None if src_rows is None else _flat(src_rows, torch.int32, n, "src_rows", dev),
+                None if status is None else _flat(status, torch.int32, 1, "status", dev))
+    if src_rows is None and n > a.n_src:
+        raise ValueError(f"slot_map: {n} rows, but k has {a.n_src}")
+    _call(lib.dt_kv_append(byref(cache.c), byref(a), _stream(stream, dev)), "dt_kv_append")
+
+
+def cache_attention(cache, q, block_table, length, *, k_new=None, v_new=None, mask=None, scale=None, out=None,
+                    lse=None, workspace, status=None, stream=None):
+    """Attention of new tokens over the cache (``dt_cache_attention``).  q [n_req, slots, n_q, head_dim] bf16;
+    block_table [n_req, max_blocks], length [n_req] int32; k_new, v_new [n_req, slots, n_kv, head_dim] bf16: the
+    tokens' own keys and values, seen by mask [n_req, slots, slots] uint8 (``tree_mask``'s) or causally.
+    scale: head_dim ** -0.5 unless given.  Returns out [n_req, slots, n_q, head_dim] bf16; lse, if given,
+    [n_req, slots, n_q] fp32 is filled."""
+    import torch
+    lib = _library()
+    dev = cache.device
+    if q.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q: expected [n_req, slots, n_q, head_dim], block_table: [n_req, max_blocks]")
+    n, slots, heads, dim = q.shape
+    if dim != cache.head_dim:
+        raise ValueError(f"q: head_dim {dim}, the cache's is {cache.head_dim}")
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new: give both or neither")
+    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
+    kp = vp = None
+    kr = kh = vr = vh = 0
+    if k_new is not None:
+        kp, kr, kh = _heads(k_new, (n, slots), cache.n_kv, dim, "k_new", dev)
+        vp, vr, vh = _heads(v_new, (n, slots), cache.n_kv, dim, "v_new", dev)
+    qp, qr, qh = _heads(q, (n, slots), heads, dim, "q", dev)
+    op, orow, oh = _heads(out, (n, slots), heads, dim, "out", dev)
+    buf = workspace.reserve(n, slots, heads, cache.n_kv, dim, dev)
+    a = _Attend(n, slots, heads, block_table.shape[1], dim ** -0.5 if scale is None else scale, qp, qr, qh, kp, vp, kr,
+                kh, vr, vh, _flat(block_table, torch.int32, n * block_table.shape[1], "block_table", dev),
+                _flat(length, torch.int32, n, "length", dev),
+                None if mask is None else _flat(mask, torch.uint8, n * slots * slots, "mask", dev), op, orow, oh,
+                None if lse is None else _flat(lse, torch.float32, n * slots * heads, "lse", dev), buf.data_ptr(),
+                buf.numel(), None if status is None else _flat(status, torch.int32, 1, "status", dev))
+    _call(lib.dt_cache_attention(byref(cache.c), byref(a), _stream(stream, dev)), "dt_cache_attention")
+    return out
+
+
+def prompt_attention(q, k, v, row_start, *, scale=None, out=None, lse=None, stream=None):
+    """Causal attention over packed prompts (``dt_prompt_attention``).  q [rows, n_q, head_dim], k, v
+    [rows, n_kv, head_dim] bf16, rows and heads may be strided (slices of one projection's output);
+    row_start [n_seq + 1] int32.  Returns out [rows, n_q, head_dim]; lse [rows, n_q] fp32 is filled if given."""
+    import torch
+    lib = _library()
+    dev = _on_device(q, "q")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k: expected [rows, heads, head_dim]")
+    rows, heads, dim = q.shape
+    kv = k.shape[1]
+    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
+    qp, qr, qh = _heads(q, (rows,), heads, dim, "q", dev)
+    kp, kr, kh = _heads(k, (rows,), kv, dim, "k", dev)
+    vp, vr, vh = _heads(v, (rows,), kv, dim, "v", dev)
+    op, orow, oh = _heads(out, (rows,), heads, dim, "out", dev)
+    a = _Prompt(row_start.numel() - 1, heads, kv, dim, rows, dim ** -0.5 if scale is None else scale, qp, kp, vp, op,
+                qr, qh, kr, kh, vr, vh, orow, oh, _flat(row_start, torch.int32, row_start.numel(), "row_start", dev),
+                None if lse is None else _flat(lse, torch.float32, rows * heads, "lse", dev))
+    _call(lib.dt_prompt_attention(byref(a), _stream(stream, dev)), "dt_prompt_attention")
+    return out

@@ -361,6 +361,185 @@ dt_status dt_build_round_host(dt_ctx* ctx, const void* H_host, const int32_t* ro
 dt_status dt_topm_noalloc(const float* logits, int rows, int V, int M, float T, int32_t* cand_tok,
                           float* cand_base, float* rest_lse, void* stream);
 
+/* --------------------------------------------------------------------------
+ * The target model's key/value cache around a round.
+ *
+ * The tree that a round emits is scored by the target model in one pass under
+ * the ancestor-only mask (DominoTree page, Verificacion), over the context the
+ * target has already read.  These calls hold that context in 8 bits and attend
+ * to it; they need no context object (dt_ctx) and allocate nothing.  One pass
+ * of a serving loop, per attention layer:
+ *   dt_kv_plan          pages and slots for new tokens (a prompt, the accepted path)
+ *   dt_prompt_attention causal attention of packed prompts
+ *   dt_kv_append        keys and values of new tokens into the cache
+ *   dt_cache_attention  a token, or a drafted tree, over the cache
+ * A drafted tree's keys and values stay outside the cache until dt_accept_walk
+ * has chosen the path: only accepted tokens are appended, so that a rejected
+ * token never widens a page's scale and nothing has to be taken out again.
+ *
+ * Activations are bf16, statistics and sums fp32.  "Rows of heads" are given
+ * as a pointer and two strides in elements: element (row, head, c) stands at
+ * data[row * row_stride + head * head_stride + c]; data must be 16-byte aligned
+ * and the strides multiples of 8.  Query head h uses key/value head
+ * h / (n_q / n_kv).
+ * Messages of refused calls are in dt_last_error().
+ * ------------------------------------------------------------------------ */
+
+/* One layer's cache: page p, key/value head h, offset o, channel c stands at
+ * k[((p * n_kv + h) * page + o) * head_dim + c], an e4m3 number to be multiplied
+ * by k_scale[p * n_kv + h]; likewise v.  A token's slot is p * page + o.  Pages
+ * hold nothing before their first append.  page is 16, 32, 64 or 128, head_dim
+ * 64 or 128; k and v are 16-byte aligned. */
+typedef struct dt_kv_cache {
+  void* k;        /* [n_pages, n_kv, page, head_dim] e4m3 */
+  void* v;        /* likewise */
+  float* k_scale; /* [n_pages, n_kv] fp32 */
+  float* v_scale; /* [n_pages, n_kv] fp32 */
+  int n_pages;
+  int page;
+  int n_kv;
+  int head_dim;
+} dt_kv_cache;
+
+/* Bits of the status words of these calls (device memory, int32). */
+#define DT_KV_SHORT_OF_PAGES 1 /* more pages wanted than are free */
+#define DT_KV_BAD_LENGTH 2     /* a length below zero or above max_blocks * page */
+#define DT_KV_SHORT_OF_ROWS 4  /* more new tokens than max_rows */
+#define DT_KV_BAD_PATH 8       /* a path shorter than the new tokens, or a slot out of range */
+#define DT_KV_BAD_INDEX 16     /* a page, slot or source row out of range (skipped), or more pages
+                                * given back than can be in use */
+
+/* Block tables and slot maps from request lengths.  Request q's new length is
+ *   len_new[q] = max(len_old[q] + delta[q] + extra, 0)   (delta NULL: all 0)
+ * so that a prompt is delta = its length, a decoding step extra = 1, a commit
+ * after dt_accept_walk delta = accept_len with extra = 1 (the root and the
+ * accepted slots), and the end of a request delta = -len_old.
+ * Free pages stand in a ring: ring_in = {head, count} says that the pages
+ * free_pages[(head + i) % n_pages], i < count, are free.  Pages for growing
+ * requests are taken from the head in the order of requests and blocks and
+ * written into block_table; pages of shrinking requests are put behind the last
+ * free one (not given out again by the same call).  Entries of block_table
+ * behind a request's length are left alone.
+ * New tokens are packed in the order of requests: rows row_start[q] to
+ * row_start[q+1]-1 are request q's, positions len_old[q] and up.  Rows from
+ * row_start[n_req] to max_rows-1 get slot, position and source row -1.
+ * All or nothing: where any bit of *status is set, len_new = len_old, ring_out =
+ * ring_in, row_start is 0, all rows are -1 and neither block_table nor
+ * free_pages has changed.  One launch; outputs must not overlap inputs. */
+typedef struct dt_kv_plan_args {
+  int n_req;               /* 1..4096 */
+  int max_blocks;          /* entries of a request in block_table, >= 1 */
+  int page;                /* 16, 32, 64 or 128 */
+  int n_pages;             /* entries of free_pages, >= 1 */
+  int extra;
+  int path_len;            /* entries of a request in path */
+  int path_rows;           /* source rows of a request (B + 1) */
+  int64_t max_rows;        /* entries of slot_map, positions, src_rows; 1..2^31-1 */
+  const int32_t* len_old;  /* [n_req] */
+  const int32_t* delta;    /* [n_req] or NULL */
+  const int32_t* path;     /* [n_req, path_len] (dt_accept_walk's accepted) or NULL */
+  const int32_t* ring_in;  /* [2] */
+  int32_t* block_table;    /* [n_req, max_blocks] in/out */
+  int32_t* free_pages;     /* [n_pages] in/out */
+  int32_t* len_new;        /* [n_req] out */
+  int32_t* ring_out;       /* [2] out */
+  int32_t* row_start;      /* [n_req + 1] out */
+  int64_t* slot_map;       /* [max_rows] out */
+  int32_t* positions;      /* [max_rows] out, or NULL */
+  int32_t* src_rows;       /* [max_rows] out, or NULL: request q's j-th new token is row
+                            * q * path_rows + (j == 0 ? 0 : path[q, j-1]); without path, its own row */
+  int32_t* status;         /* [1] out: DT_KV_* bits, 0 if none */
+} dt_kv_plan_args;
+dt_status dt_kv_plan(const dt_kv_plan_args* args, void* stream);
+
+/* Keys and values of new tokens into the cache.  Row t goes to slot slot_map[t]
+ * (negative: skipped), from row src_rows[t] of k and v (NULL: row t).  Rows that
+ * go to one page must follow one another with consecutive slots, as
+ * dt_kv_plan's do.
+ * Per page, head and tensor: the new tokens need the smallest power of two s
+ * with 448 s >= their largest finite magnitude, 2^-126 <= s <= 2^120.  Where the
+ * first of them stands at the page's start, s becomes the scale; otherwise the
+ * scale becomes max(scale, s), and where that is larger the page's earlier
+ * tokens are rounded to it (with powers of two this only touches what becomes
+ * subnormal).  Values are rounded to nearest even; a NaN or an infinity is held
+ * as a NaN.
+ * n_src: rows of k and v.  status: [1] int32 device or NULL; DT_KV_BAD_INDEX is
+ * or'ed in for a slot behind the cache (the row is skipped) and for a source row
+ * out of range (held as zeros).  One launch. */
+typedef struct dt_kv_append_args {
+  const void* k; /* rows of heads, n_kv x head_dim */
+  const void* v;
+  int64_t k_row_stride, k_head_stride;
+  int64_t v_row_stride, v_head_stride;
+  int64_t n_src;
+  int64_t n_rows;          /* entries of slot_map, 0..2^31-1 */
+  const int64_t* slot_map; /* [n_rows] */
+  const int32_t* src_rows; /* [n_rows] or NULL */
+  int32_t* status;
+} dt_kv_append_args;
+dt_status dt_kv_append(const dt_kv_cache* cache, const dt_kv_append_args* args, void* stream);
+
+/* Attention of new tokens over the cache.  Query row (q, a), a < slots, sees the
+ * length[q] cached tokens of its request, and of the request's own new tokens
+ * (k_new NULL: none) those b with mask[q, a, b] != 0, or b <= a where mask is
+ * NULL:
+ *   z_t = scale * <query, key_t>,  out = sum_t e^{z_t} value_t / sum_t e^{z_t},
+ *   lse = log sum_t e^{z_t}.
+ * A row that sees nothing gives zeros and -inf.  What a row does not see has no
+ * part in it, whatever it holds; a row that sees a value with a NaN or an
+ * infinity is not finite in that channel (other channels of that row may not be
+ * either), a row that sees a key with a NaN is NaN.
+ * Row (q, a) of q, k_new, v_new and out is row q * slots + a.
+ * workspace: dt_cache_attention_workspace() bytes of device memory, 256-byte
+ * aligned, zeroed once by the caller; every call leaves it ready for the next,
+ * and calls that share one must not overlap.  status as in dt_kv_append (a page
+ * out of range counts as not there). */
+typedef struct dt_cache_attention_args {
+  int n_req, slots, n_q, max_blocks;
+  float scale;             /* finite */
+  const void* q;           /* rows of heads, n_q x head_dim */
+  int64_t q_row_stride, q_head_stride;
+  const void* k_new;       /* rows of heads, n_kv x head_dim, or NULL (then v_new too) */
+  const void* v_new;
+  int64_t k_row_stride, k_head_stride;
+  int64_t v_row_stride, v_head_stride;
+  const int32_t* block_table; /* [n_req, max_blocks] */
+  const int32_t* length;   /* [n_req]; clamped to 0..max_blocks * page */
+  const uint8_t* mask;     /* [n_req, slots, slots] or NULL */
+  void* out;               /* rows of heads, n_q x head_dim, bf16 */
+  int64_t out_row_stride, out_head_stride;
+  float* lse;              /* [n_req, slots, n_q] or NULL */
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* status;
+} dt_cache_attention_args;
+dt_status dt_cache_attention(const dt_kv_cache* cache, const dt_cache_attention_args* args, void* stream);
+
+/* Bytes of workspace for such a call (0 where the sizes are refused). */
+size_t dt_cache_attention_workspace(int n_req, int slots, int n_q, int n_kv, int head_dim);
+
+/* Causal attention over packed prompts.  Sequence i has rows row_start[i] to
+ * row_start[i+1]-1 of q, k, v and out (dt_kv_plan's row_start); a row sees the
+ * rows of its own sequence up to itself.  Formulas, lse ([n_rows, n_q] or NULL)
+ * and the rule on NaNs as in dt_cache_attention.  row_start must ascend from 0
+ * or more to n_rows or less; rows outside are not written. */
+typedef struct dt_prompt_attention_args {
+  int n_seq, n_q, n_kv, head_dim;
+  int64_t n_rows;            /* 1..2^31-1 */
+  float scale;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  int64_t q_row_stride, q_head_stride;
+  int64_t k_row_stride, k_head_stride;
+  int64_t v_row_stride, v_head_stride;
+  int64_t out_row_stride, out_head_stride;
+  const int32_t* row_start;  /* [n_seq + 1] device */
+  float* lse;
+} dt_prompt_attention_args;
+dt_status dt_prompt_attention(const dt_prompt_attention_args* args, void* stream);
+
 /* Synchronise the context's last stream and read (and clear) its device status
  * word: DT_OK, DT_ERR_TIMEOUT or DT_ERR_DEVICE. */
 dt_status dt_get_device_status(dt_ctx* ctx);

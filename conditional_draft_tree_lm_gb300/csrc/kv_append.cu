@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(const AppendParams
         const uint32_t in[2] = {c.x, c.y};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const uint32_t lo = e4m3x2_to_f16x2(in[k] & 0xFFFFu), hi = e4m3x2_to_f16x2(in[k] >> 16);
+          uint32_t lo, hi;
+          e4m3x4_to_f16x2x2(in[k], lo, hi);
           const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
           const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
           r[k] = __nv_cvt_float2_to_fp8x2(make_float2(a.x * ratio, a.y * ratio), __NV_SATFINITE, __NV_E4M3) |

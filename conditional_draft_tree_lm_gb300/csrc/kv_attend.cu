@@ -1,6 +1,7 @@
 // dt_cache_attention and dt_prompt_attention, the plain form: one warp per row
 // and head, one key at a time with a running maximum and sum.
 #include "kv.cuh"
+#include "kv_decode.cuh"
 
 namespace dt {
 namespace {
@@ -114,6 +115,8 @@ __global__ void k_plain_prompt(const dt_prompt_attention_args a) {
 
 extern "C" size_t dt_cache_attention_workspace(int n_req, int slots, int n_q, int n_kv, int head_dim) {
   if (n_req < 1 || slots < 1 || n_kv < 1 || n_q < n_kv || n_q % n_kv != 0 || (head_dim != 64 && head_dim != 128)) return 0;
+  const int rows = slots * (n_q / n_kv);
+  if (rows <= dt::kDecodeMaxRows) return dt::decode_workspace(rows, head_dim);
   return 256;
 }
 
@@ -141,9 +144,30 @@ extern "C" dt_status dt_cache_attention(const dt_kv_cache* cache, const dt_cache
   const size_t need = dt_cache_attention_workspace(a.n_req, a.slots, a.n_q, cache->n_kv, cache->head_dim);
   if (!a.workspace || (reinterpret_cast<uintptr_t>(a.workspace) & 255u) != 0 || a.workspace_bytes < need)
     return kv_fail(DT_ERR_INVALID_ARG, "%s: the workspace is null, misaligned or below %zu bytes", who, need);
+  if (static_cast<int64_t>(a.n_req) * cache->n_kv > kMaxJoins)
+    return kv_fail(DT_ERR_SHAPE, "%s: n_req * n_kv above %d", who, kMaxJoins);
+  if ((static_cast<int64_t>(a.max_blocks) * cache->page / kDecodeTile + 1) * a.n_req * cache->n_kv > (1 << 30))
+    return kv_fail(DT_ERR_SHAPE, "%s: more than 2^37 cached tokens over all requests and heads", who);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int group = a.n_q / cache->n_kv;
+  if (a.slots * group <= kDecodeMaxRows) {
+    DecodeParams p = {};
+    p.c = *cache;
+    p.a = a;
+    p.group = group;
+    p.rows = a.slots * group;
+    p.shift = 4;
+    while ((1 << p.shift) < cache->page) ++p.shift;
+    p.done = static_cast<unsigned*>(a.workspace);
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kCounterBytes);
+    const int grid = decode_grid(a.n_req, cache->n_kv, static_cast<long long>(a.max_blocks) * cache->page);
+    cudaError_t e;
+    if (cache->head_dim == 64) e = p.rows <= 8 ? launch_decode<64, 1>(p, grid, st) : launch_decode<64, 2>(p, grid, st);
+    else e = p.rows <= 8 ? launch_decode<128, 1>(p, grid, st) : launch_decode<128, 2>(p, grid, st);
+    return kv_launched(who, e);
+  }
   const int64_t warps = static_cast<int64_t>(a.n_req) * a.slots * a.n_q;
   const unsigned grid = static_cast<unsigned>((warps + 3) / 4);
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cache->head_dim == 64) k_plain_cache<64><<<grid, 128, 0, st>>>(*cache, a);
   else k_plain_cache<128><<<grid, 128, 0, st>>>(*cache, a);
   return kv_launched(who, cudaGetLastError());

@@ -82,34 +82,6 @@ __global__ void k_plain_cache(const dt_kv_cache c, const dt_cache_attention_args
   r.end(static_cast<__nv_bfloat16*>(a.out) + row * a.out_row_stride + h * a.out_head_stride, a.lse ? a.lse + w : nullptr, lane);
 }
 
-template <int HD>
-__global__ void k_plain_prompt(const dt_prompt_attention_args a) {
-  constexpr int N = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (w >= a.n_rows * a.n_q) return;
-  const int h = static_cast<int>(w % a.n_q), kvh = h / (a.n_q / a.n_kv);
-  const int64_t row = w / a.n_q;
-  int lo = 0, hi = a.n_seq;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.row_start[mid] <= row) lo = mid; else hi = mid;
-  }
-  if (row < a.row_start[lo] || row >= a.row_start[lo + 1]) return;
-  Row<HD> r;
-  r.start(static_cast<const __nv_bfloat16*>(a.q) + row * a.q_row_stride + h * a.q_head_stride, lane);
-  for (int64_t s = a.row_start[lo]; s <= row; ++s) {
-    float k[N], v[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      k[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.k)[s * a.k_row_stride + kvh * a.k_head_stride + lane * N + i]);
-      v[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.v)[s * a.v_row_stride + kvh * a.v_head_stride + lane * N + i]);
-    }
-    r.step(k, v, a.scale);
-  }
-  r.end(static_cast<__nv_bfloat16*>(a.out) + row * a.out_row_stride + h * a.out_head_stride, a.lse ? a.lse + w : nullptr, lane);
-}
-
 }  // namespace
 }  // namespace dt
 
@@ -170,29 +142,5 @@ extern "C" dt_status dt_cache_attention(const dt_kv_cache* cache, const dt_cache
   const unsigned grid = static_cast<unsigned>((warps + 3) / 4);
   if (cache->head_dim == 64) k_plain_cache<64><<<grid, 128, 0, st>>>(*cache, a);
   else k_plain_cache<128><<<grid, 128, 0, st>>>(*cache, a);
-  return kv_launched(who, cudaGetLastError());
-}
-
-extern "C" dt_status dt_prompt_attention(const dt_prompt_attention_args* args, void* stream) {
-  using namespace dt;
-  const char* who = "dt_prompt_attention";
-  if (!args) return kv_fail(DT_ERR_INVALID_ARG, "%s: null arguments", who);
-  const dt_prompt_attention_args& a = *args;
-  if (a.n_seq < 1 || a.n_rows < 1 || a.n_kv < 1 || a.n_q < 1)
-    return kv_fail(DT_ERR_INVALID_ARG, "%s: need n_seq, n_rows, n_q, n_kv >= 1", who);
-  if (a.head_dim != 64 && a.head_dim != 128)
-    return kv_fail(DT_ERR_SHAPE, "%s: head_dim %d is not 64 or 128", who, a.head_dim);
-  if (a.n_q % a.n_kv != 0 || a.n_q / a.n_kv > 128)
-    return kv_fail(DT_ERR_SHAPE, "%s: %d query heads over %d key/value heads: need a multiple, at most 128 a head", who,
-                   a.n_q, a.n_kv);
-  if (a.n_rows > 0x7FFFFFFF) return kv_fail(DT_ERR_SHAPE, "%s: n_rows above 2^31-1", who);
-  if (!(a.scale - a.scale == 0.0f)) return kv_fail(DT_ERR_INVALID_ARG, "%s: scale is not finite", who);
-  if (!a.row_start || !kv_rows_ok(a.q, a.q_row_stride, a.q_head_stride) || !kv_rows_ok(a.k, a.k_row_stride, a.k_head_stride) ||
-      !kv_rows_ok(a.v, a.v_row_stride, a.v_head_stride) || !kv_rows_ok(a.out, a.out_row_stride, a.out_head_stride))
-    return kv_fail(DT_ERR_INVALID_ARG, "%s: null or misaligned q, k, v, out or row_start", who);
-  const unsigned grid = static_cast<unsigned>((a.n_rows * a.n_q + 3) / 4);
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (a.head_dim == 64) k_plain_prompt<64><<<grid, 128, 0, st>>>(a);
-  else k_plain_prompt<128><<<grid, 128, 0, st>>>(a);
   return kv_launched(who, cudaGetLastError());
 }

@@ -1,0 +1,149 @@
+// What the two tensor-core attention kernels share: tensor-memory accesses, the
+// products' issue, and the softmax of one 128-key tile.
+//
+// Both keep S = Q K^T (128 rows x 128 keys, fp32) and O (128 rows x head_dim) in
+// tensor memory, one lane a row.  A softmax thread owns a row: it reads its 128
+// logits, writes P as 16-bit pairs over the first half of S's columns, and the
+// next product takes P from there (A from tensor memory) and V from shared memory
+// as it was stored, rows of channels (B, MN-major), so that V is never transposed.
+// Two such tiles of rows share every key tile: while one's softmax runs on the
+// ordinary cores, the tensor core does the other's products.
+//
+// Order of one row tile's products (one issuing thread, and the tensor core runs
+// them in order): S(0); then for every key tile j, when P(j) is there: O += P(j)
+// V(j), S(j + 1).  So S(j + 1) being complete tells the softmax that O is at rest
+// and may be rescaled, and P(j)'s place free.
+//
+// The maximum in use lags behind the true one by up to 2^8: a row's O is rescaled
+// only where its maximum has grown by more (published for Blackwell attention as
+// conditional rescaling); sums and O stay exact in that unit.
+#pragma once
+
+#include "kv.cuh"
+
+namespace dt {
+
+constexpr int kKeyTile = 128;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+DT_DEVINL float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 32 lanes x 32 consecutive 32-bit columns, without waiting (tmem_wait_ld).
+DT_DEVINL void tmem_ld32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr));
+}
+DT_DEVINL void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+DT_DEVINL void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+DT_DEVINL void tmem_st32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+DT_DEVINL void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] B[smem], kind::f16
+DT_DEVINL void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// V as operand B, MN-major in the 128-byte swizzle: groups of 64 channels
+// (128 bytes a key) `group_bytes` apart, groups of 8 keys 1024 bytes apart.
+DT_DEVINL uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t group_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(group_bytes >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// kind::f16 with fp32 D; BF16: both operands bf16, else both fp16; b_mn: B is MN-major.
+template <bool BF16>
+DT_HOST_DEVICE_INLINE uint32_t idesc_flash(uint32_t M, uint32_t N, bool b_mn) {
+  return (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// A row tile's (or key tile's) operand in shared memory: halves of 64 channels, 128 rows of 128 bytes, swizzled.
+constexpr uint32_t kHalfBytes = 128 * 128;
+template <int HD>
+constexpr uint32_t kOperandBytes = HD / 64 * kHalfBytes;
+
+// S = Q K^T and O (+)= P V of one tile; issued by one thread.
+template <int HD, bool BF16>
+DT_DEVINL void issue_qk(uint32_t s_tmem, uint32_t q, uint32_t k) {
+  const uint32_t idesc = idesc_flash<BF16>(128, kKeyTile, false);
+#pragma unroll
+  for (int i = 0; i < HD / 16; ++i) {
+    const uint32_t off = (i >> 2) * kHalfBytes + (i & 3) * 32;
+    tc_mma_bf16(s_tmem, sdesc_k_sw128(q + off), sdesc_k_sw128(k + off), idesc, i != 0);
+  }
+}
+template <int HD, bool BF16>
+DT_DEVINL void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t v, bool first) {
+  const uint32_t idesc = idesc_flash<BF16>(128, HD, true);
+#pragma unroll
+  for (int i = 0; i < kKeyTile / 16; ++i)
+    tc_mma_ts(o_tmem, p_tmem + i * 8, sdesc_mn_sw128(v + i * 2048, kHalfBytes), idesc, !(first && i == 0));
+}
+
+// Two probabilities to a 16-bit pair, the first in the low half.
+template <bool BF16>
+DT_DEVINL uint32_t pack_p(float lo, float hi) {
+  if (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// O *= f for this warp's 32 lanes.
+template <int HD>
+DT_DEVINL void rescale_o(uint32_t o_tmem, float f) {
+#pragma unroll
+  for (int c = 0; c < HD; c += 32) {
+    uint32_t v[32];
+    tmem_ld32(o_tmem + c, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+    tmem_st32(o_tmem + c, v);
+  }
+  tmem_wait_st();
+}
+
+// The first `n` of 128 keys, as four words of 32 bits.
+DT_DEVINL uint32_t first_bits(int n, int word) {
+  n -= word * 32;
+  return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
+}  // namespace dt

@@ -107,13 +107,15 @@ def append(codes, scale, x, slots, src, page):
         t += len(run)
 
 
-def attend(q, k, v, see, scale):
+def attend(q, k, v, see, scale, weight_unit):
     """One head's rows q [R, hd] over keys k, v [T, hd] with see [R, T] -> out [R, hd], lse [R], and
     their tolerances.
 
     A product of hd terms in 32 bits is off by at most hd 2^-24 B, B = scale sum |q||k|; so are z and
     lse (and a sum of T terms e^z adds up to T 2^-24 at worst, 2^-14 here).  The weights are then off by
-    that and by their own rounding to 8 bits (2^-9), the output by its rounding to bf16 (2^-9 |out|)."""
+    that and by their own rounding to a 16-bit type: weight_unit, half its spacing at 1, is 2^-8 for the 8
+    significant bits of bf16 and 2^-11 for the 11 of fp16.  The output is off by its rounding to bf16, 2^-8 |out|.
+    (The bound holds for any signs; the weights' errors hardly ever add up so.)"""
     q, k, v = (np.asarray(a, np.float64) for a in (q, k, v))
     R, hd = q.shape
     out, lse = np.zeros((R, hd)), np.full(R, -np.inf)
@@ -129,5 +131,5 @@ def attend(q, k, v, see, scale):
         off = hd * 2.0 ** -24 * np.abs(scale) * (np.abs(k[s]) @ np.abs(q[r])).max() + 2.0 ** -14
         weight = p @ np.abs(v[s]) / p.sum()
         tol_lse[r] = off
-        tol_out[r] = 2.0 ** -9 * np.abs(out[r]) + (2.0 ** -9 + 2 * off) * 1.02 * weight + 1e-30
+        tol_out[r] = 2.0 ** -8 * np.abs(out[r]) + (weight_unit + 2 * off) * 1.02 * weight + 1e-30
     return out, lse, tol_out, tol_lse

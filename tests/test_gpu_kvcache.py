@@ -341,7 +341,7 @@ def check_cache(c, got, scale=None, rows=None, skip=()):
                 m = np.tril(np.ones((c["slots"],) * 2, bool)) if c["mask"] is None else c["mask"][b] != 0
                 see = np.concatenate([see, m], 1)
             for j in range(h * g, (h + 1) * g):
-                o, l, to, tl = ok.attend(qf[b, :, j], k, v, see, scale)
+                o, l, to, tl = ok.attend(qf[b, :, j], k, v, see, scale, 2.0 ** -11)
                 for a in range(c["slots"]) if rows is None else rows:
                     if (b, a) in skip:
                         continue
@@ -556,7 +556,7 @@ def check_prompt(q, k, v, lens, got, scale=None, first=0, skip=(), sample=None):
             if len(rows) == 0:
                 continue
             see = np.arange(ln) <= rows[:, None]
-            o, l, to, tl = ok.attend(qf[a + rows, h], kf[a:a + ln, h // g], vf[a:a + ln, h // g], see, scale)
+            o, l, to, tl = ok.attend(qf[a + rows, h], kf[a:a + ln, h // g], vf[a:a + ln, h // g], see, scale, 2.0 ** -8)
             for i, r in enumerate(rows):
                 if a + r in skip:
                     continue

@@ -43,11 +43,20 @@ def test_plan_by_hand():
     assert (r["head"], r["count"]) == (2, 7) and r["ring"].tolist() == [9, 8, 1, 0, 2, 4, 6, 3, 5, -1]
 
 
+def test_rounding_units_of_the_attention_bounds():
+    """The largest relative rounding error of bf16 is 2^-8 / (1 + 2^-8), of fp16 2^-11 / (1 + 2^-11)."""
+    torch = pytest.importorskip("torch")
+    x = 1 + torch.arange(1 << 16, dtype=torch.float64) / (1 << 16)
+    for dtype, unit in ((torch.bfloat16, 2.0 ** -8), (torch.float16, 2.0 ** -11)):
+        worst = ((x.to(dtype).double() - x).abs() / x).max().item()
+        assert 0.99 * unit / (1 + unit) < worst <= unit
+
+
 def test_attend_against_brute_force():
     rs = np.random.RandomState(1)
     q, k, v = rs.randn(3, 8), rs.randn(5, 8), rs.randn(5, 8)
     see = np.array([[1, 1, 0, 1, 0], [0, 0, 0, 0, 0], [0, 0, 0, 0, 1]], bool)
-    out, lse, _, _ = ok.attend(q, k, v, see, 0.5)
+    out, lse, _, _ = ok.attend(q, k, v, see, 0.5, 2.0 ** -8)
     w = [np.exp(0.5 * q[0] @ k[t]) for t in (0, 1, 3)]
     np.testing.assert_allclose(out[0], sum(a * v[t] for a, t in zip(w, (0, 1, 3))) / sum(w), rtol=1e-12)
     np.testing.assert_allclose(lse[0], np.log(sum(w)), rtol=1e-12)

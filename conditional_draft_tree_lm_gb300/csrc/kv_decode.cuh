@@ -98,32 +98,39 @@ DT_DEVINL int tiles_of(int len, int max_len, int tile) {
   len = min(max(len, 0), max_len);
   return max(1, (len + tile - 1) / tile);
 }
+struct DecodeTiles {
+  int max_len;
+  DT_DEVINL int operator()(int len) const { return tiles_of(len, max_len, kDecodeTile); }
+};
 
 // Where each request's tiles start in the row of all requests' tiles: starts of
 // THREADS bins of requests in shared memory, the rest is summed when asked for.
 // (The host refuses calls whose tiles over all heads could pass 2^30.)
-template <int THREADS>
+template <int THREADS, class Tiles>
 struct TileRow {
   const int32_t* length;
-  int n_req, max_len, tile, per;  // per: requests of a bin
-  int* start;                     // [THREADS + 1] shared
-  // All threads of the block; ends with a barrier.
+  int n_req;
+  Tiles tiles;  // of a request of that length
+  int per;      // requests of a bin
+  int* start;   // [THREADS + 1] shared
+  // All threads of the block (THREADS of them at least, and that many bins); ends with a barrier.
   DT_DEVINL void sum(int* scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     per = (n_req + THREADS - 1) / THREADS;
     int own = 0;
-    for (int q = tid * per; q < min(n_req, (tid + 1) * per); ++q) own += tiles_of(length[q], max_len, tile);
+    if (tid < THREADS)
+      for (int q = tid * per; q < min(n_req, (tid + 1) * per); ++q) own += tiles(length[q]);
     int incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
       if (lane >= o) incl += x;
     }
-    if (lane == 31) scratch[warp] = incl;
+    if (lane == 31 && tid < THREADS) scratch[warp] = incl;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) incl += w < warp ? scratch[w] : 0;
-    start[tid + 1] = incl;
+    if (tid < THREADS) start[tid + 1] = incl;
     if (tid == 0) start[0] = 0;
     __syncthreads();
   }
@@ -139,7 +146,7 @@ struct TileRow {
     first = start[lo];
     if (per == 1) return;
     for (;; ++req) {
-      const int n = tiles_of(length[req], max_len, tile);
+      const int n = tiles(length[req]);
       if (index < first + n) break;
       first += n;
     }
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas) k_decode(const De
   const int page_mask = (1 << p.shift) - 1;
   uint8_t* ring = smem + warp * Smem::kStep;
 
-  TileRow<kDecodeThreads> row_of = {a.length, a.n_req, max_len, kDecodeTile, 0, s_start};
+  TileRow<kDecodeThreads, DecodeTiles> row_of = {a.length, a.n_req, {max_len}, 0, s_start};
   row_of.sum(scratch);
   const int work = row_of.total() * n_kv;
   const int pieces = min(work, static_cast<int>(gridDim.x));

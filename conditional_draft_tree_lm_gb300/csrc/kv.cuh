@@ -13,6 +13,8 @@
 
 namespace dt {
 
+constexpr int kSms = 152;  // of a GB300: grids of one wave
+
 // Largest finite e4m3 magnitude: 1.75 * 2^8.
 constexpr float kE4m3Max = 448.0f;
 

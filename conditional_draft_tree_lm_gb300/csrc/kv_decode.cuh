@@ -42,7 +42,6 @@ constexpr int kDecodeThreads = 128;
 constexpr int kDecodeWarps = kDecodeThreads / 32;
 constexpr int kDecodeTile = 32 * kDecodeWarps;  // tokens: a step of every warp
 constexpr int kDecodeCtas = 2;                  // per SM
-constexpr int kSms = 152;
 
 // The workspace starts with the joins' counters, at the same place for every call
 // (so that no call's parts lie over another's counters), the parts follow.

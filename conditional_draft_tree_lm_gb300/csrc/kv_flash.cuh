@@ -106,12 +106,14 @@ DT_DEVINL void issue_qk(uint32_t s_tmem, uint32_t q, uint32_t k) {
     tc_mma_bf16(s_tmem, sdesc_k_sw128(q + off), sdesc_k_sw128(k + off), idesc, i != 0);
   }
 }
-template <int HD, bool BF16>
-DT_DEVINL void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t v, bool first) {
+template <int HD, bool BF16>  // half 0 or 1 of the keys
+DT_DEVINL void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t v, bool first, int half) {
   const uint32_t idesc = idesc_flash<BF16>(128, HD, true);
 #pragma unroll
-  for (int i = 0; i < kKeyTile / 16; ++i)
+  for (int k = 0; k < kKeyTile / 32; ++k) {
+    const int i = half * (kKeyTile / 32) + k;
     tc_mma_ts(o_tmem, p_tmem + i * 8, sdesc_mn_sw128(v + i * 2048, kHalfBytes), idesc, !(first && i == 0));
+  }
 }
 
 // Two probabilities to a 16-bit pair, the first in the low half.
@@ -144,6 +146,114 @@ DT_DEVINL void rescale_o(uint32_t o_tmem, float f) {
 DT_DEVINL uint32_t first_bits(int n, int word) {
   n -= word * 32;
   return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
+// Two fp32 at a time (one issue slot for a pair).
+DT_DEVINL uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+DT_DEVINL void f32x2_parts(uint64_t x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
+DT_DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+DT_DEVINL uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The running softmax of one row.
+struct SoftmaxRow {
+  float m = -INFINITY, l = 0.0f;  // the maximum in use, in powers of two, and the sum in its unit
+};
+
+// One 128-key tile of a row: S at s_at becomes P there, m and l (and O, where the
+// maximum grows or O's unit changes by `ratio`) are brought up to date.  scale(g):
+// what turns a raw logit of keys 16 g .. 16 g + 15 into powers of two, one value
+// for all where UNIFORM; negative: its sign is negative.  see: the row's visible
+// keys, all of them unless MASKED.  ready(i): called when half i of P is stored.
+template <int HD, bool BF16, bool UNIFORM, bool MASKED, class Scale, class Ready>
+DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float ratio, bool negative, Scale scale,
+                            const uint32_t (&see)[4], SoftmaxRow& row, Ready ready) {
+  uint32_t s[128];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) tmem_ld32(s_at + 32 * w, s + 32 * w);
+  tmem_wait_ld();
+  if (MASKED) {
+    const uint32_t out = negative ? 0x7F800000u : 0xFF800000u;
+#pragma unroll
+    for (int i = 0; i < 128; ++i) s[i] = see[i >> 5] >> (i & 31) & 1u ? s[i] : out;
+  }
+  float top = -INFINITY;
+  if (!negative) {
+    float x[8];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      float a = fmaxf(__uint_as_float(s[16 * g]), __uint_as_float(s[16 * g + 1])), b = fmaxf(__uint_as_float(s[16 * g + 2]), __uint_as_float(s[16 * g + 3]));
+#pragma unroll
+      for (int i = 4; i < 16; i += 4) {
+        a = fmaxf(fmaxf(a, __uint_as_float(s[16 * g + i])), __uint_as_float(s[16 * g + i + 1]));
+        b = fmaxf(fmaxf(b, __uint_as_float(s[16 * g + i + 2])), __uint_as_float(s[16 * g + i + 3]));
+      }
+      x[g] = fmaxf(a, b);
+      if (!UNIFORM) x[g] = scale(g) == 0.0f ? 0.0f : x[g] * scale(g);
+    }
+#pragma unroll
+    for (int g = 0; g < 8; ++g) top = fmaxf(top, x[g]);
+  } else {
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      float a = INFINITY;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) a = fminf(a, __uint_as_float(s[16 * g + i]));
+      top = fmaxf(top, UNIFORM ? -a : a * scale(g));
+    }
+    if (UNIFORM) top = -top;
+  }
+  if (UNIFORM) top = scale(0) == 0.0f ? 0.0f : top * scale(0);
+  // (a tile of which the row sees nothing has top = -inf, or 0 with a scale of zero: no harm, P is 0)
+  if (__any_sync(0xFFFFFFFFu, top > row.m + 8.0f || ratio != 1.0f)) {
+    const float m2 = fmaxf(row.m, top), f = m2 == -INFINITY ? 1.0f : ex2(row.m - m2);
+    if (!first) rescale_o<HD>(o_at, f * ratio);
+    row.l *= f;
+    row.m = m2;
+  }
+  const float base = row.m == -INFINITY ? 0.0f : row.m;
+  const uint64_t base2 = f32x2(-base, -base);
+  uint64_t sum[2] = {0, 0};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int k = 32 * w + 2 * i;
+      const float c = scale(UNIFORM ? 0 : k >> 4);
+      float e0, e1;
+      f32x2_parts(fma2(f32x2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f32x2(c, c), base2), e0, e1);
+      e0 = ex2(e0);
+      e1 = ex2(e1);
+      if (MASKED) {
+        e0 = see[w] >> (2 * i) & 1u ? e0 : 0.0f;
+        e1 = see[w] >> (2 * i + 1) & 1u ? e1 : 0.0f;
+      }
+      sum[i & 1] = add2(sum[i & 1], f32x2(e0, e1));
+      pk[i] = pack_p<BF16>(e0, e1);
+    }
+    tmem_st16(s_at + 16 * w, pk);
+    if (w & 1) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      ready(w >> 1);
+    }
+  }
+  float lo, hi;
+  f32x2_parts(add2(sum[0], sum[1]), lo, hi);
+  row.l += lo + hi;
 }
 
 }  // namespace dt

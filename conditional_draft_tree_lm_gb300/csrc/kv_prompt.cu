@@ -10,7 +10,10 @@
 // cores, and about as many cycles of exponentials and their surroundings on the
 // ordinary cores; the two overlap (kv_flash.cuh).  One warp feeds K and V by TMA
 // into a ring of five stages, one thread issues the products, two warpgroups do
-// the softmax of a tile each.  CTAs are started heaviest first.
+// the softmax of a tile each.  One CTA for each SM walks a fixed list of items
+// (heaviest first, in alternating directions), so that one item's loads and first
+// products run under the last one's softmax and output (a launch of one CTA an
+// item spent half of its time there on prompts of 1k).
 //
 // P is rounded to bf16 (operands of one product have one type, and V is bf16):
 // 2^-8 relative a weight at most, as the rounding of the output itself.
@@ -27,10 +30,12 @@ namespace dt {
 namespace {
 
 constexpr int kStages = 5;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10, kCleanWarps = 1;
-constexpr int kPromptThreads = 32 * (kCleanWarp + kCleanWarps);
-// Tiles of which some row does not see all: keys behind the first of a CTA's (at most 256) positions
-// lie in three at most, so each has a barrier and a word of its own.
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10;
+constexpr int kPromptThreads = 384;  // (the last warp only completes the third warpgroup)
+// Registers: 384 threads start with 168; the softmax's 256 go to 208 and the others' 128 to 80 (63488 of 64512).
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
+// Tiles of which some row does not see all: keys behind the first of an item's (at most 256) positions
+// lie in three at most, so each has barriers and a word of its own.
 constexpr int kMaskedTiles = 3;
 
 struct PromptParams {
@@ -39,7 +44,7 @@ struct PromptParams {
   const int32_t* row_start;
   int64_t n_rows, out_row_stride, out_head_stride;
   int n_seq, n_q, n_kv, group, positions;  // positions: of a tile (128 / group)
-  int slots;                               // CTAs per key/value head
+  int slots;                               // items per key/value head
   float c;                                 // scale * log2(e)
 };
 
@@ -57,6 +62,47 @@ DT_DEVINL void tma_load_3d(uint32_t dst, const void* tmap, uint64_t* bar, int x,
       : "memory");
 }
 
+// Two row tiles of a sequence, as every role sees them.
+struct PromptItem {
+  int kvh, row0, len, pos0;  // row0: the sequence's first row
+  int n_tiles[2], n;         // key tiles of each row tile
+  int masked0;               // the first key tile that holds a key behind pos0
+};
+
+// The i-th item of this CTA, if there is one left (an item may be empty: n = 0).
+// Sequence q's places stand from start_q / span + q on: at least as many as it
+// needs, and found without a sum.
+DT_DEVINL bool prompt_item(const PromptParams& p, int i, PromptItem& x) {
+  const int n = p.slots * p.n_kv, grid = static_cast<int>(gridDim.x);
+  if (static_cast<int64_t>(i) * grid >= n) return false;
+  const int at = i * grid + ((i & 1) ? grid - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
+  x.n = 0;
+  x.n_tiles[0] = x.n_tiles[1] = 0;
+  if (at >= n) return true;  // (the last round may be short; it is the last)
+  x.kvh = at % p.n_kv;
+  const int slot = p.slots - 1 - at / p.n_kv, span = 2 * p.positions;
+  const int first = __ldg(p.row_start);
+  int lo = 0, hi = p.n_seq;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((__ldg(p.row_start + mid) - first) / span + mid <= slot) lo = mid; else hi = mid;
+  }
+  const int64_t a = __ldg(p.row_start + lo), b = __ldg(p.row_start + lo + 1);
+  const int64_t pos0 = (slot - ((a - first) / span + lo)) * static_cast<int64_t>(span);
+  if (a < 0 || b > p.n_rows || pos0 < 0 || pos0 >= b - a) return true;
+  x.row0 = static_cast<int>(a);
+  x.len = static_cast<int>(b - a);
+  x.pos0 = static_cast<int>(pos0);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int from = x.pos0 + t * p.positions;
+    x.n_tiles[t] = from < x.len ? (min(x.len, from + p.positions) + kKeyTile - 1) / kKeyTile : 0;
+  }
+  x.n = max(x.n_tiles[0], x.n_tiles[1]);
+  x.masked0 = (x.pos0 + 1) / kKeyTile;
+  return true;
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     k_prompt(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -66,249 +112,218 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Smem::kBars);
   uint64_t* empty = full + kStages;
-  uint64_t* q_full = empty + kStages;
-  uint64_t* s_full = q_full + 1;  // [2]
-  uint64_t* p_full = s_full + 2;  // [2]
-  uint64_t* o_full = p_full + 2;  // [2]
-  uint64_t* clean = o_full + 2;   // [kMaskedTiles] a masked tile's values are clean
+  uint64_t* q_full = empty + kStages;      // [2]
+  uint64_t* q_free = q_full + 2;           // [2] the item's products with this Q are done
+  uint64_t* s_full = q_free + 2;           // [2]
+  uint64_t* p_full = s_full + 2;           // [2][2] halves of P
+  uint64_t* o_full = p_full + 4;           // [2]
+  uint64_t* clean = o_full + 2;            // [kMaskedTiles] a masked tile's values are clean
   uint64_t* dirty = clean + kMaskedTiles;  // [kMaskedTiles] its values are there to be cleaned
-  uint32_t* bad_key = reinterpret_cast<uint32_t*>(dirty + kMaskedTiles);  // [kMaskedTiles][4] keys of the masked tiles whose values are not finite
+  uint64_t* told = dirty + kMaskedTiles;   // the softmax has read bad_key, which may be cleared
+  uint32_t* bad_key = reinterpret_cast<uint32_t*>(told + 1);  // [kMaskedTiles][4] keys of the masked tiles whose values are not finite
   __shared__ uint32_t tmem_slot;
-  __shared__ int s_seq[3];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int kvh = blockIdx.x % p.n_kv, slot = p.slots - 1 - static_cast<int>(blockIdx.x / p.n_kv);
-  const int span = 2 * p.positions;  // positions of a CTA
-
-  // Sequence i's CTAs stand from start_i / span + i on: at least as many places as it needs, found without a sum.
-  if (tid == 0) s_seq[2] = 0;
   if (warp == kMmaWarp) tmem_alloc(&tmem_slot, 512);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(q_full, 1);
     for (int t = 0; t < 2; ++t) {
+      mbar_init(&q_full[t], 1);
+      mbar_init(&q_free[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
+      mbar_init(&p_full[2 * t], 4);
+      mbar_init(&p_full[2 * t + 1], 4);
       mbar_init(&o_full[t], 1);
     }
     for (int i = 0; i < kMaskedTiles; ++i) {
-      mbar_init(&clean[i], kCleanWarps);
+      mbar_init(&clean[i], 1);
       mbar_init(&dirty[i], 1);
     }
+    mbar_init(told, 8);
     for (int i = 0; i < 4 * kMaskedTiles; ++i) bad_key[i] = 0;
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  {
-    const int first = p.row_start[0];
-    for (int i = tid; i < p.n_seq; i += kPromptThreads) {
-      const int64_t a = p.row_start[i], b = p.row_start[i + 1];
-      const int64_t at = (a - first) / span + i;
-      if (slot >= at && slot < (b - first) / span + i + 1 && a >= 0 && b <= p.n_rows && (slot - at) * span < b - a) {
-        s_seq[0] = static_cast<int>(a);
-        s_seq[1] = static_cast<int>(b - a);
-        s_seq[2] = static_cast<int>(slot - at) + 1;
-      }
-    }
-  }
-  __syncthreads();
   const uint32_t tmem = tmem_slot;
-  const int row0 = s_seq[0], len = s_seq[1], block = s_seq[2] - 1;
-  if (block >= 0) {
-    const int pos0 = block * span;
-    // key tiles that each row tile walks, and the first one of which some row does not see all
-    int n_tiles[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int a = pos0 + t * p.positions;
-      n_tiles[t] = a < len ? (min(len, a + p.positions) + kKeyTile - 1) / kKeyTile : 0;
-    }
-    const int n = max(n_tiles[0], n_tiles[1]);
-    const int masked0 = (pos0 + 1) / kKeyTile;  // tiles from here on hold a key behind pos0
-    const uint32_t q_s = smem_u32(smem + Smem::kQ), ring = smem_u32(smem + Smem::kRing);
+  const uint32_t q_s = smem_u32(smem + Smem::kQ), ring = smem_u32(smem + Smem::kRing);
+  PromptItem it;
 
-    if (warp == kLoadWarp) {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(q_full, 2u * (HD / 64) * 128u * p.group * p.positions);
-        for (int t = 0; t < 2; ++t)
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kLoadWarp && lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      int q_use[2] = {0, 0};
+      bool ok = true;
+      for (int i = 0; ok && prompt_item(p, i, it); ++i) {
+        auto load_q = [&](int t) {
+          if (it.n_tiles[t] == 0) return;
+          ok = ok && mbar_wait(&q_free[t], (q_use[t]++ & 1) ^ 1, nullptr);
+          if (!ok) return;
+          mbar_arrive_expect_tx(&q_full[t], (HD / 64) * 128u * p.group * p.positions);
           for (int h = 0; h < HD / 64; ++h)
-            tma_load_3d(q_s + t * Smem::kOperand + h * kHalfBytes, &tm_q, q_full, h * 64, kvh * p.group,
-                        row0 + pos0 + t * p.positions);
+            tma_load_3d(q_s + t * Smem::kOperand + h * kHalfBytes, &tm_q, &q_full[t], h * 64, it.kvh * p.group,
+                        it.row0 + it.pos0 + t * p.positions);
+        };
+        load_q(0);
         // K(0), V(0), K(1), V(1), ...
-        uint32_t stage = 0, phase = 0;
-        for (int i = 0; i < 2 * n; ++i) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, nullptr)) break;
+        for (int x = 0; x < 2 * it.n && ok; ++x) {
+          ok = mbar_wait(&empty[stage], phase ^ 1u, nullptr);
+          if (!ok) break;
           mbar_arrive_expect_tx(&full[stage], Smem::kOperand);
           for (int h = 0; h < HD / 64; ++h)
-            tma_load_3d(ring + stage * Smem::kOperand + h * kHalfBytes, (i & 1) ? &tm_v : &tm_k, &full[stage], h * 64, kvh,
-                        row0 + (i >> 1) * kKeyTile);
+            tma_load_3d(ring + stage * Smem::kOperand + h * kHalfBytes, (x & 1) ? &tm_v : &tm_k, &full[stage], h * 64, it.kvh,
+                        it.row0 + (x >> 1) * kKeyTile);
           if (++stage == kStages) stage = 0, phase ^= 1u;
+          if (x == 0) load_q(1);
         }
       }
-    } else if (warp == kMmaWarp) {
-      if (lane == 0) {
-        auto full_wait = [&](int i) { return mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr); };
-        auto at = [&](int i) { return ring + (i % kStages) * Smem::kOperand; };
-        bool ok = mbar_wait(q_full, 0, nullptr) && full_wait(0);
-        if (ok) {
-          tc_fence_after();
+    } else if (warp == kMmaWarp && lane == 0) {
+      int load = 0;  // ring entries consumed
+      int q_use[2] = {0, 0}, p_use[2] = {0, 0}, masked_use[kMaskedTiles] = {0, 0, 0};
+      bool ok = true;
+      auto full_wait = [&](int i) { ok = ok && mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr); };
+      auto at = [&](int i) { return ring + (i % kStages) * Smem::kOperand; };
+      for (int i = 0; ok && prompt_item(p, i, it); ++i) {
+        if (it.n == 0) continue;
+        full_wait(load);
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (n_tiles[t] > 0) {
-              issue_qk<HD, true>(tmem + t * 128, q_s + t * Smem::kOperand, at(0));
-              tc_commit(&s_full[t]);
-            }
-          tc_commit(&empty[0]);
+        for (int t = 0; t < 2; ++t) {
+          if (it.n_tiles[t] == 0) continue;
+          ok = ok && mbar_wait(&q_full[t], q_use[t]++ & 1, nullptr);
+          if (!ok) break;
+          tc_fence_after();
+          issue_qk<HD, true>(tmem + t * 128, q_s + t * Smem::kOperand, at(load));
+          tc_commit(&s_full[t]);
+          if (it.n_tiles[t] == 1) tc_commit(&q_free[t]);
         }
-        for (int j = 0; j < n && ok; ++j) {
-          const int vi = 2 * j + 1, ki = 2 * j + 2;
+        if (ok) tc_commit(&empty[load % kStages]);
+        for (int j = 0; j < it.n && ok; ++j) {
+          const int vi = load + 2 * j + 1, ki = vi + 1, m = j - it.masked0;
+          const bool more = j + 1 < it.n;
           // (the cleaning warp cannot wait on the ring itself: it would meet its stage in some earlier turn)
-          ok = full_wait(vi);
-          if (ok && j >= masked0) mbar_arrive(&dirty[j - masked0]);
-          ok = ok && (j + 1 >= n || full_wait(ki));
-          if (ok && j >= masked0) ok = mbar_wait(&clean[j - masked0], 0, nullptr);
+          full_wait(vi);
+          if (ok && m >= 0) mbar_arrive(&dirty[m]);
+          if (more) full_wait(ki);
+          if (m >= 0) ok = ok && mbar_wait(&clean[m], masked_use[m]++ & 1, nullptr);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (!ok || j >= n_tiles[t]) continue;
-            if (!mbar_wait(&p_full[t], j & 1, nullptr)) {
-              ok = false;
-              continue;
+            if (!ok || j >= it.n_tiles[t]) continue;
+            const uint32_t turn = p_use[t]++ & 1;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              ok = ok && mbar_wait(&p_full[2 * t + half], turn, nullptr);
+              tc_fence_after();
+              if (ok) issue_pv<HD, true>(tmem + 256 + t * 128, tmem + t * 128, at(vi), j == 0, half);
             }
-            tc_fence_after();
-            issue_pv<HD, true>(tmem + 256 + t * 128, tmem + t * 128, at(vi), j == 0);
-            if (j + 1 < n_tiles[t]) {
+            if (!ok) continue;
+            if (j + 1 < it.n_tiles[t]) {
               issue_qk<HD, true>(tmem + t * 128, q_s + t * Smem::kOperand, at(ki));
               tc_commit(&s_full[t]);
+              if (j + 2 == it.n_tiles[t]) tc_commit(&q_free[t]);
             } else {
               tc_commit(&o_full[t]);
             }
           }
           if (ok) {
             tc_commit(&empty[vi % kStages]);
-            if (j + 1 < n) tc_commit(&empty[ki % kStages]);
+            if (more) tc_commit(&empty[ki % kStages]);
           }
         }
+        load += 2 * it.n;
       }
-    } else if (warp >= kCleanWarp) {
+    } else if (warp == kCleanWarp) {
       // values of the masked tiles, 16 bytes of each half at a time
-      const int ct = tid - kCleanWarp * 32;
-      for (int j = masked0; j < n; ++j) {
-        const int i = 2 * j + 1;
-        if (!mbar_wait(&dirty[j - masked0], 0, nullptr)) break;
-        uint8_t* v = smem + Smem::kRing + (i % kStages) * Smem::kOperand;
-        uint32_t* bad = bad_key + (j - masked0) * 4;
-        const int valid = len - j * kKeyTile;
-        for (int x = ct; x < kKeyTile * 8; x += 32 * kCleanWarps) {
-          const int key = x >> 3;
-          uint4* at[HD / 64];
-          bool nan = false;
-#pragma unroll
-          for (int h = 0; h < HD / 64; ++h) {
-            at[h] = reinterpret_cast<uint4*>(v + h * kHalfBytes + x * 16);  // (the swizzle stays within a key's row)
-            const uint4 w = *at[h];
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              nan |= (ws[k] & 0x7F80u) == 0x7F80u || (ws[k] & 0x7F800000u) == 0x7F800000u;
-          }
-          if (key >= valid || nan) {
-#pragma unroll
-            for (int h = 0; h < HD / 64; ++h) *at[h] = make_uint4(0, 0, 0, 0);
-            if (key < valid) atomicOr(&bad[key >> 5], 1u << (key & 31));
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&clean[j - masked0]);
-      }
-    } else {
-      // softmax: warpgroup t, a row a thread
-      const int t = warp >> 2, r = tid & 127;
-      const int pos = pos0 + t * p.positions + r / p.group, head = kvh * p.group + r % p.group;
-      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t s_at = tmem + t * 128 + lanes, o_at = tmem + 256 + t * 128 + lanes;
-      const float c = p.c;
-      float m = -INFINITY, l = 0.0f;  // m: the maximum in use, in powers of two
+      int items = 0, use[kMaskedTiles] = {0, 0, 0}, load = 0;
       bool ok = true;
-      for (int j = 0; j < n_tiles[t]; ++j) {
-        if (!mbar_wait(&s_full[t], j & 1, nullptr)) {
-          ok = false;
-          break;
+      for (int i = 0; ok && prompt_item(p, i, it); ++i) {
+        if (it.n == 0) continue;
+        if (items++ > 0) {  // the words of the last item have been read
+          ok = mbar_wait(told, (items & 1), nullptr);
+          if (lane < 4 * kMaskedTiles) bad_key[lane] = 0;
+          __syncwarp();
         }
-        tc_fence_after();
-        uint32_t s[128];
+        for (int j = max(it.masked0, 0); j < it.n && ok; ++j) {
+          const int m = j - it.masked0;
+          ok = mbar_wait(&dirty[m], use[m]++ & 1, nullptr);
+          if (!ok) break;
+          uint8_t* v = smem + Smem::kRing + ((load + 2 * j + 1) % kStages) * Smem::kOperand;
+          uint32_t* bad = bad_key + m * 4;
+          const int valid = it.len - j * kKeyTile;
+          for (int x = lane; x < kKeyTile * 8; x += 32) {
+            const int key = x >> 3;
+            uint4* at[HD / 64];
+            bool nan = false;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) tmem_ld32(s_at + 32 * w, s + 32 * w);
-        tmem_wait_ld();
-        const bool masked = (j + 1) * kKeyTile > pos0 + t * p.positions + 1;  // (for the tile's first row)
-        const int seen = pos + 1 - j * kKeyTile;                              // of this tile's keys, by this row
-        if (masked) {
-          const float out = c >= 0.0f ? -INFINITY : INFINITY;
+            for (int h = 0; h < HD / 64; ++h) {
+              at[h] = reinterpret_cast<uint4*>(v + h * kHalfBytes + x * 16);  // (the swizzle stays within a key's row)
+              const uint4 w = *at[h];
+              const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= seen) s[i] = __float_as_uint(out);
-        }
-        float top;
-        if (c >= 0.0f) {
-          float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 128; ++i) x[i & 3] = fmaxf(x[i & 3], __uint_as_float(s[i]));
-          top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-        } else {
-          float x[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
-#pragma unroll
-          for (int i = 0; i < 128; ++i) x[i & 3] = fminf(x[i & 3], __uint_as_float(s[i]));
-          top = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
-        }
-        top = c == 0.0f ? 0.0f : top * c;
-        // (an infinite logit would make exp2(inf - inf): NaN, as the formula has it)
-        const bool grow = top > m + 8.0f;
-        if (__any_sync(0xFFFFFFFFu, grow)) {
-          const float m2 = fmaxf(m, top), f = m2 == -INFINITY ? 1.0f : ex2(m - m2);
-          if (j > 0) rescale_o<HD>(o_at, f);
-          l *= f;
-          m = m2;
-        }
-        const float base = m == -INFINITY ? 0.0f : m;
-        float sum[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float e0 = ex2(fmaf(__uint_as_float(s[32 * w + 2 * i]), c, -base));
-            float e1 = ex2(fmaf(__uint_as_float(s[32 * w + 2 * i + 1]), c, -base));
-            if (masked) {
-              if (32 * w + 2 * i >= seen) e0 = 0.0f;
-              if (32 * w + 2 * i + 1 >= seen) e1 = 0.0f;
+              for (int k = 0; k < 4; ++k)
+                nan |= (ws[k] & 0x7F80u) == 0x7F80u || (ws[k] & 0x7F800000u) == 0x7F800000u;
             }
-            sum[(2 * i) & 3] += e0;
-            sum[(2 * i + 1) & 3] += e1;
-            pk[i] = pack_p<true>(e0, e1);
+            if (key >= valid || nan) {
+#pragma unroll
+              for (int h = 0; h < HD / 64; ++h) *at[h] = make_uint4(0, 0, 0, 0);
+              if (key < valid) atomicOr(&bad[key >> 5], 1u << (key & 31));
+            }
           }
-          tmem_st16(s_at + 16 * w, pk);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&clean[m]);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t]);
+        load += 2 * it.n;
       }
-      if (n_tiles[t] > 0 && ok && mbar_wait(&o_full[t], 0, nullptr)) {
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // softmax: warpgroup t, a row a thread
+    const int t = warp >> 2, r = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + t * 128 + lanes, o_at = tmem + 256 + t * 128 + lanes;
+    const float c = p.c;
+    int s_use = 0, o_use = 0;
+    bool ok = true;
+    auto scale = [&](int) { return c; };
+    auto ready = [&](int half) {
+      if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
+    };
+    for (int i = 0; ok && prompt_item(p, i, it); ++i) {
+      if (it.n == 0) continue;
+      const int n = it.n_tiles[t];
+      const int from = it.pos0 + t * p.positions, pos = from + r / p.group, head = it.kvh * p.group + r % p.group;
+      SoftmaxRow row;
+      for (int j = 0; j < n && ok; ++j) {
+        ok = mbar_wait(&s_full[t], s_use++ & 1, nullptr);
+        if (!ok) break;
         tc_fence_after();
-        // rows that see a key whose value is not finite (all cleaned tiles lie behind every o_full)
-        for (int j = masked0; j < n_tiles[t]; ++j)
+        const int seen = pos + 1 - j * kKeyTile;  // of this tile's keys, by this row
+        const uint32_t see[4] = {first_bits(seen, 0), first_bits(seen, 1), first_bits(seen, 2), first_bits(seen, 3)};
+        if ((j + 1) * kKeyTile > from + 1)
+          softmax_tile<HD, true, true, true>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
+        else
+          softmax_tile<HD, true, true, false>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
+      }
+      if (n > 0) {
+        ok = ok && mbar_wait(&o_full[t], o_use++ & 1, nullptr);
+        tc_fence_after();
+        // rows that see a key whose value is not finite (an item's cleaning is behind its o_full)
+        for (int j = max(it.masked0, 0); j < n; ++j)
 #pragma unroll
           for (int w = 0; w < 4; ++w)
-            if (bad_key[(j - masked0) * 4 + w] & first_bits(pos + 1 - j * kKeyTile, w)) l = NAN;
-        const bool live = r < p.group * p.positions && pos < len;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        __nv_bfloat16* out = p.out + static_cast<int64_t>(row0 + pos) * p.out_row_stride + head * p.out_head_stride;
+            if (bad_key[(j - it.masked0) * 4 + w] & first_bits(pos + 1 - j * kKeyTile, w)) row.l = NAN;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(told);
+      if (n > 0 && ok) {
+        const bool live = r < p.group * p.positions && pos < it.len;
+        const float inv = row.l == 0.0f ? 0.0f : 1.0f / row.l;
+        __nv_bfloat16* out = p.out + static_cast<int64_t>(it.row0 + pos) * p.out_row_stride + head * p.out_head_stride;
 #pragma unroll
         for (int x = 0; x < HD; x += 32) {
           uint32_t v[32];
@@ -316,18 +331,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           tmem_wait_ld();
           if (live) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
+            for (int k = 0; k < 32; k += 8) {
               uint4 w;
-              w.x = pack_p<true>(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
-              w.y = pack_p<true>(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
-              w.z = pack_p<true>(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv);
-              w.w = pack_p<true>(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv);
-              *reinterpret_cast<uint4*>(out + x + i) = w;
+              w.x = pack_p<true>(__uint_as_float(v[k]) * inv, __uint_as_float(v[k + 1]) * inv);
+              w.y = pack_p<true>(__uint_as_float(v[k + 2]) * inv, __uint_as_float(v[k + 3]) * inv);
+              w.z = pack_p<true>(__uint_as_float(v[k + 4]) * inv, __uint_as_float(v[k + 5]) * inv);
+              w.w = pack_p<true>(__uint_as_float(v[k + 6]) * inv, __uint_as_float(v[k + 7]) * inv);
+              *reinterpret_cast<uint4*>(out + x + k) = w;
             }
           }
         }
+        tc_fence_before();  // (O has been read before the next item's first product writes it)
         if (live && p.lse)
-          p.lse[static_cast<int64_t>(row0 + pos) * p.n_q + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+          p.lse[static_cast<int64_t>(it.row0 + pos) * p.n_q + head] = row.l == 0.0f ? -INFINITY : (row.m + log2f(row.l)) * kLn2;
       }
     }
   }
@@ -343,7 +359,8 @@ template <int HD>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PromptParams& p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(k_prompt<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem<HD>::kBytes);
   if (e != cudaSuccess) return e;
-  k_prompt<HD><<<static_cast<unsigned>(p.slots) * p.n_kv, kPromptThreads, PromptSmem<HD>::kBytes, st>>>(q, k, v, p);
+  const int items = p.slots * p.n_kv;
+  k_prompt<HD><<<items < kSms ? items : kSms, kPromptThreads, PromptSmem<HD>::kBytes, st>>>(q, k, v, p);
   return cudaGetLastError();
 }
 

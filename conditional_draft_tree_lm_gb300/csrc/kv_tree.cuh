@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
               ok = mbar_wait(&p_full[t], s_use[t]++ & 1, nullptr);
               if (!ok) break;
               tc_fence_after();
-              issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, at(vi), j == 0);
+              issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, at(vi), j == 0, 0);
+              issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, at(vi), j == 0, 1);
               if (more) {
                 issue_qk<HD, false>(tmem + t * 128, q_s + t * Smem::kOperand, at(ki));
                 tc_commit(&s_full[t]);

@@ -73,16 +73,21 @@ DT_DEVINL void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint3
       : "memory");
 }
 
-// V as operand B, MN-major in the 128-byte swizzle: groups of 64 channels
-// (128 bytes a key) `group_bytes` apart, groups of 8 keys 1024 bytes apart.
-DT_DEVINL uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t group_bytes) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(group_bytes >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// Operand descriptors in the 128-byte swizzle, to which a byte offset inside the
+// operand is added as off >> 4.  Rows of 64 channels, K-major (Q, K): groups of 8
+// rows 1024 bytes apart.  V as operand B, MN-major: groups of 64 channels (128
+// bytes a key) kHalfBytes apart, groups of 8 keys 1024 bytes apart.
+constexpr uint32_t kHalfBytes = 128 * 128;
+DT_DEVINL uint64_t flash_desc(uint32_t saddr, bool mn) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (mn ? static_cast<uint64_t>(kHalfBytes >> 4) << 16 : 0ull) |
+         static_cast<uint64_t>(1024u >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+
+// One lane of a converged warp.
+DT_DEVINL bool elect_one() {
+  uint32_t pred;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(pred));
+  return pred != 0;
 }
 
 // kind::f16 with fp32 D; BF16: both operands bf16, else both fp16; b_mn: B is MN-major.
@@ -92,27 +97,28 @@ DT_HOST_DEVICE_INLINE uint32_t idesc_flash(uint32_t M, uint32_t N, bool b_mn) {
 }
 
 // A row tile's (or key tile's) operand in shared memory: halves of 64 channels, 128 rows of 128 bytes, swizzled.
-constexpr uint32_t kHalfBytes = 128 * 128;
 template <int HD>
 constexpr uint32_t kOperandBytes = HD / 64 * kHalfBytes;
 
-// S = Q K^T and O (+)= P V of one tile; issued by one thread.
+// S = Q K^T and O (+)= P V of one tile; issued by one lane, with operands that the
+// whole warp has computed (so that they stand in uniform registers: with one lane
+// walking the tiles by itself the issue, not the tensor core, was the bound).
 template <int HD, bool BF16>
-DT_DEVINL void issue_qk(uint32_t s_tmem, uint32_t q, uint32_t k) {
+DT_DEVINL void issue_qk(uint32_t s_tmem, uint64_t q, uint64_t k) {
   const uint32_t idesc = idesc_flash<BF16>(128, kKeyTile, false);
 #pragma unroll
   for (int i = 0; i < HD / 16; ++i) {
-    const uint32_t off = (i >> 2) * kHalfBytes + (i & 3) * 32;
-    tc_mma_bf16(s_tmem, sdesc_k_sw128(q + off), sdesc_k_sw128(k + off), idesc, i != 0);
+    const uint32_t off = ((i >> 2) * kHalfBytes + (i & 3) * 32) >> 4;
+    tc_mma_bf16(s_tmem, q + off, k + off, idesc, i != 0);
   }
 }
 template <int HD, bool BF16>  // half 0 or 1 of the keys
-DT_DEVINL void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t v, bool first, int half) {
+DT_DEVINL void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint64_t v, bool first, int half) {
   const uint32_t idesc = idesc_flash<BF16>(128, HD, true);
 #pragma unroll
   for (int k = 0; k < kKeyTile / 32; ++k) {
     const int i = half * (kKeyTile / 32) + k;
-    tc_mma_ts(o_tmem, p_tmem + i * 8, sdesc_mn_sw128(v + i * 2048, kHalfBytes), idesc, !(first && i == 0));
+    tc_mma_ts(o_tmem, p_tmem + i * 8, v + (i * 2048 >> 4), idesc, !(first && i == 0));
   }
 }
 
@@ -164,6 +170,25 @@ DT_DEVINL uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// A warp's 32 rows x 64 channels of bf16, one row a lane (w: 8 pieces of 16 bytes),
+// to global memory through 4 KB of the warp's own shared memory: eight lanes write
+// a row's 128 bytes together, where a lane writing its own row would touch 32 lines
+// an instruction.  row_of(r): where the lane r's row goes, null for nowhere.
+template <class RowOf>
+DT_DEVINL void store_rows(uint8_t* mine, const uint4 (&w)[8], RowOf row_of) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();  // (the last rows have been read)
+#pragma unroll
+  for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(mine + lane * 128 + ((k ^ (lane & 7)) << 4)) = w[k];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = i * 4 + (lane >> 3), k = lane & 7;
+    __nv_bfloat16* to = row_of(r);
+    if (to) *reinterpret_cast<uint4*>(to + 8 * k) = *reinterpret_cast<const uint4*>(mine + r * 128 + ((k ^ (r & 7)) << 4));
+  }
 }
 
 // The running softmax of one row.
@@ -228,20 +253,28 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     uint32_t pk[16];
+    // (of a masked tile, most 32-key parts are seen by all of a warp's rows or by none)
+    const bool none = MASKED && __all_sync(0xFFFFFFFFu, see[w] == 0u);
+    const bool all = !MASKED || __all_sync(0xFFFFFFFFu, see[w] == 0xFFFFFFFFu);
+    if (none) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int k = 32 * w + 2 * i;
-      const float c = scale(UNIFORM ? 0 : k >> 4);
-      float e0, e1;
-      f32x2_parts(fma2(f32x2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f32x2(c, c), base2), e0, e1);
-      e0 = ex2(e0);
-      e1 = ex2(e1);
-      if (MASKED) {
-        e0 = see[w] >> (2 * i) & 1u ? e0 : 0.0f;
-        e1 = see[w] >> (2 * i + 1) & 1u ? e1 : 0.0f;
+      for (int i = 0; i < 16; ++i) pk[i] = 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int k = 32 * w + 2 * i;
+        const float c = scale(UNIFORM ? 0 : k >> 4);
+        float e0, e1;
+        f32x2_parts(fma2(f32x2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f32x2(c, c), base2), e0, e1);
+        e0 = ex2(e0);
+        e1 = ex2(e1);
+        if (!all) {
+          e0 = see[w] >> (2 * i) & 1u ? e0 : 0.0f;
+          e1 = see[w] >> (2 * i + 1) & 1u ? e1 : 0.0f;
+        }
+        sum[i & 1] = add2(sum[i & 1], f32x2(e0, e1));
+        pk[i] = pack_p<BF16>(e0, e1);
       }
-      sum[i & 1] = add2(sum[i & 1], f32x2(e0, e1));
-      pk[i] = pack_p<BF16>(e0, e1);
     }
     tmem_st16(s_at + 16 * w, pk);
     if (w & 1) {

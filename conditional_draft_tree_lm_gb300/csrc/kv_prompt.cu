@@ -9,7 +9,7 @@
 // What bounds it: 4 * head_dim flops for every visible (row, key) on the tensor
 // cores, and about as many cycles of exponentials and their surroundings on the
 // ordinary cores; the two overlap (kv_flash.cuh).  One warp feeds K and V by TMA
-// into a ring of five stages, one thread issues the products, two warpgroups do
+// into a ring of four stages, one thread issues the products, two warpgroups do
 // the softmax of a tile each.  One CTA for each SM walks a fixed list of items
 // (heaviest first, in alternating directions), so that one item's loads and first
 // products run under the last one's softmax and output (a launch of one CTA an
@@ -29,9 +29,9 @@
 namespace dt {
 namespace {
 
-constexpr int kStages = 5;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10;
-constexpr int kPromptThreads = 384;  // (the last warp only completes the third warpgroup)
+constexpr int kStages = 4;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10, kCleanWarps = 2;
+constexpr int kPromptThreads = 384;
 // Registers: 384 threads start with 168; the softmax's 256 go to 208 and the others' 128 to 80 (63488 of 64512).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
 // Tiles of which some row does not see all: keys behind the first of an item's (at most 256) positions
@@ -51,7 +51,7 @@ struct PromptParams {
 template <int HD>
 struct PromptSmem {
   static constexpr uint32_t kOperand = kOperandBytes<HD>;
-  static constexpr uint32_t kQ = 0, kRing = 2 * kOperand, kBars = kRing + kStages * kOperand;
+  static constexpr uint32_t kQ = 0, kRing = 2 * kOperand, kOut = kRing + kStages * kOperand, kBars = kOut + 8 * 4096;
   static constexpr uint32_t kBytes = kBars + 512 + 1024;  // + alignment
 };
 
@@ -87,12 +87,12 @@ DT_DEVINL bool prompt_item(const PromptParams& p, int i, PromptItem& x) {
     const int mid = (lo + hi) >> 1;
     if ((__ldg(p.row_start + mid) - first) / span + mid <= slot) lo = mid; else hi = mid;
   }
-  const int64_t a = __ldg(p.row_start + lo), b = __ldg(p.row_start + lo + 1);
-  const int64_t pos0 = (slot - ((a - first) / span + lo)) * static_cast<int64_t>(span);
-  if (a < 0 || b > p.n_rows || pos0 < 0 || pos0 >= b - a) return true;
-  x.row0 = static_cast<int>(a);
-  x.len = static_cast<int>(b - a);
-  x.pos0 = static_cast<int>(pos0);
+  const int a = __ldg(p.row_start + lo), b = __ldg(p.row_start + lo + 1);
+  const int block = slot - ((a - first) / span + lo);
+  if (a < 0 || b < a || b > p.n_rows || block < 0 || block > (b - a) / span || block * span >= b - a) return true;
+  x.row0 = a;
+  x.len = b - a;
+  x.pos0 = block * span;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int from = x.pos0 + t * p.positions;
@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint32_t* bad_key = reinterpret_cast<uint32_t*>(told + 1);  // [kMaskedTiles][4] keys of the masked tiles whose values are not finite
   __shared__ uint32_t tmem_slot;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the same for a warp's lanes, and known to be)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   if (warp == kMmaWarp) tmem_alloc(&tmem_slot, 512);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&o_full[t], 1);
     }
     for (int i = 0; i < kMaskedTiles; ++i) {
-      mbar_init(&clean[i], 1);
+      mbar_init(&clean[i], kCleanWarps);
       mbar_init(&dirty[i], 1);
     }
     mbar_init(told, 8);
@@ -182,95 +183,108 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (x == 0) load_q(1);
         }
       }
-    } else if (warp == kMmaWarp && lane == 0) {
+    } else if (warp == kMmaWarp) {
+      const bool leader = elect_one();
       int load = 0;  // ring entries consumed
       int q_use[2] = {0, 0}, p_use[2] = {0, 0}, masked_use[kMaskedTiles] = {0, 0, 0};
       bool ok = true;
-      auto full_wait = [&](int i) { ok = ok && mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, nullptr));
+        tc_fence_after();
+      };
+      auto full_wait = [&](int i) { wait(&full[i % kStages], (i / kStages) & 1); };
       auto at = [&](int i) { return ring + (i % kStages) * Smem::kOperand; };
+      auto commit = [&](uint64_t* bar) {
+        if (leader) tc_commit(bar);
+      };
+      const uint64_t q_desc[2] = {flash_desc(q_s, false), flash_desc(q_s + Smem::kOperand, false)};
       for (int i = 0; ok && prompt_item(p, i, it); ++i) {
         if (it.n == 0) continue;
         full_wait(load);
+        uint64_t kd = flash_desc(at(load), false);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (it.n_tiles[t] == 0) continue;
-          ok = ok && mbar_wait(&q_full[t], q_use[t]++ & 1, nullptr);
+          wait(&q_full[t], q_use[t]++ & 1);
           if (!ok) break;
-          tc_fence_after();
-          issue_qk<HD, true>(tmem + t * 128, q_s + t * Smem::kOperand, at(load));
-          tc_commit(&s_full[t]);
-          if (it.n_tiles[t] == 1) tc_commit(&q_free[t]);
+          if (leader) issue_qk<HD, true>(tmem + t * 128, q_desc[t], kd);
+          commit(&s_full[t]);
+          if (it.n_tiles[t] == 1) commit(&q_free[t]);
         }
-        if (ok) tc_commit(&empty[load % kStages]);
+        if (ok) commit(&empty[load % kStages]);
         for (int j = 0; j < it.n && ok; ++j) {
           const int vi = load + 2 * j + 1, ki = vi + 1, m = j - it.masked0;
           const bool more = j + 1 < it.n;
-          // (the cleaning warp cannot wait on the ring itself: it would meet its stage in some earlier turn)
+          // (the cleaning warps cannot wait on the ring themselves: they would meet their stage in some earlier turn)
           full_wait(vi);
-          if (ok && m >= 0) mbar_arrive(&dirty[m]);
+          if (ok && m >= 0 && leader) mbar_arrive(&dirty[m]);
           if (more) full_wait(ki);
-          if (m >= 0) ok = ok && mbar_wait(&clean[m], masked_use[m]++ & 1, nullptr);
+          if (m >= 0) wait(&clean[m], masked_use[m]++ & 1);
+          const uint64_t vd = flash_desc(at(vi), true);
+          kd = flash_desc(at(ki), false);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (!ok || j >= it.n_tiles[t]) continue;
             const uint32_t turn = p_use[t]++ & 1;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              ok = ok && mbar_wait(&p_full[2 * t + half], turn, nullptr);
-              tc_fence_after();
-              if (ok) issue_pv<HD, true>(tmem + 256 + t * 128, tmem + t * 128, at(vi), j == 0, half);
-            }
+            wait(&p_full[2 * t], turn);
+            if (ok && leader) issue_pv<HD, true>(tmem + 256 + t * 128, tmem + t * 128, vd, j == 0, 0);
+            wait(&p_full[2 * t + 1], turn);
             if (!ok) continue;
+            if (leader) issue_pv<HD, true>(tmem + 256 + t * 128, tmem + t * 128, vd, j == 0, 1);
             if (j + 1 < it.n_tiles[t]) {
-              issue_qk<HD, true>(tmem + t * 128, q_s + t * Smem::kOperand, at(ki));
-              tc_commit(&s_full[t]);
-              if (j + 2 == it.n_tiles[t]) tc_commit(&q_free[t]);
+              if (leader) issue_qk<HD, true>(tmem + t * 128, q_desc[t], kd);
+              commit(&s_full[t]);
+              if (j + 2 == it.n_tiles[t]) commit(&q_free[t]);
             } else {
-              tc_commit(&o_full[t]);
+              commit(&o_full[t]);
             }
           }
           if (ok) {
-            tc_commit(&empty[vi % kStages]);
-            if (more) tc_commit(&empty[ki % kStages]);
+            commit(&empty[vi % kStages]);
+            if (more) commit(&empty[ki % kStages]);
           }
         }
         load += 2 * it.n;
       }
-    } else if (warp == kCleanWarp) {
-      // values of the masked tiles, 16 bytes of each half at a time
+    } else if (warp >= kCleanWarp) {
+      // values of the masked tiles: half of the keys a warp, a key's 16-byte pieces to eight lanes
+      const int cw = warp - kCleanWarp;
       int items = 0, use[kMaskedTiles] = {0, 0, 0}, load = 0;
       bool ok = true;
       for (int i = 0; ok && prompt_item(p, i, it); ++i) {
         if (it.n == 0) continue;
         if (items++ > 0) {  // the words of the last item have been read
           ok = mbar_wait(told, (items & 1), nullptr);
-          if (lane < 4 * kMaskedTiles) bad_key[lane] = 0;
+          if (lane < 2 * kMaskedTiles) bad_key[(lane >> 1) * 4 + cw * 2 + (lane & 1)] = 0;
           __syncwarp();
         }
-        for (int j = max(it.masked0, 0); j < it.n && ok; ++j) {
+        for (int j = it.masked0; j < it.n && ok; ++j) {
           const int m = j - it.masked0;
           ok = mbar_wait(&dirty[m], use[m]++ & 1, nullptr);
           if (!ok) break;
-          uint8_t* v = smem + Smem::kRing + ((load + 2 * j + 1) % kStages) * Smem::kOperand;
-          uint32_t* bad = bad_key + m * 4;
-          const int valid = it.len - j * kKeyTile;
-          for (int x = lane; x < kKeyTile * 8; x += 32) {
-            const int key = x >> 3;
-            uint4* at[HD / 64];
-            bool nan = false;
+          // (the swizzle stays within a key's 128 bytes)
+          uint8_t* v = smem + Smem::kRing + ((load + 2 * j + 1) % kStages) * Smem::kOperand + cw * 64 * 128 + lane * 16;
+          const int valid = it.len - j * kKeyTile - cw * 64 - (lane >> 3);  // of keys lane / 8, + 4, + 8, ...
+          // an exponent of ones carries into its half's top bit
+          uint32_t seen[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            seen[x] = 0;
 #pragma unroll
             for (int h = 0; h < HD / 64; ++h) {
-              at[h] = reinterpret_cast<uint4*>(v + h * kHalfBytes + x * 16);  // (the swizzle stays within a key's row)
-              const uint4 w = *at[h];
-              const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                nan |= (ws[k] & 0x7F80u) == 0x7F80u || (ws[k] & 0x7F800000u) == 0x7F800000u;
+              const uint4 w = *reinterpret_cast<const uint4*>(v + h * kHalfBytes + x * 512);
+              seen[x] |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+                         ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
             }
-            if (key >= valid || nan) {
+          }
 #pragma unroll
-              for (int h = 0; h < HD / 64; ++h) *at[h] = make_uint4(0, 0, 0, 0);
-              if (key < valid) atomicOr(&bad[key >> 5], 1u << (key & 31));
+          for (int x = 0; x < 16; ++x) {
+            const bool nan = (seen[x] & 0x80008000u) != 0, behind = 4 * x >= valid;
+            if (nan || behind) {
+#pragma unroll
+              for (int h = 0; h < HD / 64; ++h) *reinterpret_cast<uint4*>(v + h * kHalfBytes + x * 512) = make_uint4(0, 0, 0, 0);
+              const int key = cw * 64 + 4 * x + (lane >> 3);
+              if (!behind) atomicOr(&bad_key[m * 4 + (key >> 5)], 1u << (key & 31));
             }
           }
           fence_proxy_async_smem();
@@ -313,7 +327,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         ok = ok && mbar_wait(&o_full[t], o_use++ & 1, nullptr);
         tc_fence_after();
         // rows that see a key whose value is not finite (an item's cleaning is behind its o_full)
-        for (int j = max(it.masked0, 0); j < n; ++j)
+        for (int j = it.masked0; j < n; ++j)
 #pragma unroll
           for (int w = 0; w < 4; ++w)
             if (bad_key[(j - it.masked0) * 4 + w] & first_bits(pos + 1 - j * kKeyTile, w)) row.l = NAN;
@@ -323,23 +337,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (n > 0 && ok) {
         const bool live = r < p.group * p.positions && pos < it.len;
         const float inv = row.l == 0.0f ? 0.0f : 1.0f / row.l;
-        __nv_bfloat16* out = p.out + static_cast<int64_t>(it.row0 + pos) * p.out_row_stride + head * p.out_head_stride;
+        auto row_of = [&](int x) -> __nv_bfloat16* {  // the row of the warp's lane x
+          const int y = (warp & 3) * 32 + x, at = from + y / p.group;
+          if (y >= p.group * p.positions || at >= it.len) return nullptr;
+          return p.out + static_cast<int64_t>(it.row0 + at) * p.out_row_stride + (it.kvh * p.group + y % p.group) * p.out_head_stride;
+        };
 #pragma unroll
-        for (int x = 0; x < HD; x += 32) {
-          uint32_t v[32];
+        for (int x = 0; x < HD; x += 64) {
+          uint32_t v[64];
           tmem_ld32(o_at + x, v);
+          tmem_ld32(o_at + x + 32, v + 32);
           tmem_wait_ld();
-          if (live) {
+          uint4 w[8];
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              uint4 w;
-              w.x = pack_p<true>(__uint_as_float(v[k]) * inv, __uint_as_float(v[k + 1]) * inv);
-              w.y = pack_p<true>(__uint_as_float(v[k + 2]) * inv, __uint_as_float(v[k + 3]) * inv);
-              w.z = pack_p<true>(__uint_as_float(v[k + 4]) * inv, __uint_as_float(v[k + 5]) * inv);
-              w.w = pack_p<true>(__uint_as_float(v[k + 6]) * inv, __uint_as_float(v[k + 7]) * inv);
-              *reinterpret_cast<uint4*>(out + x + k) = w;
-            }
+          for (int k = 0; k < 8; ++k) {
+            w[k].x = pack_p<true>(__uint_as_float(v[8 * k]) * inv, __uint_as_float(v[8 * k + 1]) * inv);
+            w[k].y = pack_p<true>(__uint_as_float(v[8 * k + 2]) * inv, __uint_as_float(v[8 * k + 3]) * inv);
+            w[k].z = pack_p<true>(__uint_as_float(v[8 * k + 4]) * inv, __uint_as_float(v[8 * k + 5]) * inv);
+            w[k].w = pack_p<true>(__uint_as_float(v[8 * k + 6]) * inv, __uint_as_float(v[8 * k + 7]) * inv);
           }
+          store_rows(smem + Smem::kOut + warp * 4096, w, [&](int y) {
+            __nv_bfloat16* to = row_of(y);
+            return to ? to + x : nullptr;
+          });
         }
         tc_fence_before();  // (O has been read before the next item's first product writes it)
         if (live && p.lse)

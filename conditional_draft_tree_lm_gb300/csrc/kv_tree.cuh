@@ -127,14 +127,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
   uint64_t* empty = full + kTreeStages;
   uint64_t* q_full = empty + kTreeStages;  // [2]
   uint64_t* s_full = q_full + 2;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
+  uint64_t* p_full = s_full + 2;           // [2][2] halves of P
+  uint64_t* o_full = p_full + 4;
   TreeTile* tiles = reinterpret_cast<TreeTile*>(o_full + 2);  // [kTreeSlots]
   __shared__ uint32_t tmem_slot;
   __shared__ int scratch[4], s_start[128 + 1], s_last;
   __shared__ float s_max[2][kTreeConvWarps];
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the same for a warp's lanes, and known to be)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const dt_cache_attention_args& a = p.a;
   const int n_kv = p.c.n_kv;
 
@@ -147,7 +148,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 4);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
+      mbar_init(&p_full[2 * t], 4);
+      mbar_init(&p_full[2 * t + 1], 4);
       mbar_init(&o_full[t], 1);
     }
     fence_mbar_init();
@@ -177,44 +179,59 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
     const uint32_t q_s = smem_u32(smem + Smem::kQ), ring = smem_u32(smem + Smem::kRing);
 
     if (warp == kTreeMmaWarp) {
-      if (lane == 0) {
-        int count = 0;             // key tiles so far
-        int s_use[2] = {0, 0}, segs[2] = {0, 0};
-        bool ok = true;
-        auto full_wait = [&](int i) { return mbar_wait(&full[i % kTreeStages], (i / kTreeStages) & 1, nullptr); };
-        auto at = [&](int i) { return ring + (i % kTreeStages) * Smem::kOperand; };
-        while (ok && walk.next(p, sg)) {
-          const int n = sg.key_end - sg.key_begin;
-          ok = full_wait(2 * count);
-          for (int t = 0; t < sg.tiles && ok; ++t) {
-            ok = mbar_wait(&q_full[t], segs[t]++ & 1, nullptr);
-            if (!ok) break;
-            tc_fence_after();
-            issue_qk<HD, false>(tmem + t * 128, q_s + t * Smem::kOperand, at(2 * count));
-            tc_commit(&s_full[t]);
+      const bool leader = elect_one();
+      int count = 0;  // key tiles so far
+      int s_use[2] = {0, 0}, segs[2] = {0, 0};
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, nullptr));
+        tc_fence_after();
+      };
+      auto full_wait = [&](int i) { wait(&full[i % kTreeStages], (i / kTreeStages) & 1); };
+      auto at = [&](int i) { return ring + (i % kTreeStages) * Smem::kOperand; };
+      auto commit = [&](uint64_t* bar) {
+        if (leader) tc_commit(bar);
+      };
+      const uint64_t q_desc[2] = {flash_desc(q_s, false), flash_desc(q_s + Smem::kOperand, false)};
+      while (ok && walk.next(p, sg)) {
+        const int n = sg.key_end - sg.key_begin;
+        full_wait(2 * count);
+        uint64_t kd = flash_desc(at(2 * count), false);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t >= sg.tiles) continue;
+          wait(&q_full[t], segs[t]++ & 1);
+          if (!ok) break;
+          if (leader) issue_qk<HD, false>(tmem + t * 128, q_desc[t], kd);
+          commit(&s_full[t]);
+        }
+        if (ok) commit(&empty[(2 * count) % kTreeStages]);
+        for (int j = 0; j < n && ok; ++j, ++count) {
+          const int vi = 2 * count + 1, ki = 2 * count + 2;
+          const bool more = j + 1 < n;
+          full_wait(vi);
+          if (more) full_wait(ki);
+          const uint64_t vd = flash_desc(at(vi), true);
+          kd = flash_desc(at(ki), false);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok || t >= sg.tiles) continue;
+            const uint32_t turn = s_use[t]++ & 1;
+            wait(&p_full[2 * t], turn);
+            if (ok && leader) issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, vd, j == 0, 0);
+            wait(&p_full[2 * t + 1], turn);
+            if (!ok) continue;
+            if (leader) issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, vd, j == 0, 1);
+            if (more) {
+              if (leader) issue_qk<HD, false>(tmem + t * 128, q_desc[t], kd);
+              commit(&s_full[t]);
+            } else {
+              commit(&o_full[t]);
+            }
           }
-          if (ok) tc_commit(&empty[(2 * count) % kTreeStages]);
-          for (int j = 0; j < n && ok; ++j, ++count) {
-            const int vi = 2 * count + 1, ki = 2 * count + 2;
-            const bool more = j + 1 < n;
-            ok = full_wait(vi) && (!more || full_wait(ki));
-            for (int t = 0; t < sg.tiles && ok; ++t) {
-              ok = mbar_wait(&p_full[t], s_use[t]++ & 1, nullptr);
-              if (!ok) break;
-              tc_fence_after();
-              issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, at(vi), j == 0, 0);
-              issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, at(vi), j == 0, 1);
-              if (more) {
-                issue_qk<HD, false>(tmem + t * 128, q_s + t * Smem::kOperand, at(ki));
-                tc_commit(&s_full[t]);
-              } else {
-                tc_commit(&o_full[t]);
-              }
-            }
-            if (ok) {
-              tc_commit(&empty[vi % kTreeStages]);
-              if (more) tc_commit(&empty[ki % kTreeStages]);
-            }
+          if (ok) {
+            commit(&empty[vi % kTreeStages]);
+            if (more) commit(&empty[ki % kTreeStages]);
           }
         }
       }
@@ -601,7 +618,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[t]);
+            if (lane == 0) mbar_arrive(&p_full[2 * t]), mbar_arrive(&p_full[2 * t + 1]);
           }
           if (poison) l = NAN;
           if (ok) ok = mbar_wait(&o_full[t], o_use++ & 1, nullptr);

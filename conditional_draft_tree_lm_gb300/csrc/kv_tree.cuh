@@ -10,10 +10,10 @@
 // softmax and the conversion of the cache beside it; with one tile of rows it is
 // about the cache's bytes.
 //
-// Cached keys and values come to shared memory as fp16 (e4m3 is exact in it) by
-// four converting warps: 8-bit pieces are copied a tile ahead (cp.async, into
-// slots of the copying thread's own), converted, and stored in the layout that the
-// products read.  What a page's scale would change stays exact in 32 bits: the
+// Cached keys and values come to shared memory as fp16 (e4m3 is exact in it): one
+// warp looks up page numbers and scales and fetches whole pages a tile ahead (a
+// page of a head is contiguous: one bulk copy), four converting warps turn them
+// into the layout that the products read.  What a page's scale would change stays exact in 32 bits: the
 // key's scale multiplies the logit, the value's is folded into V relative to the
 // largest scale so far, O being in units of that one (exact for powers of two).
 // Q is brought to fp16 by a power of two per row, new keys and values by one per
@@ -32,9 +32,11 @@ namespace dt {
 
 constexpr int kTreeStages = 4;   // K and V tiles, alternating
 constexpr int kTreeSlots = 4;    // what goes with a key tile: its scales and masks
-constexpr int kTreeMmaWarp = 8, kTreeConvWarp = 9, kTreeConvWarps = 4;
+constexpr int kTreeMmaWarp = 8, kTreeFetchWarp = 9, kTreeConvWarp = 12, kTreeConvWarps = 4;
 constexpr int kConvThreads = 32 * kTreeConvWarps;
-constexpr int kTreeThreads = 32 * (kTreeConvWarp + kTreeConvWarps);
+constexpr int kTreeThreads = 512;  // (warps 10 and 11 only complete a warpgroup)
+// Registers: 512 threads start with 128; the softmax's 256 go to 176 and the others to 80 (all 65536).
+constexpr int kTreeSoftmaxRegs = 176, kTreeOtherRegs = 80;
 
 struct TreeParams {
   dt_kv_cache c;
@@ -101,18 +103,57 @@ struct TreeWalk {
   }
 };
 
+// Walks a piece's key tiles, segment after segment.
+enum { kTileNone = 0, kTileCached = 1, kTileNew = 2 };
+struct TreeKeyTile {
+  int kind, first;           // first: of its segment
+  int key0, req, kvh, len;   // key0: its first cached token, or new token
+};
+struct TreeTileWalk {
+  TreeWalk walk;
+  TreeSegment sg;
+  int key;
+  DT_DEVINL void next(const TreeParams& p, TreeKeyTile& t) {
+    t.kind = kTileNone;
+    t.first = 0;
+    if (sg.tiles == 0 || key >= sg.key_end) {
+      if (!walk.next(p, sg)) {
+        sg.tiles = 0;
+        return;
+      }
+      key = sg.key_begin;
+      t.first = 1;
+    }
+    // (a request without a key at all still has a tile: a cached one of no tokens)
+    const bool fresh = p.a.k_new && key >= sg.cached;
+    t.kind = fresh ? kTileNew : kTileCached;
+    t.key0 = (fresh ? key - sg.cached : key) * kKeyTile;
+    t.req = sg.req;
+    t.kvh = sg.kvh;
+    t.len = sg.len;
+    ++key;
+  }
+};
+
+// `bytes` (a multiple of 16) of contiguous global memory to shared memory.
+DT_DEVINL void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 template <int HD>
 struct TreeSmem {
   static constexpr uint32_t kOperand = kOperandBytes<HD>;
   static constexpr uint32_t kQ = 0, kRing = 2 * kOperand, kStaging = kRing + kTreeStages * kOperand;
-  static constexpr uint32_t kStagingBytes = 2 * kKeyTile * HD;  // K, V: [piece][thread] of 16 bytes
+  static constexpr uint32_t kStagingBytes = 2 * kKeyTile * HD;  // K, V: [key][channel] in 8 bits
   static constexpr uint32_t kBars = kStaging + kStagingBytes;
   static constexpr uint32_t kBytes = kBars + 512 + 1024;  // + alignment
 };
 
-// What the converting warps leave with a key tile for the softmax.
+// What goes with a key tile.
 struct TreeTile {
-  float k_scale[8];   // of 16 keys each
+  float k_scale[8], v_scale[8];  // of 16 keys each
   uint32_t seen[4];   // cached keys that exist (new ones: the keys below slots)
   uint32_t bad[4];    // keys whose values are not finite (new ones only)
   float ratio, vref;  // O's unit before / after this tile, and after
@@ -129,7 +170,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
   uint64_t* s_full = q_full + 2;
   uint64_t* p_full = s_full + 2;           // [2][2] halves of P
   uint64_t* o_full = p_full + 4;
-  TreeTile* tiles = reinterpret_cast<TreeTile*>(o_full + 2);  // [kTreeSlots]
+  uint64_t* st_full = o_full + 2;   // [2] K, V in the staging place
+  uint64_t* st_free = st_full + 2;  // [2]
+  TreeTile* tiles = reinterpret_cast<TreeTile*>(st_free + 2);  // [kTreeSlots]
   __shared__ uint32_t tmem_slot;
   __shared__ int scratch[4], s_start[128 + 1], s_last;
   __shared__ float s_max[2][kTreeConvWarps];
@@ -151,6 +194,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
       mbar_init(&p_full[2 * t], 4);
       mbar_init(&p_full[2 * t + 1], 4);
       mbar_init(&o_full[t], 1);
+      mbar_init(&st_full[t], 1);
+      mbar_init(&st_free[t], kTreeConvWarps);
     }
     fence_mbar_init();
   }
@@ -178,6 +223,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
     TreeSegment sg = {};
     const uint32_t q_s = smem_u32(smem + Smem::kQ), ring = smem_u32(smem + Smem::kRing);
 
+    if (warp >= kTreeMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeOtherRegs));
     if (warp == kTreeMmaWarp) {
       const bool leader = elect_one();
       int count = 0;  // key tiles so far
@@ -235,45 +282,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
           }
         }
       }
-    } else if (warp >= kTreeConvWarp) {
-      // --- conversion: tile after tile, the next one's 8-bit pieces in flight, the one's after that page numbers too
-      constexpr int kLanes = HD / 16;               // threads of a key's row (16 bytes each)
-      constexpr int kPassRows = kConvThreads / kLanes;
-      constexpr int kPasses = kKeyTile / kPassRows;  // pieces of a thread
-      const int ct = tid - kTreeConvWarp * 32, cw = ct >> 5, cc = ct % kLanes, cr = ct / kLanes;
-      struct Tile {
-        int kind, key0, req, kvh, len;  // kind: 0 none, 1 cached, 2 new, + 4 for the first of a segment
-      };
-      int key = 0;
-      auto advance = [&](Tile& t) {
-        if (key >= sg.key_end || sg.tiles == 0) {
-          if (!walk.next(p, sg)) {
-            sg.tiles = 0;
-            t.kind = 0;
-            return;
-          }
-          key = sg.key_begin;
-        }
-        const bool cached = key < sg.cached;
-        // (a request without a key at all still has a tile: a cached one of length 0)
-        t.kind = (cached || !a.k_new ? 1 : 2) + (key == sg.key_begin ? 4 : 0);
-        t.key0 = (cached || !a.k_new ? key : key - sg.cached) * kKeyTile;
-        t.req = sg.req;
-        t.kvh = sg.kvh;
-        t.len = sg.len;
-        ++key;
-      };
-      struct Page {  // of 16 keys, held by lanes 0..7 of every warp
+    } else if (warp == kTreeFetchWarp) {
+      // --- pages to the staging place, a tile ahead of their conversion; page numbers and scales another tile ahead
+      struct Page {  // of 16 keys, held by lanes 0..7
         int id;
         float ks, vs;
       };
-      auto pages_of = [&](const Tile& t) {
-        Page g = {-1, 0.0f, 0.0f};
+      TreeKeyTile cur, nxt;
+      TreeTileWalk tw = {walk, {}, 0};
+      auto pages_of = [&](const TreeKeyTile& t) {
+        Page g = {-1, 1.0f, 0.0f};
         const int tok = t.key0 + lane * 16;
-        if ((t.kind & 3) == 1 && lane < 8 && tok < t.len) {
+        if (t.kind == kTileCached && lane < 8 && tok < t.len) {
           g.id = __ldg(a.block_table + static_cast<size_t>(t.req) * a.max_blocks + (tok >> p.shift));
           if (g.id < 0 || g.id >= p.c.n_pages) {
-            if (a.status && cw == 0) atomicOr(a.status, DT_KV_BAD_INDEX);
+            if (a.status) atomicOr(a.status, DT_KV_BAD_INDEX);
             g.id = -1;
           } else {
             const size_t at = static_cast<size_t>(g.id) * n_kv + t.kvh;
@@ -283,22 +306,49 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         }
         return g;
       };
-      uint8_t* staging = smem + Smem::kStaging;
-      auto fetch = [&](const Tile& t, const Page& g, const void* codes, int which) {
-        if ((t.kind & 3) == 1) {
+      const int copy_keys = min(1 << p.shift, kKeyTile);
+      tw.next(p, cur);
+      Page gc = pages_of(cur);
+      bool ok = true;
+      for (int count = 0; cur.kind != kTileNone && ok; ++count) {
+        tw.next(p, nxt);
+        const Page gn = pages_of(nxt);
+        TreeTile& info = tiles[count % kTreeSlots];
+        const bool copies = cur.kind == kTileCached && lane < 8 && gc.id >= 0 && (lane * 16 & (copy_keys - 1)) == 0;
+        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, copies)) * copy_keys * HD;
+        const uint32_t there = __ballot_sync(0xFFFFFFFFu, gc.id >= 0);
+        const size_t at = copies ? (static_cast<size_t>(gc.id) * n_kv + cur.kvh << p.shift) * HD : 0;
 #pragma unroll
-          for (int i = 0; i < kPasses; ++i) {
-            const int row = i * kPassRows + cr;
-            const int id = __shfl_sync(0xFFFFFFFFu, g.id, row >> 4);
-            if (id >= 0) {
-              const size_t at = (((static_cast<size_t>(id) * n_kv + t.kvh) << p.shift) + ((t.key0 + row) & ((1 << p.shift) - 1))) * HD + cc * 16;
-              cp_async16(smem_u32(staging + ((which * kPasses + i) * kConvThreads + ct) * 16), static_cast<const uint8_t*>(codes) + at);
+        for (int which = 0; which < 2; ++which) {
+          ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&st_free[which], (count & 1) ^ 1, nullptr));
+          if (!ok) break;
+          // (the place is free: the tile four before this one is behind its softmax, too)
+          if (which == 0) {
+            if (lane < 8) info.k_scale[lane] = gc.ks, info.v_scale[lane] = gc.vs;
+            if (lane < 4) {
+              const uint32_t two = there >> (2 * lane);
+              info.seen[lane] = cur.kind == kTileNew ? first_bits(a.slots - cur.key0, lane)
+                                                     : first_bits(cur.len - cur.key0, lane) & (((two & 1) ? 0xFFFFu : 0u) | ((two & 2) ? 0xFFFF0000u : 0u));
+              info.bad[lane] = 0;
             }
+            __syncwarp();
           }
+          if (lane == 0) mbar_arrive_expect_tx(&st_full[which], bytes);
+          __syncwarp();
+          if (copies)
+            bulk_load(smem_u32(smem + Smem::kStaging) + which * kKeyTile * HD + lane * 16 * HD,
+                      static_cast<const uint8_t*>(which ? p.c.v : p.c.k) + at, copy_keys * HD, &st_full[which]);
         }
-        cp_commit();
-      };
-      // 8 halves to their place: key `row`, channels 8 * chunk ..
+        cur = nxt;
+        gc = gn;
+      }
+    } else if (warp >= kTreeConvWarp) {
+      // --- conversion
+      constexpr int kLanes = HD / 16;               // threads of a key's row (16 bytes each)
+      constexpr int kPassRows = kConvThreads / kLanes;
+      constexpr int kPasses = kKeyTile / kPassRows;  // pieces of a thread
+      const int ct = tid - kTreeConvWarp * 32, cw = ct >> 5, cc = ct % kLanes, cr = ct / kLanes;
+      // 8 halves to their place: key `row`, channels 8 * chunk .. (the swizzle: a row's 16-byte pieces by row % 8)
       auto put = [&](uint8_t* op, int row, int chunk, const uint4& w) {
         *reinterpret_cast<uint4*>(op + (chunk >> 3) * kHalfBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) = w;
       };
@@ -307,42 +357,54 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[i % kTreeStages]);
       };
-      // a cached tile's K or V out of the staging place, values multiplied by a factor per 16 keys
-      auto convert = [&](const Tile& t, const Page& g, int which, float inv) {
+      // (where a wait gives up the loop goes on without waiting: other warps may stand at its named barrier)
+      bool ok = true;
+      auto room = [&](int i) { ok = ok && mbar_wait(&empty[i % kTreeStages], ((i / kTreeStages) & 1) ^ 1, nullptr); };
+      // a cached tile's K or V out of the staging place
+      const bool swap = HD == 128 && (cc & 4);  // the two halves of a row's threads start with different pieces: no bank conflict
+      const int first_chunk = 2 * cc + (swap ? 1 : 0);
+      const int place = (first_chunk >> 3) * kHalfBytes + cr * 128, piece0 = ((first_chunk & 7) ^ (cr & 7)) << 4;
+      auto convert = [&](const TreeKeyTile& t, const TreeTile& info, int count, int which, float inv) {
         uint4 w[kPasses];
+        const uint8_t* st = smem + Smem::kStaging + which * kKeyTile * HD + ct * 16;
 #pragma unroll
-        for (int k = 0; k < kPasses; ++k)
-          w[k] = *reinterpret_cast<const uint4*>(staging + ((which * kPasses + k) * kConvThreads + ct) * 16);
-        return [=](uint8_t* op) {
+        for (int k = 0; k < kPasses; ++k) w[k] = *reinterpret_cast<const uint4*>(st + k * kConvThreads * 16);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st_free[which]);
+        room(2 * count + which);
+        uint8_t* op = smem + Smem::kRing + ((2 * count + which) % kTreeStages) * Smem::kOperand + place;
+        const bool whole = (info.seen[0] & info.seen[1] & info.seen[2] & info.seen[3]) == 0xFFFFFFFFu;
 #pragma unroll
-          for (int k = 0; k < kPasses; ++k) {
-            const int row = k * kPassRows + cr;
-            const int id = __shfl_sync(0xFFFFFFFFu, g.id, row >> 4);
-            const float f = which ? __shfl_sync(0xFFFFFFFFu, g.vs, row >> 4) * inv : 1.0f;
-            const uint32_t in[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-            uint32_t h[8];
-            const __half2 f2 = __float2half2_rn(f);
+        for (int k = 0; k < kPasses; ++k) {
+          const int row = k * kPassRows + cr;
+          const uint32_t in[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+          uint32_t h[8];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              e4m3x4_to_f16x2x2(in[x], h[2 * x], h[2 * x + 1]);
-              if (which) {
-                __half2* y = reinterpret_cast<__half2*>(&h[2 * x]);
-                y[0] = __hmul2(y[0], f2);
-                y[1] = __hmul2(y[1], f2);
+          for (int x = 0; x < 4; ++x) e4m3x4_to_f16x2x2(in[x], h[2 * x], h[2 * x + 1]);
+          if (which) {
+            const float f = info.v_scale[row >> 4] * inv;
+            if (f != 1.0f) {
+              const __half2 f2 = __float2half2_rn(f);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[x]), f2);
+                h[x] = *reinterpret_cast<uint32_t*>(&y);
               }
             }
-            const bool live = id >= 0 && t.key0 + row < t.len;
-            const uint4 lo = live ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(0, 0, 0, 0);
-            const uint4 hi = live ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(0, 0, 0, 0);
-            // the two halves of a row's threads start with different chunks: no bank conflict
-            const bool swap = HD == 128 && (cc & 4);
-            put(op, row, 2 * cc + (swap ? 1 : 0), swap ? hi : lo);
-            put(op, row, 2 * cc + (swap ? 0 : 1), swap ? lo : hi);
           }
-        };
+          if (!whole && !(info.seen[row >> 5] >> (row & 31) & 1u)) {  // (what no row sees may be NaN, or not there)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) h[x] = 0u;
+          }
+          const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+          // (passes are multiples of 8 rows apart: the swizzle is the same)
+          *reinterpret_cast<uint4*>(op + k * kPassRows * 128 + piece0) = swap ? hi : lo;
+          *reinterpret_cast<uint4*>(op + k * kPassRows * 128 + (piece0 ^ 16)) = swap ? lo : hi;
+        }
+        arrive(2 * count + which);
       };
       // a new tile's K or V, bf16: its largest finite magnitude first, then fp16 by a power of two
-      auto convert_new = [&](const Tile& t, int which, float& vref, float& scale, uint32_t* bad, uint8_t* op) {
+      auto convert_new = [&](const TreeKeyTile& t, int which, float& vref, float& scale, uint32_t* bad, uint8_t* op) {
         constexpr int kL = HD / 8, kR = kConvThreads / kL, kP = kKeyTile / kR;
         const int c8 = ct % kL, r8 = ct / kL;
         const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(which ? a.v_new : a.k_new);
@@ -354,8 +416,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
                                                                     t.kvh * hs + c8 * 8))
                              : make_uint4(0, 0, 0, 0);
         };
-        // (read twice, the second time from L1: a tile would take 64 registers)
-#pragma unroll 4
+        // (read twice, the second time from L1: a thread's part would take 64 registers)
+#pragma unroll 8
         for (int k = 0; k < kP; ++k) {
           const uint4 w = piece_of(k);
           const uint32_t in[4] = {w.x, w.y, w.z, w.w};
@@ -379,7 +441,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         scale = kv_pow2_scale(top);
         if (which) vref = fmaxf(vref, scale), scale = vref;
         const float inv = 1.0f / scale;
-#pragma unroll 4
+#pragma unroll 8
         for (int k = 0; k < kP; ++k) {
           const int row = k * kR + r8;
           const uint4 w = piece_of(k);
@@ -393,84 +455,48 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         }
       };
 
-      sg.tiles = 0;
-      Tile cur, nxt, nx2;
-      advance(cur);
-      Page gc = pages_of(cur);
-      advance(nxt);
-      Page gn = pages_of(nxt);
-      fetch(cur, gc, p.c.k, 0);
-      fetch(cur, gc, p.c.v, 1);
+      TreeKeyTile cur;
+      TreeTileWalk tw = {walk, {}, 0};
       float vref = 0.0f;
-      // (where a wait gives up the loop goes on without waiting: other warps may stand at its named barrier)
-      bool ok = true;
-      auto room = [&](int i) { ok = ok && mbar_wait(&empty[i % kTreeStages], ((i / kTreeStages) & 1) ^ 1, nullptr); };
-      for (int count = 0; cur.kind; ++count) {
-        advance(nx2);
-        const Page g2 = pages_of(nx2);
+      for (int count = 0; tw.next(p, cur), cur.kind != kTileNone; ++count) {
         TreeTile& info = tiles[count % kTreeSlots];
-        const int ki = 2 * count, vi = ki + 1;
-        if (cur.kind & 4) vref = 1.17549435e-38f;
+        if (cur.first) vref = 1.17549435e-38f;
         const float before = vref;
-        uint8_t* k_op = smem + Smem::kRing + (ki % kTreeStages) * Smem::kOperand;
-        uint8_t* v_op = smem + Smem::kRing + (vi % kTreeStages) * Smem::kOperand;
-        if ((cur.kind & 3) == 1) {
-          cp_wait<1>();
-          auto store_k = convert(cur, gc, 0, 1.0f);
-          fetch(nxt, gn, p.c.k, 0);
-          room(ki);
-          float top = lane < 8 ? gc.vs : 0.0f;
-          top = warp_max(top);
-          vref = fmaxf(vref, top);
-          if (cw == 0) {
-            if (lane < 8) info.k_scale[lane] = gc.ks;
-            const uint32_t there = __ballot_sync(0xFFFFFFFFu, lane < 8 && gc.id >= 0);
-            if (lane < 4) {
-              const uint32_t two = there >> (2 * lane);
-              info.seen[lane] = first_bits(cur.len - cur.key0, lane) & (((two & 1) ? 0xFFFFu : 0u) | ((two & 2) ? 0xFFFF0000u : 0u));
-              info.bad[lane] = 0;
-            }
-            if (lane == 0) {
-              info.ratio = (cur.kind & 4) ? 1.0f : before / vref;
-              info.vref = vref;
-            }
-          }
-          store_k(k_op);
-          arrive(ki);
-          cp_wait<1>();
-          auto store_v = convert(cur, gc, 1, 1.0f / vref);
-          fetch(nxt, gn, p.c.v, 1);
-          room(vi);
-          store_v(v_op);
-          arrive(vi);
-        } else {
-          // (the groups of this tile hold nothing; the next tile's take their places in the count)
-          cp_wait<0>();
-          fetch(nxt, gn, p.c.k, 0);
-          room(ki);
-          if (ct < 4) info.bad[ct] = 0;
-          float scale;
-          convert_new(cur, 0, vref, scale, info.bad, k_op);  // (its barriers order the zeros before)
-          if (ct < 8) info.k_scale[ct] = scale;
-          if (ct < 4) info.seen[ct] = first_bits(a.slots - cur.key0, ct);
-          // the values before the keys are handed over: the tile's ratio goes with the keys
-          room(vi);
-          convert_new(cur, 1, vref, scale, info.bad, v_op);
+        ok = ok && mbar_wait(&st_full[0], count & 1, nullptr);
+        if (cur.kind == kTileCached) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g) vref = fmaxf(vref, info.v_scale[g]);
           if (ct == 0) {
-            info.ratio = (cur.kind & 4) ? 1.0f : before / vref;
+            info.ratio = cur.first ? 1.0f : before / vref;
             info.vref = vref;
           }
-          fetch(nxt, gn, p.c.v, 1);
-          arrive(ki);
-          arrive(vi);
+          convert(cur, info, count, 0, 1.0f);
+          ok = ok && mbar_wait(&st_full[1], count & 1, nullptr);
+          convert(cur, info, count, 1, 1.0f / vref);
+        } else {
+          ok = ok && mbar_wait(&st_full[1], count & 1, nullptr);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&st_free[0]), mbar_arrive(&st_free[1]);
+          uint8_t* k_op = smem + Smem::kRing + ((2 * count) % kTreeStages) * Smem::kOperand;
+          uint8_t* v_op = smem + Smem::kRing + ((2 * count + 1) % kTreeStages) * Smem::kOperand;
+          float scale;
+          room(2 * count);
+          convert_new(cur, 0, vref, scale, info.bad, k_op);
+          if (ct < 8) info.k_scale[ct] = scale;
+          room(2 * count + 1);
+          convert_new(cur, 1, vref, scale, info.bad, v_op);
+          if (ct == 0) {
+            info.ratio = cur.first ? 1.0f : before / vref;
+            info.vref = vref;
+          }
+          // (the keys are handed over after the values: the tile's unit goes with them)
+          arrive(2 * count);
+          arrive(2 * count + 1);
         }
-        cur = nxt;
-        gc = gn;
-        nxt = nx2;
-        gn = g2;
       }
-      cp_wait<0>();
+    }
     } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeSoftmaxRegs));
       // --- softmax: warpgroup t, a row a thread
       const int t = warp >> 2, r = tid & 127;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -479,44 +505,49 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
       int count = 0, s_use = 0, o_use = 0;
       bool ok = true;
       // (where a wait gives up, likewise)
+      auto ready = [&](int half) {
+        if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
+      };
       while (walk.next(p, sg)) {
         const int n = sg.key_end - sg.key_begin;
         const int slot = (sg.pair * 2 + t) * p.per_tile + r / p.group, head = sg.kvh * p.group + r % p.group;
         const bool live = t < sg.tiles && r < p.per_tile * p.group && slot < a.slots;
         const int64_t row = static_cast<int64_t>(sg.req) * a.slots + slot;
-        float m = -INFINITY, l = 0.0f, vref = 0.0f;
+        SoftmaxRow sm;
+        float vref = 0.0f;
         if (t < sg.tiles) {
-          // Q to fp16 by a power of two of the row's own
-          float c;
+          // Q to fp16 by a power of two of the row's own: HD / 8 lanes read a row together
+          float c = 0.0f;
           {
-            float amax = 0.0f;
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + row * a.q_row_stride + head * a.q_head_stride;
-            auto piece_of = [&](int i) {
-              return live ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
-            };
-#pragma unroll 8
-            for (int i = 0; i < HD / 8; ++i) {
-              const uint4 w = piece_of(i);
-              const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(in[y] << 16)), fabsf(__uint_as_float(in[y] & 0xFFFF0000u))));
-            }
-            int k = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-            k = min(max(k, -100), 127);
-            const float up = __uint_as_float(static_cast<uint32_t>(14 - k + 127) << 23);
-            c = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(k - 14 + 127) << 23);
+            constexpr int kL = HD / 8, kR = 32 / kL, kN = 32 / kR;  // lanes of a row, rows at a time, times
             uint8_t* op = smem + Smem::kQ + t * Smem::kOperand;
+            const int cx = lane % kL, rx = lane / kL;
 #pragma unroll 8
-            for (int i = 0; i < HD / 8; ++i) {
-              const uint4 w = piece_of(i);
+            for (int i = 0; i < kN; ++i) {
+              const int y = (warp & 3) * 32 + i * kR + rx, sl = (sg.pair * 2 + t) * p.per_tile + y / p.group;
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (y < p.per_tile * p.group && sl < a.slots)
+                w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                         (static_cast<int64_t>(sg.req) * a.slots + sl) * a.q_row_stride +
+                                                         (sg.kvh * p.group + y % p.group) * a.q_head_stride) + cx);
               const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+              float amax = 0.0f;
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(in[z] << 16)), fabsf(__uint_as_float(in[z] & 0xFFFF0000u))));
+#pragma unroll
+              for (int o = 1; o < kL; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+              int k = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+              k = min(max(k, -100), 127);
+              const float up = __uint_as_float(static_cast<uint32_t>(14 - k + 127) << 23);
               uint32_t h[4];
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                h[y] = pack_f16(__uint_as_float(in[y] << 16) * up, __uint_as_float(in[y] & 0xFFFF0000u) * up);
-              *reinterpret_cast<uint4*>(op + (i >> 3) * kHalfBytes + r * 128 + (((i & 7) ^ (r & 7)) << 4)) =
+              for (int z = 0; z < 4; ++z)
+                h[z] = pack_f16(__uint_as_float(in[z] << 16) * up, __uint_as_float(in[z] & 0xFFFF0000u) * up);
+              *reinterpret_cast<uint4*>(op + (cx >> 3) * kHalfBytes + y * 128 + (((cx & 7) ^ (y & 7)) << 4)) =
                   make_uint4(h[0], h[1], h[2], h[3]);
+              const int mine = __shfl_sync(0xFFFFFFFFu, k, (lane % kR) * kL);
+              if (lane / kR == i) c = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(mine - 14 + 127) << 23);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -529,20 +560,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             uint32_t see[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
             if (fresh) {  // which of the new tokens this row sees, while the product runs
               const int b0 = (key - sg.cached) * kKeyTile;
-              const uint8_t* mask = a.mask ? a.mask + row * a.slots + b0 : nullptr;
+              if (!a.mask) {
 #pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                if (!live) {
-                  see[w] = 0;
-                } else if (!mask) {
-                  see[w] = first_bits(slot + 1 - b0, w);
-                } else {
-                  uint32_t x = 0;
-                  for (int i = 0; i < 32; ++i)
-                    if (b0 + w * 32 + i < a.slots) x |= (mask[w * 32 + i] != 0 ? 1u : 0u) << i;
-                  see[w] = x;
+                for (int w = 0; w < 4; ++w) see[w] = first_bits(slot + 1 - b0, w);
+              } else {
+                // the warp's slots, eight at a time: a byte a lane, 32 bytes to a word by ballot
+                const int s0 = (sg.pair * 2 + t) * p.per_tile + (warp & 3) * 32 / p.group;
+                const int s1 = (sg.pair * 2 + t) * p.per_tile + ((warp & 3) * 32 + 31) / p.group;
+                const uint8_t* mask = a.mask + static_cast<int64_t>(sg.req) * a.slots * a.slots + b0 + lane;
+                for (int x = s0; x <= s1; x += 8) {
+                  uint8_t byte[8][4];
+#pragma unroll
+                  for (int y = 0; y < 8; ++y)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                      byte[y][w] = x + y <= s1 && x + y < a.slots && b0 + 32 * w + lane < a.slots
+                                       ? __ldg(mask + static_cast<int64_t>(x + y) * a.slots + 32 * w) : 0;
+#pragma unroll
+                  for (int y = 0; y < 8; ++y)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                      const uint32_t word = __ballot_sync(0xFFFFFFFFu, byte[y][w] != 0);
+                      if (slot == x + y) see[w] = word;
+                    }
                 }
               }
+              if (!live) see[0] = see[1] = see[2] = see[3] = 0;
             }
             ok = ok && mbar_wait(&s_full[t], s_use++ & 1, nullptr);
             if (!ok) break;
@@ -558,69 +601,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             const bool masked = !__all_sync(0xFFFFFFFFu, all);
             vref = info.vref;
             const float ratio = info.ratio;
-            // the largest logit that is seen, 16 keys (of one scale) at a time
-            float top = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              uint32_t s[32];
-              tmem_ld32(s_at + 32 * w, s);
-              tmem_wait_ld();
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float ck = c * info.k_scale[2 * w + h];
-                float hi = -INFINITY, lo = INFINITY;
-                if (!masked) {
-                  if (c >= 0.0f) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) hi = fmaxf(hi, __uint_as_float(s[16 * h + i]));
-                    top = fmaxf(top, hi * ck);
-                  } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) lo = fminf(lo, __uint_as_float(s[16 * h + i]));
-                    top = fmaxf(top, lo * ck);
-                  }
-                } else {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i)
-                    if (see[w] >> (16 * h + i) & 1u) top = fmaxf(top, __uint_as_float(s[16 * h + i]) * ck);
-                }
-              }
-            }
-            if (__any_sync(0xFFFFFFFFu, top > m + 8.0f || ratio != 1.0f)) {
-              const float m2 = fmaxf(m, top), f = m2 == -INFINITY ? 1.0f : ex2(m - m2);
-              if (j > 0) rescale_o<HD>(o_at, f * ratio);
-              l *= f;
-              m = m2;
-            }
-            const float base = m == -INFINITY ? 0.0f : m;
-            float sum[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              uint32_t s[32], pk[16];
-              tmem_ld32(s_at + 32 * w, s);
-              const float ck[2] = {c * info.k_scale[2 * w], c * info.k_scale[2 * w + 1]};
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float e0 = ex2(fmaf(__uint_as_float(s[2 * i]), ck[i >> 3], -base));
-                float e1 = ex2(fmaf(__uint_as_float(s[2 * i + 1]), ck[i >> 3], -base));
-                if (masked) {
-                  if (!(see[w] >> (2 * i) & 1u)) e0 = 0.0f;
-                  if (!(see[w] >> (2 * i + 1) & 1u)) e1 = 0.0f;
-                }
-                sum[(2 * i) & 3] += e0;
-                sum[(2 * i + 1) & 3] += e1;
-                pk[i] = pack_f16(e0, e1);
-              }
-              tmem_st16(s_at + 16 * w, pk);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * t]), mbar_arrive(&p_full[2 * t + 1]);
+            auto scale = [&](int g) { return c * info.k_scale[g]; };
+            if (masked) softmax_tile<HD, false, false, true>(s_at, o_at, j == 0, ratio, c < 0.0f, scale, see, sm, ready);
+            else softmax_tile<HD, false, false, false>(s_at, o_at, j == 0, ratio, c < 0.0f, scale, see, sm, ready);
           }
-          if (poison) l = NAN;
+          if (poison) sm.l = NAN;
           if (ok) ok = mbar_wait(&o_full[t], o_use++ & 1, nullptr);
           tc_fence_after();
         }
@@ -629,42 +614,50 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         // --- the end of a stretch: the answer, or a part of it
         const int c_first = cut.of(sg.first), c_last = cut.of(sg.first + sg.units - 1);
         const bool alone = c_first == c_last;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * a.out_row_stride + head * a.out_head_stride;
+        auto out_of = [&](int y) -> __nv_bfloat16* {  // row y of the tile
+          const int sl = (sg.pair * 2 + t) * p.per_tile + y / p.group;
+          if (y >= p.per_tile * p.group || sl >= a.slots) return nullptr;
+          return static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(sg.req) * a.slots + sl) * a.out_row_stride +
+                 (sg.kvh * p.group + y % p.group) * a.out_head_stride;
+        };
         auto finish_lse = [&](float top, float sum) {
           if (live && a.lse) a.lse[row * a.n_q + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
         };
         if (t < sg.tiles) {
-          const float inv = alone ? (l == 0.0f ? 0.0f : vref / l) : vref;
+          const float inv = alone ? (sm.l == 0.0f ? 0.0f : vref / sm.l) : vref;
           const size_t mine = static_cast<size_t>(2 * piece + (piece == c_first)) * 2 + t;
-          // (O in units of vref; where nothing was seen, it is zeros, or in a first tile never NaN: V is finite then)
+          const bool nan = sm.l != sm.l;
 #pragma unroll
-          for (int x = 0; x < HD; x += 32) {
-            uint32_t v[32];
+          for (int x = 0; x < HD; x += 64) {
+            uint32_t v[64];
             tmem_ld32(o_at + x, v);
+            tmem_ld32(o_at + x + 32, v + 32);
             tmem_wait_ld();
-            float o[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(v[i]) * inv;
-            if (l != l) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = NAN;
-            }
+            for (int i = 0; i < 64; ++i) v[i] = __float_as_uint(nan ? NAN : __uint_as_float(v[i]) * inv);
             if (alone) {
-              if (live) {
+              uint4 w[8];
 #pragma unroll
-                for (int i = 0; i < 32; i += 8)
-                  *reinterpret_cast<uint4*>(out + x + i) = make_uint4(pack_p<true>(o[i], o[i + 1]), pack_p<true>(o[i + 2], o[i + 3]),
-                                                                      pack_p<true>(o[i + 4], o[i + 5]), pack_p<true>(o[i + 6], o[i + 7]));
+              for (int k = 0; k < 8; ++k) {
+                w[k].x = pack_p<true>(__uint_as_float(v[8 * k]), __uint_as_float(v[8 * k + 1]));
+                w[k].y = pack_p<true>(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3]));
+                w[k].z = pack_p<true>(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5]));
+                w[k].w = pack_p<true>(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7]));
               }
+              // (through the row tile's own Q, which the next segment's replaces after this)
+              store_rows(smem + Smem::kQ + t * Smem::kOperand + (warp & 3) * 4096, w, [&](int y) -> __nv_bfloat16* {
+                __nv_bfloat16* to = out_of((warp & 3) * 32 + y);
+                return to ? to + x : nullptr;
+              });
             } else {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
+              for (int i = 0; i < 64; i += 4)
                 __stcg(reinterpret_cast<float4*>(p.part) + (mine * (HD / 4) + (x + i) / 4) * 128 + r,
-                       make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+                       make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])));
             }
           }
-          if (alone) finish_lse(m, l);
-          else __stcg(reinterpret_cast<float2*>(stats) + mine * 128 + r, make_float2(m, l));
+          if (alone) finish_lse(sm.m, sm.l);
+          else __stcg(reinterpret_cast<float2*>(stats) + mine * 128 + r, make_float2(sm.m, sm.l));
           tc_fence_before();  // (O is read before the next segment's first product writes it)
         }
         if (!alone) {
@@ -687,18 +680,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
               sum += ml.y * ex2(ml.x - base);
             }
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            for (int c8 = 0; c8 < HD / 8; ++c8) {
-              float o[8] = {};
-              for (int x = c_first; x <= c_last; ++x) {
-                const float f = ex2(__ldcg(reinterpret_cast<const float2*>(stats) + part_of(x) * 128 + r).x - base);
-                const float4* y = reinterpret_cast<const float4*>(p.part) + (part_of(x) * (HD / 4) + 2 * c8) * 128 + r;
-                const float4 y0 = __ldcg(y), y1 = __ldcg(y + 128);
-                o[0] += y0.x * f, o[1] += y0.y * f, o[2] += y0.z * f, o[3] += y0.w * f;
-                o[4] += y1.x * f, o[5] += y1.y * f, o[6] += y1.z * f, o[7] += y1.w * f;
+            for (int x = 0; x < HD; x += 64) {
+              float4 o[16] = {};
+              for (int k = c_first; k <= c_last; ++k) {
+                const float f = ex2(__ldcg(reinterpret_cast<const float2*>(stats) + part_of(k) * 128 + r).x - base);
+                const float4* y = reinterpret_cast<const float4*>(p.part) + (part_of(k) * (HD / 4) + x / 4) * 128 + r;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float4 z = __ldcg(y + i * 128);
+                  o[i].x += z.x * f, o[i].y += z.y * f, o[i].z += z.z * f, o[i].w += z.w * f;
+                }
               }
-              if (live)
-                *reinterpret_cast<uint4*>(out + 8 * c8) = make_uint4(pack_p<true>(o[0] * inv, o[1] * inv), pack_p<true>(o[2] * inv, o[3] * inv),
-                                                                     pack_p<true>(o[4] * inv, o[5] * inv), pack_p<true>(o[6] * inv, o[7] * inv));
+              uint4 w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                w[k] = make_uint4(pack_p<true>(o[2 * k].x * inv, o[2 * k].y * inv), pack_p<true>(o[2 * k].z * inv, o[2 * k].w * inv),
+                                  pack_p<true>(o[2 * k + 1].x * inv, o[2 * k + 1].y * inv),
+                                  pack_p<true>(o[2 * k + 1].z * inv, o[2 * k + 1].w * inv));
+              store_rows(smem + Smem::kQ + t * Smem::kOperand + (warp & 3) * 4096, w, [&](int y) -> __nv_bfloat16* {
+                __nv_bfloat16* to = out_of((warp & 3) * 32 + y);
+                return to ? to + x : nullptr;
+              });
             }
             finish_lse(top, sum);
           }

@@ -44,6 +44,12 @@ DT_DEVINL void tmem_ld32(uint32_t taddr, uint32_t* v) {
       : "r"(taddr));
 }
 DT_DEVINL void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// (after the wait: ties the registers to it, so that nothing that uses them moves before it)
+DT_DEVINL void tmem_landed32(uint32_t* v) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7]));
+}
 DT_DEVINL void tmem_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -141,6 +147,7 @@ DT_DEVINL void rescale_o(uint32_t o_tmem, float f) {
     uint32_t v[32];
     tmem_ld32(o_tmem + c, v);
     tmem_wait_ld();
+    tmem_landed32(v);
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
     tmem_st32(o_tmem + c, v);
@@ -201,48 +208,55 @@ struct SoftmaxRow {
 // what turns a raw logit of keys 16 g .. 16 g + 15 into powers of two, one value
 // for all where UNIFORM; negative: its sign is negative.  see: the row's visible
 // keys, all of them unless MASKED.  ready(i): called when half i of P is stored.
-template <int HD, bool BF16, bool UNIFORM, bool MASKED, class Scale, class Ready>
+// HOLD: all of S stays in registers (128 of them) between the maximum and the
+// exponentials; otherwise it is read twice, 32 columns ahead of their use.
+template <int HD, bool BF16, bool UNIFORM, bool MASKED, bool HOLD, class Scale, class Ready>
 DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float ratio, bool negative, Scale scale,
                             const uint32_t (&see)[4], SoftmaxRow& row, Ready ready) {
-  uint32_t s[128];
+  uint32_t s[HOLD ? 128 : 64];
+  auto part = [&](int w) { return s + (HOLD ? 32 * w : 32 * (w & 1)); };
+  if (HOLD) {
 #pragma unroll
-  for (int w = 0; w < 4; ++w) tmem_ld32(s_at + 32 * w, s + 32 * w);
-  tmem_wait_ld();
-  if (MASKED) {
-    const uint32_t out = negative ? 0x7F800000u : 0xFF800000u;
-#pragma unroll
-    for (int i = 0; i < 128; ++i) s[i] = see[i >> 5] >> (i & 31) & 1u ? s[i] : out;
+    for (int w = 0; w < 4; ++w) tmem_ld32(s_at + 32 * w, part(w));
+    tmem_wait_ld();
+  } else {
+    tmem_ld32(s_at, part(0));
   }
   float top = -INFINITY;
-  if (!negative) {
-    float x[8];
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      float a = fmaxf(__uint_as_float(s[16 * g]), __uint_as_float(s[16 * g + 1])), b = fmaxf(__uint_as_float(s[16 * g + 2]), __uint_as_float(s[16 * g + 3]));
+  for (int w = 0; w < 4; ++w) {
+    uint32_t* v = part(w);
+    if (!HOLD) tmem_wait_ld();
+    tmem_landed32(v);
+    if (!HOLD) tmem_ld32(s_at + 32 * ((w + 1) & 3), part(w + 1));  // (the last one: the first, for the second reading)
+    if (MASKED) {
+      const uint32_t out = negative ? 0x7F800000u : 0xFF800000u;
 #pragma unroll
-      for (int i = 4; i < 16; i += 4) {
-        a = fmaxf(fmaxf(a, __uint_as_float(s[16 * g + i])), __uint_as_float(s[16 * g + i + 1]));
-        b = fmaxf(fmaxf(b, __uint_as_float(s[16 * g + i + 2])), __uint_as_float(s[16 * g + i + 3]));
+      for (int i = 0; i < 32; ++i) v[i] = see[w] >> i & 1u ? v[i] : out;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float a = __uint_as_float(v[16 * h]), b = __uint_as_float(v[16 * h + 1]);
+      if (!negative) {
+#pragma unroll
+        for (int i = 2; i < 16; i += 4) {
+          a = fmaxf(fmaxf(a, __uint_as_float(v[16 * h + i])), __uint_as_float(v[16 * h + i + 1]));
+          if (i + 2 < 16) b = fmaxf(fmaxf(b, __uint_as_float(v[16 * h + i + 2])), __uint_as_float(v[16 * h + i + 3]));
+        }
+        a = fmaxf(a, b);
+      } else {
+#pragma unroll
+        for (int i = 2; i < 16; ++i) a = fminf(a, __uint_as_float(v[16 * h + i]));
+        a = fminf(a, b);
       }
-      x[g] = fmaxf(a, b);
-      if (!UNIFORM) x[g] = scale(g) == 0.0f ? 0.0f : x[g] * scale(g);
+      const float c = scale(UNIFORM ? 0 : 2 * w + h);
+      top = fmaxf(top, c == 0.0f ? 0.0f : a * c);
     }
-#pragma unroll
-    for (int g = 0; g < 8; ++g) top = fmaxf(top, x[g]);
-  } else {
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      float a = INFINITY;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) a = fminf(a, __uint_as_float(s[16 * g + i]));
-      top = fmaxf(top, UNIFORM ? -a : a * scale(g));
-    }
-    if (UNIFORM) top = -top;
   }
-  if (UNIFORM) top = scale(0) == 0.0f ? 0.0f : top * scale(0);
   // (a tile of which the row sees nothing has top = -inf, or 0 with a scale of zero: no harm, P is 0)
   if (__any_sync(0xFFFFFFFFu, top > row.m + 8.0f || ratio != 1.0f)) {
     const float m2 = fmaxf(row.m, top), f = m2 == -INFINITY ? 1.0f : ex2(row.m - m2);
+    if (!HOLD) tmem_wait_ld();  // (s is on its way; the rescaling waits for its own)
     if (!first) rescale_o<HD>(o_at, f * ratio);
     row.l *= f;
     row.m = m2;
@@ -253,6 +267,12 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     uint32_t pk[16];
+    uint32_t* v = part(w);
+    if (!HOLD) {
+      tmem_wait_ld();
+      tmem_landed32(v);
+      if (w < 3) tmem_ld32(s_at + 32 * (w + 1), part(w + 1));
+    }
     // (of a masked tile, most 32-key parts are seen by all of a warp's rows or by none)
     const bool none = MASKED && __all_sync(0xFFFFFFFFu, see[w] == 0u);
     const bool all = !MASKED || __all_sync(0xFFFFFFFFu, see[w] == 0xFFFFFFFFu);
@@ -262,10 +282,9 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int k = 32 * w + 2 * i;
-        const float c = scale(UNIFORM ? 0 : k >> 4);
+        const float c = scale(UNIFORM ? 0 : 2 * w + (i >> 3));
         float e0, e1;
-        f32x2_parts(fma2(f32x2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f32x2(c, c), base2), e0, e1);
+        f32x2_parts(fma2(f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f32x2(c, c), base2), e0, e1);
         e0 = ex2(e0);
         e1 = ex2(e1);
         if (!all) {
@@ -276,6 +295,7 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
         pk[i] = pack_p<BF16>(e0, e1);
       }
     }
+    // (P's columns 16 w .. lie before those of S that are still to be read, 32 (w + 1) ..)
     tmem_st16(s_at + 16 * w, pk);
     if (w & 1) {
       tmem_wait_st();

@@ -24,6 +24,8 @@
 // makes the rows that do see it NaN.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "kv_flash.cuh"
 
 namespace dt {
@@ -37,6 +39,10 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
 // Tiles of which some row does not see all: keys behind the first of an item's (at most 256) positions
 // lie in three at most, so each has barriers and a word of its own.
 constexpr int kMaskedTiles = 3;
+#ifndef DT_HOLD
+#define DT_HOLD true
+#endif
+constexpr bool kHold = DT_HOLD;
 
 struct PromptParams {
   __nv_bfloat16* out;
@@ -161,7 +167,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       int q_use[2] = {0, 0};
       bool ok = true;
       for (int i = 0; ok && prompt_item(p, i, it); ++i) {
-        auto load_q = [&](int t) {
+        auto load_q = [&](auto which) {
+          constexpr int t = decltype(which)::value;
           if (it.n_tiles[t] == 0) return;
           ok = ok && mbar_wait(&q_free[t], (q_use[t]++ & 1) ^ 1, nullptr);
           if (!ok) return;
@@ -170,7 +177,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             tma_load_3d(q_s + t * Smem::kOperand + h * kHalfBytes, &tm_q, &q_full[t], h * 64, it.kvh * p.group,
                         it.row0 + it.pos0 + t * p.positions);
         };
-        load_q(0);
+        load_q(std::integral_constant<int, 0>{});
         // K(0), V(0), K(1), V(1), ...
         for (int x = 0; x < 2 * it.n && ok; ++x) {
           ok = mbar_wait(&empty[stage], phase ^ 1u, nullptr);
@@ -180,13 +187,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             tma_load_3d(ring + stage * Smem::kOperand + h * kHalfBytes, (x & 1) ? &tm_v : &tm_k, &full[stage], h * 64, it.kvh,
                         it.row0 + (x >> 1) * kKeyTile);
           if (++stage == kStages) stage = 0, phase ^= 1u;
-          if (x == 0) load_q(1);
+          if (x == 0) load_q(std::integral_constant<int, 1>{});
         }
       }
     } else if (warp == kMmaWarp) {
       const bool leader = elect_one();
       int load = 0;  // ring entries consumed
-      int q_use[2] = {0, 0}, p_use[2] = {0, 0}, masked_use[kMaskedTiles] = {0, 0, 0};
+      int q_use[2] = {0, 0}, p_use[2] = {0, 0};
+      uint32_t masked_turns = 0;  // bit m: the parity of clean[m]'s next phase
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, nullptr));
@@ -219,7 +227,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           full_wait(vi);
           if (ok && m >= 0 && leader) mbar_arrive(&dirty[m]);
           if (more) full_wait(ki);
-          if (m >= 0) wait(&clean[m], masked_use[m]++ & 1);
+          if (m >= 0) {
+            wait(&clean[m], masked_turns >> m & 1u);
+            masked_turns ^= 1u << m;
+          }
           const uint64_t vd = flash_desc(at(vi), true);
           kd = flash_desc(at(ki), false);
 #pragma unroll
@@ -249,7 +260,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     } else if (warp >= kCleanWarp) {
       // values of the masked tiles: half of the keys a warp, a key's 16-byte pieces to eight lanes
       const int cw = warp - kCleanWarp;
-      int items = 0, use[kMaskedTiles] = {0, 0, 0}, load = 0;
+      int items = 0, load = 0;
+      uint32_t turns = 0;  // bit m: the parity of dirty[m]'s next phase
       bool ok = true;
       for (int i = 0; ok && prompt_item(p, i, it); ++i) {
         if (it.n == 0) continue;
@@ -260,7 +272,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         for (int j = it.masked0; j < it.n && ok; ++j) {
           const int m = j - it.masked0;
-          ok = mbar_wait(&dirty[m], use[m]++ & 1, nullptr);
+          ok = mbar_wait(&dirty[m], turns >> m & 1u, nullptr);
+          turns ^= 1u << m;
           if (!ok) break;
           // (the swizzle stays within a key's 128 bytes)
           uint8_t* v = smem + Smem::kRing + ((load + 2 * j + 1) % kStages) * Smem::kOperand + cw * 64 * 128 + lane * 16;
@@ -309,7 +322,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     };
     for (int i = 0; ok && prompt_item(p, i, it); ++i) {
       if (it.n == 0) continue;
-      const int n = it.n_tiles[t];
+      const int n = t == 0 ? it.n_tiles[0] : it.n_tiles[1];
       const int from = it.pos0 + t * p.positions, pos = from + r / p.group, head = it.kvh * p.group + r % p.group;
       SoftmaxRow row;
       for (int j = 0; j < n && ok; ++j) {
@@ -319,9 +332,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int seen = pos + 1 - j * kKeyTile;  // of this tile's keys, by this row
         const uint32_t see[4] = {first_bits(seen, 0), first_bits(seen, 1), first_bits(seen, 2), first_bits(seen, 3)};
         if ((j + 1) * kKeyTile > from + 1)
-          softmax_tile<HD, true, true, true>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
+          softmax_tile<HD, true, true, true, kHold>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
         else
-          softmax_tile<HD, true, true, false>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
+          softmax_tile<HD, true, true, false, kHold>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
       }
       if (n > 0) {
         ok = ok && mbar_wait(&o_full[t], o_use++ & 1, nullptr);
@@ -348,6 +361,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           tmem_ld32(o_at + x, v);
           tmem_ld32(o_at + x + 32, v + 32);
           tmem_wait_ld();
+          tmem_landed32(v);
+          tmem_landed32(v + 32);
           uint4 w[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {

@@ -32,11 +32,9 @@ namespace dt {
 
 constexpr int kTreeStages = 4;   // K and V tiles, alternating
 constexpr int kTreeSlots = 4;    // what goes with a key tile: its scales and masks
-constexpr int kTreeMmaWarp = 8, kTreeFetchWarp = 9, kTreeConvWarp = 12, kTreeConvWarps = 4;
+constexpr int kTreeMmaWarp = 8, kTreeFetchWarp = 9, kTreeConvWarp = 10, kTreeConvWarps = 4;
 constexpr int kConvThreads = 32 * kTreeConvWarps;
-constexpr int kTreeThreads = 512;  // (warps 10 and 11 only complete a warpgroup)
-// Registers: 512 threads start with 128; the softmax's 256 go to 176 and the others to 80 (all 65536).
-constexpr int kTreeSoftmaxRegs = 176, kTreeOtherRegs = 80;
+constexpr int kTreeThreads = 32 * (kTreeConvWarp + kTreeConvWarps);
 
 struct TreeParams {
   dt_kv_cache c;
@@ -223,8 +221,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
     TreeSegment sg = {};
     const uint32_t q_s = smem_u32(smem + Smem::kQ), ring = smem_u32(smem + Smem::kRing);
 
-    if (warp >= kTreeMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeOtherRegs));
     if (warp == kTreeMmaWarp) {
       const bool leader = elect_one();
       int count = 0;  // key tiles so far
@@ -494,9 +490,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
           arrive(2 * count + 1);
         }
       }
-    }
     } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeSoftmaxRegs));
       // --- softmax: warpgroup t, a row a thread
       const int t = warp >> 2, r = tid & 127;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -602,8 +596,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             vref = info.vref;
             const float ratio = info.ratio;
             auto scale = [&](int g) { return c * info.k_scale[g]; };
-            if (masked) softmax_tile<HD, false, false, true>(s_at, o_at, j == 0, ratio, c < 0.0f, scale, see, sm, ready);
-            else softmax_tile<HD, false, false, false>(s_at, o_at, j == 0, ratio, c < 0.0f, scale, see, sm, ready);
+            if (masked) softmax_tile<HD, false, false, true, false>(s_at, o_at, j == 0, ratio, c < 0.0f, scale, see, sm, ready);
+            else softmax_tile<HD, false, false, false, false>(s_at, o_at, j == 0, ratio, c < 0.0f, scale, see, sm, ready);
           }
           if (poison) sm.l = NAN;
           if (ok) ok = mbar_wait(&o_full[t], o_use++ & 1, nullptr);
@@ -633,6 +627,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             tmem_ld32(o_at + x, v);
             tmem_ld32(o_at + x + 32, v + 32);
             tmem_wait_ld();
+            tmem_landed32(v);
+            tmem_landed32(v + 32);
 #pragma unroll
             for (int i = 0; i < 64; ++i) v[i] = __float_as_uint(nan ? NAN : __uint_as_float(v[i]) * inv);
             if (alone) {

@@ -223,16 +223,21 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
     tmem_ld32(s_at, part(0));
   }
   float top = -INFINITY;
+  // (rolled up where S is read twice: with several roles' code running at once, instruction fetches count)
+#pragma unroll(HOLD ? 2 : 1)
+  for (int w2 = 0; w2 < 4; w2 += 2)
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    uint32_t* v = part(w);
+  for (int w1 = 0; w1 < 2; ++w1) {
+    const int w = w2 + w1;
+    uint32_t* v = part(HOLD ? w : w1);
     if (!HOLD) tmem_wait_ld();
     tmem_landed32(v);
-    if (!HOLD) tmem_ld32(s_at + 32 * ((w + 1) & 3), part(w + 1));  // (the last one: the first, for the second reading)
+    if (!HOLD) tmem_ld32(s_at + 32 * ((w + 1) & 3), part(w1 + 1));  // (the last one: the first, for the second reading)
     if (MASKED) {
       const uint32_t out = negative ? 0x7F800000u : 0xFF800000u;
+      const uint32_t bits = w1 == 0 ? (w2 == 0 ? see[0] : see[2]) : (w2 == 0 ? see[1] : see[3]);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = see[w] >> i & 1u ? v[i] : out;
+      for (int i = 0; i < 32; ++i) v[i] = bits >> i & 1u ? v[i] : out;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -264,18 +269,22 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
   const float base = row.m == -INFINITY ? 0.0f : row.m;
   const uint64_t base2 = f32x2(-base, -base);
   uint64_t sum[2] = {0, 0};
+#pragma unroll(HOLD ? 2 : 1)
+  for (int w2 = 0; w2 < 4; w2 += 2)
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w1 = 0; w1 < 2; ++w1) {
+    const int w = w2 + w1;
     uint32_t pk[16];
-    uint32_t* v = part(w);
+    uint32_t* v = part(HOLD ? w : w1);
     if (!HOLD) {
       tmem_wait_ld();
       tmem_landed32(v);
-      if (w < 3) tmem_ld32(s_at + 32 * (w + 1), part(w + 1));
+      if (w1 == 0 || w2 == 0) tmem_ld32(s_at + 32 * (w + 1), part(w1 + 1));
     }
     // (of a masked tile, most 32-key parts are seen by all of a warp's rows or by none)
-    const bool none = MASKED && __all_sync(0xFFFFFFFFu, see[w] == 0u);
-    const bool all = !MASKED || __all_sync(0xFFFFFFFFu, see[w] == 0xFFFFFFFFu);
+    const uint32_t bits = w1 == 0 ? (w2 == 0 ? see[0] : see[2]) : (w2 == 0 ? see[1] : see[3]);
+    const bool none = MASKED && __all_sync(0xFFFFFFFFu, bits == 0u);
+    const bool all = !MASKED || __all_sync(0xFFFFFFFFu, bits == 0xFFFFFFFFu);
     if (none) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) pk[i] = 0u;
@@ -288,8 +297,8 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
         e0 = ex2(e0);
         e1 = ex2(e1);
         if (!all) {
-          e0 = see[w] >> (2 * i) & 1u ? e0 : 0.0f;
-          e1 = see[w] >> (2 * i + 1) & 1u ? e1 : 0.0f;
+          e0 = bits >> (2 * i) & 1u ? e0 : 0.0f;
+          e1 = bits >> (2 * i + 1) & 1u ? e1 : 0.0f;
         }
         sum[i & 1] = add2(sum[i & 1], f32x2(e0, e1));
         pk[i] = pack_p<BF16>(e0, e1);
@@ -297,11 +306,11 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
     }
     // (P's columns 16 w .. lie before those of S that are still to be read, 32 (w + 1) ..)
     tmem_st16(s_at + 16 * w, pk);
-    if (w & 1) {
+    if (w1 == 1) {
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      ready(w >> 1);
+      ready(w2 >> 1);
     }
   }
   float lo, hi;

@@ -8,7 +8,9 @@
 // What bounds it: at 65 slots and 4 heads a group a cached key is worth 260 * 512
 // flops for 256 bytes, twice the tensor cores' balance, so tensor time, with the
 // softmax and the conversion of the cache beside it; with one tile of rows it is
-// about the cache's bytes.
+// about the cache's bytes.  A single row tile would leave the tensor core idle
+// during its softmax, so it is taken twice, over the even and the odd key tiles of
+// its stretch, and joined like two pieces.
 //
 // Cached keys and values come to shared memory as fp16 (e4m3 is exact in it): one
 // warp looks up page numbers and scales and fetches whole pages a tile ahead (a
@@ -154,7 +156,7 @@ struct TreeTile {
   float k_scale[8], v_scale[8];  // of 16 keys each
   uint32_t seen[4];   // cached keys that exist (new ones: the keys below slots)
   uint32_t bad[4];    // keys whose values are not finite (new ones only)
-  float ratio, vref;  // O's unit before / after this tile, and after
+  float vref;         // the unit of values, and so of O, from this tile on
 };
 
 template <int HD>
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
     if (warp == kTreeMmaWarp) {
       const bool leader = elect_one();
       int count = 0;  // key tiles so far
-      int s_use[2] = {0, 0}, segs[2] = {0, 0};
+      int p_use[2] = {0, 0};
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, nullptr));
@@ -236,46 +238,65 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         if (leader) tc_commit(bar);
       };
       const uint64_t q_desc[2] = {flash_desc(q_s, false), flash_desc(q_s + Smem::kOperand, false)};
-      while (ok && walk.next(p, sg)) {
+      auto pv = [&](int t, int i, bool first, bool last) {  // ring entry i into O of slot t
+        const uint32_t turn = p_use[t]++ & 1;
+        const uint64_t vd = flash_desc(at(i), true);
+        wait(&p_full[2 * t], turn);
+        if (ok && leader) issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, vd, first, 0);
+        wait(&p_full[2 * t + 1], turn);
+        if (ok && leader) issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, vd, first, 1);
+        if (ok && last) commit(&o_full[t]);
+      };
+      auto qk = [&](int t, int i) {
+        if (!ok) return;
+        if (leader) issue_qk<HD, false>(tmem + t * 128, q_desc[t], flash_desc(at(i), false));
+        commit(&s_full[t]);
+      };
+      auto release = [&](int i) {
+        if (ok) commit(&empty[i % kTreeStages]);
+      };
+      for (int seg = 0; ok && walk.next(p, sg); ++seg) {
         const int n = sg.key_end - sg.key_begin;
+        wait(&q_full[0], seg & 1);
+        wait(&q_full[1], seg & 1);
         full_wait(2 * count);
-        uint64_t kd = flash_desc(at(2 * count), false);
+        qk(0, 2 * count);
+        if (sg.tiles == 2) {
+          qk(1, 2 * count);
+          release(2 * count);
+          for (int j = 0; j < n && ok; ++j, ++count) {
+            const int vi = 2 * count + 1, ki = vi + 1;
+            const bool more = j + 1 < n;
+            full_wait(vi);
+            if (more) full_wait(ki);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t >= sg.tiles) continue;
-          wait(&q_full[t], segs[t]++ & 1);
-          if (!ok) break;
-          if (leader) issue_qk<HD, false>(tmem + t * 128, q_desc[t], kd);
-          commit(&s_full[t]);
-        }
-        if (ok) commit(&empty[(2 * count) % kTreeStages]);
-        for (int j = 0; j < n && ok; ++j, ++count) {
-          const int vi = 2 * count + 1, ki = 2 * count + 2;
-          const bool more = j + 1 < n;
-          full_wait(vi);
-          if (more) full_wait(ki);
-          const uint64_t vd = flash_desc(at(vi), true);
-          kd = flash_desc(at(ki), false);
+            for (int t = 0; t < 2; ++t) {
+              pv(t, vi, j == 0, !more);
+              if (more) qk(t, ki);
+            }
+            release(vi);
+            if (more) release(ki);
+          }
+        } else {
+          release(2 * count);
+#pragma unroll 1
+          for (int j0 = 0; j0 < n && ok; j0 += 2) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (!ok || t >= sg.tiles) continue;
-            const uint32_t turn = s_use[t]++ & 1;
-            wait(&p_full[2 * t], turn);
-            if (ok && leader) issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, vd, j == 0, 0);
-            wait(&p_full[2 * t + 1], turn);
-            if (!ok) continue;
-            if (leader) issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, vd, j == 0, 1);
-            if (more) {
-              if (leader) issue_qk<HD, false>(tmem + t * 128, q_desc[t], kd);
-              commit(&s_full[t]);
-            } else {
-              commit(&o_full[t]);
+            for (int t = 0; t < 2; ++t) {
+              const int j = j0 + t;
+              if (j >= n) break;
+              const int vi = 2 * (count + j) + 1, ki = vi + 1;
+              if (j + 1 < n) {
+                full_wait(ki);
+                qk(t ^ 1, ki);
+                release(ki);
+              }
+              full_wait(vi);
+              pv(t, vi, j0 == 0, j + 2 >= n);
+              release(vi);
             }
           }
-          if (ok) {
-            commit(&empty[vi % kTreeStages]);
-            if (more) commit(&empty[ki % kTreeStages]);
-          }
+          count += n;
         }
       }
     } else if (warp == kTreeFetchWarp) {
@@ -360,25 +381,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
       const bool swap = HD == 128 && (cc & 4);  // the two halves of a row's threads start with different pieces: no bank conflict
       const int first_chunk = 2 * cc + (swap ? 1 : 0);
       const int place = (first_chunk >> 3) * kHalfBytes + cr * 128, piece0 = ((first_chunk & 7) ^ (cr & 7)) << 4;
-      auto convert = [&](const TreeKeyTile& t, const TreeTile& info, int count, int which, float inv) {
-        uint4 w[kPasses];
+      auto convert = [&](const TreeTile& info, int count, int which, float inv) {
         const uint8_t* st = smem + Smem::kStaging + which * kKeyTile * HD + ct * 16;
-#pragma unroll
-        for (int k = 0; k < kPasses; ++k) w[k] = *reinterpret_cast<const uint4*>(st + k * kConvThreads * 16);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&st_free[which]);
-        room(2 * count + which);
         uint8_t* op = smem + Smem::kRing + ((2 * count + which) % kTreeStages) * Smem::kOperand + place;
         const bool whole = (info.seen[0] & info.seen[1] & info.seen[2] & info.seen[3]) == 0xFFFFFFFFu;
+        constexpr int kBatch = 4;
+#pragma unroll 1
+        for (int k0 = 0; k0 < kPasses; k0 += kBatch) {
+          uint4 w[kBatch];
 #pragma unroll
-        for (int k = 0; k < kPasses; ++k) {
-          const int row = k * kPassRows + cr;
-          const uint32_t in[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-          uint32_t h[8];
+          for (int k = 0; k < kBatch; ++k) w[k] = *reinterpret_cast<const uint4*>(st + (k0 + k) * kConvThreads * 16);
+          if (k0 + kBatch == kPasses) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&st_free[which]);
+          }
+          if (k0 == 0) room(2 * count + which);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) e4m3x4_to_f16x2x2(in[x], h[2 * x], h[2 * x + 1]);
-          if (which) {
-            const float f = info.v_scale[row >> 4] * inv;
+          for (int k = 0; k < kBatch; ++k) {
+            const int row = (k0 + k) * kPassRows + cr;
+            const uint32_t in[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) e4m3x4_to_f16x2x2(in[x], h[2 * x], h[2 * x + 1]);
+            const float f = which ? info.v_scale[row >> 4] * inv : 1.0f;
             if (f != 1.0f) {
               const __half2 f2 = __float2half2_rn(f);
 #pragma unroll
@@ -387,15 +412,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
                 h[x] = *reinterpret_cast<uint32_t*>(&y);
               }
             }
-          }
-          if (!whole && !(info.seen[row >> 5] >> (row & 31) & 1u)) {  // (what no row sees may be NaN, or not there)
+            if (!whole && !(info.seen[row >> 5] >> (row & 31) & 1u)) {  // (what no row sees may be NaN, or not there)
 #pragma unroll
-            for (int x = 0; x < 8; ++x) h[x] = 0u;
+              for (int x = 0; x < 8; ++x) h[x] = 0u;
+            }
+            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+            // (passes are multiples of 8 rows apart: the swizzle is the same)
+            uint8_t* to = op + (k0 + k) * kPassRows * 128;
+            *reinterpret_cast<uint4*>(to + piece0) = swap ? hi : lo;
+            *reinterpret_cast<uint4*>(to + (piece0 ^ 16)) = swap ? lo : hi;
           }
-          const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-          // (passes are multiples of 8 rows apart: the swizzle is the same)
-          *reinterpret_cast<uint4*>(op + k * kPassRows * 128 + piece0) = swap ? hi : lo;
-          *reinterpret_cast<uint4*>(op + k * kPassRows * 128 + (piece0 ^ 16)) = swap ? lo : hi;
         }
         arrive(2 * count + which);
       };
@@ -457,34 +483,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
       for (int count = 0; tw.next(p, cur), cur.kind != kTileNone; ++count) {
         TreeTile& info = tiles[count % kTreeSlots];
         if (cur.first) vref = 1.17549435e-38f;
-        const float before = vref;
         ok = ok && mbar_wait(&st_full[0], count & 1, nullptr);
         if (cur.kind == kTileCached) {
 #pragma unroll
           for (int g = 0; g < 8; ++g) vref = fmaxf(vref, info.v_scale[g]);
-          if (ct == 0) {
-            info.ratio = cur.first ? 1.0f : before / vref;
-            info.vref = vref;
+          if (ct == 0) info.vref = vref;
+          const float inv = 1.0f / vref;
+#pragma unroll 1
+          for (int which = 0; which < 2; ++which) {
+            if (which) ok = ok && mbar_wait(&st_full[1], count & 1, nullptr);
+            convert(info, count, which, inv);
           }
-          convert(cur, info, count, 0, 1.0f);
-          ok = ok && mbar_wait(&st_full[1], count & 1, nullptr);
-          convert(cur, info, count, 1, 1.0f / vref);
         } else {
           ok = ok && mbar_wait(&st_full[1], count & 1, nullptr);
           __syncwarp();
           if (lane == 0) mbar_arrive(&st_free[0]), mbar_arrive(&st_free[1]);
-          uint8_t* k_op = smem + Smem::kRing + ((2 * count) % kTreeStages) * Smem::kOperand;
-          uint8_t* v_op = smem + Smem::kRing + ((2 * count + 1) % kTreeStages) * Smem::kOperand;
-          float scale;
-          room(2 * count);
-          convert_new(cur, 0, vref, scale, info.bad, k_op);
-          if (ct < 8) info.k_scale[ct] = scale;
-          room(2 * count + 1);
-          convert_new(cur, 1, vref, scale, info.bad, v_op);
-          if (ct == 0) {
-            info.ratio = cur.first ? 1.0f : before / vref;
-            info.vref = vref;
+#pragma unroll 1
+          for (int which = 0; which < 2; ++which) {
+            float scale;
+            room(2 * count + which);
+            convert_new(cur, which, vref, scale, info.bad, smem + Smem::kRing + ((2 * count + which) % kTreeStages) * Smem::kOperand);
+            if (which == 0 && ct < 8) info.k_scale[ct] = scale;
           }
+          if (ct == 0) info.vref = vref;
           // (the keys are handed over after the values: the tile's unit goes with them)
           arrive(2 * count);
           arrive(2 * count + 1);
@@ -504,12 +525,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
       };
       while (walk.next(p, sg)) {
         const int n = sg.key_end - sg.key_begin;
-        const int slot = (sg.pair * 2 + t) * p.per_tile + r / p.group, head = sg.kvh * p.group + r % p.group;
-        const bool live = t < sg.tiles && r < p.per_tile * p.group && slot < a.slots;
+        // a single row tile is both slots': t takes every other key tile
+        const bool split = sg.tiles == 1;
+        const int steps = split ? (n + 1 - t) / 2 : n, tile = sg.pair * 2 + (split ? 0 : t);
+        const int slot = tile * p.per_tile + r / p.group, head = sg.kvh * p.group + r % p.group;
+        const bool live = r < p.per_tile * p.group && slot < a.slots;
         const int64_t row = static_cast<int64_t>(sg.req) * a.slots + slot;
         SoftmaxRow sm;
         float vref = 0.0f;
-        if (t < sg.tiles) {
+        {
           // Q to fp16 by a power of two of the row's own: HD / 8 lanes read a row together
           float c = 0.0f;
           {
@@ -518,7 +542,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             const int cx = lane % kL, rx = lane / kL;
 #pragma unroll 8
             for (int i = 0; i < kN; ++i) {
-              const int y = (warp & 3) * 32 + i * kR + rx, sl = (sg.pair * 2 + t) * p.per_tile + y / p.group;
+              const int y = (warp & 3) * 32 + i * kR + rx, sl = tile * p.per_tile + y / p.group;
               uint4 w = make_uint4(0, 0, 0, 0);
               if (y < p.per_tile * p.group && sl < a.slots)
                 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
@@ -548,8 +572,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             if (lane == 0) mbar_arrive(&q_full[t]);
           }
           bool poison = false;
-          for (int j = 0; j < n; ++j) {
-            const int key = sg.key_begin + j;
+          for (int i = 0; i < steps; ++i) {
+            const int j = split ? 2 * i + t : i, key = sg.key_begin + j;
             const bool fresh = a.k_new && key >= sg.cached;
             uint32_t see[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
             if (fresh) {  // which of the new tokens this row sees, while the product runs
@@ -559,8 +583,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
                 for (int w = 0; w < 4; ++w) see[w] = first_bits(slot + 1 - b0, w);
               } else {
                 // the warp's slots, eight at a time: a byte a lane, 32 bytes to a word by ballot
-                const int s0 = (sg.pair * 2 + t) * p.per_tile + (warp & 3) * 32 / p.group;
-                const int s1 = (sg.pair * 2 + t) * p.per_tile + ((warp & 3) * 32 + 31) / p.group;
+                const int s0 = tile * p.per_tile + (warp & 3) * 32 / p.group;
+                const int s1 = tile * p.per_tile + ((warp & 3) * 32 + 31) / p.group;
                 const uint8_t* mask = a.mask + static_cast<int64_t>(sg.req) * a.slots * a.slots + b0 + lane;
                 for (int x = s0; x <= s1; x += 8) {
                   uint8_t byte[8][4];
@@ -593,23 +617,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
               all &= see[w] == 0xFFFFFFFFu;
             }
             const bool masked = !__all_sync(0xFFFFFFFFu, all);
+            const float ratio = i == 0 || vref == info.vref ? 1.0f : vref / info.vref;
             vref = info.vref;
-            const float ratio = info.ratio;
             auto scale = [&](int g) { return c * info.k_scale[g]; };
-            if (masked) softmax_tile<HD, false, false, true, false>(s_at, o_at, j == 0, ratio, c < 0.0f, scale, see, sm, ready);
-            else softmax_tile<HD, false, false, false, false>(s_at, o_at, j == 0, ratio, c < 0.0f, scale, see, sm, ready);
+            if (masked) softmax_tile<HD, false, false, true, false>(s_at, o_at, i == 0, ratio, c < 0.0f, scale, see, sm, ready);
+            else softmax_tile<HD, false, false, false, false>(s_at, o_at, i == 0, ratio, c < 0.0f, scale, see, sm, ready);
           }
           if (poison) sm.l = NAN;
-          if (ok) ok = mbar_wait(&o_full[t], o_use++ & 1, nullptr);
+          if (steps > 0) ok = ok && mbar_wait(&o_full[t], o_use++ & 1, nullptr);
           tc_fence_after();
         }
         count += n;
 
         // --- the end of a stretch: the answer, or a part of it
         const int c_first = cut.of(sg.first), c_last = cut.of(sg.first + sg.units - 1);
-        const bool alone = c_first == c_last;
+        const bool alone = c_first == c_last && !split;
         auto out_of = [&](int y) -> __nv_bfloat16* {  // row y of the tile
-          const int sl = (sg.pair * 2 + t) * p.per_tile + y / p.group;
+          const int sl = tile * p.per_tile + y / p.group;
           if (y >= p.per_tile * p.group || sl >= a.slots) return nullptr;
           return static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(sg.req) * a.slots + sl) * a.out_row_stride +
                  (sg.kvh * p.group + y % p.group) * a.out_head_stride;
@@ -617,10 +641,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         auto finish_lse = [&](float top, float sum) {
           if (live && a.lse) a.lse[row * a.n_q + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
         };
-        if (t < sg.tiles) {
+        {
           const float inv = alone ? (sm.l == 0.0f ? 0.0f : vref / sm.l) : vref;
           const size_t mine = static_cast<size_t>(2 * piece + (piece == c_first)) * 2 + t;
-          const bool nan = sm.l != sm.l;
+          const bool nan = sm.l != sm.l, none = steps == 0;  // (none: nothing was put into O)
 #pragma unroll
           for (int x = 0; x < HD; x += 64) {
             uint32_t v[64];
@@ -630,7 +654,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             tmem_landed32(v);
             tmem_landed32(v + 32);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) v[i] = __float_as_uint(nan ? NAN : __uint_as_float(v[i]) * inv);
+            for (int i = 0; i < 64; ++i) v[i] = none ? 0u : __float_as_uint(nan ? NAN : __uint_as_float(v[i]) * inv);
             if (alone) {
               uint4 w[8];
 #pragma unroll
@@ -665,20 +689,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             if (s_last) *done = 0u;  // ready for the next call
           }
           asm volatile("bar.sync 1, 256;" ::: "memory");
-          if (s_last && t < sg.tiles) {
+          if (s_last && !(split && t == 1)) {
             __threadfence();
-            auto part_of = [&](int x) { return static_cast<size_t>(2 * x + (x == c_first)) * 2 + t; };
+            // parts in the order of keys: of each piece that of this row tile, or both slots' of a split one
+            const int parts = (c_last - c_first + 1) << (split ? 1 : 0);
+            auto part_of = [&](int x) {
+              const int pc = c_first + (split ? x >> 1 : x);
+              return static_cast<size_t>(2 * pc + (pc == c_first)) * 2 + (split ? x & 1 : t);
+            };
             float top = -INFINITY, sum = 0.0f;
-            for (int x = c_first; x <= c_last; ++x) top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(stats) + part_of(x) * 128 + r).x);
+            for (int x = 0; x < parts; ++x) top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(stats) + part_of(x) * 128 + r).x);
             const float base = top == -INFINITY ? 0.0f : top;
-            for (int x = c_first; x <= c_last; ++x) {
+            for (int x = 0; x < parts; ++x) {
               const float2 ml = __ldcg(reinterpret_cast<const float2*>(stats) + part_of(x) * 128 + r);
               sum += ml.y * ex2(ml.x - base);
             }
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             for (int x = 0; x < HD; x += 64) {
               float4 o[16] = {};
-              for (int k = c_first; k <= c_last; ++k) {
+              for (int k = 0; k < parts; ++k) {
                 const float f = ex2(__ldcg(reinterpret_cast<const float2*>(stats) + part_of(k) * 128 + r).x - base);
                 const float4* y = reinterpret_cast<const float4*>(p.part) + (part_of(k) * (HD / 4) + x / 4) * 128 + r;
 #pragma unroll

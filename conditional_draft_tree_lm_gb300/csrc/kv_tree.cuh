@@ -43,6 +43,7 @@ struct TreeParams {
   dt_cache_attention_args a;
   int group, shift;
   int per_tile;     // slots of a row tile
+  uint32_t inverse; // ceil(2^16 / group): y / group = y * inverse >> 16 for y < 128
   int pairs, odd;   // pairs of row tiles, and whether one is left
   int fresh_tiles;  // key tiles of new tokens
   unsigned* done;   // [n_req * n_kv * (pairs + odd)] zero between launches
@@ -156,8 +157,12 @@ struct TreeTile {
   float k_scale[8], v_scale[8];  // of 16 keys each
   uint32_t seen[4];   // cached keys that exist (new ones: the keys below slots)
   uint32_t bad[4];    // keys whose values are not finite (new ones only)
+  float v_top;        // the largest v_scale
+  int plain;          // all keys exist, all v_scale are v_top
   float vref;         // the unit of values, and so of O, from this tile on
 };
+
+DT_DEVINL int by_group(const TreeParams& p, int y) { return static_cast<int>(static_cast<uint32_t>(y) * p.inverse >> 16); }
 
 template <int HD>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
@@ -341,7 +346,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
           if (!ok) break;
           // (the place is free: the tile four before this one is behind its softmax, too)
           if (which == 0) {
+            const float v_top = warp_max(lane < 8 ? gc.vs : 0.0f);
+            const bool plain = __all_sync(0xFFFFFFFFu, lane >= 8 || (gc.id >= 0 && gc.vs == v_top)) && cur.len - cur.key0 >= kKeyTile;
             if (lane < 8) info.k_scale[lane] = gc.ks, info.v_scale[lane] = gc.vs;
+            if (lane == 0) info.v_top = v_top, info.plain = plain;
             if (lane < 4) {
               const uint32_t two = there >> (2 * lane);
               info.seen[lane] = cur.kind == kTileNew ? first_bits(a.slots - cur.key0, lane)
@@ -377,106 +385,136 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
       // (where a wait gives up the loop goes on without waiting: other warps may stand at its named barrier)
       bool ok = true;
       auto room = [&](int i) { ok = ok && mbar_wait(&empty[i % kTreeStages], ((i / kTreeStages) & 1) ^ 1, nullptr); };
-      // a cached tile's K or V out of the staging place
-      const bool swap = HD == 128 && (cc & 4);  // the two halves of a row's threads start with different pieces: no bank conflict
-      const int first_chunk = 2 * cc + (swap ? 1 : 0);
-      const int place = (first_chunk >> 3) * kHalfBytes + cr * 128, piece0 = ((first_chunk & 7) ^ (cr & 7)) << 4;
-      auto convert = [&](const TreeTile& info, int count, int which, float inv) {
-        const uint8_t* st = smem + Smem::kStaging + which * kKeyTile * HD + ct * 16;
+      // a cached tile's K or V out of the staging place.  The two halves of a row's threads begin with different
+      // halves of their 16 bytes, so that their stores meet different banks.
+      const bool swap = HD == 128 && (cc & 4);
+      const int chunk0 = 2 * cc + (swap ? 1 : 0);
+      const int place = (chunk0 >> 3) * kHalfBytes + cr * 128, piece0 = ((chunk0 & 7) ^ (cr & 7)) << 4;
+      const uint8_t* st0 = smem + Smem::kStaging + ct * 16 + (swap ? 8 : 0);
+      const int st1 = swap ? -8 : 8;
+      // (passes are multiples of 8 rows apart: the swizzle is the same; plain: neither masks nor factors)
+      auto convert = [&](const TreeTile& info, int count, int which, bool plain, float inv) {
+        const uint8_t* st = st0 + which * kKeyTile * HD;
         uint8_t* op = smem + Smem::kRing + ((2 * count + which) % kTreeStages) * Smem::kOperand + place;
-        const bool whole = (info.seen[0] & info.seen[1] & info.seen[2] & info.seen[3]) == 0xFFFFFFFFu;
         constexpr int kBatch = 4;
 #pragma unroll 1
         for (int k0 = 0; k0 < kPasses; k0 += kBatch) {
-          uint4 w[kBatch];
+          uint2 w[kBatch][2];
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) w[k] = *reinterpret_cast<const uint4*>(st + (k0 + k) * kConvThreads * 16);
+          for (int k = 0; k < kBatch; ++k) {
+            const uint8_t* x = st + (k0 + k) * kConvThreads * 16;
+            w[k][0] = *reinterpret_cast<const uint2*>(x);
+            w[k][1] = *reinterpret_cast<const uint2*>(x + st1);
+          }
           if (k0 + kBatch == kPasses) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&st_free[which]);
           }
           if (k0 == 0) room(2 * count + which);
+          uint32_t h[kBatch][8];
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int row = (k0 + k) * kPassRows + cr;
-            const uint32_t in[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-            uint32_t h[8];
+          for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) e4m3x4_to_f16x2x2(in[x], h[2 * x], h[2 * x + 1]);
-            const float f = which ? info.v_scale[row >> 4] * inv : 1.0f;
-            if (f != 1.0f) {
-              const __half2 f2 = __float2half2_rn(f);
+            for (int y = 0; y < 2; ++y) {
+              e4m3x4_to_f16x2x2(w[k][y].x, h[k][4 * y], h[k][4 * y + 1]);
+              e4m3x4_to_f16x2x2(w[k][y].y, h[k][4 * y + 2], h[k][4 * y + 3]);
+            }
+          if (!plain) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const int row = (k0 + k) * kPassRows + cr;
+              const bool seen = info.seen[row >> 5] >> (row & 31) & 1u;  // (what no row sees may be NaN, or not there)
+              const __half2 f2 = __float2half2_rn(which ? info.v_scale[row >> 4] * inv : 1.0f);
 #pragma unroll
               for (int x = 0; x < 8; ++x) {
-                __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[x]), f2);
-                h[x] = *reinterpret_cast<uint32_t*>(&y);
+                const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[k][x]), f2);
+                h[k][x] = seen ? *reinterpret_cast<const uint32_t*>(&y) : 0u;
               }
             }
-            if (!whole && !(info.seen[row >> 5] >> (row & 31) & 1u)) {  // (what no row sees may be NaN, or not there)
+          }
 #pragma unroll
-              for (int x = 0; x < 8; ++x) h[x] = 0u;
-            }
-            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-            // (passes are multiples of 8 rows apart: the swizzle is the same)
+          for (int k = 0; k < kBatch; ++k) {
             uint8_t* to = op + (k0 + k) * kPassRows * 128;
-            *reinterpret_cast<uint4*>(to + piece0) = swap ? hi : lo;
-            *reinterpret_cast<uint4*>(to + (piece0 ^ 16)) = swap ? lo : hi;
+            *reinterpret_cast<uint4*>(to + piece0) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
+            *reinterpret_cast<uint4*>(to + (piece0 ^ 16)) = make_uint4(h[k][4], h[k][5], h[k][6], h[k][7]);
           }
         }
         arrive(2 * count + which);
       };
-      // a new tile's K or V, bf16: its largest finite magnitude first, then fp16 by a power of two
-      auto convert_new = [&](const TreeKeyTile& t, int which, float& vref, float& scale, uint32_t* bad, uint8_t* op) {
-        constexpr int kL = HD / 8, kR = kConvThreads / kL, kP = kKeyTile / kR;
-        const int c8 = ct % kL, r8 = ct / kL;
-        const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(which ? a.v_new : a.k_new);
-        const int64_t rs = which ? a.v_row_stride : a.k_row_stride, hs = which ? a.v_head_stride : a.k_head_stride;
-        float top = 0.0f;
-        auto piece_of = [&](int k) {
-          const int b = t.key0 + k * kR + r8;
-          return b < a.slots ? __ldg(reinterpret_cast<const uint4*>(x + (static_cast<int64_t>(t.req) * a.slots + b) * rs +
-                                                                    t.kvh * hs + c8 * 8))
-                             : make_uint4(0, 0, 0, 0);
-        };
-        // (read twice, the second time from L1: a thread's part would take 64 registers)
-#pragma unroll 8
-        for (int k = 0; k < kP; ++k) {
-          const uint4 w = piece_of(k);
-          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-          bool odd = false;
+      // A new tile, bf16: the largest finite magnitudes first, then fp16 by a power of two each.  K stays in
+      // registers between, V is read twice.
+      constexpr int kL = HD / 8, kR = kConvThreads / kL, kP = kKeyTile / kR;
+      const int c8 = ct % kL, r8 = ct / kL;
+      auto piece_of = [&](const TreeKeyTile& t, const void* x, int64_t row_stride, int64_t head_stride, int k) {
+        const int b = t.key0 + k * kR + r8;
+        return b < a.slots ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) +
+                                                                  (static_cast<int64_t>(t.req) * a.slots + b) * row_stride +
+                                                                  t.kvh * head_stride + c8 * 8))
+                           : make_uint4(0, 0, 0, 0);
+      };
+      auto largest = [&](const uint4& w, float& top) {  // returns whether something is not finite
+        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+        bool odd = false;
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float lo = fabsf(__uint_as_float(in[y] << 16)), hi = fabsf(__uint_as_float(in[y] & 0xFFFF0000u));
-            const bool fl = lo <= 3.402823466e38f, fh = hi <= 3.402823466e38f;
-            odd |= !fl || !fh;
-            top = fmaxf(top, fmaxf(fl ? lo : 0.0f, fh ? hi : 0.0f));
-          }
-          // the key's value takes no part in the product, the rows that see it become NaN
-          if (which && odd) atomicOr(&bad[(k * kR + r8) >> 5], 1u << ((k * kR + r8) & 31));
+        for (int y = 0; y < 4; ++y) {
+          const float lo = fabsf(__uint_as_float(in[y] << 16)), hi = fabsf(__uint_as_float(in[y] & 0xFFFF0000u));
+          const bool fl = lo <= 3.402823466e38f, fh = hi <= 3.402823466e38f;
+          odd |= !fl || !fh;
+          top = fmaxf(top, fmaxf(fl ? lo : 0.0f, fh ? hi : 0.0f));
         }
-        top = warp_max(top);
-        if (lane == 0) s_max[which][cw] = top;
+        return odd;
+      };
+      auto put_new = [&](uint8_t* op, int k, const uint4& w, float inv) {
+        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+        uint32_t h[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          h[y] = pack_f16(__uint_as_float(in[y] << 16) * inv, __uint_as_float(in[y] & 0xFFFF0000u) * inv);
+        put(op, k * kR + r8, c8, make_uint4(h[0], h[1], h[2], h[3]));
+      };
+      auto convert_new = [&](const TreeKeyTile& t, TreeTile& info, int count, float& vref) {
+        uint4 w[kP];
+#pragma unroll
+        for (int k = 0; k < kP; ++k) w[k] = piece_of(t, a.k_new, a.k_row_stride, a.k_head_stride, k);
+        float top[2] = {0.0f, 0.0f};
+#pragma unroll 8
+        for (int k = 0; k < kP; ++k)
+          // the key's value takes no part in the product, the rows that see it become NaN
+          if (largest(piece_of(t, a.v_new, a.v_row_stride, a.v_head_stride, k), top[1]))
+            atomicOr(&info.bad[(k * kR + r8) >> 5], 1u << ((k * kR + r8) & 31));
+#pragma unroll
+        for (int k = 0; k < kP; ++k) largest(w[k], top[0]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          top[x] = warp_max(top[x]);
+          if (lane == 0) s_max[x][cw] = top[x];
+        }
         asm volatile("bar.sync 2, %0;" ::"n"(kConvThreads) : "memory");
 #pragma unroll
-        for (int k = 0; k < kTreeConvWarps; ++k) top = fmaxf(top, s_max[which][k]);
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int k = 0; k < kTreeConvWarps; ++k) top[x] = fmaxf(top[x], s_max[x][k]);
         asm volatile("bar.sync 2, %0;" ::"n"(kConvThreads) : "memory");
-        scale = kv_pow2_scale(top);
-        if (which) vref = fmaxf(vref, scale), scale = vref;
-        const float inv = 1.0f / scale;
+        const float k_scale = kv_pow2_scale(top[0]);
+        vref = fmaxf(vref, kv_pow2_scale(top[1]));
+        if (ct < 8) info.k_scale[ct] = k_scale;
+        if (ct == 0) info.vref = vref;
+        const float k_inv = 1.0f / k_scale, v_inv = 1.0f / vref;
+        room(2 * count);
+        uint8_t* op = smem + Smem::kRing + ((2 * count) % kTreeStages) * Smem::kOperand;
+#pragma unroll
+        for (int k = 0; k < kP; ++k) put_new(op, k, w[k], k_inv);
+        arrive(2 * count);
+        room(2 * count + 1);
+        op = smem + Smem::kRing + ((2 * count + 1) % kTreeStages) * Smem::kOperand;
 #pragma unroll 8
         for (int k = 0; k < kP; ++k) {
           const int row = k * kR + r8;
-          const uint4 w = piece_of(k);
-          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-          uint32_t h[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            h[y] = pack_f16(__uint_as_float(in[y] << 16) * inv, __uint_as_float(in[y] & 0xFFFF0000u) * inv);
-          const bool zero = which && (bad[row >> 5] >> (row & 31) & 1u);
-          put(op, row, c8, zero ? make_uint4(0, 0, 0, 0) : make_uint4(h[0], h[1], h[2], h[3]));
+          const bool bad = info.bad[row >> 5] >> (row & 31) & 1u;
+          put_new(op, k, bad ? make_uint4(0, 0, 0, 0) : piece_of(t, a.v_new, a.v_row_stride, a.v_head_stride, k), v_inv);
         }
+        arrive(2 * count + 1);
       };
-
       TreeKeyTile cur;
       TreeTileWalk tw = {walk, {}, 0};
       float vref = 0.0f;
@@ -485,30 +523,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         if (cur.first) vref = 1.17549435e-38f;
         ok = ok && mbar_wait(&st_full[0], count & 1, nullptr);
         if (cur.kind == kTileCached) {
-#pragma unroll
-          for (int g = 0; g < 8; ++g) vref = fmaxf(vref, info.v_scale[g]);
+          vref = fmaxf(vref, info.v_top);
           if (ct == 0) info.vref = vref;
           const float inv = 1.0f / vref;
+          const bool plain = info.plain, even = vref == info.v_top;
 #pragma unroll 1
           for (int which = 0; which < 2; ++which) {
             if (which) ok = ok && mbar_wait(&st_full[1], count & 1, nullptr);
-            convert(info, count, which, inv);
+            convert(info, count, which, plain && (which == 0 || even), inv);
           }
         } else {
           ok = ok && mbar_wait(&st_full[1], count & 1, nullptr);
           __syncwarp();
           if (lane == 0) mbar_arrive(&st_free[0]), mbar_arrive(&st_free[1]);
-#pragma unroll 1
-          for (int which = 0; which < 2; ++which) {
-            float scale;
-            room(2 * count + which);
-            convert_new(cur, which, vref, scale, info.bad, smem + Smem::kRing + ((2 * count + which) % kTreeStages) * Smem::kOperand);
-            if (which == 0 && ct < 8) info.k_scale[ct] = scale;
-          }
-          if (ct == 0) info.vref = vref;
-          // (the keys are handed over after the values: the tile's unit goes with them)
-          arrive(2 * count);
-          arrive(2 * count + 1);
+          convert_new(cur, info, count, vref);
         }
       }
     } else {
@@ -528,7 +556,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         // a single row tile is both slots': t takes every other key tile
         const bool split = sg.tiles == 1;
         const int steps = split ? (n + 1 - t) / 2 : n, tile = sg.pair * 2 + (split ? 0 : t);
-        const int slot = tile * p.per_tile + r / p.group, head = sg.kvh * p.group + r % p.group;
+        const int slot = tile * p.per_tile + by_group(p, r), head = sg.kvh * p.group + r - by_group(p, r) * p.group;
         const bool live = r < p.per_tile * p.group && slot < a.slots;
         const int64_t row = static_cast<int64_t>(sg.req) * a.slots + slot;
         SoftmaxRow sm;
@@ -542,12 +570,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             const int cx = lane % kL, rx = lane / kL;
 #pragma unroll 8
             for (int i = 0; i < kN; ++i) {
-              const int y = (warp & 3) * 32 + i * kR + rx, sl = tile * p.per_tile + y / p.group;
+              const int y = (warp & 3) * 32 + i * kR + rx, ys = by_group(p, y), sl = tile * p.per_tile + ys;
               uint4 w = make_uint4(0, 0, 0, 0);
               if (y < p.per_tile * p.group && sl < a.slots)
                 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
                                                          (static_cast<int64_t>(sg.req) * a.slots + sl) * a.q_row_stride +
-                                                         (sg.kvh * p.group + y % p.group) * a.q_head_stride) + cx);
+                                                         (sg.kvh * p.group + y - ys * p.group) * a.q_head_stride) + cx);
               const uint32_t in[4] = {w.x, w.y, w.z, w.w};
               float amax = 0.0f;
 #pragma unroll
@@ -583,8 +611,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
                 for (int w = 0; w < 4; ++w) see[w] = first_bits(slot + 1 - b0, w);
               } else {
                 // the warp's slots, eight at a time: a byte a lane, 32 bytes to a word by ballot
-                const int s0 = tile * p.per_tile + (warp & 3) * 32 / p.group;
-                const int s1 = tile * p.per_tile + ((warp & 3) * 32 + 31) / p.group;
+                const int s0 = tile * p.per_tile + by_group(p, (warp & 3) * 32);
+                const int s1 = tile * p.per_tile + by_group(p, (warp & 3) * 32 + 31);
                 const uint8_t* mask = a.mask + static_cast<int64_t>(sg.req) * a.slots * a.slots + b0 + lane;
                 for (int x = s0; x <= s1; x += 8) {
                   uint8_t byte[8][4];
@@ -633,10 +661,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         const int c_first = cut.of(sg.first), c_last = cut.of(sg.first + sg.units - 1);
         const bool alone = c_first == c_last && !split;
         auto out_of = [&](int y) -> __nv_bfloat16* {  // row y of the tile
-          const int sl = tile * p.per_tile + y / p.group;
+          const int ys = by_group(p, y), sl = tile * p.per_tile + ys;
           if (y >= p.per_tile * p.group || sl >= a.slots) return nullptr;
           return static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(sg.req) * a.slots + sl) * a.out_row_stride +
-                 (sg.kvh * p.group + y % p.group) * a.out_head_stride;
+                 (sg.kvh * p.group + y - ys * p.group) * a.out_head_stride;
         };
         auto finish_lse = [&](float top, float sum) {
           if (live && a.lse) a.lse[row * a.n_q + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
@@ -681,16 +709,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
           tc_fence_before();  // (O is read before the next segment's first product writes it)
         }
         if (!alone) {
-          __threadfence();
+          const bool own = c_first == c_last;  // (a split row tile of one piece: both parts are this CTA's)
+          if (!own) __threadfence();
           asm volatile("bar.sync 1, 256;" ::: "memory");
-          if (tid == 0) {
+          if (own) {
+            if (tid == 0) s_last = 1;
+          } else if (tid == 0) {
             unsigned* done = p.done + (static_cast<size_t>(sg.req) * n_kv + sg.kvh) * (p.pairs + p.odd) + sg.pair;
             s_last = atomicAdd(done, 1u) == static_cast<unsigned>(c_last - c_first);
             if (s_last) *done = 0u;  // ready for the next call
           }
           asm volatile("bar.sync 1, 256;" ::: "memory");
           if (s_last && !(split && t == 1)) {
-            __threadfence();
+            if (!own) __threadfence();
             // parts in the order of keys: of each piece that of this row tile, or both slots' of a split one
             const int parts = (c_last - c_first + 1) << (split ? 1 : 0);
             auto part_of = [&](int x) {

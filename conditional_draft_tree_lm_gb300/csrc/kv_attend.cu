@@ -71,7 +71,7 @@ extern "C" dt_status dt_cache_attention(const dt_kv_cache* cache, const dt_cache
   p.pairs = row_tiles / 2;
   p.odd = row_tiles % 2;
   p.fresh_tiles = a.k_new ? (a.slots + kKeyTile - 1) / kKeyTile : 0;
-  const int64_t key_tiles = (static_cast<int64_t>(a.max_blocks) * cache->page + kKeyTile - 1) / kKeyTile + p.fresh_tiles + 1;
+  const int64_t key_tiles = (static_cast<int64_t>(a.max_blocks) * cache->page + kKeyTile - 1) / kKeyTile + p.fresh_tiles * kNewCost + 1;
   const int64_t units = key_tiles * (p.pairs + p.odd) * a.n_req * cache->n_kv;
   if (units > (1 << 30)) return kv_fail(DT_ERR_SHAPE, "%s: more than 2^30 tiles over all requests and heads", who);
   if (static_cast<int64_t>(a.n_req) * cache->n_kv * (p.pairs + p.odd) > kMaxJoins)

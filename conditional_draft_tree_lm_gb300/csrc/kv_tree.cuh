@@ -22,8 +22,9 @@
 // tile.  fp16 keeps 11 bits of P where bf16 would keep 8.
 //
 // Split.  The work is the list of (key/value head, request, row tiles, key tile),
-// cut into equal pieces, one for each SM; a unit is a key tile for two row tiles
-// and two key tiles for one.  A stretch that several pieces share is joined by the
+// cut into equal pieces, one for each SM.  A tile of new keys counts kNewCost times
+// (it is read and reduced before it can be converted: 18 000 cycles against 4 400).
+// A stretch that several pieces share is joined by the
 // CTA that finishes last, in the order of keys.
 #pragma once
 
@@ -50,17 +51,19 @@ struct TreeParams {
   float* part;      // [2 * pieces][2 tiles][HD / 4][128][4], then [2 * pieces][2][128][2]
 };
 
-// The key tiles of a request, and its units over all its row tiles.
-DT_DEVINL int tree_key_tiles(int len, int max_len, int fresh) {
+#ifndef DT_NEW_COST
+#define DT_NEW_COST 4
+#endif
+constexpr int kNewCost = DT_NEW_COST;
+
+// What a row tile or a pair of them costs over a request's keys, at least 1.
+DT_DEVINL int tree_cost(int len, int max_len, int fresh) {
   len = min(max(len, 0), max_len);
-  return max(1, (len + kKeyTile - 1) / kKeyTile + fresh);
+  return max(1, (len + kKeyTile - 1) / kKeyTile + fresh * kNewCost);
 }
 struct TreeUnits {
-  int max_len, fresh, pairs, odd;
-  DT_DEVINL int operator()(int len) const {
-    const int kt = tree_key_tiles(len, max_len, fresh);
-    return pairs * kt + odd * ((kt + 1) / 2);
-  }
+  int max_len, fresh, row_tiles;  // row_tiles: pairs and the odd one
+  DT_DEVINL int operator()(int len) const { return row_tiles * tree_cost(len, max_len, fresh); }
 };
 
 // A stretch of key tiles of one (head, request, pair of row tiles or single one).
@@ -78,21 +81,24 @@ struct TreeWalk {
     if (u >= u_end) return false;
     const int max_len = p.a.max_blocks << p.shift;
     const int len = min(max(p.a.length[req], 0), max_len);
-    const int kt = tree_key_tiles(len, max_len, p.fresh_tiles), half = (kt + 1) / 2;
+    const int cost = tree_cost(len, max_len, p.fresh_tiles);
     s.req = req;
     s.kvh = kvh;
     s.len = len;
     s.cached = (len + kKeyTile - 1) / kKeyTile;
-    s.pair = min(local / kt, p.pairs);
+    s.pair = local / cost;
     s.tiles = s.pair < p.pairs ? 2 : 1;
-    const int in_req = s.pair * kt;
-    s.first = base + in_req;
-    s.units = s.tiles == 2 ? kt : half;
-    const int stop = min(u_end, s.first + s.units);
-    const int per = 3 - s.tiles;  // key tiles of a unit
-    s.key_begin = (u - s.first) * per;
-    s.key_end = min(kt, (stop - s.first) * per);
-    const int total = p.pairs * kt + p.odd * half;
+    s.first = base + s.pair * cost;
+    s.units = cost;
+    const int stop = min(u_end, s.first + cost);
+    // a key tile belongs to the piece that its first unit is in; a stretch inside a new tile holds none
+    auto tiles_before = [&](int x) {
+      const int fresh = x - s.cached;
+      return fresh <= 0 ? x : s.cached + (fresh + kNewCost - 1) / kNewCost;
+    };
+    s.key_begin = tiles_before(u - s.first);
+    s.key_end = stop == s.first + cost ? max(1, s.cached + p.fresh_tiles) : tiles_before(stop - s.first);
+    const int total = (p.pairs + p.odd) * cost;
     local += stop - u;
     u = stop;
     if (local == total) {
@@ -117,7 +123,7 @@ struct TreeTileWalk {
   DT_DEVINL void next(const TreeParams& p, TreeKeyTile& t) {
     t.kind = kTileNone;
     t.first = 0;
-    if (sg.tiles == 0 || key >= sg.key_end) {
+    while (sg.tiles == 0 || key >= sg.key_end) {
       if (!walk.next(p, sg)) {
         sg.tiles = 0;
         return;
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
     fence_mbar_init();
   }
   tc_fence_before();
-  const TreeUnits units = {a.max_blocks << p.shift, p.fresh_tiles, p.pairs, p.odd};
+  const TreeUnits units = {a.max_blocks << p.shift, p.fresh_tiles, p.pairs + p.odd};
   TileRow<128, TreeUnits> row_of = {a.length, a.n_req, units, 0, s_start};
   row_of.sum(scratch);  // (ends with a barrier)
   tc_fence_after();
@@ -264,6 +270,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         const int n = sg.key_end - sg.key_begin;
         wait(&q_full[0], seg & 1);
         wait(&q_full[1], seg & 1);
+        if (n == 0) continue;
         full_wait(2 * count);
         qk(0, 2 * count);
         if (sg.tiles == 2) {

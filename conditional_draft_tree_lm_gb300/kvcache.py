@@ -15,7 +15,8 @@ computes: tensors become pointers, a refused call raises ``DtreeError``.
 from __future__ import annotations
 
 import ctypes
-from ctypes import POINTER, byref, c_float, c_int, c_int64, c_size_t, c_void_p
+import struct
+from ctypes import c_float, c_int, c_int64, c_size_t, c_void_p
 
 from .dtree import DtreeError, load_library
 
@@ -63,6 +64,17 @@ class _Prompt(ctypes.Structure):
                 ("out_row_stride", c_int64), ("out_head_stride", c_int64), ("row_start", c_void_p), ("lse", c_void_p)]
 
 
+def _packer(cls):
+    """Packs a mirror's fields, given in order, to the bytes of the C struct (native alignment): several times
+    faster than filling a ctypes.Structure, and a call of a few microseconds notices."""
+    codes = {c_int: "i", c_int64: "q", c_float: "f", c_void_p: "P", c_size_t: "N"}
+    s = struct.Struct("@" + "".join(codes[t] for _, t in cls._fields_) + "0P")  # (0P: the tail's padding)
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_cache, _pack_plan, _pack_append, _pack_attend, _pack_prompt = map(_packer, (_Cache, _Plan, _Append, _Attend, _Prompt))
+
 _lib = None
 
 
@@ -71,60 +83,58 @@ def _library():
     if _lib is None:
         lib = load_library()
         for name, res, args in (
-                ("dt_kv_plan", c_int, [POINTER(_Plan), c_void_p]),
-                ("dt_kv_append", c_int, [POINTER(_Cache), POINTER(_Append), c_void_p]),
-                ("dt_cache_attention", c_int, [POINTER(_Cache), POINTER(_Attend), c_void_p]),
+                ("dt_kv_plan", c_int, [c_void_p] * 2),
+                ("dt_kv_append", c_int, [c_void_p] * 3),
+                ("dt_cache_attention", c_int, [c_void_p] * 3),
                 ("dt_cache_attention_workspace", c_size_t, [c_int] * 5),
-                ("dt_prompt_attention", c_int, [POINTER(_Prompt), c_void_p])):
+                ("dt_prompt_attention", c_int, [c_void_p] * 2)):
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = res, args
         _lib = lib
     return _lib
 
 
-def _stream(stream, device):
+def _stream(stream, index):
     import torch
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _call(status, where):
-    if status != 0:
-        raise DtreeError(status, where + ": " + _lib.dt_last_error().decode(errors="replace"))
+def _refused(status, where):
+    return DtreeError(status, where + ": " + _lib.dt_last_error().decode(errors="replace"))
 
 
-def _flat(t, dtype, numel, name, device):
-    """Pointer of a contiguous tensor of `numel` elements."""
-    if t.dtype != dtype:
+def _flat(t, dtype, numel, name, index):
+    """Pointer of a contiguous tensor of `numel` elements on CUDA device `index`."""
+    if t.dtype is dtype and t.get_device() == index and t.numel() == numel and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the others on {device}")
-    if t.numel() != numel or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor of {numel} elements, got {tuple(t.shape)}")
-    return t.data_ptr()
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, the others on cuda:{index}")
+    raise ValueError(f"{name}: expected a contiguous tensor of {numel} elements, got {tuple(t.shape)}")
 
 
-def _heads(t, lead, heads, dim, name, device):
+def _heads(t, lead, heads, dim, name, index):
     """Pointer, row stride and head stride of a bf16 tensor [*lead, heads, dim].
     Only rows and heads may be strided: several leading dimensions must fold into
     one row index, and channels must be adjacent."""
     import torch
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the others on {device}")
-    if tuple(t.shape) != (*lead, heads, dim):
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, the others on cuda:{index}")
+    if t.shape != (*lead, heads, dim):
         raise ValueError(f"{name}: expected {(*lead, heads, dim)}, got {tuple(t.shape)}")
     st = t.stride()
     if st[-1] != 1 or (len(lead) == 2 and lead[0] > 1 and st[0] != st[1] * lead[1]):
         raise ValueError(f"{name}: strides {st}: channels must be adjacent and rows evenly spaced")
-    row, head = st[-3], st[-2]
-    return t.data_ptr(), (row if lead[-1] > 1 or len(lead) == 1 else st[0]), (head if heads > 1 else 0)
+    return t.data_ptr(), (st[-3] if lead[-1] > 1 or len(lead) == 1 else st[0]), (st[-2] if heads > 1 else 0)
 
 
 def _on_device(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
 class KvCache:
@@ -135,15 +145,14 @@ class KvCache:
         import torch
         if k.dim() != 4:
             raise ValueError("k: expected [n_pages, n_kv, page, head_dim]")
-        self.device = _on_device(k, "k")
+        self.index = index = _on_device(k, "k")
         self.n_pages, self.n_kv, self.page, self.head_dim = k.shape
         n, s = k.numel(), self.n_pages * self.n_kv
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.c = _Cache(_flat(k, torch.float8_e4m3fn, n, "k", self.device),
-                        _flat(v, torch.float8_e4m3fn, n, "v", self.device),
-                        _flat(k_scale, torch.float32, s, "k_scale", self.device),
-                        _flat(v_scale, torch.float32, s, "v_scale", self.device),
-                        self.n_pages, self.page, self.n_kv, self.head_dim)
+        self.c = _pack_cache(_flat(k, torch.float8_e4m3fn, n, "k", index), _flat(v, torch.float8_e4m3fn, n, "v", index),
+                             _flat(k_scale, torch.float32, s, "k_scale", index),
+                             _flat(v_scale, torch.float32, s, "v_scale", index),
+                             self.n_pages, self.page, self.n_kv, self.head_dim)
 
     @classmethod
     def empty(cls, n_pages, page, n_kv, head_dim, device="cuda"):
@@ -164,10 +173,10 @@ class AttentionWorkspace:
 
     def reserve(self, n_req, slots, n_q, n_kv, head_dim, device="cuda"):
         import torch
-        sizes = (n_req, slots, n_q, n_kv, head_dim)
+        sizes = (n_req, slots, n_q, n_kv, head_dim, device)
         if sizes != self.sizes:
-            need = _library().dt_cache_attention_workspace(*sizes)
-            if self.buffer is None or self.buffer.numel() < need or self.buffer.device != torch.device(device):
+            need = _library().dt_cache_attention_workspace(*sizes[:5])
+            if self.buffer is None or self.buffer.numel() < need or self.buffer.device != torch.empty(0, device=device).device:
                 self.buffer = torch.zeros(max(need, 256), dtype=torch.uint8, device=device)
             self.sizes = sizes
         return self.buffer
@@ -191,18 +200,20 @@ def kv_plan(len_old, len_new, block_table, free_pages, ring_in, ring_out, row_st
             raise ValueError("path: expected [n_req, path_len]")
         path_len = path.shape[1]
     width = block_table.shape[1]
-    a = _Plan(n, width, page, free_pages.numel(), extra, path_len, path_rows, rows,
-              _flat(len_old, i32, n, "len_old", dev),
-              None if delta is None else _flat(delta, i32, n, "delta", dev),
-              None if path is None else _flat(path, i32, n * path_len, "path", dev),
-              _flat(ring_in, i32, 2, "ring_in", dev), _flat(block_table, i32, n * width, "block_table", dev),
-              _flat(free_pages, i32, free_pages.numel(), "free_pages", dev), _flat(len_new, i32, n, "len_new", dev),
-              _flat(ring_out, i32, 2, "ring_out", dev), _flat(row_start, i32, n + 1, "row_start", dev),
-              _flat(slot_map, torch.int64, rows, "slot_map", dev),
-              None if positions is None else _flat(positions, i32, rows, "positions", dev),
-              None if src_rows is None else _flat(src_rows, i32, rows, "src_rows", dev),
-              _flat(status, i32, 1, "status", dev))
-    _call(lib.dt_kv_plan(byref(a), _stream(stream, dev)), "dt_kv_plan")
+    a = _pack_plan(n, width, page, free_pages.numel(), extra, path_len, path_rows, rows,
+                   _flat(len_old, i32, n, "len_old", dev),
+                   0 if delta is None else _flat(delta, i32, n, "delta", dev),
+                   0 if path is None else _flat(path, i32, n * path_len, "path", dev),
+                   _flat(ring_in, i32, 2, "ring_in", dev), _flat(block_table, i32, n * width, "block_table", dev),
+                   _flat(free_pages, i32, free_pages.numel(), "free_pages", dev),
+                   _flat(len_new, i32, n, "len_new", dev), _flat(ring_out, i32, 2, "ring_out", dev),
+                   _flat(row_start, i32, n + 1, "row_start", dev), _flat(slot_map, torch.int64, rows, "slot_map", dev),
+                   0 if positions is None else _flat(positions, i32, rows, "positions", dev),
+                   0 if src_rows is None else _flat(src_rows, i32, rows, "src_rows", dev),
+                   _flat(status, i32, 1, "status", dev))
+    err = lib.dt_kv_plan(a, _stream(stream, dev))
+    if err:
+        raise _refused(err, "dt_kv_plan")
 
 
 def kv_append(cache, k, v, slot_map, *, src_rows=None, status=None, stream=None):
@@ -210,17 +221,19 @@ def kv_append(cache, k, v, slot_map, *, src_rows=None, status=None, stream=None)
     [rows, n_kv, head_dim] or [n_req, rows, n_kv, head_dim], rows and heads may be strided."""
     import torch
     lib = _library()
-    dev, n = cache.device, slot_map.numel()
+    dev, n = cache.index, slot_map.numel()
     lead = tuple(k.shape[:-2])
     kp, kr, kh = _heads(k, lead, cache.n_kv, cache.head_dim, "k", dev)
     vp, vr, vh = _heads(v, lead, cache.n_kv, cache.head_dim, "v", dev)
-    a = _Append(kp, vp, kr, kh, vr, vh, lead[0] if len(lead) == 1 else lead[0] * lead[1], n,
-                _flat(slot_map, torch.int64, n, "slot_map", dev),
-                None if src_rows is None else _flat(src_rows, torch.int32, n, "src_rows", dev),
-                None if status is None else _flat(status, torch.int32, 1, "status", dev))
-    if src_rows is None and n > a.n_src:
-        raise ValueError(f"slot_map: {n} rows, but k has {a.n_src}")
-    _call(lib.dt_kv_append(byref(cache.c), byref(a), _stream(stream, dev)), "dt_kv_append")
+    n_src = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    if src_rows is None and n > n_src:
+        raise ValueError(f"slot_map: {n} rows, but k has {n_src}")
+    a = _pack_append(kp, vp, kr, kh, vr, vh, n_src, n, _flat(slot_map, torch.int64, n, "slot_map", dev),
+                     0 if src_rows is None else _flat(src_rows, torch.int32, n, "src_rows", dev),
+                     0 if status is None else _flat(status, torch.int32, 1, "status", dev))
+    err = lib.dt_kv_append(cache.c, a, _stream(stream, dev))
+    if err:
+        raise _refused(err, "dt_kv_append")
 
 
 def cache_attention(cache, q, block_table, length, *, k_new=None, v_new=None, mask=None, scale=None, out=None,
@@ -232,30 +245,33 @@ def cache_attention(cache, q, block_table, length, *, k_new=None, v_new=None, ma
     [n_req, slots, n_q] fp32 is filled."""
     import torch
     lib = _library()
-    dev = cache.device
+    dev = cache.index
     if q.dim() != 4 or block_table.dim() != 2:
         raise ValueError("q: expected [n_req, slots, n_q, head_dim], block_table: [n_req, max_blocks]")
     n, slots, heads, dim = q.shape
+    width = block_table.shape[1]
     if dim != cache.head_dim:
         raise ValueError(f"q: head_dim {dim}, the cache's is {cache.head_dim}")
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new: give both or neither")
     out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
-    kp = vp = None
-    kr = kh = vr = vh = 0
+    lead = (n, slots)
+    kp = kr = kh = vp = vr = vh = 0
     if k_new is not None:
-        kp, kr, kh = _heads(k_new, (n, slots), cache.n_kv, dim, "k_new", dev)
-        vp, vr, vh = _heads(v_new, (n, slots), cache.n_kv, dim, "v_new", dev)
-    qp, qr, qh = _heads(q, (n, slots), heads, dim, "q", dev)
-    op, orow, oh = _heads(out, (n, slots), heads, dim, "out", dev)
+        kp, kr, kh = _heads(k_new, lead, cache.n_kv, dim, "k_new", dev)
+        vp, vr, vh = _heads(v_new, lead, cache.n_kv, dim, "v_new", dev)
+    qp, qr, qh = _heads(q, lead, heads, dim, "q", dev)
+    op, orow, oh = _heads(out, lead, heads, dim, "out", dev)
     buf = workspace.reserve(n, slots, heads, cache.n_kv, dim, dev)
-    a = _Attend(n, slots, heads, block_table.shape[1], dim ** -0.5 if scale is None else scale, qp, qr, qh, kp, vp, kr,
-                kh, vr, vh, _flat(block_table, torch.int32, n * block_table.shape[1], "block_table", dev),
-                _flat(length, torch.int32, n, "length", dev),
-                None if mask is None else _flat(mask, torch.uint8, n * slots * slots, "mask", dev), op, orow, oh,
-                None if lse is None else _flat(lse, torch.float32, n * slots * heads, "lse", dev), buf.data_ptr(),
-                buf.numel(), None if status is None else _flat(status, torch.int32, 1, "status", dev))
-    _call(lib.dt_cache_attention(byref(cache.c), byref(a), _stream(stream, dev)), "dt_cache_attention")
+    a = _pack_attend(n, slots, heads, width, dim ** -0.5 if scale is None else scale, qp, qr, qh, kp, vp, kr, kh, vr, vh,
+                     _flat(block_table, torch.int32, n * width, "block_table", dev),
+                     _flat(length, torch.int32, n, "length", dev),
+                     0 if mask is None else _flat(mask, torch.uint8, n * slots * slots, "mask", dev), op, orow, oh,
+                     0 if lse is None else _flat(lse, torch.float32, n * slots * heads, "lse", dev), buf.data_ptr(),
+                     buf.numel(), 0 if status is None else _flat(status, torch.int32, 1, "status", dev))
+    err = lib.dt_cache_attention(cache.c, a, _stream(stream, dev))
+    if err:
+        raise _refused(err, "dt_cache_attention")
     return out
 
 
@@ -271,12 +287,16 @@ def prompt_attention(q, k, v, row_start, *, scale=None, out=None, lse=None, stre
     rows, heads, dim = q.shape
     kv = k.shape[1]
     out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
-    qp, qr, qh = _heads(q, (rows,), heads, dim, "q", dev)
-    kp, kr, kh = _heads(k, (rows,), kv, dim, "k", dev)
-    vp, vr, vh = _heads(v, (rows,), kv, dim, "v", dev)
-    op, orow, oh = _heads(out, (rows,), heads, dim, "out", dev)
-    a = _Prompt(row_start.numel() - 1, heads, kv, dim, rows, dim ** -0.5 if scale is None else scale, qp, kp, vp, op,
-                qr, qh, kr, kh, vr, vh, orow, oh, _flat(row_start, torch.int32, row_start.numel(), "row_start", dev),
-                None if lse is None else _flat(lse, torch.float32, rows * heads, "lse", dev))
-    _call(lib.dt_prompt_attention(byref(a), _stream(stream, dev)), "dt_prompt_attention")
+    lead = (rows,)
+    qp, qr, qh = _heads(q, lead, heads, dim, "q", dev)
+    kp, kr, kh = _heads(k, lead, kv, dim, "k", dev)
+    vp, vr, vh = _heads(v, lead, kv, dim, "v", dev)
+    op, orow, oh = _heads(out, lead, heads, dim, "out", dev)
+    n = row_start.numel()
+    a = _pack_prompt(n - 1, heads, kv, dim, rows, dim ** -0.5 if scale is None else scale, qp, kp, vp, op,
+                     qr, qh, kr, kh, vr, vh, orow, oh, _flat(row_start, torch.int32, n, "row_start", dev),
+                     0 if lse is None else _flat(lse, torch.float32, rows * heads, "lse", dev))
+    err = lib.dt_prompt_attention(a, _stream(stream, dev))
+    if err:
+        raise _refused(err, "dt_prompt_attention")
     return out

@@ -10,10 +10,11 @@
 // cores, and about as many cycles of exponentials and their surroundings on the
 // ordinary cores; the two overlap (kv_flash.cuh).  One warp feeds K and V by TMA
 // into a ring of four stages, one thread issues the products, two warpgroups do
-// the softmax of a tile each.  One CTA for each SM walks a fixed list of items
-// (heaviest first, in alternating directions), so that one item's loads and first
-// products run under the last one's softmax and output (a launch of one CTA an
-// item spent half of its time there on prompts of 1k).
+// the softmax of a tile each.  The grid has a CTA for every item, but a running CTA
+// takes over items whose CTA has not started (cluster launch control), so that one
+// item's loads and first products run under the last one's softmax and output, and
+// SMs end together: items differ by their position in the prompt (with a fixed list
+// of items for each SM, the SMs of 48 ragged prompts ended 30 % apart).
 //
 // P is rounded to bf16 (operands of one product have one type, and V is bf16):
 // 2^-8 relative a weight at most, as the rounding of the output itself.
@@ -75,38 +76,70 @@ struct PromptItem {
   int masked0;               // the first key tile that holds a key behind pos0
 };
 
-// The i-th item of this CTA, if there is one left (an item may be empty: n = 0).
-// Sequence q's places stand from start_q / span + q on: at least as many as it
-// needs, and found without a sum.
-DT_DEVINL bool prompt_item(const PromptParams& p, int i, PromptItem& x) {
-  const int n = p.slots * p.n_kv, grid = static_cast<int>(gridDim.x);
-  if (static_cast<int64_t>(i) * grid >= n) return false;
-  const int at = i * grid + ((i & 1) ? grid - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
-  x.n = 0;
-  x.n_tiles[0] = x.n_tiles[1] = 0;
-  if (at >= n) return true;  // (the last round may be short; it is the last)
-  x.kvh = at % p.n_kv;
+constexpr int kItemSlots = 4;
+struct PromptPlace {  // what a slot of the schedule holds
+  int kvh, row0, len, pos0;  // len 0: nothing to do, < 0: no more items
+};
+
+// The place of item `at`, by a whole warp: sequence q's places stand from
+// start_q / span + q on, at least as many as it needs, found without a sum.
+DT_DEVINL PromptPlace prompt_place(const PromptParams& p, int at) {
+  const int lane = threadIdx.x & 31;
+  PromptPlace x = {at % p.n_kv, 0, 0, 0};
+  // heaviest first: late positions
   const int slot = p.slots - 1 - at / p.n_kv, span = 2 * p.positions;
   const int first = __ldg(p.row_start);
-  int lo = 0, hi = p.n_seq;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((__ldg(p.row_start + mid) - first) / span + mid <= slot) lo = mid; else hi = mid;
+  int lo = 0, n = p.n_seq;  // the last sequence whose first place is not behind `slot` is one of lo .. lo + n - 1
+  while (n > 1) {
+    const int step = (n + 31) / 32, q = lo + lane * step;
+    const bool before = lane * step < n && (__ldg(p.row_start + q) - first) / span + q <= slot;
+    const int k = 31 - __clz(__ballot_sync(0xFFFFFFFFu, before) | 1u);
+    n = min(step, n - k * step);
+    lo += k * step;
   }
   const int a = __ldg(p.row_start + lo), b = __ldg(p.row_start + lo + 1);
   const int block = slot - ((a - first) / span + lo);
-  if (a < 0 || b < a || b > p.n_rows || block < 0 || block > (b - a) / span || block * span >= b - a) return true;
+  if (a < 0 || b < a || b > p.n_rows || block < 0 || block > (b - a) / span || block * span >= b - a) return x;
   x.row0 = a;
   x.len = b - a;
   x.pos0 = block * span;
+  return x;
+}
+
+DT_DEVINL void prompt_item(const PromptParams& p, const PromptPlace& x, PromptItem& it) {
+  it.kvh = x.kvh;
+  it.row0 = x.row0;
+  it.len = x.len;
+  it.pos0 = x.pos0;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int from = x.pos0 + t * p.positions;
-    x.n_tiles[t] = from < x.len ? (min(x.len, from + p.positions) + kKeyTile - 1) / kKeyTile : 0;
+    it.n_tiles[t] = from < x.len ? (min(x.len, from + p.positions) + kKeyTile - 1) / kKeyTile : 0;
   }
-  x.n = max(x.n_tiles[0], x.n_tiles[1]);
-  x.masked0 = (x.pos0 + 1) / kKeyTile;
-  return true;
+  it.n = max(it.n_tiles[0], it.n_tiles[1]);
+  it.masked0 = (x.pos0 + 1) / kKeyTile;
+}
+
+// Asks for a CTA of this grid that has not started; the answer (16 bytes) completes on `bar`.
+DT_DEVINL void take_next(void* answer, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The CTA that was taken over, or -1.
+DT_DEVINL int taken(const void* answer) {
+  const volatile uint64_t* w = reinterpret_cast<const volatile uint64_t*>(answer);
+  const uint64_t lo = w[0], hi = w[1];
+  int ok, id;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tmov.b128 h, {%2, %3};\n\tmov.b32 %1, 0;\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.b32 %0, 1, 0, p;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(id)
+      : "l"(lo), "l"(hi));
+  return ok ? id : -1;
 }
 
 template <int HD>
@@ -126,7 +159,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint64_t* clean = o_full + 2;            // [kMaskedTiles] a masked tile's values are clean
   uint64_t* dirty = clean + kMaskedTiles;  // [kMaskedTiles] its values are there to be cleaned
   uint64_t* told = dirty + kMaskedTiles;   // the softmax has read bad_key, which may be cleared
-  uint32_t* bad_key = reinterpret_cast<uint32_t*>(told + 1);  // [kMaskedTiles][4] keys of the masked tiles whose values are not finite
+  uint64_t* item_full = told + 1;                // [kItemSlots] the schedule
+  uint64_t* item_free = item_full + kItemSlots;  // [kItemSlots]
+  uint64_t* answered = item_free + kItemSlots;
+  PromptPlace* places = reinterpret_cast<PromptPlace*>(answered + 1);         // [kItemSlots]
+  uint8_t* answer = reinterpret_cast<uint8_t*>(places + kItemSlots);          // 16 bytes
+  uint32_t* bad_key = reinterpret_cast<uint32_t*>(answer + 16);  // [kMaskedTiles][4] keys of the masked tiles whose values are not finite
   __shared__ uint32_t tmem_slot;
 
   // (the same for a warp's lanes, and known to be)
@@ -150,6 +188,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&dirty[i], 1);
     }
     mbar_init(told, 8);
+    for (int i = 0; i < kItemSlots; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_free[i], kPromptThreads / 32 - 1);  // every warp but the scheduling one
+    }
+    mbar_init(answered, 1);
     for (int i = 0; i < 4 * kMaskedTiles; ++i) bad_key[i] = 0;
     fence_mbar_init();
   }
@@ -159,14 +202,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const uint32_t tmem = tmem_slot;
   const uint32_t q_s = smem_u32(smem + Smem::kQ), ring = smem_u32(smem + Smem::kRing);
   PromptItem it;
+  // the i-th item of this CTA into `it`; false: there is none (or a wait gave up)
+  auto next_item = [&](int i) {
+    bool got = __all_sync(0xFFFFFFFFu, mbar_wait(&item_full[i % kItemSlots], (i / kItemSlots) & 1, nullptr));
+    PromptPlace x = {0, 0, -1, 0};
+    if (got) x = places[i % kItemSlots];
+    __syncwarp();
+    if (got && lane == 0) mbar_arrive(&item_free[i % kItemSlots]);
+    prompt_item(p, x, it);
+    return x.len >= 0;
+  };
 
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kLoadWarp && lane == 0) {
+    if (warp == kLoadWarp) {
       uint32_t stage = 0, phase = 0;
       int q_use[2] = {0, 0};
       bool ok = true;
-      for (int i = 0; ok && prompt_item(p, i, it); ++i) {
+      for (int i = 0; ok && next_item(i); ++i) {
+        if (lane == 0) {
         auto load_q = [&](auto which) {
           constexpr int t = decltype(which)::value;
           if (it.n_tiles[t] == 0) return;
@@ -189,6 +243,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (++stage == kStages) stage = 0, phase ^= 1u;
           if (x == 0) load_q(std::integral_constant<int, 1>{});
         }
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       }
     } else if (warp == kMmaWarp) {
       const bool leader = elect_one();
@@ -206,7 +262,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (leader) tc_commit(bar);
       };
       const uint64_t q_desc[2] = {flash_desc(q_s, false), flash_desc(q_s + Smem::kOperand, false)};
-      for (int i = 0; ok && prompt_item(p, i, it); ++i) {
+      for (int i = 0; ok && next_item(i); ++i) {
         if (it.n == 0) continue;
         full_wait(load);
         uint64_t kd = flash_desc(at(load), false);
@@ -263,8 +319,43 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       int items = 0, load = 0;
       uint32_t turns = 0;  // bit m: the parity of dirty[m]'s next phase
       bool ok = true;
-      for (int i = 0; ok && prompt_item(p, i, it); ++i) {
-        if (it.n == 0) continue;
+      // (the last warp also keeps the schedule, an item ahead)
+      const bool plans = cw == kCleanWarps - 1;
+      PromptPlace here = {0, 0, -1, 0}, ahead = here;
+      auto publish = [&](int i, const PromptPlace& x) {
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&item_free[i % kItemSlots], ((i / kItemSlots) & 1) ^ 1, nullptr));
+        if (lane == 0) {
+          places[i % kItemSlots] = x;
+          mbar_arrive(&item_full[i % kItemSlots]);
+        }
+        __syncwarp();
+      };
+      if (plans) {
+        here = prompt_place(p, static_cast<int>(blockIdx.x));
+        publish(0, here);
+      }
+      for (int i = 0; ok; ++i) {
+        if (plans) {
+          if (lane == 0) {
+            fence_proxy_async_smem();  // (the last answer has been read)
+            take_next(answer, answered);
+          }
+          __syncwarp();
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(answered, i & 1, nullptr));
+          const int id = ok ? taken(answer) : -1;
+          __syncwarp();
+          ahead.len = -1;
+          if (id >= 0) ahead = prompt_place(p, id);
+          publish(i + 1, ahead);
+          prompt_item(p, here, it);
+          here = ahead;
+        } else if (!next_item(i)) {
+          break;
+        }
+        if (it.n == 0) {
+          if (plans && here.len < 0) break;
+          continue;
+        }
         if (items++ > 0) {  // the words of the last item have been read
           ok = mbar_wait(told, (items & 1), nullptr);
           if (lane < 2 * kMaskedTiles) bad_key[(lane >> 1) * 4 + cw * 2 + (lane & 1)] = 0;
@@ -305,6 +396,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (lane == 0) mbar_arrive(&clean[m]);
         }
         load += 2 * it.n;
+        if (plans && here.len < 0) break;
       }
     }
   } else {
@@ -320,7 +412,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     auto ready = [&](int half) {
       if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
     };
-    for (int i = 0; ok && prompt_item(p, i, it); ++i) {
+    for (int i = 0; ok && next_item(i); ++i) {
       if (it.n == 0) continue;
       const int n = t == 0 ? it.n_tiles[0] : it.n_tiles[1];
       const int from = it.pos0 + t * p.positions, pos = from + r / p.group, head = it.kvh * p.group + r % p.group;
@@ -395,7 +487,7 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
   cudaError_t e = cudaFuncSetAttribute(k_prompt<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem<HD>::kBytes);
   if (e != cudaSuccess) return e;
   const int items = p.slots * p.n_kv;
-  k_prompt<HD><<<items < kSms ? items : kSms, kPromptThreads, PromptSmem<HD>::kBytes, st>>>(q, k, v, p);
+  k_prompt<HD><<<items, kPromptThreads, PromptSmem<HD>::kBytes, st>>>(q, k, v, p);
   return cudaGetLastError();
 }
 

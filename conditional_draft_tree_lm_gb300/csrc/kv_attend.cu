@@ -66,7 +66,7 @@ extern "C" dt_status dt_cache_attention(const dt_kv_cache* cache, const dt_cache
   p.shift = 4;
   while ((1 << p.shift) < cache->page) ++p.shift;
   p.per_tile = 128 / group;
-  p.inverse = (65536u + group - 1) / group;
+  p.inverse = group_inverse(group);
   const int row_tiles = (a.slots + p.per_tile - 1) / p.per_tile;
   p.pairs = row_tiles / 2;
   p.odd = row_tiles % 2;

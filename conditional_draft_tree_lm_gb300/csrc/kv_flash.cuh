@@ -198,6 +198,10 @@ DT_DEVINL void store_rows(uint8_t* mine, const uint4 (&w)[8], RowOf row_of) {
   }
 }
 
+// y / group for y < 128, group <= 128: y * inverse >> 16 with inverse = ceil(2^16 / group).
+inline uint32_t group_inverse(int group) { return (65536u + group - 1) / group; }
+DT_DEVINL int over_group(int y, uint32_t inverse) { return static_cast<int>(static_cast<uint32_t>(y) * inverse >> 16); }
+
 // The running softmax of one row.
 struct SoftmaxRow {
   float m = -INFINITY, l = 0.0f;  // the maximum in use, in powers of two, and the sum in its unit
@@ -281,8 +285,8 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
       tmem_landed32(v);
       if (w1 == 0 || w2 == 0) tmem_ld32(s_at + 32 * (w + 1), part(w1 + 1));
     }
-    // (of a masked tile, most 32-key parts are seen by all of a warp's rows or by none)
     const uint32_t bits = w1 == 0 ? (w2 == 0 ? see[0] : see[2]) : (w2 == 0 ? see[1] : see[3]);
+    // (of a masked tile, most 32-key parts are seen by all of a warp's rows or by none)
     const bool none = MASKED && __all_sync(0xFFFFFFFFu, bits == 0u);
     const bool all = !MASKED || __all_sync(0xFFFFFFFFu, bits == 0xFFFFFFFFu);
     if (none) {

@@ -52,6 +52,7 @@ struct PromptParams {
   int64_t n_rows, out_row_stride, out_head_stride;
   int n_seq, n_q, n_kv, group, positions;  // positions: of a tile (128 / group)
   int slots;                               // items per key/value head
+  uint32_t inverse;                        // group_inverse(group)
   float c;                                 // scale * log2(e)
 };
 
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     for (int i = 0; ok && next_item(i); ++i) {
       if (it.n == 0) continue;
       const int n = t == 0 ? it.n_tiles[0] : it.n_tiles[1];
-      const int from = it.pos0 + t * p.positions, pos = from + r / p.group, head = it.kvh * p.group + r % p.group;
+      const int from = it.pos0 + t * p.positions, pos = from + over_group(r, p.inverse);
       SoftmaxRow row;
       for (int j = 0; j < n && ok; ++j) {
         ok = mbar_wait(&s_full[t], s_use++ & 1, nullptr);
@@ -442,11 +443,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (n > 0 && ok) {
         const bool live = r < p.group * p.positions && pos < it.len;
         const float inv = row.l == 0.0f ? 0.0f : 1.0f / row.l;
-        auto row_of = [&](int x) -> __nv_bfloat16* {  // the row of the warp's lane x
-          const int y = (warp & 3) * 32 + x, at = from + y / p.group;
-          if (y >= p.group * p.positions || at >= it.len) return nullptr;
-          return p.out + static_cast<int64_t>(it.row0 + at) * p.out_row_stride + (it.kvh * p.group + y % p.group) * p.out_head_stride;
-        };
 #pragma unroll
         for (int x = 0; x < HD; x += 64) {
           uint32_t v[64];
@@ -463,14 +459,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             w[k].z = pack_p<true>(__uint_as_float(v[8 * k + 4]) * inv, __uint_as_float(v[8 * k + 5]) * inv);
             w[k].w = pack_p<true>(__uint_as_float(v[8 * k + 6]) * inv, __uint_as_float(v[8 * k + 7]) * inv);
           }
-          store_rows(smem + Smem::kOut + warp * 4096, w, [&](int y) {
-            __nv_bfloat16* to = row_of(y);
-            return to ? to + x : nullptr;
+          store_rows(smem + Smem::kOut + warp * 4096, w, [&](int z) -> __nv_bfloat16* {
+            const int y = (warp & 3) * 32 + z, ys = over_group(y, p.inverse), at = from + ys;
+            return y < p.group * p.positions && at < it.len
+                       ? p.out + static_cast<int64_t>(it.row0 + at) * p.out_row_stride +
+                             (it.kvh * p.group + y - ys * p.group) * p.out_head_stride + x
+                       : nullptr;
           });
         }
         tc_fence_before();  // (O has been read before the next item's first product writes it)
         if (live && p.lse)
-          p.lse[static_cast<int64_t>(it.row0 + pos) * p.n_q + head] = row.l == 0.0f ? -INFINITY : (row.m + log2f(row.l)) * kLn2;
+          p.lse[static_cast<int64_t>(it.row0 + pos) * p.n_q + it.kvh * p.group + r - (pos - from) * p.group] = row.l == 0.0f ? -INFINITY : (row.m + log2f(row.l)) * kLn2;
       }
     }
   }
@@ -523,6 +522,7 @@ extern "C" dt_status dt_prompt_attention(const dt_prompt_attention_args* args, v
   p.n_kv = a.n_kv;
   p.group = a.n_q / a.n_kv;
   p.positions = 128 / p.group;
+  p.inverse = group_inverse(p.group);
   const int64_t slots = a.n_rows / (2 * p.positions) + a.n_seq;
   if (slots * a.n_kv > 0x7FFFFFFF) return kv_fail(DT_ERR_SHAPE, "%s: too many rows and heads for one launch", who);
   p.slots = static_cast<int>(slots);

@@ -44,7 +44,7 @@ struct TreeParams {
   dt_cache_attention_args a;
   int group, shift;
   int per_tile;     // slots of a row tile
-  uint32_t inverse; // ceil(2^16 / group): y / group = y * inverse >> 16 for y < 128
+  uint32_t inverse; // group_inverse(group)
   int pairs, odd;   // pairs of row tiles, and whether one is left
   int fresh_tiles;  // key tiles of new tokens
   unsigned* done;   // [n_req * n_kv * (pairs + odd)] zero between launches
@@ -168,7 +168,7 @@ struct TreeTile {
   float vref;         // the unit of values, and so of O, from this tile on
 };
 
-DT_DEVINL int by_group(const TreeParams& p, int y) { return static_cast<int>(static_cast<uint32_t>(y) * p.inverse >> 16); }
+DT_DEVINL int by_group(const TreeParams& p, int y) { return over_group(y, p.inverse); }
 
 template <int HD>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
@@ -667,11 +667,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         // --- the end of a stretch: the answer, or a part of it
         const int c_first = cut.of(sg.first), c_last = cut.of(sg.first + sg.units - 1);
         const bool alone = c_first == c_last && !split;
-        auto out_of = [&](int y) -> __nv_bfloat16* {  // row y of the tile
-          const int ys = by_group(p, y), sl = tile * p.per_tile + ys;
-          if (y >= p.per_tile * p.group || sl >= a.slots) return nullptr;
-          return static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(sg.req) * a.slots + sl) * a.out_row_stride +
-                 (sg.kvh * p.group + y - ys * p.group) * a.out_head_stride;
+        auto out_of = [&](int z, int x) -> __nv_bfloat16* {  // row z of the warp, channel x
+          const int y = (warp & 3) * 32 + z, ys = by_group(p, y), sl = tile * p.per_tile + ys;
+          return y < p.per_tile * p.group && sl < a.slots
+                     ? static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(sg.req) * a.slots + sl) * a.out_row_stride +
+                           (sg.kvh * p.group + y - ys * p.group) * a.out_head_stride + x
+                     : nullptr;
         };
         auto finish_lse = [&](float top, float sum) {
           if (live && a.lse) a.lse[row * a.n_q + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
@@ -700,10 +701,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
                 w[k].w = pack_p<true>(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7]));
               }
               // (through the row tile's own Q, which the next segment's replaces after this)
-              store_rows(smem + Smem::kQ + t * Smem::kOperand + (warp & 3) * 4096, w, [&](int y) -> __nv_bfloat16* {
-                __nv_bfloat16* to = out_of((warp & 3) * 32 + y);
-                return to ? to + x : nullptr;
-              });
+              store_rows(smem + Smem::kQ + t * Smem::kOperand + (warp & 3) * 4096, w, [&](int z) { return out_of(z, x); });
             } else {
 #pragma unroll
               for (int i = 0; i < 64; i += 4)
@@ -760,10 +758,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
                 w[k] = make_uint4(pack_p<true>(o[2 * k].x * inv, o[2 * k].y * inv), pack_p<true>(o[2 * k].z * inv, o[2 * k].w * inv),
                                   pack_p<true>(o[2 * k + 1].x * inv, o[2 * k + 1].y * inv),
                                   pack_p<true>(o[2 * k + 1].z * inv, o[2 * k + 1].w * inv));
-              store_rows(smem + Smem::kQ + t * Smem::kOperand + (warp & 3) * 4096, w, [&](int y) -> __nv_bfloat16* {
-                __nv_bfloat16* to = out_of((warp & 3) * 32 + y);
-                return to ? to + x : nullptr;
-              });
+              store_rows(smem + Smem::kQ + t * Smem::kOperand + (warp & 3) * 4096, w, [&](int z) { return out_of(z, x); });
             }
             finish_lse(top, sum);
           }

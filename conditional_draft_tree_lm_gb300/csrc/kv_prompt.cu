@@ -40,10 +40,6 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
 // Tiles of which some row does not see all: keys behind the first of an item's (at most 256) positions
 // lie in three at most, so each has barriers and a word of its own.
 constexpr int kMaskedTiles = 3;
-#ifndef DT_HOLD
-#define DT_HOLD true
-#endif
-constexpr bool kHold = DT_HOLD;
 
 struct PromptParams {
   __nv_bfloat16* out;
@@ -159,11 +155,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint64_t* o_full = p_full + 4;           // [2]
   uint64_t* clean = o_full + 2;            // [kMaskedTiles] a masked tile's values are clean
   uint64_t* dirty = clean + kMaskedTiles;  // [kMaskedTiles] its values are there to be cleaned
-  uint64_t* told = dirty + kMaskedTiles;   // the softmax has read bad_key, which may be cleared
-  uint64_t* item_full = told + 1;                // [kItemSlots] the schedule
+  uint64_t* told = dirty + kMaskedTiles;   // [2] row tile t's softmax has read bad_key
+  uint64_t* item_full = told + 2;                // [kItemSlots] the schedule
   uint64_t* item_free = item_full + kItemSlots;  // [kItemSlots]
   uint64_t* answered = item_free + kItemSlots;
-  PromptPlace* places = reinterpret_cast<PromptPlace*>(answered + 1);         // [kItemSlots]
+  PromptPlace* places = reinterpret_cast<PromptPlace*>(answered + 2);         // [kItemSlots]; 16-byte aligned, as the answer is
   uint8_t* answer = reinterpret_cast<uint8_t*>(places + kItemSlots);          // 16 bytes
   uint32_t* bad_key = reinterpret_cast<uint32_t*>(answer + 16);  // [kMaskedTiles][4] keys of the masked tiles whose values are not finite
   __shared__ uint32_t tmem_slot;
@@ -188,7 +184,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&clean[i], kCleanWarps);
       mbar_init(&dirty[i], 1);
     }
-    mbar_init(told, 8);
+    for (int t = 0; t < 2; ++t) mbar_init(&told[t], 4);
     for (int i = 0; i < kItemSlots; ++i) {
       mbar_init(&item_full[i], 1);
       mbar_init(&item_free[i], kPromptThreads / 32 - 1);  // every warp but the scheduling one
@@ -317,7 +313,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     } else if (warp >= kCleanWarp) {
       // values of the masked tiles: half of the keys a warp, a key's 16-byte pieces to eight lanes
       const int cw = warp - kCleanWarp;
-      int items = 0, load = 0;
+      int load = 0, was_active[2] = {0, 0}, told_use[2] = {0, 0};  // was_active: row tiles of the last item
       uint32_t turns = 0;  // bit m: the parity of dirty[m]'s next phase
       bool ok = true;
       // (the last warp also keeps the schedule, an item ahead)
@@ -357,11 +353,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (plans && here.len < 0) break;
           continue;
         }
-        if (items++ > 0) {  // the words of the last item have been read
-          ok = mbar_wait(told, (items & 1), nullptr);
-          if (lane < 2 * kMaskedTiles) bad_key[(lane >> 1) * 4 + cw * 2 + (lane & 1)] = 0;
-          __syncwarp();
+        // the words of the last item have been read (by the row tiles that it had: another's softmax may be items ahead)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (was_active[t]) ok = ok && mbar_wait(&told[t], told_use[t]++ & 1, nullptr);
+          was_active[t] = it.n_tiles[t] > 0;
         }
+        if (lane < 2 * kMaskedTiles) bad_key[(lane >> 1) * 4 + cw * 2 + (lane & 1)] = 0;
+        __syncwarp();
         for (int j = it.masked0; j < it.n && ok; ++j) {
           const int m = j - it.masked0;
           ok = mbar_wait(&dirty[m], turns >> m & 1u, nullptr);
@@ -425,9 +424,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int seen = pos + 1 - j * kKeyTile;  // of this tile's keys, by this row
         const uint32_t see[4] = {first_bits(seen, 0), first_bits(seen, 1), first_bits(seen, 2), first_bits(seen, 3)};
         if ((j + 1) * kKeyTile > from + 1)
-          softmax_tile<HD, true, true, true, kHold>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
+          softmax_tile<HD, true, true, true, false>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
         else
-          softmax_tile<HD, true, true, false, kHold>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
+          softmax_tile<HD, true, true, false, true>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
       }
       if (n > 0) {
         ok = ok && mbar_wait(&o_full[t], o_use++ & 1, nullptr);
@@ -439,7 +438,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (bad_key[(j - it.masked0) * 4 + w] & first_bits(pos + 1 - j * kKeyTile, w)) row.l = NAN;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(told);
+      if (lane == 0 && n > 0) mbar_arrive(&told[t]);
       if (n > 0 && ok) {
         const bool live = r < p.group * p.positions && pos < it.len;
         const float inv = row.l == 0.0f ? 0.0f : 1.0f / row.l;

@@ -266,11 +266,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
       auto release = [&](int i) {
         if (ok) commit(&empty[i % kTreeStages]);
       };
-      for (int seg = 0; ok && walk.next(p, sg); ++seg) {
+      for (int seg = 0; ok && walk.next(p, sg);) {
         const int n = sg.key_end - sg.key_begin;
+        if (n == 0) continue;
         wait(&q_full[0], seg & 1);
         wait(&q_full[1], seg & 1);
-        if (n == 0) continue;
+        ++seg;
         full_wait(2 * count);
         qk(0, 2 * count);
         if (sg.tiles == 2) {
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         {
           // Q to fp16 by a power of two of the row's own: HD / 8 lanes read a row together
           float c = 0.0f;
-          {
+          if (n > 0) {
             constexpr int kL = HD / 8, kR = 32 / kL, kN = 32 / kR;  // lanes of a row, rows at a time, times
             uint8_t* op = smem + Smem::kQ + t * Smem::kOperand;
             const int cx = lane % kL, rx = lane / kL;

@@ -623,6 +623,29 @@ def test_prompt_attention_nan_stays_where_it_is_seen():
         assert not np.isfinite(out[r, :, 3]).any(), r
 
 
+def test_prompt_attention_many_short_sequences_again_and_again():
+    """Most items have one row tile of two, so that the two softmax groups of a CTA are often items apart; the same
+    bits in every pass, and no wait that gives up (it would leave rows unwritten)."""
+    torch = _t()
+    from conditional_draft_tree_lm_gb300 import prompt_attention
+    rs = np.random.RandomState(35)
+    lens = np.concatenate([rs.randint(1, 33, 3000), [700, 290, 0, 65]])
+    rs.shuffle(lens)
+    n = int(lens.sum())
+    q, k, v = (dev(rs.randn(n, x, 128), torch.bfloat16) for x in (8, 2, 2))
+    start = dev(np.concatenate([[0], np.cumsum(lens)]), torch.int32)
+    first = run_prompt(q, k, v, lens)
+    some = np.concatenate([[0], np.cumsum(lens)])
+    for i in list(range(0, 3004, 301)) + [int(np.argmax(lens))]:
+        part = (first[0][some[i]:some[i + 1]], first[1][some[i]:some[i + 1]])
+        check_prompt(q[some[i]:some[i + 1]], k[some[i]:some[i + 1]], v[some[i]:some[i + 1]], [int(lens[i])], part)
+    want = torch.from_numpy(first[0]).cuda()
+    for _ in range(100):
+        out = torch.full((n, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        prompt_attention(q, k, v, start, out=out)
+        assert torch.equal(out.float(), want)
+
+
 def test_prompt_attention_large_logits():
     """Maxima that rise along the keys, so that the running sums are rescaled again and again, and logits in the hundreds."""
     torch = _t()

@@ -35,6 +35,28 @@ DT_DEVINL void e4m3x4_to_f16x2x2(uint32_t four, uint32_t& lo, uint32_t& hi) {
       : "r"(four));
 }
 
+// Asks for a CTA of this grid that has not started; the answer (16 bytes) completes on `bar`.
+DT_DEVINL void take_next(void* answer, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The CTA that was taken over, or -1.
+DT_DEVINL int taken(const void* answer) {
+  const volatile uint64_t* w = reinterpret_cast<const volatile uint64_t*>(answer);
+  const uint64_t lo = w[0], hi = w[1];
+  int ok, id;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tmov.b128 h, {%2, %3};\n\tmov.b32 %1, 0;\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.b32 %0, 1, 0, p;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(id)
+      : "l"(lo), "l"(hi));
+  return ok ? id : -1;
+}
+
 inline dt_status kv_fail(dt_status s, const char* fmt, ...) {
   char msg[240];
   va_list ap;

@@ -44,6 +44,7 @@ constexpr int kMaskedTiles = 3;
 struct PromptParams {
   __nv_bfloat16* out;
   float* lse;
+  int32_t* status;
   const int32_t* row_start;
   int64_t n_rows, out_row_stride, out_head_stride;
   int n_seq, n_q, n_kv, group, positions;  // positions: of a tile (128 / group)
@@ -117,28 +118,6 @@ DT_DEVINL void prompt_item(const PromptParams& p, const PromptPlace& x, PromptIt
   it.masked0 = (x.pos0 + 1) / kKeyTile;
 }
 
-// Asks for a CTA of this grid that has not started; the answer (16 bytes) completes on `bar`.
-DT_DEVINL void take_next(void* answer, uint64_t* bar) {
-  mbar_arrive_expect_tx(bar, 16);
-  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                   smem_u32(answer)),
-               "r"(smem_u32(bar))
-               : "memory");
-}
-// The CTA that was taken over, or -1.
-DT_DEVINL int taken(const void* answer) {
-  const volatile uint64_t* w = reinterpret_cast<const volatile uint64_t*>(answer);
-  const uint64_t lo = w[0], hi = w[1];
-  int ok, id;
-  asm volatile(
-      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tmov.b128 h, {%2, %3};\n\tmov.b32 %1, 0;\n\t"
-      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.b32 %0, 1, 0, p;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
-      : "=r"(ok), "=r"(id)
-      : "l"(lo), "l"(hi));
-  return ok ? id : -1;
-}
-
 template <int HD>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     k_prompt(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -199,9 +178,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const uint32_t tmem = tmem_slot;
   const uint32_t q_s = smem_u32(smem + Smem::kQ), ring = smem_u32(smem + Smem::kRing);
   PromptItem it;
+  bool gave_up = false;  // a bounded wait did
   // the i-th item of this CTA into `it`; false: there is none (or a wait gave up)
   auto next_item = [&](int i) {
     bool got = __all_sync(0xFFFFFFFFu, mbar_wait(&item_full[i % kItemSlots], (i / kItemSlots) & 1, nullptr));
+    gave_up |= !got;
     PromptPlace x = {0, 0, -1, 0};
     if (got) x = places[i % kItemSlots];
     __syncwarp();
@@ -242,6 +223,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         }
         ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      }
+      gave_up |= !ok;
+      if (!ok && lane == 0) {  // (no copy may outlive the CTA)
+        for (int s = 0; s < kStages; ++s) mbar_wait(&full[s], (s < static_cast<int>(stage) ? phase : phase ^ 1u), nullptr);
+        for (int t = 0; t < 2; ++t)
+          if (q_use[t] > 0) mbar_wait(&q_full[t], (q_use[t] - 1) & 1, nullptr);
       }
     } else if (warp == kMmaWarp) {
       const bool leader = elect_one();
@@ -310,6 +297,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         load += 2 * it.n;
       }
+      gave_up |= !ok;
     } else if (warp >= kCleanWarp) {
       // values of the masked tiles: half of the keys a warp, a key's 16-byte pieces to eight lanes
       const int cw = warp - kCleanWarp;
@@ -398,6 +386,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         load += 2 * it.n;
         if (plans && here.len < 0) break;
       }
+      gave_up |= !ok;
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -471,7 +460,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           p.lse[static_cast<int64_t>(it.row0 + pos) * p.n_q + it.kvh * p.group + r - (pos - from) * p.group] = row.l == 0.0f ? -INFINITY : (row.m + log2f(row.l)) * kLn2;
       }
     }
+    gave_up |= !ok;
   }
+  if (gave_up && p.status) atomicOr(p.status, DT_KV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -512,6 +503,7 @@ extern "C" dt_status dt_prompt_attention(const dt_prompt_attention_args* args, v
   PromptParams p = {};
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
+  p.status = a.status;
   p.row_start = a.row_start;
   p.n_rows = a.n_rows;
   p.out_row_stride = a.out_row_stride;

@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
     TreeSegment sg = {};
     const uint32_t q_s = smem_u32(smem + Smem::kQ), ring = smem_u32(smem + Smem::kRing);
 
+    bool gave_up = false;  // a bounded wait did
     if (warp == kTreeMmaWarp) {
       const bool leader = elect_one();
       int count = 0;  // key tiles so far
@@ -312,6 +313,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
           count += n;
         }
       }
+      gave_up = !ok;
     } else if (warp == kTreeFetchWarp) {
       // --- pages to the staging place, a tile ahead of their conversion; page numbers and scales another tile ahead
       struct Page {  // of 16 keys, held by lanes 0..7
@@ -340,6 +342,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
       tw.next(p, cur);
       Page gc = pages_of(cur);
       bool ok = true;
+      int fetched[2] = {0, 0};
       for (int count = 0; cur.kind != kTileNone && ok; ++count) {
         tw.next(p, nxt);
         const Page gn = pages_of(nxt);
@@ -367,6 +370,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             __syncwarp();
           }
           if (lane == 0) mbar_arrive_expect_tx(&st_full[which], bytes);
+          ++fetched[which];
           __syncwarp();
           if (copies)
             bulk_load(smem_u32(smem + Smem::kStaging) + which * kKeyTile * HD + lane * 16 * HD,
@@ -375,6 +379,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         cur = nxt;
         gc = gn;
       }
+      // (where a wait gave up: no copy may outlive the CTA)
+      if (!ok)
+        for (int which = 0; which < 2; ++which)
+          if (fetched[which] > 0) mbar_wait(&st_full[which], (fetched[which] - 1) & 1, nullptr);
+      gave_up = !ok;
     } else if (warp >= kTreeConvWarp) {
       // --- conversion
       constexpr int kLanes = HD / 16;               // threads of a key's row (16 bytes each)
@@ -547,6 +556,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
           convert_new(cur, info, count, vref);
         }
       }
+      gave_up = !ok;
     } else {
       // --- softmax: warpgroup t, a row a thread
       const int t = warp >> 2, r = tid & 127;
@@ -766,7 +776,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
           asm volatile("bar.sync 1, 256;" ::: "memory");  // (s_last has been read)
         }
       }
+      gave_up = !ok;
     }
+    if (gave_up && a.status) atomicOr(a.status, DT_KV_TIMEOUT);
   }
   tc_fence_before();
   __syncthreads();

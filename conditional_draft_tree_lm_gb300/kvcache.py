@@ -26,6 +26,7 @@ KV_BAD_LENGTH = 2
 KV_SHORT_OF_ROWS = 4
 KV_BAD_PATH = 8
 KV_BAD_INDEX = 16
+KV_TIMEOUT = 32
 
 
 class _Cache(ctypes.Structure):
@@ -61,7 +62,8 @@ class _Prompt(ctypes.Structure):
                 ("scale", c_float), ("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("out", c_void_p),
                 ("q_row_stride", c_int64), ("q_head_stride", c_int64), ("k_row_stride", c_int64),
                 ("k_head_stride", c_int64), ("v_row_stride", c_int64), ("v_head_stride", c_int64),
-                ("out_row_stride", c_int64), ("out_head_stride", c_int64), ("row_start", c_void_p), ("lse", c_void_p)]
+                ("out_row_stride", c_int64), ("out_head_stride", c_int64), ("row_start", c_void_p), ("lse", c_void_p),
+                ("status", c_void_p)]
 
 
 def _packer(cls):
@@ -275,7 +277,7 @@ def cache_attention(cache, q, block_table, length, *, k_new=None, v_new=None, ma
     return out
 
 
-def prompt_attention(q, k, v, row_start, *, scale=None, out=None, lse=None, stream=None):
+def prompt_attention(q, k, v, row_start, *, scale=None, out=None, lse=None, status=None, stream=None):
     """Causal attention over packed prompts (``dt_prompt_attention``).  q [rows, n_q, head_dim], k, v
     [rows, n_kv, head_dim] bf16, rows and heads may be strided (slices of one projection's output);
     row_start [n_seq + 1] int32.  Returns out [rows, n_q, head_dim]; lse [rows, n_q] fp32 is filled if given."""
@@ -295,7 +297,8 @@ def prompt_attention(q, k, v, row_start, *, scale=None, out=None, lse=None, stre
     n = row_start.numel()
     a = _pack_prompt(n - 1, heads, kv, dim, rows, dim ** -0.5 if scale is None else scale, qp, kp, vp, op,
                      qr, qh, kr, kh, vr, vh, orow, oh, _flat(row_start, torch.int32, n, "row_start", dev),
-                     0 if lse is None else _flat(lse, torch.float32, rows * heads, "lse", dev))
+                     0 if lse is None else _flat(lse, torch.float32, rows * heads, "lse", dev),
+                     0 if status is None else _flat(status, torch.int32, 1, "status", dev))
     err = lib.dt_prompt_attention(a, _stream(stream, dev))
     if err:
         raise _refused(err, "dt_prompt_attention")

@@ -408,6 +408,7 @@ typedef struct dt_kv_cache {
 #define DT_KV_BAD_PATH 8       /* a path shorter than the new tokens, or a slot out of range */
 #define DT_KV_BAD_INDEX 16     /* a page, slot or source row out of range (skipped), or more pages
                                 * given back than can be in use */
+#define DT_KV_TIMEOUT 32        /* a bounded wait inside a kernel gave up: outputs are incomplete */
 
 /* Block tables and slot maps from request lengths.  Request q's new length is
  *   len_new[q] = max(len_old[q] + delta[q] + extra, 0)   (delta NULL: all 0)
@@ -493,7 +494,7 @@ dt_status dt_kv_append(const dt_kv_cache* cache, const dt_kv_append_args* args, 
  * workspace: dt_cache_attention_workspace() bytes of device memory, 256-byte
  * aligned, zeroed once by the caller; every call leaves it ready for the next,
  * and calls that share one must not overlap.  status as in dt_kv_append (a page
- * out of range counts as not there). */
+ * out of range counts as not there; DT_KV_TIMEOUT is or'ed in too). */
 typedef struct dt_cache_attention_args {
   int n_req, slots, n_q, max_blocks;
   float scale;             /* finite */
@@ -522,7 +523,8 @@ size_t dt_cache_attention_workspace(int n_req, int slots, int n_q, int n_kv, int
  * row_start[i+1]-1 of q, k, v and out (dt_kv_plan's row_start); a row sees the
  * rows of its own sequence up to itself.  Formulas, lse ([n_rows, n_q] or NULL)
  * and the rule on NaNs as in dt_cache_attention.  row_start must ascend from 0
- * or more to n_rows or less; rows outside are not written. */
+ * or more to n_rows or less; rows outside are not written.  status: [1] int32
+ * device or NULL; DT_KV_TIMEOUT is or'ed in. */
 typedef struct dt_prompt_attention_args {
   int n_seq, n_q, n_kv, head_dim;
   int64_t n_rows;            /* 1..2^31-1 */
@@ -537,6 +539,7 @@ typedef struct dt_prompt_attention_args {
   int64_t out_row_stride, out_head_stride;
   const int32_t* row_start;  /* [n_seq + 1] device */
   float* lse;
+  int32_t* status;
 } dt_prompt_attention_args;
 dt_status dt_prompt_attention(const dt_prompt_attention_args* args, void* stream);
 

@@ -54,9 +54,17 @@ extern "C" dt_status dt_cache_attention(const dt_kv_cache* cache, const dt_cache
     p.done = static_cast<unsigned*>(a.workspace);
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kCounterBytes);
     const int grid = decode_grid(a.n_req, cache->n_kv, static_cast<long long>(a.max_blocks) * cache->page);
+    // key rows of the whole cache: row ((page * n_kv) + head) * page_size + offset
+    const int64_t rows = static_cast<int64_t>(cache->n_pages) * cache->n_kv * cache->page;
+    if (rows > 0x7FFFFFFF) return kv_fail(DT_ERR_SHAPE, "%s: more than 2^31-1 cached tokens and heads", who);
+    p.box = cache->page < 32 ? 16 : 32;
+    CUtensorMap k, v;
+    if (!make_tmap_u8_rows(&k, cache->k, cache->head_dim, rows, p.box) ||
+        !make_tmap_u8_rows(&v, cache->v, cache->head_dim, rows, p.box))
+      return kv_fail(DT_ERR_SHAPE, "%s: no tensor map for this cache", who);
     cudaError_t e;
-    if (cache->head_dim == 64) e = p.rows <= 8 ? launch_decode<64, 1>(p, grid, st) : launch_decode<64, 2>(p, grid, st);
-    else e = p.rows <= 8 ? launch_decode<128, 1>(p, grid, st) : launch_decode<128, 2>(p, grid, st);
+    if (cache->head_dim == 64) e = p.rows <= 8 ? launch_decode<64, 1>(k, v, p, grid, st) : launch_decode<64, 2>(k, v, p, grid, st);
+    else e = p.rows <= 8 ? launch_decode<128, 1>(k, v, p, grid, st) : launch_decode<128, 2>(k, v, p, grid, st);
     return kv_launched(who, e);
   }
   TreeParams p = {};

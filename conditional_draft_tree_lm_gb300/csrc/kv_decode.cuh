@@ -17,9 +17,10 @@
 // one's first steps are put in flight before the last one is joined.
 //
 // A warp takes steps of two times 16 keys (two, so that their chains of products
-// overlap), each thread copying (cp.async) just the bytes that
-// it will itself feed to mma.m16n8k16 into slots of its own in shared memory: a
-// ring of steps in flight without a barrier, and without bank conflicts:
+// overlap) from a ring of its own in shared memory, which one of its lanes keeps
+// filled by TMA (copies by the threads themselves, 16 bytes each, stopped at 4.9
+// TB/s whatever their number in flight; with TMA the same stream runs at 6.5).  The
+// 128-byte swizzle spreads a fragment's rows over the banks:
 //   S^T[key, row] = K (A, 16 keys) Q^T (B, 8 rows): a thread supplies 4 adjacent
 //     channels of keys lane/4 and lane/4 + 8 per product; which channel is which k
 //     is free as long as Q uses the same order, so 16-byte pieces feed four products.
@@ -32,6 +33,8 @@
 // row (exact to 2^-40 of the row's maximum), P is held in fp16: 11 bits, where
 // bf16 would give 8.  Maxima, sums and O are 32 bits.
 #pragma once
+
+#include <cuda.h>
 
 #include "kv.cuh"
 
@@ -52,6 +55,7 @@ struct DecodeParams {
   dt_kv_cache c;
   dt_cache_attention_args a;
   int group, rows, shift;  // rows = slots * group
+  int box;                 // rows of a copy: 32, or a page of 16
   unsigned* done;          // [n_req * n_kv] pieces that are done; zero between launches
   float* part;             // [2 * pieces][rows][HD], then [2 * pieces][rows][2]: a piece's first and last (request, head)
 };
@@ -78,18 +82,6 @@ DT_DEVINL float fast_exp2(float x) {
 DT_DEVINL uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-DT_DEVINL void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-DT_DEVINL void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-DT_DEVINL void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-DT_DEVINL void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Tiles of a request: at least one, so that a request without cached tokens has a place in the work too.
@@ -163,17 +155,25 @@ struct Cut {
   }
 };
 
+// p.box key rows from row `row` of the cache, all of a row's bytes.
+DT_DEVINL void tma_rows(void* dst, const void* tmap, uint64_t* bar, int row) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(0), "r"(row)
+      : "memory");
+}
+
 template <int HD, int RH>
 struct DecodeSmem {
-  // [stage][warp][half][piece][lane]: K of key g (HD/64 pieces of 16 bytes), of key g + 8, V of keys 2t, 2t+1, 2t+8, 2t+9
+  // ring: [stage][warp][K, V][32 keys][HD], rows swizzled in 16-byte pieces; then the join (whose place the sums
+  // of lengths take at first), the ring's barriers
   static constexpr int kStages = RH == 1 ? 3 : 2;  // (two CTAs' rings and joins fill an SM's shared memory)
-  static constexpr int kKPiece = 16 * 32, kVPiece = HD / 8 * 32;
-  static constexpr int kHalf = 2 * (HD / 64) * kKPiece + 4 * kVPiece;  // 16 keys
-  static constexpr int kStep = 2 * kHalf;                              // a warp's step
+  static constexpr int kStep = 2 * 32 * HD;        // a warp's step
   static constexpr int kRing = kStages * kDecodeWarps * kStep;
   static constexpr int kRows = 8 * RH;
   static constexpr int kJoin = kDecodeWarps * kRows * (HD + 2) * 4;
-  static constexpr int kBytes = kRing + kJoin;
+  static constexpr int kBytes = kRing + kJoin + kStages * kDecodeWarps * 8 + 16;
 };
 
 // A stretch of one (request, head) inside a piece.
@@ -184,30 +184,36 @@ struct DecodeSegment {
 };
 
 template <int HD, int RH>  // RH: halves of 8 rows in use, 1 or 2
-__global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas) k_decode(const DecodeParams p) {
+__global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
+    k_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const DecodeParams p) {
   using Smem = DecodeSmem<HD, RH>;
   constexpr int kStages = Smem::kStages;
   constexpr int kKSteps = HD / 16;  // products of 16 channels; also tiles of 16 output channels
   constexpr int kVec = HD / 64;     // 16-byte pieces of a key per thread
   constexpr int kRows = Smem::kRows;
   constexpr int kQuads = HD / 4;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int scratch[kDecodeWarps], s_start[kDecodeThreads + 1], s_last;
+  extern __shared__ __align__(1024) uint8_t smem[];
   float* s_o = reinterpret_cast<float*>(smem + Smem::kRing);  // [warps][kRows][HD]
   float* s_m = s_o + kDecodeWarps * kRows * HD;               // [warps][kRows]
   float* s_l = s_m + kDecodeWarps * kRows;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Smem::kRing + Smem::kJoin);  // [warps][stages]
+  int& s_last = *reinterpret_cast<int*>(bars + kDecodeWarps * kStages);
+  int* s_start = reinterpret_cast<int*>(s_o);  // [threads + 1], then [warps]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const dt_cache_attention_args& a = p.a;
   const int n_kv = p.c.n_kv, max_len = a.max_blocks << p.shift;
   const __nv_bfloat16* q_base = static_cast<const __nv_bfloat16*>(a.q);
-  const uint8_t* kc = static_cast<const uint8_t*>(p.c.k);
-  const uint8_t* vc = static_cast<const uint8_t*>(p.c.v);
   const int page_mask = (1 << p.shift) - 1;
   uint8_t* ring = smem + warp * Smem::kStep;
 
+  if (tid < kDecodeWarps * kStages) mbar_init(&bars[tid], 1);
+  fence_mbar_init();
+  bars += warp * kStages;
+  int issued = 0, used = 0;  // of this warp's steps
+  bool gave_up = false;      // a bounded wait did
   TileRow<kDecodeThreads, DecodeTiles> row_of = {a.length, a.n_req, {max_len}, 0, s_start};
-  row_of.sum(scratch);
+  row_of.sum(s_start + kDecodeThreads + 1);
   const int work = row_of.total() * n_kv;
   const int pieces = min(work, static_cast<int>(gridDim.x));
   if (static_cast<int>(blockIdx.x) >= pieces) return;
@@ -215,6 +221,16 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas) k_decode(const De
   float* stats = p.part + static_cast<size_t>(2 * pieces) * p.rows * HD;
   const int piece = blockIdx.x;
   const int u_end = cut.begin(piece + 1);
+
+  // where this thread's bytes of a key row stand: K: channels t * HD / 4 .. of key g; V: channels g * HD / 8 .. of
+  // keys 2t and 2t + 1 (16-byte piece x of row r is at x ^ r % 8, of 64-byte rows at x ^ r / 2 % 4)
+  int k_at[kVec], v_at[2];
+#pragma unroll
+  for (int y = 0; y < kVec; ++y)
+    k_at[y] = g * HD + (HD == 128 ? ((2 * t + y) ^ g) << 4 : (t ^ (g >> 1)) << 4);
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    v_at[r] = (2 * t + r) * HD + (HD == 128 ? (g ^ (2 * t + r)) << 4 : ((g >> 1) ^ t) << 4 | (g & 1) << 3);
 
   // --- a segment's start: page numbers, the first steps and Q on their way
   DecodeSegment sg = {};
@@ -253,41 +269,36 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas) k_decode(const De
         if ((i >> 4) & 1) ks[1] = k1, vs[1] = v1;
         else ks[0] = k1, vs[0] = v1;
       }
-      uint8_t* st = ring + (i % kStages) * kDecodeWarps * Smem::kStep;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int page = __shfl_sync(0xFFFFFFFFu, pg, (i & 15) * 2 + x);
-        if (page < 0) continue;
-        const int tok = tok0 + i * kDecodeTile + x * 16;
-        const size_t base = (((static_cast<size_t>(page) * n_kv + sg.kvh) << p.shift) + (tok & page_mask)) * HD;
-        const uint32_t dk = smem_u32(st) + x * Smem::kHalf + lane * 16;
-        const uint8_t* kp = kc + base + g * HD + t * 16;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int y = 0; y < kVec; ++y)
-            cp_async16(dk + (n * kVec + y) * Smem::kKPiece, kp + n * 8 * HD + y * 64);
-        const uint32_t dv = smem_u32(st) + x * Smem::kHalf + 2 * kVec * Smem::kKPiece + lane * (HD / 8);
-        const uint8_t* vp = vc + base + (2 * t) * HD + g * (HD / 8);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint8_t* src = vp + ((r & 1) + (r >> 1) * 8) * HD;
-          if (HD == 128) cp_async16(dv + r * Smem::kVPiece, src);
-          else cp_async8(dv + r * Smem::kVPiece, src);
+      const int p0 = __shfl_sync(0xFFFFFFFFu, pg, (i & 15) * 2), p1 = __shfl_sync(0xFFFFFFFFu, pg, (i & 15) * 2 + 1);
+      if (lane == 0) {
+        uint8_t* st = ring + (issued % kStages) * kDecodeWarps * Smem::kStep;
+        uint64_t* bar = &bars[issued % kStages];
+        const int off = (tok0 + i * kDecodeTile) & page_mask;
+        const bool second = p.box == 16 && p1 >= 0;  // (pages of 16: a copy for each half)
+        mbar_arrive_expect_tx(bar, ((p0 >= 0) + second) * p.box * 2 * HD);
+        if (p0 >= 0) {
+          const int row = ((p0 * n_kv + sg.kvh) << p.shift) + off;
+          tma_rows(st, &tm_k, bar, row);
+          tma_rows(st + 32 * HD, &tm_v, bar, row);
+        }
+        if (second) {
+          const int row = (p1 * n_kv + sg.kvh) << p.shift;
+          tma_rows(st + 16 * HD, &tm_k, bar, row);
+          tma_rows(st + 48 * HD, &tm_v, bar, row);
         }
       }
+      ++issued;
     }
-    cp_commit();
   };
   auto start = [&]() {
 #pragma unroll
     for (int h = 0; h < RH; ++h) {
       const int r = g + 8 * h;
       const __nv_bfloat16* row = q_base + (static_cast<int64_t>(sg.req) * a.slots + r / p.group) * a.q_row_stride +
-                                 (sg.kvh * p.group + r % p.group) * a.q_head_stride + t * 16;
+                                 (sg.kvh * p.group + r % p.group) * a.q_head_stride + t * (HD / 4);
 #pragma unroll
       for (int s = 0; s < kKSteps; ++s)  // channels in the order that K's pieces give
-        qw[h][s] = r < p.rows ? __ldg(reinterpret_cast<const uint2*>(row + (s >> 2) * 64 + (s & 3) * 4)) : make_uint2(0, 0);
+        qw[h][s] = r < p.rows ? __ldg(reinterpret_cast<const uint2*>(row + (s >> 2) * 16 + (s & 3) * 4)) : make_uint2(0, 0);
     }
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue(i);
@@ -298,6 +309,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas) k_decode(const De
     row_of.find(u - sg.kvh * total, sg.req, sg.first);
     sg.first += sg.kvh * total;
     place(u);
+    __syncthreads();  // (the sums of lengths have been read)
     start();
   }
 
@@ -394,8 +406,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas) k_decode(const De
     float vref = 1.17549435e-38f, vinv = 8.507059173e37f;
 
     for (int i = 0; i < steps; ++i) {
-      cp_wait<kStages - 2>();
-      const uint8_t* st = ring + (i % kStages) * kDecodeWarps * Smem::kStep;
+      gave_up |= !mbar_wait(&bars[used % kStages], (used / kStages) & 1, nullptr);
+      const uint8_t* st = ring + (used++ % kStages) * kDecodeWarps * Smem::kStep;
+      __syncwarp();  // (every lane has read the step before this one: its place is free)
+      issue(i + kStages - 1);
       const int set = (i >> 4) & 1;
       float s[2][RH][4], k_scale[2], v_scale[2];
       int valid[2];  // keys of this half that exist, if below 16
@@ -417,7 +431,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas) k_decode(const De
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int n = 0; n < 2; ++n)
-            kf[x][n] = *reinterpret_cast<const uint4*>(st + x * Smem::kHalf + (n * kVec + y) * Smem::kKPiece + lane * 16);
+            kf[x][n] = *reinterpret_cast<const uint4*>(st + (16 * x + 8 * n) * HD + k_at[y]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -501,7 +515,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas) k_decode(const De
         uint32_t vf[4][HD / 32];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const uint8_t* v = st + x * Smem::kHalf + 2 * kVec * Smem::kKPiece + r * Smem::kVPiece + lane * (HD / 8);
+          const uint8_t* v = st + (32 + 16 * x + (r >> 1) * 8) * HD + v_at[r & 1];
           if (HD == 128) {
             const uint4 y = *reinterpret_cast<const uint4*>(v);
             vf[r][0] = y.x, vf[r][1] = y.y, vf[r][HD / 32 - 2] = y.z, vf[r][HD / 32 - 1] = y.w;
@@ -534,7 +548,6 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas) k_decode(const De
           }
         }
       }
-      issue(i + kStages - 1);
     }
     // --- this warp's part, with that of the new tokens: sums over its keys, O in true units
     {
@@ -677,9 +690,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas) k_decode(const De
         }
       }
     }
-    if (!more) return;
+    if (!more) break;
     __syncthreads();  // (the join has been read)
   }
+  if (gave_up && a.status) atomicOr(a.status, DT_KV_TIMEOUT);
 }
 
 // Grid: one wave, and no more CTAs than tiles there can be (the host knows the longest possible request).
@@ -694,11 +708,11 @@ inline size_t decode_workspace(int rows, int head_dim) {
 }
 
 template <int HD, int RH>
-cudaError_t launch_decode(const DecodeParams& p, int grid, cudaStream_t st) {
+cudaError_t launch_decode(const CUtensorMap& k, const CUtensorMap& v, const DecodeParams& p, int grid, cudaStream_t st) {
   constexpr int bytes = DecodeSmem<HD, RH>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(k_decode<HD, RH>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  k_decode<HD, RH><<<grid, kDecodeThreads, bytes, st>>>(p);
+  k_decode<HD, RH><<<grid, kDecodeThreads, bytes, st>>>(k, v, p);
   return cudaGetLastError();
 }
 

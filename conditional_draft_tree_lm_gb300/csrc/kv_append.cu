@@ -13,9 +13,11 @@
 // (16-byte loads), so that it is read once: amax first, codes from the same
 // registers.  Runs are found from the slot map itself: a row leads a run unless
 // its slot is the previous row's plus one inside the same page, so no list of
-// pages is needed and no CTA waits for another.  With enough runs a CTA takes
-// several heads and tensors of its run, the next one's loads in flight while one
-// is reduced and written; with few, one each, for latency.
+// pages is needed and no CTA waits for another.  A CTA looks at a window of rows, a
+// warp at a row at a time: a run of up to eight rows (tokens, accepted paths) is the
+// warp's own, longer ones (prompts) are taken by the whole CTA afterwards, several
+// heads and tensors one after the other, the next one's loads in flight while one is
+// reduced and written.
 #include "kv.cuh"
 
 namespace dt {
@@ -41,39 +43,140 @@ DT_DEVINL float2 bf16x2_f32(uint32_t w) {
 }
 DT_DEVINL float finite_or(float x, float other) { return fabsf(x) <= 3.402823466e38f ? x : other; }
 
+// One vector of 8 channels: its largest finite magnitude, and its codes.
+DT_DEVINL float largest(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float amax = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = bf16x2_f32(w[k]);
+    amax = fmaxf(amax, fmaxf(fabsf(finite_or(f.x, 0.0f)), fabsf(finite_or(f.y, 0.0f))));
+  }
+  return amax;
+}
+// (1 / now is exact for a power of two; a scale that a caller set otherwise is divided by)
+DT_DEVINL uint2 encode(const uint4& v, float now) {
+  const float nan = __uint_as_float(0x7FC00000u);
+  const bool pow2 = (__float_as_uint(now) & 0x7FFFFFu) == 0;
+  const float inv = 1.0f / now;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float2 f = bf16x2_f32(w[k]);
+    f.x = finite_or(f.x, nan);
+    f.y = finite_or(f.y, nan);
+    f = pow2 ? make_float2(f.x * inv, f.y * inv) : make_float2(f.x / now, f.y / now);
+    o[k >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3)) << ((k & 1) * 16);
+  }
+  return make_uint2(o[0], o[1]);
+}
+// 8 earlier codes, moved to a scale that is 1 / ratio times as large.
+DT_DEVINL void move_codes(uint8_t* codes, float ratio) {
+  uint2* at = reinterpret_cast<uint2*>(codes);
+  const uint2 w = *at;
+  uint32_t r[2];
+  const uint32_t in[2] = {w.x, w.y};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t lo, hi;
+    e4m3x4_to_f16x2x2(in[k], lo, hi);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    r[k] = __nv_cvt_float2_to_fp8x2(make_float2(a.x * ratio, a.y * ratio), __NV_SATFINITE, __NV_E4M3) |
+           static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(b.x * ratio, b.y * ratio), __NV_SATFINITE, __NV_E4M3)) << 16;
+  }
+  *at = make_uint2(r[0], r[1]);
+}
+
+// A run of up to kShort rows, of one head and tensor, by a warp.
+constexpr int kShort = 8;
+template <int HD>
+DT_DEVINL void append_short(const AppendParams& p, int64_t t, int64_t slot, int len, int item) {
+  constexpr int kVecs = HD / 8, kRowsAtOnce = 32 / kVecs, kHeld = kShort / kRowsAtOnce;
+  const int lane = threadIdx.x & 31, head = item >> 1, which = item & 1;
+  const int page = 1 << p.shift, off = static_cast<int>(slot & (page - 1));
+  const int c = (lane % kVecs) * 8, r0 = lane / kVecs;
+  uint4 v[kHeld];
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int r = r0 + i * kRowsAtOnce;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (r < len) {
+      const int64_t src = p.src_rows ? p.src_rows[t + r] : t + r;
+      if (src >= 0 && src < p.n_src)
+        v[i] = __ldg(reinterpret_cast<const uint4*>(p.x[which] + src * p.row_stride[which] + head * p.head_stride[which] + c));
+      else if (p.status)
+        atomicOr(p.status, DT_KV_BAD_INDEX);
+    }
+  }
+  const int64_t tile = (slot >> p.shift) * p.n_kv + head;  // the page's part of this head
+  float* scale_at = p.scale[which] + tile;
+  const float old = off > 0 ? *scale_at : 0.0f;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) amax = fmaxf(amax, largest(v[i]));
+  const float need = kv_pow2_scale(warp_max(amax));
+  const float now = off > 0 && old > need ? old : need;
+  uint8_t* codes = p.codes[which] + tile * page * HD;
+  if (off > 0 && now > old) {
+    const float ratio = old / now;
+    for (int i = lane; i < off * kVecs; i += 32) move_codes(codes + static_cast<size_t>(i) * 8, ratio);
+  }
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int r = r0 + i * kRowsAtOnce;
+    if (r < len) *reinterpret_cast<uint2*>(codes + static_cast<size_t>(off + r) * HD + c) = encode(v[i], now);
+  }
+  __syncwarp();  // (every lane has read the old scale)
+  if (lane == 0 && now != old) *scale_at = now;
+}
+
 // NV: 16-byte vectors per thread of a full page (page * HD / 8 / threads, at least 1).
 template <int HD, int NV>
 __global__ void __launch_bounds__(kAppendThreads, NV >= 8 ? 2 : 4) k_kv_append(const AppendParams p) {
   constexpr int kVecs = HD / 8;  // vectors per row
   constexpr int kWarps = kAppendThreads / 32;
   __shared__ float warp_max_s[2][kWarps];
-  __shared__ int run_len_s;
-  const int tid = threadIdx.x;
+  __shared__ int n_long, long_at[128 / kShort + 1], long_len[128 / kShort + 1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int page = 1 << p.shift;
   const int item0 = blockIdx.y * p.items, item1 = min(item0 + p.items, 2 * p.n_kv);  // item: 2 * head + tensor
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.window;
-  const int64_t t1 = t0 + p.window < p.n_rows ? t0 + p.window : p.n_rows;
+  if (tid == 0) n_long = 0;
+  __syncthreads();
 
-  for (int64_t t = t0; t < t1;) {
-    const int64_t slot = p.slot_map[t];
-    const int64_t before = t > 0 ? p.slot_map[t - 1] : -1;
+  for (int i = warp; i < p.window && t0 + i < p.n_rows; i += kWarps) {
+    const int64_t t = t0 + i, slot = p.slot_map[t], before = t > 0 ? p.slot_map[t - 1] : -1;
     const int off = static_cast<int>(slot & (page - 1));
-    if (slot < 0 || slot >= p.n_slots) {
-      if (slot >= 0 && p.status && tid == 0) atomicOr(p.status, DT_KV_BAD_INDEX);
-      ++t;
+    if (slot < 0) continue;
+    if (slot >= p.n_slots) {
+      if (p.status && lane == 0) atomicOr(p.status, DT_KV_BAD_INDEX);
       continue;
     }
-    if (before >= 0 && before + 1 == slot && off != 0) {  // inside a run that starts before this row
-      ++t;
-      continue;
-    }
+    if (before >= 0 && before + 1 == slot && off != 0) continue;  // inside a run that starts before this row
     // the run: rows whose slots count up inside the page
-    __syncthreads();
-    if (tid == 0) run_len_s = page - off;
-    __syncthreads();
-    if (tid < page - off && (t + tid >= p.n_rows || p.slot_map[t + tid] != slot + tid)) atomicMin(&run_len_s, tid);
-    __syncthreads();
-    const int len = run_len_s;
+    int len = 1;
+    for (int x = 1; x < page - off; x += 32) {
+      const int r = x + lane;
+      const bool same = r < page - off && t + r < p.n_rows && p.slot_map[t + r] == slot + r;
+      const uint32_t more = __ballot_sync(0xFFFFFFFFu, same);
+      len += more == 0xFFFFFFFFu ? 32 : __ffs(~more) - 1;
+      if (more != 0xFFFFFFFFu) break;
+    }
+    if (len <= kShort) {
+      for (int item = item0; item < item1; ++item) append_short<HD>(p, t, slot, len, item);
+    } else if (lane == 0) {
+      const int at = atomicAdd(&n_long, 1);
+      long_at[at] = i;
+      long_len[at] = len;
+    }
+  }
+  __syncthreads();
+
+  for (int run = 0; run < n_long; ++run) {
+    const int64_t t = t0 + long_at[run], slot = p.slot_map[t];
+    const int off = static_cast<int>(slot & (page - 1)), len = long_len[run];
 
     // this thread's vectors: rows of the source, the same for every head and tensor
     int64_t src[NV];
@@ -101,14 +204,7 @@ __global__ void __launch_bounds__(kAppendThreads, NV >= 8 ? 2 : 4) k_kv_append(c
       const int which = item & 1, head = item >> 1;
       float amax = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = bf16x2_f32(w[k]);
-          amax = fmaxf(amax, fmaxf(fabsf(finite_or(f.x, 0.0f)), fabsf(finite_or(f.y, 0.0f))));
-        }
-      }
+      for (int i = 0; i < NV; ++i) amax = fmaxf(amax, largest(v[i]));
       const int64_t tile = (slot >> p.shift) * p.n_kv + head;  // the page's part of this head
       float* scale_at = p.scale[which] + tile;
       const float old = off > 0 ? *scale_at : 0.0f;  // (read by all before thread 0 may write it)
@@ -124,44 +220,12 @@ __global__ void __launch_bounds__(kAppendThreads, NV >= 8 ? 2 : 4) k_kv_append(c
       const float now = off > 0 && old > need ? old : need;
       if (off > 0 && now > old) {
         const float ratio = old / now;
-        for (int i = tid; i < off * kVecs; i += kAppendThreads) {
-          uint2* at = reinterpret_cast<uint2*>(codes + static_cast<size_t>(i) * 8);
-          const uint2 w = *at;
-          uint32_t r[2];
-          const uint32_t in[2] = {w.x, w.y};
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t lo, hi;
-            e4m3x4_to_f16x2x2(in[k], lo, hi);
-            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-            r[k] = __nv_cvt_float2_to_fp8x2(make_float2(a.x * ratio, a.y * ratio), __NV_SATFINITE, __NV_E4M3) |
-                   static_cast<uint32_t>(
-                       __nv_cvt_float2_to_fp8x2(make_float2(b.x * ratio, b.y * ratio), __NV_SATFINITE, __NV_E4M3))
-                       << 16;
-          }
-          *at = make_uint2(r[0], r[1]);
-        }
+        for (int i = tid; i < off * kVecs; i += kAppendThreads) move_codes(codes + static_cast<size_t>(i) * 8, ratio);
       }
-      // (1 / now is exact for a power of two; a scale that a caller set otherwise is divided by)
-      const float nan = __uint_as_float(0x7FC00000u);
-      const bool pow2 = (__float_as_uint(now) & 0x7FFFFFu) == 0;
-      const float inv = 1.0f / now;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int r = (tid + i * kAppendThreads) / kVecs;
-        if (r >= len) continue;
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t o[2] = {0, 0};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float2 f = bf16x2_f32(w[k]);
-          f.x = finite_or(f.x, nan);
-          f.y = finite_or(f.y, nan);
-          f = pow2 ? make_float2(f.x * inv, f.y * inv) : make_float2(f.x / now, f.y / now);
-          o[k >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3)) << ((k & 1) * 16);
-        }
-        *reinterpret_cast<uint2*>(codes + static_cast<size_t>(off + r) * HD + c) = make_uint2(o[0], o[1]);
+        if (r < len) *reinterpret_cast<uint2*>(codes + static_cast<size_t>(off + r) * HD + c) = encode(v[i], now);
       }
       if (tid == 0 && now != old) *scale_at = now;
     };
@@ -174,7 +238,7 @@ __global__ void __launch_bounds__(kAppendThreads, NV >= 8 ? 2 : 4) k_kv_append(c
       if (item + 2 < item1) load(v[0], item + 2);
       use(v[1], item + 1);
     }
-    t += len;
+    __syncthreads();  // (the next run's maxima take the same places)
   }
 }
 
@@ -225,16 +289,16 @@ extern "C" dt_status dt_kv_append(const dt_kv_cache* cache, const dt_kv_append_a
   while ((16 << p.shift) < cache->page) ++p.shift;
   p.shift += 4;
   p.n_slots = static_cast<int64_t>(cache->n_pages) << p.shift;
-  // Rows a CTA looks for runs in: one while the CTAs still fit the GPU a few times over
-  // (each row may be a run of its own, a token per request), up to a page for long prompts.
-  p.window = 1;
-  while (p.window < cache->page && (a.n_rows / p.window) * cache->n_kv * 2 > 16384) p.window *= 2;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // Rows of a window: eight, a row a warp, up to a page with many rows, so that the CTAs stay some waves.
+  p.window = 8;
+  while (p.window < cache->page && (a.n_rows / p.window) * cache->n_kv * 2 > kSms * 32) p.window *= 2;
   const int64_t windows = (a.n_rows + p.window - 1) / p.window;
-  // (head, tensor) pairs a CTA takes one after the other: one until there are 16 CTAs for each SM (40960 rows of
-  // prompts: 81 us, 86 with 8 or 4, 96 with 32; 512 padded rows of accepted paths: 10.2, 13.0, 20.8 and 9.0 us)
+  // (head, tensor) pairs a CTA takes one after the other: one until there are 16 CTAs for each SM.  (40960 rows of
+  // prompts, 8 heads of 128: 78 us, 3.2 TB/s; 4096 tokens of as many requests 33 us; the accepted paths of 32 trees
+  // 5.0 us, 32 tokens 3.0 us.  One CTA for each run, head and tensor took 165, 287, 10.2 and 4.2 us.)
   p.items = 1;
   while (p.items < 2 * cache->n_kv && windows * 2 * cache->n_kv / p.items > kSms * 16) p.items *= 2;
   const dim3 grid(static_cast<unsigned>(windows), static_cast<unsigned>((2 * cache->n_kv + p.items - 1) / p.items));
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return kv_launched(who, cache->head_dim == 64 ? launch<64>(p, grid, st) : launch<128>(p, grid, st));
 }

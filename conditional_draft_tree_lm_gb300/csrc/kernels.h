@@ -53,11 +53,6 @@ struct GemmParams {
 
 bool make_tmap_bf16_2d(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t rows,
                        uint64_t row_stride_bytes, uint32_t box_rows);
-// Rows of heads (strides in elements) as a 3D map: boxes of 64 channels x heads x rows.
-bool make_tmap_bf16_heads(CUtensorMap* tm, const void* base, int head_dim, int heads, int64_t rows, int64_t head_stride,
-                          int64_t row_stride, int box_heads, int box_rows);
-// Contiguous rows of 64 or 128 bytes as a 2D map of bytes, swizzled by the row's length: boxes of whole rows.
-bool make_tmap_u8_rows(CUtensorMap* tm, const void* base, int row_bytes, int64_t rows, int box_rows);
 void gemm_plan(GemmParams& p, int BN);
 size_t gemm_smem_bytes(const GemmParams& p);
 // The grid of a launch (one persistent CTA per SM at most).

@@ -5,6 +5,7 @@
 #include <cstdarg>
 #include <cstdio>
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -82,8 +83,13 @@ inline bool kv_rows_ok(const void* p, int64_t row_stride, int64_t head_stride) {
 
 dt_status kv_check_cache(const char* who, const dt_kv_cache* c);
 
-// SM count of the current device, and one-time raising of a kernel's dynamic
-// shared-memory limit per device.
+// Rows of heads in bf16 (strides in elements) as a 3D tensor map: boxes of 64 channels x heads x rows, swizzled.
+bool kv_tmap_heads(CUtensorMap* tm, const void* base, int head_dim, int heads, int64_t rows, int64_t head_stride,
+                   int64_t row_stride, int box_heads, int box_rows);
+// Contiguous rows of 64 or 128 bytes as a 2D map of bytes, swizzled by the row's length: boxes of whole rows.
+bool kv_tmap_rows(CUtensorMap* tm, const void* base, int row_bytes, int64_t rows, int box_rows);
+
+// SM count of the current device.
 cudaError_t kv_num_sms(int* n);
 
 }  // namespace dt

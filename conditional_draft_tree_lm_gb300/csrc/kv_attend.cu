@@ -59,8 +59,8 @@ extern "C" dt_status dt_cache_attention(const dt_kv_cache* cache, const dt_cache
     if (rows > 0x7FFFFFFF) return kv_fail(DT_ERR_SHAPE, "%s: more than 2^31-1 cached tokens and heads", who);
     p.box = cache->page < 32 ? 16 : 32;
     CUtensorMap k, v;
-    if (!make_tmap_u8_rows(&k, cache->k, cache->head_dim, rows, p.box) ||
-        !make_tmap_u8_rows(&v, cache->v, cache->head_dim, rows, p.box))
+    if (!kv_tmap_rows(&k, cache->k, cache->head_dim, rows, p.box) ||
+        !kv_tmap_rows(&v, cache->v, cache->head_dim, rows, p.box))
       return kv_fail(DT_ERR_SHAPE, "%s: no tensor map for this cache", who);
     cudaError_t e;
     if (cache->head_dim == 64) e = p.rows <= 8 ? launch_decode<64, 1>(k, v, p, grid, st) : launch_decode<64, 2>(k, v, p, grid, st);

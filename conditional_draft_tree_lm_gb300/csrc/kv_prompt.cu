@@ -519,9 +519,9 @@ extern "C" dt_status dt_prompt_attention(const dt_prompt_attention_args* args, v
   p.slots = static_cast<int>(slots);
   p.c = a.scale * kLog2e;
   CUtensorMap q, k, v;
-  if (!make_tmap_bf16_heads(&q, a.q, a.head_dim, a.n_q, a.n_rows, a.q_head_stride, a.q_row_stride, p.group, p.positions) ||
-      !make_tmap_bf16_heads(&k, a.k, a.head_dim, a.n_kv, a.n_rows, a.k_head_stride, a.k_row_stride, 1, kKeyTile) ||
-      !make_tmap_bf16_heads(&v, a.v, a.head_dim, a.n_kv, a.n_rows, a.v_head_stride, a.v_row_stride, 1, kKeyTile))
+  if (!kv_tmap_heads(&q, a.q, a.head_dim, a.n_q, a.n_rows, a.q_head_stride, a.q_row_stride, p.group, p.positions) ||
+      !kv_tmap_heads(&k, a.k, a.head_dim, a.n_kv, a.n_rows, a.k_head_stride, a.k_row_stride, 1, kKeyTile) ||
+      !kv_tmap_heads(&v, a.v, a.head_dim, a.n_kv, a.n_rows, a.v_head_stride, a.v_row_stride, 1, kKeyTile))
     return kv_fail(DT_ERR_SHAPE, "%s: strides that a tensor map does not take (zero, or 2^40 bytes and more)", who);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return kv_launched(who, a.head_dim == 64 ? launch<64>(q, k, v, p, st) : launch<128>(q, k, v, p, st));

@@ -212,31 +212,26 @@ struct SoftmaxRow {
 // what turns a raw logit of keys 16 g .. 16 g + 15 into powers of two, one value
 // for all where UNIFORM; negative: its sign is negative.  see: the row's visible
 // keys, all of them unless MASKED.  ready(i): called when half i of P is stored.
-// HOLD: all of S stays in registers (128 of them) between the maximum and the
-// exponentials; otherwise it is read twice, 32 columns ahead of their use.
-template <int HD, bool BF16, bool UNIFORM, bool MASKED, bool HOLD, class Scale, class Ready>
+// S is read twice, 32 columns ahead of their use, and both loops are rolled up: with
+// several roles' code running at once, instruction fetches count (S in 128 registers
+// between the maximum and the exponentials, loops unrolled: 48 prompts of up to 1k
+// tokens 300 us instead of 272, 16k tokens 1380 instead of 1367).  One body for
+// masked tiles and others costs more than it saves there: 288 and 1650 us.
+template <int HD, bool BF16, bool UNIFORM, bool MASKED, class Scale, class Ready>
 DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float ratio, bool negative, Scale scale,
                             const uint32_t (&see)[4], SoftmaxRow& row, Ready ready) {
-  uint32_t s[HOLD ? 128 : 64];
-  auto part = [&](int w) { return s + (HOLD ? 32 * w : 32 * (w & 1)); };
-  if (HOLD) {
-#pragma unroll
-    for (int w = 0; w < 4; ++w) tmem_ld32(s_at + 32 * w, part(w));
-    tmem_wait_ld();
-  } else {
-    tmem_ld32(s_at, part(0));
-  }
+  uint32_t s[64];
+  tmem_ld32(s_at, s);
   float top = -INFINITY;
-  // (rolled up where S is read twice: with several roles' code running at once, instruction fetches count)
-#pragma unroll(HOLD ? 2 : 1)
+#pragma unroll 1
   for (int w2 = 0; w2 < 4; w2 += 2)
 #pragma unroll
   for (int w1 = 0; w1 < 2; ++w1) {
     const int w = w2 + w1;
-    uint32_t* v = part(HOLD ? w : w1);
-    if (!HOLD) tmem_wait_ld();
+    uint32_t* v = s + 32 * w1;
+    tmem_wait_ld();
     tmem_landed32(v);
-    if (!HOLD) tmem_ld32(s_at + 32 * ((w + 1) & 3), part(w1 + 1));  // (the last one: the first, for the second reading)
+    tmem_ld32(s_at + 32 * ((w + 1) & 3), s + 32 * (w1 ^ 1));  // (the last one: the first, for the second reading)
     if (MASKED) {
       const uint32_t out = negative ? 0x7F800000u : 0xFF800000u;
       const uint32_t bits = w1 == 0 ? (w2 == 0 ? see[0] : see[2]) : (w2 == 0 ? see[1] : see[3]);
@@ -265,7 +260,7 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
   // (a tile of which the row sees nothing has top = -inf, or 0 with a scale of zero: no harm, P is 0)
   if (__any_sync(0xFFFFFFFFu, top > row.m + 8.0f || ratio != 1.0f)) {
     const float m2 = fmaxf(row.m, top), f = m2 == -INFINITY ? 1.0f : ex2(row.m - m2);
-    if (!HOLD) tmem_wait_ld();  // (s is on its way; the rescaling waits for its own)
+    tmem_wait_ld();  // (s is on its way; the rescaling waits for its own)
     if (!first) rescale_o<HD>(o_at, f * ratio);
     row.l *= f;
     row.m = m2;
@@ -273,18 +268,16 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
   const float base = row.m == -INFINITY ? 0.0f : row.m;
   const uint64_t base2 = f32x2(-base, -base);
   uint64_t sum[2] = {0, 0};
-#pragma unroll(HOLD ? 2 : 1)
+#pragma unroll 1
   for (int w2 = 0; w2 < 4; w2 += 2)
 #pragma unroll
   for (int w1 = 0; w1 < 2; ++w1) {
     const int w = w2 + w1;
     uint32_t pk[16];
-    uint32_t* v = part(HOLD ? w : w1);
-    if (!HOLD) {
-      tmem_wait_ld();
-      tmem_landed32(v);
-      if (w1 == 0 || w2 == 0) tmem_ld32(s_at + 32 * (w + 1), part(w1 + 1));
-    }
+    uint32_t* v = s + 32 * w1;
+    tmem_wait_ld();
+    tmem_landed32(v);
+    if (w1 == 0 || w2 == 0) tmem_ld32(s_at + 32 * (w + 1), s + 32 * (w1 ^ 1));
     const uint32_t bits = w1 == 0 ? (w2 == 0 ? see[0] : see[2]) : (w2 == 0 ? see[1] : see[3]);
     // (of a masked tile, most 32-key parts are seen by all of a warp's rows or by none)
     const bool none = MASKED && __all_sync(0xFFFFFFFFu, bits == 0u);

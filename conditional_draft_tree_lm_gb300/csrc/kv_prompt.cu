@@ -413,9 +413,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int seen = pos + 1 - j * kKeyTile;  // of this tile's keys, by this row
         const uint32_t see[4] = {first_bits(seen, 0), first_bits(seen, 1), first_bits(seen, 2), first_bits(seen, 3)};
         if ((j + 1) * kKeyTile > from + 1)
-          softmax_tile<HD, true, true, true, false>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
+          softmax_tile<HD, true, true, true>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
         else
-          softmax_tile<HD, true, true, false, true>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
+          softmax_tile<HD, true, true, false>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
       }
       if (n > 0) {
         ok = ok && mbar_wait(&o_full[t], o_use++ & 1, nullptr);

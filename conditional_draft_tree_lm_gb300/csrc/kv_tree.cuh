@@ -663,8 +663,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             const float ratio = i == 0 || vref == info.vref ? 1.0f : vref / info.vref;
             vref = info.vref;
             auto scale = [&](int g) { return c * info.k_scale[g]; };
-            if (masked) softmax_tile<HD, false, false, true, false>(s_at, o_at, i == 0, ratio, c < 0.0f, scale, see, sm, ready);
-            else softmax_tile<HD, false, false, false, false>(s_at, o_at, i == 0, ratio, c < 0.0f, scale, see, sm, ready);
+            if (masked) softmax_tile<HD, false, false, true>(s_at, o_at, i == 0, ratio, c < 0.0f, scale, see, sm, ready);
+            else softmax_tile<HD, false, false, false>(s_at, o_at, i == 0, ratio, c < 0.0f, scale, see, sm, ready);
           }
           if (poison) sm.l = NAN;
           if (steps > 0) ok = ok && mbar_wait(&o_full[t], o_use++ & 1, nullptr);

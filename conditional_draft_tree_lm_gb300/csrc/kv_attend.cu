@@ -2,15 +2,40 @@
 //
 // Up to 16 rows (new tokens x heads of a group) per key/value head the cache is
 // streamed through mma.m16n8k16 (kv_decode.cuh), whose time does not depend on the
-// rows there; above, 128-row tiles on tcgen05 (kv_tree.cuh).
+// rows there; above, 128-row tiles on tcgen05 (kv_tree.cuh).  What is left over
+// behind pairs of full row tiles, as with a root and 64 drafted tokens of 4 heads a
+// group, would cost as much there as a pair: up to 16 such rows go to the streaming
+// kernel, launched beside the other, where there are enough heads and requests.
 #include "kv_decode.cuh"
 #include "kv_tree.cuh"
 
+namespace dt {
+
+// Row tiles of a call with more than 16 rows per key/value head: pairs, the odd one, and
+// the first slot of those left to the streaming kernel (0: none).  It takes them where
+// the odd tile holds 16 rows at most and there are 32 key/value heads over all
+// requests.  65 slots of 4 heads a group, 8 key/value heads, us without and with it: 32
+// requests of up to 4k tokens 305 and 228, of up to 512 148 and 101; 4 requests of
+// up to 4k 63 and 60; but one request of 2k tokens 53 and 59, of 32k 119 and 149.
+struct RowTiles {
+  int pairs, odd, rest;
+  RowTiles(int n_req, int slots, int group, int n_kv) {
+    const int per_tile = 128 / group, tiles = (slots + per_tile - 1) / per_tile;
+    pairs = tiles / 2;
+    odd = tiles % 2;
+    const int first = (tiles - 1) * per_tile;
+    rest = odd && pairs > 0 && (slots - first) * group <= kDecodeMaxRows && static_cast<int64_t>(n_req) * n_kv >= 32 ? first : 0;
+  }
+};
+
+}  // namespace dt
+
 extern "C" size_t dt_cache_attention_workspace(int n_req, int slots, int n_q, int n_kv, int head_dim) {
   if (n_req < 1 || slots < 1 || n_kv < 1 || n_q < n_kv || n_q % n_kv != 0 || (head_dim != 64 && head_dim != 128)) return 0;
-  const int rows = slots * (n_q / n_kv);
-  if (rows <= dt::kDecodeMaxRows) return dt::decode_workspace(rows, head_dim);
-  return dt::tree_workspace(head_dim);
+  if (static_cast<int64_t>(slots) * (n_q / n_kv) <= dt::kDecodeMaxRows) return dt::decode_workspace(slots * (n_q / n_kv), head_dim);
+  if (n_q / n_kv > 128) return 0;
+  const dt::RowTiles tiles(n_req, slots, n_q / n_kv, n_kv);
+  return dt::tree_workspace(head_dim) + (tiles.rest ? dt::decode_workspace(dt::kDecodeMaxRows, head_dim) : 0);
 }
 
 extern "C" dt_status dt_cache_attention(const dt_kv_cache* cache, const dt_cache_attention_args* args, void* stream) {
@@ -43,49 +68,57 @@ extern "C" dt_status dt_cache_attention(const dt_kv_cache* cache, const dt_cache
     return kv_fail(DT_ERR_SHAPE, "%s: more than 2^37 cached tokens over all requests and heads", who);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int group = a.n_q / cache->n_kv;
-  if (a.slots * group <= kDecodeMaxRows) {
+  const dt::RowTiles rows(a.n_req, a.slots, group, cache->n_kv);
+  int shift = 4;
+  while ((1 << shift) < cache->page) ++shift;
+  unsigned* done = static_cast<unsigned*>(a.workspace);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kCounterBytes);
+  // key rows of the whole cache, as the streaming kernel's copies count them: ((page * n_kv) + head) * page_size + offset
+  const int64_t key_rows = static_cast<int64_t>(cache->n_pages) * cache->n_kv * cache->page;
+  auto decode = [&](int slot0) -> dt_status {  // the slots from slot0 on
     DecodeParams p = {};
     p.c = *cache;
     p.a = a;
     p.group = group;
-    p.rows = a.slots * group;
-    p.shift = 4;
-    while ((1 << p.shift) < cache->page) ++p.shift;
-    p.done = static_cast<unsigned*>(a.workspace);
-    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kCounterBytes);
+    p.slot0 = slot0;
+    p.rows = (a.slots - slot0) * group;
+    p.shift = shift;
+    p.done = slot0 ? done + a.n_req * cache->n_kv * rows.pairs : done;  // (behind what the tree kernel uses)
+    p.part = slot0 ? part + (tree_workspace(cache->head_dim) - kCounterBytes) / 4 : part;
     const int grid = decode_grid(a.n_req, cache->n_kv, static_cast<long long>(a.max_blocks) * cache->page);
-    // key rows of the whole cache: row ((page * n_kv) + head) * page_size + offset
-    const int64_t rows = static_cast<int64_t>(cache->n_pages) * cache->n_kv * cache->page;
-    if (rows > 0x7FFFFFFF) return kv_fail(DT_ERR_SHAPE, "%s: more than 2^31-1 cached tokens and heads", who);
     p.box = cache->page < 32 ? 16 : 32;
     CUtensorMap k, v;
-    if (!kv_tmap_rows(&k, cache->k, cache->head_dim, rows, p.box) ||
-        !kv_tmap_rows(&v, cache->v, cache->head_dim, rows, p.box))
+    if (!kv_tmap_rows(&k, cache->k, cache->head_dim, key_rows, p.box) ||
+        !kv_tmap_rows(&v, cache->v, cache->head_dim, key_rows, p.box))
       return kv_fail(DT_ERR_SHAPE, "%s: no tensor map for this cache", who);
     cudaError_t e;
-    if (cache->head_dim == 64) e = p.rows <= 8 ? launch_decode<64, 1>(k, v, p, grid, st) : launch_decode<64, 2>(k, v, p, grid, st);
-    else e = p.rows <= 8 ? launch_decode<128, 1>(k, v, p, grid, st) : launch_decode<128, 2>(k, v, p, grid, st);
+    if (cache->head_dim == 64) e = p.rows <= 8 ? launch_decode<64, 1>(k, v, p, grid, slot0 > 0, st) : launch_decode<64, 2>(k, v, p, grid, slot0 > 0, st);
+    else e = p.rows <= 8 ? launch_decode<128, 1>(k, v, p, grid, slot0 > 0, st) : launch_decode<128, 2>(k, v, p, grid, slot0 > 0, st);
     return kv_launched(who, e);
+  };
+  if (static_cast<int64_t>(a.slots) * group <= kDecodeMaxRows) {
+    if (key_rows > 0x7FFFFFFF) return kv_fail(DT_ERR_SHAPE, "%s: more than 2^31-1 cached tokens and heads", who);
+    return decode(0);
   }
   TreeParams p = {};
   p.c = *cache;
   p.a = a;
   p.group = group;
-  p.shift = 4;
-  while ((1 << p.shift) < cache->page) ++p.shift;
+  p.shift = shift;
   p.per_tile = 128 / group;
   p.inverse = group_inverse(group);
-  const int row_tiles = (a.slots + p.per_tile - 1) / p.per_tile;
-  p.pairs = row_tiles / 2;
-  p.odd = row_tiles % 2;
+  const bool stream_rest = rows.rest > 0 && key_rows <= 0x7FFFFFFF;
+  p.pairs = rows.pairs;
+  p.odd = stream_rest ? 0 : rows.odd;
   p.fresh_tiles = a.k_new ? (a.slots + kKeyTile - 1) / kKeyTile : 0;
   const int64_t key_tiles = (static_cast<int64_t>(a.max_blocks) * cache->page + kKeyTile - 1) / kKeyTile + p.fresh_tiles * kNewCost + 1;
   const int64_t units = key_tiles * (p.pairs + p.odd) * a.n_req * cache->n_kv;
   if (units > (1 << 30)) return kv_fail(DT_ERR_SHAPE, "%s: more than 2^30 tiles over all requests and heads", who);
-  if (static_cast<int64_t>(a.n_req) * cache->n_kv * (p.pairs + p.odd) > kMaxJoins)
+  if (static_cast<int64_t>(a.n_req) * cache->n_kv * (rows.pairs + rows.odd) > kMaxJoins)
     return kv_fail(DT_ERR_SHAPE, "%s: n_req * n_kv * pairs of row tiles above %d", who, kMaxJoins);
-  p.done = static_cast<unsigned*>(a.workspace);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kCounterBytes);
+  p.done = done;
+  p.part = part;
   const int grid = tree_grid(units);
-  return kv_launched(who, cache->head_dim == 64 ? launch_tree<64>(p, grid, st) : launch_tree<128>(p, grid, st));
+  if (dt_status s = kv_launched(who, cache->head_dim == 64 ? launch_tree<64>(p, grid, st) : launch_tree<128>(p, grid, st))) return s;
+  return stream_rest ? decode(rows.rest) : DT_OK;
 }

@@ -1,5 +1,6 @@
 // dt_cache_attention for few query rows per key/value head (slots * group <= 16:
-// single tokens, short drafts): streaming the 8-bit cache once.
+// single tokens, short drafts; or as few rows behind a tree's full row tiles):
+// streaming the 8-bit cache once.
 //
 // Per key/value head the group's rows share every cached key, so a call reads
 // len * 2 * head_dim bytes for 4 * rows * len * head_dim flops: at most 32 flops
@@ -31,7 +32,12 @@
 // outside: the key's multiplies the logit, the value's is folded into P relative
 // to the largest scale seen so far.  Q is brought to fp16 by a power of two per
 // row (exact to 2^-40 of the row's maximum), P is held in fp16: 11 bits, where
-// bf16 would give 8.  Maxima, sums and O are 32 bits.
+// bf16 would give 8.  Maxima, sums and O are 32 bits.  New tokens' keys and values
+// take the same products in bf16 (row by row with plain multiplications: 15 us more
+// for 32 trees of 65 slots, 40 us for a tree of 513).
+//
+// Measured: 32 tokens over caches of up to 16k tokens (671 MB) 109 us, 6.2 TB/s, 91 %
+// of the measured copy bandwidth; one token over 2k 8.0 us, a chain of latencies.
 #pragma once
 
 #include <cuda.h>
@@ -54,7 +60,8 @@ constexpr int kMaxJoins = static_cast<int>(kCounterBytes / 4);
 struct DecodeParams {
   dt_kv_cache c;
   dt_cache_attention_args a;
-  int group, rows, shift;  // rows = slots * group
+  int group, rows, shift;  // rows: of the slots from slot0 on, times group
+  int slot0;
   int box;                 // rows of a copy: 32, or a page of 16
   unsigned* done;          // [n_req * n_kv] pieces that are done; zero between launches
   float* part;             // [2 * pieces][rows][HD], then [2 * pieces][rows][2]: a piece's first and last (request, head)
@@ -62,6 +69,12 @@ struct DecodeParams {
 
 DT_DEVINL void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+DT_DEVINL void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -176,6 +189,9 @@ struct DecodeSmem {
   static constexpr int kBytes = kRing + kJoin + kStages * kDecodeWarps * 8 + 16;
 };
 
+// A kernel that was started beside the one before it in the stream ends after that one.
+DT_DEVINL void after_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // A stretch of one (request, head) inside a piece.
 struct DecodeSegment {
   int req, kvh, first, tiles;  // first: the (request, head)'s first tile in the work
@@ -216,7 +232,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
   row_of.sum(s_start + kDecodeThreads + 1);
   const int work = row_of.total() * n_kv;
   const int pieces = min(work, static_cast<int>(gridDim.x));
-  if (static_cast<int>(blockIdx.x) >= pieces) return;
+  if (static_cast<int>(blockIdx.x) >= pieces) {
+    after_kernel_before();
+    return;
+  }
   const Cut cut(work, pieces);
   float* stats = p.part + static_cast<size_t>(2 * pieces) * p.rows * HD;
   const int piece = blockIdx.x;
@@ -294,7 +313,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
 #pragma unroll
     for (int h = 0; h < RH; ++h) {
       const int r = g + 8 * h;
-      const __nv_bfloat16* row = q_base + (static_cast<int64_t>(sg.req) * a.slots + r / p.group) * a.q_row_stride +
+      const __nv_bfloat16* row = q_base + (static_cast<int64_t>(sg.req) * a.slots + p.slot0 + r / p.group) * a.q_row_stride +
                                  (sg.kvh * p.group + r % p.group) * a.q_head_stride + t * (HD / 4);
 #pragma unroll
       for (int s = 0; s < kKSteps; ++s)  // channels in the order that K's pieces give
@@ -314,51 +333,148 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
   }
 
   for (;;) {
-    // --- the new tokens' own keys, at most 16, with the (request, head)'s first tile: a warp per row.
-    // Part of the warp's share: m, l and O of its rows wait in the join's place.
+    // --- the new tokens' own keys, with the (request, head)'s first tile: 16 of them a step, the warps in turn.
+    // The same products in bf16, as Q and they come; P as the sum of two bf16 (16 bits).  Part of the warp's share:
+    // m, l and O wait in the join's place.
     const bool with_fresh = sg.begin == 0 && a.k_new;
     if (with_fresh) {
-      constexpr int N = HD / 32;
-      int span = 1;
-      while (span < a.slots) span <<= 1;  // lanes: key lane % span, channels (lane / span) * HD / (32 / span) ..
-      const int b = lane & (span - 1), chans = HD * span / 32, c0 = lane / span * chans;
+      float fo[RH][kKSteps][4], fm[RH][2], fl[RH][2];
       const int64_t row0 = static_cast<int64_t>(sg.req) * a.slots;
-      for (int r = warp; r < kRows; r += kDecodeWarps) {
-        float z = -INFINITY, fo[N];
-        bool see = false;
+      const uint8_t* mask[RH][2];
+      int slot[RH][2];  // of rows 8 h + 2t and 2t + 1; -1: no such row
 #pragma unroll
-        for (int i = 0; i < N; ++i) fo[i] = 0.0f;
-        if (r < p.rows) {
-          const int slot = r / p.group;
-          see = b < a.slots && (a.mask ? a.mask[(row0 + slot) * a.slots + b] != 0 : b <= slot);
-          float dot = 0.0f;
-          if (b < a.slots) {
-            const __nv_bfloat16* qp = q_base + (row0 + slot) * a.q_row_stride + (sg.kvh * p.group + r % p.group) * a.q_head_stride + c0;
-            const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(a.k_new) + (row0 + b) * a.k_row_stride + sg.kvh * a.k_head_stride + c0;
-            for (int c = 0; c < chans; c += 2) {
-              const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(qp + c));
-              const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(kp + c));
-              dot += x.x * y.x + x.y * y.y;
+      for (int h = 0; h < RH; ++h) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = 8 * h + 2 * t + k;
+          slot[h][k] = r < p.rows ? p.slot0 + r / p.group : -1;
+          mask[h][k] = a.mask + (row0 + slot[h][k]) * a.slots;
+          fm[h][k] = -INFINITY;
+          fl[h][k] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < kKSteps; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) fo[h][j][k] = 0.0f;
+      }
+      for (int k0 = 16 * warp; k0 < a.slots; k0 += 16 * kDecodeWarps) {
+        uint4 kw[2][HD / 32], vw[4][HD / 64];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int b = k0 + g + 8 * x;
+          const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(a.k_new) + (row0 + b) * a.k_row_stride + sg.kvh * a.k_head_stride + t * (HD / 4);
+#pragma unroll
+          for (int c = 0; c < HD / 32; ++c) kw[x][c] = b < a.slots ? __ldg(reinterpret_cast<const uint4*>(kp) + c) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int b = k0 + 2 * t + (x & 1) + 8 * (x >> 1);
+          const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v_new) + (row0 + b) * a.v_row_stride + sg.kvh * a.v_head_stride + g * (HD / 8);
+#pragma unroll
+          for (int c = 0; c < HD / 64; ++c) vw[x][c] = b < a.slots ? __ldg(reinterpret_cast<const uint4*>(vp) + c) : make_uint4(0, 0, 0, 0);
+        }
+        uint32_t see = 0;  // bit 4 h + 2 x + k: row 8 h + 2t + k sees key k0 + g + 8 x
+#pragma unroll
+        for (int h = 0; h < RH; ++h)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int b = k0 + g + 8 * x;
+              if (slot[h][k] >= 0 && b < a.slots && (a.mask ? __ldg(mask[h][k] + b) != 0 : b <= slot[h][k])) see |= 1u << (4 * h + 2 * x + k);
+            }
+        // values that are not finite: the key takes no part in the product, the rows that see it become NaN
+        uint32_t bad = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          bool odd = false;
+#pragma unroll
+          for (int c = 0; c < HD / 64; ++c) {
+            const uint32_t y[4] = {vw[x][c].x, vw[x][c].y, vw[x][c].z, vw[x][c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) odd |= (y[i] & 0x7F80u) == 0x7F80u || (y[i] & 0x7F800000u) == 0x7F800000u;
+          }
+          if (odd) bad |= 1u << (2 * t + (x & 1) + 8 * (x >> 1));
+        }
+        bad = __reduce_or_sync(0xFFFFFFFFu, bad);
+        if (bad) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (bad >> (2 * t + (x & 1) + 8 * (x >> 1)) & 1u) {
+#pragma unroll
+              for (int c = 0; c < HD / 64; ++c) vw[x][c] = make_uint4(0, 0, 0, 0);
+            }
+        }
+        uint32_t ph[RH][2], pl[RH][2];
+#pragma unroll
+        for (int h = 0; h < RH; ++h) {
+          float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int c = 0; c < HD / 32; ++c) {
+            mma_bf16(s, kw[0][c].x, kw[1][c].x, kw[0][c].y, kw[1][c].y, qw[h][2 * c].x, qw[h][2 * c].y);
+            mma_bf16(s, kw[0][c].z, kw[1][c].z, kw[0][c].w, kw[1][c].w, qw[h][2 * c + 1].x, qw[h][2 * c + 1].y);
+          }
+          float e[4], f[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const bool s0 = see >> (4 * h + k) & 1u, s1 = see >> (4 * h + 2 + k) & 1u;
+            const float z0 = s0 ? s[k] * (a.scale * 1.4426950408889634f) : -INFINITY;
+            const float z1 = s1 ? s[k + 2] * (a.scale * 1.4426950408889634f) : -INFINITY;
+            float top = fmaxf(fm[h][k], fmaxf(z0, z1));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+            const float base = top == -INFINITY ? 0.0f : top;
+            f[k] = fast_exp2(fm[h][k] - base);
+            fm[h][k] = top;
+            e[k] = s0 ? fast_exp2(z0 - base) : 0.0f;
+            e[k + 2] = s1 ? fast_exp2(z1 - base) : 0.0f;
+            fl[h][k] = fl[h][k] * f[k] + (e[k] + e[k + 2]);
+            if ((s0 && bad >> g & 1u) || (s1 && bad >> (g + 8) & 1u)) fl[h][k] = NAN;
+          }
+#pragma unroll
+          for (int j = 0; j < kKSteps; ++j) {
+            fo[h][j][0] *= f[0], fo[h][j][1] *= f[1];
+            fo[h][j][2] *= f[0], fo[h][j][3] *= f[1];
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(e[2 * x], e[2 * x + 1]);
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(e[2 * x] - __low2float(hi), e[2 * x + 1] - __high2float(hi));
+            ph[h][x] = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi));
+            pl[h][x] = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < HD / 64; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) w[x] = i == 0 ? vw[x][c].x : i == 1 ? vw[x][c].y : i == 2 ? vw[x][c].z : vw[x][c].w;
+            const uint32_t a0 = __byte_perm(w[0], w[1], 0x5410), a1 = __byte_perm(w[0], w[1], 0x7632);
+            const uint32_t a2 = __byte_perm(w[2], w[3], 0x5410), a3 = __byte_perm(w[2], w[3], 0x7632);
+#pragma unroll
+            for (int h = 0; h < RH; ++h) {
+              mma_bf16(fo[h][4 * c + i], a0, a1, a2, a3, ph[h][0], ph[h][1]);
+              mma_bf16(fo[h][4 * c + i], a0, a1, a2, a3, pl[h][0], pl[h][1]);
             }
           }
-          for (int o = span; o < 32; o <<= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-          if (see) z = dot * (a.scale * 1.4426950408889634f);
-        }
-        float top = warp_max(z);
-        const float base = top == -INFINITY ? 0.0f : top;
-        const float e = see ? fast_exp2(z - base) : 0.0f;
-        const float sum = warp_sum(lane < span ? e : 0.0f);
-        for (int k = 0; k < a.slots && r < p.rows; ++k) {
-          const float w = __shfl_sync(0xFFFFFFFFu, e, k);
-          if (!__shfl_sync(0xFFFFFFFFu, see, k)) continue;  // (what a row does not see may be NaN)
-          const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v_new) + (row0 + k) * a.v_row_stride + sg.kvh * a.v_head_stride + lane * N;
-#pragma unroll
-          for (int i = 0; i < N; ++i) fo[i] += w * __bfloat162float(vp[i]);
-        }
-        if (lane == 0) s_m[warp * kRows + r] = top, s_l[warp * kRows + r] = sum;
-#pragma unroll
-        for (int i = 0; i < N; ++i) s_o[(warp * kRows + r) * HD + lane * N + i] = fo[i];
       }
+#pragma unroll
+      for (int h = 0; h < RH; ++h)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = warp * kRows + 8 * h + 2 * t + k;
+          float sum = fl[h][k];
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+          if (g == 0) s_m[r] = fm[h][k], s_l[r] = sum;
+#pragma unroll
+          for (int j = 0; j < kKSteps; ++j)
+            *reinterpret_cast<float2*>(s_o + r * HD + g * (HD / 8) + 2 * j) = make_float2(fo[h][j][k], fo[h][j][k + 2]);
+        }
       __syncwarp();
     }
 
@@ -561,11 +677,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
           sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
           sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
           sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
-          const bool mine = with_fresh && (r & (kDecodeWarps - 1)) == warp;
-          const float fm = mine ? s_m[at] : -INFINITY, fl = mine ? s_l[at] : 0.0f;
+          const float fm = with_fresh ? s_m[at] : -INFINITY, fl = with_fresh ? s_l[at] : 0.0f;
           const float top = fmaxf(m[h][k], fm), base = top == -INFINITY ? 0.0f : top;
           f_old[h][k] = fast_exp2(m[h][k] - base);
-          f_fresh[h][k] = mine ? fast_exp2(fm - base) : 0.0f;
+          f_fresh[h][k] = with_fresh ? fast_exp2(fm - base) : 0.0f;
           m[h][k] = top;
           l[h][k] = sum * f_old[h][k] + fl * f_fresh[h][k];
           f_old[h][k] *= vref;
@@ -577,7 +692,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
             const int r = 8 * h + 2 * t + k;
             float2* x = reinterpret_cast<float2*>(s_o + (warp * kRows + r) * HD + g * (HD / 8) + 2 * j);
             float2 y = make_float2(o[h][j][k] * f_old[h][k], o[h][j][k + 2] * f_old[h][k]);
-            if (with_fresh && (r & (kDecodeWarps - 1)) == warp) {
+            if (with_fresh) {
               y.x += x->x * f_fresh[h][k];
               y.y += x->y * f_fresh[h][k];
             }
@@ -612,7 +727,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
     const bool alone = c_first == c_last;
     auto finish = [&](int r, int c, float top, float sum, const float4& acc) {
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      const int64_t row = static_cast<int64_t>(was.req) * a.slots + r / p.group;
+      const int64_t row = static_cast<int64_t>(was.req) * a.slots + p.slot0 + r / p.group;
       const int head = was.kvh * p.group + r % p.group;
       __nv_bfloat162 w[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv), __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * a.out_row_stride + head * a.out_head_stride + c) =
@@ -637,9 +752,9 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
       if (alone) {
         finish(r, c, top, sum, acc);
       } else {
-        const size_t mine = static_cast<size_t>(2 * piece + (piece == c_first)) * p.rows + r;
-        __stcg(reinterpret_cast<float4*>(p.part + mine * HD + c), acc);
-        if (c == 0) __stcg(reinterpret_cast<float2*>(stats + mine * 2), make_float2(top, sum));
+        const size_t own = static_cast<size_t>(2 * piece + (piece == c_first)) * p.rows + r;
+        __stcg(reinterpret_cast<float4*>(p.part + own * HD + c), acc);
+        if (c == 0) __stcg(reinterpret_cast<float2*>(stats + own * 2), make_float2(top, sum));
       }
     }
     if (!alone) {
@@ -694,6 +809,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
     __syncthreads();  // (the join has been read)
   }
   if (gave_up && a.status) atomicOr(a.status, DT_KV_TIMEOUT);
+  after_kernel_before();
 }
 
 // Grid: one wave, and no more CTAs than tiles there can be (the host knows the longest possible request).
@@ -707,13 +823,24 @@ inline size_t decode_workspace(int rows, int head_dim) {
   return kCounterBytes + (parts + 255) / 256 * 256;
 }
 
+// beside: started when the kernel before it in the stream, the tree kernel of the same call, has left SMs free
+// (they share neither counters nor parts).
 template <int HD, int RH>
-cudaError_t launch_decode(const CUtensorMap& k, const CUtensorMap& v, const DecodeParams& p, int grid, cudaStream_t st) {
+cudaError_t launch_decode(const CUtensorMap& k, const CUtensorMap& v, const DecodeParams& p, int grid, bool beside, cudaStream_t st) {
   constexpr int bytes = DecodeSmem<HD, RH>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(k_decode<HD, RH>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  k_decode<HD, RH><<<grid, kDecodeThreads, bytes, st>>>(k, v, p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kDecodeThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k_decode<HD, RH>, k, v, p);
 }
 
 }  // namespace dt

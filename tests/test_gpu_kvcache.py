@@ -459,6 +459,58 @@ def test_cache_attention_nan_in_masked_tokens(slots):
         assert not np.isfinite(out[b, a, :, 5]).any()
 
 
+# 32 and more key/value heads over all requests, rows behind pairs of full 128-row tiles: up to 16 of them are streamed
+REST = [
+    ([0, 1, 130, 64, 500, 3, 90, 257], 65, 16, 4, 128, 64, "tree"),     # 4 rows left
+    ([0, 1, 130, 64, 500, 3, 90, 257], 34, 32, 4, 64, 16, "random"),    # 16 rows
+    ([40, 300, 0, 129], 259, 8, 8, 128, 32, "causal"),                  # 3 rows of single heads
+    ([40, 300, 0, 129], 66, 32, 8, 128, 128, None),                     # 8 rows, cached tokens only
+    ([700, 20, 0, 33], 69, 32, 8, 128, 64, "random"),                   # 20 rows: a tile of their own
+    ([65] * 33, 129, 4, 1, 64, 64, "random"),                           # behind two pairs
+]
+
+
+@pytest.mark.parametrize("lens,slots,heads,kv,hd,page,fresh", REST)
+def test_cache_attention_rows_left_over(lens, slots, heads, kv, hd, page, fresh):
+    c = cache_case(np.random.RandomState(len(lens) * 2000 + slots), lens, slots, heads, kv, hd, page, fresh)
+    check_cache(c, run_cache(c), rows=[0, 1, 31, slots // 2, *range(slots - 6, slots)])
+
+
+def test_cache_attention_rows_left_over_nan():
+    torch = _t()
+    rs = np.random.RandomState(41)
+    slots = 66
+    c = cache_case(rs, [50, 0, 200, 9], slots, 32, 8, 128, 64, "random")
+    skip = set()
+    for (b, s), val in {(0, 1): float("nan"), (1, 40): float("inf"), (2, slots - 1): float("-inf")}.items():
+        c["v"][b, s, :, 5] = val
+        c["k"][b, s, 0, 7] = val
+        c["mask"][b, slots - 1, s] = b != 2  # the last row sees two of them, the one before it the third
+        c["mask"][b, slots - 2, s] = b == 2
+        skip |= {(b, a) for a in range(slots) if c["mask"][b, a, s]}
+    out, lse = run_cache(c)
+    clean = dict(c, k=c["k"].nan_to_num(0, 0, 0), v=c["v"].nan_to_num(0, 0, 0))
+    check_cache(clean, (out, lse), skip=skip, rows=[0, 2, slots - 3, slots - 2, slots - 1])
+    for b, a in skip:
+        assert not np.isfinite(out[b, a, :, 5]).any()
+
+
+def test_cache_attention_rows_left_over_repeats():
+    """Both kernels of a call in one workspace, again and again, next to calls of other kinds."""
+    from conditional_draft_tree_lm_gb300 import AttentionWorkspace
+    work = AttentionWorkspace()
+    rs = np.random.RandomState(42)
+    c = cache_case(rs, [3000, 10, 0, 900], 65, 32, 8, 128, 64, "tree")
+    d = cache_case(rs, [50, 1000, 7], 1, 8, 4, 64, 16, "tree")
+    first = run_cache(c, work=work)
+    check_cache(c, first, rows=[0, 63, 64])
+    for _ in range(5):
+        check_cache(d, run_cache(d, work=work))
+        again = run_cache(c, work=work)
+        np.testing.assert_array_equal(first[0], again[0])
+        np.testing.assert_array_equal(first[1], again[1])
+
+
 def test_cache_attention_bad_pages_count_as_absent():
     torch = _t()
     for slots in (1, 30):

@@ -23,9 +23,17 @@
 //
 // Split.  The work is the list of (key/value head, request, row tiles, key tile),
 // cut into equal pieces, one for each SM.  A tile of new keys counts kNewCost times
-// (it is read and reduced before it can be converted: 18 000 cycles against 4 400).
-// A stretch that several pieces share is joined by the
-// CTA that finishes last, in the order of keys.
+// (it is read and reduced before it can be converted: some 18 000 cycles against
+// 4 400).  A stretch that several pieces share is joined by the CTA that finishes
+// last, in the order of keys.
+//
+// Measured: 32 trees of 65 slots (4 rows of each head streamed by the other kernel)
+// over up to 4k cached tokens, 32 heads over 8, 218 us; one of 513 slots over 32k 325
+// us, 0.85 PFLOP/s.  Where the time goes: the products 2048 cycles of a pair of row
+// tiles' 4 400 a key tile, the rest the softmax between them and shared memory (Q, K
+// and V are read by both tiles' products, and written by the conversion); and what a
+// stretch costs besides, its Q and its join, some 30 000 cycles, two or three times
+// a CTA.  Reading the next stretch's Q and new tokens into L2 ahead changes nothing.
 #pragma once
 
 #include "kv_decode.cuh"
@@ -35,9 +43,14 @@ namespace dt {
 
 constexpr int kTreeStages = 4;   // K and V tiles, alternating
 constexpr int kTreeSlots = 4;    // what goes with a key tile: its scales and masks
-constexpr int kTreeMmaWarp = 8, kTreeFetchWarp = 9, kTreeConvWarp = 10, kTreeConvWarps = 4;
+constexpr int kTreeMmaWarp = 8, kTreeFetchWarp = 9, kTreeConvWarp = 12, kTreeConvWarps = 4;  // (10 and 11: none)
 constexpr int kConvThreads = 32 * kTreeConvWarps;
 constexpr int kTreeThreads = 32 * (kTreeConvWarp + kTreeConvWarps);
+// Registers: 512 threads start with 128; the softmax's 256 go to 144, the others' to 112.  What a role spills goes
+// to L2, there being no L1 left beside the shared memory (us for 32 trees and for the wide one: 136 and 120: 217 and
+// 339; 144 and 112: 215 and 336; 152 and 104: 220 and 344; 160 and 96: 217 and 342).
+constexpr int kTreeSoftmaxRegs = 144, kTreeOtherRegs = 112;
+static_assert(2 * kTreeSoftmaxRegs + 2 * kTreeOtherRegs <= 4 * 128, "");
 
 struct TreeParams {
   dt_kv_cache c;
@@ -51,7 +64,7 @@ struct TreeParams {
   float* part;      // [2 * pieces][2 tiles][HD / 4][128][4], then [2 * pieces][2][128][2]
 };
 
-constexpr int kNewCost = 4;  // (of 2, 4, 6: 315, 303, 303 us for 32 trees, 359, 338, 332 us for the wide one)
+constexpr int kNewCost = 5;  // (of 3, 4, 5: 221, 215, 218 us for 32 trees, 337, 334, 325 us for the wide one)
 
 // What a row tile or a pair of them costs over a request's keys, at least 1.
 DT_DEVINL int tree_cost(int len, int max_len, int fresh) {
@@ -234,329 +247,330 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
     const uint32_t q_s = smem_u32(smem + Smem::kQ), ring = smem_u32(smem + Smem::kRing);
 
     bool gave_up = false;  // a bounded wait did
-    if (warp == kTreeMmaWarp) {
-      const bool leader = elect_one();
-      int count = 0;  // key tiles so far
-      int p_use[2] = {0, 0};
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, nullptr));
-        tc_fence_after();
-      };
-      auto full_wait = [&](int i) { wait(&full[i % kTreeStages], (i / kTreeStages) & 1); };
-      auto at = [&](int i) { return ring + (i % kTreeStages) * Smem::kOperand; };
-      auto commit = [&](uint64_t* bar) {
-        if (leader) tc_commit(bar);
-      };
-      const uint64_t q_desc[2] = {flash_desc(q_s, false), flash_desc(q_s + Smem::kOperand, false)};
-      auto pv = [&](int t, int i, bool first, bool last) {  // ring entry i into O of slot t
-        const uint32_t turn = p_use[t]++ & 1;
-        const uint64_t vd = flash_desc(at(i), true);
-        wait(&p_full[2 * t], turn);
-        if (ok && leader) issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, vd, first, 0);
-        wait(&p_full[2 * t + 1], turn);
-        if (ok && leader) issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, vd, first, 1);
-        if (ok && last) commit(&o_full[t]);
-      };
-      auto qk = [&](int t, int i) {
-        if (!ok) return;
-        if (leader) issue_qk<HD, false>(tmem + t * 128, q_desc[t], flash_desc(at(i), false));
-        commit(&s_full[t]);
-      };
-      auto release = [&](int i) {
-        if (ok) commit(&empty[i % kTreeStages]);
-      };
-      for (int seg = 0; ok && walk.next(p, sg);) {
-        const int n = sg.key_end - sg.key_begin;
-        if (n == 0) continue;
-        wait(&q_full[0], seg & 1);
-        wait(&q_full[1], seg & 1);
-        ++seg;
-        full_wait(2 * count);
-        qk(0, 2 * count);
-        if (sg.tiles == 2) {
-          qk(1, 2 * count);
-          release(2 * count);
-          for (int j = 0; j < n && ok; ++j, ++count) {
-            const int vi = 2 * count + 1, ki = vi + 1;
-            const bool more = j + 1 < n;
-            full_wait(vi);
-            if (more) full_wait(ki);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              pv(t, vi, j == 0, !more);
-              if (more) qk(t, ki);
-            }
-            release(vi);
-            if (more) release(ki);
-          }
-        } else {
-          release(2 * count);
-#pragma unroll 1
-          for (int j0 = 0; j0 < n && ok; j0 += 2) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const int j = j0 + t;
-              if (j >= n) break;
-              const int vi = 2 * (count + j) + 1, ki = vi + 1;
-              if (j + 1 < n) {
-                full_wait(ki);
-                qk(t ^ 1, ki);
-                release(ki);
-              }
+    if (warp >= kTreeMmaWarp) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeOtherRegs));
+      if (warp == kTreeMmaWarp) {
+        const bool leader = elect_one();
+        int count = 0;  // key tiles so far
+        int p_use[2] = {0, 0};
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, nullptr));
+          tc_fence_after();
+        };
+        auto full_wait = [&](int i) { wait(&full[i % kTreeStages], (i / kTreeStages) & 1); };
+        auto at = [&](int i) { return ring + (i % kTreeStages) * Smem::kOperand; };
+        auto commit = [&](uint64_t* bar) {
+          if (leader) tc_commit(bar);
+        };
+        const uint64_t q_desc[2] = {flash_desc(q_s, false), flash_desc(q_s + Smem::kOperand, false)};
+        auto pv = [&](int t, int i, bool first, bool last) {  // ring entry i into O of slot t
+          const uint32_t turn = p_use[t]++ & 1;
+          const uint64_t vd = flash_desc(at(i), true);
+          wait(&p_full[2 * t], turn);
+          if (ok && leader) issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, vd, first, 0);
+          wait(&p_full[2 * t + 1], turn);
+          if (ok && leader) issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, vd, first, 1);
+          if (ok && last) commit(&o_full[t]);
+        };
+        auto qk = [&](int t, int i) {
+          if (!ok) return;
+          if (leader) issue_qk<HD, false>(tmem + t * 128, q_desc[t], flash_desc(at(i), false));
+          commit(&s_full[t]);
+        };
+        auto release = [&](int i) {
+          if (ok) commit(&empty[i % kTreeStages]);
+        };
+        for (int seg = 0; ok && walk.next(p, sg);) {
+          const int n = sg.key_end - sg.key_begin;
+          if (n == 0) continue;
+          wait(&q_full[0], seg & 1);
+          wait(&q_full[1], seg & 1);
+          ++seg;
+          full_wait(2 * count);
+          qk(0, 2 * count);
+          if (sg.tiles == 2) {
+            qk(1, 2 * count);
+            release(2 * count);
+            for (int j = 0; j < n && ok; ++j, ++count) {
+              const int vi = 2 * count + 1, ki = vi + 1;
+              const bool more = j + 1 < n;
               full_wait(vi);
-              pv(t, vi, j0 == 0, j + 2 >= n);
+              if (more) full_wait(ki);
+  #pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                pv(t, vi, j == 0, !more);
+                if (more) qk(t, ki);
+              }
               release(vi);
+              if (more) release(ki);
             }
-          }
-          count += n;
-        }
-      }
-      gave_up = !ok;
-    } else if (warp == kTreeFetchWarp) {
-      // --- pages to the staging place, a tile ahead of their conversion; page numbers and scales another tile ahead
-      struct Page {  // of 16 keys, held by lanes 0..7
-        int id;
-        float ks, vs;
-      };
-      TreeKeyTile cur, nxt;
-      TreeTileWalk tw = {walk, {}, 0};
-      auto pages_of = [&](const TreeKeyTile& t) {
-        Page g = {-1, 1.0f, 0.0f};
-        const int tok = t.key0 + lane * 16;
-        if (t.kind == kTileCached && lane < 8 && tok < t.len) {
-          g.id = __ldg(a.block_table + static_cast<size_t>(t.req) * a.max_blocks + (tok >> p.shift));
-          if (g.id < 0 || g.id >= p.c.n_pages) {
-            if (a.status) atomicOr(a.status, DT_KV_BAD_INDEX);
-            g.id = -1;
           } else {
-            const size_t at = static_cast<size_t>(g.id) * n_kv + t.kvh;
-            g.ks = __ldg(p.c.k_scale + at);
-            g.vs = __ldg(p.c.v_scale + at);
-          }
-        }
-        return g;
-      };
-      const int copy_keys = min(1 << p.shift, kKeyTile);
-      tw.next(p, cur);
-      Page gc = pages_of(cur);
-      bool ok = true;
-      int fetched[2] = {0, 0};
-      for (int count = 0; cur.kind != kTileNone && ok; ++count) {
-        tw.next(p, nxt);
-        const Page gn = pages_of(nxt);
-        TreeTile& info = tiles[count % kTreeSlots];
-        const bool copies = cur.kind == kTileCached && lane < 8 && gc.id >= 0 && (lane * 16 & (copy_keys - 1)) == 0;
-        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, copies)) * copy_keys * HD;
-        const uint32_t there = __ballot_sync(0xFFFFFFFFu, gc.id >= 0);
-        const size_t at = copies ? (static_cast<size_t>(gc.id) * n_kv + cur.kvh << p.shift) * HD : 0;
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&st_free[which], (count & 1) ^ 1, nullptr));
-          if (!ok) break;
-          // (the place is free: the tile four before this one is behind its softmax, too)
-          if (which == 0) {
-            const float v_top = warp_max(lane < 8 ? gc.vs : 0.0f);
-            const bool plain = __all_sync(0xFFFFFFFFu, lane >= 8 || (gc.id >= 0 && gc.vs == v_top)) && cur.len - cur.key0 >= kKeyTile;
-            if (lane < 8) info.k_scale[lane] = gc.ks, info.v_scale[lane] = gc.vs;
-            if (lane == 0) info.v_top = v_top, info.plain = plain;
-            if (lane < 4) {
-              const uint32_t two = there >> (2 * lane);
-              info.seen[lane] = cur.kind == kTileNew ? first_bits(a.slots - cur.key0, lane)
-                                                     : first_bits(cur.len - cur.key0, lane) & (((two & 1) ? 0xFFFFu : 0u) | ((two & 2) ? 0xFFFF0000u : 0u));
-              info.bad[lane] = 0;
-            }
-            __syncwarp();
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&st_full[which], bytes);
-          ++fetched[which];
-          __syncwarp();
-          if (copies)
-            bulk_load(smem_u32(smem + Smem::kStaging) + which * kKeyTile * HD + lane * 16 * HD,
-                      static_cast<const uint8_t*>(which ? p.c.v : p.c.k) + at, copy_keys * HD, &st_full[which]);
-        }
-        cur = nxt;
-        gc = gn;
-      }
-      // (where a wait gave up: no copy may outlive the CTA)
-      if (!ok)
-        for (int which = 0; which < 2; ++which)
-          if (fetched[which] > 0) mbar_wait(&st_full[which], (fetched[which] - 1) & 1, nullptr);
-      gave_up = !ok;
-    } else if (warp >= kTreeConvWarp) {
-      // --- conversion
-      constexpr int kLanes = HD / 16;               // threads of a key's row (16 bytes each)
-      constexpr int kPassRows = kConvThreads / kLanes;
-      constexpr int kPasses = kKeyTile / kPassRows;  // pieces of a thread
-      const int ct = tid - kTreeConvWarp * 32, cw = ct >> 5, cc = ct % kLanes, cr = ct / kLanes;
-      // 8 halves to their place: key `row`, channels 8 * chunk .. (the swizzle: a row's 16-byte pieces by row % 8)
-      auto put = [&](uint8_t* op, int row, int chunk, const uint4& w) {
-        *reinterpret_cast<uint4*>(op + (chunk >> 3) * kHalfBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) = w;
-      };
-      auto arrive = [&](int i) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[i % kTreeStages]);
-      };
-      // (where a wait gives up the loop goes on without waiting: other warps may stand at its named barrier)
-      bool ok = true;
-      auto room = [&](int i) { ok = ok && mbar_wait(&empty[i % kTreeStages], ((i / kTreeStages) & 1) ^ 1, nullptr); };
-      // a cached tile's K or V out of the staging place.  The two halves of a row's threads begin with different
-      // halves of their 16 bytes, so that their stores meet different banks.
-      const bool swap = HD == 128 && (cc & 4);
-      const int chunk0 = 2 * cc + (swap ? 1 : 0);
-      const int place = (chunk0 >> 3) * kHalfBytes + cr * 128, piece0 = ((chunk0 & 7) ^ (cr & 7)) << 4;
-      const uint8_t* st0 = smem + Smem::kStaging + ct * 16 + (swap ? 8 : 0);
-      const int st1 = swap ? -8 : 8;
-      // (passes are multiples of 8 rows apart: the swizzle is the same; plain: neither masks nor factors)
-      auto convert = [&](const TreeTile& info, int count, int which, bool plain, float inv) {
-        const uint8_t* st = st0 + which * kKeyTile * HD;
-        uint8_t* op = smem + Smem::kRing + ((2 * count + which) % kTreeStages) * Smem::kOperand + place;
-        constexpr int kBatch = 4;
-#pragma unroll 1
-        for (int k0 = 0; k0 < kPasses; k0 += kBatch) {
-          uint2 w[kBatch][2];
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const uint8_t* x = st + (k0 + k) * kConvThreads * 16;
-            w[k][0] = *reinterpret_cast<const uint2*>(x);
-            w[k][1] = *reinterpret_cast<const uint2*>(x + st1);
-          }
-          if (k0 + kBatch == kPasses) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&st_free[which]);
-          }
-          if (k0 == 0) room(2 * count + which);
-          uint32_t h[kBatch][8];
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              e4m3x4_to_f16x2x2(w[k][y].x, h[k][4 * y], h[k][4 * y + 1]);
-              e4m3x4_to_f16x2x2(w[k][y].y, h[k][4 * y + 2], h[k][4 * y + 3]);
-            }
-          if (!plain) {
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              const int row = (k0 + k) * kPassRows + cr;
-              const bool seen = info.seen[row >> 5] >> (row & 31) & 1u;  // (what no row sees may be NaN, or not there)
-              const __half2 f2 = __float2half2_rn(which ? info.v_scale[row >> 4] * inv : 1.0f);
-#pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[k][x]), f2);
-                h[k][x] = seen ? *reinterpret_cast<const uint32_t*>(&y) : 0u;
+            release(2 * count);
+  #pragma unroll 1
+            for (int j0 = 0; j0 < n && ok; j0 += 2) {
+  #pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                const int j = j0 + t;
+                if (j >= n) break;
+                const int vi = 2 * (count + j) + 1, ki = vi + 1;
+                if (j + 1 < n) {
+                  full_wait(ki);
+                  qk(t ^ 1, ki);
+                  release(ki);
+                }
+                full_wait(vi);
+                pv(t, vi, j0 == 0, j + 2 >= n);
+                release(vi);
               }
             }
-          }
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            uint8_t* to = op + (k0 + k) * kPassRows * 128;
-            *reinterpret_cast<uint4*>(to + piece0) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
-            *reinterpret_cast<uint4*>(to + (piece0 ^ 16)) = make_uint4(h[k][4], h[k][5], h[k][6], h[k][7]);
+            count += n;
           }
         }
-        arrive(2 * count + which);
-      };
-      // A new tile, bf16: the largest finite magnitudes first, then fp16 by a power of two each.  K stays in
-      // registers between, V is read twice.
-      constexpr int kL = HD / 8, kR = kConvThreads / kL, kP = kKeyTile / kR;
-      const int c8 = ct % kL, r8 = ct / kL;
-      auto piece_of = [&](const TreeKeyTile& t, const void* x, int64_t row_stride, int64_t head_stride, int k) {
-        const int b = t.key0 + k * kR + r8;
-        return b < a.slots ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) +
-                                                                  (static_cast<int64_t>(t.req) * a.slots + b) * row_stride +
-                                                                  t.kvh * head_stride + c8 * 8))
-                           : make_uint4(0, 0, 0, 0);
-      };
-      auto largest = [&](const uint4& w, float& top) {  // returns whether something is not finite
-        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-        bool odd = false;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float lo = fabsf(__uint_as_float(in[y] << 16)), hi = fabsf(__uint_as_float(in[y] & 0xFFFF0000u));
-          const bool fl = lo <= 3.402823466e38f, fh = hi <= 3.402823466e38f;
-          odd |= !fl || !fh;
-          top = fmaxf(top, fmaxf(fl ? lo : 0.0f, fh ? hi : 0.0f));
-        }
-        return odd;
-      };
-      auto put_new = [&](uint8_t* op, int k, const uint4& w, float inv) {
-        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-        uint32_t h[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          h[y] = pack_f16(__uint_as_float(in[y] << 16) * inv, __uint_as_float(in[y] & 0xFFFF0000u) * inv);
-        put(op, k * kR + r8, c8, make_uint4(h[0], h[1], h[2], h[3]));
-      };
-      auto convert_new = [&](const TreeKeyTile& t, TreeTile& info, int count, float& vref) {
-        uint4 w[kP];
-#pragma unroll
-        for (int k = 0; k < kP; ++k) w[k] = piece_of(t, a.k_new, a.k_row_stride, a.k_head_stride, k);
-        float top[2] = {0.0f, 0.0f};
-#pragma unroll 8
-        for (int k = 0; k < kP; ++k)
-          // the key's value takes no part in the product, the rows that see it become NaN
-          if (largest(piece_of(t, a.v_new, a.v_row_stride, a.v_head_stride, k), top[1]))
-            atomicOr(&info.bad[(k * kR + r8) >> 5], 1u << ((k * kR + r8) & 31));
-#pragma unroll
-        for (int k = 0; k < kP; ++k) largest(w[k], top[0]);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          top[x] = warp_max(top[x]);
-          if (lane == 0) s_max[x][cw] = top[x];
-        }
-        asm volatile("bar.sync 2, %0;" ::"n"(kConvThreads) : "memory");
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int k = 0; k < kTreeConvWarps; ++k) top[x] = fmaxf(top[x], s_max[x][k]);
-        asm volatile("bar.sync 2, %0;" ::"n"(kConvThreads) : "memory");
-        const float k_scale = kv_pow2_scale(top[0]);
-        vref = fmaxf(vref, kv_pow2_scale(top[1]));
-        if (ct < 8) info.k_scale[ct] = k_scale;
-        if (ct == 0) info.vref = vref;
-        const float k_inv = 1.0f / k_scale, v_inv = 1.0f / vref;
-        room(2 * count);
-        uint8_t* op = smem + Smem::kRing + ((2 * count) % kTreeStages) * Smem::kOperand;
-#pragma unroll
-        for (int k = 0; k < kP; ++k) put_new(op, k, w[k], k_inv);
-        arrive(2 * count);
-        room(2 * count + 1);
-        op = smem + Smem::kRing + ((2 * count + 1) % kTreeStages) * Smem::kOperand;
-#pragma unroll 8
-        for (int k = 0; k < kP; ++k) {
-          const int row = k * kR + r8;
-          const bool bad = info.bad[row >> 5] >> (row & 31) & 1u;
-          put_new(op, k, bad ? make_uint4(0, 0, 0, 0) : piece_of(t, a.v_new, a.v_row_stride, a.v_head_stride, k), v_inv);
-        }
-        arrive(2 * count + 1);
-      };
-      TreeKeyTile cur;
-      TreeTileWalk tw = {walk, {}, 0};
-      float vref = 0.0f;
-      for (int count = 0; tw.next(p, cur), cur.kind != kTileNone; ++count) {
-        TreeTile& info = tiles[count % kTreeSlots];
-        if (cur.first) vref = 1.17549435e-38f;
-        ok = ok && mbar_wait(&st_full[0], count & 1, nullptr);
-        if (cur.kind == kTileCached) {
-          vref = fmaxf(vref, info.v_top);
-          if (ct == 0) info.vref = vref;
-          const float inv = 1.0f / vref;
-          const bool plain = info.plain, even = vref == info.v_top;
-#pragma unroll 1
+        gave_up = !ok;
+      } else if (warp == kTreeFetchWarp) {
+        // --- pages to the staging place, a tile ahead of their conversion; page numbers and scales another tile ahead
+        struct Page {  // of 16 keys, held by lanes 0..7
+          int id;
+          float ks, vs;
+        };
+        TreeKeyTile cur, nxt;
+        TreeTileWalk tw = {walk, {}, 0};
+        auto pages_of = [&](const TreeKeyTile& t) {
+          Page g = {-1, 1.0f, 0.0f};
+          const int tok = t.key0 + lane * 16;
+          if (t.kind == kTileCached && lane < 8 && tok < t.len) {
+            g.id = __ldg(a.block_table + static_cast<size_t>(t.req) * a.max_blocks + (tok >> p.shift));
+            if (g.id < 0 || g.id >= p.c.n_pages) {
+              if (a.status) atomicOr(a.status, DT_KV_BAD_INDEX);
+              g.id = -1;
+            } else {
+              const size_t at = static_cast<size_t>(g.id) * n_kv + t.kvh;
+              g.ks = __ldg(p.c.k_scale + at);
+              g.vs = __ldg(p.c.v_scale + at);
+            }
+          }
+          return g;
+        };
+        const int copy_keys = min(1 << p.shift, kKeyTile);
+        tw.next(p, cur);
+        Page gc = pages_of(cur);
+        bool ok = true;
+        int fetched[2] = {0, 0};
+        for (int count = 0; cur.kind != kTileNone && ok; ++count) {
+          tw.next(p, nxt);
+          const Page gn = pages_of(nxt);
+          TreeTile& info = tiles[count % kTreeSlots];
+          const bool copies = cur.kind == kTileCached && lane < 8 && gc.id >= 0 && (lane * 16 & (copy_keys - 1)) == 0;
+          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, copies)) * copy_keys * HD;
+          const uint32_t there = __ballot_sync(0xFFFFFFFFu, gc.id >= 0);
+          const size_t at = copies ? (static_cast<size_t>(gc.id) * n_kv + cur.kvh << p.shift) * HD : 0;
+  #pragma unroll
           for (int which = 0; which < 2; ++which) {
-            if (which) ok = ok && mbar_wait(&st_full[1], count & 1, nullptr);
-            convert(info, count, which, plain && (which == 0 || even), inv);
+            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&st_free[which], (count & 1) ^ 1, nullptr));
+            if (!ok) break;
+            // (the place is free: the tile four before this one is behind its softmax, too)
+            if (which == 0) {
+              const float v_top = warp_max(lane < 8 ? gc.vs : 0.0f);
+              const bool plain = __all_sync(0xFFFFFFFFu, lane >= 8 || (gc.id >= 0 && gc.vs == v_top)) && cur.len - cur.key0 >= kKeyTile;
+              if (lane < 8) info.k_scale[lane] = gc.ks, info.v_scale[lane] = gc.vs;
+              if (lane == 0) info.v_top = v_top, info.plain = plain;
+              if (lane < 4) {
+                const uint32_t two = there >> (2 * lane);
+                info.seen[lane] = cur.kind == kTileNew ? first_bits(a.slots - cur.key0, lane)
+                                                       : first_bits(cur.len - cur.key0, lane) & (((two & 1) ? 0xFFFFu : 0u) | ((two & 2) ? 0xFFFF0000u : 0u));
+                info.bad[lane] = 0;
+              }
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&st_full[which], bytes);
+            ++fetched[which];
+            __syncwarp();
+            if (copies)
+              bulk_load(smem_u32(smem + Smem::kStaging) + which * kKeyTile * HD + lane * 16 * HD,
+                        static_cast<const uint8_t*>(which ? p.c.v : p.c.k) + at, copy_keys * HD, &st_full[which]);
           }
-        } else {
-          ok = ok && mbar_wait(&st_full[1], count & 1, nullptr);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&st_free[0]), mbar_arrive(&st_free[1]);
-          convert_new(cur, info, count, vref);
+          cur = nxt;
+          gc = gn;
         }
+        // (where a wait gave up: no copy may outlive the CTA)
+        if (!ok)
+          for (int which = 0; which < 2; ++which)
+            if (fetched[which] > 0) mbar_wait(&st_full[which], (fetched[which] - 1) & 1, nullptr);
+        gave_up = !ok;
+      } else if (warp >= kTreeConvWarp) {
+        // --- conversion
+        constexpr int kLanes = HD / 16;               // threads of a key's row (16 bytes each)
+        constexpr int kPassRows = kConvThreads / kLanes;
+        constexpr int kPasses = kKeyTile / kPassRows;  // pieces of a thread
+        const int ct = tid - kTreeConvWarp * 32, cw = ct >> 5, cc = ct % kLanes, cr = ct / kLanes;
+        // 8 halves to their place: key `row`, channels 8 * chunk .. (the swizzle: a row's 16-byte pieces by row % 8)
+        auto put = [&](uint8_t* op, int row, int chunk, const uint4& w) {
+          *reinterpret_cast<uint4*>(op + (chunk >> 3) * kHalfBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) = w;
+        };
+        auto arrive = [&](int i) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[i % kTreeStages]);
+        };
+        // (where a wait gives up the loop goes on without waiting: other warps may stand at its named barrier)
+        bool ok = true;
+        auto room = [&](int i) { ok = ok && mbar_wait(&empty[i % kTreeStages], ((i / kTreeStages) & 1) ^ 1, nullptr); };
+        // a cached tile's K or V out of the staging place.  The two halves of a row's threads begin with different
+        // halves of their 16 bytes, so that their stores meet different banks.
+        const bool swap = HD == 128 && (cc & 4);
+        const int chunk0 = 2 * cc + (swap ? 1 : 0);
+        const int place = (chunk0 >> 3) * kHalfBytes + cr * 128, piece0 = ((chunk0 & 7) ^ (cr & 7)) << 4;
+        const uint8_t* st0 = smem + Smem::kStaging + ct * 16 + (swap ? 8 : 0);
+        const int st1 = swap ? -8 : 8;
+        // (passes are multiples of 8 rows apart: the swizzle is the same; plain: neither masks nor factors)
+        auto convert = [&](const TreeTile& info, int count, int which, bool plain, float inv) {
+          const uint8_t* st = st0 + which * kKeyTile * HD;
+          uint8_t* op = smem + Smem::kRing + ((2 * count + which) % kTreeStages) * Smem::kOperand + place;
+          constexpr int kBatch = 4;
+  #pragma unroll 1
+          for (int k0 = 0; k0 < kPasses; k0 += kBatch) {
+            uint2 w[kBatch][2];
+  #pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const uint8_t* x = st + (k0 + k) * kConvThreads * 16;
+              w[k][0] = *reinterpret_cast<const uint2*>(x);
+              w[k][1] = *reinterpret_cast<const uint2*>(x + st1);
+            }
+            if (k0 + kBatch == kPasses) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&st_free[which]);
+            }
+            if (k0 == 0) room(2 * count + which);
+            uint32_t h[kBatch][8];
+  #pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+  #pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                e4m3x4_to_f16x2x2(w[k][y].x, h[k][4 * y], h[k][4 * y + 1]);
+                e4m3x4_to_f16x2x2(w[k][y].y, h[k][4 * y + 2], h[k][4 * y + 3]);
+              }
+            if (!plain) {
+  #pragma unroll
+              for (int k = 0; k < kBatch; ++k) {
+                const int row = (k0 + k) * kPassRows + cr;
+                const bool seen = info.seen[row >> 5] >> (row & 31) & 1u;  // (what no row sees may be NaN, or not there)
+                const __half2 f2 = __float2half2_rn(which ? info.v_scale[row >> 4] * inv : 1.0f);
+  #pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                  const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[k][x]), f2);
+                  h[k][x] = seen ? *reinterpret_cast<const uint32_t*>(&y) : 0u;
+                }
+              }
+            }
+  #pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              uint8_t* to = op + (k0 + k) * kPassRows * 128;
+              *reinterpret_cast<uint4*>(to + piece0) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
+              *reinterpret_cast<uint4*>(to + (piece0 ^ 16)) = make_uint4(h[k][4], h[k][5], h[k][6], h[k][7]);
+            }
+          }
+          arrive(2 * count + which);
+        };
+        // A new tile, bf16: the largest finite magnitudes first, then fp16 by a power of two each.  Read
+        // twice: what a tile holds would fill the registers (64 of them for K alone).
+        constexpr int kL = HD / 8, kR = kConvThreads / kL, kP = kKeyTile / kR;
+        const int c8 = ct % kL, r8 = ct / kL;
+        auto piece_of = [&](const TreeKeyTile& t, const void* x, int64_t row_stride, int64_t head_stride, int k) {
+          const int b = t.key0 + k * kR + r8;
+          return b < a.slots ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) +
+                                                                    (static_cast<int64_t>(t.req) * a.slots + b) * row_stride +
+                                                                    t.kvh * head_stride + c8 * 8))
+                             : make_uint4(0, 0, 0, 0);
+        };
+        auto largest = [&](const uint4& w, float& top) {  // returns whether something is not finite
+          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+          bool odd = false;
+  #pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float lo = fabsf(__uint_as_float(in[y] << 16)), hi = fabsf(__uint_as_float(in[y] & 0xFFFF0000u));
+            const bool fl = lo <= 3.402823466e38f, fh = hi <= 3.402823466e38f;
+            odd |= !fl || !fh;
+            top = fmaxf(top, fmaxf(fl ? lo : 0.0f, fh ? hi : 0.0f));
+          }
+          return odd;
+        };
+        auto put_new = [&](uint8_t* op, int k, const uint4& w, float inv) {
+          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+          uint32_t h[4];
+  #pragma unroll
+          for (int y = 0; y < 4; ++y)
+            h[y] = pack_f16(__uint_as_float(in[y] << 16) * inv, __uint_as_float(in[y] & 0xFFFF0000u) * inv);
+          put(op, k * kR + r8, c8, make_uint4(h[0], h[1], h[2], h[3]));
+        };
+        auto convert_new = [&](const TreeKeyTile& t, TreeTile& info, int count, float& vref) {
+          float top[2] = {0.0f, 0.0f};
+  #pragma unroll 8
+          for (int k = 0; k < kP; ++k) largest(piece_of(t, a.k_new, a.k_row_stride, a.k_head_stride, k), top[0]);
+  #pragma unroll 8
+          for (int k = 0; k < kP; ++k)
+            // the key's value takes no part in the product, the rows that see it become NaN
+            if (largest(piece_of(t, a.v_new, a.v_row_stride, a.v_head_stride, k), top[1]))
+              atomicOr(&info.bad[(k * kR + r8) >> 5], 1u << ((k * kR + r8) & 31));
+  #pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            top[x] = warp_max(top[x]);
+            if (lane == 0) s_max[x][cw] = top[x];
+          }
+          asm volatile("bar.sync 2, %0;" ::"n"(kConvThreads) : "memory");
+  #pragma unroll
+          for (int x = 0; x < 2; ++x)
+  #pragma unroll
+            for (int k = 0; k < kTreeConvWarps; ++k) top[x] = fmaxf(top[x], s_max[x][k]);
+          asm volatile("bar.sync 2, %0;" ::"n"(kConvThreads) : "memory");
+          const float k_scale = kv_pow2_scale(top[0]);
+          vref = fmaxf(vref, kv_pow2_scale(top[1]));
+          if (ct < 8) info.k_scale[ct] = k_scale;
+          if (ct == 0) info.vref = vref;
+          const float k_inv = 1.0f / k_scale, v_inv = 1.0f / vref;
+          room(2 * count);
+          uint8_t* op = smem + Smem::kRing + ((2 * count) % kTreeStages) * Smem::kOperand;
+  #pragma unroll 8
+          for (int k = 0; k < kP; ++k) put_new(op, k, piece_of(t, a.k_new, a.k_row_stride, a.k_head_stride, k), k_inv);
+          arrive(2 * count);
+          room(2 * count + 1);
+          op = smem + Smem::kRing + ((2 * count + 1) % kTreeStages) * Smem::kOperand;
+  #pragma unroll 8
+          for (int k = 0; k < kP; ++k) {
+            const int row = k * kR + r8;
+            const bool bad = info.bad[row >> 5] >> (row & 31) & 1u;
+            put_new(op, k, bad ? make_uint4(0, 0, 0, 0) : piece_of(t, a.v_new, a.v_row_stride, a.v_head_stride, k), v_inv);
+          }
+          arrive(2 * count + 1);
+        };
+        TreeKeyTile cur;
+        TreeTileWalk tw = {walk, {}, 0};
+        float vref = 0.0f;
+        for (int count = 0; tw.next(p, cur), cur.kind != kTileNone; ++count) {
+          TreeTile& info = tiles[count % kTreeSlots];
+          if (cur.first) vref = 1.17549435e-38f;
+          ok = ok && mbar_wait(&st_full[0], count & 1, nullptr);
+          if (cur.kind == kTileCached) {
+            vref = fmaxf(vref, info.v_top);
+            if (ct == 0) info.vref = vref;
+            const float inv = 1.0f / vref;
+            const bool plain = info.plain, even = vref == info.v_top;
+  #pragma unroll 1
+            for (int which = 0; which < 2; ++which) {
+              if (which) ok = ok && mbar_wait(&st_full[1], count & 1, nullptr);
+              convert(info, count, which, plain && (which == 0 || even), inv);
+            }
+          } else {
+            ok = ok && mbar_wait(&st_full[1], count & 1, nullptr);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&st_free[0]), mbar_arrive(&st_free[1]);
+            convert_new(cur, info, count, vref);
+          }
+        }
+        gave_up = !ok;
       }
-      gave_up = !ok;
     } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeSoftmaxRegs));
       // --- softmax: warpgroup t, a row a thread
       const int t = warp >> 2, r = tid & 127;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;

@@ -14,6 +14,12 @@
 
 namespace dt {
 
+DT_DEVINL float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 constexpr int kSms = 152;  // of a GB300: grids of one wave
 
 // Largest finite e4m3 magnitude: 1.75 * 2^8.

@@ -86,12 +86,6 @@ DT_DEVINL uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-DT_DEVINL float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 DT_DEVINL uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -425,10 +419,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
             const float base = top == -INFINITY ? 0.0f : top;
-            f[k] = fast_exp2(fm[h][k] - base);
+            f[k] = ex2(fm[h][k] - base);
             fm[h][k] = top;
-            e[k] = s0 ? fast_exp2(z0 - base) : 0.0f;
-            e[k + 2] = s1 ? fast_exp2(z1 - base) : 0.0f;
+            e[k] = s0 ? ex2(z0 - base) : 0.0f;
+            e[k + 2] = s1 ? ex2(z1 - base) : 0.0f;
             fl[h][k] = fl[h][k] * f[k] + (e[k] + e[k + 2]);
             if ((s0 && bad >> g & 1u) || (s1 && bad >> (g + 8) & 1u)) fl[h][k] = NAN;
           }
@@ -597,7 +591,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-            f[k] = top == -INFINITY ? 1.0f : fast_exp2(m[h][k] - top);
+            f[k] = top == -INFINITY ? 1.0f : ex2(m[h][k] - top);
             m[h][k] = top;
             l[h][k] *= f[k];
             f[k] *= vratio;
@@ -618,8 +612,8 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const float v_rel = v_scale[x] * vinv;
-          const float e0 = fast_exp2(z[h][x][0] - b0), e1 = fast_exp2(z[h][x][1] - b1);
-          const float e2 = fast_exp2(z[h][x][2] - b0), e3 = fast_exp2(z[h][x][3] - b1);
+          const float e0 = ex2(z[h][x][0] - b0), e1 = ex2(z[h][x][1] - b1);
+          const float e2 = ex2(z[h][x][2] - b0), e3 = ex2(z[h][x][3] - b1);
           l[h][0] += e0 + e2;
           l[h][1] += e1 + e3;
           pb[h][x][0] = transpose8x8(pack_f16(e0 * v_rel, e1 * v_rel));
@@ -679,8 +673,8 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
           sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
           const float fm = with_fresh ? s_m[at] : -INFINITY, fl = with_fresh ? s_l[at] : 0.0f;
           const float top = fmaxf(m[h][k], fm), base = top == -INFINITY ? 0.0f : top;
-          f_old[h][k] = fast_exp2(m[h][k] - base);
-          f_fresh[h][k] = with_fresh ? fast_exp2(fm - base) : 0.0f;
+          f_old[h][k] = ex2(m[h][k] - base);
+          f_fresh[h][k] = with_fresh ? ex2(fm - base) : 0.0f;
           m[h][k] = top;
           l[h][k] = sum * f_old[h][k] + fl * f_fresh[h][k];
           f_old[h][k] *= vref;
@@ -744,7 +738,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
       float4 acc = make_float4(0, 0, 0, 0);
 #pragma unroll
       for (int w = 0; w < kDecodeWarps; ++w) {
-        const float f = fast_exp2(s_m[w * kRows + r] - base);
+        const float f = ex2(s_m[w * kRows + r] - base);
         const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kRows + r) * HD + c);
         sum += s_l[w * kRows + r] * f;
         acc.x += x.x * f, acc.y += x.y * f, acc.z += x.z * f, acc.w += x.w * f;
@@ -788,12 +782,12 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
             }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) high = fmaxf(high, ml[k].x);
-            const float base = high == -INFINITY ? 0.0f : high, f0 = fast_exp2(top - base);
+            const float base = high == -INFINITY ? 0.0f : high, f0 = ex2(top - base);
             sum *= f0;
             acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-              const float f = fast_exp2(ml[k].x - base);
+              const float f = ex2(ml[k].x - base);
               if (x0 + k <= c_last) {
                 sum += ml[k].y * f;
                 acc.x += y[k].x * f, acc.y += y[k].y * f, acc.z += y[k].z * f, acc.w += y[k].w * f;

@@ -15,8 +15,7 @@
 // and may be rescaled, and P(j)'s place free.
 //
 // The maximum in use lags behind the true one by up to 2^8: a row's O is rescaled
-// only where its maximum has grown by more (published for Blackwell attention as
-// conditional rescaling); sums and O stay exact in that unit.
+// only where its maximum has grown by more; sums and O stay exact in that unit.
 #pragma once
 
 #include "kv.cuh"
@@ -25,12 +24,6 @@ namespace dt {
 
 constexpr int kKeyTile = 128;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-DT_DEVINL float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // 32 lanes x 32 consecutive 32-bit columns, without waiting (tmem_wait_ld).
 DT_DEVINL void tmem_ld32(uint32_t taddr, uint32_t* v) {

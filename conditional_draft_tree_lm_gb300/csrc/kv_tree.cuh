@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
   }
   tc_fence_before();
   // (the rows left over, if any, may start on the SMs that this kernel leaves first)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  dt_grid_release();
   const TreeUnits units = {a.max_blocks << p.shift, p.fresh_tiles, p.pairs + p.odd};
   TileRow<128, TreeUnits> row_of = {a.length, a.n_req, units, 0, s_start};
   row_of.sum(scratch);  // (ends with a barrier)

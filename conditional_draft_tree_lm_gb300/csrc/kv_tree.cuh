@@ -437,10 +437,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
               w[k][0] = *reinterpret_cast<const uint2*>(x);
               w[k][1] = *reinterpret_cast<const uint2*>(x + st1);
             }
-            if (k0 + kBatch == kPasses) {
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&st_free[which]);
-            }
             if (k0 == 0) room(2 * count + which);
             uint32_t h[kBatch][8];
   #pragma unroll
@@ -471,6 +467,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             }
           }
           arrive(2 * count + which);
+          // The staging place goes back here, and no earlier: a load from shared memory is certain to have been made when
+          // its value has been used.  (Handed back between the loads and the wait for room, it was overwritten by the
+          // next page's copy now and then before they had read it.)
+          if (lane == 0) mbar_arrive(&st_free[which]);
         };
         // A new tile, bf16: the largest finite magnitudes first, then fp16 by a power of two each.  Read
         // twice: what a tile holds would fill the registers (64 of them for K alone).

@@ -1,0 +1,36 @@
+"""The same bits from the same call, many times over, where a kernel hands shared memory from one role to another."""
+import numpy as np
+import pytest
+
+from tests.test_gpu_kvcache import _t, cache_case, dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("lens,slots,heads,kv,hd,page,fresh", [
+    ([257] * 20, 32, 32, 4, 64, 16, None),
+    ([0, 1, 130, 64, 500, 3, 90, 257], 34, 32, 4, 64, 16, "random"),
+    ([0, 1, 130, 64, 500, 3, 90, 257], 34, 32, 4, 64, 64, "random"),
+    ([0, 1, 130, 64, 500, 3, 90, 257], 34, 32, 4, 64, 128, "random"),
+    ([257] * 20, 32, 32, 4, 128, 64, "tree"),
+    ([700, 20, 0, 33], 129, 32, 8, 128, 32, "random"),
+])
+def test_cache_attention_gives_the_same_bits_every_time(lens, slots, heads, kv, hd, page, fresh):
+    """Stretches of a full key tile and one that holds a few keys, the unseen ones NaN: a page copied over one that is
+    still to be converted shows in the output."""
+    torch = _t()
+    from conditional_draft_tree_lm_gb300 import AttentionWorkspace, cache_attention
+    c = cache_case(np.random.RandomState(slots + hd + page), lens, slots, heads, kv, hd, page, fresh)
+    table, length, work = dev(c["table"], torch.int32), dev(c["lens"], torch.int32), AttentionWorkspace()
+    mask = None if c["mask"] is None else dev(c["mask"], torch.uint8)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    first, first_lse, differ = None, None, torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(200):
+        lse = torch.full((len(lens), slots, heads), 7.0, device="cuda")
+        out = cache_attention(c["cache"], c["q"], table, length, k_new=c["k"], v_new=c["v"], mask=mask, lse=lse, workspace=work,
+                              status=status)
+        if first is None:
+            first, first_lse = out, lse
+        differ += (out.view(torch.int16) != first.view(torch.int16)).sum() + (lse.view(torch.int32) != first_lse.view(torch.int32)).sum()
+    assert status.item() == 0 and differ.item() == 0
+    assert torch.isfinite(first).all()

@@ -82,7 +82,7 @@ struct PromptItem {
 };
 
 constexpr int kItemSlots = 4;
-struct PromptPlace {  // what a slot of the schedule holds
+struct __align__(16) PromptPlace {  // what a slot of the schedule holds
   int kvh, row0, len, pos0;  // len 0: nothing to do, < 0: no more items
 };
 
@@ -191,9 +191,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     bool got = __all_sync(0xFFFFFFFFu, mbar_wait(&item_full[i % kItemSlots], (i / kItemSlots) & 1, nullptr));
     gave_up |= !got;
     PromptPlace x = {0, 0, -1, 0};
-    if (got) x = places[i % kItemSlots];
-    __syncwarp();
-    if (got && lane == 0) mbar_arrive(&item_free[i % kItemSlots]);
+    if (got) {
+      const int4 y = *reinterpret_cast<const int4*>(&places[i % kItemSlots]);
+      x = {y.x, y.y, y.z, y.w};
+    }
+    // (always so: a load from shared memory is certain to have been made when its value has been used, and the place is written again
+    // after the arrival)
+    const bool read = __all_sync(0xFFFFFFFFu, x.len >= -1);
+    if (got && read && lane == 0) mbar_arrive(&item_free[i % kItemSlots]);
     prompt_item(p, x, it);
     return x.len >= 0;
   };
@@ -433,7 +438,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           for (int w = 0; w < 4; ++w)
             if (bad_key[(j - it.masked0) * 4 + w] & first_bits(pos + 1 - j * kKeyTile, w)) row.l = NAN;
       }
-      __syncwarp();
+      // (the vote uses the words, so that they have been read before they are cleared for the next item)
+      if (__ballot_sync(0xFFFFFFFFu, row.l != row.l) >> lane & 1u) row.l = NAN;
       if (lane == 0 && n > 0) mbar_arrive(&told[t]);
       if (n > 0 && ok) {
         const bool live = r < p.group * p.positions && pos < it.len;

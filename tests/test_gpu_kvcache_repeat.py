@@ -34,3 +34,32 @@ def test_cache_attention_gives_the_same_bits_every_time(lens, slots, heads, kv, 
         differ += (out.view(torch.int16) != first.view(torch.int16)).sum() + (lse.view(torch.int32) != first_lse.view(torch.int32)).sum()
     assert status.item() == 0 and differ.item() == 0
     assert torch.isfinite(first).all()
+
+
+def test_prompt_attention_gives_the_same_bits_every_time():
+    """Short and long sequences in turn, infinities and NaNs among the last keys of some: items follow one another in a
+    CTA, and what one notes for its rows is cleared for the next."""
+    torch = _t()
+    from conditional_draft_tree_lm_gb300 import prompt_attention
+    rs = np.random.RandomState(71)
+    for hd in (64, 128):
+        lens = np.concatenate([rs.randint(1, 300, 400), [700, 1500, 0]])
+        rs.shuffle(lens)
+        at = np.concatenate([[0], np.cumsum(lens)])
+        n = int(at[-1])
+        q, k, v = (dev(rs.randn(n, x, hd), torch.bfloat16) for x in (8, 2, 2))
+        finite = np.ones(n, bool)
+        for i in rs.choice(np.nonzero(lens > 1)[0], 150, replace=False):
+            row = rs.randint(max(at[i], at[i + 1] - 20), at[i + 1])
+            v[row, :, rs.randint(hd)] = float(rs.choice([np.nan, np.inf, -np.inf]))
+            finite[row:at[i + 1]] = False
+        start = dev(at, torch.int32)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        first, differ = None, torch.zeros((), dtype=torch.int64, device="cuda")
+        for _ in range(200):
+            out = prompt_attention(q, k, v, start, status=status)
+            first = out if first is None else first
+            differ += (out.isnan() != first.isnan()).sum() + (out.nan_to_num(0) != first.nan_to_num(0)).sum()
+        assert status.item() == 0 and differ.item() == 0
+        seen = torch.isfinite(first).flatten(1).all(1).cpu().numpy()
+        np.testing.assert_array_equal(seen, finite)

@@ -20,6 +20,12 @@ DT_DEVINL float ex2(float x) {
   return y;
 }
 
+DT_DEVINL float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 constexpr int kSms = 152;  // of a GB300: grids of one wave
 
 // Largest finite e4m3 magnitude: 1.75 * 2^8.

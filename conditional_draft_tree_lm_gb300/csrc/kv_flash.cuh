@@ -3,9 +3,9 @@
 //
 // Both keep S = Q K^T (128 rows x 128 keys, fp32) and O (128 rows x head_dim) in
 // tensor memory, one lane a row.  A softmax thread owns a row: it reads its 128
-// logits, writes P as 16-bit pairs over the first half of S's columns, and the
-// next product takes P from there (A from tensor memory) and V from shared memory
-// as it was stored, rows of channels (B, MN-major), so that V is never transposed.
+// logits, writes P as 16-bit pairs over S's columns, and the next product takes P
+// from there (A from tensor memory) and V from shared memory as it was stored, rows
+// of channels (B, MN-major), so that V is never transposed.
 // Two such tiles of rows share every key tile: while one's softmax runs on the
 // ordinary cores, the tensor core does the other's products.
 //
@@ -14,8 +14,9 @@
 // V(j), S(j + 1).  So S(j + 1) being complete tells the softmax that O is at rest
 // and may be rescaled, and P(j)'s place free.
 //
-// The maximum in use lags behind the true one by up to 2^8: a row's O is rescaled
-// only where its maximum has grown by more; sums and O stay exact in that unit.
+// The maximum in use lags behind the true one by up to 2^8: a row's sum (and with it
+// the prompts' O) is rescaled only where its maximum has grown by more; sums and O
+// stay exact in that unit.
 #pragma once
 
 #include "kv.cuh"
@@ -42,6 +43,11 @@ DT_DEVINL void tmem_landed32(uint32_t* v) {
 #pragma unroll
   for (int i = 0; i < 32; i += 8)
     asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7]));
+}
+DT_DEVINL void tmem_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 DT_DEVINL void tmem_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
@@ -89,10 +95,13 @@ DT_DEVINL bool elect_one() {
   return pred != 0;
 }
 
-// kind::f16 with fp32 D; BF16: both operands bf16, else both fp16; b_mn: B is MN-major.
-template <bool BF16>
-DT_HOST_DEVICE_INLINE uint32_t idesc_flash(uint32_t M, uint32_t N, bool b_mn) {
-  return (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((N >> 3) << 17) | ((M >> 4) << 24);
+// What P is: the probabilities in bf16 (prompts); probabilities times their keys' value scales, in fp16 and the row's
+// unit (cached tokens); or the same as the sum of two bf16 (new tokens), see softmax_tile.
+enum { kProbs, kWeights, kWeightPairs };
+
+// kind::f16 with fp32 D; operands in bf16 or both in fp16; b_mn: B is MN-major.
+DT_HOST_DEVICE_INLINE uint32_t idesc_flash(bool bf16, uint32_t M, uint32_t N, bool b_mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
 // A row tile's (or key tile's) operand in shared memory: halves of 64 channels, 128 rows of 128 bytes, swizzled.
@@ -102,33 +111,30 @@ constexpr uint32_t kOperandBytes = HD / 64 * kHalfBytes;
 // S = Q K^T and O (+)= P V of one tile; issued by one lane, with operands that the
 // whole warp has computed (so that they stand in uniform registers: with one lane
 // walking the tiles by itself the issue, not the tensor core, was the bound).
-template <int HD, bool BF16>
-DT_DEVINL void issue_qk(uint32_t s_tmem, uint64_t q, uint64_t k) {
-  const uint32_t idesc = idesc_flash<BF16>(128, kKeyTile, false);
+template <int HD>
+DT_DEVINL void issue_qk(bool bf16, uint32_t s_tmem, uint64_t q, uint64_t k) {
+  const uint32_t idesc = idesc_flash(bf16, 128, kKeyTile, false);
 #pragma unroll
   for (int i = 0; i < HD / 16; ++i) {
     const uint32_t off = ((i >> 2) * kHalfBytes + (i & 3) * 32) >> 4;
     tc_mma_bf16(s_tmem, q + off, k + off, idesc, i != 0);
   }
 }
-template <int HD, bool BF16>  // half 0 or 1 of the keys
-DT_DEVINL void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint64_t v, bool first, int half) {
-  const uint32_t idesc = idesc_flash<BF16>(128, HD, true);
+template <int HD>  // half 0 or 1 of the keys; p: what P is
+DT_DEVINL void issue_pv(int p, uint32_t o_tmem, uint32_t p_tmem, uint64_t v, bool first, int half) {
+  const uint32_t idesc = idesc_flash(p != kWeights, 128, HD, true);
 #pragma unroll
   for (int k = 0; k < kKeyTile / 32; ++k) {
     const int i = half * (kKeyTile / 32) + k;
-    tc_mma_ts(o_tmem, p_tmem + i * 8, v + (i * 2048 >> 4), idesc, !(first && i == 0));
+    const uint32_t at = p_tmem + (p == kWeightPairs ? (i >> 1) * 32 + (i & 1) * 8 : i * 8);
+    tc_mma_ts(o_tmem, at, v + (i * 2048 >> 4), idesc, !(first && i == 0));
+    if (p == kWeightPairs) tc_mma_ts(o_tmem, at + 16, v + (i * 2048 >> 4), idesc, 1u);
   }
 }
 
-// Two probabilities to a 16-bit pair, the first in the low half.
-template <bool BF16>
+// Two numbers to a pair of bf16, the first in the low half.
 DT_DEVINL uint32_t pack_p(float lo, float hi) {
-  if (BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  const __half2 h = __floats2half2_rn(lo, hi);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
@@ -171,6 +177,11 @@ DT_DEVINL uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+DT_DEVINL uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // A warp's 32 rows x 64 channels of bf16, one row a lane (w: 8 pieces of 16 bytes),
 // to global memory through 4 KB of the warp's own shared memory: eight lanes write
@@ -198,24 +209,38 @@ DT_DEVINL int over_group(int y, uint32_t inverse) { return static_cast<int>(stat
 // The running softmax of one row.
 struct SoftmaxRow {
   float m = -INFINITY, l = 0.0f;  // the maximum in use, in powers of two, and the sum in its unit
+  // kWeights, kWeightPairs: O is in units of 2^u, whatever m is; the largest u so far
+  float u = -INFINITY, u_high = -INFINITY;
 };
+// A weight 2^z v of a cached tile (z: logit, v: its key's value scale) is held in fp16 as 2^(z - u) v.  u follows the
+// tiles, up and down: a tile's largest weight stands at 2^0 .. 2^15 (2^8 when u moves), so that what fp16 cannot hold, 2^-25 or
+// less, is that small beside the largest of the same 128 keys, whatever stands in other tiles.  Downwards u stops 60 below its highest
+// value, where O, in 32 bits, might overflow (and what is that small is lost to it all the same).
+constexpr float kUnitTop = 15.0f, kUnitSet = 8.0f, kUnitFall = 60.0f;
+// u >= m - kUnitBelow, so that 2^(m - u) is a number; and u >= m + kUnitNew where new tokens come in, the largest
+// of whose values stay finite in O.
+constexpr float kUnitBelow = 118.0f, kUnitNew = 16.0f;
 
-// One 128-key tile of a row: S at s_at becomes P there, m and l (and O, where the
-// maximum grows or O's unit changes by `ratio`) are brought up to date.  scale(g):
-// what turns a raw logit of keys 16 g .. 16 g + 15 into powers of two, one value
-// for all where UNIFORM; negative: its sign is negative.  see: the row's visible
-// keys, all of them unless MASKED.  ready(i): called when half i of P is stored.
+// One 128-key tile of a row: S at s_at becomes P there, and the row's state (and O, where its unit changes: for
+// kProbs with m) is brought up to date.  scale(g): what turns a raw logit of keys 16 g .. 16 g + 15 into
+// powers of two; value(g), value_log(g): those keys' value scale and its logarithm (kWeights).  All three are asked for
+// two g at a time, by g / 2.  negative: the scale's sign is negative (kProbs only).  see: the row's visible keys, all of them unless MASKED.  ready(i):
+// called when half i of P is stored.
+// kWeightPairs: a weight goes to the product as the sum of two bf16 (its first 8 bits, cut off, and the rest
+// rounded: 2^-16 relative), since a new token's values come in bf16, which fp16 cannot hold beside each other.  The
+// pair stands in the 32 columns that its keys' logits leave, first parts before rests.
 // S is read twice, 32 columns ahead of their use, and both loops are rolled up: with
 // several roles' code running at once, instruction fetches count (S in 128 registers
 // between the maximum and the exponentials, loops unrolled: 48 prompts of up to 1k
 // tokens 300 us instead of 272, 16k tokens 1380 instead of 1367).  One body for
 // masked tiles and others costs more than it saves there: 288 and 1650 us.
-template <int HD, bool BF16, bool UNIFORM, bool MASKED, class Scale, class Ready>
-DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float ratio, bool negative, Scale scale,
+template <int HD, int P, bool MASKED, class Scale, class Value, class ValueLog, class Ready>
+DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, bool negative, Scale scale, Value value, ValueLog value_log,
                             const uint32_t (&see)[4], SoftmaxRow& row, Ready ready) {
+  constexpr bool SPLIT = P == kWeightPairs;
   uint32_t s[64];
   tmem_ld32(s_at, s);
-  float top = -INFINITY;
+  float top = -INFINITY, top_weight = -INFINITY;
 #pragma unroll 1
   for (int w2 = 0; w2 < 4; w2 += 2)
 #pragma unroll
@@ -225,8 +250,9 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
     tmem_wait_ld();
     tmem_landed32(v);
     tmem_ld32(s_at + 32 * ((w + 1) & 3), s + 32 * (w1 ^ 1));  // (the last one: the first, for the second reading)
+    const float2 scale2 = scale(w), log2v = P == kWeights ? value_log(w) : make_float2(0.0f, 0.0f);
     if (MASKED) {
-      const uint32_t out = negative ? 0x7F800000u : 0xFF800000u;
+      const uint32_t out = P == kProbs && negative ? 0x7F800000u : 0xFF800000u;
       const uint32_t bits = w1 == 0 ? (w2 == 0 ? see[0] : see[2]) : (w2 == 0 ? see[1] : see[3]);
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = bits >> i & 1u ? v[i] : out;
@@ -234,7 +260,7 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float a = __uint_as_float(v[16 * h]), b = __uint_as_float(v[16 * h + 1]);
-      if (!negative) {
+      if (P != kProbs || !negative) {
 #pragma unroll
         for (int i = 2; i < 16; i += 4) {
           a = fmaxf(fmaxf(a, __uint_as_float(v[16 * h + i])), __uint_as_float(v[16 * h + i + 1]));
@@ -246,18 +272,41 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
         for (int i = 2; i < 16; ++i) a = fminf(a, __uint_as_float(v[16 * h + i]));
         a = fminf(a, b);
       }
-      const float c = scale(UNIFORM ? 0 : 2 * w + h);
-      top = fmaxf(top, c == 0.0f ? 0.0f : a * c);
+      // (the maximum passes over a NaN, as an unseen -inf times a scale of zero is)
+      const float c = h ? scale2.y : scale2.x;
+      top = fmaxf(top, a * c);
+      if (P == kWeights) top_weight = fmaxf(top_weight, fmaf(a, c, h ? log2v.y : log2v.x));
     }
   }
-  // (a tile of which the row sees nothing has top = -inf, or 0 with a scale of zero: no harm, P is 0)
-  if (__any_sync(0xFFFFFFFFu, top > row.m + 8.0f || ratio != 1.0f)) {
+  // (a tile of which the row sees nothing has top = -inf: no harm, P is 0)
+  bool moves = top > row.m + 8.0f;
+  if (P == kWeights)
+    moves |= top_weight > row.u + kUnitTop ||
+             (top_weight < row.u && top_weight > -INFINITY && fmaxf(top_weight - kUnitSet, row.u_high - kUnitFall) < row.u);
+  if (P == kWeightPairs) moves |= row.u < row.m + kUnitNew;
+  if (__any_sync(0xFFFFFFFFu, moves)) {
     const float m2 = fmaxf(row.m, top), f = m2 == -INFINITY ? 1.0f : ex2(row.m - m2);
-    tmem_wait_ld();  // (s is on its way; the rescaling waits for its own)
-    if (!first) rescale_o<HD>(o_at, f * ratio);
     row.l *= f;
     row.m = m2;
+    float f_o = f;
+    bool o_moves = true;
+    if (P != kProbs) {
+      float u2 = row.u;
+      if (P == kWeights) {
+        if (top_weight > -INFINITY && (top_weight > u2 + kUnitTop || top_weight < u2)) u2 = fmaxf(top_weight - kUnitSet, row.u_high - kUnitFall);
+        u2 = fmaxf(u2, m2 - kUnitBelow);
+      } else {
+        u2 = fmaxf(u2, m2 + kUnitNew);
+      }
+      o_moves = __any_sync(0xFFFFFFFFu, u2 != row.u);
+      f_o = u2 == row.u ? 1.0f : ex2(row.u - u2);
+      row.u = u2;
+      row.u_high = fmaxf(row.u_high, u2);
+    }
+    tmem_wait_ld();  // (s is on its way; the rescaling waits for its own)
+    if (!first && o_moves) rescale_o<HD>(o_at, f_o);
   }
+  const float unit = P == kProbs || row.u == -INFINITY ? 1.0f : ex2(row.m - row.u);
   const float base = row.m == -INFINITY ? 0.0f : row.m;
   const uint64_t base2 = f32x2(-base, -base);
   uint64_t sum[2] = {0, 0};
@@ -268,6 +317,7 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
     const int w = w2 + w1;
     uint32_t pk[16];
     uint32_t* v = s + 32 * w1;
+    const uint32_t p_at = s_at + (SPLIT ? 32 : 16) * w;
     tmem_wait_ld();
     tmem_landed32(v);
     if (w1 == 0 || w2 == 0) tmem_ld32(s_at + 32 * (w + 1), s + 32 * (w1 ^ 1));
@@ -278,10 +328,14 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
     if (none) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) pk[i] = 0u;
+      if (SPLIT) tmem_st16(p_at + 16, pk);
     } else {
+      const float2 scale2 = scale(w);
+      float2 f2 = P == kWeights ? value(w) : make_float2(1.0f, 1.0f);
+      f2.x *= unit, f2.y *= unit;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float c = scale(UNIFORM ? 0 : 2 * w + (i >> 3));
+        const float c = i < 8 ? scale2.x : scale2.y, f = i < 8 ? f2.x : f2.y;
         float e0, e1;
         f32x2_parts(fma2(f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f32x2(c, c), base2), e0, e1);
         e0 = ex2(e0);
@@ -290,12 +344,31 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, float rati
           e0 = bits >> (2 * i) & 1u ? e0 : 0.0f;
           e1 = bits >> (2 * i + 1) & 1u ? e1 : 0.0f;
         }
-        sum[i & 1] = add2(sum[i & 1], f32x2(e0, e1));
-        pk[i] = pack_p<BF16>(e0, e1);
+        const uint64_t e = f32x2(e0, e1);
+        sum[i & 1] = add2(sum[i & 1], e);
+        if (P == kProbs) {
+          pk[i] = pack_p(e0, e1);
+        } else if (P == kWeights) {
+          float w0, w1;
+          f32x2_parts(mul2(e, f32x2(f, f)), w0, w1);
+          const __half2 h = __floats2half2_rn(w0, w1);
+          pk[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          float w0, w1, r0, r1;
+          f32x2_parts(mul2(e, f32x2(f, f)), w0, w1);
+          const uint32_t b0 = __float_as_uint(w0), b1 = __float_as_uint(w1);
+          f32x2_parts(add2(f32x2(w0, w1), f32x2(__uint_as_float(b0 & 0xFFFF0000u ^ 0x80000000u), __uint_as_float(b1 & 0xFFFF0000u ^ 0x80000000u))), r0, r1);
+          pk[i & 7] = __byte_perm(b0, b1, 0x7632);
+          pk[8 + (i & 7)] = pack_p(r0, r1);
+          if ((i & 7) == 7) {
+            tmem_st8(p_at + (i & 8), pk);
+            tmem_st8(p_at + 16 + (i & 8), pk + 8);
+          }
+        }
       }
     }
-    // (P's columns 16 w .. lie before those of S that are still to be read, 32 (w + 1) ..)
-    tmem_st16(s_at + 16 * w, pk);
+    // (P's columns end before those of S that are still to be read, 32 (w + 1) ..)
+    if (!SPLIT || none) tmem_st16(p_at, pk);
     if (w1 == 1) {
       tmem_wait_st();
       tc_fence_before();

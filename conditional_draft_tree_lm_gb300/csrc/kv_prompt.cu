@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (it.n_tiles[t] == 0) continue;
           wait(&q_full[t], q_use[t]++ & 1);
           if (!ok) break;
-          if (leader) issue_qk<HD, true>(tmem + t * 128, q_desc[t], kd);
+          if (leader) issue_qk<HD>(true, tmem + t * 128, q_desc[t], kd);
           commit(&s_full[t]);
           if (it.n_tiles[t] == 1) commit(&q_free[t]);
         }
@@ -290,12 +290,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (!ok || j >= it.n_tiles[t]) continue;
             const uint32_t turn = p_use[t]++ & 1;
             wait(&p_full[2 * t], turn);
-            if (ok && leader) issue_pv<HD, true>(tmem + 256 + t * 128, tmem + t * 128, vd, j == 0, 0);
+            if (ok && leader) issue_pv<HD>(kProbs, tmem + 256 + t * 128, tmem + t * 128, vd, j == 0, 0);
             wait(&p_full[2 * t + 1], turn);
             if (!ok) continue;
-            if (leader) issue_pv<HD, true>(tmem + 256 + t * 128, tmem + t * 128, vd, j == 0, 1);
+            if (leader) issue_pv<HD>(kProbs, tmem + 256 + t * 128, tmem + t * 128, vd, j == 0, 1);
             if (j + 1 < it.n_tiles[t]) {
-              if (leader) issue_qk<HD, true>(tmem + t * 128, q_desc[t], kd);
+              if (leader) issue_qk<HD>(true, tmem + t * 128, q_desc[t], kd);
               commit(&s_full[t]);
               if (j + 2 == it.n_tiles[t]) commit(&q_free[t]);
             } else {
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const float c = p.c;
     int s_use = 0, o_use = 0;
     bool ok = true;
-    auto scale = [&](int) { return c; };
+    auto scale = [&](int) { return make_float2(c, c); };
     auto ready = [&](int half) {
       if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
     };
@@ -425,9 +425,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int seen = pos + 1 - j * kKeyTile;  // of this tile's keys, by this row
         const uint32_t see[4] = {first_bits(seen, 0), first_bits(seen, 1), first_bits(seen, 2), first_bits(seen, 3)};
         if ((j + 1) * kKeyTile > from + 1)
-          softmax_tile<HD, true, true, true>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
+          softmax_tile<HD, kProbs, true>(s_at, o_at, j == 0, c < 0.0f, scale, scale, scale, see, row, ready);
         else
-          softmax_tile<HD, true, true, false>(s_at, o_at, j == 0, 1.0f, c < 0.0f, scale, see, row, ready);
+          softmax_tile<HD, kProbs, false>(s_at, o_at, j == 0, c < 0.0f, scale, scale, scale, see, row, ready);
       }
       if (n > 0) {
         ok = ok && mbar_wait(&o_full[t], o_use++ & 1, nullptr);
@@ -455,10 +455,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           uint4 w[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            w[k].x = pack_p<true>(__uint_as_float(v[8 * k]) * inv, __uint_as_float(v[8 * k + 1]) * inv);
-            w[k].y = pack_p<true>(__uint_as_float(v[8 * k + 2]) * inv, __uint_as_float(v[8 * k + 3]) * inv);
-            w[k].z = pack_p<true>(__uint_as_float(v[8 * k + 4]) * inv, __uint_as_float(v[8 * k + 5]) * inv);
-            w[k].w = pack_p<true>(__uint_as_float(v[8 * k + 6]) * inv, __uint_as_float(v[8 * k + 7]) * inv);
+            w[k].x = pack_p(__uint_as_float(v[8 * k]) * inv, __uint_as_float(v[8 * k + 1]) * inv);
+            w[k].y = pack_p(__uint_as_float(v[8 * k + 2]) * inv, __uint_as_float(v[8 * k + 3]) * inv);
+            w[k].z = pack_p(__uint_as_float(v[8 * k + 4]) * inv, __uint_as_float(v[8 * k + 5]) * inv);
+            w[k].w = pack_p(__uint_as_float(v[8 * k + 6]) * inv, __uint_as_float(v[8 * k + 7]) * inv);
           }
           store_rows(smem + Smem::kOut + warp * 4096, w, [&](int z) -> __nv_bfloat16* {
             const int y = (warp & 3) * 32 + z, ys = over_group(y, p.inverse), at = from + ys;

@@ -15,22 +15,23 @@
 // Cached keys and values come to shared memory as fp16 (e4m3 is exact in it): one
 // warp looks up page numbers and scales and fetches whole pages a tile ahead (a
 // page of a head is contiguous: one bulk copy), four converting warps turn them
-// into the layout that the products read.  What a page's scale would change stays exact in 32 bits: the
-// key's scale multiplies the logit, the value's is folded into V relative to the
-// largest scale so far, O being in units of that one (exact for powers of two).
-// Q is brought to fp16 by a power of two per row, new keys and values by one per
-// tile.  fp16 keeps 11 bits of P where bf16 would keep 8.
+// into the layout that the products read.  Scales stay in 32 bits: the key's multiplies the logit, the value's the weight,
+// which the product takes in fp16 (11 bits of P where bf16 would keep 8) and a unit of the row's own (kv_flash.cuh).  Q comes to fp16 by a
+// power of two per row (exact to 2^-40 of the row's maximum).  New tokens are bf16, whose range fp16 has not, and taken as they
+// are: Q is laid out once more in bf16 before a stretch's first tile of them, under the last product with P, and P is the
+// sum of two bf16.  So nothing shares a power of two with what only stands beside it (with one for all of a tile's new
+// tokens, an unseen one of 1e30 wiped out the others).  With bf16 throughout and P as two bf16 in every tile the
+// wide tree took 417 to 457 us, with that for new tiles only but Q and K in bf16 everywhere some 35 us more than now.
 //
 // Split.  The work is the list of (key/value head, request, row tiles, key tile),
-// cut into equal pieces, one for each SM.  A tile of new keys counts kNewCost times
-// (it is read and reduced before it can be converted: some 18 000 cycles against
-// 4 400).  A stretch that several pieces share is joined by the CTA that finishes
+// cut into equal pieces, one for each SM.  A tile of new keys counts kNewCost times,
+// for itself and for what the end of a stretch costs.  A stretch that several pieces share is joined by the CTA that finishes
 // last, in the order of keys.
 //
 // Measured: 32 trees of 65 slots (4 rows of each head streamed by the other kernel)
-// over up to 4k cached tokens, 32 heads over 8, 218 us; one of 513 slots over 32k 325
-// us, 0.85 PFLOP/s.  Where the time goes: the products 2048 cycles of a pair of row
-// tiles' 4 400 a key tile, the rest the softmax between them and shared memory (Q, K
+// over up to 4k cached tokens, 32 heads over 8, 210 us; one of 513 slots over 32k 335
+// us, 0.82 PFLOP/s.  Where the time goes: the products 2048 cycles of a pair of row
+// tiles' 4 600 a key tile, the rest the softmax between them and shared memory (Q, K
 // and V are read by both tiles' products, and written by the conversion); and what a
 // stretch costs besides, its Q and its join, some 30 000 cycles, two or three times
 // a CTA.  Reading the next stretch's Q and new tokens into L2 ahead changes nothing.
@@ -64,7 +65,9 @@ struct TreeParams {
   float* part;      // [2 * pieces][2 tiles][HD / 4][128][4], then [2 * pieces][2][128][2]
 };
 
-constexpr int kNewCost = 5;  // (of 3, 4, 5: 221, 215, 218 us for 32 trees, 337, 334, 325 us for the wide one)
+// (2, 3, 4, 5, 6: 220, 213, 219, 209, 209 us for 32 trees, 328, 324, 324, 335, 340 for the wide one, 80, 74, 57, 55, 60 for
+// 4 trees over 4k tokens)
+constexpr int kNewCost = 5;
 
 // What a row tile or a pair of them costs over a request's keys, at least 1.
 DT_DEVINL int tree_cost(int len, int max_len, int fresh) {
@@ -121,9 +124,14 @@ struct TreeWalk {
 };
 
 // Walks a piece's key tiles, segment after segment.
+// Which of a stretch's key tiles is the first of new tokens (0 and less: all of them are).
+DT_DEVINL int first_new_tile(const TreeParams& p, const TreeSegment& s) {
+  return p.a.k_new ? s.cached - s.key_begin : 1 << 30;
+}
+
 enum { kTileNone = 0, kTileCached = 1, kTileNew = 2 };
 struct TreeKeyTile {
-  int kind, first;           // first: of its segment
+  int kind;
   int key0, req, kvh, len;   // key0: its first cached token, or new token
 };
 struct TreeTileWalk {
@@ -132,14 +140,12 @@ struct TreeTileWalk {
   int key;
   DT_DEVINL void next(const TreeParams& p, TreeKeyTile& t) {
     t.kind = kTileNone;
-    t.first = 0;
     while (sg.tiles == 0 || key >= sg.key_end) {
       if (!walk.next(p, sg)) {
         sg.tiles = 0;
         return;
       }
       key = sg.key_begin;
-      t.first = 1;
     }
     // (a request without a key at all still has a tile: a cached one of no tokens)
     const bool fresh = p.a.k_new && key >= sg.cached;
@@ -165,18 +171,22 @@ struct TreeSmem {
   static constexpr uint32_t kQ = 0, kRing = 2 * kOperand, kStaging = kRing + kTreeStages * kOperand;
   static constexpr uint32_t kStagingBytes = 2 * kKeyTile * HD;  // K, V: [key][channel] in 8 bits
   static constexpr uint32_t kBars = kStaging + kStagingBytes;
-  static constexpr uint32_t kBytes = kBars + 512 + 1024;  // + alignment
+  static constexpr uint32_t kBytes = kBars + 768 + 1024;  // barriers and tiles' notes (720), alignment
 };
 
 // What goes with a key tile.
-struct TreeTile {
-  float k_scale[8], v_scale[8];  // of 16 keys each
+struct alignas(8) TreeTile {
+  float k_scale[8], v_scale[8], v_log[8];  // of 16 keys each, and the value scale's logarithm
   uint32_t seen[4];   // cached keys that exist (new ones: the keys below slots)
   uint32_t bad[4];    // keys whose values are not finite (new ones only)
-  float v_top;        // the largest v_scale
-  int plain;          // all keys exist, all v_scale are v_top
-  float vref;         // the unit of values, and so of O, from this tile on
+  int plain;          // all keys exist
 };
+
+// 16 bytes of global memory to shared memory, without a register; zeros where not `there`.
+DT_DEVINL void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+DT_DEVINL void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 DT_DEVINL int by_group(const TreeParams& p, int y) { return over_group(y, p.inverse); }
 
@@ -196,7 +206,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
   TreeTile* tiles = reinterpret_cast<TreeTile*>(st_free + 2);  // [kTreeSlots]
   __shared__ uint32_t tmem_slot;
   __shared__ int scratch[4], s_start[128 + 1], s_last;
-  __shared__ float s_max[2][kTreeConvWarps];
 
   // (the same for a warp's lanes, and known to be)
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
@@ -252,7 +261,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
       if (warp == kTreeMmaWarp) {
         const bool leader = elect_one();
         int count = 0;  // key tiles so far
-        int p_use[2] = {0, 0};
+        int p_use[2] = {0, 0}, q_use[2] = {0, 0};
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
           ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, nullptr));
@@ -264,33 +273,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
           if (leader) tc_commit(bar);
         };
         const uint64_t q_desc[2] = {flash_desc(q_s, false), flash_desc(q_s + Smem::kOperand, false)};
-        auto pv = [&](int t, int i, bool first, bool last) {  // ring entry i into O of slot t
+        auto pv = [&](int t, int i, bool fresh, bool first, bool last) {  // ring entry i into O of slot t
           const uint32_t turn = p_use[t]++ & 1;
           const uint64_t vd = flash_desc(at(i), true);
           wait(&p_full[2 * t], turn);
-          if (ok && leader) issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, vd, first, 0);
+          if (ok && leader) issue_pv<HD>(fresh ? kWeightPairs : kWeights, tmem + 256 + t * 128, tmem + t * 128, vd, first, 0);
           wait(&p_full[2 * t + 1], turn);
-          if (ok && leader) issue_pv<HD, false>(tmem + 256 + t * 128, tmem + t * 128, vd, first, 1);
+          if (ok && leader) issue_pv<HD>(fresh ? kWeightPairs : kWeights, tmem + 256 + t * 128, tmem + t * 128, vd, first, 1);
           if (ok && last) commit(&o_full[t]);
         };
-        auto qk = [&](int t, int i) {
+        auto qk = [&](int t, int i, bool fresh, bool new_q) {  // new_q: Q of slot t is laid out (again) for this tile
+          if (new_q) wait(&q_full[t], q_use[t]++ & 1);
           if (!ok) return;
-          if (leader) issue_qk<HD, false>(tmem + t * 128, q_desc[t], flash_desc(at(i), false));
+          if (leader) issue_qk<HD>(fresh, tmem + t * 128, q_desc[t], flash_desc(at(i), false));
           commit(&s_full[t]);
         };
         auto release = [&](int i) {
           if (ok) commit(&empty[i % kTreeStages]);
         };
-        for (int seg = 0; ok && walk.next(p, sg);) {
+        while (ok && walk.next(p, sg)) {
           const int n = sg.key_end - sg.key_begin;
           if (n == 0) continue;
-          wait(&q_full[0], seg & 1);
-          wait(&q_full[1], seg & 1);
-          ++seg;
+          const int first_new = first_new_tile(p, sg);
           full_wait(2 * count);
-          qk(0, 2 * count);
+          qk(0, 2 * count, first_new <= 0, true);
           if (sg.tiles == 2) {
-            qk(1, 2 * count);
+            qk(1, 2 * count, first_new <= 0, true);
             release(2 * count);
             for (int j = 0; j < n && ok; ++j, ++count) {
               const int vi = 2 * count + 1, ki = vi + 1;
@@ -299,8 +307,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
               if (more) full_wait(ki);
   #pragma unroll
               for (int t = 0; t < 2; ++t) {
-                pv(t, vi, j == 0, !more);
-                if (more) qk(t, ki);
+                pv(t, vi, j >= first_new, j == 0, !more);
+                if (more) qk(t, ki, j + 1 >= first_new, j + 1 == first_new);
               }
               release(vi);
               if (more) release(ki);
@@ -316,11 +324,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
                 const int vi = 2 * (count + j) + 1, ki = vi + 1;
                 if (j + 1 < n) {
                   full_wait(ki);
-                  qk(t ^ 1, ki);
+                  qk(t ^ 1, ki, j + 1 >= first_new, j == 0 || (j + 1 >= first_new && j - 1 < first_new));
                   release(ki);
                 }
                 full_wait(vi);
-                pv(t, vi, j0 == 0, j + 2 >= n);
+                pv(t, vi, j >= first_new, j0 == 0, j + 2 >= n);
                 release(vi);
               }
             }
@@ -371,10 +379,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             if (!ok) break;
             // (the place is free: the tile four before this one is behind its softmax, too)
             if (which == 0) {
-              const float v_top = warp_max(lane < 8 ? gc.vs : 0.0f);
-              const bool plain = __all_sync(0xFFFFFFFFu, lane >= 8 || (gc.id >= 0 && gc.vs == v_top)) && cur.len - cur.key0 >= kKeyTile;
-              if (lane < 8) info.k_scale[lane] = gc.ks, info.v_scale[lane] = gc.vs;
-              if (lane == 0) info.v_top = v_top, info.plain = plain;
+              const bool plain = __all_sync(0xFFFFFFFFu, lane >= 8 || gc.id >= 0) && cur.len - cur.key0 >= kKeyTile;
+              if (lane < 8) info.k_scale[lane] = gc.ks, info.v_scale[lane] = gc.vs, info.v_log[lane] = lg2(gc.vs);
+              if (lane == 0) info.plain = plain;
               if (lane < 4) {
                 const uint32_t two = there >> (2 * lane);
                 info.seen[lane] = cur.kind == kTileNew ? first_bits(a.slots - cur.key0, lane)
@@ -403,11 +410,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         constexpr int kLanes = HD / 16;               // threads of a key's row (16 bytes each)
         constexpr int kPassRows = kConvThreads / kLanes;
         constexpr int kPasses = kKeyTile / kPassRows;  // pieces of a thread
-        const int ct = tid - kTreeConvWarp * 32, cw = ct >> 5, cc = ct % kLanes, cr = ct / kLanes;
-        // 8 halves to their place: key `row`, channels 8 * chunk .. (the swizzle: a row's 16-byte pieces by row % 8)
-        auto put = [&](uint8_t* op, int row, int chunk, const uint4& w) {
-          *reinterpret_cast<uint4*>(op + (chunk >> 3) * kHalfBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) = w;
-        };
+        const int ct = tid - kTreeConvWarp * 32, cc = ct % kLanes, cr = ct / kLanes;
         auto arrive = [&](int i) {
           fence_proxy_async_smem();
           __syncwarp();
@@ -423,8 +426,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         const int place = (chunk0 >> 3) * kHalfBytes + cr * 128, piece0 = ((chunk0 & 7) ^ (cr & 7)) << 4;
         const uint8_t* st0 = smem + Smem::kStaging + ct * 16 + (swap ? 8 : 0);
         const int st1 = swap ? -8 : 8;
-        // (passes are multiples of 8 rows apart: the swizzle is the same; plain: neither masks nor factors)
-        auto convert = [&](const TreeTile& info, int count, int which, bool plain, float inv) {
+        // (passes are multiples of 8 rows apart: the swizzle is the same)
+        auto convert = [&](const TreeTile& info, int count, int which) {
+          const bool plain = info.plain;
           const uint8_t* st = st0 + which * kKeyTile * HD;
           uint8_t* op = smem + Smem::kRing + ((2 * count + which) % kTreeStages) * Smem::kOperand + place;
           constexpr int kBatch = 4;
@@ -451,12 +455,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
               for (int k = 0; k < kBatch; ++k) {
                 const int row = (k0 + k) * kPassRows + cr;
                 const bool seen = info.seen[row >> 5] >> (row & 31) & 1u;  // (what no row sees may be NaN, or not there)
-                const __half2 f2 = __float2half2_rn(which ? info.v_scale[row >> 4] * inv : 1.0f);
   #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                  const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[k][x]), f2);
-                  h[k][x] = seen ? *reinterpret_cast<const uint32_t*>(&y) : 0u;
-                }
+                for (int x = 0; x < 8; ++x) h[k][x] = seen ? h[k][x] : 0u;
               }
             }
   #pragma unroll
@@ -472,99 +472,59 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
           // next page's copy now and then before they had read it.)
           if (lane == 0) mbar_arrive(&st_free[which]);
         };
-        // A new tile, bf16: the largest finite magnitudes first, then fp16 by a power of two each.  Read
-        // twice: what a tile holds would fill the registers (64 of them for K alone).
-        constexpr int kL = HD / 8, kR = kConvThreads / kL, kP = kKeyTile / kR;
+        // A new tile, bf16 as it comes, all of it in flight at once.  Values that are not finite become zeros and
+        // their keys are noted, for the rows that see them: before K is handed over, since S tells the softmax that
+        // the notes are there.
+        constexpr int kL = HD / 8, kR = kConvThreads / kL, kP = kKeyTile / kR;  // threads of a row, rows at a time, pieces of a thread
         const int c8 = ct % kL, r8 = ct / kL;
-        auto piece_of = [&](const TreeKeyTile& t, const void* x, int64_t row_stride, int64_t head_stride, int k) {
-          const int b = t.key0 + k * kR + r8;
-          return b < a.slots ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) +
-                                                                    (static_cast<int64_t>(t.req) * a.slots + b) * row_stride +
-                                                                    t.kvh * head_stride + c8 * 8))
-                             : make_uint4(0, 0, 0, 0);
-        };
-        auto largest = [&](const uint4& w, float& top) {  // returns whether something is not finite
-          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-          bool odd = false;
+        auto convert_new = [&](const TreeKeyTile& t, TreeTile& info, int count) {
+          // (rows are multiples of 8 apart: the swizzle is the same)
+          const uint32_t place_new = (c8 >> 3) * kHalfBytes + r8 * 128 + (((c8 & 7) ^ (r8 & 7)) << 4);
+          uint8_t* op[2];
   #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float lo = fabsf(__uint_as_float(in[y] << 16)), hi = fabsf(__uint_as_float(in[y] & 0xFFFF0000u));
-            const bool fl = lo <= 3.402823466e38f, fh = hi <= 3.402823466e38f;
-            odd |= !fl || !fh;
-            top = fmaxf(top, fmaxf(fl ? lo : 0.0f, fh ? hi : 0.0f));
+          for (int which = 0; which < 2; ++which) {
+            const int64_t row_stride = which ? a.v_row_stride : a.k_row_stride;
+            const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(which ? a.v_new : a.k_new) + t.kvh * (which ? a.v_head_stride : a.k_head_stride) + c8 * 8;
+            op[which] = smem + Smem::kRing + ((2 * count + which) % kTreeStages) * Smem::kOperand + place_new;
+            room(2 * count + which);
+  #pragma unroll 4
+            for (int k = 0; k < kP; ++k) {
+              const int b = t.key0 + k * kR + r8;
+              copy16(smem_u32(op[which] + k * kR * 128), x + (static_cast<int64_t>(t.req) * a.slots + min(b, a.slots - 1)) * row_stride, b < a.slots);
+            }
           }
-          return odd;
-        };
-        auto put_new = [&](uint8_t* op, int k, const uint4& w, float inv) {
-          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-          uint32_t h[4];
-  #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            h[y] = pack_f16(__uint_as_float(in[y] << 16) * inv, __uint_as_float(in[y] & 0xFFFF0000u) * inv);
-          put(op, k * kR + r8, c8, make_uint4(h[0], h[1], h[2], h[3]));
-        };
-        auto convert_new = [&](const TreeKeyTile& t, TreeTile& info, int count, float& vref) {
-          float top[2] = {0.0f, 0.0f};
-  #pragma unroll 8
-          for (int k = 0; k < kP; ++k) largest(piece_of(t, a.k_new, a.k_row_stride, a.k_head_stride, k), top[0]);
-  #pragma unroll 8
-          for (int k = 0; k < kP; ++k)
-            // the key's value takes no part in the product, the rows that see it become NaN
-            if (largest(piece_of(t, a.v_new, a.v_row_stride, a.v_head_stride, k), top[1]))
-              atomicOr(&info.bad[(k * kR + r8) >> 5], 1u << ((k * kR + r8) & 31));
-  #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            top[x] = warp_max(top[x]);
-            if (lane == 0) s_max[x][cw] = top[x];
-          }
-          asm volatile("bar.sync 2, %0;" ::"n"(kConvThreads) : "memory");
-  #pragma unroll
-          for (int x = 0; x < 2; ++x)
-  #pragma unroll
-            for (int k = 0; k < kTreeConvWarps; ++k) top[x] = fmaxf(top[x], s_max[x][k]);
-          asm volatile("bar.sync 2, %0;" ::"n"(kConvThreads) : "memory");
-          const float k_scale = kv_pow2_scale(top[0]);
-          vref = fmaxf(vref, kv_pow2_scale(top[1]));
-          if (ct < 8) info.k_scale[ct] = k_scale;
-          if (ct == 0) info.vref = vref;
-          const float k_inv = 1.0f / k_scale, v_inv = 1.0f / vref;
-          room(2 * count);
-          uint8_t* op = smem + Smem::kRing + ((2 * count) % kTreeStages) * Smem::kOperand;
-  #pragma unroll 8
-          for (int k = 0; k < kP; ++k) put_new(op, k, piece_of(t, a.k_new, a.k_row_stride, a.k_head_stride, k), k_inv);
-          arrive(2 * count);
-          room(2 * count + 1);
-          op = smem + Smem::kRing + ((2 * count + 1) % kTreeStages) * Smem::kOperand;
-  #pragma unroll 8
+          copies_landed();
+  #pragma unroll 4
           for (int k = 0; k < kP; ++k) {
-            const int row = k * kR + r8;
-            const bool bad = info.bad[row >> 5] >> (row & 31) & 1u;
-            put_new(op, k, bad ? make_uint4(0, 0, 0, 0) : piece_of(t, a.v_new, a.v_row_stride, a.v_head_stride, k), v_inv);
+            uint4* at = reinterpret_cast<uint4*>(op[1] + k * kR * 128);
+            const uint4 w = *at;
+            // (an exponent of ones carries into its half's top bit)
+            const uint32_t odd = ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+                                 ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+            if (odd & 0x80008000u) {
+              *at = make_uint4(0, 0, 0, 0);
+              atomicOr(&info.bad[(k * kR + r8) >> 5], 1u << ((k * kR + r8) & 31));
+            }
           }
+          arrive(2 * count);
           arrive(2 * count + 1);
         };
         TreeKeyTile cur;
         TreeTileWalk tw = {walk, {}, 0};
-        float vref = 0.0f;
         for (int count = 0; tw.next(p, cur), cur.kind != kTileNone; ++count) {
           TreeTile& info = tiles[count % kTreeSlots];
-          if (cur.first) vref = 1.17549435e-38f;
           ok = ok && mbar_wait(&st_full[0], count & 1, nullptr);
           if (cur.kind == kTileCached) {
-            vref = fmaxf(vref, info.v_top);
-            if (ct == 0) info.vref = vref;
-            const float inv = 1.0f / vref;
-            const bool plain = info.plain, even = vref == info.v_top;
   #pragma unroll 1
             for (int which = 0; which < 2; ++which) {
               if (which) ok = ok && mbar_wait(&st_full[1], count & 1, nullptr);
-              convert(info, count, which, plain && (which == 0 || even), inv);
+              convert(info, count, which);
             }
           } else {
             ok = ok && mbar_wait(&st_full[1], count & 1, nullptr);
             __syncwarp();
             if (lane == 0) mbar_arrive(&st_free[0]), mbar_arrive(&st_free[1]);
-            convert_new(cur, info, count, vref);
+            convert_new(cur, info, count);
           }
         }
         gave_up = !ok;
@@ -591,49 +551,55 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         const bool live = r < p.per_tile * p.group && slot < a.slots;
         const int64_t row = static_cast<int64_t>(sg.req) * a.slots + slot;
         SoftmaxRow sm;
-        float vref = 0.0f;
-        {
-          // Q to fp16 by a power of two of the row's own: HD / 8 lanes read a row together
-          float c = 0.0f;
-          if (n > 0) {
-            constexpr int kL = HD / 8, kR = 32 / kL, kN = 32 / kR;  // lanes of a row, rows at a time, times
-            uint8_t* op = smem + Smem::kQ + t * Smem::kOperand;
-            const int cx = lane % kL, rx = lane / kL;
+        const int first_new = first_new_tile(p, sg);
+        float c = 0.0f;  // what makes a power of two of a raw logit, but for the key's scale
+        // Q, HD / 8 lanes a row: to fp16 by a power of two of the row's own, or as it comes; with the scale's sign
+        auto load_q = [&](bool bf16) {
+          constexpr int kL = HD / 8, kR = 32 / kL, kN = 32 / kR;  // lanes of a row, rows at a time, times
+          uint8_t* op = smem + Smem::kQ + t * Smem::kOperand;
+          const int cx = lane % kL, rx = lane / kL;
+          const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+          const float unit = fabsf(a.scale) * kLog2e;
+          c = unit;
 #pragma unroll 8
-            for (int i = 0; i < kN; ++i) {
-              const int y = (warp & 3) * 32 + i * kR + rx, ys = by_group(p, y), sl = tile * p.per_tile + ys;
-              uint4 w = make_uint4(0, 0, 0, 0);
-              if (y < p.per_tile * p.group && sl < a.slots)
-                w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                         (static_cast<int64_t>(sg.req) * a.slots + sl) * a.q_row_stride +
-                                                         (sg.kvh * p.group + y - ys * p.group) * a.q_head_stride) + cx);
-              const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+          for (int i = 0; i < kN; ++i) {
+            const int y = (warp & 3) * 32 + i * kR + rx, ys = by_group(p, y), sl = tile * p.per_tile + ys;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (y < p.per_tile * p.group && sl < a.slots)
+              w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                       (static_cast<int64_t>(sg.req) * a.slots + sl) * a.q_row_stride +
+                                                       (sg.kvh * p.group + y - ys * p.group) * a.q_head_stride) + cx);
+            uint32_t h[4] = {w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip};
+            if (!bf16) {
               float amax = 0.0f;
 #pragma unroll
               for (int z = 0; z < 4; ++z)
-                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(in[z] << 16)), fabsf(__uint_as_float(in[z] & 0xFFFF0000u))));
+                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(h[z] << 16)), fabsf(__uint_as_float(h[z] & 0xFFFF0000u))));
 #pragma unroll
               for (int o = 1; o < kL; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
               int k = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
               k = min(max(k, -100), 127);
               const float up = __uint_as_float(static_cast<uint32_t>(14 - k + 127) << 23);
-              uint32_t h[4];
 #pragma unroll
               for (int z = 0; z < 4; ++z)
-                h[z] = pack_f16(__uint_as_float(in[z] << 16) * up, __uint_as_float(in[z] & 0xFFFF0000u) * up);
-              *reinterpret_cast<uint4*>(op + (cx >> 3) * kHalfBytes + y * 128 + (((cx & 7) ^ (y & 7)) << 4)) =
-                  make_uint4(h[0], h[1], h[2], h[3]);
+                h[z] = pack_f16(__uint_as_float(h[z] << 16) * up, __uint_as_float(h[z] & 0xFFFF0000u) * up);
               const int mine = __shfl_sync(0xFFFFFFFFu, k, (lane % kR) * kL);
-              if (lane / kR == i) c = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(mine - 14 + 127) << 23);
+              if (lane / kR == i) c = unit * __uint_as_float(static_cast<uint32_t>(mine - 14 + 127) << 23);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full[t]);
+            *reinterpret_cast<uint4*>(op + (cx >> 3) * kHalfBytes + y * 128 + (((cx & 7) ^ (y & 7)) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_full[t]);
+        };
+        {
           bool poison = false;
           for (int i = 0; i < steps; ++i) {
             const int j = split ? 2 * i + t : i, key = sg.key_begin + j;
-            const bool fresh = a.k_new && key >= sg.cached;
+            const bool fresh = j >= first_new;
+            // (this row tile's last product with Q, that of its last step, is done: S has been read)
+            if (i == 0 || (fresh && j - (split ? 2 : 1) < first_new)) load_q(fresh);
             uint32_t see[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
             if (fresh) {  // which of the new tokens this row sees, while the product runs
               const int b0 = (key - sg.cached) * kKeyTile;
@@ -676,11 +642,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
               all &= see[w] == 0xFFFFFFFFu;
             }
             const bool masked = !__all_sync(0xFFFFFFFFu, all);
-            const float ratio = i == 0 || vref == info.vref ? 1.0f : vref / info.vref;
-            vref = info.vref;
-            auto scale = [&](int g) { return c * info.k_scale[g]; };
-            if (masked) softmax_tile<HD, false, false, true>(s_at, o_at, i == 0, ratio, c < 0.0f, scale, see, sm, ready);
-            else softmax_tile<HD, false, false, false>(s_at, o_at, i == 0, ratio, c < 0.0f, scale, see, sm, ready);
+            auto scale = [&](int w) {
+              const float2 x = *reinterpret_cast<const float2*>(&info.k_scale[2 * w]);
+              return make_float2(c * x.x, c * x.y);
+            };
+            auto value = [&](int w) { return *reinterpret_cast<const float2*>(&info.v_scale[2 * w]); };
+            auto value_log = [&](int w) { return *reinterpret_cast<const float2*>(&info.v_log[2 * w]); };
+            if (fresh) softmax_tile<HD, kWeightPairs, true>(s_at, o_at, i == 0, false, scale, value, value_log, see, sm, ready);
+            else if (masked) softmax_tile<HD, kWeights, true>(s_at, o_at, i == 0, false, scale, value, value_log, see, sm, ready);
+            else softmax_tile<HD, kWeights, false>(s_at, o_at, i == 0, false, scale, value, value_log, see, sm, ready);
           }
           if (poison) sm.l = NAN;
           if (steps > 0) ok = ok && mbar_wait(&o_full[t], o_use++ & 1, nullptr);
@@ -702,7 +672,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
           if (live && a.lse) a.lse[row * a.n_q + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
         };
         {
-          const float inv = alone ? (sm.l == 0.0f ? 0.0f : vref / sm.l) : vref;
+          const float unit = ex2(sm.u - sm.m), inv = sm.u == -INFINITY || sm.l == 0.0f ? 0.0f : alone ? unit / sm.l : unit;  // (O to the sum's unit)
           const size_t mine = static_cast<size_t>(2 * piece + (piece == c_first)) * 2 + t;
           const bool nan = sm.l != sm.l, none = steps == 0;  // (none: nothing was put into O)
 #pragma unroll
@@ -719,10 +689,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
               uint4 w[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                w[k].x = pack_p<true>(__uint_as_float(v[8 * k]), __uint_as_float(v[8 * k + 1]));
-                w[k].y = pack_p<true>(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3]));
-                w[k].z = pack_p<true>(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5]));
-                w[k].w = pack_p<true>(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7]));
+                w[k].x = pack_p(__uint_as_float(v[8 * k]), __uint_as_float(v[8 * k + 1]));
+                w[k].y = pack_p(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3]));
+                w[k].z = pack_p(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5]));
+                w[k].w = pack_p(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7]));
               }
               // (through the row tile's own Q, which the next segment's replaces after this)
               store_rows(smem + Smem::kQ + t * Smem::kOperand + (warp & 3) * 4096, w, [&](int z) { return out_of(z, x); });
@@ -779,9 +749,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
               uint4 w[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                w[k] = make_uint4(pack_p<true>(o[2 * k].x * inv, o[2 * k].y * inv), pack_p<true>(o[2 * k].z * inv, o[2 * k].w * inv),
-                                  pack_p<true>(o[2 * k + 1].x * inv, o[2 * k + 1].y * inv),
-                                  pack_p<true>(o[2 * k + 1].z * inv, o[2 * k + 1].w * inv));
+                w[k] = make_uint4(pack_p(o[2 * k].x * inv, o[2 * k].y * inv), pack_p(o[2 * k].z * inv, o[2 * k].w * inv),
+                                  pack_p(o[2 * k + 1].x * inv, o[2 * k + 1].y * inv),
+                                  pack_p(o[2 * k + 1].z * inv, o[2 * k + 1].w * inv));
               store_rows(smem + Smem::kQ + t * Smem::kOperand + (warp & 3) * 4096, w, [&](int z) { return out_of(z, x); });
             }
             finish_lse(top, sum);

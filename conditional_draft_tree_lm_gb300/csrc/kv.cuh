@@ -26,6 +26,22 @@ DT_DEVINL float lg2(float x) {
   return y;
 }
 
+// The unit of a row's O over cached tokens.  A weight 2^z v (z: logit, v: its key's value scale) goes to the product with V
+// in fp16 as 2^(z - u) v, and O is in units of 2^u.  u follows the keys, up and down: of the keys of a tile or step the
+// largest weight stands at 2^0 .. 2^15 (2^8 where u has moved), so that what fp16 cannot hold, 2^-25 or less, is that small beside
+// the largest of the same keys, whatever stands in other tiles and whatever scale a page without weight has.  Downwards u
+// stops 60 below its highest value, behind which O, in 32 bits, might overflow and what is added is lost to it all the same;
+// and it stays above m - 118 (m: the maximum in use), so that 2^(m - u) is a number.
+constexpr float kUnitTop = 15.0f, kUnitSet = 8.0f, kUnitFall = 60.0f, kUnitBelow = 118.0f;
+// weight: the largest z + log2 v of the row's keys.  Returns what O is to be multiplied by.
+DT_DEVINL float move_unit(float weight, float m, float& u, float& high) {
+  const float before = u;
+  if (weight > -INFINITY && (weight > u + kUnitTop || weight < u)) u = fmaxf(weight - kUnitSet, high - kUnitFall);
+  u = fmaxf(u, m - kUnitBelow);
+  high = fmaxf(high, u);
+  return u == before ? 1.0f : ex2(before - u);
+}
+
 constexpr int kSms = 152;  // of a GB300: grids of one wave
 
 // Largest finite e4m3 magnitude: 1.75 * 2^8.

@@ -29,15 +29,15 @@
 //     transposed by movmatrix, is the B fragment; a thread supplies 16 adjacent
 //     channels of 4 keys, two keys' bytes interleaved by a byte permute.
 // e4m3 goes to fp16 exactly (one conversion for two values).  The page scales stay
-// outside: the key's multiplies the logit, the value's is folded into P relative
-// to the largest scale seen so far.  Q is brought to fp16 by a power of two per
+// outside: the key's multiplies the logit, the value's is folded into P, in a
+// unit of the row's own that follows the keys (move_unit).  Q is brought to fp16 by a power of two per
 // row (exact to 2^-40 of the row's maximum), P is held in fp16: 11 bits, where
 // bf16 would give 8.  Maxima, sums and O are 32 bits.  New tokens' keys and values
 // take the same products in bf16 (row by row with plain multiplications: 15 us more
 // for 32 trees of 65 slots, 40 us for a tree of 513).
 //
 // Measured: 32 tokens over caches of up to 16k tokens (671 MB) 109 us, 6.2 TB/s, 91 %
-// of the measured copy bandwidth; one token over 2k 8.0 us, a chain of latencies.
+// of the measured copy bandwidth; one token over 2k 7.7 us, a chain of latencies.
 #pragma once
 
 #include <cuda.h>
@@ -501,17 +501,17 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
 
     float o[RH][kKSteps][4];
     float m[RH][2], l[RH][2];  // of rows 8 h + 2t and 2t + 1; l: over this thread's keys
+    float u[RH][2], u_high[RH][2];  // O is in units of 2^u; the largest u so far
 #pragma unroll
     for (int h = 0; h < RH; ++h) {
       m[h][0] = m[h][1] = -INFINITY;
       l[h][0] = l[h][1] = 0.0f;
+      u[h][0] = u[h][1] = u_high[h][0] = u_high[h][1] = -INFINITY;
 #pragma unroll
       for (int j = 0; j < kKSteps; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[h][j][k] = 0.0f;
     }
-    // the largest value scale so far and its reciprocal; O is in units of it
-    float vref = 1.17549435e-38f, vinv = 8.507059173e37f;
 
     for (int i = 0; i < steps; ++i) {
       gave_up |= !mbar_wait(&bars[used % kStages], (used / kStages) & 1, nullptr);
@@ -554,10 +554,11 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
           }
         }
       }
-      // logits in powers of two: [half][key g, key g + 8] of rows 2t and 2t + 1
-      float z[RH][2][4], high[RH][2];
-      const float v_top = fmaxf(v_scale[0], v_scale[1]);
-      bool grow = v_top > vref;
+      // logits in powers of two: [half][key g, key g + 8] of rows 2t and 2t + 1; and the largest, without and with the
+      // value scale's logarithm
+      float z[RH][2][4], high[RH][2], high_weight[RH][2];
+      const float v_log[2] = {lg2(v_scale[0]), lg2(v_scale[1])};
+      bool moves = false;
 #pragma unroll
       for (int h = 0; h < RH; ++h) {
 #pragma unroll
@@ -572,27 +573,31 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          high[h][k] = fmaxf(fmaxf(z[h][0][k], z[h][0][k + 2]), fmaxf(z[h][1][k], z[h][1][k + 2]));
-          grow |= high[h][k] > m[h][k] + 8.0f;
+          const float high0 = fmaxf(z[h][0][k], z[h][0][k + 2]), high1 = fmaxf(z[h][1][k], z[h][1][k + 2]);
+          high[h][k] = fmaxf(high0, high1);
+          high_weight[h][k] = fmaxf(high0 + v_log[0], high1 + v_log[1]);  // (a NaN where a page is not there)
+          // (a row's logits are in the lanes of its t)
+          const bool small = (__ballot_sync(0xFFFFFFFFu, high_weight[h][k] >= u[h][k]) & 0x11111111u << t) == 0;
+          moves |= high[h][k] > m[h][k] + 8.0f || high_weight[h][k] > u[h][k] + kUnitTop || (small && u[h][k] > u_high[h][k] - kUnitFall);
         }
       }
-      // The maximum in use may lag behind the true one by 2^8 (P then reaches 256, well inside
-      // fp16), so that O is rescaled a few times in a stretch and not at every step.
-      if (__any_sync(0xFFFFFFFFu, grow)) {
-        const float vnew = fmaxf(vref, v_top), vratio = vref / vnew;
+      // The maximum in use may lag behind the true one by 2^8, and O's unit moves only where a step's largest weight
+      // leaves its range, so that O is rescaled a few times in a stretch and not at every step.
+      if (__any_sync(0xFFFFFFFFu, moves)) {
 #pragma unroll
         for (int h = 0; h < RH; ++h) {
           float f[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float top = fmaxf(high[h][k], m[h][k]);
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-            f[k] = top == -INFINITY ? 1.0f : ex2(m[h][k] - top);
+            float top = fmaxf(high[h][k], m[h][k]), weight = high_weight[h][k];
+#pragma unroll
+            for (int y = 4; y < 32; y <<= 1) {
+              top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, y));
+              weight = fmaxf(weight, __shfl_xor_sync(0xFFFFFFFFu, weight, y));
+            }
+            l[h][k] *= top == -INFINITY ? 1.0f : ex2(m[h][k] - top);
             m[h][k] = top;
-            l[h][k] *= f[k];
-            f[k] *= vratio;
+            f[k] = move_unit(weight, top, u[h][k], u_high[h][k]);
           }
 #pragma unroll
           for (int j = 0; j < kKSteps; ++j) {
@@ -600,22 +605,21 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
             o[h][j][2] *= f[0], o[h][j][3] *= f[1];
           }
         }
-        vref = vnew;
-        vinv = 1.0f / vnew;
       }
       uint32_t pb[RH][2][2];
 #pragma unroll
       for (int h = 0; h < RH; ++h) {
         const float b0 = m[h][0] == -INFINITY ? 0.0f : m[h][0], b1 = m[h][1] == -INFINITY ? 0.0f : m[h][1];
+        const float unit0 = u[h][0] == -INFINITY ? 1.0f : ex2(m[h][0] - u[h][0]), unit1 = u[h][1] == -INFINITY ? 1.0f : ex2(m[h][1] - u[h][1]);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float v_rel = v_scale[x] * vinv;
+          const float f0 = v_scale[x] * unit0, f1 = v_scale[x] * unit1;
           const float e0 = ex2(z[h][x][0] - b0), e1 = ex2(z[h][x][1] - b1);
           const float e2 = ex2(z[h][x][2] - b0), e3 = ex2(z[h][x][3] - b1);
           l[h][0] += e0 + e2;
           l[h][1] += e1 + e3;
-          pb[h][x][0] = transpose8x8(pack_f16(e0 * v_rel, e1 * v_rel));
-          pb[h][x][1] = transpose8x8(pack_f16(e2 * v_rel, e3 * v_rel));
+          pb[h][x][0] = transpose8x8(pack_f16(e0 * f0, e1 * f1));
+          pb[h][x][1] = transpose8x8(pack_f16(e2 * f0, e3 * f1));
         }
       }
 #pragma unroll
@@ -659,7 +663,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
     }
     // --- this warp's part, with that of the new tokens: sums over its keys, O in true units
     {
-      float f_old[RH][2], f_fresh[RH][2];
+      float f_old[RH][2], f_fresh[RH][2];  // of O
 #pragma unroll
       for (int h = 0; h < RH; ++h) {
 #pragma unroll
@@ -671,11 +675,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
           sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
           const float fm = with_fresh ? s_m[at] : -INFINITY, fl = with_fresh ? s_l[at] : 0.0f;
           const float top = fmaxf(m[h][k], fm), base = top == -INFINITY ? 0.0f : top;
-          f_old[h][k] = ex2(m[h][k] - base);
+          f_old[h][k] = ex2(u[h][k] - base);
           f_fresh[h][k] = with_fresh ? ex2(fm - base) : 0.0f;
+          l[h][k] = sum * ex2(m[h][k] - base) + fl * f_fresh[h][k];
           m[h][k] = top;
-          l[h][k] = sum * f_old[h][k] + fl * f_fresh[h][k];
-          f_old[h][k] *= vref;
         }
 #pragma unroll
         for (int j = 0; j < kKSteps; ++j)

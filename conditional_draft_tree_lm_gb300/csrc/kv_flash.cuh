@@ -212,14 +212,8 @@ struct SoftmaxRow {
   // kWeights, kWeightPairs: O is in units of 2^u, whatever m is; the largest u so far
   float u = -INFINITY, u_high = -INFINITY;
 };
-// A weight 2^z v of a cached tile (z: logit, v: its key's value scale) is held in fp16 as 2^(z - u) v.  u follows the
-// tiles, up and down: a tile's largest weight stands at 2^0 .. 2^15 (2^8 when u moves), so that what fp16 cannot hold, 2^-25 or
-// less, is that small beside the largest of the same 128 keys, whatever stands in other tiles.  Downwards u stops 60 below its highest
-// value, where O, in 32 bits, might overflow (and what is that small is lost to it all the same).
-constexpr float kUnitTop = 15.0f, kUnitSet = 8.0f, kUnitFall = 60.0f;
-// u >= m - kUnitBelow, so that 2^(m - u) is a number; and u >= m + kUnitNew where new tokens come in, the largest
-// of whose values stay finite in O.
-constexpr float kUnitBelow = 118.0f, kUnitNew = 16.0f;
+// New tokens come in where u >= m + kUnitNew: the largest of their values stay finite in O.
+constexpr float kUnitNew = 16.0f;
 
 // One 128-key tile of a row: S at s_at becomes P there, and the row's state (and O, where its unit changes: for
 // kProbs with m) is brought up to date.  scale(g): what turns a raw logit of keys 16 g .. 16 g + 15 into
@@ -291,17 +285,14 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, bool negat
     float f_o = f;
     bool o_moves = true;
     if (P != kProbs) {
-      float u2 = row.u;
+      const float before = row.u;
       if (P == kWeights) {
-        if (top_weight > -INFINITY && (top_weight > u2 + kUnitTop || top_weight < u2)) u2 = fmaxf(top_weight - kUnitSet, row.u_high - kUnitFall);
-        u2 = fmaxf(u2, m2 - kUnitBelow);
+        f_o = move_unit(top_weight, m2, row.u, row.u_high);
       } else {
-        u2 = fmaxf(u2, m2 + kUnitNew);
+        row.u = fmaxf(before, m2 + kUnitNew);
+        f_o = row.u == before ? 1.0f : ex2(before - row.u);
       }
-      o_moves = __any_sync(0xFFFFFFFFu, u2 != row.u);
-      f_o = u2 == row.u ? 1.0f : ex2(row.u - u2);
-      row.u = u2;
-      row.u_high = fmaxf(row.u_high, u2);
+      o_moves = __any_sync(0xFFFFFFFFu, row.u != before);
     }
     tmem_wait_ld();  // (s is on its way; the rescaling waits for its own)
     if (!first && o_moves) rescale_o<HD>(o_at, f_o);

@@ -14,6 +14,7 @@ computes: tensors become pointers, a refused call raises ``DtreeError``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import struct
 from ctypes import c_float, c_int, c_int64, c_size_t, c_void_p
@@ -101,6 +102,12 @@ def _stream(stream, index):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
+def _allocating(stream):
+    """What a call allocates belongs to the stream that it runs on."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _refused(status, where):
     return DtreeError(status, where + ": " + _lib.dt_last_error().decode(errors="replace"))
 
@@ -168,19 +175,27 @@ class KvCache:
 class AttentionWorkspace:
     """Device memory that ``cache_attention`` calls use one after the other (calls that may
     overlap, on several streams, need one each).  It grows with the largest call so far;
-    grow it before a stream capture by a call of the captured sizes or by ``reserve``."""
+    grow it before a stream capture by a call of the captured sizes or by ``reserve``.
+    Memory is taken and zeroed in the order of the stream of the call that needs it, and
+    goes back only behind the work of every stream that has used it."""
 
     def __init__(self):
-        self.buffer, self.sizes = None, None
+        self.buffer, self.sizes, self.streams = None, None, set()
 
-    def reserve(self, n_req, slots, n_q, n_kv, head_dim, device="cuda"):
+    def reserve(self, n_req, slots, n_q, n_kv, head_dim, device="cuda", stream=None):
         import torch
         sizes = (n_req, slots, n_q, n_kv, head_dim, device)
         if sizes != self.sizes:
             need = _library().dt_cache_attention_workspace(*sizes[:5])
             if self.buffer is None or self.buffer.numel() < need or self.buffer.device != torch.empty(0, device=device).device:
-                self.buffer = torch.zeros(max(need, 256), dtype=torch.uint8, device=device)
+                with _allocating(stream):
+                    self.buffer = torch.zeros(max(need, 256), dtype=torch.uint8, device=device)
+                self.streams = {_stream(stream, self.buffer.get_device())}
             self.sizes = sizes
+        raw = _stream(stream, self.buffer.get_device())
+        if raw not in self.streams:
+            self.streams.add(raw)
+            self.buffer.record_stream(torch.cuda.current_stream(self.buffer.device) if stream is None else stream)
         return self.buffer
 
 
@@ -256,7 +271,9 @@ def cache_attention(cache, q, block_table, length, *, k_new=None, v_new=None, ma
         raise ValueError(f"q: head_dim {dim}, the cache's is {cache.head_dim}")
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new: give both or neither")
-    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
+    if out is None:
+        with _allocating(stream):
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
     lead = (n, slots)
     kp = kr = kh = vp = vr = vh = 0
     if k_new is not None:
@@ -264,7 +281,7 @@ def cache_attention(cache, q, block_table, length, *, k_new=None, v_new=None, ma
         vp, vr, vh = _heads(v_new, lead, cache.n_kv, dim, "v_new", dev)
     qp, qr, qh = _heads(q, lead, heads, dim, "q", dev)
     op, orow, oh = _heads(out, lead, heads, dim, "out", dev)
-    buf = workspace.reserve(n, slots, heads, cache.n_kv, dim, dev)
+    buf = workspace.reserve(n, slots, heads, cache.n_kv, dim, dev, stream)
     a = _pack_attend(n, slots, heads, width, dim ** -0.5 if scale is None else scale, qp, qr, qh, kp, vp, kr, kh, vr, vh,
                      _flat(block_table, torch.int32, n * width, "block_table", dev),
                      _flat(length, torch.int32, n, "length", dev),
@@ -288,7 +305,9 @@ def prompt_attention(q, k, v, row_start, *, scale=None, out=None, lse=None, stat
         raise ValueError("q and k: expected [rows, heads, head_dim]")
     rows, heads, dim = q.shape
     kv = k.shape[1]
-    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
+    if out is None:
+        with _allocating(stream):
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
     lead = (rows,)
     qp, qr, qh = _heads(q, lead, heads, dim, "q", dev)
     kp, kr, kh = _heads(k, lead, kv, dim, "k", dev)

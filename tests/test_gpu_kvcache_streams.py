@@ -1,0 +1,73 @@
+"""The bindings' memory next to streams, captured graphs and devices."""
+import numpy as np
+import pytest
+
+from tests.test_gpu_kvcache import _t, cache_case, check_cache, check_prompt, dev
+
+pytestmark = pytest.mark.gpu
+
+LATE = 400_000_000  # cycles: some 0.2 s
+
+
+@pytest.mark.parametrize("slots", [1, 40])
+def test_a_call_on_another_stream_does_not_wait_for_the_current_ones_memory(slots):
+    """The current stream is busy for a while; a call on another stream has its workspace zeroed and its output written in
+    that stream's order, and nothing that the current stream still has to do falls on them."""
+    torch = _t()
+    from conditional_draft_tree_lm_gb300 import AttentionWorkspace, cache_attention, prompt_attention
+    c = cache_case(np.random.RandomState(81), [3000, 10, 0, 900], slots, 8, 2, 128, 64, "tree")
+    table, length, mask = dev(c["table"], torch.int32), dev(c["lens"], torch.int32), dev(c["mask"], torch.uint8)
+    lse = torch.zeros(4, slots, 8, device="cuda")
+    q, k, v = (torch.randn(300, h, 128, device="cuda").to(torch.bfloat16) for h in (8, 2, 2))
+    start = dev([0, 300], torch.int32)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    # memory of the outputs' and the workspace's sizes, which the current stream has yet to overwrite when it is free again
+    sizes = [c["q"].numel() * 2, q.numel() * 2] + [s << 20 for s in (2, 8, 16, 32, 48, 64)]
+    spare = [torch.empty(s, dtype=torch.uint8, device="cuda") for s in sizes]
+
+    def call():
+        out = cache_attention(c["cache"], c["q"], table, length, k_new=c["k"], v_new=c["v"], mask=mask, lse=lse,
+                              workspace=AttentionWorkspace(), stream=side)
+        return out, prompt_attention(q, k, v, start, stream=side)
+    call()  # (loading kernels and getting memory from the driver wait for the device: done here)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(LATE)
+    for x in spare:
+        x.fill_(0xFF)
+    del spare, x
+    busy = torch.cuda.Event()
+    busy.record()
+    out, full = call()
+    side.synchronize()
+    assert not busy.query()  # (the test holds only while the current stream is still busy)
+    with torch.cuda.stream(side):
+        out_then, full_then = out.clone(), full.clone()
+    torch.cuda.synchronize()
+    assert torch.equal(out, out_then) and torch.equal(full, full_then)
+    check_cache(c, (out.float().cpu().numpy(), lse.cpu().numpy()))
+    full_lse = torch.zeros(300, 8, device="cuda")
+    assert torch.equal(full, prompt_attention(q, k, v, start, lse=full_lse))
+    check_prompt(q, k, v, [300], (full.float().cpu().numpy(), full_lse.cpu().numpy()), sample=[0, 150, 299])
+
+
+def test_a_workspace_outlives_the_streams_that_use_it():
+    """Dropped while another stream still works in it, its memory is not given out again before that work is done."""
+    torch = _t()
+    from conditional_draft_tree_lm_gb300 import AttentionWorkspace, cache_attention
+    c = cache_case(np.random.RandomState(82), [3000, 900], 1, 8, 2, 128, 64, None)
+    table, length = dev(c["table"], torch.int32), dev(c["lens"], torch.int32)
+    side = torch.cuda.Stream()
+    work = AttentionWorkspace()
+    first = cache_attention(c["cache"], c["q"], table, length, workspace=work)
+    torch.cuda.synchronize()
+    at = work.buffer.data_ptr()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(LATE)
+    out = cache_attention(c["cache"], c["q"], table, length, workspace=work, stream=side)
+    n = work.buffer.numel()
+    del work
+    again = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert at not in [x.data_ptr() for x in again]
+    torch.cuda.synchronize()
+    assert torch.equal(out, first)

@@ -174,13 +174,15 @@ class KvCache:
 
 class AttentionWorkspace:
     """Device memory that ``cache_attention`` calls use one after the other (calls that may
-    overlap, on several streams, need one each).  It grows with the largest call so far;
-    grow it before a stream capture by a call of the captured sizes or by ``reserve``.
-    Memory is taken and zeroed in the order of the stream of the call that needs it, and
+    overlap, on several streams, need one each).  It grows with the largest call so far,
+    at least to twice its size; what it had before stays with it, since captured graphs may
+    work there.  While a stream is being captured it cannot grow (its zeros would be the
+    graph's): grow it before by a call of the captured sizes or by ``reserve``, and keep it
+    as long as the graph.  Memory is taken and zeroed in the order of the stream of the call that needs it, and
     goes back only behind the work of every stream that has used it."""
 
     def __init__(self):
-        self.buffer, self.sizes, self.streams = None, None, set()
+        self.buffer, self.sizes, self.streams, self.outgrown = None, None, set(), []
 
     def reserve(self, n_req, slots, n_q, n_kv, head_dim, device="cuda", stream=None):
         import torch
@@ -189,6 +191,11 @@ class AttentionWorkspace:
             need = _library().dt_cache_attention_workspace(*sizes[:5])
             if self.buffer is None or self.buffer.numel() < need or self.buffer.device != torch.empty(0, device=device).device:
                 with _allocating(stream):
+                    if torch.cuda.is_current_stream_capturing():
+                        raise RuntimeError(f"workspace: {need} bytes are needed while a stream is being captured; reserve them before")
+                    if self.buffer is not None:
+                        self.outgrown.append(self.buffer)
+                        need = max(need, 2 * self.buffer.numel())
                     self.buffer = torch.zeros(max(need, 256), dtype=torch.uint8, device=device)
                 self.streams = {_stream(stream, self.buffer.get_device())}
             self.sizes = sizes

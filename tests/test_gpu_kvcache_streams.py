@@ -71,3 +71,47 @@ def test_a_workspace_outlives_the_streams_that_use_it():
     assert at not in [x.data_ptr() for x in again]
     torch.cuda.synchronize()
     assert torch.equal(out, first)
+
+
+def test_captured_calls_keep_their_workspace_when_it_grows():
+    """A single-token step is captured, then larger calls grow the workspace; the graph's memory is still there, and its
+    replays give what the call gave.  A workspace that would have to grow refuses to do so inside a capture."""
+    torch = _t()
+    from conditional_draft_tree_lm_gb300 import AttentionWorkspace, cache_attention
+    work = AttentionWorkspace()
+    c = cache_case(np.random.RandomState(83), [3000, 900, 0], 1, 8, 2, 128, 64, "tree")
+    d = cache_case(np.random.RandomState(84), [500, 40], 70, 8, 2, 128, 64, "tree")
+    args = [(x["cache"], x["q"], dev(x["table"], torch.int32), dev(x["lens"], torch.int32)) for x in (c, d)]
+    new = [dict(k_new=x["k"], v_new=x["v"], mask=dev(x["mask"], torch.uint8), workspace=work) for x in (c, d)]
+    want = cache_attention(*args[0], **new[0])
+    out = torch.zeros_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache_attention(*args[0], out=out, **new[0])
+    small = work.buffer
+    at, size = small.data_ptr(), small.numel()
+    del small
+    with pytest.raises(RuntimeError, match="captured"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            cache_attention(*args[1], out=torch.empty_like(d["q"]), **new[1])
+    torch.cuda.synchronize()
+    large = cache_attention(*args[1], **new[1])
+    assert work.buffer.data_ptr() != at and work.buffer.numel() >= 2 * size
+    other = [torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert at not in [x.data_ptr() for x in other]
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want) and torch.equal(large, cache_attention(*args[1], **new[1]))
+    torch.cuda.synchronize()
+    assert all((x == 0xFF).all() for x in other)
+    # grown, it is captured too
+    out = torch.zeros_like(large)
+    second = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(second):
+        cache_attention(*args[1], out=out, **new[1])
+    second.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, large)
+    check_cache(d, (large.float().cpu().numpy(), None), rows=[0, 30, 69])

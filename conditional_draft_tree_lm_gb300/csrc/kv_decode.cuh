@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
               const int b = k0 + g + 8 * x;
               if (slot[h][k] >= 0 && b < a.slots && (a.mask ? __ldg(mask[h][k] + b) != 0 : b <= slot[h][k])) see |= 1u << (4 * h + 2 * x + k);
             }
-        // values that are not finite: the key takes no part in the product, the rows that see it become NaN
+        // values that are not finite: they take no part in the product, and O becomes NaN in the rows that see them
         uint32_t bad = 0;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -407,6 +407,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
             mma_bf16(s, kw[0][c].z, kw[1][c].z, kw[0][c].w, kw[1][c].w, qw[h][2 * c + 1].x, qw[h][2 * c + 1].y);
           }
           float e[4], f[2];
+          bool odd[2];  // the row sees a value that is not finite
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const bool s0 = see >> (4 * h + k) & 1u, s1 = see >> (4 * h + 2 + k) & 1u;
@@ -422,12 +423,16 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
             e[k] = s0 ? ex2(z0 - base) : 0.0f;
             e[k + 2] = s1 ? ex2(z1 - base) : 0.0f;
             fl[h][k] = fl[h][k] * f[k] + (e[k] + e[k + 2]);
-            if ((s0 && bad >> g & 1u) || (s1 && bad >> (g + 8) & 1u)) fl[h][k] = NAN;
+            // (a row's keys are in the lanes of its t)
+            odd[k] = (__ballot_sync(0xFFFFFFFFu, (s0 && bad >> g & 1u) || (s1 && bad >> (g + 8) & 1u)) & 0x11111111u << t) != 0;
           }
 #pragma unroll
           for (int j = 0; j < kKSteps; ++j) {
             fo[h][j][0] *= f[0], fo[h][j][1] *= f[1];
             fo[h][j][2] *= f[0], fo[h][j][3] *= f[1];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (odd[k & 1]) fo[h][j][k] = NAN;
           }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {

@@ -22,7 +22,7 @@
 // Tiles that hold keys which some row must not see are cleaned before their
 // product (0 * NaN would reach that row): values behind the sequence become
 // zeros, and a key whose value is not finite becomes zeros and is noted, which
-// makes the rows that do see it NaN.
+// makes the output of the rows that do see it NaN (their lse has no values in it).
 //
 // Measured, 32 heads of 128 over 8: one prompt of 16k tokens 1340 us, 1.64 PFLOP/s, 87 %
 // of the measured bf16 rate (the exponentials and the maximum are what the products
@@ -429,6 +429,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         else
           softmax_tile<HD, kProbs, false>(s_at, o_at, j == 0, c < 0.0f, scale, scale, scale, see, row, ready);
       }
+      bool poison = false;
       if (n > 0) {
         ok = ok && mbar_wait(&o_full[t], o_use++ & 1, nullptr);
         tc_fence_after();
@@ -436,14 +437,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         for (int j = it.masked0; j < n; ++j)
 #pragma unroll
           for (int w = 0; w < 4; ++w)
-            if (bad_key[(j - it.masked0) * 4 + w] & first_bits(pos + 1 - j * kKeyTile, w)) row.l = NAN;
+            if (bad_key[(j - it.masked0) * 4 + w] & first_bits(pos + 1 - j * kKeyTile, w)) poison = true;
       }
       // (the vote uses the words, so that they have been read before they are cleared for the next item)
-      if (__ballot_sync(0xFFFFFFFFu, row.l != row.l) >> lane & 1u) row.l = NAN;
+      poison = __ballot_sync(0xFFFFFFFFu, poison) >> lane & 1u;
       if (lane == 0 && n > 0) mbar_arrive(&told[t]);
       if (n > 0 && ok) {
         const bool live = r < p.group * p.positions && pos < it.len;
-        const float inv = row.l == 0.0f ? 0.0f : 1.0f / row.l;
+        const float inv = poison ? NAN : row.l == 0.0f ? 0.0f : 1.0f / row.l;
 #pragma unroll
         for (int x = 0; x < HD; x += 64) {
           uint32_t v[64];

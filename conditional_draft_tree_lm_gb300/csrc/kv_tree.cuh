@@ -551,6 +551,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         const bool live = r < p.per_tile * p.group && slot < a.slots;
         const int64_t row = static_cast<int64_t>(sg.req) * a.slots + slot;
         SoftmaxRow sm;
+        bool poison = false;  // the row sees a new token's value that is not finite: O is NaN, the sum is not
         const int first_new = first_new_tile(p, sg);
         float c = 0.0f;  // what makes a power of two of a raw logit, but for the key's scale
         // Q, HD / 8 lanes a row: to fp16 by a power of two of the row's own, or as it comes; with the scale's sign
@@ -594,7 +595,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
           if (lane == 0) mbar_arrive(&q_full[t]);
         };
         {
-          bool poison = false;
           for (int i = 0; i < steps; ++i) {
             const int j = split ? 2 * i + t : i, key = sg.key_begin + j;
             const bool fresh = j >= first_new;
@@ -652,7 +652,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             else if (masked) softmax_tile<HD, kWeights, true>(s_at, o_at, i == 0, false, scale, value, value_log, see, sm, ready);
             else softmax_tile<HD, kWeights, false>(s_at, o_at, i == 0, false, scale, value, value_log, see, sm, ready);
           }
-          if (poison) sm.l = NAN;
           if (steps > 0) ok = ok && mbar_wait(&o_full[t], o_use++ & 1, nullptr);
           tc_fence_after();
         }
@@ -674,7 +673,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         {
           const float unit = ex2(sm.u - sm.m), inv = sm.u == -INFINITY || sm.l == 0.0f ? 0.0f : alone ? unit / sm.l : unit;  // (O to the sum's unit)
           const size_t mine = static_cast<size_t>(2 * piece + (piece == c_first)) * 2 + t;
-          const bool nan = sm.l != sm.l, none = steps == 0;  // (none: nothing was put into O)
+          const bool nan = sm.l != sm.l || poison, none = steps == 0;  // (none: nothing was put into O)
 #pragma unroll
           for (int x = 0; x < HD; x += 64) {
             uint32_t v[64];

@@ -489,7 +489,8 @@ dt_status dt_kv_append(const dt_kv_cache* cache, const dt_kv_append_args* args, 
  * A row that sees nothing gives zeros and -inf.  What a row does not see has no
  * part in it, whatever it holds; a row that sees a value with a NaN or an
  * infinity is not finite in that channel (other channels of that row may not be
- * either), a row that sees a key with a NaN is NaN.
+ * either; lse has no values in it and is what it would be without them), a row that
+ * sees a key with a NaN is NaN, its lse too.
  * Row (q, a) of q, k_new, v_new and out is row q * slots + a.
  * workspace: dt_cache_attention_workspace() bytes of device memory, 256-byte
  * aligned, zeroed once by the caller; every call leaves it ready for the next,

@@ -113,3 +113,53 @@ def test_scales_that_are_no_powers_of_two_keep_the_weights_bits():
     """The shape of the repeated calls, whose value scales differ by odd factors."""
     c = cache_case(np.random.RandomState(32 + 64 + 16), [257] * 20, 32, 32, 4, 64, 16, None)
     check_cache(c, run_cache(c), rows=[0, 1, 16, 31])
+
+
+# ---------------------------------------------------------------------------
+# values that are not finite, and lse
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("lens,slots,heads,kv,hd", SIZES)
+def test_lse_has_no_values_in_it(lens, slots, heads, kv, hd):
+    """NaN and infinite values among the new tokens and in the cache: the rows that see them are not finite in that
+    channel, every row's lse is what it would be without them."""
+    torch = _t()
+    c = cache_case(np.random.RandomState(55), lens, slots, heads, kv, hd, 64, "random")
+    clean = dict(c, v=c["v"].clone())
+    want, want_lse = run_cache(clean)
+    bad = np.zeros((len(lens), slots), bool)
+    for b, (s, val) in enumerate([(0, np.nan), (slots - 1, np.inf), (slots // 2, -np.inf), (1, np.nan)][:len(lens)]):
+        c["v"][b, s, :, 5] = float(val)
+        bad[b] = c["mask"][b, :, s] != 0
+    out, lse = run_cache(c)
+    np.testing.assert_array_equal(lse, want_lse)
+    assert bad.any() and not bad.all()
+    np.testing.assert_array_equal(out[~bad], want[~bad])
+    assert not np.isfinite(out[bad][..., 5]).any()
+    # a cached value
+    b = int(np.argmax(lens))
+    cache, page = c["cache"], c["table"][int(np.argmax(lens)), 0]
+    cache.v.view(torch.uint8)[int(page), :, 7, 3] = 0x7F
+    out, lse = run_cache(clean)
+    np.testing.assert_array_equal(lse, want_lse)
+    assert not np.isfinite(out[b, :, :, 3]).any()
+    keep = np.arange(len(lens)) != b
+    np.testing.assert_array_equal(out[keep], want[keep])
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_lse_of_prompts_has_no_values_in_it(hd):
+    """The same wherever the value stands in a prompt: in its first key tiles, or among a tile's last keys."""
+    torch = _t()
+    from tests.test_gpu_kvcache import dev, run_prompt
+    rs = np.random.RandomState(56)
+    lens = [300, 700, 17]
+    q, k, v = (dev(rs.randn(sum(lens), h, hd), torch.bfloat16) for h in (8, 2, 2))
+    want, want_lse = run_prompt(q, k, v, lens)
+    bad = np.zeros(sum(lens), bool)
+    for row, end, val in ((3, 300, np.nan), (299, 300, np.inf), (300 + 650, 1000, -np.inf), (1010, 1017, np.nan)):
+        v[row, :, 9] = float(val)
+        bad[row:end] = True
+    out, lse = run_prompt(q, k, v, lens)
+    np.testing.assert_array_equal(lse, want_lse)
+    np.testing.assert_array_equal(out[~bad], want[~bad])
+    assert not np.isfinite(out[bad][..., 9]).any()

@@ -227,7 +227,8 @@ def kv_plan(len_old, len_new, block_table, free_pages, ring_in, ring_out, row_st
     a = _pack_plan(n, width, page, free_pages.numel(), extra, path_len, path_rows, rows,
                    _flat(len_old, i32, n, "len_old", dev),
                    0 if delta is None else _flat(delta, i32, n, "delta", dev),
-                   0 if path is None else _flat(path, i32, n * path_len, "path", dev),
+                   # (a path of no width is one all the same: it has no pointer of its own, and nothing is read from it)
+                   0 if path is None else _flat(path, i32, n * path_len, "path", dev) or len_old.data_ptr(),
                    _flat(ring_in, i32, 2, "ring_in", dev), _flat(block_table, i32, n * width, "block_table", dev),
                    _flat(free_pages, i32, free_pages.numel(), "free_pages", dev),
                    _flat(len_new, i32, n, "len_new", dev), _flat(ring_out, i32, 2, "ring_out", dev),

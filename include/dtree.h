@@ -438,7 +438,8 @@ typedef struct dt_kv_plan_args {
   int64_t max_rows;        /* entries of slot_map, positions, src_rows; 1..2^31-1 */
   const int32_t* len_old;  /* [n_req] */
   const int32_t* delta;    /* [n_req] or NULL */
-  const int32_t* path;     /* [n_req, path_len] (dt_accept_walk's accepted) or NULL */
+  const int32_t* path;     /* [n_req, path_len] (dt_accept_walk's accepted) or NULL; not NULL with path_len 0:
+                            * only roots are added, from rows q * path_rows */
   const int32_t* ring_in;  /* [2] */
   int32_t* block_table;    /* [n_req, max_blocks] in/out */
   int32_t* free_pages;     /* [n_pages] in/out */

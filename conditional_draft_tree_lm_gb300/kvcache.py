@@ -126,7 +126,8 @@ def _flat(t, dtype, numel, name, index):
 def _heads(t, lead, heads, dim, name, index):
     """Pointer, row stride and head stride of a bf16 tensor [*lead, heads, dim].
     Only rows and heads may be strided: several leading dimensions must fold into
-    one row index, and channels must be adjacent."""
+    one row index, and channels must be adjacent.  The stride of a dimension of one
+    entry says nothing and is not looked at."""
     import torch
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
@@ -135,9 +136,9 @@ def _heads(t, lead, heads, dim, name, index):
     if t.shape != (*lead, heads, dim):
         raise ValueError(f"{name}: expected {(*lead, heads, dim)}, got {tuple(t.shape)}")
     st = t.stride()
-    if st[-1] != 1 or (len(lead) == 2 and lead[0] > 1 and st[0] != st[1] * lead[1]):
+    if st[-1] != 1 or (len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and st[0] != st[1] * lead[1]):
         raise ValueError(f"{name}: strides {st}: channels must be adjacent and rows evenly spaced")
-    return t.data_ptr(), (st[-3] if lead[-1] > 1 or len(lead) == 1 else st[0]), (st[-2] if heads > 1 else 0)
+    return t.data_ptr(), (st[-3] if lead[-1] > 1 else st[0] if lead[0] > 1 else 0), (st[-2] if heads > 1 else 0)
 
 
 def _on_device(t, name):

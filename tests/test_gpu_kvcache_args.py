@@ -22,3 +22,23 @@ def test_plan_with_a_path_of_no_width():
     want = ok.plan(old, delta, 1, table, ring, head, count, 16, 8, path, 65)
     assert want["status"] == ok.BAD_PATH
     same_plan(run_plan(old, delta, 1, table, ring, head, count, 16, 8, path, 65), want)
+
+
+def test_rows_of_single_slots_and_entries():
+    """The first slot of every request, heads and rows of one entry with strides of their own: rows are evenly spaced."""
+    torch = _t()
+    from conditional_draft_tree_lm_gb300 import kv_append
+    rs = np.random.RandomState(92)
+    c = cache_case(rs, [70, 33, 0], 1, 4, 2, 64, 16, "causal")
+    wide = torch.randn(3, 5, 4 + 2 + 2, 64, device="cuda").to(torch.bfloat16)
+    one = wide[:, :1]
+    c["q"], c["k"], c["v"] = one[:, :, :4], one[:, :, 4:6], one[:, :, 6:]
+    assert c["q"].stride(0) != c["q"].stride(1)
+    check_cache(c, run_cache(c))
+    check_append(c["cache"], c["k"], c["v"], [7 * 16, -1, 3 * 16])
+    # one request of one slot whose outer strides fit nothing
+    c = cache_case(rs, [70], 1, 4, 2, 64, 16, "causal")
+    for x, heads in (("q", 4), ("k", 2), ("v", 2)):
+        c[x] = c[x].as_strided((1, 1, heads, 64), (3, 5, 64, 1))
+    check_cache(c, run_cache(c))
+    kv_append(c["cache"], c["k"][0], c["v"][0], dev([16], torch.int64))

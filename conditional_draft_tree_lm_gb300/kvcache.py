@@ -248,6 +248,8 @@ def kv_append(cache, k, v, slot_map, *, src_rows=None, status=None, stream=None)
     import torch
     lib = _library()
     dev, n = cache.index, slot_map.numel()
+    if k.dim() not in (3, 4):
+        raise ValueError("k: expected [rows, n_kv, head_dim] or [n_req, rows, n_kv, head_dim]")
     lead = tuple(k.shape[:-2])
     kp, kr, kh = _heads(k, lead, cache.n_kv, cache.head_dim, "k", dev)
     vp, vr, vh = _heads(v, lead, cache.n_kv, cache.head_dim, "v", dev)

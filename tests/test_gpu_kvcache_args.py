@@ -42,3 +42,14 @@ def test_rows_of_single_slots_and_entries():
         c[x] = c[x].as_strided((1, 1, heads, 64), (3, 5, 64, 1))
     check_cache(c, run_cache(c))
     kv_append(c["cache"], c["k"][0], c["v"][0], dev([16], torch.int64))
+
+
+def test_keys_of_other_dimensions_are_refused():
+    torch = _t()
+    from conditional_draft_tree_lm_gb300 import kv_append
+    cache = new_cache(np.random.RandomState(93), 4, 2, 16, 64)
+    x = torch.zeros(2, 3, 4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    for k in (x, x[0, 0, 0]):
+        with pytest.raises(ValueError):
+            kv_append(cache, k, k, dev([0], torch.int64))
+    torch.cuda.synchronize()

@@ -97,9 +97,21 @@ def _library():
     return _lib
 
 
-def _stream(stream, index):
+def _current_device():
     import torch
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getDevice()
+
+
+def _stream(stream, index):
+    """The stream of a call whose tensors are on CUDA device `index`, which must be the current one: the library launches there."""
+    import torch
+    if _current_device() != index:
+        raise ValueError(f"tensors on cuda:{index}, but the current device is cuda:{_current_device()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device_index != index:
+        raise ValueError(f"stream: on cuda:{stream.device_index}, the tensors on cuda:{index}")
+    return stream.cuda_stream
 
 
 def _allocating(stream):

@@ -1,0 +1,81 @@
+"""The cache's bindings on the host: what they refuse before anything is launched (CPU, no GPU call)."""
+import pytest
+
+from conditional_draft_tree_lm_gb300 import kvcache as kc
+
+
+class _Stream:
+    def __init__(self, index):
+        self.device_index, self.cuda_stream = index, 77
+
+
+def test_tensors_on_another_device_than_the_current_one_are_refused(monkeypatch):
+    monkeypatch.setattr(kc, "_current_device", lambda: 0)
+    assert kc._stream(_Stream(0), 0) == 77
+    for stream, index in ((None, 1), (_Stream(1), 1), (_Stream(1), 0)):
+        with pytest.raises(ValueError, match="cuda:1"):
+            kc._stream(stream, index)
+
+
+def test_every_binding_asks_for_its_stream_before_it_launches(monkeypatch):
+    """With a stand-in for the library and for tensors on cuda:1: the call is refused and never made."""
+    torch = pytest.importorskip("torch")
+
+    class Tensor:
+        is_cuda = True
+
+        def __init__(self, dtype, *shape):
+            self.dtype, self.shape = dtype, torch.Size(shape)
+
+        def dim(self):
+            return len(self.shape)
+
+        def numel(self):
+            return self.shape.numel()
+
+        def get_device(self):
+            return 1
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 4096
+
+        def stride(self, i=None):
+            st = torch.empty(self.shape, device="meta").stride()
+            return st if i is None else st[i]
+
+    class Work:
+        def reserve(self, *sizes):
+            return Tensor(torch.uint8, 1 << 20)
+
+    calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: calls.append(name) or 0
+
+    monkeypatch.setattr(kc, "_library", Library)
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    cache = kc.KvCache(*(Tensor(torch.float8_e4m3fn, 4, 2, 16, 64) for _ in range(2)), *(Tensor(f32, 4, 2) for _ in range(2)))
+    rows, one = Tensor(torch.int64, 3), Tensor(i32, 1)
+    k = Tensor(bf16, 3, 2, 64)
+
+    def all_calls():
+        yield lambda: kc.kv_plan(one, one, Tensor(i32, 1, 2), Tensor(i32, 4), Tensor(i32, 2), Tensor(i32, 2), Tensor(i32, 2), rows, one, page=16)
+        yield lambda: kc.kv_append(cache, k, k, rows)
+        yield lambda: kc.cache_attention(cache, Tensor(bf16, 1, 3, 2, 64), Tensor(i32, 1, 2), one, out=Tensor(bf16, 1, 3, 2, 64), workspace=Work())
+        yield lambda: kc.prompt_attention(k, k, k, Tensor(i32, 2), out=Tensor(bf16, 3, 2, 64))
+
+    monkeypatch.setattr(kc, "_current_device", lambda: 0)
+    for call in all_calls():
+        with pytest.raises(ValueError, match="cuda:1"):
+            call()
+    assert calls == []
+    # on the current device the same arguments reach the library
+    monkeypatch.setattr(kc, "_current_device", lambda: 1)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
+    for call in all_calls():
+        call()
+    assert calls == ["dt_kv_plan", "dt_kv_append", "dt_cache_attention", "dt_prompt_attention"]

@@ -24,6 +24,8 @@
 namespace dt {
 
 constexpr int kKeyTile = 128;
+// Shared memory of a CTA, and what of it a kernel's static variables may take (with their alignment).
+constexpr uint32_t kSmemBytes = 227 * 1024, kStaticBytes = 1024;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // 32 lanes x 32 consecutive 32-bit columns, without waiting (tmem_wait_ld).

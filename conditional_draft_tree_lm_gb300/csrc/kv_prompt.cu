@@ -60,13 +60,6 @@ struct PromptParams {
   float c;                                 // scale * log2(e)
 };
 
-template <int HD>
-struct PromptSmem {
-  static constexpr uint32_t kOperand = kOperandBytes<HD>;
-  static constexpr uint32_t kQ = 0, kRing = 2 * kOperand, kOut = kRing + kStages * kOperand, kBars = kOut + 8 * 4096;
-  static constexpr uint32_t kBytes = kBars + 512 + 1024;  // + alignment
-};
-
 DT_DEVINL void tma_load_3d(uint32_t dst, const void* tmap, uint64_t* bar, int x, int y, int z) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
@@ -84,6 +77,17 @@ struct PromptItem {
 constexpr int kItemSlots = 4;
 struct __align__(16) PromptPlace {  // what a slot of the schedule holds
   int kvh, row0, len, pos0;  // len 0: nothing to do, < 0: no more items
+};
+
+// full, empty; q_full, q_free, s_full, o_full, told of two each, p_full of four; clean, dirty; item_full, item_free; answered and
+// what brings the places to 16 bytes
+constexpr int kPromptBarriers = 2 * kStages + 5 * 2 + 4 + 2 * kMaskedTiles + 2 * kItemSlots + 2;
+template <int HD>
+struct PromptSmem {
+  static constexpr uint32_t kOperand = kOperandBytes<HD>;
+  static constexpr uint32_t kQ = 0, kRing = 2 * kOperand, kOut = kRing + kStages * kOperand, kBars = kOut + 8 * 4096;
+  static constexpr uint32_t kPlaces = kBars + kPromptBarriers * 8, kBytes = kPlaces + kItemSlots * sizeof(PromptPlace) + 16 + kMaskedTiles * 16 + 1024;  // + alignment
+  static_assert(kPlaces % 16 == 0 && kBytes + kStaticBytes <= kSmemBytes, "");
 };
 
 // The place of item `at`, by a whole warp: sequence q's places stand from
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint64_t* item_full = told + 2;                // [kItemSlots] the schedule
   uint64_t* item_free = item_full + kItemSlots;  // [kItemSlots]
   uint64_t* answered = item_free + kItemSlots;
-  PromptPlace* places = reinterpret_cast<PromptPlace*>(answered + 2);         // [kItemSlots]; 16-byte aligned, as the answer is
+  PromptPlace* places = reinterpret_cast<PromptPlace*>(full + kPromptBarriers);  // [kItemSlots], behind `answered`; 16-byte aligned, as the answer is
   uint8_t* answer = reinterpret_cast<uint8_t*>(places + kItemSlots);          // 16 bytes
   uint32_t* bad_key = reinterpret_cast<uint32_t*>(answer + 16);  // [kMaskedTiles][4] keys of the masked tiles whose values are not finite
   __shared__ uint32_t tmem_slot;

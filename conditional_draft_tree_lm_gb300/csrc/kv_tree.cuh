@@ -165,21 +165,25 @@ DT_DEVINL void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t
                : "memory");
 }
 
-template <int HD>
-struct TreeSmem {
-  static constexpr uint32_t kOperand = kOperandBytes<HD>;
-  static constexpr uint32_t kQ = 0, kRing = 2 * kOperand, kStaging = kRing + kTreeStages * kOperand;
-  static constexpr uint32_t kStagingBytes = 2 * kKeyTile * HD;  // K, V: [key][channel] in 8 bits
-  static constexpr uint32_t kBars = kStaging + kStagingBytes;
-  static constexpr uint32_t kBytes = kBars + 768 + 1024;  // barriers and tiles' notes (720), alignment
-};
-
 // What goes with a key tile.
 struct alignas(8) TreeTile {
   float k_scale[8], v_scale[8], v_log[8];  // of 16 keys each, and the value scale's logarithm
   uint32_t seen[4];   // cached keys that exist (new ones: the keys below slots)
   uint32_t bad[4];    // keys whose values are not finite (new ones only)
   int plain;          // all keys exist
+};
+
+// full, empty; q_full, s_full, o_full, st_full, st_free of two each, p_full of four
+constexpr int kTreeBarriers = 2 * kTreeStages + 5 * 2 + 4;
+
+template <int HD>
+struct TreeSmem {
+  static constexpr uint32_t kOperand = kOperandBytes<HD>;
+  static constexpr uint32_t kQ = 0, kRing = 2 * kOperand, kStaging = kRing + kTreeStages * kOperand;
+  static constexpr uint32_t kStagingBytes = 2 * kKeyTile * HD;  // K, V: [key][channel] in 8 bits
+  static constexpr uint32_t kBars = kStaging + kStagingBytes, kTiles = kBars + kTreeBarriers * 8;
+  static constexpr uint32_t kBytes = kTiles + kTreeSlots * sizeof(TreeTile) + 1024;  // + alignment
+  static_assert(kTiles % alignof(TreeTile) == 0 && kBytes + kStaticBytes <= kSmemBytes, "");
 };
 
 // 16 bytes of global memory to shared memory, without a register; zeros where not `there`.
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
   uint64_t* o_full = p_full + 4;
   uint64_t* st_full = o_full + 2;   // [2] K, V in the staging place
   uint64_t* st_free = st_full + 2;  // [2]
-  TreeTile* tiles = reinterpret_cast<TreeTile*>(st_free + 2);  // [kTreeSlots]
+  TreeTile* tiles = reinterpret_cast<TreeTile*>(full + kTreeBarriers);  // [kTreeSlots], behind st_free
   __shared__ uint32_t tmem_slot;
   __shared__ int scratch[4], s_start[128 + 1], s_last;
 

@@ -218,7 +218,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
   fence_mbar_init();
   bars += warp * kStages;
   int issued = 0, used = 0;  // of this warp's steps
-  bool gave_up = false;      // a bounded wait did
+  // a bounded wait did (the same for a warp's lanes): from then on there are neither waits nor copies, the joins go on as ever,
+  // and the copies from `lost` on are waited for at the end
+  bool gave_up = false;
+  int lost = 0;
   TileRow<kDecodeThreads, DecodeTiles> row_of = {a.length, a.n_req, {max_len}, 0, s_start};
   row_of.sum(s_start + kDecodeThreads + 1);
   const int work = row_of.total() * n_kv;
@@ -261,7 +264,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
     steps = tok0 < sg.end ? (sg.end - tok0 + kDecodeTile - 1) / kDecodeTile : 0;
   };
   auto issue = [&](int i) {
-    if (i < steps) {
+    if (i < steps && !gave_up) {
       if ((i & 15) == 0) {
         const int tok = tok0 + (i + (lane >> 1)) * kDecodeTile + (lane & 1) * 16;
         float k1 = 0.0f, v1 = -1.0f;  // (a page out of range: as if it were not there)
@@ -519,7 +522,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
     }
 
     for (int i = 0; i < steps; ++i) {
-      gave_up |= !mbar_wait(&bars[used % kStages], (used / kStages) & 1, nullptr);
+      if (!gave_up && !__all_sync(0xFFFFFFFFu, mbar_wait(&bars[used % kStages], (used / kStages) & 1, nullptr))) {
+        gave_up = true;
+        lost = used;
+      }
       const uint8_t* st = ring + (used++ % kStages) * kDecodeWarps * Smem::kStep;
       __syncwarp();  // (every lane has read the step before this one: its place is free)
       issue(i + kStages - 1);
@@ -808,7 +814,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtas)
     if (!more) break;
     __syncthreads();  // (the join has been read)
   }
-  if (gave_up && a.status) atomicOr(a.status, DT_KV_TIMEOUT);
+  if (gave_up) {
+    if (a.status) atomicOr(a.status, DT_KV_TIMEOUT);
+    for (; lost < issued; ++lost) mbar_wait(&bars[lost % kStages], (lost / kStages) & 1, nullptr);  // (no copy may outlive the CTA)
+  }
   dt_grid_wait();
 }
 

@@ -39,6 +39,9 @@ DT_DEVINL void tmem_ld32(uint32_t taddr, uint32_t* v) {
         "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(taddr));
 }
+// A bounded wait by a whole warp, which goes on or gives up together.
+DT_DEVINL bool warp_wait(uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, nullptr)); }
+
 DT_DEVINL void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // (after the wait: ties the registers to it, so that nothing that uses them moves before it)
 DT_DEVINL void tmem_landed32(uint32_t* v) {

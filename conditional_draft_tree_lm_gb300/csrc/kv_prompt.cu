@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint8_t* answer = reinterpret_cast<uint8_t*>(places + kItemSlots);          // 16 bytes
   uint32_t* bad_key = reinterpret_cast<uint32_t*>(answer + 16);  // [kMaskedTiles][4] keys of the masked tiles whose values are not finite
   __shared__ uint32_t tmem_slot;
+  __shared__ __align__(8) uint64_t drained;  // all products are done
 
   // (the same for a warp's lanes, and known to be)
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
@@ -180,6 +181,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&item_free[i], kPromptThreads / 32 - 1);  // every warp but the scheduling one
     }
     mbar_init(answered, 1);
+    mbar_init(&drained, 1);
     for (int i = 0; i < 4 * kMaskedTiles; ++i) bad_key[i] = 0;
     fence_mbar_init();
   }
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   bool gave_up = false;  // a bounded wait did
   // the i-th item of this CTA into `it`; false: there is none (or a wait gave up)
   auto next_item = [&](int i) {
-    bool got = __all_sync(0xFFFFFFFFu, mbar_wait(&item_full[i % kItemSlots], (i / kItemSlots) & 1, nullptr));
+    bool got = warp_wait(&item_full[i % kItemSlots], (i / kItemSlots) & 1);
     gave_up |= !got;
     PromptPlace x = {0, 0, -1, 0};
     if (got) {
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       uint32_t masked_turns = 0;  // bit m: the parity of clean[m]'s next phase
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, nullptr));
+        ok = ok && warp_wait(bar, parity);
         tc_fence_after();
       };
       auto full_wait = [&](int i) { wait(&full[i % kStages], (i / kStages) & 1); };
@@ -323,8 +325,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // (the last warp also keeps the schedule, an item ahead)
       const bool plans = cw == kCleanWarps - 1;
       PromptPlace here = {0, 0, -1, 0}, ahead = here;
+      int asked = -1;
       auto publish = [&](int i, const PromptPlace& x) {
-        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&item_free[i % kItemSlots], ((i / kItemSlots) & 1) ^ 1, nullptr));
+        ok = ok && warp_wait(&item_free[i % kItemSlots], ((i / kItemSlots) & 1) ^ 1);
         if (lane == 0) {
           places[i % kItemSlots] = x;
           mbar_arrive(&item_full[i % kItemSlots]);
@@ -342,7 +345,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             take_next(answer, answered);
           }
           __syncwarp();
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(answered, i & 1, nullptr));
+          ok = warp_wait(answered, i & 1);
+          asked = i;
           const int id = ok ? taken(answer) : -1;
           __syncwarp();
           ahead.len = -1;
@@ -365,11 +369,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         if (lane < 2 * kMaskedTiles) bad_key[(lane >> 1) * 4 + cw * 2 + (lane & 1)] = 0;
         __syncwarp();
-        for (int j = it.masked0; j < it.n && ok; ++j) {
+        // (where a wait gives up the item goes on without waiting: lanes give up one by one, the warp's votes need them all)
+        for (int j = it.masked0; j < it.n; ++j) {
           const int m = j - it.masked0;
-          ok = mbar_wait(&dirty[m], turns >> m & 1u, nullptr);
+          ok = ok && mbar_wait(&dirty[m], turns >> m & 1u, nullptr);
           turns ^= 1u << m;
-          if (!ok) break;
           // (the swizzle stays within a key's 128 bytes)
           uint8_t* v = smem + Smem::kRing + ((load + 2 * j + 1) % kStages) * Smem::kOperand + cw * 64 * 128 + lane * 16;
           const int valid = it.len - j * kKeyTile - cw * 64 - (lane >> 3);  // of keys lane / 8, + 4, + 8, ...
@@ -400,8 +404,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (lane == 0) mbar_arrive(&clean[m]);
         }
         load += 2 * it.n;
+        ok = __all_sync(0xFFFFFFFFu, ok);
         if (plans && here.len < 0) break;
       }
+      if (!ok && asked >= 0) mbar_wait(answered, asked & 1, nullptr);  // (the answer is a write to this CTA, too)
       gave_up |= !ok;
     }
   } else {
@@ -423,7 +429,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int from = it.pos0 + t * p.positions, pos = from + over_group(r, p.inverse);
       SoftmaxRow row;
       for (int j = 0; j < n && ok; ++j) {
-        ok = mbar_wait(&s_full[t], s_use++ & 1, nullptr);
+        ok = warp_wait(&s_full[t], s_use++ & 1);
         if (!ok) break;
         tc_fence_after();
         const int seen = pos + 1 - j * kKeyTile;  // of this tile's keys, by this row
@@ -435,7 +441,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
       bool poison = false;
       if (n > 0) {
-        ok = ok && mbar_wait(&o_full[t], o_use++ & 1, nullptr);
+        ok = ok && warp_wait(&o_full[t], o_use++ & 1);
         tc_fence_after();
         // rows that see a key whose value is not finite (an item's cleaning is behind its o_full)
         for (int j = it.masked0; j < n; ++j)
@@ -484,6 +490,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
+    // (where a wait gave up: no product may outlive its operands and tensor memory)
+    if (elect_one()) tc_commit(&drained);
+    mbar_wait(&drained, 0, nullptr);
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

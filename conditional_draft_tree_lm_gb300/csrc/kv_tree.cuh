@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
   uint64_t* st_free = st_full + 2;  // [2]
   TreeTile* tiles = reinterpret_cast<TreeTile*>(full + kTreeBarriers);  // [kTreeSlots], behind st_free
   __shared__ uint32_t tmem_slot;
+  __shared__ __align__(8) uint64_t drained;  // all products are done
   __shared__ int scratch[4], s_start[128 + 1], s_last;
 
   // (the same for a warp's lanes, and known to be)
@@ -231,6 +232,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
       mbar_init(&st_full[t], 1);
       mbar_init(&st_free[t], kTreeConvWarps);
     }
+    mbar_init(&drained, 1);
     fence_mbar_init();
   }
   tc_fence_before();
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
         int p_use[2] = {0, 0}, q_use[2] = {0, 0};
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-          ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, nullptr));
+          ok = ok && warp_wait(bar, parity);
           tc_fence_after();
         };
         auto full_wait = [&](int i) { wait(&full[i % kTreeStages], (i / kTreeStages) & 1); };
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
           const size_t at = copies ? (static_cast<size_t>(gc.id) * n_kv + cur.kvh << p.shift) * HD : 0;
   #pragma unroll
           for (int which = 0; which < 2; ++which) {
-            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&st_free[which], (count & 1) ^ 1, nullptr));
+            ok = ok && warp_wait(&st_free[which], (count & 1) ^ 1);
             if (!ok) break;
             // (the place is free: the tile four before this one is behind its softmax, too)
             if (which == 0) {
@@ -542,7 +544,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
       float* stats = p.part + static_cast<size_t>(2 * pieces) * 2 * 128 * HD;
       int count = 0, s_use = 0, o_use = 0;
       bool ok = true;
-      // (where a wait gives up, likewise)
       auto ready = [&](int half) {
         if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
       };
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
               }
               if (!live) see[0] = see[1] = see[2] = see[3] = 0;
             }
-            ok = ok && mbar_wait(&s_full[t], s_use++ & 1, nullptr);
+            ok = ok && warp_wait(&s_full[t], s_use++ & 1);
             if (!ok) break;
             tc_fence_after();
             const TreeTile& info = tiles[(count + j) % kTreeSlots];
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             else if (masked) softmax_tile<HD, kWeights, true>(s_at, o_at, i == 0, false, scale, value, value_log, see, sm, ready);
             else softmax_tile<HD, kWeights, false>(s_at, o_at, i == 0, false, scale, value, value_log, see, sm, ready);
           }
-          if (steps > 0) ok = ok && mbar_wait(&o_full[t], o_use++ & 1, nullptr);
+          if (steps > 0) ok = ok && warp_wait(&o_full[t], o_use++ & 1);
           tc_fence_after();
         }
         count += n;
@@ -769,6 +770,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
   tc_fence_before();
   __syncthreads();
   if (warp == kTreeMmaWarp) {
+    // (where a wait gave up: no product may outlive its operands and tensor memory)
+    if (elect_one()) tc_commit(&drained);
+    mbar_wait(&drained, 0, nullptr);
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -11,6 +11,9 @@
 
 namespace dt {
 
+// Rows or tokens by which a kernel's counts may pass the last one: 16 steps of 128 tokens, a tile more, and room.
+constexpr int kAhead = 4095;
+
 // Row tiles of a call with more than 16 rows per key/value head: pairs, the odd one, and
 // the first slot of those left to the streaming kernel (0: none).  It takes them where
 // the odd tile holds 16 rows at most and there are 32 key/value heads over all
@@ -31,7 +34,7 @@ struct RowTiles {
 }  // namespace dt
 
 extern "C" size_t dt_cache_attention_workspace(int n_req, int slots, int n_q, int n_kv, int head_dim) {
-  if (n_req < 1 || slots < 1 || n_kv < 1 || n_q < n_kv || n_q % n_kv != 0 || (head_dim != 64 && head_dim != 128)) return 0;
+  if (n_req < 1 || slots < 1 || slots > 0x7FFFFFFF - dt::kAhead || n_kv < 1 || n_q < n_kv || n_q % n_kv != 0 || (head_dim != 64 && head_dim != 128)) return 0;
   if (static_cast<int64_t>(slots) * (n_q / n_kv) <= dt::kDecodeMaxRows) return dt::decode_workspace(slots * (n_q / n_kv), head_dim);
   if (n_q / n_kv > 128) return 0;
   const dt::RowTiles tiles(n_req, slots, n_q / n_kv, n_kv);
@@ -49,8 +52,9 @@ extern "C" dt_status dt_cache_attention(const dt_kv_cache* cache, const dt_cache
   if (a.n_q % cache->n_kv != 0 || a.n_q / cache->n_kv > 128)
     return kv_fail(DT_ERR_SHAPE, "%s: %d query heads over %d key/value heads: need a multiple, at most 128 a head", who,
                    a.n_q, cache->n_kv);
-  if (static_cast<int64_t>(a.n_req) * a.slots > 0x7FFFFFFF || static_cast<int64_t>(a.max_blocks) * cache->page > 0x7FFFFFFF)
-    return kv_fail(DT_ERR_SHAPE, "%s: more than 2^31-1 rows or tokens", who);
+  // (positions are counted some tiles ahead, in 32 bits)
+  if (static_cast<int64_t>(a.n_req) * a.slots > 0x7FFFFFFF - kAhead || static_cast<int64_t>(a.max_blocks) * cache->page > 0x7FFFFFFF - kAhead)
+    return kv_fail(DT_ERR_SHAPE, "%s: more than 2^31-%d rows or tokens", who, kAhead + 1);
   if (!(a.scale - a.scale == 0.0f)) return kv_fail(DT_ERR_INVALID_ARG, "%s: scale is not finite", who);
   if (!a.block_table || !a.length || !kv_rows_ok(a.q, a.q_row_stride, a.q_head_stride) ||
       !kv_rows_ok(a.out, a.out_row_stride, a.out_head_stride))

@@ -498,7 +498,7 @@ dt_status dt_kv_append(const dt_kv_cache* cache, const dt_kv_append_args* args, 
  * and calls that share one must not overlap.  status as in dt_kv_append (a page
  * out of range counts as not there; DT_KV_TIMEOUT is or'ed in too). */
 typedef struct dt_cache_attention_args {
-  int n_req, slots, n_q, max_blocks;
+  int n_req, slots, n_q, max_blocks; /* n_req * slots and max_blocks * page: at most 2^31 - 4096 */
   float scale;             /* finite */
   const void* q;           /* rows of heads, n_q x head_dim */
   int64_t q_row_stride, q_head_stride;

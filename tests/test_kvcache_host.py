@@ -79,3 +79,28 @@ def test_every_binding_asks_for_its_stream_before_it_launches(monkeypatch):
     for call in all_calls():
         call()
     assert calls == ["dt_kv_plan", "dt_kv_append", "dt_cache_attention", "dt_prompt_attention"]
+
+
+def test_sizes_that_32_bit_counts_would_pass_are_refused():
+    """Lengths and rows up to 2^31-4097 may be asked for; behind that a count some tiles ahead would turn negative."""
+    import ctypes
+    from conditional_draft_tree_lm_gb300 import build as dtbuild
+    dtbuild.build_library()
+    lib = kc._library()
+
+    def refused(**kw):
+        c = kc._Cache(256, 256, 256, 256, 4, kw.pop("page", 128), 1, 128)
+        a = kc._Attend(n_req=1, slots=1, n_q=1, max_blocks=1, scale=1.0, q=256, block_table=256, length=256, out=256,
+                       workspace=256, workspace_bytes=0)
+        for k, v in kw.items():
+            setattr(a, k, v)
+        return lib.dt_cache_attention(ctypes.byref(c), ctypes.byref(a), None), lib.dt_last_error().decode()
+
+    # (the workspace of no bytes refuses what the sizes let through, before any CUDA call)
+    for kw, msg in ((dict(max_blocks=2 ** 24 - 32), "workspace"), (dict(max_blocks=2 ** 24 - 31), "2^31-4096"),
+                    (dict(max_blocks=2 ** 27 - 1, page=16), "2^31-4096"), (dict(max_blocks=2 ** 27 - 256, page=16), "workspace"),
+                    (dict(slots=2 ** 31 - 4096), "workspace"), (dict(slots=2 ** 31 - 4095), "2^31-4096"),
+                    (dict(slots=2 ** 30, n_req=2), "2^31-4096")):
+        err, text = refused(**kw)
+        assert err != 0 and msg in text, (kw, text)
+    assert lib.dt_cache_attention_workspace(1, 2 ** 31 - 1, 1, 1, 128) == 0

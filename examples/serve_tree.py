@@ -61,6 +61,8 @@ class Server:
         self.length = [torch.zeros(n, dtype=i32, device=dev) for _ in range(2)]
         self.ring = [torch.tensor([0, pages], dtype=i32, device=dev), torch.zeros(2, dtype=i32, device=dev)]
         self.row_start = torch.zeros(n + 1, dtype=i32, device=dev)
+        # what any call has reported: a plan writes its own word, the others add theirs
+        self.planned = torch.zeros(1, dtype=i32, device=dev)
         self.status = torch.zeros(1, dtype=i32, device=dev)
 
     def plan(self, max_rows, **kw):
@@ -69,7 +71,8 @@ class Server:
         slots = torch.empty(max_rows, dtype=torch.int64, device="cuda")
         src = torch.empty(max_rows, dtype=torch.int32, device="cuda")
         kv_plan(self.length[0], self.length[1], self.table, self.free, self.ring[0], self.ring[1], self.row_start, slots,
-                self.status, page=self.page, src_rows=src, **kw)
+                self.planned, page=self.page, src_rows=src, **kw)
+        self.status |= self.planned
         self.length.reverse()
         self.ring.reverse()
         return slots, src
@@ -81,8 +84,8 @@ class Server:
         tokens = torch.cat(prompts)
         q, k, v = self.target.project(tokens)
         slots, _ = self.plan(tokens.numel(), delta=torch.tensor([p.numel() for p in prompts], dtype=torch.int32, device="cuda"))
-        attended = prompt_attention(q, k, v, self.row_start)
-        kv_append(self.cache, k, v, slots)
+        attended = prompt_attention(q, k, v, self.row_start, status=self.status)
+        kv_append(self.cache, k, v, slots, status=self.status)
         return self.target.logits(attended[(self.row_start[1:] - 1).long()])
 
     def score_tree(self, tree):
@@ -90,7 +93,7 @@ class Server:
         from conditional_draft_tree_lm_gb300 import cache_attention
         q, k, v = self.target.project(tree["tok"])
         attended = cache_attention(self.cache, q, self.table, self.length[0], k_new=k, v_new=v, mask=tree["mask"],
-                                   workspace=self.work)
+                                   workspace=self.work, status=self.status)
         return self.target.logits(attended), k, v
 
     def commit(self, walk, k, v):
@@ -99,7 +102,7 @@ class Server:
         n, slots = k.shape[:2]
         where, src = self.plan(n * (walk["accepted"].shape[1] + 1), delta=walk["accept_len"], extra=1,
                                path=walk["accepted"], path_rows=slots)
-        kv_append(self.cache, k, v, where, src_rows=src)
+        kv_append(self.cache, k, v, where, src_rows=src, status=self.status)
 
 
 def serve(requests=3, rounds=8, follow=0.7, seed=0):
@@ -136,7 +139,7 @@ def serve(requests=3, rounds=8, follow=0.7, seed=0):
         counts.append(acc)
         root = walk["bonus"]
     if server.status.item() != 0 or builder.device_status() != 0:
-        raise RuntimeError(f"plan status {server.status.item()}, builder status {builder.device_status()}")
+        raise RuntimeError(f"cache status {server.status.item()}, builder status {builder.device_status()}")
     builder.close()
     return server, committed, counts
 

@@ -109,6 +109,12 @@ inline bool kv_rows_ok(const void* p, int64_t row_stride, int64_t head_stride) {
          row_stride % 8 == 0 && head_stride % 8 == 0;
 }
 
+// Rows of heads that are written: no two of them may share an element.
+inline bool kv_rows_apart(int64_t rows, int heads, int head_dim, int64_t row_stride, int64_t head_stride) {
+  return (rows == 1 || row_stride >= head_dim) && (heads == 1 || head_stride >= head_dim) &&
+         (rows == 1 || heads == 1 || row_stride >= (heads - 1) * head_stride + head_dim || head_stride >= (rows - 1) * row_stride + head_dim);
+}
+
 dt_status kv_check_cache(const char* who, const dt_kv_cache* c);
 
 // Rows of heads in bf16 (strides in elements) as a 3D tensor map: boxes of 64 channels x heads x rows, swizzled.

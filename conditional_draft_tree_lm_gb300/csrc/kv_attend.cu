@@ -59,6 +59,8 @@ extern "C" dt_status dt_cache_attention(const dt_kv_cache* cache, const dt_cache
   if (!a.block_table || !a.length || !kv_rows_ok(a.q, a.q_row_stride, a.q_head_stride) ||
       !kv_rows_ok(a.out, a.out_row_stride, a.out_head_stride))
     return kv_fail(DT_ERR_INVALID_ARG, "%s: null or misaligned q, out, block_table or length", who);
+  if (!kv_rows_apart(static_cast<int64_t>(a.n_req) * a.slots, a.n_q, cache->head_dim, a.out_row_stride, a.out_head_stride))
+    return kv_fail(DT_ERR_INVALID_ARG, "%s: rows of out overlap", who);
   if ((a.k_new != nullptr) != (a.v_new != nullptr) ||
       (a.k_new && (!kv_rows_ok(a.k_new, a.k_row_stride, a.k_head_stride) || !kv_rows_ok(a.v_new, a.v_row_stride, a.v_head_stride))))
     return kv_fail(DT_ERR_INVALID_ARG, "%s: k_new and v_new: one is null or misaligned", who);

@@ -527,6 +527,8 @@ extern "C" dt_status dt_prompt_attention(const dt_prompt_attention_args* args, v
   if (!a.row_start || !kv_rows_ok(a.q, a.q_row_stride, a.q_head_stride) || !kv_rows_ok(a.k, a.k_row_stride, a.k_head_stride) ||
       !kv_rows_ok(a.v, a.v_row_stride, a.v_head_stride) || !kv_rows_ok(a.out, a.out_row_stride, a.out_head_stride))
     return kv_fail(DT_ERR_INVALID_ARG, "%s: null or misaligned q, k, v, out or row_start", who);
+  if (!kv_rows_apart(a.n_rows, a.n_q, a.head_dim, a.out_row_stride, a.out_head_stride))
+    return kv_fail(DT_ERR_INVALID_ARG, "%s: rows of out overlap", who);
   PromptParams p = {};
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;

@@ -381,7 +381,7 @@ dt_status dt_topm_noalloc(const float* logits, int rows, int V, int M, float T, 
  * as a pointer and two strides in elements: element (row, head, c) stands at
  * data[row * row_stride + head * head_stride + c]; data must be 16-byte aligned
  * and the strides multiples of 8.  Query head h uses key/value head
- * h / (n_q / n_kv).
+ * h / (n_q / n_kv).  Rows that are written must not share elements.
  * Messages of refused calls are in dt_last_error().
  * ------------------------------------------------------------------------ */
 

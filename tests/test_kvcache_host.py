@@ -90,7 +90,7 @@ def test_sizes_that_32_bit_counts_would_pass_are_refused():
 
     def refused(**kw):
         c = kc._Cache(256, 256, 256, 256, 4, kw.pop("page", 128), 1, 128)
-        a = kc._Attend(n_req=1, slots=1, n_q=1, max_blocks=1, scale=1.0, q=256, block_table=256, length=256, out=256,
+        a = kc._Attend(n_req=1, slots=1, n_q=1, max_blocks=1, scale=1.0, q=256, block_table=256, length=256, out=256, out_row_stride=128,
                        workspace=256, workspace_bytes=0)
         for k, v in kw.items():
             setattr(a, k, v)
@@ -104,3 +104,22 @@ def test_sizes_that_32_bit_counts_would_pass_are_refused():
         err, text = refused(**kw)
         assert err != 0 and msg in text, (kw, text)
     assert lib.dt_cache_attention_workspace(1, 2 ** 31 - 1, 1, 1, 128) == 0
+
+
+@pytest.mark.parametrize("row,head,overlaps", [(0, 128, True), (512, 0, True), (512, 64, True), (504, 128, True), (128, 128, True),
+                                               (512, 128, False), (640, 128, False), (128, 768, False), (128, 640, True), (1024, 256, False)])
+def test_outputs_whose_rows_overlap_are_refused(row, head, overlaps):
+    """Six rows of four heads of 128, by their strides; what passes is refused for its workspace of no bytes."""
+    import ctypes
+    from conditional_draft_tree_lm_gb300 import build as dtbuild
+    dtbuild.build_library()
+    lib = kc._library()
+    c = kc._Cache(256, 256, 256, 256, 4, 64, 2, 128)
+    a = kc._Attend(n_req=2, slots=3, n_q=4, max_blocks=1, scale=1.0, q=256, block_table=256, length=256, out=256, out_row_stride=row,
+                   out_head_stride=head, workspace=256, workspace_bytes=0)
+    assert lib.dt_cache_attention(ctypes.byref(c), ctypes.byref(a), None) != 0
+    assert (b"overlap" in lib.dt_last_error()) == overlaps
+    p = kc._Prompt(n_seq=1, n_q=4, n_kv=2, head_dim=128, n_rows=6, scale=1.0, q=256, k=256, v=256, out=256, out_row_stride=row,
+                   out_head_stride=head, row_start=256)
+    if overlaps:
+        assert lib.dt_prompt_attention(ctypes.byref(p), None) != 0 and b"overlap" in lib.dt_last_error()

@@ -16,10 +16,15 @@ constexpr int kAhead = 4095;
 
 // Row tiles of a call with more than 16 rows per key/value head: pairs, the odd one, and
 // the first slot of those left to the streaming kernel (0: none).  It takes them where
-// the odd tile holds 16 rows at most and there are 32 key/value heads over all
-// requests.  65 slots of 4 heads a group, 8 key/value heads, us without and with it: 32
-// requests of up to 4k tokens 305 and 228, of up to 512 148 and 101; 4 requests of
-// up to 4k 63 and 60; but one request of 2k tokens 53 and 59, of 32k 119 and 149.
+// the odd tile holds 16 rows at most, there are 8 key/value heads over all requests, for its
+// pieces, and 32 pairs over all of them, which the odd tiles would keep from the SMs.  us without and
+// with it (8 key/value heads of 128, 4 heads a group, where nothing else is said):
+//   65 slots, 32 requests of up to 4k tokens 307 and 209, of up to 512 129 and 97; 8 requests of 4k 102 and 77; 4 of 4k 61 and
+//     55, of 512 36 and 38; but 2 of 4k 52 and 75, 1 of 32k 114 and 138; head_dim 64: 32 requests 228 and 134, 4 39 and 30
+//   129 slots, 32 requests of 4k 454 and 346; 2 of 32k 168 and 151; but 1 of 4k 49 and 53, of 32k 126 and 127
+//   257 slots, 1 request of 2k 58 and 50, of 32k 183 and 187; 513 slots, 1 of 32k 336 and 311, of 2k 72 and 74
+//   34 slots of 8 heads a group, 32 requests 309 and 220, 4 63 and 62; 1 of 8k 70 and 108
+//   513 slots over 2 key/value heads, 2 requests of 16k 88 and 101; 65 slots over 1, 32 requests of 4k 66 and 60
 struct RowTiles {
   int pairs, odd, rest;
   RowTiles(int n_req, int slots, int group, int n_kv) {
@@ -27,7 +32,8 @@ struct RowTiles {
     pairs = tiles / 2;
     odd = tiles % 2;
     const int first = (tiles - 1) * per_tile;
-    rest = odd && pairs > 0 && (slots - first) * group <= kDecodeMaxRows && static_cast<int64_t>(n_req) * n_kv >= 32 ? first : 0;
+    const int64_t heads = static_cast<int64_t>(n_req) * n_kv;
+    rest = odd && pairs > 0 && (slots - first) * group <= kDecodeMaxRows && heads >= 8 && heads * pairs >= 32 ? first : 0;
   }
 };
 

@@ -53,3 +53,13 @@ def test_keys_of_other_dimensions_are_refused():
         with pytest.raises(ValueError):
             kv_append(cache, k, k, dev([0], torch.int64))
     torch.cuda.synchronize()
+
+
+# (rows left over behind two, four and eight pairs of row tiles, which the streaming kernel takes from 8 key/value heads on)
+@pytest.mark.parametrize("lens,slots,heads,kv,hd,page,fresh", [
+    ([700, 33], 129, 32, 8, 128, 64, "tree"), ([300], 257, 32, 8, 64, 32, "random"), ([0], 513, 32, 8, 128, 64, "tree"),
+    ([150, 0, 40], 513, 8, 2, 128, 16, "tree"), ([40], 259, 16, 16, 128, 128, "causal"),
+])
+def test_rows_left_over_behind_several_pairs(lens, slots, heads, kv, hd, page, fresh):
+    c = cache_case(np.random.RandomState(slots + kv), lens, slots, heads, kv, hd, page, fresh)
+    check_cache(c, run_cache(c), rows=[0, 31, slots // 2, *range(slots - 4, slots)])

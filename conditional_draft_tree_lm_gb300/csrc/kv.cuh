@@ -44,9 +44,6 @@ DT_DEVINL float move_unit(float weight, float m, float& u, float& high) {
 
 constexpr int kSms = 152;  // of a GB300: grids of one wave
 
-// Largest finite e4m3 magnitude: 1.75 * 2^8.
-constexpr float kE4m3Max = 448.0f;
-
 // Smallest power of two s in [2^-126, 2^120] with 448 s >= amax (amax finite,
 // >= 0).  448 = 1.75 * 2^8, so with amax = m 2^k (1 <= m < 2) s is 2^(k-8)
 // where m <= 1.75 and 2^(k-7) above: read off the bits, no logarithm.
@@ -122,8 +119,5 @@ bool kv_tmap_heads(CUtensorMap* tm, const void* base, int head_dim, int heads, i
                    int64_t row_stride, int box_heads, int box_rows);
 // Contiguous rows of 64 or 128 bytes as a 2D map of bytes, swizzled by the row's length: boxes of whole rows.
 bool kv_tmap_rows(CUtensorMap* tm, const void* base, int row_bytes, int64_t rows, int box_rows);
-
-// SM count of the current device.
-cudaError_t kv_num_sms(int* n);
 
 }  // namespace dt

@@ -1,8 +1,6 @@
 // Host-side helpers of the key/value cache entry points.
 #include <cuda.h>
 
-#include <mutex>
-
 #include "kv.cuh"
 
 namespace dt {
@@ -65,22 +63,6 @@ bool kv_tmap_rows(CUtensorMap* tm, const void* base, int row_bytes, int64_t rows
   return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-cudaError_t kv_num_sms(int* n) {
-  static std::mutex mu;
-  static int known[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  std::lock_guard<std::mutex> lock(mu);
-  if (!known[dev]) {
-    e = cudaDeviceGetAttribute(&known[dev], cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-  }
-  *n = known[dev];
-  return cudaSuccess;
 }
 
 }  // namespace dt

@@ -206,17 +206,16 @@ extern "C" dt_status dt_kv_plan(const dt_kv_plan_args* args, void* stream) {
   if (a.path && (!a.src_rows || a.path_len < 0 || a.path_rows < 1 ||
                  static_cast<int64_t>(a.n_req) * a.path_rows > 0x7FFFFFFF))
     return kv_fail(DT_ERR_INVALID_ARG, "%s: a path needs src_rows, path_len >= 0 and path_rows >= 1", who);
-  int sms = 0;
-  cudaError_t e = kv_num_sms(&sms);
+  cudaError_t e = cudaSuccess;
   const size_t smem = (a.n_req + 1) * sizeof(PlanReq);
-  if (e == cudaSuccess && smem > 46 * 1024)
+  if (smem > 46 * 1024)
     e = cudaFuncSetAttribute(k_kv_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return kv_launched(who, e);
   int shift = 4;
   while ((1 << shift) < a.page) ++shift;
   // four rows a thread, so that the sums are formed by few CTAs, up to one CTA per SM
   int64_t grid = (a.max_rows + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
-  grid = grid > sms ? sms : grid;
+  grid = grid > kSms ? kSms : grid;
   k_kv_plan<<<static_cast<int>(grid), kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(a, shift);
   return kv_launched(who, cudaGetLastError());
 }

@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + t * 128 + lanes, o_at = tmem + 256 + t * 128 + lanes;
-    const float c = p.c;
+    float c = 0.0f;
     int s_use = 0, o_use = 0;
     bool ok = true;
     auto scale = [&](int) { return make_float2(c, c); };
@@ -427,7 +427,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (it.n == 0) continue;
       const int n = t == 0 ? it.n_tiles[0] : it.n_tiles[1];
       const int from = it.pos0 + t * p.positions, pos = from + over_group(r, p.inverse);
+      // (a row of the tile without a query gets its S from whatever stands in Q's place, the next sequence or an earlier item:
+      // with a factor of 0 and a maximum of 0 it has no say in when the warp's rows are rescaled, whatever S is)
+      const bool query = r < p.group * p.positions && pos < it.len;
       SoftmaxRow row;
+      c = query ? p.c : 0.0f;
+      row.m = query ? -INFINITY : 0.0f;
       for (int j = 0; j < n && ok; ++j) {
         ok = warp_wait(&s_full[t], s_use++ & 1);
         if (!ok) break;
@@ -435,9 +440,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int seen = pos + 1 - j * kKeyTile;  // of this tile's keys, by this row
         const uint32_t see[4] = {first_bits(seen, 0), first_bits(seen, 1), first_bits(seen, 2), first_bits(seen, 3)};
         if ((j + 1) * kKeyTile > from + 1)
-          softmax_tile<HD, kProbs, true>(s_at, o_at, j == 0, c < 0.0f, scale, scale, scale, see, row, ready);
+          softmax_tile<HD, kProbs, true>(s_at, o_at, j == 0, p.c < 0.0f, scale, scale, scale, see, row, ready);
         else
-          softmax_tile<HD, kProbs, false>(s_at, o_at, j == 0, c < 0.0f, scale, scale, scale, see, row, ready);
+          softmax_tile<HD, kProbs, false>(s_at, o_at, j == 0, p.c < 0.0f, scale, scale, scale, see, row, ready);
       }
       bool poison = false;
       if (n > 0) {

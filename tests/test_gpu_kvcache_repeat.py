@@ -63,3 +63,30 @@ def test_prompt_attention_gives_the_same_bits_every_time():
         assert status.item() == 0 and differ.item() == 0
         seen = torch.isfinite(first).flatten(1).all(1).cpu().numpy()
         np.testing.assert_array_equal(seen, finite)
+
+
+@pytest.mark.parametrize("heads,kv,hd", [(6, 2, 128), (7, 1, 64), (40, 8, 128), (6, 1, 64), (100, 2, 128)])
+def test_prompt_attention_of_odd_groups_gives_the_same_bits_every_time(heads, kv, hd):
+    """Where a group's heads do not divide 128, a tile has rows without a query; and a sequence's last tile has rows of the
+    next one's, whose queries are changed in between: neither has a say in a row's bits."""
+    torch = _t()
+    from conditional_draft_tree_lm_gb300 import prompt_attention
+    rs = np.random.RandomState(72)
+    lens = rs.randint(1, 700, 12)
+    at = np.concatenate([[0], np.cumsum(lens)])
+    n = int(at[-1])
+    q, k, v = (dev(rs.randn(n, x, hd), torch.bfloat16) for x in (heads, kv, kv))
+    other = q.clone()
+    for i in range(1, 12, 2):  # every other sequence's queries
+        other[at[i]:at[i + 1]] *= 30
+    loud = [30 * dev(rs.randn(900, x, hd), torch.bfloat16) for x in (8 * kv, kv, kv)]
+    start, one = dev(at, torch.int32), dev([0, 900], torch.int32)
+    same = torch.cat([torch.arange(at[i], at[i + 1]) for i in range(0, 12, 2)]).cuda()
+    first, differ = prompt_attention(q, k, v, start), torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(60):
+        if i % 3 == 0:
+            prompt_attention(*loud, one)
+        differ += (prompt_attention(q, k, v, start).view(torch.int16) != first.view(torch.int16)).sum()
+        got = prompt_attention(other, k, v, start)
+        differ += (got[same].view(torch.int16) != first[same].view(torch.int16)).sum()
+    assert differ.item() == 0

@@ -223,7 +223,8 @@ constexpr float kUnitNew = 16.0f;
 // One 128-key tile of a row: S at s_at becomes P there, and the row's state (and O, where its unit changes: for
 // kProbs with m) is brought up to date.  scale(g): what turns a raw logit of keys 16 g .. 16 g + 15 into
 // powers of two; value(g), value_log(g): those keys' value scale and its logarithm (kWeights).  All three are asked for
-// two g at a time, by g / 2.  negative: the scale's sign is negative (kProbs only).  see: the row's visible keys, all of them unless MASKED.  ready(i):
+// two g at a time, by g / 2.  NEGATIVE: the scale is (as code of its own: beside the other's it cost 65 of 440 us in the
+// tree kernel, whose queries take the sign instead, and 11 of 278 for 48 prompts').  see: the row's visible keys, all of them unless MASKED.  ready(i):
 // called when half i of P is stored.
 // kWeightPairs: a weight goes to the product as the sum of two bf16 (its first 8 bits, cut off, and the rest
 // rounded: 2^-16 relative), since a new token's values come in bf16, which fp16 cannot hold beside each other.  The
@@ -233,8 +234,8 @@ constexpr float kUnitNew = 16.0f;
 // between the maximum and the exponentials, loops unrolled: 48 prompts of up to 1k
 // tokens 300 us instead of 272, 16k tokens 1380 instead of 1367).  One body for
 // masked tiles and others costs more than it saves there: 288 and 1650 us.
-template <int HD, int P, bool MASKED, class Scale, class Value, class ValueLog, class Ready>
-DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, bool negative, Scale scale, Value value, ValueLog value_log,
+template <int HD, int P, bool MASKED, bool NEGATIVE, class Scale, class Value, class ValueLog, class Ready>
+DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, Scale scale, Value value, ValueLog value_log,
                             const uint32_t (&see)[4], SoftmaxRow& row, Ready ready) {
   constexpr bool SPLIT = P == kWeightPairs;
   uint32_t s[64];
@@ -251,7 +252,7 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, bool negat
     tmem_ld32(s_at + 32 * ((w + 1) & 3), s + 32 * (w1 ^ 1));  // (the last one: the first, for the second reading)
     const float2 scale2 = scale(w), log2v = P == kWeights ? value_log(w) : make_float2(0.0f, 0.0f);
     if (MASKED) {
-      const uint32_t out = P == kProbs && negative ? 0x7F800000u : 0xFF800000u;
+      const uint32_t out = NEGATIVE ? 0x7F800000u : 0xFF800000u;
       const uint32_t bits = w1 == 0 ? (w2 == 0 ? see[0] : see[2]) : (w2 == 0 ? see[1] : see[3]);
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = bits >> i & 1u ? v[i] : out;
@@ -259,7 +260,7 @@ DT_DEVINL void softmax_tile(uint32_t s_at, uint32_t o_at, bool first, bool negat
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float a = __uint_as_float(v[16 * h]), b = __uint_as_float(v[16 * h + 1]);
-      if (P != kProbs || !negative) {
+      if (!NEGATIVE) {
 #pragma unroll
         for (int i = 2; i < 16; i += 4) {
           a = fmaxf(fmaxf(a, __uint_as_float(v[16 * h + i])), __uint_as_float(v[16 * h + i + 1]));

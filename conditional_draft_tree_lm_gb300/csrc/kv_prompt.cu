@@ -129,7 +129,7 @@ DT_DEVINL void prompt_item(const PromptParams& p, const PromptPlace& x, PromptIt
   it.masked0 = (x.pos0 + 1) / kKeyTile;
 }
 
-template <int HD>
+template <int HD, bool NEGATIVE>  // NEGATIVE: the softmax's scale is
 __global__ void __launch_bounds__(kPromptThreads, 1)
     k_prompt(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v, const PromptParams p) {
@@ -440,9 +440,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int seen = pos + 1 - j * kKeyTile;  // of this tile's keys, by this row
         const uint32_t see[4] = {first_bits(seen, 0), first_bits(seen, 1), first_bits(seen, 2), first_bits(seen, 3)};
         if ((j + 1) * kKeyTile > from + 1)
-          softmax_tile<HD, kProbs, true>(s_at, o_at, j == 0, p.c < 0.0f, scale, scale, scale, see, row, ready);
+          softmax_tile<HD, kProbs, true, NEGATIVE>(s_at, o_at, j == 0, scale, scale, scale, see, row, ready);
         else
-          softmax_tile<HD, kProbs, false>(s_at, o_at, j == 0, p.c < 0.0f, scale, scale, scale, see, row, ready);
+          softmax_tile<HD, kProbs, false, NEGATIVE>(s_at, o_at, j == 0, scale, scale, scale, see, row, ready);
       }
       bool poison = false;
       if (n > 0) {
@@ -503,12 +503,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
 }
 
-template <int HD>
+template <int HD, bool NEGATIVE>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PromptParams& p, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(k_prompt<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem<HD>::kBytes);
+  cudaError_t e = cudaFuncSetAttribute(k_prompt<HD, NEGATIVE>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem<HD>::kBytes);
   if (e != cudaSuccess) return e;
   const int items = p.slots * p.n_kv;
-  k_prompt<HD><<<items, kPromptThreads, PromptSmem<HD>::kBytes, st>>>(q, k, v, p);
+  k_prompt<HD, NEGATIVE><<<items, kPromptThreads, PromptSmem<HD>::kBytes, st>>>(q, k, v, p);
   return cudaGetLastError();
 }
 
@@ -558,5 +558,6 @@ extern "C" dt_status dt_prompt_attention(const dt_prompt_attention_args* args, v
       !kv_tmap_heads(&v, a.v, a.head_dim, a.n_kv, a.n_rows, a.v_head_stride, a.v_row_stride, 1, kKeyTile))
     return kv_fail(DT_ERR_SHAPE, "%s: strides that a tensor map does not take (zero, or 2^40 bytes and more)", who);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return kv_launched(who, a.head_dim == 64 ? launch<64>(q, k, v, p, st) : launch<128>(q, k, v, p, st));
+  if (p.c < 0.0f) return kv_launched(who, a.head_dim == 64 ? launch<64, true>(q, k, v, p, st) : launch<128, true>(q, k, v, p, st));
+  return kv_launched(who, a.head_dim == 64 ? launch<64, false>(q, k, v, p, st) : launch<128, false>(q, k, v, p, st));
 }

@@ -653,9 +653,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree(const TreeParams p) {
             };
             auto value = [&](int w) { return *reinterpret_cast<const float2*>(&info.v_scale[2 * w]); };
             auto value_log = [&](int w) { return *reinterpret_cast<const float2*>(&info.v_log[2 * w]); };
-            if (fresh) softmax_tile<HD, kWeightPairs, true>(s_at, o_at, i == 0, false, scale, value, value_log, see, sm, ready);
-            else if (masked) softmax_tile<HD, kWeights, true>(s_at, o_at, i == 0, false, scale, value, value_log, see, sm, ready);
-            else softmax_tile<HD, kWeights, false>(s_at, o_at, i == 0, false, scale, value, value_log, see, sm, ready);
+            if (fresh) softmax_tile<HD, kWeightPairs, true, false>(s_at, o_at, i == 0, scale, value, value_log, see, sm, ready);
+            else if (masked) softmax_tile<HD, kWeights, true, false>(s_at, o_at, i == 0, scale, value, value_log, see, sm, ready);
+            else softmax_tile<HD, kWeights, false, false>(s_at, o_at, i == 0, scale, value, value_log, see, sm, ready);
           }
           if (steps > 0) ok = ok && warp_wait(&o_full[t], o_use++ & 1);
           tc_fence_after();

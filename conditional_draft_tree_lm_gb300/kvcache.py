@@ -97,9 +97,15 @@ def _library():
     return _lib
 
 
+_cuda = None
+
+
 def _current_device():
-    import torch
-    return torch._C._cuda_getDevice()
+    global _cuda
+    if _cuda is None:
+        import torch
+        _cuda = torch._C
+    return _cuda._cuda_getDevice()
 
 
 def _stream(stream, index):
@@ -212,8 +218,12 @@ class AttentionWorkspace:
                     self.buffer = torch.zeros(max(need, 256), dtype=torch.uint8, device=device)
                 self.streams = {_stream(stream, self.buffer.get_device())}
             self.sizes = sizes
-        raw = _stream(stream, self.buffer.get_device())
+        return self._on(stream, _stream(stream, self.buffer.get_device()))
+
+    def _on(self, stream, raw):
+        """The buffer, for work on `stream` (whose handle is `raw`)."""
         if raw not in self.streams:
+            import torch
             self.streams.add(raw)
             self.buffer.record_stream(torch.cuda.current_stream(self.buffer.device) if stream is None else stream)
         return self.buffer
@@ -304,14 +314,16 @@ def cache_attention(cache, q, block_table, length, *, k_new=None, v_new=None, ma
         vp, vr, vh = _heads(v_new, lead, cache.n_kv, dim, "v_new", dev)
     qp, qr, qh = _heads(q, lead, heads, dim, "q", dev)
     op, orow, oh = _heads(out, lead, heads, dim, "out", dev)
-    buf = workspace.reserve(n, slots, heads, cache.n_kv, dim, dev, stream)
+    raw = _stream(stream, dev)
+    sizes = (n, slots, heads, cache.n_kv, dim, dev)
+    buf = workspace._on(stream, raw) if workspace.sizes == sizes else workspace.reserve(*sizes, stream)
     a = _pack_attend(n, slots, heads, width, dim ** -0.5 if scale is None else scale, qp, qr, qh, kp, vp, kr, kh, vr, vh,
                      _flat(block_table, torch.int32, n * width, "block_table", dev),
                      _flat(length, torch.int32, n, "length", dev),
                      0 if mask is None else _flat(mask, torch.uint8, n * slots * slots, "mask", dev), op, orow, oh,
                      0 if lse is None else _flat(lse, torch.float32, n * slots * heads, "lse", dev), buf.data_ptr(),
                      buf.numel(), 0 if status is None else _flat(status, torch.int32, 1, "status", dev))
-    err = lib.dt_cache_attention(cache.c, a, _stream(stream, dev))
+    err = lib.dt_cache_attention(cache.c, a, raw)
     if err:
         raise _refused(err, "dt_cache_attention")
     return out

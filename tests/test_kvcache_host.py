@@ -47,6 +47,8 @@ def test_every_binding_asks_for_its_stream_before_it_launches(monkeypatch):
             return st if i is None else st[i]
 
     class Work:
+        sizes = None
+
         def reserve(self, *sizes):
             return Tensor(torch.uint8, 1 << 20)
 

@@ -24,12 +24,12 @@
 // zeros, and a key whose value is not finite becomes zeros and is noted, which
 // makes the output of the rows that do see it NaN (their lse has no values in it).
 //
-// Measured, 32 heads of 128 over 8: one prompt of 16k tokens 1340 us, 1.64 PFLOP/s, 87 %
+// Measured, 32 heads of 128 over 8: one prompt of 16k tokens 1335 us, 1.64 PFLOP/s, 87 %
 // of the measured bf16 rate (the exponentials and the maximum are what the products
-// wait for); 48 ragged prompts of up to 1k tokens 272 us, a third of the tensor
+// wait for); 48 ragged prompts of up to 1k tokens 267 us, a third of the tensor
 // cores' time and 38 % of the measured bandwidth: an item has four key tiles on
-// average, so that its start (Q, the first product) and its output weigh as much as
-// they; one of 300 tokens 11.4 us, two items' latency.
+// average, so that its start (the first product) and its end (the last one, the output) weigh as much as
+// they; one of 300 tokens 11.1 us, one item's chain (40 items, one a CTA).
 #include <cuda.h>
 
 #include <type_traits>

@@ -29,8 +29,8 @@
 // last, in the order of keys.
 //
 // Measured: 32 trees of 65 slots (4 rows of each head streamed by the other kernel)
-// over up to 4k cached tokens, 32 heads over 8, 210 us; one of 513 slots over 32k 335
-// us, 0.82 PFLOP/s.  Where the time goes: the products 2048 cycles of a pair of row
+// over up to 4k cached tokens, 32 heads over 8, 209 us; one of 513 slots over 32k 310
+// us (likewise; 335 with a row tile for the rows left over), 0.89 PFLOP/s.  Where the time goes: the products 2048 cycles of a pair of row
 // tiles' 4 600 a key tile, the rest the softmax between them and shared memory (Q, K
 // and V are read by both tiles' products, and written by the conversion); and what a
 // stretch costs besides, its Q and its join, some 30 000 cycles, two or three times
@@ -47,9 +47,9 @@ constexpr int kTreeSlots = 4;    // what goes with a key tile: its scales and ma
 constexpr int kTreeMmaWarp = 8, kTreeFetchWarp = 9, kTreeConvWarp = 12, kTreeConvWarps = 4;  // (10 and 11: none)
 constexpr int kConvThreads = 32 * kTreeConvWarps;
 constexpr int kTreeThreads = 32 * (kTreeConvWarp + kTreeConvWarps);
-// Registers: 512 threads start with 128; the softmax's 256 go to 144, the others' to 112.  What a role spills goes
-// to L2, there being no L1 left beside the shared memory (us for 32 trees and for the wide one: 136 and 120: 217 and
-// 339; 144 and 112: 215 and 336; 152 and 104: 220 and 344; 160 and 96: 217 and 342).
+// Registers: 512 threads start with 128; the softmax's 256 go to 144, the others' to 112.  What a role spills would go
+// to L2, there being no L1 left beside the shared memory (nothing now; us for 32 trees and for the wide one when something did: 136 and 120:
+// 217 and 339; 144 and 112: 215 and 336; 152 and 104: 220 and 344; 160 and 96: 217 and 342).
 constexpr int kTreeSoftmaxRegs = 144, kTreeOtherRegs = 112;
 static_assert(2 * kTreeSoftmaxRegs + 2 * kTreeOtherRegs <= 4 * 128, "");
 

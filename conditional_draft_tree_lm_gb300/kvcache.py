@@ -195,9 +195,10 @@ class AttentionWorkspace:
     """Device memory that ``cache_attention`` calls use one after the other (calls that may
     overlap, on several streams, need one each).  It grows with the largest call so far,
     at least to twice its size; what it had before stays with it, since captured graphs may
-    work there.  While a stream is being captured it cannot grow (its zeros would be the
-    graph's): grow it before by a call of the captured sizes or by ``reserve``, and keep it
-    as long as the graph.  Memory is taken and zeroed in the order of the stream of the call that needs it, and
+    work there: keep it as long as the graph.  It does not grow while a stream is being
+    captured (its zeros would be the graph's): a call that needs more then has memory of the
+    graph's own, zeroed in every replay.  Grow it before, by a call of the captured sizes or by
+    ``reserve``, to have neither.  Memory is taken and zeroed in the order of the stream of the call that needs it, and
     goes back only behind the work of every stream that has used it."""
 
     def __init__(self):
@@ -211,7 +212,7 @@ class AttentionWorkspace:
             if self.buffer is None or self.buffer.numel() < need or self.buffer.device != torch.empty(0, device=device).device:
                 with _allocating(stream):
                     if torch.cuda.is_current_stream_capturing():
-                        raise RuntimeError(f"workspace: {need} bytes are needed while a stream is being captured; reserve them before")
+                        return torch.zeros(max(need, 256), dtype=torch.uint8, device=device)
                     if self.buffer is not None:
                         self.outgrown.append(self.buffer)
                         need = max(need, 2 * self.buffer.numel())

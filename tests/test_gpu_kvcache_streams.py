@@ -75,7 +75,7 @@ def test_a_workspace_outlives_the_streams_that_use_it():
 
 def test_captured_calls_keep_their_workspace_when_it_grows():
     """A single-token step is captured, then larger calls grow the workspace; the graph's memory is still there, and its
-    replays give what the call gave.  A workspace that would have to grow refuses to do so inside a capture."""
+    replays give what the call gave.  A call that needs more inside a capture has the graph's own memory."""
     torch = _t()
     from conditional_draft_tree_lm_gb300 import AttentionWorkspace, cache_attention
     work = AttentionWorkspace()
@@ -91,11 +91,26 @@ def test_captured_calls_keep_their_workspace_when_it_grows():
     small = work.buffer
     at, size = small.data_ptr(), small.numel()
     del small
-    with pytest.raises(RuntimeError, match="captured"):
-        with torch.cuda.graph(torch.cuda.CUDAGraph()):
-            cache_attention(*args[1], out=torch.empty_like(d["q"]), **new[1])
+    inside, twice, third = torch.cuda.CUDAGraph(), torch.zeros_like(d["q"]), torch.zeros_like(d["q"])
+    with torch.cuda.graph(inside):
+        cache_attention(*args[1], out=twice, **new[1])
+        cache_attention(*args[0], out=out, **new[0])
+        cache_attention(*args[1], out=third, **new[1])
+    assert work.buffer.data_ptr() == at
+    fresh = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(fresh):
+        cache_attention(*args[0], out=out, **dict(new[0], workspace=AttentionWorkspace()))
     torch.cuda.synchronize()
+    assert torch.equal(cache_attention(*args[0], **new[0]), want)  # (before any replay)
     large = cache_attention(*args[1], **new[1])
+    for _ in range(3):
+        for x in (out, twice, third):
+            x.fill_(7)
+        inside.replay()
+        assert torch.equal(twice, large) and torch.equal(third, large) and torch.equal(out, want)
+        out.fill_(7)
+        fresh.replay()
+        assert torch.equal(out, want)
     assert work.buffer.data_ptr() != at and work.buffer.numel() >= 2 * size
     other = [torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(4)]
     assert at not in [x.data_ptr() for x in other]

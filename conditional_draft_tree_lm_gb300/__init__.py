@@ -17,3 +17,9 @@ from .kvcache import (  # noqa: F401
     kv_plan,
     prompt_attention,
 )
+from .layer import (  # noqa: F401
+    Rotary,
+    linear,
+    qk_norm_rope,
+    token_logprobs,
+)

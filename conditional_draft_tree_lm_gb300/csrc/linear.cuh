@@ -1,0 +1,84 @@
+// What the kernels of dt_linear share: arguments on the device, activations, the last step of an output.
+#pragma once
+
+#include "kv.cuh"
+
+namespace dt {
+
+struct LinearParams {
+  const uint16_t* bias;
+  const uint16_t* gate_bias;
+  const uint16_t* residual;
+  void* out;
+  int64_t residual_stride, out_stride;
+  int rows, outer, k_blocks;  // k_blocks: of 64
+  int activation, out_fp32;
+  int bn, split, stages, tmem_cols;  // few rows: tokens of a tile, CTAs of a cluster
+  uint32_t stage_bytes;
+  int wide;  // outputs (and residuals) are written and read 4 at a time
+  int32_t* status;
+};
+
+DT_DEVINL float activate(float z, int act) {
+  switch (act) {
+    case DT_ACT_RELU: return z < 0.0f ? 0.0f : z;  // (a NaN stays one)
+    case DT_ACT_SILU: return z / (1.0f + expf(-z));
+    case DT_ACT_GELU: return 0.5f * z * erfcf(-0.707106781186547524f * z);
+    // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+    case DT_ACT_GELU_TANH: return z / (1.0f + expf(-1.59576912160573071f * fmaf(0.044715f * z * z, z, z)));
+    default: return z;
+  }
+}
+
+// Four neighbouring outputs of row t from column n on (those behind the last column are left out): the sums of the
+// product (and of the gate's) in, bias, activation and residual, one rounding, out.
+template <int SIDES>
+DT_DEVINL void finish4(const LinearParams& p, int64_t t, int n, const float4& y4, const float4& z4) {
+  float y[4] = {y4.x, y4.y, y4.z, y4.w}, z[4] = {z4.x, z4.y, z4.z, z4.w};
+  const int valid = min(4, p.outer - n);
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < valid) y[i] += bf16_to_f32(p.bias[n + i]);
+  }
+  if (SIDES == 2) {
+    if (p.gate_bias) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < valid) z[i] += bf16_to_f32(p.gate_bias[n + i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] *= activate(z[i], p.activation);
+  } else if (p.activation != DT_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = activate(y[i], p.activation);
+  }
+  const int64_t at = t * p.out_stride + n;
+  const uint16_t* res = p.residual ? p.residual + t * p.residual_stride + n : nullptr;
+  if (p.wide && valid == 4) {
+    if (res) {
+      const uint2 r = *reinterpret_cast<const uint2*>(res);
+      y[0] += __uint_as_float(r.x << 16);
+      y[1] += __uint_as_float(r.x & 0xFFFF0000u);
+      y[2] += __uint_as_float(r.y << 16);
+      y[3] += __uint_as_float(r.y & 0xFFFF0000u);
+    }
+    if (p.out_fp32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(y[0], y[1]), b = __floats2bfloat162_rn(y[2], y[3]);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= valid) break;
+      if (res) y[i] += bf16_to_f32(res[i]);
+      if (p.out_fp32) static_cast<float*>(p.out)[at + i] = y[i];
+      else static_cast<__nv_bfloat16*>(p.out)[at + i] = __float2bfloat16_rn(y[i]);
+    }
+  }
+}
+
+}  // namespace dt

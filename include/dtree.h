@@ -545,6 +545,138 @@ typedef struct dt_prompt_attention_args {
 } dt_prompt_attention_args;
 dt_status dt_prompt_attention(const dt_prompt_attention_args* args, void* stream);
 
+/* --------------------------------------------------------------------------
+ * A target layer around its attention.
+ *
+ * What a pass of the target model computes before and behind the attention
+ * calls above, and what is read off its logits; like them without a context
+ * and without memory of their own.  Per layer:
+ *   dt_linear          the joint projection of queries, keys and values
+ *   dt_qk_norm_rope    norms of queries and keys, turned by their positions
+ *   (attention, append: above)
+ *   dt_linear          back to the residual stream, which is added
+ *   dt_linear          the gated feed-forward width; then back, added again
+ * and behind the last layer
+ *   dt_linear          the output head, logits in fp32 (dt_accept_walk's input)
+ *   dt_token_logprobs  log probabilities of given tokens
+ * Activations and weights are bf16, sums fp32, one rounding at the end.
+ * ------------------------------------------------------------------------ */
+
+/* Activations of dt_linear. */
+#define DT_ACT_NONE 0
+#define DT_ACT_RELU 1      /* max(z, 0) */
+#define DT_ACT_SILU 2      /* z / (1 + e^-z) */
+#define DT_ACT_GELU 3      /* z (1 + erf(z / sqrt 2)) / 2 */
+#define DT_ACT_GELU_TANH 4 /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+
+/* Matrix product with bias, activation or gate, and residual:
+ *   out[t, n] = act(x[t] . weight[n] + bias[n]) + residual[t, n]
+ * or, with gate not NULL,
+ *   out[t, n] = act(x[t] . gate[n] + gate_bias[n]) * (x[t] . weight[n] + bias[n]) + residual[t, n].
+ * x [rows, inner], weight and gate [outer, inner], bias and gate_bias [outer],
+ * residual [rows, outer] are bf16, out [rows, outer] bf16 or fp32.  Row strides
+ * are in elements; columns are adjacent.  x, weight and gate must be 16-byte
+ * aligned, inner and their row strides multiples of 8; residual and out may be
+ * anywhere, and out may be the residual itself (same address and stride), but
+ * must not overlap another input, nor its rows one another.  Sums are in fp32,
+ * in an order that depends on the sizes only: the same call gives the same bits.
+ * rows 0: nothing is done.  One launch.  status: [1] int32 device or NULL;
+ * DT_KV_TIMEOUT is or'ed in. */
+typedef struct dt_linear_args {
+  int64_t rows; /* 0..2^31-257 */
+  int inner;    /* multiple of 8, >= 8 */
+  int outer;    /* 1..2^31-257 */
+  const void* x;
+  int64_t x_row_stride;
+  const void* weight;
+  int64_t weight_row_stride;
+  const void* bias; /* or NULL */
+  const void* gate; /* or NULL */
+  int64_t gate_row_stride;
+  const void* gate_bias; /* or NULL; without gate NULL */
+  int activation;        /* DT_ACT_* */
+  const void* residual;  /* or NULL */
+  int64_t residual_row_stride;
+  void* out;
+  int64_t out_row_stride;
+  int out_fp32; /* 0: bf16 */
+  int32_t* status;
+} dt_linear_args;
+dt_status dt_linear(const dt_linear_args* args, void* stream);
+
+/* Norms of queries and keys for each head, and their rotation by position, in
+ * one pass.  Of every head of every row, where q_weight (k_weight) is not NULL:
+ *   y[c] = x[c] / sqrt(mean over c of x[c]^2 + eps) * weight[c],
+ * and where turns is not NULL, with i < rot / 2 and the pair (a, b) =
+ * (y[i], y[i + rot / 2]) or, interleaved, (y[2 i], y[2 i + 1]):
+ *   a' = amplitude * (a cos p_i - b sin p_i),  b' = amplitude * (b cos p_i + a sin p_i),
+ *   p_i = 2 pi * position * turns[i] / 2^64;
+ * channels from rot on are not turned.  turns[i] is the part of a full turn
+ * that a step of one position takes, in units of 2^-64, so that the angle of a
+ * far position is as good as that of a near one.
+ * Row (q, a) is row q * slots + a, at position
+ *   (base ? base[q] : 0) + (positions ? positions[row] : a).
+ * Rows whose positions[row] is negative (as dt_kv_plan leaves behind the last token) are
+ * not written.  Rows of heads as above; q_out may be q and k_out k (same
+ * strides), other overlaps are not allowed.  k NULL: queries only.  n_req or
+ * slots 0: nothing is done.  One launch. */
+typedef struct dt_qk_norm_rope_args {
+  int n_req, slots; /* n_req * slots at most 2^31-1 */
+  int n_q, n_kv;    /* at most 4096 each */
+  int head_dim;     /* multiple of 16, 32..256 */
+  int rot;          /* multiple of 16, at most head_dim; without turns 0 */
+  int interleaved;
+  float eps;       /* finite, >= 0 */
+  float amplitude; /* finite */
+  const void* q;
+  const void* k; /* or NULL */
+  int64_t q_row_stride, q_head_stride;
+  int64_t k_row_stride, k_head_stride;
+  const void* q_weight; /* [head_dim] bf16 or NULL: no norm */
+  const void* k_weight;
+  const uint64_t* turns;    /* [rot / 2] device, or NULL: no rotation */
+  const int32_t* positions; /* [n_req * slots] or NULL */
+  const int32_t* base;      /* [n_req] or NULL */
+  void* q_out;
+  void* k_out;
+  int64_t q_out_row_stride, q_out_head_stride;
+  int64_t k_out_row_stride, k_out_head_stride;
+} dt_qk_norm_rope_args;
+dt_status dt_qk_norm_rope(const dt_qk_norm_rope_args* args, void* stream);
+
+/* Log probabilities of given tokens, with entropy and the best alternatives.
+ * Per row, with z = logits / temperature:
+ *   lse = log sum_v e^{z_v},  logp[j] = z_{tokens[j]} - lse,
+ *   entropy = sum_v p_v (lse - z_v), p_v = e^{z_v - lse},
+ * and the n_top tokens of the largest logits, the lower token among equals,
+ * with their log probabilities.  A logit of -inf has no part in the sums and a
+ * log probability of -inf; it counts below every other among the best.  A row
+ * of nothing but -inf gives lse and log probabilities of -inf and entropy 0.  A
+ * row with a NaN or +inf gives NaN everywhere, -1 for its best tokens, and no
+ * row but it.  What is beyond fp32 in the end is infinite.  A token that is negative asks for
+ * nothing and gives 0 (dt_accept_walk pads its paths with -1); one at vocab or above gives
+ * NaN and sets DT_KV_BAD_INDEX in status.
+ * logits [rows, vocab] fp32 or bf16, the row stride in elements and any, the
+ * address aligned to its elements.  rows 0: nothing is done.  One launch. */
+typedef struct dt_token_logprobs_args {
+  int64_t rows;    /* 0..2^26 */
+  int vocab;       /* 1..2^30 */
+  int n_tokens;    /* given tokens of a row, 0..65536 */
+  int n_top;       /* 0..64, at most vocab */
+  int logits_bf16; /* 0: fp32 */
+  float temperature; /* finite, at least 2^-100 */
+  const void* logits;
+  int64_t logits_row_stride;
+  const int32_t* tokens; /* [rows, n_tokens] */
+  float* logp;           /* [rows, n_tokens] */
+  float* lse;            /* [rows] or NULL */
+  float* entropy;        /* [rows] or NULL */
+  int32_t* top_tok;      /* [rows, n_top] */
+  float* top_logp;       /* [rows, n_top] */
+  int32_t* status;       /* [1] or NULL */
+} dt_token_logprobs_args;
+dt_status dt_token_logprobs(const dt_token_logprobs_args* args, void* stream);
+
 /* Synchronise the context's last stream and read (and clear) its device status
  * word: DT_OK, DT_ERR_TIMEOUT or DT_ERR_DEVICE. */
 dt_status dt_get_device_status(dt_ctx* ctx);

@@ -162,6 +162,38 @@ cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& g, const CUtenso
   return cudaLaunchKernelEx(&cfg, k_few<SIDES>, w, g, x, p);
 }
 
+// Few tokens: one tile of them, padded to 16, two CTAs an SM where their sums leave room for it, and clusters of as many
+// CTAs as there are places, with four blocks of 64 or more each.
+void plan_few(LinearParams& p, int sides) {
+  const int most = 256 / sides, token_tiles = (p.rows + most - 1) / most;
+  p.bn = ((p.rows + token_tiles - 1) / token_tiles + 15) & ~15;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < sides * p.bn) p.tmem_cols *= 2;
+  p.stage_bytes = sides * kTileBytes + p.bn * 128;
+  p.stages = static_cast<int>((sides * p.bn <= 128 ? 110u * 1024 : 220u * 1024) / p.stage_bytes);
+  if (p.stages > 8) p.stages = 8;
+  const int64_t tiles = static_cast<int64_t>((p.outer + 127) / 128) * token_tiles;
+  p.split = 1;
+  while (p.split < 8 && tiles * (p.split + 1) <= 2 * kSms && p.k_blocks >= 4 * (p.split + 1)) ++p.split;
+}
+
+// Many tokens: the tile's columns so that the pairs' rounds of tiles cost least, a tile as much as its columns and 32 more.
+void plan_many(LinearParams& p, int sides) {
+  p.m_tiles = (p.rows + 255) / 256;
+  int64_t least = INT64_MAX;
+  for (int bn = 256; bn >= 64; bn -= 32 * sides) {
+    const int outs = bn / sides;
+    const int64_t tiles = static_cast<int64_t>(p.m_tiles) * ((p.outer + outs - 1) / outs);
+    const int64_t cost = (tiles + kSms / 2 - 1) / (kSms / 2) * (bn + 32);
+    if (cost < least) {
+      least = cost;
+      p.bn = bn;
+      p.tile_outs = outs;
+      p.n_tiles = (p.outer + outs - 1) / outs;
+    }
+  }
+}
+
 }  // namespace
 
 bool make_tmap_bf16_2d(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t rows, uint64_t row_stride_bytes, uint32_t box_rows);
@@ -203,28 +235,26 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
   p.activation = a.activation;
   p.out_fp32 = a.out_fp32 != 0;
   p.status = a.status;
-  p.wide = out % (4 * bytes) == 0 && (a.rows == 1 || a.out_row_stride % 4 == 0) &&
-           (!a.residual || (reinterpret_cast<uintptr_t>(a.residual) % 8 == 0 && (a.rows == 1 || a.residual_row_stride % 4 == 0)));
-  const int sides = a.gate ? 2 : 1, most = 256 / sides;
-  const int token_tiles = (p.rows + most - 1) / most;
-  p.bn = ((p.rows + token_tiles - 1) / token_tiles + 15) & ~15;
-  if ((p.rows + p.bn - 1) / p.bn > 65535) return kv_fail(DT_ERR_SHAPE, "%s: more than 65535 tiles of rows", who);
-  p.tmem_cols = 32;
-  while (p.tmem_cols < sides * p.bn) p.tmem_cols *= 2;
-  p.stage_bytes = sides * kTileBytes + p.bn * 128;
-  // two CTAs an SM where their sums leave room for it
-  p.stages = static_cast<int>((sides * p.bn <= 128 ? 110u * 1024 : 220u * 1024) / p.stage_bytes);
-  if (p.stages > 8) p.stages = 8;
-  const int64_t tiles = static_cast<int64_t>((a.outer + 127) / 128) * token_tiles;
-  p.split = 1;
-  while (p.split < 8 && tiles * (p.split + 1) <= 2 * kSms && p.k_blocks >= 4 * (p.split + 1)) ++p.split;
-  if (static_cast<int64_t>((a.outer + 127) / 128) * p.split > 0x7FFFFFFF) return kv_fail(DT_ERR_SHAPE, "%s: too many tiles", who);
+  const int sides = a.gate ? 2 : 1;
+  const bool many = p.rows > 256;
+  const uintptr_t res = reinterpret_cast<uintptr_t>(a.residual);
+  const int64_t at_once = many ? 16 / static_cast<int64_t>(bytes) : 4;  // outputs written together
+  p.wide = out % (at_once * bytes) == 0 && (a.rows == 1 || a.out_row_stride % at_once == 0) &&
+           (!res || (many ? res % 16 == 0 && a.residual_row_stride % 8 == 0 : res % 8 == 0 && (a.rows == 1 || a.residual_row_stride % 4 == 0)));
+  if (many) {
+    plan_many(p, sides);
+    if (static_cast<int64_t>(p.m_tiles) * p.n_tiles > (1 << 30)) return kv_fail(DT_ERR_SHAPE, "%s: more than 2^30 tiles", who);
+  } else {
+    plan_few(p, sides);
+    if (static_cast<int64_t>((a.outer + 127) / 128) * p.split > 0x7FFFFFFF) return kv_fail(DT_ERR_SHAPE, "%s: too many tiles", who);
+  }
   auto stride = [&](int64_t s, int64_t rows) { return static_cast<uint64_t>(rows == 1 ? (a.inner + 7) / 8 * 8 : s) * 2; };
   CUtensorMap w, g, x;
-  if (!make_tmap_bf16_2d(&w, a.weight, a.inner, a.outer, stride(a.weight_row_stride, a.outer), 128) ||
-      !make_tmap_bf16_2d(&g, a.gate ? a.gate : a.weight, a.inner, a.outer, stride(a.gate ? a.gate_row_stride : a.weight_row_stride, a.outer), 128) ||
-      !make_tmap_bf16_2d(&x, a.x, a.inner, a.rows, stride(a.x_row_stride, a.rows), p.bn))
+  if (!make_tmap_bf16_2d(&w, a.weight, a.inner, a.outer, stride(a.weight_row_stride, a.outer), many ? p.bn / 2 : 128) ||
+      !make_tmap_bf16_2d(&g, a.gate ? a.gate : a.weight, a.inner, a.outer, stride(a.gate ? a.gate_row_stride : a.weight_row_stride, a.outer), many ? p.bn / 2 : 128) ||
+      !make_tmap_bf16_2d(&x, a.x, a.inner, a.rows, stride(a.x_row_stride, a.rows), many ? 128 : p.bn))
     return kv_fail(DT_ERR_SHAPE, "%s: strides that a tensor map does not take (2^40 bytes and more)", who);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (many) return kv_launched(who, launch_linear_wide(w, g, x, p, sides == 2, st));
   return kv_launched(who, sides == 2 ? launch_few<2>(w, g, x, p, st) : launch_few<1>(w, g, x, p, st));
 }

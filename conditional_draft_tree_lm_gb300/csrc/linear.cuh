@@ -15,18 +15,33 @@ struct LinearParams {
   int activation, out_fp32;
   int bn, split, stages, tmem_cols;  // few rows: tokens of a tile, CTAs of a cluster
   uint32_t stage_bytes;
-  int wide;  // outputs (and residuals) are written and read 4 at a time
+  int m_tiles, n_tiles, tile_outs;  // many rows: tiles of 256 tokens, of outputs, and outputs of a tile (bn: its columns)
+  int wide;  // outputs (and residuals) are written and read 4 at a time, or 16 bytes where rows are many
   int32_t* status;
 };
 
-DT_DEVINL float activate(float z, int act) {
+template <int ACT>
+DT_DEVINL float activate(float z) {
+  if (ACT == DT_ACT_RELU) return z < 0.0f ? 0.0f : z;  // (a NaN stays one)
+  if (ACT == DT_ACT_SILU) return z / (1.0f + expf(-z));
+  if (ACT == DT_ACT_GELU) return 0.5f * z * erfcf(-0.707106781186547524f * z);
+  // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+  if (ACT == DT_ACT_GELU_TANH) return z / (1.0f + expf(-1.59576912160573071f * fmaf(0.044715f * z * z, z, z)));
+  return z;
+}
+template <int ACT, int N>
+DT_DEVINL void activate_all(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = activate<ACT>(v[i]);
+}
+template <int N>
+DT_DEVINL void activate(float (&v)[N], int act) {
   switch (act) {
-    case DT_ACT_RELU: return z < 0.0f ? 0.0f : z;  // (a NaN stays one)
-    case DT_ACT_SILU: return z / (1.0f + expf(-z));
-    case DT_ACT_GELU: return 0.5f * z * erfcf(-0.707106781186547524f * z);
-    // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
-    case DT_ACT_GELU_TANH: return z / (1.0f + expf(-1.59576912160573071f * fmaf(0.044715f * z * z, z, z)));
-    default: return z;
+    case DT_ACT_RELU: activate_all<DT_ACT_RELU>(v); break;
+    case DT_ACT_SILU: activate_all<DT_ACT_SILU>(v); break;
+    case DT_ACT_GELU: activate_all<DT_ACT_GELU>(v); break;
+    case DT_ACT_GELU_TANH: activate_all<DT_ACT_GELU_TANH>(v); break;
+    default: break;
   }
 }
 
@@ -47,11 +62,11 @@ DT_DEVINL void finish4(const LinearParams& p, int64_t t, int n, const float4& y4
       for (int i = 0; i < 4; ++i)
         if (i < valid) z[i] += bf16_to_f32(p.gate_bias[n + i]);
     }
+    activate(z, p.activation);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] *= activate(z[i], p.activation);
-  } else if (p.activation != DT_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = activate(y[i], p.activation);
+    for (int i = 0; i < 4; ++i) y[i] *= z[i];
+  } else {
+    activate(y, p.activation);
   }
   const int64_t at = t * p.out_stride + n;
   const uint16_t* res = p.residual ? p.residual + t * p.residual_stride + n : nullptr;
@@ -80,5 +95,8 @@ DT_DEVINL void finish4(const LinearParams& p, int64_t t, int n, const float4& y4
     }
   }
 }
+
+cudaError_t launch_linear_wide(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, bool gate,
+                               cudaStream_t st);
 
 }  // namespace dt

@@ -10,7 +10,7 @@ DT_DEVINL uint32_t cta_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// Every thread of every CTA of the cluster; what was written to shared memory before is seen behind it.
+// Every thread of every CTA; what was written to shared memory before is seen behind it.
 DT_DEVINL void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

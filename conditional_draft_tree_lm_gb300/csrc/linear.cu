@@ -40,14 +40,28 @@ __global__ void __launch_bounds__(kFewThreads)
   const int n0 = tile * 128, t0 = static_cast<int>(blockIdx.y) * p.bn;
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * rank / p.split);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (rank + 1) / p.split);
-  if (tid == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+  const uint64_t stream = l2_policy_evict_first(), keep = l2_policy_evict_last();
+  auto load = [&](int kb, uint32_t stage) {
+    uint8_t* at = smem + stage * p.stage_bytes;
+    mbar_arrive_expect_tx(&full[stage], p.stage_bytes);
+    if (SIDES == 2) tma_load_2d(at, &tm_g, &full[stage], kb * 64, n0, stream);
+    tma_load_2d(at + (SIDES - 1) * kTileBytes, &tm_w, &full[stage], kb * 64, n0, stream);
+    tma_load_2d(at + SIDES * kTileBytes, &tm_x, &full[stage], kb * 64, t0, keep);
+  };
+  // the first loads are under way before tensor memory is asked for
+  const int ahead = min(p.stages, kb1 - kb0);
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int s = 0; s < p.stages; ++s) {
+        mbar_init(&full[s], 1);
+        mbar_init(&empty[s], 1);
+      }
+      mbar_init(done, 1);
+      mbar_init(drained, 1);
+      fence_mbar_init();
+      for (int s = 0; s < ahead; ++s) load(kb0 + s, s);
     }
-    mbar_init(done, 1);
-    mbar_init(drained, 1);
-    fence_mbar_init();
+    __syncwarp();
   }
   if (warp == 1) tmem_alloc(tmem_slot, p.tmem_cols);
   tc_fence_before();
@@ -57,18 +71,11 @@ __global__ void __launch_bounds__(kFewThreads)
   bool ok = true;
 
   if (warp == 0) {
-    const uint64_t stream = l2_policy_evict_first(), keep = l2_policy_evict_last();
     uint32_t stage = 0, phase = 0;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      ok = warp_wait(&empty[stage], phase ^ 1u);
+    for (int kb = kb0 + ahead; kb < kb1; ++kb) {
+      ok = warp_wait(&empty[stage], phase);
       if (!ok) break;
-      if (elect_one()) {
-        uint8_t* at = smem + stage * p.stage_bytes;
-        mbar_arrive_expect_tx(&full[stage], p.stage_bytes);
-        if (SIDES == 2) tma_load_2d(at, &tm_g, &full[stage], kb * 64, n0, stream);
-        tma_load_2d(at + (SIDES - 1) * kTileBytes, &tm_w, &full[stage], kb * 64, n0, stream);
-        tma_load_2d(at + SIDES * kTileBytes, &tm_x, &full[stage], kb * 64, t0, keep);
-      }
+      if (elect_one()) load(kb, stage);
       __syncwarp();
       if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
     }
@@ -121,6 +128,7 @@ __global__ void __launch_bounds__(kFewThreads)
     tc_fence_after();
     tmem_dealloc(tmem, p.tmem_cols);
   }
+  __syncwarp();
   if (p.split > 1) cluster_barrier();
   // four neighbouring rows of weight for a token at a time, an equal share of them for each rank
   const int units = tokens * 32;
@@ -163,18 +171,19 @@ cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& g, const CUtenso
 }
 
 // Few tokens: one tile of them, padded to 16, two CTAs an SM where their sums leave room for it, and clusters of as many
-// CTAs as there are places, with four blocks of 64 or more each.
+// CTAs as leave all of them beside each other (clusters do not fill every SM), with four blocks of 64 or more each.
 void plan_few(LinearParams& p, int sides) {
   const int most = 256 / sides, token_tiles = (p.rows + most - 1) / most;
   p.bn = ((p.rows + token_tiles - 1) / token_tiles + 15) & ~15;
   p.tmem_cols = 32;
   while (p.tmem_cols < sides * p.bn) p.tmem_cols *= 2;
   p.stage_bytes = sides * kTileBytes + p.bn * 128;
-  p.stages = static_cast<int>((sides * p.bn <= 128 ? 110u * 1024 : 220u * 1024) / p.stage_bytes);
+  const bool two = sides * p.bn <= 128;
+  p.stages = static_cast<int>((two ? 110u * 1024 : 220u * 1024) / p.stage_bytes);
   if (p.stages > 8) p.stages = 8;
   const int64_t tiles = static_cast<int64_t>((p.outer + 127) / 128) * token_tiles;
   p.split = 1;
-  while (p.split < 8 && tiles * (p.split + 1) <= 2 * kSms && p.k_blocks >= 4 * (p.split + 1)) ++p.split;
+  while (p.split < 8 && tiles * (p.split + 1) <= (two ? 2 * kSms : kSms) * 7 / 8 && p.k_blocks >= 4 * (p.split + 1)) ++p.split;
 }
 
 // Many tokens: the tile's columns so that the pairs' rounds of tiles cost least, a tile as much as its columns and 32 more.
@@ -235,6 +244,8 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
   p.activation = a.activation;
   p.out_fp32 = a.out_fp32 != 0;
   p.status = a.status;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (p.rows <= kTokensMost) return kv_launched(who, launch_linear_token(a, p, st));
   const int sides = a.gate ? 2 : 1;
   const bool many = p.rows > 256;
   const uintptr_t res = reinterpret_cast<uintptr_t>(a.residual);
@@ -254,7 +265,6 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
       !make_tmap_bf16_2d(&g, a.gate ? a.gate : a.weight, a.inner, a.outer, stride(a.gate ? a.gate_row_stride : a.weight_row_stride, a.outer), many ? p.bn / 2 : 128) ||
       !make_tmap_bf16_2d(&x, a.x, a.inner, a.rows, stride(a.x_row_stride, a.rows), many ? 128 : p.bn))
     return kv_fail(DT_ERR_SHAPE, "%s: strides that a tensor map does not take (2^40 bytes and more)", who);
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (many) return kv_launched(who, launch_linear_wide(w, g, x, p, sides == 2, st));
   return kv_launched(who, sides == 2 ? launch_few<2>(w, g, x, p, st) : launch_few<1>(w, g, x, p, st));
 }

@@ -13,7 +13,8 @@ struct LinearParams {
   int64_t residual_stride, out_stride;
   int rows, outer, k_blocks;  // k_blocks: of 64
   int activation, out_fp32;
-  int bn, split, stages, tmem_cols;  // few rows: tokens of a tile, CTAs of a cluster
+  int bn, stages, tmem_cols;  // few rows: tokens of a tile
+  int split;                  // CTAs of a cluster
   uint32_t stage_bytes;
   int m_tiles, n_tiles, tile_outs;  // many rows: tiles of 256 tokens, of outputs, and outputs of a tile (bn: its columns)
   int wide;  // outputs (and residuals) are written and read 4 at a time, or 16 bytes where rows are many
@@ -45,22 +46,42 @@ DT_DEVINL void activate(float (&v)[N], int act) {
   }
 }
 
-// Four neighbouring outputs of row t from column n on (those behind the last column are left out): the sums of the
-// product (and of the gate's) in, bias, activation and residual, one rounding, out.
+// One output, column n of row t: the sums of the product (and of the gate's) in, bias, activation and residual, one
+// rounding, out.
+template <int SIDES>
+DT_DEVINL void finish(const LinearParams& p, int64_t t, int n, float product, float gate) {
+  float y[1] = {product}, z[1] = {gate};
+  if (p.bias) y[0] += bf16_to_f32(p.bias[n]);
+  if (SIDES == 2) {
+    if (p.gate_bias) z[0] += bf16_to_f32(p.gate_bias[n]);
+    activate(z, p.activation);
+    y[0] *= z[0];
+  } else {
+    activate(y, p.activation);
+  }
+  if (p.residual) y[0] += bf16_to_f32(p.residual[t * p.residual_stride + n]);
+  if (p.out_fp32) static_cast<float*>(p.out)[t * p.out_stride + n] = y[0];
+  else static_cast<__nv_bfloat16*>(p.out)[t * p.out_stride + n] = __float2bfloat16_rn(y[0]);
+}
+
+// Four neighbouring outputs from column n on (those behind the last column are left out).
 template <int SIDES>
 DT_DEVINL void finish4(const LinearParams& p, int64_t t, int n, const float4& y4, const float4& z4) {
   float y[4] = {y4.x, y4.y, y4.z, y4.w}, z[4] = {z4.x, z4.y, z4.z, z4.w};
-  const int valid = min(4, p.outer - n);
-  if (p.bias) {
+  if (!p.wide || n + 4 > p.outer) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (i < valid) y[i] += bf16_to_f32(p.bias[n + i]);
+      if (n + i < p.outer) finish<SIDES>(p, t, n + i, y[i], z[i]);
+    return;
+  }
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] += bf16_to_f32(p.bias[n + i]);
   }
   if (SIDES == 2) {
     if (p.gate_bias) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < valid) z[i] += bf16_to_f32(p.gate_bias[n + i]);
+      for (int i = 0; i < 4; ++i) z[i] += bf16_to_f32(p.gate_bias[n + i]);
     }
     activate(z, p.activation);
 #pragma unroll
@@ -68,34 +89,25 @@ DT_DEVINL void finish4(const LinearParams& p, int64_t t, int n, const float4& y4
   } else {
     activate(y, p.activation);
   }
+  if (p.residual) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p.residual + t * p.residual_stride + n);
+    y[0] += __uint_as_float(r.x << 16);
+    y[1] += __uint_as_float(r.x & 0xFFFF0000u);
+    y[2] += __uint_as_float(r.y << 16);
+    y[3] += __uint_as_float(r.y & 0xFFFF0000u);
+  }
   const int64_t at = t * p.out_stride + n;
-  const uint16_t* res = p.residual ? p.residual + t * p.residual_stride + n : nullptr;
-  if (p.wide && valid == 4) {
-    if (res) {
-      const uint2 r = *reinterpret_cast<const uint2*>(res);
-      y[0] += __uint_as_float(r.x << 16);
-      y[1] += __uint_as_float(r.x & 0xFFFF0000u);
-      y[2] += __uint_as_float(r.y << 16);
-      y[3] += __uint_as_float(r.y & 0xFFFF0000u);
-    }
-    if (p.out_fp32) {
-      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
-    } else {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(y[0], y[1]), b = __floats2bfloat162_rn(y[2], y[3]);
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    }
+  if (p.out_fp32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i >= valid) break;
-      if (res) y[i] += bf16_to_f32(res[i]);
-      if (p.out_fp32) static_cast<float*>(p.out)[at + i] = y[i];
-      else static_cast<__nv_bfloat16*>(p.out)[at + i] = __float2bfloat16_rn(y[i]);
-    }
+    const __nv_bfloat162 a = __floats2bfloat162_rn(y[0], y[1]), b = __floats2bfloat162_rn(y[2], y[3]);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
 }
 
+constexpr int kTokensMost = 2;  // of launch_linear_token
+cudaError_t launch_linear_token(const dt_linear_args& a, const LinearParams& p, cudaStream_t st);
 cudaError_t launch_linear_wide(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, bool gate,
                                cudaStream_t st);
 

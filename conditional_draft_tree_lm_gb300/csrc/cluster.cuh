@@ -36,4 +36,15 @@ DT_DEVINL uint64_t peer_ld_u64(uint32_t a) {
   return v;
 }
 
+// Whether a phase is complete, without waiting (try_wait may hold the thread for microseconds).
+DT_DEVINL bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 }  // namespace dt

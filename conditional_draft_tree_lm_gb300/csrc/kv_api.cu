@@ -1,7 +1,7 @@
 // Host-side helpers of the key/value cache entry points.
 #include <cuda.h>
 
-#include "kv.cuh"
+#include "linear.cuh"
 
 namespace dt {
 
@@ -51,6 +51,17 @@ bool kv_tmap_heads(CUtensorMap* tm, const void* base, int head_dim, int heads, i
   return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool linear_map(CUtensorMap* m, const void* base, int inner, int64_t rows, int64_t stride, int box_rows, int per) {
+  EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(per == 1 ? inner : 64), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(per == 1 ? 1 : inner / 64)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride) * 2, 128u};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(per)};
+  const cuuint32_t es[3] = {1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool kv_tmap_rows(CUtensorMap* tm, const void* base, int row_bytes, int64_t rows, int box_rows) {

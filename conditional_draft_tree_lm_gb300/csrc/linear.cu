@@ -1,11 +1,17 @@
 // dt_linear: matrix product with bias, activation or gate, and residual, on tcgen05.
 //
-// k_few: 128 rows of weight are the product's rows (its A operand) and up to 256 tokens its columns, so that few tokens
-// still fill the tensor core's 128 lanes, and the kernel streams the weights once; with a gate, 128 rows of each of the
-// two matrices, whose sums meet in one epilogue.  Where the tiles are fewer than the SMs, a cluster shares one: every CTA
-// takes a part of the inner dimension, and the partial sums, fp32 in shared memory, are added over distributed shared
-// memory in the order of ranks, each CTA finishing a part of the tile.  Tensor memory is given back before the cluster's
-// barrier: a CTA that holds some waits for no other, so that kernels side by side on an SM cannot wait in a circle.
+// Few tokens.  Rows of weight are the product's rows (its A operand, up to 128 of them) and up to 256 tokens its columns,
+// so that few tokens still fill the tensor core's lanes, and the kernels stream the weights once; with a gate, as many
+// rows of each of the two matrices, whose sums meet in one epilogue.
+//
+// k_stream, where there are tiles for half of the SMs or more: persistent, one CTA an SM with all its shared memory for the
+// stream, which runs on from tile to tile; two sets of accumulators, so that the epilogue of a tile stands beside the next
+// one's products.
+//
+// k_few, where there are fewer: a cluster shares a tile.  Every CTA takes a part of the inner dimension, and the partial
+// sums, fp32 in shared memory, are added over distributed shared memory in the order of ranks, each CTA finishing a
+// part of the tile.  Tensor memory is given back before the cluster's barrier: a CTA that holds some waits for no other, so
+// that kernels side by side on an SM cannot wait in a circle.
 #include "linear.cuh"
 #include "cluster.cuh"
 #include "kv_flash.cuh"
@@ -13,8 +19,29 @@
 namespace dt {
 namespace {
 
-constexpr int kFewThreads = 256;
+constexpr int kFewThreads = 256, kMostSplit = 8;
 constexpr uint32_t kTileBytes = 128 * 128;  // 128 rows of 64 bf16
+
+// A step of a stage: `per` blocks of 64 of the inner dimension (one copy: the map has them as a third dimension, where they
+// are whole), rows from `row` on, block after block.
+DT_DEVINL void load_step(void* to, const CUtensorMap& map, uint64_t* bar, int per, int step, int row, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(
+          smem_u32(to)),
+      "l"(reinterpret_cast<uint64_t>(&map)), "r"(smem_u32(bar)), "r"(per == 1 ? step * 64 : 0), "r"(row), "r"(per == 1 ? 0 : step * per), "l"(policy)
+      : "memory");
+}
+// Its products; tile: bytes of a block of one side's rows.
+template <int SIDES>
+DT_DEVINL void step_products(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, const LinearParams& p, uint32_t tile, bool more) {
+  for (int j = 0; j < p.per; ++j) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int s = 0; s < SIDES; ++s)
+        tc_mma_bf16(d + s * p.bn, a + (((s * p.per + j) * tile + k * 32) >> 4), b + ((j * p.bn * 128 + k * 32) >> 4), idesc, more || j != 0 || k != 0);
+  }
+}
 
 // Shared memory from the 1024-aligned base: the ring of stages (and behind the products the partial sums, in its place),
 // then the barriers.
@@ -38,18 +65,19 @@ __global__ void __launch_bounds__(kFewThreads)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(blockIdx.x) % p.split, tile = static_cast<int>(blockIdx.x) / p.split;
   const int n0 = tile * 128, t0 = static_cast<int>(blockIdx.y) * p.bn;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * rank / p.split);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (rank + 1) / p.split);
+  const int ks0 = static_cast<int>(static_cast<int64_t>(p.k_steps) * rank / p.split);
+  const int ks1 = static_cast<int>(static_cast<int64_t>(p.k_steps) * (rank + 1) / p.split);
   const uint64_t stream = l2_policy_evict_first(), keep = l2_policy_evict_last();
-  auto load = [&](int kb, uint32_t stage) {
+  const uint32_t side_bytes = p.per * kTileBytes;
+  auto load = [&](int ks, uint32_t stage) {
     uint8_t* at = smem + stage * p.stage_bytes;
     mbar_arrive_expect_tx(&full[stage], p.stage_bytes);
-    if (SIDES == 2) tma_load_2d(at, &tm_g, &full[stage], kb * 64, n0, stream);
-    tma_load_2d(at + (SIDES - 1) * kTileBytes, &tm_w, &full[stage], kb * 64, n0, stream);
-    tma_load_2d(at + SIDES * kTileBytes, &tm_x, &full[stage], kb * 64, t0, keep);
+    if (SIDES == 2) load_step(at, tm_g, &full[stage], p.per, ks, n0, stream);
+    load_step(at + (SIDES - 1) * side_bytes, tm_w, &full[stage], p.per, ks, n0, stream);
+    load_step(at + SIDES * side_bytes, tm_x, &full[stage], p.per, ks, t0, keep);
   };
   // the first loads are under way before tensor memory is asked for
-  const int ahead = min(p.stages, kb1 - kb0);
+  const int ahead = min(p.stages, ks1 - ks0);
   if (warp == 0) {
     if (elect_one()) {
       for (int s = 0; s < p.stages; ++s) {
@@ -59,7 +87,7 @@ __global__ void __launch_bounds__(kFewThreads)
       mbar_init(done, 1);
       mbar_init(drained, 1);
       fence_mbar_init();
-      for (int s = 0; s < ahead; ++s) load(kb0 + s, s);
+      for (int s = 0; s < ahead; ++s) load(ks0 + s, s);
     }
     __syncwarp();
   }
@@ -72,32 +100,31 @@ __global__ void __launch_bounds__(kFewThreads)
 
   if (warp == 0) {
     uint32_t stage = 0, phase = 0;
-    for (int kb = kb0 + ahead; kb < kb1; ++kb) {
+    for (int ks = ks0 + ahead; ks < ks1; ++ks) {
       ok = warp_wait(&empty[stage], phase);
       if (!ok) break;
-      if (elect_one()) load(kb, stage);
+      if (elect_one()) load(ks, stage);
       __syncwarp();
       if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
     }
   } else if (warp == 1) {
     const uint32_t idesc = idesc_bf16_f32(128, p.bn);
     uint32_t stage = 0, phase = 0;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      ok = warp_wait(&full[stage], phase);
+    bool there = false;
+    for (int ks = ks0; ks < ks1; ++ks) {
+      ok = there || warp_wait(&full[stage], phase);
       if (!ok) break;
       tc_fence_after();
       const uint32_t at = smem_u32(smem + stage * p.stage_bytes);
-      const uint64_t a = sdesc_k_sw128(at), b = sdesc_k_sw128(at + SIDES * kTileBytes);
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int s = 0; s < SIDES; ++s)
-            tc_mma_bf16(tmem + s * p.bn, a + ((s * kTileBytes + k * 32) >> 4), b + (k * 32 >> 4), idesc, kb != kb0 || k != 0);
-        tc_commit(&empty[stage]);
-      }
-      __syncwarp();
+      const uint64_t a = sdesc_k_sw128(at), b = sdesc_k_sw128(at + SIDES * side_bytes);
+      uint64_t* used = &empty[stage];
       if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
+      const bool next = mbar_test(&full[stage], phase);  // (asked before the products that stand in its way)
+      if (elect_one()) {
+        step_products<SIDES>(tmem, a, b, idesc, p, kTileBytes, ks != ks0);
+        tc_commit(used);
+      }
+      there = __all_sync(0xFFFFFFFFu, next);
     }
     if (elect_one()) tc_commit(ok ? done : drained);
     __syncwarp();
@@ -140,15 +167,175 @@ __global__ void __launch_bounds__(kFewThreads)
 #pragma unroll
     for (int s = 0; s < SIDES; ++s) {
       const float* at = sums + (t * SIDES + s) * 128 + f;
-      acc[s] = p.split > 1 ? peer_ld4(peer_addr(at, 0)) : *reinterpret_cast<const float4*>(at);
-      for (int r = 1; r < p.split; ++r) {
-        const float4 v = peer_ld4(peer_addr(at, r));
-        acc[s].x += v.x, acc[s].y += v.y, acc[s].z += v.z, acc[s].w += v.w;
+      if (p.split == 1) {
+        acc[s] = *reinterpret_cast<const float4*>(at);
+        continue;
       }
+      float4 v[kMostSplit];  // (all on their way before the first is added)
+#pragma unroll
+      for (int r = 0; r < kMostSplit; ++r)
+        if (r < p.split) v[r] = peer_ld4(peer_addr(at, r));
+      acc[s] = v[0];
+#pragma unroll
+      for (int r = 1; r < kMostSplit; ++r)
+        if (r < p.split) acc[s].x += v[r].x, acc[s].y += v[r].y, acc[s].z += v[r].z, acc[s].w += v[r].w;
     }
     finish4<SIDES>(p, t0 + t, n0 + f, acc[SIDES - 1], acc[0]);
   }
   if (p.split > 1) cluster_barrier();  // (no CTA leaves while its sums are read)
+}
+
+constexpr int kStreamThreads = 384, kStreamWarps = 8, kStreamTokens = 32;  // epilogue warps, and tokens that they write together
+
+// Shared memory: the ring of stages, 32 tokens' sums, the barriers.
+DT_HOST_DEVICE_INLINE uint32_t stream_sums(const LinearParams& p) { return p.stages * p.stage_bytes; }
+DT_HOST_DEVICE_INLINE uint32_t stream_bars(const LinearParams& p, int sides) { return stream_sums(p) + kStreamTokens * sides * 512u; }
+
+template <int SIDES>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    k_stream(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_g,
+             const __grid_constant__ CUtensorMap tm_x, const LinearParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* sums = reinterpret_cast<float*>(smem + stream_sums(p));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + stream_bars(p, SIDES));
+  uint64_t* empty = full + p.stages;
+  uint64_t* tfull = empty + p.stages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drained = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tiles = p.n_tiles * p.m_tiles;  // (m_tiles: of tokens)
+  const uint32_t tile_bytes = p.tile_outs * 128u, side_bytes = p.per * tile_bytes, acc_cols = SIDES * p.bn;
+  if (tid == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], kStreamWarps);
+    }
+    mbar_init(drained, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, p.tmem_cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+
+  if (warp == 0) {
+    const uint64_t stream = l2_policy_evict_first(), keep = l2_policy_evict_last();
+    uint32_t stage = 0, phase = 0;
+    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      const int n0 = tile / p.m_tiles * p.tile_outs, t0 = tile % p.m_tiles * p.bn;
+      for (int ks = 0; ks < p.k_steps; ++ks) {
+        ok = warp_wait(&empty[stage], phase ^ 1u);
+        if (!ok) break;
+        if (elect_one()) {
+          uint8_t* at = smem + stage * p.stage_bytes;
+          mbar_arrive_expect_tx(&full[stage], p.stage_bytes);
+          if (SIDES == 2) load_step(at, tm_g, &full[stage], p.per, ks, n0, stream);
+          load_step(at + (SIDES - 1) * side_bytes, tm_w, &full[stage], p.per, ks, n0, stream);
+          load_step(at + SIDES * side_bytes, tm_x, &full[stage], p.per, ks, t0, keep);
+        }
+        __syncwarp();
+        if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
+      }
+    }
+  } else if (warp == 1) {
+    // (rows of the product behind the tile's rows of weight come from whatever follows them, and go nowhere)
+    const uint32_t idesc = idesc_bf16_f32(128, p.bn);
+    uint32_t stage = 0, phase = 0;
+    int local = 0;
+    bool there = false;
+    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++local) {
+      const int acc = local & 1;
+      ok = warp_wait(&tempty[acc], (local >> 1 & 1) ^ 1u);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + acc * acc_cols;
+      for (int ks = 0; ks < p.k_steps; ++ks) {
+        ok = there || warp_wait(&full[stage], phase);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = smem_u32(smem + stage * p.stage_bytes);
+        const uint64_t a = sdesc_k_sw128(at), b = sdesc_k_sw128(at + SIDES * side_bytes);
+        uint64_t* used = &empty[stage];
+        if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
+        const bool next = mbar_test(&full[stage], phase);  // (asked before the products that stand in its way)
+        if (elect_one()) {
+          step_products<SIDES>(d, a, b, idesc, p, tile_bytes, ks != 0);
+          tc_commit(used);
+          if (ks + 1 == p.k_steps) tc_commit(&tfull[acc]);
+        }
+        there = __all_sync(0xFFFFFFFFu, next);
+      }
+    }
+    if (!ok) {  // (no product may outlive its operands and tensor memory)
+      if (elect_one()) tc_commit(drained);
+      __syncwarp();
+      mbar_wait(drained, 0, nullptr);
+    }
+  } else if (warp >= 4) {
+    const int quarter = warp & 3, half = (warp - 4) >> 2, et = tid - 128;
+    auto together = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    static_assert(kStreamWarps * 32 == 256 && kStreamTokens == 32, "");
+    int local = 0;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++local) {
+      const int acc = local & 1;
+      // (a wait that gave up in one warp: the others would wait for it at the barrier, so it goes on, and writes nothing)
+      ok = ok && warp_wait(&tfull[acc], local >> 1 & 1);
+      tc_fence_after();
+      const int n0 = tile / p.m_tiles * p.tile_outs, t0 = tile % p.m_tiles * p.bn, tokens = min(p.bn, p.rows - t0);
+      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * acc_cols;
+      for (int c0 = 0; c0 < tokens; c0 += kStreamTokens) {
+        const int c = c0 + 16 * half;  // 16 tokens of this warp's rows
+        if (c < p.bn && ok) {
+#pragma unroll
+          for (int s = 0; s < SIDES; ++s) {
+            uint32_t v[16];
+            tmem_ld16(from + s * p.bn + c, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sums[((16 * half + j) * SIDES + s) * 128 + quarter * 32 + lane] = __uint_as_float(v[j]);
+          }
+        }
+        if (c0 + kStreamTokens >= tokens) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[acc]);
+        }
+        together();
+        const int units = min(kStreamTokens, tokens - c0) * 32;
+        for (int u = et; u < units; u += 256) {
+          const int t = u >> 5, f = (u & 31) * 4;
+          if (f >= p.tile_outs || n0 + f >= p.outer || !ok) continue;
+          const float4* at = reinterpret_cast<const float4*>(sums + t * SIDES * 128 + f);
+          finish4<SIDES>(p, t0 + c0 + t, n0 + f, at[(SIDES - 1) * 32], at[0]);
+        }
+        together();
+      }
+    }
+  }
+  if (!ok && p.status && lane == 0) atomicOr(p.status, DT_KV_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+}
+
+template <int SIDES>
+cudaError_t launch_stream(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(k_stream<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e != cudaSuccess) return e;
+  const uint32_t smem = 1024 + stream_bars(p, SIDES) + (2 * p.stages + 5) * 8 + 16;
+  k_stream<SIDES><<<min(p.n_tiles * p.m_tiles, kSms), kStreamThreads, smem, st>>>(w, g, x, p);
+  return cudaGetLastError();
 }
 
 template <int SIDES>
@@ -157,7 +344,7 @@ cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& g, const CUtenso
   cudaError_t e = cudaFuncSetAttribute(k_few<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.outer + 127) / 128 * p.split), static_cast<unsigned>((p.rows + p.bn - 1) / p.bn));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.n_tiles * p.split), static_cast<unsigned>(p.m_tiles));
   cfg.blockDim = dim3(kFewThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -170,24 +357,64 @@ cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& g, const CUtenso
   return cudaLaunchKernelEx(&cfg, k_few<SIDES>, w, g, x, p);
 }
 
-// Few tokens: one tile of them, padded to 16, two CTAs an SM where their sums leave room for it, and clusters of as many
-// CTAs as leave all of them beside each other (clusters do not fill every SM), with four blocks of 64 or more each.
+// Few tokens: in one tile, padded to 16.
+void plan_tokens(LinearParams& p, int sides) {
+  const int most = 256 / sides;
+  p.m_tiles = (p.rows + most - 1) / most;
+  p.bn = ((p.rows + p.m_tiles - 1) / p.m_tiles + 15) & ~15;
+  p.m_tiles = (p.rows + p.bn - 1) / p.bn;
+}
+// Steps of the inner dimension and their stages in `room` bytes: two blocks of 64 a step where blocks are whole and three
+// such stages fit, since a step's copies, waits and products each have costs of their own.
+void steps_of(LinearParams& p, int sides, uint32_t room) {
+  const uint32_t block = (sides * p.tile_outs + p.bn) * 128u;
+  p.per = p.inner % 128 == 0 && room / (2 * block) >= 3 ? 2 : 1;
+  p.k_steps = (p.k_blocks + p.per - 1) / p.per;
+  p.stage_bytes = p.per * block;
+  p.stages = static_cast<int>(room / p.stage_bytes);
+  if (p.stages > 12) p.stages = 12;
+}
+int tmem_columns(int n) {
+  int cols = 32;
+  while (cols < n) cols *= 2;
+  return cols;
+}
+
+// Persistent CTAs: rows of weight for tiles that divide evenly over them.  False where a cluster's CTAs serve a tile better.
+bool plan_stream(LinearParams& p, int sides) {
+  const int64_t tiles = static_cast<int64_t>((p.outer + 127) / 128) * p.m_tiles;
+  if (tiles < kSms / 2 || tiles > (1 << 29)) return false;
+  const int64_t rounds = (tiles + kSms - 1) / kSms;
+  const int64_t per = (static_cast<int64_t>(p.outer) * p.m_tiles + rounds * kSms - 1) / (rounds * kSms);
+  p.tile_outs = static_cast<int>((per + 7) / 8 * 8);
+  if (p.tile_outs > 128) p.tile_outs = 128;
+  auto n_tiles = [&] { return (p.outer + p.tile_outs - 1) / p.tile_outs; };
+  while (p.tile_outs < 128 && static_cast<int64_t>(n_tiles()) * p.m_tiles > rounds * kSms) p.tile_outs += 8;
+  p.n_tiles = n_tiles();
+  p.tmem_cols = tmem_columns(2 * sides * p.bn);
+  steps_of(p, sides, 224u * 1024 - 1024 - kStreamTokens * sides * 512);
+  return true;
+}
+
+// Clusters of as many CTAs as leave all of them beside each other: with one CTA an SM 128 or so are (36 clusters of 4: one
+// wave takes 32), with two 256; and with four blocks of 64 or more each.  Two CTAs an SM for up to 64 tokens, and where
+// one would leave clusters of two.  us with two and with one an SM: 4 tokens, 2560 to 6144 9.4 (4 CTAs a cluster) and 10.0 (2);
+// 16, 4096 to 2560 8.5 (8) and 8.7 (4); 65, 4096 to 2560 10.6 and 9.9 (6); 65, 2560 to 6144 11.8 (5) and 12.3 (2); 128, 4096 to
+// 4096 14.8 and 13.1 (4).
 void plan_few(LinearParams& p, int sides) {
-  const int most = 256 / sides, token_tiles = (p.rows + most - 1) / most;
-  p.bn = ((p.rows + token_tiles - 1) / token_tiles + 15) & ~15;
-  p.tmem_cols = 32;
-  while (p.tmem_cols < sides * p.bn) p.tmem_cols *= 2;
-  p.stage_bytes = sides * kTileBytes + p.bn * 128;
-  const bool two = sides * p.bn <= 128;
-  p.stages = static_cast<int>((two ? 110u * 1024 : 220u * 1024) / p.stage_bytes);
-  if (p.stages > 8) p.stages = 8;
-  const int64_t tiles = static_cast<int64_t>((p.outer + 127) / 128) * token_tiles;
+  p.tile_outs = 128;
+  p.n_tiles = (p.outer + 127) / 128;
+  p.tmem_cols = tmem_columns(sides * p.bn);
+  const int64_t tiles = static_cast<int64_t>(p.n_tiles) * p.m_tiles;
+  const bool two = sides * p.bn <= 64 || (sides * p.bn <= 128 && 3 * tiles > 128);
+  steps_of(p, sides, two ? 110u * 1024 : 220u * 1024);
   p.split = 1;
-  while (p.split < 8 && tiles * (p.split + 1) <= (two ? 2 * kSms : kSms) * 7 / 8 && p.k_blocks >= 4 * (p.split + 1)) ++p.split;
+  while (p.split < kMostSplit && tiles * (p.split + 1) <= (two ? 256 : 128) && p.k_steps * p.per >= 4 * (p.split + 1)) ++p.split;
 }
 
 // Many tokens: the tile's columns so that the pairs' rounds of tiles cost least, a tile as much as its columns and 32 more.
 void plan_many(LinearParams& p, int sides) {
+  p.per = 1;
   p.m_tiles = (p.rows + 255) / 256;
   int64_t least = INT64_MAX;
   for (int bn = 256; bn >= 64; bn -= 32 * sides) {
@@ -204,8 +431,6 @@ void plan_many(LinearParams& p, int sides) {
 }
 
 }  // namespace
-
-bool make_tmap_bf16_2d(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t rows, uint64_t row_stride_bytes, uint32_t box_rows);
 
 }  // namespace dt
 
@@ -240,6 +465,7 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
   p.out_stride = a.out_row_stride;
   p.rows = static_cast<int>(a.rows);
   p.outer = a.outer;
+  p.inner = a.inner;
   p.k_blocks = (a.inner + 63) / 64;
   p.activation = a.activation;
   p.out_fp32 = a.out_fp32 != 0;
@@ -252,19 +478,25 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
   const int64_t at_once = many ? 16 / static_cast<int64_t>(bytes) : 4;  // outputs written together
   p.wide = out % (at_once * bytes) == 0 && (a.rows == 1 || a.out_row_stride % at_once == 0) &&
            (!res || (many ? res % 16 == 0 && a.residual_row_stride % 8 == 0 : res % 8 == 0 && (a.rows == 1 || a.residual_row_stride % 4 == 0)));
+  bool stream_tiles = false;
   if (many) {
     plan_many(p, sides);
     if (static_cast<int64_t>(p.m_tiles) * p.n_tiles > (1 << 30)) return kv_fail(DT_ERR_SHAPE, "%s: more than 2^30 tiles", who);
   } else {
-    plan_few(p, sides);
-    if (static_cast<int64_t>((a.outer + 127) / 128) * p.split > 0x7FFFFFFF) return kv_fail(DT_ERR_SHAPE, "%s: too many tiles", who);
+    plan_tokens(p, sides);
+    stream_tiles = plan_stream(p, sides);
+    if (!stream_tiles) plan_few(p, sides);
   }
-  auto stride = [&](int64_t s, int64_t rows) { return static_cast<uint64_t>(rows == 1 ? (a.inner + 7) / 8 * 8 : s) * 2; };
+  const int w_rows = many ? p.bn / 2 : p.tile_outs;
+  auto map = [&](CUtensorMap* m, const void* d, int64_t stride, int64_t rows, int box) {
+    return linear_map(m, d, a.inner, rows, rows == 1 ? a.inner : stride, box, p.per);
+  };
   CUtensorMap w, g, x;
-  if (!make_tmap_bf16_2d(&w, a.weight, a.inner, a.outer, stride(a.weight_row_stride, a.outer), many ? p.bn / 2 : 128) ||
-      !make_tmap_bf16_2d(&g, a.gate ? a.gate : a.weight, a.inner, a.outer, stride(a.gate ? a.gate_row_stride : a.weight_row_stride, a.outer), many ? p.bn / 2 : 128) ||
-      !make_tmap_bf16_2d(&x, a.x, a.inner, a.rows, stride(a.x_row_stride, a.rows), many ? 128 : p.bn))
+  if (!map(&w, a.weight, a.weight_row_stride, a.outer, w_rows) ||
+      !map(&g, a.gate ? a.gate : a.weight, a.gate ? a.gate_row_stride : a.weight_row_stride, a.outer, w_rows) ||
+      !map(&x, a.x, a.x_row_stride, a.rows, many ? 128 : p.bn))
     return kv_fail(DT_ERR_SHAPE, "%s: strides that a tensor map does not take (2^40 bytes and more)", who);
   if (many) return kv_launched(who, launch_linear_wide(w, g, x, p, sides == 2, st));
+  if (stream_tiles) return kv_launched(who, sides == 2 ? launch_stream<2>(w, g, x, p, st) : launch_stream<1>(w, g, x, p, st));
   return kv_launched(who, sides == 2 ? launch_few<2>(w, g, x, p, st) : launch_few<1>(w, g, x, p, st));
 }

@@ -11,12 +11,13 @@ struct LinearParams {
   const uint16_t* residual;
   void* out;
   int64_t residual_stride, out_stride;
-  int rows, outer, k_blocks;  // k_blocks: of 64
+  int rows, outer, inner, k_blocks;  // k_blocks: of 64
+  int per, k_steps;           // blocks of a step, steps
   int activation, out_fp32;
-  int bn, stages, tmem_cols;  // few rows: tokens of a tile
+  int bn, stages, tmem_cols;        // bn: few rows: tokens of a tile; many: its columns (with a gate, two for an output)
   int split;                  // CTAs of a cluster
   uint32_t stage_bytes;
-  int m_tiles, n_tiles, tile_outs;  // many rows: tiles of 256 tokens, of outputs, and outputs of a tile (bn: its columns)
+  int m_tiles, n_tiles, tile_outs;  // tiles of tokens, of outputs, and outputs of a tile
   int wide;  // outputs (and residuals) are written and read 4 at a time, or 16 bytes where rows are many
   int32_t* status;
 };
@@ -105,6 +106,10 @@ DT_DEVINL void finish4(const LinearParams& p, int64_t t, int n, const float4& y4
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
 }
+
+// Rows of bf16 (stride in elements) as a 3D map, swizzled by 128 bytes: boxes of 64 channels x box_rows rows x per blocks of
+// 64 channels, which have to be whole where per > 1 (per 1: the first coordinate is the channel, the third 0).
+bool linear_map(CUtensorMap* m, const void* base, int inner, int64_t rows, int64_t stride, int box_rows, int per);
 
 constexpr int kTokensMost = 2;  // of launch_linear_token
 cudaError_t launch_linear_token(const dt_linear_args& a, const LinearParams& p, cudaStream_t st);

@@ -45,13 +45,13 @@ DT_DEVINL void tc_commit_pair(uint64_t* bar) {
 // A box into this CTA's shared memory, counted on a barrier of either CTA (a cluster address).
 DT_DEVINL void tma_load_pair(void* dst, const void* tmap, uint32_t bar, int x, int y, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(0), "l"(policy)
       : "memory");
 }
 DT_DEVINL void peer_arrive(uint32_t bar) { asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory"); }
-// Bounded wait for arrivals from the whole cluster.
+// Bounded wait of a warp for arrivals from the whole cluster.
 DT_DEVINL bool pair_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok = 0, n = 0;
   uint64_t t0 = 0;
@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const uint32_t idesc = idesc_bf16_f32(256, p.bn);
     uint32_t stage = 0, phase = 0;
     int local = 0;
+    bool there = false;
     for (int tile = pair; tile < tiles && ok; tile += pairs, ++local) {
       const int acc = local & 1;
       ok = pair_wait(&tempty[acc], (local >> 1 & 1) ^ 1u);
@@ -156,19 +157,21 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       tc_fence_after();
       const uint32_t d = tmem + acc * 256;
       for (int kb = 0; kb < p.k_blocks; ++kb) {
-        ok = pair_wait(&full[stage], phase);
+        ok = there || pair_wait(&full[stage], phase);
         if (!ok) break;
         tc_fence_after();
         const uint32_t at = smem_u32(smem + stage * kWideStage);
         const uint64_t a = sdesc_k_sw128(at), b = sdesc_k_sw128(at + kHalf);
+        uint64_t* used = &empty[stage];
+        if (++stage == kWideStages) stage = 0, phase ^= 1u;
+        const bool next = mbar_test(&full[stage], phase);  // (asked before the products that stand in its way)
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) tc_mma_pair(d, a + (k * 32 >> 4), b + (k * 32 >> 4), idesc, kb != 0 || k != 0);
-          tc_commit_pair(&empty[stage]);
+          tc_commit_pair(used);
           if (kb + 1 == p.k_blocks) tc_commit_pair(&tfull[acc]);
         }
-        __syncwarp();
-        if (++stage == kWideStages) stage = 0, phase ^= 1u;
+        there = __all_sync(0xFFFFFFFFu, next);
       }
     }
     if (!ok) {  // (no product may outlive its operands and tensor memory)

@@ -2,124 +2,166 @@
 //
 // A head is held by G lanes (a power of two), 16 channels a lane, as the two pieces of 8 whose channels turn together:
 // pieces i and i + rot / 2 (halves) or 16 neighbouring channels.  So a lane reads and writes 16 bytes at a time, the sum
-// of squares takes log2 G shuffles, and the rotation none.  A lane's 8 angles are the same for every head of a row: a
-// warp takes several heads of one row, and has cosines and sines once.
+// of squares takes log2 G shuffles, and the rotation none.  A CTA takes all heads of a row (of several rows beside each
+// other where heads are few), so that its cosines are had once, by its threads together, into shared memory, and where rows
+// are many two such rows one after the other, whose channels are all on their way before the cosines are computed: a
+// thread keeps its place in the heads, so that its addresses and weights serve two rows.
 //
 // Angles: a position times turns[i], in 64-bit integers, wraps by whole turns; the upper 32 bits are what is left of a
 // turn, and exact for any position (fp32 has lost a radian at position 2^24).
 //
-// Bound by memory where there are many rows, by the latency of one pass where there are few.
-#include "kv.cuh"
+// Bound by instructions and memory alike where there are many rows: 32k rows of 32 + 8 heads of 128 124 us, 5.4 TB/s (one row a
+// CTA 159 us, with 326 instructions a warp in 67 % of the issue slots; four rows 127 us; persistent CTAs with the next row ahead
+// 149 us; without norms 116 us), by the latency of one pass where there are few: 32 rows 2.6 us.
+#include "kv_flash.cuh"
 
 namespace dt {
 namespace {
 
-constexpr int kRotateThreads = 256;
+constexpr int kRotateThreads = 512;  // of a CTA at most
+constexpr int kMaxAngles = 1024;     // of the rows that a CTA takes at once
 
 struct RotateParams {
   dt_qk_norm_rope_args a;
   int64_t rows;
-  int lanes;      // of a head that hold channels
-  int pairs;      // of those, lanes whose channels turn
-  int per_warp;   // heads of a warp
-  int row_warps;  // warps of a row
+  int lanes;   // of a head that hold channels
+  int pairs;   // of those, lanes whose channels turn
+  int heads;   // of a CTA (blockIdx.y counts those)
+  int at_once; // rows of a CTA
+  float one_over;  // 1 / head_dim
 };
 
-DT_DEVINL void unpack8(const uint4& r, float* v) {
+// 8 bf16 as pairs of fp32, and back.
+DT_DEVINL void unpack8(const uint4& r, uint64_t* v) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) v[i] = f32x2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-DT_DEVINL uint4 pack8(const float* v) {
+DT_DEVINL uint4 pack8(const uint64_t* v) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    float lo, hi;
+    f32x2_parts(v[i], lo, hi);
+    w[i] = pack_p(lo, hi);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int G, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRotateThreads) k_rotate(const RotateParams p) {
+template <int G, bool INTERLEAVED, int ROWS>
+__global__ void __launch_bounds__(kRotateThreads, ROWS == 1 ? 3 : 2) k_rotate(const RotateParams p) {
+  __shared__ __align__(16) float s_cos[kMaxAngles], s_sin[kMaxAngles];
   const dt_qk_norm_rope_args& a = p.a;
-  const int lane = threadIdx.x & 31, part = lane % G;
-  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kRotateThreads / 32) + (threadIdx.x >> 5);
-  const int64_t row = warp / p.row_warps;
-  if (row >= p.rows) return;
-  const int first = static_cast<int>(warp - row * p.row_warps) * p.per_warp, heads = a.n_q + a.n_kv;
-  const int last = min(heads, first + p.per_warp);
-  const bool holds = part < p.lanes, turns = part < p.pairs;
-  const int at0 = !INTERLEAVED && turns ? 8 * part : 16 * part, at1 = !INTERLEAVED && turns ? a.rot / 2 + 8 * part : 16 * part + 8;
-
-  const int off = a.positions ? a.positions[row] : 0;
-  if (off < 0) return;
-  float cs[8], sn[8];
+  const int tid = threadIdx.x, part = tid % G, unit = tid / G;
+  const int nth = p.at_once == 1 ? 0 : unit / p.heads, h = blockIdx.y * p.heads + unit - nth * p.heads;  // row beside the others, head
+  const bool key = h >= a.n_q, turns = part < p.pairs;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (ROWS * p.at_once), row0 = first + nth;
+  const bool holds = part < p.lanes && nth < p.at_once && h < a.n_q + a.n_kv;
+  const int left_rows = holds ? static_cast<int>(min(static_cast<int64_t>(ROWS * p.at_once), p.rows - row0)) : 0;  // row r is there where r at_once < left_rows
+  const int at0 = !INTERLEAVED && turns ? 8 * part : 16 * part, apart = !INTERLEAVED && turns ? a.rot / 2 : 8;
+  const __nv_bfloat16* weight = static_cast<const __nv_bfloat16*>(key ? a.k_weight : a.q_weight);
+  const int head = key ? h - a.n_q : h;
+  const int64_t from_row = key ? a.k_row_stride : a.q_row_stride;
+  const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(key ? a.k : a.q) + row0 * from_row + head * (key ? a.k_head_stride : a.q_head_stride) + at0;
+  uint4 x[ROWS][2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = 1.0f, sn[i] = 0.0f;
-  if (turns) {
-    const int64_t req = row / a.slots;
-    const int64_t pos = (a.base ? static_cast<int64_t>(a.base[req]) : 0) + (a.positions ? off : row - req * a.slots);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int left = static_cast<int>((a.turns[8 * part + i] * static_cast<uint64_t>(pos)) >> 32);
-      sincospif(static_cast<float>(left) * 0x1p-31f, &sn[i], &cs[i]);
-      cs[i] *= a.amplitude;
-      sn[i] *= a.amplitude;
+  for (int r = 0; r < ROWS; ++r)
+    if (r * p.at_once < left_rows) {
+      const __nv_bfloat16* at = from + r * p.at_once * from_row;
+      x[r][0] = *reinterpret_cast<const uint4*>(at);
+      x[r][1] = *reinterpret_cast<const uint4*>(at + apart);
+    } else {
+      x[r][0] = x[r][1] = make_uint4(0, 0, 0, 0);
     }
+  uint4 w0 = {}, w1 = {};
+  if (holds && weight) {
+    w0 = *reinterpret_cast<const uint4*>(weight + at0);
+    w1 = *reinterpret_cast<const uint4*>(weight + at0 + apart);
   }
-  for (int h0 = first; h0 < last; h0 += 32 / G) {
-    const int h = h0 + lane / G;
-    const bool here = holds && h < last, key = h >= a.n_q;
-    const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(key ? a.k : a.q) +
-                                (key ? row * a.k_row_stride + (h - a.n_q) * a.k_head_stride : row * a.q_row_stride + h * a.q_head_stride);
-    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(key ? a.k_out : a.q_out) +
-                        (key ? row * a.k_out_row_stride + (h - a.n_q) * a.k_out_head_stride : row * a.q_out_row_stride + h * a.q_out_head_stride);
-    const __nv_bfloat16* weight = static_cast<const __nv_bfloat16*>(key ? a.k_weight : a.q_weight);
-    float v[16];
+  // (the channels are asked for whether a row is written or not: else they would wait for its position)
+  int off[ROWS];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-    if (here) {
-      unpack8(*reinterpret_cast<const uint4*>(from + at0), v);
-      unpack8(*reinterpret_cast<const uint4*>(from + at1), v + 8);
+  for (int r = 0; r < ROWS; ++r) off[r] = a.positions && r * p.at_once < left_rows ? a.positions[row0 + r * p.at_once] : 0;
+  const int angles = a.rot / 2, rows = static_cast<int>(min(static_cast<int64_t>(ROWS * p.at_once), p.rows - first));
+  for (int e = tid; e < rows * angles; e += blockDim.x) {
+    const int r = e / angles, i = e - r * angles;
+    const uint32_t row = static_cast<uint32_t>(first + r), req = a.base || !a.positions ? row / static_cast<uint32_t>(a.slots) : 0;
+    const int64_t pos = (a.base ? static_cast<int64_t>(a.base[req]) : 0) + (a.positions ? a.positions[row] : static_cast<int>(row - req * a.slots));
+    const int left = static_cast<int>((a.turns[i] * static_cast<uint64_t>(pos)) >> 32);
+    float c, s;
+    sincospif(static_cast<float>(left) * 0x1p-31f, &s, &c);
+    s_cos[e] = c * a.amplitude;
+    s_sin[e] = s * a.amplitude;
+  }
+  __syncthreads();
+  uint64_t w[8];
+  unpack8(w0, w);
+  unpack8(w1, w + 4);
+  const int64_t to_row = key ? a.k_out_row_stride : a.q_out_row_stride;
+  __nv_bfloat16* to = static_cast<__nv_bfloat16*>(key ? a.k_out : a.q_out) + row0 * to_row + head * (key ? a.k_out_head_stride : a.q_out_head_stride) + at0;
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    uint64_t v[8];
+    unpack8(x[r][0], v);
+    unpack8(x[r][1], v + 4);
+    if (weight) {  // (the same for all lanes of a head)
+      uint64_t sum2 = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum2 = fma2(v[i], v[i], sum2);
+      float sum, other;
+      f32x2_parts(sum2, sum, other);
+      sum += other;
+      const uint32_t lanes = ((1u << G) - 1u) << (tid & 31 & ~(G - 1));
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(lanes, sum, o);
+      const float scale = rsqrtf(fmaf(sum, p.one_over, a.eps));
+      const uint64_t scale2 = f32x2(scale, scale);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = mul2(mul2(v[i], scale2), w[i]);
     }
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) sum = fmaf(v[i], v[i], sum);
-#pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (!here) continue;
-    if (weight) {
-      const float r = rsqrtf(sum / static_cast<float>(a.head_dim) + a.eps);
-      float w[16];
-      unpack8(*reinterpret_cast<const uint4*>(weight + at0), w);
-      unpack8(*reinterpret_cast<const uint4*>(weight + at1), w + 8);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = v[i] * r * w[i];
-    }
+    if (r * p.at_once >= left_rows || off[r] < 0) continue;
     if (turns) {
+      const int at = (r * p.at_once + nth) * angles + 8 * part;
+      const float4* cs = reinterpret_cast<const float4*>(&s_cos[at]);
+      const float4* sn = reinterpret_cast<const float4*>(&s_sin[at]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float& x = INTERLEAVED ? v[2 * i] : v[i];
-        float& y = INTERLEAVED ? v[2 * i + 1] : v[8 + i];
-        const float u = x * cs[i] - y * sn[i];
-        y = y * cs[i] + x * sn[i];
-        x = u;
+      for (int j = 0; j < 2; ++j) {
+        const float4 c = cs[j], s = sn[j];
+        if (INTERLEAVED) {  // (a, b) (c, c) + (b, a) (-s, s)
+          const float c4[4] = {c.x, c.y, c.z, c.w}, s4[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float y, z;
+            f32x2_parts(v[4 * j + i], y, z);
+            v[4 * j + i] = fma2(f32x2(z, y), f32x2(-s4[i], s4[i]), mul2(v[4 * j + i], f32x2(c4[i], c4[i])));
+          }
+        } else {
+          const uint64_t c2[2] = {f32x2(c.x, c.y), f32x2(c.z, c.w)}, s2[2] = {f32x2(s.x, s.y), f32x2(s.z, s.w)};
+          const uint64_t minus[2] = {f32x2(-s.x, -s.y), f32x2(-s.z, -s.w)};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint64_t y = v[2 * j + i], z = v[4 + 2 * j + i];
+            v[2 * j + i] = fma2(z, minus[i], mul2(y, c2[i]));
+            v[4 + 2 * j + i] = fma2(y, s2[i], mul2(z, c2[i]));
+          }
+        }
       }
     }
-    *reinterpret_cast<uint4*>(to + at0) = pack8(v);
-    *reinterpret_cast<uint4*>(to + at1) = pack8(v + 8);
+    __nv_bfloat16* at = to + r * p.at_once * to_row;
+    *reinterpret_cast<uint4*>(at) = pack8(v);
+    *reinterpret_cast<uint4*>(at + apart) = pack8(v + 4);
   }
 }
 
-template <int G>
-cudaError_t launch(const RotateParams& p, int64_t blocks, cudaStream_t st) {
-  if (p.a.interleaved) k_rotate<G, true><<<static_cast<unsigned>(blocks), kRotateThreads, 0, st>>>(p);
-  else k_rotate<G, false><<<static_cast<unsigned>(blocks), kRotateThreads, 0, st>>>(p);
+template <int G, bool INTERLEAVED>
+cudaError_t launch(const RotateParams& p, int sequence, dim3 grid, int threads, cudaStream_t st) {
+  if (sequence == 2) k_rotate<G, INTERLEAVED, 2><<<grid, threads, 0, st>>>(p);
+  else k_rotate<G, INTERLEAVED, 1><<<grid, threads, 0, st>>>(p);
   return cudaGetLastError();
+}
+template <int G>
+cudaError_t launch(const RotateParams& p, int sequence, dim3 grid, int threads, cudaStream_t st) {
+  return p.a.interleaved ? launch<G, true>(p, sequence, grid, threads, st) : launch<G, false>(p, sequence, grid, threads, st);
 }
 
 }  // namespace
@@ -158,16 +200,19 @@ extern "C" dt_status dt_qk_norm_rope(const dt_qk_norm_rope_args* args, void* str
   p.rows = rows;
   p.lanes = a.head_dim / 16;
   p.pairs = a.rot / 16;
+  p.one_over = 1.0f / static_cast<float>(a.head_dim);
   int g = 2;
   while (g < p.lanes) g *= 2;
-  // A warp takes as many heads of a row as leave 16 warps an SM (its cosines are had once), at least one of each lane group.
-  const int heads = a.n_q + a.n_kv, step = 32 / g, most = (heads + step - 1) / step;
-  const int64_t wanted = (16 * kSms + rows - 1) / rows;
-  p.row_warps = static_cast<int>(wanted < most ? wanted : most);
-  p.per_warp = (most + p.row_warps - 1) / p.row_warps * step;
-  p.row_warps = (heads + p.per_warp - 1) / p.per_warp;
-  const int64_t blocks = (rows * p.row_warps + kRotateThreads / 32 - 1) / (kRotateThreads / 32);
-  if (blocks > 0x7FFFFFFF) return kv_fail(DT_ERR_SHAPE, "%s: too many rows and heads for one launch", who);
+  // All heads of a row to a CTA where they fit, as many rows beside each other as make 256 threads, and two of those one
+  // after the other, while two CTAs an SM are left.
+  const int heads = a.n_q + a.n_kv, most = kRotateThreads / g, parts = (heads + most - 1) / most;
+  p.heads = (heads + parts - 1) / parts;
+  auto enough = [&](int n) { return n * (a.rot / 2) <= kMaxAngles && rows >= 2 * kSms * static_cast<int64_t>(n); };
+  p.at_once = 256 / (p.heads * g) > 1 ? 256 / (p.heads * g) : 1;
+  while (p.at_once > 1 && !enough(p.at_once)) --p.at_once;
+  const int sequence = enough(2 * p.at_once) ? 2 : 1;
+  const int threads = (p.at_once * p.heads * g + 31) / 32 * 32;
+  const dim3 grid(static_cast<unsigned>((rows + p.at_once * sequence - 1) / (p.at_once * sequence)), static_cast<unsigned>(parts));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return kv_launched(who, g == 2 ? launch<2>(p, blocks, st) : g == 4 ? launch<4>(p, blocks, st) : g == 8 ? launch<8>(p, blocks, st) : launch<16>(p, blocks, st));
+  return kv_launched(who, g == 2 ? launch<2>(p, sequence, grid, threads, st) : g == 4 ? launch<4>(p, sequence, grid, threads, st) : g == 8 ? launch<8>(p, sequence, grid, threads, st) : launch<16>(p, sequence, grid, threads, st));
 }

@@ -2,6 +2,7 @@
 // checks, the smallest power-of-two scale, e4m3 conversions.
 #pragma once
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 
@@ -96,6 +97,20 @@ inline dt_status kv_fail(dt_status s, const char* fmt, ...) {
 inline dt_status kv_launched(const char* who, cudaError_t e) {
   if (e == cudaSuccess) return DT_OK;
   return kv_fail(DT_ERR_CUDA, "%s: launch failed: %s (%d)", who, cudaGetErrorString(e), static_cast<int>(e));
+}
+
+// Settings that a kernel needs once on every device, before its first launch there: `set` runs then, and not again (the call
+// costs a third of a microsecond).  done: a bit for each device.
+template <class Set>
+cudaError_t once_a_device(std::atomic<uint64_t>& done, Set set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit & done.load(std::memory_order_acquire)) return cudaSuccess;
+  e = set();
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 inline bool kv_page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }

@@ -331,7 +331,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
 template <int SIDES>
 cudaError_t launch_stream(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(k_stream<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = once_a_device(done, [] { return cudaFuncSetAttribute(k_stream<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024); });
   if (e != cudaSuccess) return e;
   const uint32_t smem = 1024 + stream_bars(p, SIDES) + (2 * p.stages + 5) * 8 + 16;
   k_stream<SIDES><<<min(p.n_tiles * p.m_tiles, kSms), kStreamThreads, smem, st>>>(w, g, x, p);
@@ -341,7 +342,8 @@ cudaError_t launch_stream(const CUtensorMap& w, const CUtensorMap& g, const CUte
 template <int SIDES>
 cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, cudaStream_t st) {
   const uint32_t smem = 1024 + few_bars(p, SIDES) + (2 * p.stages + 2) * 8 + 16;
-  cudaError_t e = cudaFuncSetAttribute(k_few<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = once_a_device(done, [] { return cudaFuncSetAttribute(k_few<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024); });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.n_tiles * p.split), static_cast<unsigned>(p.m_tiles));

@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 
 template <int SIDES>
 cudaError_t launch(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(k_wide<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = once_a_device(done, [] { return cudaFuncSetAttribute(k_wide<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem); });
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
   cudaLaunchConfig_t cfg = {};

@@ -386,8 +386,11 @@ __global__ void __launch_bounds__(kLogpThreads, 4) k_logp(const LogpParams p) {
 
 template <bool BF16, int PER>
 cudaError_t launch(const LogpParams& p, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(k_logp<BF16, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, logp_smem(PER > 0));
-  if (e == cudaSuccess && p.split > 8) e = cudaFuncSetAttribute(k_logp<BF16, PER>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = once_a_device(done, [] {
+    const cudaError_t e = cudaFuncSetAttribute(k_logp<BF16, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, logp_smem(PER > 0));
+    return e == cudaSuccess ? cudaFuncSetAttribute(k_logp<BF16, PER>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : e;
+  });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.a.rows * p.split));

@@ -75,12 +75,12 @@ def _refused(status, where):
 def _rows(t, cols, dtypes, name, index):
     """Pointer, number of rows and row stride of a tensor [..., cols] of one of `dtypes`, whose columns are adjacent and
     whose leading dimensions fold into one row index (the stride of a dimension of one entry is not looked at)."""
+    shape, st = t.shape, t.stride()
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.get_device() != index:
         raise ValueError(f"{name}: on {t.device}, the others on cuda:{index}")
-    shape, st = t.shape, t.stride()
-    if len(shape) == 2 and shape[1] == cols and (st[1] == 1 or cols == 1):
+    if len(shape) == 2 and shape[1] == cols and st[1] == 1:
         return t.data_ptr(), shape[0], st[0] if shape[0] > 1 else cols
     if len(shape) < 1 or shape[-1] != cols:
         raise ValueError(f"{name}: expected [..., {cols}], got {tuple(shape)}")
@@ -93,6 +93,19 @@ def _rows(t, cols, dtypes, name, index):
     if cols > 1 and st[-1] != 1:
         raise ValueError(f"{name}: strides {st}: columns must be adjacent")
     return t.data_ptr(), rows, cols if stride is None else stride
+
+
+def _head_rows(t, shape, dtype, name, index):
+    """As ``kvcache._heads``, in a shorter way for the usual strides."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        st = t.stride()
+        if len(st) == 4:
+            n, slots, heads, _ = shape
+            if st[3] == 1 and heads > 1 and n > 1 and (slots == 1 or st[0] == st[1] * slots):
+                return t.data_ptr(), st[0] if slots == 1 else st[1], st[2]
+        elif st[2] == 1 and shape[0] > 1 and shape[1] > 1:
+            return t.data_ptr(), st[0], st[1]
+    return _heads(t, tuple(shape[:-2]), shape[-2], shape[-1], name, index)
 
 
 def _status(status, index):
@@ -183,41 +196,45 @@ def qk_norm_rope(q, k=None, *, positions=None, base=None, rotary=None, q_weight=
     import torch
     lib = _library()
     dev = _on_device(q, "q")
-    if q.dim() not in (3, 4):
+    bf16, i32, shape = torch.bfloat16, torch.int32, q.shape
+    if len(shape) == 4:
+        n_req, slots, heads, dim = shape
+    elif len(shape) == 3:
+        n_req, (slots, heads, dim) = 1, shape
+    else:
         raise ValueError("q: expected [rows, heads, head_dim] or [n_req, slots, heads, head_dim]")
-    lead = tuple(q.shape[:-2])
-    heads, dim = q.shape[-2:]
-    n_req, slots = lead if len(lead) == 2 else (1, lead[0])
-    rows = n_req * slots
-
-    def of(t, n, name):
-        if t is not None and rows == 0:
-            if t.shape != (*lead, n, dim) or t.dtype is not torch.bfloat16:
-                raise ValueError(f"{name}: expected {(*lead, n, dim)} torch.bfloat16, got {tuple(t.shape)} {t.dtype}")
-            return 0, 0, 0
-        return (0, 0, 0) if t is None else _heads(t, lead, n, dim, name, dev)
-
-    kv = 0
+    rows, kv, k_shape = n_req * slots, 0, None
     if k is not None:
-        if k.dim() != q.dim():
-            raise ValueError("k: expected as many dimensions as q")
-        kv = k.shape[-2]
+        k_shape = k.shape
+        kv = k_shape[-2] if len(k_shape) == len(shape) else 0
+        if kv == 0 or k_shape[-1] != dim or k_shape[0] != shape[0] or (len(shape) == 4 and k_shape[1] != slots):
+            raise ValueError(f"k: expected {(*shape[:-2], 'heads', dim)}, got {tuple(k.shape)}")
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out or k_weight without k")
     if q_out is None or (k is not None and k_out is None):
         with _allocating(stream):
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k is not None and k_out is None else k_out
-    qp, qr, qh = of(q, heads, "q")
-    kp, kr, kh = of(k, kv, "k")
-    qop, qor, qoh = of(q_out, heads, "q_out")
-    kop, kor, koh = of(k_out, kv, "k_out")
-    bf16, i32 = torch.bfloat16, torch.int32
-    a = _pack_rotate(n_req, slots, heads, kv, dim, 0 if rotary is None else rotary.dim, rotary is not None and rotary.interleaved,
-                     eps, 1.0 if rotary is None else rotary.amplitude, qp, kp, qr, qh, kr, kh,
+            q_out = torch.empty(shape, dtype=bf16, device=q.device) if q_out is None else q_out
+            k_out = torch.empty(k_shape, dtype=bf16, device=q.device) if k is not None and k_out is None else k_out
+    kp = kr = kh = kop = kor = koh = 0
+    if rows:
+        qp, qr, qh = _head_rows(q, shape, bf16, "q", dev)
+        qop, qor, qoh = _head_rows(q_out, shape, bf16, "q_out", dev)
+        if k is not None:
+            kp, kr, kh = _head_rows(k, k_shape, bf16, "k", dev)
+            kop, kor, koh = _head_rows(k_out, k_shape, bf16, "k_out", dev)
+    else:
+        qp = qr = qh = qop = qor = qoh = 0
+        for t, s, name in ((q, shape, "q"), (q_out, shape, "q_out"), (k, k_shape, "k"), (k_out, k_shape, "k_out")):
+            if t is not None and (t.shape != s or t.dtype is not bf16):
+                raise ValueError(f"{name}: expected {tuple(s)} {bf16}, got {tuple(t.shape)} {t.dtype}")
+    if rotary is None:
+        rot, inter, amplitude, turns = 0, 0, 1.0, 0
+    else:
+        rot, inter, amplitude = rotary.dim, rotary.interleaved, rotary.amplitude
+        turns = _flat(rotary.turns, torch.int64, rot // 2, "rotary.turns", dev)
+    a = _pack_rotate(n_req, slots, heads, kv, dim, rot, inter, eps, amplitude, qp, kp, qr, qh, kr, kh,
                      0 if q_weight is None else _flat(q_weight, bf16, dim, "q_weight", dev),
-                     0 if k_weight is None else _flat(k_weight, bf16, dim, "k_weight", dev),
-                     0 if rotary is None else _flat(rotary.turns, torch.int64, rotary.dim // 2, "rotary.turns", dev),
+                     0 if k_weight is None else _flat(k_weight, bf16, dim, "k_weight", dev), turns,
                      0 if positions is None else _flat(positions, i32, rows, "positions", dev),
                      0 if base is None else _flat(base, i32, n_req, "base", dev), qop, kop, qor, qoh, kor, koh)
     raw = kvcache._stream(stream, dev)
@@ -237,35 +254,51 @@ def token_logprobs(logits, tokens=None, *, top=0, temperature=1.0, out=None, sta
     import torch
     lib = _library()
     dev = _on_device(logits, "logits")
-    if logits.dim() < 1:
+    i32, f32, shape, at = torch.int32, torch.float32, logits.shape, logits.device
+    if not shape:
         raise ValueError("logits: expected [..., vocab]")
-    vocab, lead = logits.shape[-1], tuple(logits.shape[:-1])
-    lp, rows, ls = _rows(logits, vocab, (torch.float32, torch.bfloat16), "logits", dev)
-    n = 0
+    if top < 0:
+        raise ValueError(f"top: {top} is negative")
+    vocab, lead = shape[-1], shape[:-1]
+    lp, rows, ls = _rows(logits, vocab, (f32, torch.bfloat16), "logits", dev)
+    n = tp = 0
     if tokens is not None:
-        if tuple(tokens.shape[:len(lead)]) != lead or tokens.dim() - len(lead) not in (0, 1):
-            raise ValueError(f"tokens: expected {lead} or {(*lead, 'n')}, got {tuple(tokens.shape)}")
-        n = tokens.shape[-1] if tokens.dim() > len(lead) else 1
-    i32, f32 = torch.int32, torch.float32
-    want = {"lse": (lead, f32), "entropy": (lead, f32)}
-    if tokens is not None:
-        want["logp"] = (tuple(tokens.shape), f32)
-    if top:
-        want["top_tok"], want["top_logp"] = ((*lead, top), i32), ((*lead, top), f32)
-    found = {}
+        asked = tokens.shape
+        if asked == lead:
+            n = 1
+        elif len(asked) == len(shape) and asked[:-1] == lead:
+            n = asked[-1]
+        else:
+            raise ValueError(f"tokens: expected {tuple(lead)} or {(*lead, 'n')}, got {tuple(asked)}")
+        tp = _flat(tokens, i32, rows * n, "tokens", dev)
+    best = (*lead, top)
     with _allocating(stream):
-        for name, (shape, dtype) in want.items():
-            t = None if out is None else out.get(name)
-            if t is None:
-                t = torch.empty(shape, dtype=dtype, device=logits.device)
-            elif tuple(t.shape) != shape:
-                raise ValueError(f"out[{name!r}]: expected {shape}, got {tuple(t.shape)}")
-            found[name] = t
-    at = {name: _flat(t, want[name][1], rows * (n if name == "logp" else top if name.startswith("top") else 1), name, dev)
-          for name, t in found.items()}
-    a = _pack_logprobs(rows, vocab, n, top, logits.dtype is torch.bfloat16, temperature, lp, ls,
-                       0 if tokens is None else _flat(tokens, i32, rows * n, "tokens", dev), at.get("logp", 0), at["lse"],
-                       at["entropy"], at.get("top_tok", 0), at.get("top_logp", 0), _status(status, dev))
+        if out is None:
+            empty = torch.empty
+            lse, entropy = empty(lead, dtype=f32, device=at), empty(lead, dtype=f32, device=at)
+            found = {"lse": lse, "entropy": entropy}
+            pointers = [0, lse.data_ptr(), entropy.data_ptr(), 0, 0]
+            if tokens is not None:
+                found["logp"] = logp = empty(asked, dtype=f32, device=at)
+                pointers[0] = logp.data_ptr()
+            if top:
+                found["top_tok"], found["top_logp"] = ids, values = empty(best, dtype=i32, device=at), empty(best, dtype=f32, device=at)
+                pointers[3:] = ids.data_ptr(), values.data_ptr()
+        else:
+            found, pointers = {}, []
+            for name, size, dtype in (("logp", asked if tokens is not None else None, f32), ("lse", lead, f32), ("entropy", lead, f32),
+                                      ("top_tok", best if top else None, i32), ("top_logp", best if top else None, f32)):
+                if size is None:
+                    pointers.append(0)
+                    continue
+                t = out.get(name)
+                if t is None:
+                    t = torch.empty(size, dtype=dtype, device=at)
+                elif tuple(t.shape) != tuple(size):
+                    raise ValueError(f"out[{name!r}]: expected {tuple(size)}, got {tuple(t.shape)}")
+                found[name] = t
+                pointers.append(_flat(t, dtype, t.numel(), name, dev))
+    a = _pack_logprobs(rows, vocab, n, top, logits.dtype is not f32, temperature, lp, ls, tp, *pointers, _status(status, dev))
     raw = kvcache._stream(stream, dev)
     if rows:
         err = lib.dt_token_logprobs(a, raw)

@@ -12,6 +12,11 @@
 // sums, fp32 in shared memory, are added over distributed shared memory in the order of ranks, each CTA finishing a
 // part of the tile.  Tensor memory is given back before the cluster's barrier: a CTA that holds some waits for no other, so
 // that kernels side by side on an SM cannot wait in a circle.
+//
+// Outputs in 32 bits: the tensor core cuts what it adds to an accumulator, and hundreds of additions of 16 channels lean to
+// one side (2560 channels: 3e-6 of the result, six times what sums in fp32 are off by).  So an accumulator takes 512
+// channels, and these parts are added in fp32, rounded: in shared memory by k_stream's epilogue, from accumulators
+// beside each other by k_few.  Outputs in bf16 (half a step is 4e-3) have one accumulator over all channels.
 #include "linear.cuh"
 #include "cluster.cuh"
 #include "kv_flash.cuh"
@@ -110,6 +115,7 @@ __global__ void __launch_bounds__(kFewThreads)
   } else if (warp == 1) {
     const uint32_t idesc = idesc_bf16_f32(128, p.bn);
     uint32_t stage = 0, phase = 0;
+    int segment = 0, in_segment = 0;
     bool there = false;
     for (int ks = ks0; ks < ks1; ++ks) {
       ok = there || warp_wait(&full[stage], phase);
@@ -121,9 +127,10 @@ __global__ void __launch_bounds__(kFewThreads)
       if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
       const bool next = mbar_test(&full[stage], phase);  // (asked before the products that stand in its way)
       if (elect_one()) {
-        step_products<SIDES>(tmem, a, b, idesc, p, kTileBytes, ks != ks0);
+        step_products<SIDES>(tmem + segment * (SIDES * p.bn), a, b, idesc, p, kTileBytes, in_segment != 0);
         tc_commit(used);
       }
+      if (++in_segment == p.segment_steps) in_segment = 0, ++segment;
       there = __all_sync(0xFFFFFFFFu, next);
     }
     if (elect_one()) tc_commit(ok ? done : drained);
@@ -141,8 +148,15 @@ __global__ void __launch_bounds__(kFewThreads)
     const int quarter = warp & 3;
     for (int x = warp >> 2; x < SIDES * p.bn / 16; x += 2) {
       const int side = x / (p.bn / 16), c0 = (x - side * (p.bn / 16)) * 16;
+      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + side * p.bn + c0;
       uint32_t v[16];
-      tmem_ld16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + side * p.bn + c0, v);
+      tmem_ld16(from, v);
+      for (int i = p.segment_steps; i < ks1 - ks0; i += p.segment_steps) {
+        uint32_t w[16];
+        tmem_ld16(from + i / p.segment_steps * (SIDES * p.bn), w);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
+      }
 #pragma unroll
       for (int j = 0; j < 16; ++j) sums[((c0 + j) * SIDES + side) * 128 + quarter * 32 + lane] = __uint_as_float(v[j]);
     }
@@ -185,11 +199,11 @@ __global__ void __launch_bounds__(kFewThreads)
   if (p.split > 1) cluster_barrier();  // (no CTA leaves while its sums are read)
 }
 
-constexpr int kStreamThreads = 384, kStreamWarps = 8, kStreamTokens = 32;  // epilogue warps, and tokens that they write together
+constexpr int kStreamThreads = 384, kStreamWarps = 8;  // (epilogue warps)
 
-// Shared memory: the ring of stages, 32 tokens' sums, the barriers.
+// Shared memory: the ring of stages, the sums of sum_tokens tokens, the barriers.
 DT_HOST_DEVICE_INLINE uint32_t stream_sums(const LinearParams& p) { return p.stages * p.stage_bytes; }
-DT_HOST_DEVICE_INLINE uint32_t stream_bars(const LinearParams& p, int sides) { return stream_sums(p) + kStreamTokens * sides * 512u; }
+DT_HOST_DEVICE_INLINE uint32_t stream_bars(const LinearParams& p, int sides) { return stream_sums(p) + p.sum_tokens * sides * 512u; }
 
 template <int SIDES>
 __global__ void __launch_bounds__(kStreamThreads, 1)
@@ -228,7 +242,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   bool ok = true;
 
   if (warp == 0) {
-    const uint64_t stream = l2_policy_evict_first(), keep = l2_policy_evict_last();
+    const uint64_t keep = l2_policy_evict_last(), stream = p.m_tiles == 1 ? l2_policy_evict_first() : keep;
     uint32_t stage = 0, phase = 0;
     for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
       const int n0 = tile / p.m_tiles * p.tile_outs, t0 = tile % p.m_tiles * p.bn;
@@ -250,31 +264,32 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     // (rows of the product behind the tile's rows of weight come from whatever follows them, and go nowhere)
     const uint32_t idesc = idesc_bf16_f32(128, p.bn);
     uint32_t stage = 0, phase = 0;
-    int local = 0;
+    int local = 0;  // segments so far
     bool there = false;
-    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++local) {
-      const int acc = local & 1;
-      ok = warp_wait(&tempty[acc], (local >> 1 & 1) ^ 1u);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem + acc * acc_cols;
-      for (int ks = 0; ks < p.k_steps; ++ks) {
-        ok = there || warp_wait(&full[stage], phase);
+    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x)
+      for (int ks0 = 0; ks0 < p.k_steps && ok; ks0 += p.segment_steps, ++local) {
+        const int acc = local & 1, ks1 = min(p.k_steps, ks0 + p.segment_steps);
+        ok = warp_wait(&tempty[acc], (local >> 1 & 1) ^ 1u);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t at = smem_u32(smem + stage * p.stage_bytes);
-        const uint64_t a = sdesc_k_sw128(at), b = sdesc_k_sw128(at + SIDES * side_bytes);
-        uint64_t* used = &empty[stage];
-        if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
-        const bool next = mbar_test(&full[stage], phase);  // (asked before the products that stand in its way)
-        if (elect_one()) {
-          step_products<SIDES>(d, a, b, idesc, p, tile_bytes, ks != 0);
-          tc_commit(used);
-          if (ks + 1 == p.k_steps) tc_commit(&tfull[acc]);
+        const uint32_t d = tmem + acc * acc_cols;
+        for (int ks = ks0; ks < ks1; ++ks) {
+          ok = there || warp_wait(&full[stage], phase);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t at = smem_u32(smem + stage * p.stage_bytes);
+          const uint64_t a = sdesc_k_sw128(at), b = sdesc_k_sw128(at + SIDES * side_bytes);
+          uint64_t* used = &empty[stage];
+          if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
+          const bool next = mbar_test(&full[stage], phase);  // (asked before the products that stand in its way)
+          if (elect_one()) {
+            step_products<SIDES>(d, a, b, idesc, p, tile_bytes, ks != ks0);
+            tc_commit(used);
+            if (ks + 1 == ks1) tc_commit(&tfull[acc]);
+          }
+          there = __all_sync(0xFFFFFFFFu, next);
         }
-        there = __all_sync(0xFFFFFFFFu, next);
       }
-    }
     if (!ok) {  // (no product may outlive its operands and tensor memory)
       if (elect_one()) tc_commit(drained);
       __syncwarp();
@@ -283,40 +298,60 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   } else if (warp >= 4) {
     const int quarter = warp & 3, half = (warp - 4) >> 2, et = tid - 128;
     auto together = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
-    static_assert(kStreamWarps * 32 == 256 && kStreamTokens == 32, "");
+    static_assert(kStreamWarps * 32 == 256, "");
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    // 16 tokens from column c of an accumulator on, to or onto the sums from token `at` on
+    auto take = [&](uint32_t acc, int c, int at, bool onto) {
+#pragma unroll
+      for (int s = 0; s < SIDES; ++s) {
+        uint32_t v[16];
+        tmem_ld16(tmem + lanes + acc * acc_cols + s * p.bn + c, v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float& sum = sums[((at + j) * SIDES + s) * 128 + quarter * 32 + lane];
+          sum = onto ? sum + __uint_as_float(v[j]) : __uint_as_float(v[j]);
+        }
+      }
+    };
+    auto give_back = [&](uint32_t acc) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[acc]);
+    };
     int local = 0;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++local) {
-      const int acc = local & 1;
-      // (a wait that gave up in one warp: the others would wait for it at the barrier, so it goes on, and writes nothing)
-      ok = ok && warp_wait(&tfull[acc], local >> 1 & 1);
-      tc_fence_after();
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
       const int n0 = tile / p.m_tiles * p.tile_outs, t0 = tile % p.m_tiles * p.bn, tokens = min(p.bn, p.rows - t0);
-      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * acc_cols;
-      for (int c0 = 0; c0 < tokens; c0 += kStreamTokens) {
-        const int c = c0 + 16 * half;  // 16 tokens of this warp's rows
-        if (c < p.bn && ok) {
-#pragma unroll
-          for (int s = 0; s < SIDES; ++s) {
-            uint32_t v[16];
-            tmem_ld16(from + s * p.bn + c, v);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) sums[((16 * half + j) * SIDES + s) * 128 + quarter * 32 + lane] = __uint_as_float(v[j]);
-          }
-        }
-        if (c0 + kStreamTokens >= tokens) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tempty[acc]);
-        }
-        together();
-        const int units = min(kStreamTokens, tokens - c0) * 32;
-        for (int u = et; u < units; u += 256) {
+      auto write = [&](int c0, int count) {  // tokens c0 .. of the tile, whose sums are complete
+        for (int u = et; u < count * 32; u += 256) {
           const int t = u >> 5, f = (u & 31) * 4;
           if (f >= p.tile_outs || n0 + f >= p.outer || !ok) continue;
           const float4* at = reinterpret_cast<const float4*>(sums + t * SIDES * 128 + f);
           finish4<SIDES>(p, t0 + c0 + t, n0 + f, at[(SIDES - 1) * 32], at[0]);
         }
+      };
+      // (a wait that gave up in one warp: the others would wait for it at the barrier, so it goes on, and writes nothing)
+      if (p.segment_steps < p.k_steps) {  // all tokens' sums, part by part
+        for (int ks = 0; ks < p.k_steps; ks += p.segment_steps, ++local) {
+          ok = ok && warp_wait(&tfull[local & 1], local >> 1 & 1);
+          tc_fence_after();
+          for (int c = 16 * half; c < p.bn && ok; c += 32) take(local & 1, c, c, ks > 0);
+          give_back(local & 1);
+        }
         together();
+        write(0, tokens);
+        together();
+      } else {  // 32 tokens after 32
+        const int acc = local & 1;
+        ok = ok && warp_wait(&tfull[acc], local >> 1 & 1);
+        tc_fence_after();
+        for (int c0 = 0; c0 < tokens; c0 += 32) {
+          if (c0 + 16 * half < p.bn && ok) take(acc, c0 + 16 * half, 16 * half, false);
+          if (c0 + 32 >= tokens) give_back(acc);
+          together();
+          write(c0, min(32, tokens - c0));
+          together();
+        }
+        ++local;
       }
     }
   }
@@ -359,9 +394,11 @@ cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& g, const CUtenso
   return cudaLaunchKernelEx(&cfg, k_few<SIDES>, w, g, x, p);
 }
 
-// Few tokens: in one tile, padded to 16.
+constexpr int kSegmentBlocks = 8;  // of 64 channels, for outputs in 32 bits
+
+// Tokens in tiles, padded to 16: of 256 at most, 128 where their sums stay in shared memory.
 void plan_tokens(LinearParams& p, int sides) {
-  const int most = 256 / sides;
+  const int most = (p.out_fp32 ? 128 : 256) / sides;
   p.m_tiles = (p.rows + most - 1) / most;
   p.bn = ((p.rows + p.m_tiles - 1) / p.m_tiles + 15) & ~15;
   p.m_tiles = (p.rows + p.bn - 1) / p.bn;
@@ -375,6 +412,7 @@ void steps_of(LinearParams& p, int sides, uint32_t room) {
   p.stage_bytes = p.per * block;
   p.stages = static_cast<int>(room / p.stage_bytes);
   if (p.stages > 12) p.stages = 12;
+  p.segment_steps = p.out_fp32 ? kSegmentBlocks / p.per : p.k_steps;
 }
 int tmem_columns(int n) {
   int cols = 32;
@@ -382,10 +420,8 @@ int tmem_columns(int n) {
   return cols;
 }
 
-// Persistent CTAs: rows of weight for tiles that divide evenly over them.  False where a cluster's CTAs serve a tile better.
-bool plan_stream(LinearParams& p, int sides) {
-  const int64_t tiles = static_cast<int64_t>((p.outer + 127) / 128) * p.m_tiles;
-  if (tiles < kSms / 2 || tiles > (1 << 29)) return false;
+// Persistent CTAs: rows of weight for tiles that divide evenly over them.
+void plan_stream(LinearParams& p, int sides, int64_t tiles) {
   const int64_t rounds = (tiles + kSms - 1) / kSms;
   const int64_t per = (static_cast<int64_t>(p.outer) * p.m_tiles + rounds * kSms - 1) / (rounds * kSms);
   p.tile_outs = static_cast<int>((per + 7) / 8 * 8);
@@ -394,8 +430,8 @@ bool plan_stream(LinearParams& p, int sides) {
   while (p.tile_outs < 128 && static_cast<int64_t>(n_tiles()) * p.m_tiles > rounds * kSms) p.tile_outs += 8;
   p.n_tiles = n_tiles();
   p.tmem_cols = tmem_columns(2 * sides * p.bn);
-  steps_of(p, sides, 224u * 1024 - 1024 - kStreamTokens * sides * 512);
-  return true;
+  p.sum_tokens = p.out_fp32 ? (p.bn + 31) & ~31 : 32;
+  steps_of(p, sides, 224u * 1024 - 1024 - p.sum_tokens * sides * 512);
 }
 
 // Clusters of as many CTAs as leave all of them beside each other: with one CTA an SM 128 or so are (36 clusters of 4: one
@@ -403,15 +439,17 @@ bool plan_stream(LinearParams& p, int sides) {
 // one would leave clusters of two.  us with two and with one an SM: 4 tokens, 2560 to 6144 9.4 (4 CTAs a cluster) and 10.0 (2);
 // 16, 4096 to 2560 8.5 (8) and 8.7 (4); 65, 4096 to 2560 10.6 and 9.9 (6); 65, 2560 to 6144 11.8 (5) and 12.3 (2); 128, 4096 to
 // 4096 14.8 and 13.1 (4).
-void plan_few(LinearParams& p, int sides) {
+// False where there are too few accumulators for outputs in 32 bits.
+bool plan_few(LinearParams& p, int sides, int64_t tiles) {
   p.tile_outs = 128;
   p.n_tiles = (p.outer + 127) / 128;
-  p.tmem_cols = tmem_columns(sides * p.bn);
-  const int64_t tiles = static_cast<int64_t>(p.n_tiles) * p.m_tiles;
   const bool two = sides * p.bn <= 64 || (sides * p.bn <= 128 && 3 * tiles > 128);
   steps_of(p, sides, two ? 110u * 1024 : 220u * 1024);
   p.split = 1;
   while (p.split < kMostSplit && tiles * (p.split + 1) <= (two ? 256 : 128) && p.k_steps * p.per >= 4 * (p.split + 1)) ++p.split;
+  const int steps = (p.k_steps + p.split - 1) / p.split, segments = (steps + p.segment_steps - 1) / p.segment_steps;
+  p.tmem_cols = tmem_columns(segments * sides * p.bn);
+  return segments * sides * p.bn <= (two ? 256 : 512);
 }
 
 // Many tokens: the tile's columns so that the pairs' rounds of tiles cost least, a tile as much as its columns and 32 more.
@@ -475,7 +513,7 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (p.rows <= kTokensMost) return kv_launched(who, launch_linear_token(a, p, st));
   const int sides = a.gate ? 2 : 1;
-  const bool many = p.rows > 256;
+  const bool many = p.rows > 256 && !p.out_fp32;
   const uintptr_t res = reinterpret_cast<uintptr_t>(a.residual);
   const int64_t at_once = many ? 16 / static_cast<int64_t>(bytes) : 4;  // outputs written together
   p.wide = out % (at_once * bytes) == 0 && (a.rows == 1 || a.out_row_stride % at_once == 0) &&
@@ -486,8 +524,11 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
     if (static_cast<int64_t>(p.m_tiles) * p.n_tiles > (1 << 30)) return kv_fail(DT_ERR_SHAPE, "%s: more than 2^30 tiles", who);
   } else {
     plan_tokens(p, sides);
-    stream_tiles = plan_stream(p, sides);
-    if (!stream_tiles) plan_few(p, sides);
+    const int64_t tiles = static_cast<int64_t>((a.outer + 127) / 128) * p.m_tiles;
+    if (tiles > (1 << 29)) return kv_fail(DT_ERR_SHAPE, "%s: more than 2^29 tiles", who);
+    // (clusters where tiles leave half of the SMs without one)
+    stream_tiles = tiles >= kSms / 2 || !plan_few(p, sides, tiles);
+    if (stream_tiles) plan_stream(p, sides, tiles);
   }
   const int w_rows = many ? p.bn / 2 : p.tile_outs;
   auto map = [&](CUtensorMap* m, const void* d, int64_t stride, int64_t rows, int box) {

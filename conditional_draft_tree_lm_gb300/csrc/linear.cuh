@@ -13,6 +13,8 @@ struct LinearParams {
   int64_t residual_stride, out_stride;
   int rows, outer, inner, k_blocks;  // k_blocks: of 64
   int per, k_steps;           // blocks of a step, steps
+  int segment_steps;          // steps that one accumulator adds
+  int sum_tokens;             // tokens whose sums stand in shared memory
   int activation, out_fp32;
   int bn, stages, tmem_cols;        // bn: few rows: tokens of a tile; many: its columns (with a gate, two for an output)
   int split;                  // CTAs of a cluster

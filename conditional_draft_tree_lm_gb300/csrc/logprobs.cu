@@ -25,13 +25,13 @@
 namespace dt {
 namespace {
 
-constexpr int kLogpThreads = 256, kLogpWarps = kLogpThreads / 32;
 constexpr int kVecs = 4;  // pieces of 16 bytes of a thread's round
 constexpr int kStretches = 16;
 constexpr int kMaxTop = 64, kMaxSplit = 16;
+constexpr int kShortRow = 8192;  // logits
 // Rounds in shared memory, and its bytes: with the stretches' largest in it, two rounds leave room for four CTAs an SM.
 constexpr int rounds_ahead(bool best) { return best ? 2 : 3; }
-constexpr int logp_smem(bool best) { return rounds_ahead(best) * kVecs * kLogpThreads * 16 + (best ? kStretches * kLogpThreads * 4 : 0); }
+constexpr int logp_smem(bool best, int threads) { return rounds_ahead(best) * kVecs * threads * 16 + (best ? kStretches * threads * 4 : 0); }
 constexpr float kLag = 8.0f;
 
 struct LogpParams {
@@ -71,11 +71,13 @@ DT_DEVINL void copy16(void* to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
 
-// PER: keys of a lane when a warp's list is full, 32 PER in all (0: no best tokens are asked for).
-template <bool BF16, int PER>
-__global__ void __launch_bounds__(kLogpThreads, 4) k_logp(const LogpParams p) {
+// PER: keys of a lane when a warp's list is full, 32 PER in all (0: no best tokens are asked for).  Rows that a CTA reads
+// alone and that are short take 64 threads, whose own costs count there (333 to 8192 logits; see the choice below).
+template <bool BF16, int PER, int kLogpThreads>
+__global__ void __launch_bounds__(kLogpThreads, 1024 / kLogpThreads) k_logp(const LogpParams p) {
+  constexpr int kLogpWarps = kLogpThreads / 32, kMostSplit = kLogpThreads == 64 ? 1 : kMaxSplit;
   constexpr int kElems = BF16 ? 8 : 4, kBytes = BF16 ? 2 : 4, kCap = 32 * (PER ? PER : 1);
-  constexpr int kKeys = kLogpWarps * kCap > kMaxSplit * kMaxTop ? kLogpWarps * kCap : kMaxSplit * kMaxTop;
+  constexpr int kKeys = kLogpWarps * kCap > kMostSplit * kMaxTop ? kLogpWarps * kCap : kMostSplit * kMaxTop;
   constexpr int kAhead = rounds_ahead(PER > 0), kRingBytes = kAhead * kVecs * kLogpThreads * 16;
   // the ring of rounds; behind the stream, the warps' lists, what is ranked of them and of the CTAs, and the stretches to read
   // again; then 64 bytes of each thread, its stretches' largest
@@ -210,6 +212,7 @@ __global__ void __launch_bounds__(kLogpThreads, 4) k_logp(const LogpParams p) {
     if (lane == 0) s_bound[warp] = q;
     if (tid == 0) s_n[0] = s_n[1] = 0;
     if (tid < kMaxTop) s_best[tid] = 0;
+    static_assert(kMaxTop <= 64, "");
   }
   __syncthreads();  // (and the ring has been read)
   if (warp == 0) {
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(kLogpThreads, 4) k_logp(const LogpParams p) {
     int n_again = 0;
     uint32_t reach = 0;
 #pragma unroll
-    for (int i = 0; i < kStretches; ++i) reach |= (stretch_max(i) >= least ? 1u : 0u) << i;
+    for (int i = 0; i < kStretches; ++i) reach |= (stretch_max(i) >= least && stretch_max(i) > -INFINITY ? 1u : 0u) << i;
     reach &= (1u << stretches) - 1u;
     while (__any_sync(0xFFFFFFFFu, reach != 0)) {
       const uint32_t who = __ballot_sync(0xFFFFFFFFu, reach != 0);
@@ -277,28 +280,53 @@ __global__ void __launch_bounds__(kLogpThreads, 4) k_logp(const LogpParams p) {
       n_again += __popc(who);
     }
     __syncwarp();
-    for (int from = lane; from - lane < stretch * kVecs; from += 32)
-      for (int s = 0; s < n_again; s += 4) {
+    // (a list that has been cut has raised the bound: of equal logits later stretches have nothing then)
+    const float* largest_of = reinterpret_cast<const float*>(ring + kRingBytes) + warp * 512;
+    auto value_of = [](uint64_t key) { return key ? key_f32(static_cast<uint32_t>(key >> 32)) : -INFINITY; };
+    for (int s = 0; s < n_again; s += 4) {
+      int begin[4];  // the stretch's first piece, -1 where it cannot reach the bound
+      bool any = false;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int which = s + u < n_again ? again[s + u] : -1, i = which >> 5, owner = which & 31;
+        begin[u] = -1;
+        if (which < 0) continue;
+        const int at = warp * 32 + owner + i * stretch * kRound;
+        if (rank_key(largest_of[(i >> 2) * 128 + owner * 4 + (i & 3)] + 0.0f, static_cast<uint32_t>(first + at * kElems)) > tau) begin[u] = at, any = true;
+      }
+      if (!any) continue;
+      for (int from = lane; from - lane < stretch * kVecs; from += 32) {
         int here[4];
         uint4 piece[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int which = s + u < n_again ? again[s + u] : 0;
-          here[u] = warp * 32 + (which & 31) + ((which >> 5) * stretch * kVecs + from) * kLogpThreads;
-          if (s + u >= n_again || from >= stretch * kVecs || here[u] >= vecs) here[u] = -1;
+          here[u] = begin[u] + from * kLogpThreads;
+          if (begin[u] < 0 || from >= stretch * kVecs || here[u] >= vecs) here[u] = -1;
           piece[u] = here[u] < 0 ? make_uint4(0, 0, 0, 0) : __ldg(vec + here[u]);
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          if (s + u >= n_again) break;
+          if (begin[u] < 0) continue;
+          const float now = value_of(tau);
           float v[kElems];
           unpack(piece[u], v);
           uint32_t mask = 0;
 #pragma unroll
-          for (int i = 0; i < kElems; ++i) mask |= (v[i] >= least ? 1u : 0u) << i;
+          for (int i = 0; i < kElems; ++i) mask |= (v[i] >= now && v[i] > -INFINITY ? 1u : 0u) << i;
           take(v, here[u] < 0 ? 0u : mask, first + here[u] * kElems);
         }
       }
+    }
+    // where a mask leaves fewer logits than are asked for: the first of -inf, piece after piece
+    for (int at = warp * 32; n < top && tau == 0 && at < vecs; at += kLogpThreads) {
+      const bool there = at + lane < vecs;
+      float v[kElems];
+      unpack(there ? __ldg(vec + at + lane) : make_uint4(0, 0, 0, 0), v);
+      uint32_t mask = 0;
+#pragma unroll
+      for (int i = 0; i < kElems; ++i) mask |= (v[i] == -INFINITY ? 1u : 0u) << i;
+      take(v, there ? mask : 0u, first + (at + lane) * kElems);
+    }
     if (warp == 0) {
       float v[kElems] = {edge[0]};
       take(v, lane < head && edge[0] >= least ? 1u : 0u, lo + lane);
@@ -316,7 +344,7 @@ __global__ void __launch_bounds__(kLogpThreads, 4) k_logp(const LogpParams p) {
   __syncthreads();
   const uint64_t* best = s_best;
   Sums all = s_sums;
-  if (p.split > 1) {
+  if (kMostSplit > 1 && p.split > 1) {
     cluster_barrier();
     if (part == 0) {
       if (warp == 0) {
@@ -384,18 +412,19 @@ __global__ void __launch_bounds__(kLogpThreads, 4) k_logp(const LogpParams p) {
     }
 }
 
-template <bool BF16, int PER>
+template <bool BF16, int PER, int THREADS>
 cudaError_t launch(const LogpParams& p, cudaStream_t st) {
+  const auto kernel = k_logp<BF16, PER, THREADS>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = once_a_device(done, [] {
-    const cudaError_t e = cudaFuncSetAttribute(k_logp<BF16, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, logp_smem(PER > 0));
-    return e == cudaSuccess ? cudaFuncSetAttribute(k_logp<BF16, PER>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : e;
+  cudaError_t e = once_a_device(done, [&] {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, logp_smem(PER > 0, THREADS));
+    return e == cudaSuccess && THREADS > 64 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : e;
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.a.rows * p.split));
-  cfg.blockDim = dim3(kLogpThreads);
-  cfg.dynamicSmemBytes = logp_smem(PER > 0);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = logp_smem(PER > 0, THREADS);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -403,7 +432,11 @@ cudaError_t launch(const LogpParams& p, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_logp<BF16, PER>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+template <bool BF16, int PER>
+cudaError_t launch(const LogpParams& p, cudaStream_t st) {
+  return p.split == 1 && p.a.vocab <= kShortRow ? launch<BF16, PER, 64>(p, st) : launch<BF16, PER, 256>(p, st);
 }
 
 }  // namespace

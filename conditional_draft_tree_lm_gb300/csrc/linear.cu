@@ -27,24 +27,30 @@ namespace {
 constexpr int kFewThreads = 256, kMostSplit = 8;
 constexpr uint32_t kTileBytes = 128 * 128;  // 128 rows of 64 bf16
 
-// A step of a stage: `per` blocks of 64 of the inner dimension (one copy: the map has them as a third dimension, where they
+// A step of a stage: PER blocks of 64 of the inner dimension (one copy: the map has them as a third dimension, where they
 // are whole), rows from `row` on, block after block.
-DT_DEVINL void load_step(void* to, const CUtensorMap& map, uint64_t* bar, int per, int step, int row, uint64_t policy) {
+template <int PER>
+DT_DEVINL void load_step(void* to, const CUtensorMap& map, uint64_t* bar, int step, int row, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(
           smem_u32(to)),
-      "l"(reinterpret_cast<uint64_t>(&map)), "r"(smem_u32(bar)), "r"(per == 1 ? step * 64 : 0), "r"(row), "r"(per == 1 ? 0 : step * per), "l"(policy)
+      "l"(reinterpret_cast<uint64_t>(&map)), "r"(smem_u32(bar)), "r"(PER == 1 ? step * 64 : 0), "r"(row), "r"(PER == 1 ? 0 : step * PER), "l"(policy)
       : "memory");
 }
-// Its products; tile: bytes of a block of one side's rows.
-template <int SIDES>
+// Its products (one block or two, straight on); tile: bytes of a block of one side's rows.
+template <int SIDES, int PER>
 DT_DEVINL void step_products(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, const LinearParams& p, uint32_t tile, bool more) {
-  for (int j = 0; j < p.per; ++j) {
+  const uint64_t side = PER * tile >> 4;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int s = 0; s < SIDES; ++s) tc_mma_bf16(d + s * p.bn, a + s * side + (k * 32 >> 4), b + (k * 32 >> 4), idesc, more || k != 0);
+  if (PER == 2) {
+    const uint64_t a1 = a + (tile >> 4), b1 = b + (p.bn * 128 >> 4);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int s = 0; s < SIDES; ++s)
-        tc_mma_bf16(d + s * p.bn, a + (((s * p.per + j) * tile + k * 32) >> 4), b + ((j * p.bn * 128 + k * 32) >> 4), idesc, more || j != 0 || k != 0);
+      for (int s = 0; s < SIDES; ++s) tc_mma_bf16(d + s * p.bn, a1 + s * side + (k * 32 >> 4), b1 + (k * 32 >> 4), idesc, 1u);
   }
 }
 
@@ -55,7 +61,7 @@ DT_HOST_DEVICE_INLINE uint32_t few_bars(const LinearParams& p, int sides) {
   return ring > sums ? ring : sums;
 }
 
-template <int SIDES>
+template <int SIDES, int PER>
 __global__ void __launch_bounds__(kFewThreads)
     k_few(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_g,
           const __grid_constant__ CUtensorMap tm_x, const LinearParams p) {
@@ -73,13 +79,13 @@ __global__ void __launch_bounds__(kFewThreads)
   const int ks0 = static_cast<int>(static_cast<int64_t>(p.k_steps) * rank / p.split);
   const int ks1 = static_cast<int>(static_cast<int64_t>(p.k_steps) * (rank + 1) / p.split);
   const uint64_t stream = l2_policy_evict_first(), keep = l2_policy_evict_last();
-  const uint32_t side_bytes = p.per * kTileBytes;
+  const uint32_t side_bytes = PER * kTileBytes;
   auto load = [&](int ks, uint32_t stage) {
     uint8_t* at = smem + stage * p.stage_bytes;
     mbar_arrive_expect_tx(&full[stage], p.stage_bytes);
-    if (SIDES == 2) load_step(at, tm_g, &full[stage], p.per, ks, n0, stream);
-    load_step(at + (SIDES - 1) * side_bytes, tm_w, &full[stage], p.per, ks, n0, stream);
-    load_step(at + SIDES * side_bytes, tm_x, &full[stage], p.per, ks, t0, keep);
+    if (SIDES == 2) load_step<PER>(at, tm_g, &full[stage], ks, n0, stream);
+    load_step<PER>(at + (SIDES - 1) * side_bytes, tm_w, &full[stage], ks, n0, stream);
+    load_step<PER>(at + SIDES * side_bytes, tm_x, &full[stage], ks, t0, keep);
   };
   // the first loads are under way before tensor memory is asked for
   const int ahead = min(p.stages, ks1 - ks0);
@@ -127,7 +133,7 @@ __global__ void __launch_bounds__(kFewThreads)
       if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
       const bool next = mbar_test(&full[stage], phase);  // (asked before the products that stand in its way)
       if (elect_one()) {
-        step_products<SIDES>(tmem + segment * (SIDES * p.bn), a, b, idesc, p, kTileBytes, in_segment != 0);
+        step_products<SIDES, PER>(tmem + segment * (SIDES * p.bn), a, b, idesc, p, kTileBytes, in_segment != 0);
         tc_commit(used);
       }
       if (++in_segment == p.segment_steps) in_segment = 0, ++segment;
@@ -205,7 +211,7 @@ constexpr int kStreamThreads = 384, kStreamWarps = 8;  // (epilogue warps)
 DT_HOST_DEVICE_INLINE uint32_t stream_sums(const LinearParams& p) { return p.stages * p.stage_bytes; }
 DT_HOST_DEVICE_INLINE uint32_t stream_bars(const LinearParams& p, int sides) { return stream_sums(p) + p.sum_tokens * sides * 512u; }
 
-template <int SIDES>
+template <int SIDES, int PER>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     k_stream(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_g,
              const __grid_constant__ CUtensorMap tm_x, const LinearParams p) {
@@ -221,7 +227,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tiles = p.n_tiles * p.m_tiles;  // (m_tiles: of tokens)
-  const uint32_t tile_bytes = p.tile_outs * 128u, side_bytes = p.per * tile_bytes, acc_cols = SIDES * p.bn;
+  const uint32_t tile_bytes = p.tile_outs * 128u, side_bytes = PER * tile_bytes, acc_cols = SIDES * p.bn;
   if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
@@ -252,9 +258,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         if (elect_one()) {
           uint8_t* at = smem + stage * p.stage_bytes;
           mbar_arrive_expect_tx(&full[stage], p.stage_bytes);
-          if (SIDES == 2) load_step(at, tm_g, &full[stage], p.per, ks, n0, stream);
-          load_step(at + (SIDES - 1) * side_bytes, tm_w, &full[stage], p.per, ks, n0, stream);
-          load_step(at + SIDES * side_bytes, tm_x, &full[stage], p.per, ks, t0, keep);
+          if (SIDES == 2) load_step<PER>(at, tm_g, &full[stage], ks, n0, stream);
+          load_step<PER>(at + (SIDES - 1) * side_bytes, tm_w, &full[stage], ks, n0, stream);
+          load_step<PER>(at + SIDES * side_bytes, tm_x, &full[stage], ks, t0, keep);
         }
         __syncwarp();
         if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
           const bool next = mbar_test(&full[stage], phase);  // (asked before the products that stand in its way)
           if (elect_one()) {
-            step_products<SIDES>(d, a, b, idesc, p, tile_bytes, ks != ks0);
+            step_products<SIDES, PER>(d, a, b, idesc, p, tile_bytes, ks != ks0);
             tc_commit(used);
             if (ks + 1 == ks1) tc_commit(&tfull[acc]);
           }
@@ -364,21 +370,25 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   }
 }
 
-template <int SIDES>
+template <int SIDES, int PER>
 cudaError_t launch_stream(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = once_a_device(done, [] { return cudaFuncSetAttribute(k_stream<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024); });
+  cudaError_t e = once_a_device(done, [] { return cudaFuncSetAttribute(k_stream<SIDES, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024); });
   if (e != cudaSuccess) return e;
   const uint32_t smem = 1024 + stream_bars(p, SIDES) + (2 * p.stages + 5) * 8 + 16;
-  k_stream<SIDES><<<min(p.n_tiles * p.m_tiles, kSms), kStreamThreads, smem, st>>>(w, g, x, p);
+  k_stream<SIDES, PER><<<min(p.n_tiles * p.m_tiles, kSms), kStreamThreads, smem, st>>>(w, g, x, p);
   return cudaGetLastError();
 }
+cudaError_t launch_stream(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, bool gate, cudaStream_t st) {
+  if (p.per == 2) return gate ? launch_stream<2, 2>(w, g, x, p, st) : launch_stream<1, 2>(w, g, x, p, st);
+  return gate ? launch_stream<2, 1>(w, g, x, p, st) : launch_stream<1, 1>(w, g, x, p, st);
+}
 
-template <int SIDES>
+template <int SIDES, int PER>
 cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, cudaStream_t st) {
   const uint32_t smem = 1024 + few_bars(p, SIDES) + (2 * p.stages + 2) * 8 + 16;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = once_a_device(done, [] { return cudaFuncSetAttribute(k_few<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024); });
+  cudaError_t e = once_a_device(done, [] { return cudaFuncSetAttribute(k_few<SIDES, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024); });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.n_tiles * p.split), static_cast<unsigned>(p.m_tiles));
@@ -391,7 +401,11 @@ cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& g, const CUtenso
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_few<SIDES>, w, g, x, p);
+  return cudaLaunchKernelEx(&cfg, k_few<SIDES, PER>, w, g, x, p);
+}
+cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, bool gate, cudaStream_t st) {
+  if (p.per == 2) return gate ? launch_few<2, 2>(w, g, x, p, st) : launch_few<1, 2>(w, g, x, p, st);
+  return gate ? launch_few<2, 1>(w, g, x, p, st) : launch_few<1, 1>(w, g, x, p, st);
 }
 
 constexpr int kSegmentBlocks = 8;  // of 64 channels, for outputs in 32 bits
@@ -454,7 +468,6 @@ bool plan_few(LinearParams& p, int sides, int64_t tiles) {
 
 // Many tokens: the tile's columns so that the pairs' rounds of tiles cost least, a tile as much as its columns and 32 more.
 void plan_many(LinearParams& p, int sides) {
-  p.per = 1;
   p.m_tiles = (p.rows + 255) / 256;
   int64_t least = INT64_MAX;
   for (int bn = 256; bn >= 64; bn -= 32 * sides) {
@@ -468,6 +481,12 @@ void plan_many(LinearParams& p, int sides) {
       p.n_tiles = (p.outer + outs - 1) / outs;
     }
   }
+  // a CTA's part of a step: 128 tokens and half of the columns
+  const uint32_t block = 16384 + p.bn * 64;
+  p.per = p.inner % 128 == 0 && p.bn <= 128 ? 2 : 1;  // (512 tokens, 4096 to 2560, 96 columns 17.3 us, by one block 18.2; 160 columns 20.2, by two 22.6)
+  p.k_steps = (p.k_blocks + p.per - 1) / p.per;
+  p.stage_bytes = p.per * block;
+  p.stages = static_cast<int>(kWideRing / p.stage_bytes);
 }
 
 }  // namespace
@@ -540,6 +559,5 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
       !map(&x, a.x, a.x_row_stride, a.rows, many ? 128 : p.bn))
     return kv_fail(DT_ERR_SHAPE, "%s: strides that a tensor map does not take (2^40 bytes and more)", who);
   if (many) return kv_launched(who, launch_linear_wide(w, g, x, p, sides == 2, st));
-  if (stream_tiles) return kv_launched(who, sides == 2 ? launch_stream<2>(w, g, x, p, st) : launch_stream<1>(w, g, x, p, st));
-  return kv_launched(who, sides == 2 ? launch_few<2>(w, g, x, p, st) : launch_few<1>(w, g, x, p, st));
+  return kv_launched(who, stream_tiles ? launch_stream(w, g, x, p, sides == 2, st) : launch_few(w, g, x, p, sides == 2, st));
 }

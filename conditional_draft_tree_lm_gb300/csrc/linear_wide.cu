@@ -17,10 +17,10 @@
 namespace dt {
 namespace {
 
-constexpr int kWideThreads = 384, kEpilogueWarps = 8, kWideStages = 6;
+constexpr int kWideThreads = 384, kEpilogueWarps = 8;
 constexpr uint32_t kHalf = 128 * 128;  // 128 rows of 64 bf16
-constexpr uint32_t kWideStage = 2 * kHalf, kStagingBytes = 4096;
-constexpr uint32_t kWideSmem = 1024 + kWideStages * kWideStage + kEpilogueWarps * kStagingBytes + 256;
+constexpr uint32_t kStagingBytes = 4096;
+constexpr uint32_t kWideSmem = 1024 + kWideRing + kEpilogueWarps * kStagingBytes + 512;
 static_assert(kWideSmem <= kSmemBytes, "");
 
 DT_DEVINL void tmem_alloc_pair(uint32_t* dst, uint32_t cols) {
@@ -42,12 +42,13 @@ DT_DEVINL void tc_commit_pair(uint64_t* bar) {
                "h"(static_cast<uint16_t>(3))
                : "memory");
 }
-// A box into this CTA's shared memory, counted on a barrier of either CTA (a cluster address).
-DT_DEVINL void tma_load_pair(void* dst, const void* tmap, uint32_t bar, int x, int y, uint64_t policy) {
+// A step's rows into this CTA's shared memory, counted on a barrier of either CTA (a cluster address).
+template <int PER>
+DT_DEVINL void tma_load_pair(void* dst, const void* tmap, uint32_t bar, int step, int row, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(0), "l"(policy)
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(PER == 1 ? step * 64 : 0), "r"(row), "r"(PER == 1 ? 0 : step * PER), "l"(policy)
       : "memory");
 }
 DT_DEVINL void peer_arrive(uint32_t bar) { asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory"); }
@@ -86,16 +87,16 @@ DT_DEVINL uint32_t piece_at(int row, int k) {
   return E == 2 ? row * 64 + ((k ^ (row >> 1 & 3)) << 4) : row * 128 + ((k ^ (row & 7)) << 4);
 }
 
-template <int SIDES>
+template <int SIDES, int PER>
 __global__ void __launch_bounds__(kWideThreads, 1)
     k_wide(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_g,
            const __grid_constant__ CUtensorMap tm_x, const LinearParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* staging = smem + kWideStages * kWideStage;
+  uint8_t* staging = smem + kWideRing;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpilogueWarps * kStagingBytes);
-  uint64_t* empty = full + kWideStages;
-  uint64_t* tfull = empty + kWideStages;
+  uint64_t* empty = full + p.stages;
+  uint64_t* tfull = empty + p.stages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drained = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int rank = static_cast<int>(cta_rank());
   const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1, tiles = p.m_tiles * p.n_tiles;
   if (tid == 0) {
-    for (int s = 0; s < kWideStages; ++s) {
+    for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -125,24 +126,23 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 
   if (warp == 0) {
     const uint64_t keep = l2_policy_evict_last();
-    const uint32_t bytes = 2 * (kHalf + p.bn * 64);  // of both CTAs
     uint32_t stage = 0, phase = 0;
     for (int tile = pair; tile < tiles && ok; tile += pairs) {
       const Place at = place(p, tile);
       const int t0 = at.m0 + rank * 128, n0 = SIDES == 2 ? at.n0 : at.n0 + rank * (p.bn / 2);
       const void* tm_b = SIDES == 2 && rank == 0 ? static_cast<const void*>(&tm_g) : static_cast<const void*>(&tm_w);
-      for (int kb = 0; kb < p.k_blocks; ++kb) {
+      for (int ks = 0; ks < p.k_steps; ++ks) {
         ok = pair_wait(&empty[stage], phase ^ 1u);
         if (!ok) break;
         if (elect_one()) {
-          uint8_t* to = smem + stage * kWideStage;
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
+          uint8_t* to = smem + stage * p.stage_bytes;
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * p.stage_bytes);  // (both CTAs')
           const uint32_t bar = peer_addr(&full[stage], 0);
-          tma_load_pair(to, &tm_x, bar, kb * 64, t0, keep);
-          tma_load_pair(to + kHalf, tm_b, bar, kb * 64, n0, keep);
+          tma_load_pair<PER>(to, &tm_x, bar, ks, t0, keep);
+          tma_load_pair<PER>(to + PER * kHalf, tm_b, bar, ks, n0, keep);
         }
         __syncwarp();
-        if (++stage == kWideStages) stage = 0, phase ^= 1u;
+        if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
       }
     }
   } else if (warp == 1 && rank == 0) {
@@ -156,20 +156,26 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + acc * 256;
-      for (int kb = 0; kb < p.k_blocks; ++kb) {
+      for (int ks = 0; ks < p.k_steps; ++ks) {
         ok = there || pair_wait(&full[stage], phase);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t at = smem_u32(smem + stage * kWideStage);
-        const uint64_t a = sdesc_k_sw128(at), b = sdesc_k_sw128(at + kHalf);
+        const uint32_t at = smem_u32(smem + stage * p.stage_bytes);
+        const uint64_t a = sdesc_k_sw128(at), b = sdesc_k_sw128(at + PER * kHalf);
         uint64_t* used = &empty[stage];
-        if (++stage == kWideStages) stage = 0, phase ^= 1u;
+        if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
         const bool next = mbar_test(&full[stage], phase);  // (asked before the products that stand in its way)
         if (elect_one()) {
+          // (straight on: a loop of a length that is known late cost 5 % of large products, an eighth of ordinary ones)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) tc_mma_pair(d, a + (k * 32 >> 4), b + (k * 32 >> 4), idesc, kb != 0 || k != 0);
+          for (int k = 0; k < 4; ++k) tc_mma_pair(d, a + (k * 32 >> 4), b + (k * 32 >> 4), idesc, ks != 0 || k != 0);
+          if (PER == 2) {
+            const uint64_t b1 = b + (p.bn * 64 >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tc_mma_pair(d, a + ((kHalf + k * 32) >> 4), b1 + (k * 32 >> 4), idesc, 1u);
+          }
           tc_commit_pair(used);
-          if (kb + 1 == p.k_blocks) tc_commit_pair(&tfull[acc]);
+          if (ks + 1 == p.k_steps) tc_commit_pair(&tfull[acc]);
         }
         there = __all_sync(0xFFFFFFFFu, next);
       }
@@ -308,10 +314,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   }
 }
 
-template <int SIDES>
+template <int SIDES, int PER>
 cudaError_t launch(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = once_a_device(done, [] { return cudaFuncSetAttribute(k_wide<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem); });
+  cudaError_t e = once_a_device(done, [] { return cudaFuncSetAttribute(k_wide<SIDES, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem); });
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
   cudaLaunchConfig_t cfg = {};
@@ -325,13 +331,14 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_wide<SIDES>, w, g, x, p);
+  return cudaLaunchKernelEx(&cfg, k_wide<SIDES, PER>, w, g, x, p);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_wide(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, bool gate, cudaStream_t st) {
-  return gate ? launch<2>(w, g, x, p, st) : launch<1>(w, g, x, p, st);
+  if (p.per == 2) return gate ? launch<2, 2>(w, g, x, p, st) : launch<1, 2>(w, g, x, p, st);
+  return gate ? launch<2, 1>(w, g, x, p, st) : launch<1, 1>(w, g, x, p, st);
 }
 
 }  // namespace dt

@@ -28,7 +28,6 @@ namespace {
 constexpr int kVecs = 4;  // pieces of 16 bytes of a thread's round
 constexpr int kStretches = 16;
 constexpr int kMaxTop = 64, kMaxSplit = 16;
-constexpr int kShortRow = 8192;  // logits
 // Rounds in shared memory, and its bytes: with the stretches' largest in it, two rounds leave room for four CTAs an SM.
 constexpr int rounds_ahead(bool best) { return best ? 2 : 3; }
 constexpr int logp_smem(bool best, int threads) { return rounds_ahead(best) * kVecs * threads * 16 + (best ? kStretches * threads * 4 : 0); }
@@ -72,7 +71,7 @@ DT_DEVINL void copy16(void* to, const void* from) {
 }
 
 // PER: keys of a lane when a warp's list is full, 32 PER in all (0: no best tokens are asked for).  Rows that a CTA reads
-// alone and that are short take 64 threads, whose own costs count there (333 to 8192 logits; see the choice below).
+// alone may take 64 threads (see the choice below).
 template <bool BF16, int PER, int kLogpThreads>
 __global__ void __launch_bounds__(kLogpThreads, 1024 / kLogpThreads) k_logp(const LogpParams p) {
   constexpr int kLogpWarps = kLogpThreads / 32, kMostSplit = kLogpThreads == 64 ? 1 : kMaxSplit;
@@ -436,7 +435,12 @@ cudaError_t launch(const LogpParams& p, cudaStream_t st) {
 }
 template <bool BF16, int PER>
 cudaError_t launch(const LogpParams& p, cudaStream_t st) {
-  return p.split == 1 && p.a.vocab <= kShortRow ? launch<BF16, PER, 64>(p, st) : launch<BF16, PER, 256>(p, st);
+  // 64 threads: short rows, and where rows fill all places and their ends, of which there are more side by side then, count.
+  // us by 256 and 64 threads: 4000 rows of 8192, 5 best 70 and 39, of 32768 111 and 100; 2000 of 65536 102 and 98; 8192 of 151936 in
+  // bf16 468 and 414, without best 380 and 396; but 2080 of 151936 212 and 223; 320 of 32768 17 and 22.
+  const int64_t bytes = static_cast<int64_t>(p.a.vocab) * (BF16 ? 2 : 4);
+  const bool small = p.split == 1 && (bytes <= 8192 || (p.a.rows >= 12 * kSms && bytes <= (PER ? 320 : 32) * 1024));
+  return small ? launch<BF16, PER, 64>(p, st) : launch<BF16, PER, 256>(p, st);
 }
 
 }  // namespace

@@ -1,7 +1,9 @@
 """The operators around a target layer's attention on the GPU against their 64-bit definitions.
 
 Tolerances count roundings.  Half a step of bf16 is 2^-8 of a value, of fp32 2^-24.  A sum of K products in fp32 is off by
-at most K 2^-23 of the sum of their magnitudes (a rounding or a cut at every addition).
+at most K 2^-23 of the sum of their magnitudes (a rounding or a cut at every addition).  Where outputs are fp32, an accumulator of
+the tensor core adds 512 channels, 16 at a time (two cuts each, one of the terms and one of the sum), and the accumulators, or
+for one or two tokens the channels of 64 pairs of lanes, are added with a rounding each: (2 * 32 + K / 128 + 16) 2^-23.
 """
 import math
 
@@ -61,6 +63,8 @@ def check_linear(c, out, cols=None):
     got = f64(out if cols is None else out[:, cols])
     want = ol.linear(x, w, b, g, gb, act, res)
     unit = (x.shape[1] + 8) * 2.0 ** -23
+    if str(out.dtype) == "torch.float32":
+        unit = min(unit, (80 + x.shape[1] / 128) * 2.0 ** -23)
     off = (np.abs(x) @ np.abs(w).T + (0 if b is None else np.abs(b))) * unit
     y = x @ w.T + (0 if b is None else b)
     if g is not None:
@@ -79,15 +83,17 @@ def check_linear(c, out, cols=None):
 @pytest.mark.parametrize("rows,inner,outer", [
     (1, 8, 1), (1, 2560, 6144), (2, 64, 5), (7, 72, 127), (16, 1032, 128), (17, 512, 129), (33, 2560, 300), (65, 520, 1001),
     (128, 256, 2501), (129, 136, 130), (255, 448, 257), (256, 64, 64), (257, 72, 513), (300, 4096, 1000), (1000, 192, 200),
-    (1, 16384, 40), (2, 8, 20000), (513, 8, 3)])
-@pytest.mark.parametrize("form", ["plain", "all", "gate"])
+    (1, 16384, 40), (2, 8, 20000), (513, 8, 3), (3, 8192, 130), (40, 8192, 200), (250, 4096, 129), (20, 256, 10240), (9, 72, 12345),
+    (150, 136, 10000), (600, 256, 700), (300, 640, 64)])
+@pytest.mark.parametrize("form", ["plain", "all", "gate", "gate32"])
 def test_linear_sizes(rows, inner, outer, form):
     torch = _t()
     from conditional_draft_tree_lm_gb300 import linear
-    kw = dict(plain={}, all=dict(act="gelu_tanh", bias=True, res=True), gate=dict(gate=True, act="silu", bias=True, res=True))[form]
+    kw = dict(plain={}, all=dict(act="gelu_tanh", bias=True, res=True), gate=dict(gate=True, act="silu", bias=True, res=True),
+              gate32=dict(gate=True, act="gelu"))[form]
     c = linear_case(rows + inner, rows, inner, outer, **kw)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    out = linear(status=status, out_dtype=torch.float32 if form == "plain" else None, **c)
+    out = linear(status=status, out_dtype=torch.float32 if form in ("plain", "gate32") else None, **c)
     check_linear(c, out)
     assert status.item() == 0
 
@@ -182,7 +188,8 @@ def test_linear_outputs_behind_32_bits():
     check_linear(last, out[-3:, -200:])
 
 
-@pytest.mark.parametrize("rows,inner,outer,gate", [(1, 2560, 6144, False), (32, 2560, 1280, True), (700, 512, 600, False), (700, 512, 600, True)])
+@pytest.mark.parametrize("rows,inner,outer,gate", [(1, 2560, 6144, False), (32, 2560, 1280, True), (700, 512, 600, False), (700, 512, 600, True),
+                                                   (64, 1024, 20000, False), (2100, 4096, 2560, False)])
 def test_linear_gives_the_same_bits_alone_beside_others_and_replayed(rows, inner, outer, gate):
     torch = _t()
     from conditional_draft_tree_lm_gb300 import linear
@@ -426,6 +433,33 @@ def test_logprobs_of_masked_rows_and_values_that_are_not_finite(full, vocab, row
     check_logp(x, tokens, 0, 1.0, found, rows=range(7))
     assert status.item() == KV_BAD_INDEX
     token_logprobs(x, tokens)
+
+
+@pytest.mark.parametrize("rows,vocab,top,full", [(2000, 5003, 5, True), (2000, 8192, 40, True), (1900, 20000, 5, False), (1900, 20011, 0, False),
+                                                 (2000, 2000, 20, False), (400, 1999, 33, True)])
+def test_logprobs_of_many_rows_with_and_without_masks(rows, vocab, top, full):
+    """Rows that fill all places at once: by turns as they are, with a few logits left, with fewer than are asked for, and
+    with logits in one stretch of the row only."""
+    torch = _t()
+    from conditional_draft_tree_lm_gb300 import token_logprobs
+    rs = np.random.RandomState(rows + vocab)
+    gen = torch.Generator(device="cuda").manual_seed(vocab)
+    x = torch.randn(rows, vocab, generator=gen, device="cuda") * 3
+    keep = torch.rand(rows, vocab, generator=gen, device="cuda")
+    x[1::4] = x[1::4].masked_fill(keep[1::4] > 60 / vocab, -math.inf)
+    x[2::4] = x[2::4].masked_fill(keep[2::4] > 3 / vocab, -math.inf)
+    x[3::4, vocab // 3 + 37:] = -math.inf
+    x[3::4, :vocab // 3] = -math.inf
+    x = x if full else x.to(torch.bfloat16)
+    tokens = torch.as_tensor(rs.randint(0, vocab, (rows, 2)), dtype=torch.int32, device="cuda")
+    found = token_logprobs(x, tokens, top=top)
+    check_logp(x, tokens, top, 1.0, found, rows=[*range(8), *range(rows - 8, rows)])
+    # every row as it is alone: read by several CTAs there
+    for r in (0, 1, 2, 3, rows - 1):
+        alone = token_logprobs(x[r:r + 1], tokens[r:r + 1], top=top)
+        if top:
+            assert torch.equal(alone["top_tok"][0], found["top_tok"][r])
+        check_logp(x[r:r + 1], tokens[r:r + 1], top, 1.0, alone)
 
 
 def test_logprobs_of_large_logits():

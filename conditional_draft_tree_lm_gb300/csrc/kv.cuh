@@ -127,6 +127,21 @@ inline bool kv_rows_apart(int64_t rows, int heads, int head_dim, int64_t row_str
          (rows == 1 || heads == 1 || row_stride >= (heads - 1) * head_stride + head_dim || head_stride >= (rows - 1) * row_stride + head_dim);
 }
 
+// Rows in memory, in bytes, and whether two sets of them share any (rows of one stride may stand beside each other in it; of
+// different strides in one stretch of memory they are taken to meet).
+struct MemoryRows {
+  uintptr_t at;
+  int64_t rows, stride, width;
+};
+inline bool rows_meet(const MemoryRows& a, const MemoryRows& b) {
+  const auto end = [](const MemoryRows& r) { return r.at + static_cast<uintptr_t>((r.rows - 1) * r.stride + r.width); };
+  if (a.at >= end(b) || b.at >= end(a)) return false;
+  const int64_t s = a.rows > 1 ? a.stride : b.stride;
+  if ((a.rows == 1 && b.rows == 1) || (b.rows > 1 && b.stride != s) || a.width > s || b.width > s) return true;
+  const int64_t d = (static_cast<int64_t>(a.at - b.at) % s + s) % s;  // columns from b's rows to a's
+  return d < b.width || d + a.width > s;
+}
+
 dt_status kv_check_cache(const char* who, const dt_kv_cache* c);
 
 // Rows of heads in bf16 (strides in elements) as a 3D tensor map: boxes of 64 channels x heads x rows, swizzled.

@@ -118,6 +118,8 @@ __global__ void __launch_bounds__(kFewThreads)
       __syncwarp();
       if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
     }
+    // no copy may outlive the CTA, whichever wait gave up
+    for (uint32_t s = 0; s < static_cast<uint32_t>(ahead); ++s) mbar_wait(&full[s], s < stage ? phase ^ 1u : phase, nullptr);
   } else if (warp == 1) {
     const uint32_t idesc = idesc_bf16_f32(128, p.bn);
     uint32_t stage = 0, phase = 0;
@@ -266,6 +268,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
       }
     }
+    // no copy may outlive the CTA, whichever wait gave up
+    for (uint32_t s = 0; s < static_cast<uint32_t>(p.stages); ++s) mbar_wait(&full[s], s < stage ? phase : phase ^ 1u, nullptr);
   } else if (warp == 1) {
     // (rows of the product behind the tile's rows of weight come from whatever follows them, and go nowhere)
     const uint32_t idesc = idesc_bf16_f32(128, p.bn);
@@ -408,8 +412,6 @@ cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& g, const CUtenso
   return gate ? launch_few<2, 1>(w, g, x, p, st) : launch_few<1, 1>(w, g, x, p, st);
 }
 
-constexpr int kSegmentBlocks = 8;  // of 64 channels, for outputs in 32 bits
-
 // Tokens in tiles, padded to 16: of 256 at most, 128 where their sums stay in shared memory.
 void plan_tokens(LinearParams& p, int sides) {
   const int most = (p.out_fp32 ? 128 : 256) / sides;
@@ -515,6 +517,15 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
     return kv_fail(DT_ERR_INVALID_ARG, "%s: out is null or misaligned, or its rows overlap", who);
   if (((reinterpret_cast<uintptr_t>(a.residual) | reinterpret_cast<uintptr_t>(a.bias) | reinterpret_cast<uintptr_t>(a.gate_bias)) & 1u) != 0)
     return kv_fail(DT_ERR_INVALID_ARG, "%s: misaligned residual or bias", who);
+  const MemoryRows to = {out, a.rows, a.out_row_stride * static_cast<int64_t>(bytes), a.outer * static_cast<int64_t>(bytes)};
+  auto meets = [&](const void* d, int64_t rows, int64_t stride, int64_t width) {
+    return d && rows_meet(to, {reinterpret_cast<uintptr_t>(d), rows, stride * 2, width * 2});
+  };
+  const bool in_place = a.residual == a.out && !a.out_fp32 && (a.rows == 1 || a.residual_row_stride == a.out_row_stride);
+  if (meets(a.x, a.rows, a.x_row_stride, a.inner) || meets(a.weight, a.outer, a.weight_row_stride, a.inner) ||
+      meets(a.gate, a.outer, a.gate_row_stride, a.inner) || (!in_place && meets(a.residual, a.rows, a.residual_row_stride, a.outer)) ||
+      meets(a.bias, 1, 0, a.outer) || meets(a.gate_bias, 1, 0, a.outer))
+    return kv_fail(DT_ERR_INVALID_ARG, "%s: out overlaps an input and is not the residual itself", who);
   LinearParams p = {};
   p.bias = static_cast<const uint16_t*>(a.bias);
   p.gate_bias = static_cast<const uint16_t*>(a.gate_bias);
@@ -532,7 +543,7 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (p.rows <= kTokensMost) return kv_launched(who, launch_linear_token(a, p, st));
   const int sides = a.gate ? 2 : 1;
-  const bool many = p.rows > 256 && !p.out_fp32;
+  const bool many = p.rows > 256;
   const uintptr_t res = reinterpret_cast<uintptr_t>(a.residual);
   const int64_t at_once = many ? 16 / static_cast<int64_t>(bytes) : 4;  // outputs written together
   p.wide = out % (at_once * bytes) == 0 && (a.rows == 1 || a.out_row_stride % at_once == 0) &&

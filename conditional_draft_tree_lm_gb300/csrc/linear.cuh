@@ -113,6 +113,7 @@ DT_DEVINL void finish4(const LinearParams& p, int64_t t, int n, const float4& y4
 // 64 channels, which have to be whole where per > 1 (per 1: the first coordinate is the channel, the third 0).
 bool linear_map(CUtensorMap* m, const void* base, int inner, int64_t rows, int64_t stride, int box_rows, int per);
 
+constexpr int kSegmentBlocks = 8;          // blocks of 64 channels that an accumulator adds, for outputs in 32 bits
 constexpr uint32_t kWideRing = 6 * 32768;  // of launch_linear_wide: bytes of its stages
 constexpr int kTokensMost = 2;  // of launch_linear_token
 cudaError_t launch_linear_token(const dt_linear_args& a, const LinearParams& p, cudaStream_t st);

@@ -18,6 +18,7 @@ namespace dt {
 namespace {
 
 constexpr int kWideThreads = 384, kEpilogueWarps = 8;
+constexpr int kOtherRegs = 72, kSumRegs = 216;  // of the warps that issue and of the epilogue's, outputs in 32 bits
 constexpr uint32_t kHalf = 128 * 128;  // 128 rows of 64 bf16
 constexpr uint32_t kStagingBytes = 4096;
 constexpr uint32_t kWideSmem = 1024 + kWideRing + kEpilogueWarps * kStagingBytes + 512;
@@ -87,7 +88,106 @@ DT_DEVINL uint32_t piece_at(int row, int k) {
   return E == 2 ? row * 64 + ((k ^ (row >> 1 & 3)) << 4) : row * 128 + ((k ^ (row & 7)) << 4);
 }
 
-template <int SIDES, int PER>
+// A warp's chunk of an output tile: rows t0 .. of 32, columns n .. of 32, of which `rows` and `cols` are there.
+struct Chunk {
+  int t0, n, rows, cols, lane;
+  bool whole;  // 16 bytes at a time
+  uint8_t* mine;
+};
+// The residual's, lanes 4 i .. 4 i + 3 a row.
+DT_DEVINL void ask_residual(const LinearParams& p, const Chunk& at, uint4 (&res)[4]) {
+  if (!p.residual || !at.whole) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (at.lane >> 2);
+    res[i] = r < at.rows ? *reinterpret_cast<const uint4*>(p.residual + (at.t0 + r) * p.residual_stride + at.n + 8 * (at.lane & 3)) : make_uint4(0, 0, 0, 0);
+  }
+}
+// y (and the gate's z): the sums of the product, a row a lane; bias, activation and residual, and out.
+template <int SIDES, bool FULL>
+DT_DEVINL void finish_chunk(const LinearParams& p, const Chunk& at, float (&y)[32], float (&z)[32], const uint4 (&res)[4]) {
+  const int lane = at.lane, rows = at.rows, cols = at.cols, n = at.n, t0 = at.t0;
+  uint8_t* mine = at.mine;
+  if (p.bias) {
+    const float b = lane < cols ? bf16_to_f32(p.bias[n + lane]) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) y[j] += __shfl_sync(0xFFFFFFFFu, b, j);
+  }
+  if (SIDES == 2) {
+    if (p.gate_bias) {
+      const float b = lane < cols ? bf16_to_f32(p.gate_bias[n + lane]) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) z[j] += __shfl_sync(0xFFFFFFFFu, b, j);
+    }
+    activate(z, p.activation);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) y[j] *= z[j];
+  } else {
+    activate(y, p.activation);
+  }
+  if (p.residual) {
+    __syncwarp();  // (what stood there has been read)
+    if (at.whole) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(mine + piece_at<2>(i * 8 + (lane >> 2), lane & 3)) = res[i];
+    } else if (lane < cols) {
+      for (int r = 0; r < rows; ++r)
+        *reinterpret_cast<uint16_t*>(mine + piece_at<2>(r, lane >> 3) + 2 * (lane & 7)) = p.residual[(t0 + r) * p.residual_stride + n + lane];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint4 w = *reinterpret_cast<const uint4*>(mine + piece_at<2>(lane, k));
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = 8 * k + 2 * i;
+        y[j] += __uint_as_float(u[i] << 16);
+        y[j + 1] += __uint_as_float(u[i] & 0xFFFF0000u);
+      }
+    }
+  }
+  __syncwarp();
+  if (FULL) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      *reinterpret_cast<float4*>(mine + piece_at<4>(lane, k)) = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+    __syncwarp();
+    float* out = static_cast<float*>(p.out) + t0 * p.out_stride + n;
+    if (at.whole) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3);
+        if (r < rows) *reinterpret_cast<uint4*>(out + r * p.out_stride + 4 * (lane & 7)) = *reinterpret_cast<const uint4*>(mine + piece_at<4>(r, lane & 7));
+      }
+    } else if (lane < cols) {
+      for (int r = 0; r < rows; ++r) out[r * p.out_stride + lane] = *reinterpret_cast<const float*>(mine + piece_at<4>(r, lane >> 2) + 4 * (lane & 3));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = pack_p(y[8 * k + 2 * i], y[8 * k + 2 * i + 1]);
+      *reinterpret_cast<uint4*>(mine + piece_at<2>(lane, k)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    uint16_t* out = static_cast<uint16_t*>(p.out) + t0 * p.out_stride + n;
+    if (at.whole) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2);
+        if (r < rows) *reinterpret_cast<uint4*>(out + r * p.out_stride + 8 * (lane & 3)) = *reinterpret_cast<const uint4*>(mine + piece_at<2>(r, lane & 3));
+      }
+    } else if (lane < cols) {
+      for (int r = 0; r < rows; ++r) out[r * p.out_stride + lane] = *reinterpret_cast<const uint16_t*>(mine + piece_at<2>(r, lane >> 3) + 2 * (lane & 7));
+    }
+  }
+  __syncwarp();  // (the staging place has been read)
+}
+
+// FULL: outputs in 32 bits.
+template <int SIDES, int PER, bool FULL>
 __global__ void __launch_bounds__(kWideThreads, 1)
     k_wide(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_g,
            const __grid_constant__ CUtensorMap tm_x, const LinearParams p) {
@@ -122,8 +222,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   cluster_barrier();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const int segment = FULL ? kSegmentBlocks / PER : p.k_steps;  // steps that an accumulator adds
   bool ok = true;
 
+  // (the epilogue's sums: 72 + 2 x 216 = 3 x 168, what the block was launched with)
+  static_assert(kOtherRegs + 2 * kSumRegs <= 3 * 168, "");
+  if (FULL && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 0) {
     const uint64_t keep = l2_policy_evict_last();
     uint32_t stage = 0, phase = 0;
@@ -145,163 +249,130 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
       }
     }
+    // no copy may outlive the CTA, whichever wait gave up (the first CTA's barriers count both CTAs' copies)
+    for (uint32_t s = 0; rank == 0 && s < static_cast<uint32_t>(p.stages); ++s) mbar_wait(&full[s], s < stage ? phase : phase ^ 1u, nullptr);
   } else if (warp == 1 && rank == 0) {
     const uint32_t idesc = idesc_bf16_f32(256, p.bn);
     uint32_t stage = 0, phase = 0;
-    int local = 0;
+    int local = 0;  // accumulators filled
     bool there = false;
-    for (int tile = pair; tile < tiles && ok; tile += pairs, ++local) {
-      const int acc = local & 1;
-      ok = pair_wait(&tempty[acc], (local >> 1 & 1) ^ 1u);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem + acc * 256;
-      for (int ks = 0; ks < p.k_steps; ++ks) {
-        ok = there || pair_wait(&full[stage], phase);
+    for (int tile = pair; tile < tiles && ok; tile += pairs)
+      for (int ks0 = 0; ks0 < p.k_steps && ok; ks0 += segment, ++local) {
+        const int acc = local & 1, ks1 = FULL ? min(p.k_steps, ks0 + segment) : p.k_steps;
+        ok = pair_wait(&tempty[acc], (local >> 1 & 1) ^ 1u);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t at = smem_u32(smem + stage * p.stage_bytes);
-        const uint64_t a = sdesc_k_sw128(at), b = sdesc_k_sw128(at + PER * kHalf);
-        uint64_t* used = &empty[stage];
-        if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
-        const bool next = mbar_test(&full[stage], phase);  // (asked before the products that stand in its way)
-        if (elect_one()) {
-          // (straight on: a loop of a length that is known late cost 5 % of large products, an eighth of ordinary ones)
+        const uint32_t d = tmem + acc * 256;
+        for (int ks = ks0; ks < ks1; ++ks) {
+          ok = there || pair_wait(&full[stage], phase);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t at = smem_u32(smem + stage * p.stage_bytes);
+          const uint64_t a = sdesc_k_sw128(at), b = sdesc_k_sw128(at + PER * kHalf);
+          uint64_t* used = &empty[stage];
+          if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
+          const bool next = mbar_test(&full[stage], phase);  // (asked before the products that stand in its way)
+          if (elect_one()) {
+            // (straight on: a loop of a length that is known late cost 5 % of large products, an eighth of ordinary ones)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) tc_mma_pair(d, a + (k * 32 >> 4), b + (k * 32 >> 4), idesc, ks != 0 || k != 0);
-          if (PER == 2) {
-            const uint64_t b1 = b + (p.bn * 64 >> 4);
+            for (int k = 0; k < 4; ++k) tc_mma_pair(d, a + (k * 32 >> 4), b + (k * 32 >> 4), idesc, ks != ks0 || k != 0);
+            if (PER == 2) {
+              const uint64_t b1 = b + (p.bn * 64 >> 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) tc_mma_pair(d, a + ((kHalf + k * 32) >> 4), b1 + (k * 32 >> 4), idesc, 1u);
+              for (int k = 0; k < 4; ++k) tc_mma_pair(d, a + ((kHalf + k * 32) >> 4), b1 + (k * 32 >> 4), idesc, 1u);
+            }
+            tc_commit_pair(used);
+            if (ks + 1 == ks1) tc_commit_pair(&tfull[acc]);
           }
-          tc_commit_pair(used);
-          if (ks + 1 == p.k_steps) tc_commit_pair(&tfull[acc]);
+          there = __all_sync(0xFFFFFFFFu, next);
         }
-        there = __all_sync(0xFFFFFFFFu, next);
       }
-    }
     if (!ok) {  // (no product may outlive its operands and tensor memory)
       if (elect_one()) tc_commit_pair(drained);
       __syncwarp();
       pair_wait(drained, 0);
     }
   } else if (warp >= 4) {
+    if (FULL) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
     const int quarter = warp & 3, group = (warp - 4) >> 2;
     uint8_t* mine = staging + (warp - 4) * kStagingBytes;
-    int local = 0;
-    for (int tile = pair; tile < tiles; tile += pairs, ++local) {
-      const int acc = local & 1;
-      ok = pair_wait(&tfull[acc], local >> 1 & 1);
-      if (!ok) break;
-      tc_fence_after();
-      const Place at = place(p, tile);
-      const int t0 = at.m0 + rank * 128 + quarter * 32, rows = min(32, p.rows - t0);
-      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * 256;
-      for (int c = group * 32; c < p.tile_outs; c += 64) {
-        const int n = at.n0 + c, cols = min(32, p.outer - n);
-        if (cols <= 0 || rows <= 0) break;
-        const bool whole = p.wide && cols == 32;
-        // the residual's 32 x 32, lanes 4 i .. 4 i + 3 a row
-        uint4 res[4];
-        if (p.residual && whole) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + (lane >> 2);
-            res[i] = r < rows ? *reinterpret_cast<const uint4*>(p.residual + (t0 + r) * p.residual_stride + n + 8 * (lane & 3)) : make_uint4(0, 0, 0, 0);
-          }
-        }
-        uint32_t raw[32 * SIDES];
-        tmem_ld32(from + c, raw);
-        if (SIDES == 2) tmem_ld32(from + p.tile_outs + c, raw + 32);
-        tmem_wait_ld();
-        tmem_landed32(raw);
-        if (SIDES == 2) tmem_landed32(raw + 32);
-        float y[32], z[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          y[j] = __uint_as_float(raw[32 * (SIDES - 1) + j]);
-          z[j] = __uint_as_float(raw[j]);
-        }
-        if (p.bias) {
-          const float b = lane < cols ? bf16_to_f32(p.bias[n + lane]) : 0.0f;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) y[j] += __shfl_sync(0xFFFFFFFFu, b, j);
-        }
-        if (SIDES == 2) {
-          if (p.gate_bias) {
-            const float b = lane < cols ? bf16_to_f32(p.gate_bias[n + lane]) : 0.0f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) z[j] += __shfl_sync(0xFFFFFFFFu, b, j);
-          }
-          activate(z, p.activation);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) y[j] *= z[j];
-        } else {
-          activate(y, p.activation);
-        }
-        if (p.residual) {
-          __syncwarp();  // (what stood there has been read)
-          if (whole) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(mine + piece_at<2>(i * 8 + (lane >> 2), lane & 3)) = res[i];
-          } else if (lane < cols) {
-            for (int r = 0; r < rows; ++r)
-              *reinterpret_cast<uint16_t*>(mine + piece_at<2>(r, lane >> 3) + 2 * (lane & 7)) = p.residual[(t0 + r) * p.residual_stride + n + lane];
-          }
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 w = *reinterpret_cast<const uint4*>(mine + piece_at<2>(lane, k));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int j = 8 * k + 2 * i;
-              y[j] += __uint_as_float(u[i] << 16);
-              y[j + 1] += __uint_as_float(u[i] & 0xFFFF0000u);
-            }
-          }
-        }
-        __syncwarp();
-        if (p.out_fp32) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<float4*>(mine + piece_at<4>(lane, k)) = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-          __syncwarp();
-          float* out = static_cast<float*>(p.out) + t0 * p.out_stride + n;
-          if (whole) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = i * 4 + (lane >> 3);
-              if (r < rows) *reinterpret_cast<uint4*>(out + r * p.out_stride + 4 * (lane & 7)) = *reinterpret_cast<const uint4*>(mine + piece_at<4>(r, lane & 7));
-            }
-          } else if (lane < cols) {
-            for (int r = 0; r < rows; ++r) out[r * p.out_stride + lane] = *reinterpret_cast<const float*>(mine + piece_at<4>(r, lane >> 2) + 4 * (lane & 3));
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = pack_p(y[8 * k + 2 * i], y[8 * k + 2 * i + 1]);
-            *reinterpret_cast<uint4*>(mine + piece_at<2>(lane, k)) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          __syncwarp();
-          uint16_t* out = static_cast<uint16_t*>(p.out) + t0 * p.out_stride + n;
-          if (whole) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = i * 8 + (lane >> 2);
-              if (r < rows) *reinterpret_cast<uint4*>(out + r * p.out_stride + 8 * (lane & 3)) = *reinterpret_cast<const uint4*>(mine + piece_at<2>(r, lane & 3));
-            }
-          } else if (lane < cols) {
-            for (int r = 0; r < rows; ++r) out[r * p.out_stride + lane] = *reinterpret_cast<const uint16_t*>(mine + piece_at<2>(r, lane >> 3) + 2 * (lane & 7));
-          }
-        }
-        __syncwarp();  // (the staging place has been read)
-      }
+    auto give_back = [&](int acc) {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) peer_arrive(peer_addr(&tempty[acc], 0));
+    };
+    int local = 0;
+    for (int tile = pair; tile < tiles && ok; tile += pairs) {
+      const Place at = place(p, tile);
+      const int t0 = at.m0 + rank * 128 + quarter * 32, rows = min(32, p.rows - t0);
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+      auto chunk_at = [&](int c) {
+        const int n = at.n0 + c, cols = min(32, p.outer - n);
+        return Chunk{t0, n, rows, cols, lane, p.wide && cols == 32, mine};
+      };
+      uint4 res[4];
+      if (FULL) {
+        // sums of up to 4 / SIDES chunks of 32 columns, [chunk][side], over the accumulators of the tile
+        float sum[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[i][j] = 0.0f;
+        for (int ks0 = 0; ks0 < p.k_steps && ok; ks0 += segment, ++local) {
+          const int acc = local & 1;
+          ok = pair_wait(&tfull[acc], local >> 1 & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = group * 32 + 64 * (i / SIDES);
+            if (c >= p.tile_outs) break;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint32_t v[16];
+              tmem_ld16(lanes + acc * 256 + (i % SIDES) * p.tile_outs + c + 16 * q, v);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum[i][16 * q + j] += __uint_as_float(v[j]);
+            }
+          }
+          give_back(acc);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 4; i += SIDES) {
+          const int c = group * 32 + 64 * (i / SIDES);
+          const Chunk chunk = chunk_at(c);
+          if (c >= p.tile_outs || chunk.cols <= 0 || rows <= 0) break;
+          ask_residual(p, chunk, res);
+          finish_chunk<SIDES, FULL>(p, chunk, sum[i + SIDES - 1], sum[i], res);
+        }
+      } else {
+        const int acc = local & 1;
+        ok = pair_wait(&tfull[acc], local >> 1 & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t from = lanes + acc * 256;
+        for (int c = group * 32; c < p.tile_outs; c += 64) {
+          const Chunk chunk = chunk_at(c);
+          if (chunk.cols <= 0 || rows <= 0) break;
+          ask_residual(p, chunk, res);
+          uint32_t raw[32 * SIDES];
+          tmem_ld32(from + c, raw);
+          if (SIDES == 2) tmem_ld32(from + p.tile_outs + c, raw + 32);
+          tmem_wait_ld();
+          tmem_landed32(raw);
+          if (SIDES == 2) tmem_landed32(raw + 32);
+          float y[32], z[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            y[j] = __uint_as_float(raw[32 * (SIDES - 1) + j]);
+            z[j] = __uint_as_float(raw[j]);
+          }
+          finish_chunk<SIDES, FULL>(p, chunk, y, z, res);
+        }
+        give_back(acc);
+        ++local;
+      }
     }
   }
   if (!ok && p.status && lane == 0) atomicOr(p.status, DT_KV_TIMEOUT);
@@ -314,10 +385,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   }
 }
 
-template <int SIDES, int PER>
+template <int SIDES, int PER, bool FULL>
 cudaError_t launch(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = once_a_device(done, [] { return cudaFuncSetAttribute(k_wide<SIDES, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem); });
+  cudaError_t e = once_a_device(done, [] { return cudaFuncSetAttribute(k_wide<SIDES, PER, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem); });
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
   cudaLaunchConfig_t cfg = {};
@@ -331,7 +402,12 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_wide<SIDES, PER>, w, g, x, p);
+  return cudaLaunchKernelEx(&cfg, k_wide<SIDES, PER, FULL>, w, g, x, p);
+}
+
+template <int SIDES, int PER>
+cudaError_t launch(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, cudaStream_t st) {
+  return p.out_fp32 ? launch<SIDES, PER, true>(w, g, x, p, st) : launch<SIDES, PER, false>(w, g, x, p, st);
 }
 
 }  // namespace

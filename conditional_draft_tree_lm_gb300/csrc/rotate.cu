@@ -195,6 +195,25 @@ extern "C" dt_status dt_qk_norm_rope(const dt_qk_norm_rope_args* args, void* str
   if (!kv_rows_apart(rows, a.n_q, a.head_dim, a.q_out_row_stride, a.q_out_head_stride) ||
       (a.k && !kv_rows_apart(rows, a.n_kv, a.head_dim, a.k_out_row_stride, a.k_out_head_stride)))
     return kv_fail(DT_ERR_INVALID_ARG, "%s: rows of q_out or k_out overlap", who);
+  struct Heads {
+    const void* at;
+    int heads;
+    int64_t row_stride, head_stride;
+  };
+  // (the larger stride's as rows, whatever order they stand in)
+  auto in_memory = [&](const Heads& h) {
+    const bool head_rows = h.heads > 1 && (rows == 1 || h.head_stride > h.row_stride);
+    const int64_t in = head_rows ? (rows - 1) * h.row_stride : (h.heads - 1) * h.head_stride;
+    return MemoryRows{reinterpret_cast<uintptr_t>(h.at), head_rows ? h.heads : rows, 2 * (head_rows ? h.head_stride : h.row_stride), 2 * (in + a.head_dim)};
+  };
+  auto meet = [&](const Heads& x, const Heads& y) { return rows_meet(in_memory(x), in_memory(y)); };
+  auto same = [&](const Heads& x, const Heads& y) {
+    return x.at == y.at && (rows == 1 || x.row_stride == y.row_stride) && (x.heads == 1 || x.head_stride == y.head_stride);
+  };
+  const Heads q = {a.q, a.n_q, a.q_row_stride, a.q_head_stride}, q_out = {a.q_out, a.n_q, a.q_out_row_stride, a.q_out_head_stride};
+  const Heads k = {a.k, a.n_kv, a.k_row_stride, a.k_head_stride}, k_out = {a.k_out, a.n_kv, a.k_out_row_stride, a.k_out_head_stride};
+  if ((!same(q, q_out) && meet(q, q_out)) || (a.k && ((!same(k, k_out) && meet(k, k_out)) || meet(q, k_out) || meet(k, q_out) || meet(q_out, k_out))))
+    return kv_fail(DT_ERR_INVALID_ARG, "%s: q_out or k_out overlaps another tensor and is not q or k itself", who);
   RotateParams p = {};
   p.a = a;
   p.rows = rows;

@@ -577,8 +577,9 @@ dt_status dt_prompt_attention(const dt_prompt_attention_args* args, void* stream
  * residual [rows, outer] are bf16, out [rows, outer] bf16 or fp32.  Row strides
  * are in elements; columns are adjacent.  x, weight and gate must be 16-byte
  * aligned, inner and their row strides multiples of 8; residual and out may be
- * anywhere, and out may be the residual itself (same address and stride), but
- * must not overlap another input, nor its rows one another.  Sums are in fp32,
+ * anywhere, and out may be the residual itself (bf16, same address and stride), but
+ * must not overlap another input, nor its rows one another (refused; columns of a
+ * tensor that holds an input in others of its columns do not overlap it).  Sums are in fp32,
  * in an order that depends on the sizes only: the same call gives the same bits.
  * rows 0: nothing is done.  One launch.  status: [1] int32 device or NULL;
  * DT_KV_TIMEOUT is or'ed in. */
@@ -618,7 +619,7 @@ dt_status dt_linear(const dt_linear_args* args, void* stream);
  *   (base ? base[q] : 0) + (positions ? positions[row] : a).
  * Rows whose positions[row] is negative (as dt_kv_plan leaves behind the last token) are
  * not written.  Rows of heads as above; q_out may be q and k_out k (same
- * strides), other overlaps are not allowed.  k NULL: queries only.  n_req or
+ * strides), other overlaps are refused.  k NULL: queries only.  n_req or
  * slots 0: nothing is done.  One launch. */
 typedef struct dt_qk_norm_rope_args {
   int n_req, slots; /* n_req * slots at most 2^31-1 */

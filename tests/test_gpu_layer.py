@@ -168,6 +168,38 @@ def test_linear_of_no_rows():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("rows,inner,outer", [(257, 512, 96), (300, 520, 256), (700, 1024, 1000), (1000, 2568, 2600), (400, 8192, 77), (5000, 576, 513)])
+@pytest.mark.parametrize("gate", [False, True])
+def test_linear_of_many_rows_in_32_bits(rows, inner, outer, gate):
+    """Several accumulators of 512 channels and one, tiles of all widths, with everything behind the product."""
+    torch = _t()
+    from conditional_draft_tree_lm_gb300 import linear
+    c = linear_case(rows, rows, inner, outer, gate=gate, act="silu", bias=True, res=True)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = linear(out_dtype=torch.float32, status=status, **c)
+    check_linear(c, out)
+    assert status.item() == 0 and torch.equal(out, linear(out_dtype=torch.float32, **c))
+    # rows that do not start on 16 bytes, and a residual that does not
+    room = torch.full((rows, outer + 3), 7.0, device="cuda")
+    c["residual"] = torch.cat([c["residual"], c["residual"][:, :3]], 1)[:, 1:outer + 1]
+    linear(out=room[:, 1:outer + 1], **c)
+    check_linear(c, room[:, 1:outer + 1])
+    assert (room[:, 0] == 7).all() and (room[:, outer + 1:] == 7).all()
+
+
+@pytest.mark.parametrize("rows", [1, 2, 40, 300])
+def test_linear_between_columns_of_one_tensor(rows):
+    torch = _t()
+    from conditional_draft_tree_lm_gb300 import linear
+    rs = np.random.RandomState(rows)
+    room, w = bf16(rs, rows, 640), bf16(rs, 256, 128, scale=0.1)
+    c = dict(x=room[:, :128].clone(), weight=w, residual=room[:, 384:].clone(), activation=None)
+    check_linear(c, linear(room[:, :128], w, residual=room[:, 384:], out=room[:, 128:384]))
+    assert torch.equal(room[:, :128], c["x"]) and torch.equal(room[:, 384:], c["residual"])
+    with pytest.raises(Exception, match="overlaps an input"):
+        linear(room[:, :128], w, out=room[:, 127:383])
+
+
 def test_linear_outputs_behind_32_bits():
     torch = _t()
     from conditional_draft_tree_lm_gb300 import linear

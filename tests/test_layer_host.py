@@ -216,3 +216,24 @@ def test_rotary_turns():
     for bad in (dict(dim=7), dict(dim=0), dict(dim=4, inv_freq=[1.0]), dict(dim=4, inv_freq=[1.0, INF])):
         with pytest.raises(ValueError):
             ly.Rotary(device="cpu", **bad)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=8192), dict(out=8192 + 3 * 128), dict(out=8192 - 3 * 96), dict(out=65536 + 32, out_row_stride=64), dict(out=65536 + 6144 - 16),
+    dict(residual=131072 + 2, residual_row_stride=48), dict(residual=131072, residual_row_stride=56), dict(residual=131072, residual_row_stride=0),
+    dict(residual=131072, residual_row_stride=48, out_fp32=1), dict(bias=131072 + 94), dict(rows=1, out=8192 + 126),
+    dict(x_row_stride=128, out_row_stride=128, out=8192 + 256 - 64), dict(x_row_stride=128, out_row_stride=128, out=8192 + 126)])
+def test_linear_refuses_an_output_over_an_input(lib, kw):
+    a = dict(x=8192, weight=65536, out=131072)
+    err, msg = call(lib, "dt_linear", linear_args(**{**a, **kw}))
+    assert err == INVALID and "overlaps an input" in msg
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_out=8192 + 512), dict(q_out=8192, q_out_row_stride=264), dict(q_out=16384 + 128, q_out_row_stride=384, k_row_stride=384),
+    dict(k_out=8192 + 6 * 512 - 16), dict(k_out=65536 + 64, k_out_row_stride=256), dict(q_out=8192, q_row_stride=384, k=8192 + 512, k_row_stride=384,
+                                                                                      q_out_row_stride=384, q_out_head_stride=72)])
+def test_qk_norm_rope_refuses_outputs_over_other_tensors(lib, kw):
+    a = dict(q=8192, k=16384, q_out=65536, k_out=131072)
+    err, msg = call(lib, "dt_qk_norm_rope", rotate_args(**{**a, **kw}))
+    assert err == INVALID and "overlaps another tensor" in msg

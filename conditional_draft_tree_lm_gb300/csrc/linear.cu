@@ -65,8 +65,46 @@ DT_HOST_DEVICE_INLINE uint32_t few_bars(const LinearParams& p, int sides) {
   return ring > sums ? ring : sums;
 }
 
+// A CTA's share of a tile: four neighbouring rows of weight for a token at a time, their sums over the cluster's CTAs.  A thread's
+// units are 8 tokens apart, of the same rows; the reads of several are on their way together.  RANKS: the cluster's CTAs at most.
+template <int SIDES, int RANKS>
+DT_DEVINL void finish_share(const LinearParams& p, const float* sums, int rank, int tokens, int t0, int n0) {
+  constexpr int kFit = 16 / (RANKS * SIDES), kUnits = kFit > 4 ? 4 : kFit < 1 ? 1 : kFit, kStep = kFewThreads / 32;
+  // (whole tokens)
+  const int first = tokens * rank / p.split, end = tokens * (rank + 1) / p.split, f = (threadIdx.x & 31) * 4;
+  for (int t = first + static_cast<int>(threadIdx.x >> 5); t < end; t += kUnits * kStep) {
+    float4 v[kUnits][SIDES][RANKS];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+      for (int s = 0; s < SIDES; ++s) {
+        const float* at = sums + (min(t + i * kStep, end - 1) * SIDES + s) * 128 + f;
+        if (RANKS == 1) {
+          v[i][s][0] = *reinterpret_cast<const float4*>(at);
+          continue;
+        }
+#pragma unroll
+        for (int r = 0; r < RANKS; ++r)
+          if (r < p.split) v[i][s][r] = peer_ld4(peer_addr(at, r));
+      }
+    float y[4 * kUnits], z[4 * kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+      for (int s = 0; s < SIDES; ++s) {
+        float4& acc = v[i][s][0];
+#pragma unroll
+        for (int r = 1; r < RANKS; ++r)
+          if (r < p.split) acc.x += v[i][s][r].x, acc.y += v[i][s][r].y, acc.z += v[i][s][r].z, acc.w += v[i][s][r].w;
+        float* to = s == SIDES - 1 ? y : z;
+        to[4 * i] = acc.x, to[4 * i + 1] = acc.y, to[4 * i + 2] = acc.z, to[4 * i + 3] = acc.w;
+      }
+    finish_rows<SIDES, kUnits>(p, t0 + t, kStep, (end - t + kStep - 1) / kStep, n0 + f, y, z);
+  }
+}
+
 template <int SIDES, int PER>
-__global__ void __launch_bounds__(kFewThreads)
+__global__ void __launch_bounds__(kFewThreads, 2)
     k_few(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_g,
           const __grid_constant__ CUtensorMap tm_x, const LinearParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -159,20 +197,30 @@ __global__ void __launch_bounds__(kFewThreads)
   ok = ok && warp_wait(done, 0);
   tc_fence_after();
   if (ok) {
-    const int quarter = warp & 3;
-    for (int x = warp >> 2; x < SIDES * p.bn / 16; x += 2) {
-      const int side = x / (p.bn / 16), c0 = (x - side * (p.bn / 16)) * 16;
-      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + side * p.bn + c0;
-      uint32_t v[16];
-      tmem_ld16(from, v);
+    // (32 columns of the sides' accumulators, which lie one behind the other, at a time; 16 behind the last are nobody's)
+    const int quarter = warp & 3, columns = SIDES * p.bn;
+    for (int c = (warp >> 2) * 32; c < columns; c += 64) {
+      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c;
+      uint32_t v[32];
+      tmem_ld32(from, v);
+      tmem_wait_ld();
+      tmem_landed32(v);
       for (int i = p.segment_steps; i < ks1 - ks0; i += p.segment_steps) {
-        uint32_t w[16];
-        tmem_ld16(from + i / p.segment_steps * (SIDES * p.bn), w);
+        uint32_t w[32];
+        tmem_ld32(from + i / p.segment_steps * columns, w);
+        tmem_wait_ld();
+        tmem_landed32(w);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
+        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
       }
 #pragma unroll
-      for (int j = 0; j < 16; ++j) sums[((c0 + j) * SIDES + side) * 128 + quarter * 32 + lane] = __uint_as_float(v[j]);
+      for (int h = 0; h < 2; ++h) {
+        const int c16 = c + 16 * h, side = SIDES == 2 && c16 >= p.bn ? 1 : 0;
+        float* to = sums + ((c16 - side * p.bn) * SIDES + side) * 128 + quarter * 32 + lane;
+        if (c16 < columns)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) to[j * SIDES * 128] = __uint_as_float(v[16 * h + j]);
+      }
     }
   } else if (p.status && lane == 0) {
     atomicOr(p.status, DT_KV_TIMEOUT);
@@ -185,31 +233,10 @@ __global__ void __launch_bounds__(kFewThreads)
   }
   __syncwarp();
   if (p.split > 1) cluster_barrier();
-  // four neighbouring rows of weight for a token at a time, an equal share of them for each rank
-  const int units = tokens * 32;
-  const int u1 = static_cast<int>(static_cast<int64_t>(units) * (rank + 1) / p.split);
-  for (int u = static_cast<int>(static_cast<int64_t>(units) * rank / p.split) + tid; u < u1; u += kFewThreads) {
-    const int t = u >> 5, f = (u & 31) * 4;
-    if (n0 + f >= p.outer) continue;
-    float4 acc[SIDES];
-#pragma unroll
-    for (int s = 0; s < SIDES; ++s) {
-      const float* at = sums + (t * SIDES + s) * 128 + f;
-      if (p.split == 1) {
-        acc[s] = *reinterpret_cast<const float4*>(at);
-        continue;
-      }
-      float4 v[kMostSplit];  // (all on their way before the first is added)
-#pragma unroll
-      for (int r = 0; r < kMostSplit; ++r)
-        if (r < p.split) v[r] = peer_ld4(peer_addr(at, r));
-      acc[s] = v[0];
-#pragma unroll
-      for (int r = 1; r < kMostSplit; ++r)
-        if (r < p.split) acc[s].x += v[r].x, acc[s].y += v[r].y, acc[s].z += v[r].z, acc[s].w += v[r].w;
-    }
-    finish4<SIDES>(p, t0 + t, n0 + f, acc[SIDES - 1], acc[0]);
-  }
+  if (p.split == 1) finish_share<SIDES, 1>(p, sums, rank, tokens, t0, n0);
+  else if (p.split == 2) finish_share<SIDES, 2>(p, sums, rank, tokens, t0, n0);
+  else if (p.split <= 4) finish_share<SIDES, 4>(p, sums, rank, tokens, t0, n0);
+  else finish_share<SIDES, kMostSplit>(p, sums, rank, tokens, t0, n0);
   if (p.split > 1) cluster_barrier();  // (no CTA leaves while its sums are read)
 }
 
@@ -338,12 +365,19 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     int local = 0;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
       const int n0 = tile / p.m_tiles * p.tile_outs, t0 = tile % p.m_tiles * p.bn, tokens = min(p.bn, p.rows - t0);
-      auto write = [&](int c0, int count) {  // tokens c0 .. of the tile, whose sums are complete
-        for (int u = et; u < count * 32; u += 256) {
-          const int t = u >> 5, f = (u & 31) * 4;
-          if (f >= p.tile_outs || n0 + f >= p.outer || !ok) continue;
-          const float4* at = reinterpret_cast<const float4*>(sums + t * SIDES * 128 + f);
-          finish4<SIDES>(p, t0 + c0 + t, n0 + f, at[(SIDES - 1) * 32], at[0]);
+      auto write = [&](int c0, int count) {  // tokens c0 .. of the tile, whose sums are complete; a thread's are 8 apart
+        const int f = (et & 31) * 4;
+        if (f >= p.tile_outs || !ok) return;
+        for (int t = et >> 5; t < count; t += 32) {
+          float y[16], z[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4* at = reinterpret_cast<const float4*>(sums + min(t + 8 * i, count - 1) * SIDES * 128 + f);
+            const float4 a = at[(SIDES - 1) * 32], b = at[0];
+            y[4 * i] = a.x, y[4 * i + 1] = a.y, y[4 * i + 2] = a.z, y[4 * i + 3] = a.w;
+            z[4 * i] = b.x, z[4 * i + 1] = b.y, z[4 * i + 2] = b.z, z[4 * i + 3] = b.w;
+          }
+          finish_rows<SIDES, 4>(p, t0 + c0 + t, 8, (count - t + 7) / 8, n0 + f, y, z);
         }
       };
       // (a wait that gave up in one warp: the others would wait for it at the barrier, so it goes on, and writes nothing)
@@ -460,8 +494,9 @@ bool plan_few(LinearParams& p, int sides, int64_t tiles) {
   p.split = 1;
   while (p.split < kMostSplit && tiles * (p.split + 1) <= (two ? 256 : 128) && p.k_steps * p.per >= 4 * (p.split + 1)) ++p.split;
   const int steps = (p.k_steps + p.split - 1) / p.split, segments = (steps + p.segment_steps - 1) / p.segment_steps;
-  p.tmem_cols = tmem_columns(segments * sides * p.bn);
-  return segments * sides * p.bn <= (two ? 256 : 512);
+  const int columns = (segments - 1) * sides * p.bn + (sides * p.bn + 31) / 32 * 32;  // (they are read by 32)
+  p.tmem_cols = tmem_columns(columns);
+  return columns <= (two ? 256 : 512);
 }
 
 // Many tokens: the tile's columns so that the pairs' rounds of tiles cost least, a tile as much as its columns and 32 more.

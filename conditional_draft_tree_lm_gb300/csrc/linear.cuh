@@ -67,45 +67,63 @@ DT_DEVINL void finish(const LinearParams& p, int64_t t, int n, float product, fl
   else static_cast<__nv_bfloat16*>(p.out)[t * p.out_stride + n] = __float2bfloat16_rn(y[0]);
 }
 
-// Four neighbouring outputs from column n on (those behind the last column are left out).
-template <int SIDES>
-DT_DEVINL void finish4(const LinearParams& p, int64_t t, int n, const float4& y4, const float4& z4) {
-  float y[4] = {y4.x, y4.y, y4.z, y4.w}, z[4] = {z4.x, z4.y, z4.z, z4.w};
+// Four neighbouring outputs from column n on (those behind the last column are left out) of rows t, t + step, .. (`count` of N): the
+// product's sums y and the gate's z.  All rows step by step together: a warp's own chain of instructions is what an epilogue of few
+// warps takes its time for.
+template <int SIDES, int N>
+DT_DEVINL void finish_rows(const LinearParams& p, int64_t t, int step, int count, int n, float (&y)[4 * N], float (&z)[4 * N]) {
+  if (n >= p.outer) return;
   if (!p.wide || n + 4 > p.outer) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i < p.outer) finish<SIDES>(p, t, n + i, y[i], z[i]);
+    for (int i = 0; i < 4 * N; ++i)
+      if (i / 4 < count && n + i % 4 < p.outer) finish<SIDES>(p, t + i / 4 * step, n + i % 4, y[i], z[i]);
     return;
   }
-  if (p.bias) {
+  uint2 r[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] += bf16_to_f32(p.bias[n + i]);
+  for (int i = 0; i < N; ++i)
+    r[i] = p.residual && i < count ? *reinterpret_cast<const uint2*>(p.residual + (t + i * step) * p.residual_stride + n) : make_uint2(0, 0);
+  if (p.bias) {
+    float b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = bf16_to_f32(p.bias[n + j]);
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) y[i] += b[i % 4];
   }
   if (SIDES == 2) {
     if (p.gate_bias) {
+      float b[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) z[i] += bf16_to_f32(p.gate_bias[n + i]);
+      for (int j = 0; j < 4; ++j) b[j] = bf16_to_f32(p.gate_bias[n + j]);
+#pragma unroll
+      for (int i = 0; i < 4 * N; ++i) z[i] += b[i % 4];
     }
     activate(z, p.activation);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] *= z[i];
+    for (int i = 0; i < 4 * N; ++i) y[i] *= z[i];
   } else {
     activate(y, p.activation);
   }
   if (p.residual) {
-    const uint2 r = *reinterpret_cast<const uint2*>(p.residual + t * p.residual_stride + n);
-    y[0] += __uint_as_float(r.x << 16);
-    y[1] += __uint_as_float(r.x & 0xFFFF0000u);
-    y[2] += __uint_as_float(r.y << 16);
-    y[3] += __uint_as_float(r.y & 0xFFFF0000u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      y[4 * i] += __uint_as_float(r[i].x << 16);
+      y[4 * i + 1] += __uint_as_float(r[i].x & 0xFFFF0000u);
+      y[4 * i + 2] += __uint_as_float(r[i].y << 16);
+      y[4 * i + 3] += __uint_as_float(r[i].y & 0xFFFF0000u);
+    }
   }
-  const int64_t at = t * p.out_stride + n;
-  if (p.out_fp32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
-  } else {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(y[0], y[1]), b = __floats2bfloat162_rn(y[2], y[3]);
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i >= count) break;
+    const int64_t at = (t + i * step) * p.out_stride + n;
+    if (p.out_fp32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(y[4 * i], y[4 * i + 1]), b = __floats2bfloat162_rn(y[4 * i + 2], y[4 * i + 3]);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
   }
 }
 

@@ -18,9 +18,11 @@
 // channels, and these parts are added in fp32, rounded: in shared memory by k_stream's epilogue, from accumulators
 // beside each other by k_few.  Outputs in bf16 (half a step is 4e-3) have one accumulator over all channels.
 //
-// Bound by streaming the weights where they are many: 65 tokens' logits (2560 to 151936, fp32) 130 us, 6.1 TB/s; gated 32 tokens
-// (2560 to 2 x 10240) 22 us, 4.8 TB/s, a third of it before the first products and behind the last.  By that latency where
-// they are few: 65 tokens, 4096 to 2560 10.1 us, 2.2 TB/s.
+// Bound by streaming the weights where they are many: 65 tokens' logits (2560 to 151936, fp32) 129 us, 6.2 TB/s; gated 32 tokens
+// (2560 to 2 x 10240) 21 us, 5.0 TB/s, a quarter of it before the first products and behind the last.  By that latency where
+// they are few: 65 tokens, 4096 to 2560 10.1 us, of which the copies take 2.  Tokens by the hundred: by the operands that every SM
+// brings and by the sums of a split, which come over distributed shared memory at 18 bytes a clock (bulk copies are no faster): 200
+// tokens, 2560 to 6144 14.3 us, 256, 4096 to 4096 16.5.
 #include "linear.cuh"
 #include "cluster.cuh"
 #include "kv_flash.cuh"
@@ -29,6 +31,7 @@ namespace dt {
 namespace {
 
 constexpr int kFewThreads = 256, kMostSplit = 8;
+constexpr int kFewSmem = 222 * 1024;  // of k_few at most
 constexpr uint32_t kTileBytes = 128 * 128;  // 128 rows of 64 bf16
 
 // A step of a stage: PER blocks of 64 of the inner dimension (one copy: the map has them as a third dimension, where they
@@ -104,7 +107,7 @@ DT_DEVINL void finish_share(const LinearParams& p, const float* sums, int rank, 
 }
 
 template <int SIDES, int PER>
-__global__ void __launch_bounds__(kFewThreads, 2)
+__global__ void __launch_bounds__(kFewThreads, 1)
     k_few(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_g,
           const __grid_constant__ CUtensorMap tm_x, const LinearParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   if (ok) {
     // (32 columns of the sides' accumulators, which lie one behind the other, at a time; 16 behind the last are nobody's)
     const int quarter = warp & 3, columns = SIDES * p.bn;
-    for (int c = (warp >> 2) * 32; c < columns; c += 64) {
+    for (int c = (warp >> 2) * 32; c < columns; c += kFewThreads / 4) {
       const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c;
       uint32_t v[32];
       tmem_ld32(from, v);
@@ -480,23 +483,49 @@ void plan_stream(LinearParams& p, int sides, int64_t tiles) {
   steps_of(p, sides, 224u * 1024 - 1024 - p.sum_tokens * sides * 512);
 }
 
-// Clusters of as many CTAs as leave all of them beside each other: with one CTA an SM 128 or so are (36 clusters of 4: one
-// wave takes 32), with two 256; and with four blocks of 64 or more each.  Two CTAs an SM for up to 64 tokens, and where
-// one would leave clusters of two.  us with two and with one an SM: 4 tokens, 2560 to 6144 9.4 (4 CTAs a cluster) and 10.0 (2);
-// 16, 4096 to 2560 8.5 (8) and 8.7 (4); 65, 4096 to 2560 10.6 and 9.9 (6); 65, 2560 to 6144 11.8 (5) and 12.3 (2); 128, 4096 to
-// 4096 14.8 and 13.1 (4).
+// How many clusters of k_few stand beside each other, a CTA an SM: a property of the device (GPCs differ in their SMs), asked for
+// once.  (Here 76 of 2, 46, 36, 28, 23, 15, 15 of 8.)
+int clusters_beside(int size) {
+  static std::atomic<int> known[64][kMostSplit + 1];  // 0: not asked for yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::atomic<int>* at = dev < 64 ? &known[dev][size] : nullptr;
+  int n = at ? at->load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = kFewSmem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(k_few<1, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, k_few<1, 1>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (at) at->store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Clusters of as many CTAs as leave all of them beside each other, with four blocks of 64 or more each.  A CTA has an SM with all its
+// shared memory: two an SM, in clusters twice as large, were ahead up to 4 tokens only (2560 to 6144 9.2 us, one 9.5; 16 tokens the same;
+// 65 tokens, 4096 to 2560 13.0, one 10.1).
 // False where there are too few accumulators for outputs in 32 bits.
 bool plan_few(LinearParams& p, int sides, int64_t tiles) {
   p.tile_outs = 128;
   p.n_tiles = (p.outer + 127) / 128;
-  const bool two = sides * p.bn <= 64 || (sides * p.bn <= 128 && 3 * tiles > 128);
-  steps_of(p, sides, two ? 110u * 1024 : 220u * 1024);
+  steps_of(p, sides, kFewSmem - 2048);
   p.split = 1;
-  while (p.split < kMostSplit && tiles * (p.split + 1) <= (two ? 256 : 128) && p.k_steps * p.per >= 4 * (p.split + 1)) ++p.split;
+  for (int n = 2; n <= kMostSplit && p.k_steps * p.per >= 4 * n; ++n)
+    if (tiles <= clusters_beside(n)) p.split = n;
   const int steps = (p.k_steps + p.split - 1) / p.split, segments = (steps + p.segment_steps - 1) / p.segment_steps;
   const int columns = (segments - 1) * sides * p.bn + (sides * p.bn + 31) / 32 * 32;  // (they are read by 32)
   p.tmem_cols = tmem_columns(columns);
-  return columns <= (two ? 256 : 512);
+  return columns <= 512;
 }
 
 // Many tokens: the tile's columns so that the pairs' rounds of tiles cost least, a tile as much as its columns and 32 more.
@@ -588,7 +617,8 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
     plan_tokens(p, sides);
     const int64_t tiles = static_cast<int64_t>((a.outer + 127) / 128) * p.m_tiles;
     if (tiles > (1 << 29)) return kv_fail(DT_ERR_SHAPE, "%s: more than 2^29 tiles", who);
-    // (clusters where tiles leave half of the SMs without one)
+    // Clusters where tiles leave half of the SMs without one.  us by clusters and by persistent CTAs: 65 tokens, 2560 to 6144 10.7 and 12.1,
+    // to 8192 12.1 and 12.6, to 9728 13.4 and 13.4; 200 tokens 14.4 and 17.7, 15.7 and 18.3, 18.0 and 18.9.
     stream_tiles = tiles >= kSms / 2 || !plan_few(p, sides, tiles);
     if (stream_tiles) plan_stream(p, sides, tiles);
   }

@@ -266,17 +266,33 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tiles = p.n_tiles * p.m_tiles;  // (m_tiles: of tokens)
   const uint32_t tile_bytes = p.tile_outs * 128u, side_bytes = PER * tile_bytes, acc_cols = SIDES * p.bn;
-  if (tid == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+  const uint64_t keep = l2_policy_evict_last(), stream = p.m_tiles == 1 ? l2_policy_evict_first() : keep;
+  auto load = [&](int tile, int ks, uint32_t stage) {
+    const int n0 = tile / p.m_tiles * p.tile_outs, t0 = tile % p.m_tiles * p.bn;
+    uint8_t* at = smem + stage * p.stage_bytes;
+    mbar_arrive_expect_tx(&full[stage], p.stage_bytes);
+    if (SIDES == 2) load_step<PER>(at, tm_g, &full[stage], ks, n0, stream);
+    load_step<PER>(at + (SIDES - 1) * side_bytes, tm_w, &full[stage], ks, n0, stream);
+    load_step<PER>(at + SIDES * side_bytes, tm_x, &full[stage], ks, t0, keep);
+  };
+  // the first loads are under way before tensor memory is asked for
+  const int ahead = min(p.stages, p.k_steps);
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int s = 0; s < p.stages; ++s) {
+        mbar_init(&full[s], 1);
+        mbar_init(&empty[s], 1);
+      }
+      for (int a = 0; a < 2; ++a) {
+        mbar_init(&tfull[a], 1);
+        mbar_init(&tempty[a], kStreamWarps);
+      }
+      mbar_init(drained, 1);
+      fence_mbar_init();
+      dt_grid_wait();
+      for (int s = 0; s < ahead; ++s) load(blockIdx.x, s, s);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], kStreamWarps);
-    }
-    mbar_init(drained, 1);
-    fence_mbar_init();
+    __syncwarp();
   }
   dt_grid_wait();
   if (warp == 1) tmem_alloc(tmem_slot, p.tmem_cols);
@@ -287,24 +303,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   bool ok = true;
 
   if (warp == 0) {
-    const uint64_t keep = l2_policy_evict_last(), stream = p.m_tiles == 1 ? l2_policy_evict_first() : keep;
-    uint32_t stage = 0, phase = 0;
-    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-      const int n0 = tile / p.m_tiles * p.tile_outs, t0 = tile % p.m_tiles * p.bn;
-      for (int ks = 0; ks < p.k_steps; ++ks) {
+    uint32_t stage = ahead == p.stages ? 0 : ahead, phase = ahead == p.stages;
+    int begun = ahead;  // steps of the first tile
+    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, begun = 0)
+      for (int ks = begun; ks < p.k_steps; ++ks) {
         ok = warp_wait(&empty[stage], phase ^ 1u);
         if (!ok) break;
-        if (elect_one()) {
-          uint8_t* at = smem + stage * p.stage_bytes;
-          mbar_arrive_expect_tx(&full[stage], p.stage_bytes);
-          if (SIDES == 2) load_step<PER>(at, tm_g, &full[stage], ks, n0, stream);
-          load_step<PER>(at + (SIDES - 1) * side_bytes, tm_w, &full[stage], ks, n0, stream);
-          load_step<PER>(at + SIDES * side_bytes, tm_x, &full[stage], ks, t0, keep);
-        }
+        if (elect_one()) load(tile, ks, stage);
         __syncwarp();
         if (++stage == static_cast<uint32_t>(p.stages)) stage = 0, phase ^= 1u;
       }
-    }
     // no copy may outlive the CTA, whichever wait gave up
     for (uint32_t s = 0; s < static_cast<uint32_t>(p.stages); ++s) mbar_wait(&full[s], s < stage ? phase : phase ^ 1u, nullptr);
   } else if (warp == 1) {

@@ -4,9 +4,10 @@
 // all warps read, from L1.  Where there are enough rows of weight to keep 16 warps an SM busy, a warp has two of them (with
 // a gate one, and the gate's); else the four warps of a CTA share the inner dimension of four rows, so that few rows
 // keep as many bytes in flight as many do.  Products are added in pairs of channels (fma.rn.f32x2), then over lanes
-// and warps.  us by a warp alone, by four and by the tensor-core kernel for few tokens, one token: 2560 to 6144 7.2, 8.0, 9.6;
-// 4096 to 2560 7.9, 5.6, 8.5; 10240 to 2560 16.7, 10.6, 14.1; 2560 to 2 x 10240 17.8, 19.2, 26.0; two tokens: 7.8, 9.5, 9.6;
-// 8.5, 6.0, 8.6; 17.6, 11.3, 14.3; 21.6, 22.5, 25.9; with three, products and the tokens' reads take over: 11.4, 10.4, 9.6.
+// and warps.  us by a warp alone, by four and by the
+// tensor-core kernels for few tokens, one token: 2560 to 6144 7.2, 8.0, 9.6; 4096 to 2560 7.9, 5.6, 8.1; 10240 to 2560 16.7, 10.6, 12.9;
+// 2560 to 2 x 10240 18.6, 19.2, 20.7; two tokens: 8.0, 9.5, 9.5; 8.5, 5.9, 8.1; 17.6, 10.8, 13.0; 20.7, 22.5, 21.0; with three, products and
+// the tokens' reads take over: 2560 to 6144 11.4, 10.4, 9.2.
 // Bound by streaming the weights once; no tensor memory, barrier or cluster stands before the first byte.
 #include "linear.cuh"
 #include "kv_flash.cuh"

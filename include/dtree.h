@@ -580,7 +580,8 @@ dt_status dt_prompt_attention(const dt_prompt_attention_args* args, void* stream
  * anywhere, and out may be the residual itself (bf16, same address and stride), but
  * must not overlap another input, nor its rows one another (refused; columns of a
  * tensor that holds an input in others of its columns do not overlap it).  Sums are in fp32,
- * in an order that depends on the sizes only: the same call gives the same bits.
+ * in an order that depends on sizes, types and the device only: the same call
+ * gives the same bits.
  * rows 0: nothing is done.  One launch.  status: [1] int32 device or NULL;
  * DT_KV_TIMEOUT is or'ed in. */
 typedef struct dt_linear_args {

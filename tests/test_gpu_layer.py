@@ -694,3 +694,39 @@ def test_calls_that_follow_one_another_see_what_was_written(rows, inner):
             graph.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("rows,outer", [(1, 1024), (20, 1024), (65, 10240), (300, 1024)])
+def test_a_call_behind_another_streams_late_event_waits_for_it(rows, outer):
+    """The kernel before the call in its own stream is long done, and is one of the same kind; what the call reads comes late from another."""
+    torch = _t()
+    from conditional_draft_tree_lm_gb300 import Rotary, linear, qk_norm_rope, token_logprobs
+    rs = np.random.RandomState(rows)
+    x, w = bf16(rs, rows, 1024), bf16(rs, outer, 1024, scale=0.03)
+    late, rotary, side = torch.zeros_like(x), Rotary(128), torch.cuda.Stream()
+    heads = late.view(rows, 8, 128)
+    calls = [lambda: linear(late, w), lambda: qk_norm_rope(heads, rotary=rotary)[0], lambda: token_logprobs(late, top=4)["top_logp"]]
+
+    def run(call):
+        late.zero_()
+        call()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(400_000)
+            late.copy_(x)
+        torch.cuda.current_stream().wait_stream(side)
+        return call()
+
+    for call in calls:
+        late.copy_(x)
+        want = call().clone()
+        for _ in range(3):
+            assert torch.equal(run(call), want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = run(call)
+        for _ in range(3):
+            got.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)

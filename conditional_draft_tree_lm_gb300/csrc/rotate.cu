@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(kRotateThreads, ROWS == 1 ? 3 : 2) k_rotate(co
   const int nth = p.at_once == 1 ? 0 : unit / p.heads, h = blockIdx.y * p.heads + unit - nth * p.heads;  // row beside the others, head
   const bool key = h >= a.n_q, turns = part < p.pairs;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (ROWS * p.at_once), row0 = first + nth;
-  const bool holds = part < p.lanes && nth < p.at_once && h < a.n_q + a.n_kv;
+  // (units behind the CTA's own, with which its last warp is filled, have nothing: their heads are the next CTA's)
+  const bool holds = part < p.lanes && unit < p.heads * p.at_once && h < a.n_q + a.n_kv;
   const int left_rows = holds ? static_cast<int>(min(static_cast<int64_t>(ROWS * p.at_once), p.rows - row0)) : 0;  // row r is there where r at_once < left_rows
   const int at0 = !INTERLEAVED && turns ? 8 * part : 16 * part, apart = !INTERLEAVED && turns ? a.rot / 2 : 8;
   const __nv_bfloat16* weight = static_cast<const __nv_bfloat16*>(key ? a.k_weight : a.q_weight);

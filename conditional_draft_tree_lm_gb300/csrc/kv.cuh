@@ -114,7 +114,8 @@ cudaError_t once_a_device(std::atomic<uint64_t>& done, Set set) {
 }
 
 // A launch that may begin while the kernel before it in the stream ends: every thread of the kernel calls dt_grid_wait before it
-// touches memory that others use.  us without and with it, back to back in a graph: rotation of 32 rows 2.8 and 2.1, of 2080 12.3 and
+// touches memory that others use, and reads it by ordinary loads or copies (read-only loads are for memory that nobody writes while the
+// kernel runs, and this one runs already while the one before it writes).  us without and with it, back to back in a graph: rotation of 32 rows 2.8 and 2.1, of 2080 12.3 and
 // 11.6; 32 tokens gated 23.4 and 22.7; 2080 tokens 34.4 and 33.8.
 template <class... P, class... A>
 cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, unsigned cluster, const A&... args) {

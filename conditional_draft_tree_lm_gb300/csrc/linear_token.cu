@@ -19,6 +19,13 @@ constexpr int kTokenThreads = 128, kTokenWarps = kTokenThreads / 32;
 
 DT_DEVINL uint64_t pair_of(uint32_t w) { return f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
 
+// 16 bytes that are read once.  (volatile: no load may be moved before dt_grid_wait)
+DT_DEVINL uint4 stream16(const uint4* at) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at) : "memory");
+  return v;
+}
+
 struct TokenOperands {
   const uint16_t* x;
   const uint16_t* w;
@@ -56,13 +63,13 @@ __global__ void __launch_bounds__(kTokenThreads) k_token(const TokenOperands o, 
     for (int u = 0; u < AHEAD; ++u)
 #pragma unroll
       for (int r = 0; r < kStreams; ++r)
-        if (k + STEP * u < pieces) w[u][r] = __ldcs(row[r] + k + STEP * u);
+        if (k + STEP * u < pieces) w[u][r] = stream16(row[r] + k + STEP * u);
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
       if (k + STEP * u >= pieces) break;
       uint4 x[T];
 #pragma unroll
-      for (int t = 0; t < T; ++t) x[t] = __ldg(reinterpret_cast<const uint4*>(o.x + t * o.x_stride) + k + STEP * u);
+      for (int t = 0; t < T; ++t) x[t] = reinterpret_cast<const uint4*>(o.x + t * o.x_stride)[k + STEP * u];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint64_t x2[T];

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kLogpThreads, 1024 / kLogpThreads) k_logp(cons
   const int lo = min(vocab, part * p.chunk), hi = min(vocab, lo + p.chunk);
   const char* x = static_cast<const char*>(p.a.logits) + row * p.a.logits_row_stride * kBytes;
   auto load = [&](int i) -> float {
-    return BF16 ? bf16_to_f32(__ldg(reinterpret_cast<const uint16_t*>(x) + i)) : __ldg(reinterpret_cast<const float*>(x) + i);
+    return BF16 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(x)[i]) : reinterpret_cast<const float*>(x)[i];
   };
   // the part's logits: `head` up to a 16-byte boundary, `vecs` pieces of 16 bytes, the rest
   const int to_edge = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(x) + static_cast<int64_t>(lo) * kBytes) % 16u) % 16u) / kBytes;
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kLogpThreads, 1024 / kLogpThreads) k_logp(cons
         for (int u = 0; u < 4; ++u) {
           here[u] = begin[u] + from * kLogpThreads;
           if (begin[u] < 0 || from >= stretch * kVecs || here[u] >= vecs) here[u] = -1;
-          piece[u] = here[u] < 0 ? make_uint4(0, 0, 0, 0) : __ldg(vec + here[u]);
+          piece[u] = here[u] < 0 ? make_uint4(0, 0, 0, 0) : vec[here[u]];
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kLogpThreads, 1024 / kLogpThreads) k_logp(cons
     for (int at = warp * 32; n < top && tau == 0 && at < vecs; at += kLogpThreads) {
       const bool there = at + lane < vecs;
       float v[kElems];
-      unpack(there ? __ldg(vec + at + lane) : make_uint4(0, 0, 0, 0), v);
+      unpack(there ? vec[at + lane] : make_uint4(0, 0, 0, 0), v);
       uint32_t mask = 0;
 #pragma unroll
       for (int i = 0; i < kElems; ++i) mask |= (v[i] == -INFINITY ? 1u : 0u) << i;

@@ -30,10 +30,22 @@ DT_DEVINL float peer_ld(uint32_t a) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
 }
+DT_DEVINL uint32_t peer_ld_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
 DT_DEVINL uint64_t peer_ld_u64(uint32_t a) {
   uint64_t v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
+}
+
+// What a warp whose wait gave up has to tell the cluster's other CTAs: a word of shared memory, 0 at first, that it sets before the
+// cluster's barrier.  Behind it, in every lane of a warp, not 0 in one of them where any of the `ctas` has set its own.
+DT_DEVINL uint32_t gave_up_beside(const uint32_t* word, int ctas) {
+  const uint32_t lane = threadIdx.x & 31u;
+  return ctas == 1 ? *const_cast<const volatile uint32_t*>(word) : lane < static_cast<uint32_t>(ctas) ? peer_ld_u32(peer_addr(word, lane)) : 0u;
 }
 
 // Whether a phase is complete, without waiting (try_wait may hold the thread for microseconds).

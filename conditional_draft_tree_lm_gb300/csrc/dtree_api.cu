@@ -959,7 +959,7 @@ dt_status dt_build_round_host(dt_ctx* c, const void* H_host, const int32_t* root
 }
 
 dt_status dt_check_bounded_waits(dt_ctx* c, int which, void* stream) {
-  if (!c || (which != 0 && which != 1)) return DT_ERR_INVALID_ARG;
+  if (!c || which < 0 || which > 2) return DT_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   unsigned* bar = c->at<unsigned>(c->lay.bar);
   DT_TRY(cudaMemsetAsync(bar, 0, sizeof(unsigned), st));

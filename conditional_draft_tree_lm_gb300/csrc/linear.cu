@@ -70,11 +70,14 @@ DT_HOST_DEVICE_INLINE uint32_t few_bars(const LinearParams& p, int sides) {
 
 // A CTA's share of a tile: four neighbouring rows of weight for a token at a time, their sums over the cluster's CTAs.  A thread's
 // units are 8 tokens apart, of the same rows; the reads of several are on their way together.  RANKS: the cluster's CTAs at most.
+// gave_up: a wait of one of them gave up, so that sums are missing and nothing of the tile is written (looked at once the sums are here,
+// since both come from the peers' memory).
 template <int SIDES, int RANKS>
-DT_DEVINL void finish_share(const LinearParams& p, const float* sums, int rank, int tokens, int t0, int n0) {
+DT_DEVINL void finish_share(const LinearParams& p, const float* sums, const uint32_t* gave_up, int rank, int tokens, int t0, int n0) {
   constexpr int kFit = 16 / (RANKS * SIDES), kUnits = kFit > 4 ? 4 : kFit < 1 ? 1 : kFit, kStep = kFewThreads / 32;
   // (whole tokens)
   const int first = tokens * rank / p.split, end = tokens * (rank + 1) / p.split, f = (threadIdx.x & 31) * 4;
+  const uint32_t lost = gave_up_beside(gave_up, RANKS == 1 ? 1 : p.split);
   for (int t = first + static_cast<int>(threadIdx.x >> 5); t < end; t += kUnits * kStep) {
     float4 v[kUnits][SIDES][RANKS];
 #pragma unroll
@@ -90,6 +93,7 @@ DT_DEVINL void finish_share(const LinearParams& p, const float* sums, int rank, 
         for (int r = 0; r < RANKS; ++r)
           if (r < p.split) v[i][s][r] = peer_ld4(peer_addr(at, r));
       }
+    if (__any_sync(0xFFFFFFFFu, lost != 0)) return;
     float y[4 * kUnits], z[4 * kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
@@ -117,6 +121,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   uint64_t* done = empty + p.stages;
   uint64_t* drained = done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+  uint32_t* gave_up = tmem_slot + 1;  // (a wait of a warp)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(blockIdx.x) % p.split, tile = static_cast<int>(blockIdx.x) / p.split;
@@ -142,6 +147,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
       mbar_init(done, 1);
       mbar_init(drained, 1);
+      *gave_up = 0;
       fence_mbar_init();
       dt_grid_wait();
       for (int s = 0; s < ahead; ++s) load(ks0 + s, s);
@@ -225,8 +231,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           for (int j = 0; j < 16; ++j) to[j * SIDES * 128] = __uint_as_float(v[16 * h + j]);
       }
     }
-  } else if (p.status && lane == 0) {
-    atomicOr(p.status, DT_KV_TIMEOUT);
+  } else if (lane == 0) {
+    *gave_up = 1;
+    if (p.status) atomicOr(p.status, DT_KV_TIMEOUT);
   }
   tc_fence_before();
   __syncthreads();
@@ -236,10 +243,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
   __syncwarp();
   if (p.split > 1) cluster_barrier();
-  if (p.split == 1) finish_share<SIDES, 1>(p, sums, rank, tokens, t0, n0);
-  else if (p.split == 2) finish_share<SIDES, 2>(p, sums, rank, tokens, t0, n0);
-  else if (p.split <= 4) finish_share<SIDES, 4>(p, sums, rank, tokens, t0, n0);
-  else finish_share<SIDES, kMostSplit>(p, sums, rank, tokens, t0, n0);
+  if (p.split == 1) finish_share<SIDES, 1>(p, sums, gave_up, rank, tokens, t0, n0);
+  else if (p.split == 2) finish_share<SIDES, 2>(p, sums, gave_up, rank, tokens, t0, n0);
+  else if (p.split <= 4) finish_share<SIDES, 4>(p, sums, gave_up, rank, tokens, t0, n0);
+  else finish_share<SIDES, kMostSplit>(p, sums, gave_up, rank, tokens, t0, n0);
   if (p.split > 1) cluster_barrier();  // (no CTA leaves while its sums are read)
 }
 
@@ -353,6 +360,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   } else if (warp >= 4) {
     const int quarter = warp & 3, half = (warp - 4) >> 2, et = tid - 128;
     auto together = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    // the warps' common verdict: what a wait of one of them has missed is in the outputs of all
+    auto all_together = [](bool mine) {
+      uint32_t r;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(r)
+          : "r"(static_cast<uint32_t>(mine))
+          : "memory");
+      return r != 0;
+    };
     static_assert(kStreamWarps * 32 == 256, "");
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     // 16 tokens from column c of an accumulator on, to or onto the sums from token `at` on
@@ -391,7 +408,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           finish_rows<SIDES, 4>(p, t0 + c0 + t, 8, (count - t + 7) / 8, n0 + f, y, z);
         }
       };
-      // (a wait that gave up in one warp: the others would wait for it at the barrier, so it goes on, and writes nothing)
+      // (a wait that gave up in one warp: the others would wait for it at the barrier, so it goes on, and none of them writes)
       if (p.segment_steps < p.k_steps) {  // all tokens' sums, part by part
         for (int ks = 0; ks < p.k_steps; ks += p.segment_steps, ++local) {
           ok = ok && warp_wait(&tfull[local & 1], local >> 1 & 1);
@@ -399,7 +416,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           for (int c = 16 * half; c < p.bn && ok; c += 32) take(local & 1, c, c, ks > 0);
           give_back(local & 1);
         }
-        together();
+        ok = all_together(ok);
         write(0, tokens);
         together();
       } else {  // 32 tokens after 32
@@ -409,7 +426,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         for (int c0 = 0; c0 < tokens; c0 += 32) {
           if (c0 + 16 * half < p.bn && ok) take(acc, c0 + 16 * half, 16 * half, false);
           if (c0 + 32 >= tokens) give_back(acc);
-          together();
+          ok = all_together(ok);
           write(c0, min(32, tokens - c0));
           together();
         }

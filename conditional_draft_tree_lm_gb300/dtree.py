@@ -364,8 +364,9 @@ class DraftTreeBuilder:
 
     def check_bounded_waits(self, which: int, stream=None):
         """Launch the bounded-wait self-check (0: grid barrier with a missing
-        participant, 1: an mbarrier nothing arrives on); read the outcome with
-        device_status()."""
+        participant, 1: an mbarrier nothing arrives on, 2: such an mbarrier
+        in one CTA of a cluster, another of which records it); read the
+        outcome with device_status()."""
         _check(self.lib.dt_check_bounded_waits(self.ctx, int(which), _stream(stream)), "dt_check_bounded_waits")
 
     def device_status(self) -> int:

@@ -583,7 +583,8 @@ dt_status dt_prompt_attention(const dt_prompt_attention_args* args, void* stream
  * in an order that depends on sizes, types and the device only: the same call
  * gives the same bits.
  * rows 0: nothing is done.  One launch.  status: [1] int32 device or NULL;
- * DT_KV_TIMEOUT is or'ed in. */
+ * DT_KV_TIMEOUT is or'ed in where a wait gave up, and the outputs that stood
+ * behind it are left as they were. */
 typedef struct dt_linear_args {
   int64_t rows; /* 0..2^31-257 */
   int inner;    /* multiple of 8, >= 8 */
@@ -685,7 +686,8 @@ dt_status dt_get_device_status(dt_ctx* ctx);
 
 /* Self-check of the bounded device-side waits, on the context's status word:
  * which = 0 launches a grid barrier of two CTAs that one CTA never reaches,
- * which = 1 a wait on an mbarrier phase that nothing completes.  The waiting
+ * which = 1 a wait on an mbarrier phase that nothing completes, which = 2 such
+ * a wait in one CTA of a cluster, which another one records.  The waiting
  * thread gives up after the wait limit (2 s), records the timeout and returns;
  * dt_get_device_status then returns DT_ERR_TIMEOUT and the context stays
  * usable.  Returns DT_ERR_INVALID_ARG for another `which`.

@@ -212,7 +212,12 @@ extern "C" dt_status dt_qk_norm_rope(const dt_qk_norm_rope_args* args, void* str
   };
   const Heads q = {a.q, a.n_q, a.q_row_stride, a.q_head_stride}, q_out = {a.q_out, a.n_q, a.q_out_row_stride, a.q_out_head_stride};
   const Heads k = {a.k, a.n_kv, a.k_row_stride, a.k_head_stride}, k_out = {a.k_out, a.n_kv, a.k_out_row_stride, a.k_out_head_stride};
-  if ((!same(q, q_out) && meet(q, q_out)) || (a.k && ((!same(k, k_out) && meet(k, k_out)) || meet(q, k_out) || meet(k, q_out) || meet(q_out, k_out))))
+  auto over = [&](const void* d, int64_t bytes) {  // whether what is written lies over d
+    const MemoryRows r = {reinterpret_cast<uintptr_t>(d), 1, 0, bytes};
+    return d && (rows_meet(in_memory(q_out), r) || (a.k && rows_meet(in_memory(k_out), r)));
+  };
+  if ((!same(q, q_out) && meet(q, q_out)) || (a.k && ((!same(k, k_out) && meet(k, k_out)) || meet(q, k_out) || meet(k, q_out) || meet(q_out, k_out))) ||
+      over(a.q_weight, 2 * a.head_dim) || over(a.k_weight, 2 * a.head_dim) || over(a.turns, 4 * a.rot) || over(a.positions, 4 * rows) || over(a.base, 4 * static_cast<int64_t>(a.n_req)))
     return kv_fail(DT_ERR_INVALID_ARG, "%s: q_out or k_out overlaps another tensor and is not q or k itself", who);
   RotateParams p = {};
   p.a = a;

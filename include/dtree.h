@@ -621,7 +621,7 @@ dt_status dt_linear(const dt_linear_args* args, void* stream);
  *   (base ? base[q] : 0) + (positions ? positions[row] : a).
  * Rows whose positions[row] is negative (as dt_kv_plan leaves behind the last token) are
  * not written.  Rows of heads as above; q_out may be q and k_out k (same
- * strides), other overlaps are refused.  k NULL: queries only.  n_req or
+ * strides), other overlaps of what is written are refused.  k NULL: queries only.  n_req or
  * slots 0: nothing is done.  One launch. */
 typedef struct dt_qk_norm_rope_args {
   int n_req, slots; /* n_req * slots at most 2^31-1 */

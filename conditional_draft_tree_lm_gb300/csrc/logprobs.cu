@@ -453,6 +453,17 @@ extern "C" dt_status dt_token_logprobs(const dt_token_logprobs_args* args, void*
     return kv_fail(DT_ERR_INVALID_ARG, "%s: null or misaligned logits", who);
   if ((a.n_tokens && (!a.tokens || !a.logp)) || (a.n_top && (!a.top_tok || !a.top_logp)))
     return kv_fail(DT_ERR_INVALID_ARG, "%s: null tokens, logp, top_tok or top_logp", who);
+  const int64_t item = a.logits_bf16 ? 2 : 4;
+  auto flat = [](const void* d, int64_t count) { return MemoryRows{reinterpret_cast<uintptr_t>(d), 1, 0, 4 * count}; };
+  const MemoryRows read[2] = {{reinterpret_cast<uintptr_t>(a.logits), a.rows, a.logits_row_stride * item, a.vocab * item}, flat(a.tokens, a.rows * a.n_tokens)};
+  const MemoryRows written[6] = {flat(a.logp, a.rows * a.n_tokens), flat(a.lse, a.rows), flat(a.entropy, a.rows), flat(a.top_tok, a.rows * a.n_top),
+                                 flat(a.top_logp, a.rows * a.n_top), flat(a.status, 1)};
+  for (int i = 0; i < 6; ++i) {
+    if (!written[i].at || !written[i].width) continue;
+    bool meets = rows_meet(written[i], read[0]) || (a.n_tokens && rows_meet(written[i], read[1]));
+    for (int j = 0; j < i; ++j) meets = meets || (written[j].at && written[j].width && rows_meet(written[i], written[j]));
+    if (meets) return kv_fail(DT_ERR_INVALID_ARG, "%s: an output overlaps logits, tokens or another output", who);
+  }
   LogpParams p = {};
   p.a = a;
   p.c = static_cast<float>(1.4426950408889634 / a.temperature);

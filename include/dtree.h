@@ -660,7 +660,8 @@ dt_status dt_qk_norm_rope(const dt_qk_norm_rope_args* args, void* stream);
  * nothing and gives 0 (dt_accept_walk pads its paths with -1); one at vocab or above gives
  * NaN and sets DT_KV_BAD_INDEX in status.
  * logits [rows, vocab] fp32 or bf16, the row stride in elements and any, the
- * address aligned to its elements.  rows 0: nothing is done.  One launch. */
+ * address aligned to its elements.  What is written must not overlap logits,
+ * tokens or one another (refused).  rows 0: nothing is done.  One launch. */
 typedef struct dt_token_logprobs_args {
   int64_t rows;    /* 0..2^26 */
   int vocab;       /* 1..2^30 */

@@ -11,3 +11,15 @@ def test_qk_norm_rope_refuses_outputs_over_what_else_it_reads(lib, kw):  # noqa:
     a = dict(q=8192, k=16384, turns=32768, q_out=65536, k_out=131072)
     err, msg = call(lib, "dt_qk_norm_rope", rotate_args(**{**a, **kw}))
     assert err == INVALID and "overlaps another tensor" in msg
+
+
+OUTPUTS = dict(logp=65536, lse=66048, entropy=66560, top_tok=67072, top_logp=67584)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lse=8192), dict(entropy=8192 + 796), dict(logp=8192 - 4), dict(top_tok=8192 + 400), dict(top_logp=8192 + 784), dict(logp=32768), dict(lse=32768 + 4),
+    dict(lse=66560), dict(entropy=66048 + 4), dict(top_tok=65536), dict(top_logp=67072 + 12), dict(status=66048), dict(status=8192 + 4),
+    dict(logits_row_stride=200, lse=8192 + 396), dict(logits_row_stride=0, entropy=8192 + 4)])
+def test_token_logprobs_refuses_outputs_over_its_inputs_or_one_another(lib, kw):  # noqa: F811
+    err, msg = call(lib, "dt_token_logprobs", logp_args(**{**dict(logits=8192, tokens=32768), **OUTPUTS, **kw}))
+    assert err == INVALID and "overlaps" in msg

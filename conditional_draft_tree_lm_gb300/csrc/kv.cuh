@@ -137,6 +137,12 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t s
 
 inline bool kv_page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 
+// Whether all of them (some may be NULL) are multiples of `n`, a power of two.
+template <class... P>
+bool kv_aligned(uintptr_t n, const P*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & (n - 1)) == 0;
+}
+
 // Rows of heads: 16-byte aligned base, strides that keep every head 16-byte aligned.
 inline bool kv_rows_ok(const void* p, int64_t row_stride, int64_t head_stride) {
   return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && row_stride >= 0 && head_stride >= 0 &&

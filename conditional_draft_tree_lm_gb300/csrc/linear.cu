@@ -601,8 +601,8 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
   const uintptr_t out = reinterpret_cast<uintptr_t>(a.out), bytes = a.out_fp32 ? 4 : 2;
   if (!a.out || out % bytes != 0 || (a.rows > 1 && a.out_row_stride < a.outer))
     return kv_fail(DT_ERR_INVALID_ARG, "%s: out is null or misaligned, or its rows overlap", who);
-  if (((reinterpret_cast<uintptr_t>(a.residual) | reinterpret_cast<uintptr_t>(a.bias) | reinterpret_cast<uintptr_t>(a.gate_bias)) & 1u) != 0)
-    return kv_fail(DT_ERR_INVALID_ARG, "%s: misaligned residual or bias", who);
+  if (!kv_aligned(2, a.residual, a.bias, a.gate_bias) || !kv_aligned(4, a.status))
+    return kv_fail(DT_ERR_INVALID_ARG, "%s: misaligned residual, bias or status", who);
   const MemoryRows to = {out, a.rows, a.out_row_stride * static_cast<int64_t>(bytes), a.outer * static_cast<int64_t>(bytes)};
   auto meets = [&](const void* d, int64_t rows, int64_t stride, int64_t width) {
     return d && rows_meet(to, {reinterpret_cast<uintptr_t>(d), rows, stride * 2, width * 2});
@@ -610,7 +610,7 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
   const bool in_place = a.residual == a.out && !a.out_fp32 && (a.rows == 1 || a.residual_row_stride == a.out_row_stride);
   if (meets(a.x, a.rows, a.x_row_stride, a.inner) || meets(a.weight, a.outer, a.weight_row_stride, a.inner) ||
       meets(a.gate, a.outer, a.gate_row_stride, a.inner) || (!in_place && meets(a.residual, a.rows, a.residual_row_stride, a.outer)) ||
-      meets(a.bias, 1, 0, a.outer) || meets(a.gate_bias, 1, 0, a.outer))
+      meets(a.bias, 1, 0, a.outer) || meets(a.gate_bias, 1, 0, a.outer) || meets(a.status, 1, 0, 2))
     return kv_fail(DT_ERR_INVALID_ARG, "%s: out overlaps an input and is not the residual itself", who);
   LinearParams p = {};
   p.bias = static_cast<const uint16_t*>(a.bias);

@@ -453,6 +453,8 @@ extern "C" dt_status dt_token_logprobs(const dt_token_logprobs_args* args, void*
     return kv_fail(DT_ERR_INVALID_ARG, "%s: null or misaligned logits", who);
   if ((a.n_tokens && (!a.tokens || !a.logp)) || (a.n_top && (!a.top_tok || !a.top_logp)))
     return kv_fail(DT_ERR_INVALID_ARG, "%s: null tokens, logp, top_tok or top_logp", who);
+  if (!kv_aligned(4, a.tokens, a.logp, a.lse, a.entropy, a.top_tok, a.top_logp, a.status))
+    return kv_fail(DT_ERR_INVALID_ARG, "%s: misaligned tokens, logp, lse, entropy, top_tok, top_logp or status", who);
   const int64_t item = a.logits_bf16 ? 2 : 4;
   auto flat = [](const void* d, int64_t count) { return MemoryRows{reinterpret_cast<uintptr_t>(d), 1, 0, 4 * count}; };
   const MemoryRows read[2] = {{reinterpret_cast<uintptr_t>(a.logits), a.rows, a.logits_row_stride * item, a.vocab * item}, flat(a.tokens, a.rows * a.n_tokens)};

@@ -189,9 +189,8 @@ extern "C" dt_status dt_qk_norm_rope(const dt_qk_norm_rope_args* args, void* str
   if (!kv_rows_ok(a.q, a.q_row_stride, a.q_head_stride) || !kv_rows_ok(a.q_out, a.q_out_row_stride, a.q_out_head_stride) ||
       (a.k && (!kv_rows_ok(a.k, a.k_row_stride, a.k_head_stride) || !kv_rows_ok(a.k_out, a.k_out_row_stride, a.k_out_head_stride))))
     return kv_fail(DT_ERR_INVALID_ARG, "%s: null or misaligned q, k, q_out or k_out", who);
-  if (((reinterpret_cast<uintptr_t>(a.q_weight) | reinterpret_cast<uintptr_t>(a.k_weight)) & 15u) != 0 ||
-      (reinterpret_cast<uintptr_t>(a.turns) & 7u) != 0)
-    return kv_fail(DT_ERR_INVALID_ARG, "%s: misaligned weights or turns", who);
+  if (!kv_aligned(16, a.q_weight, a.k_weight) || !kv_aligned(8, a.turns) || !kv_aligned(4, a.positions, a.base))
+    return kv_fail(DT_ERR_INVALID_ARG, "%s: misaligned weights, turns, positions or base", who);
   if (!kv_rows_apart(rows, a.n_q, a.head_dim, a.q_out_row_stride, a.q_out_head_stride) ||
       (a.k && !kv_rows_apart(rows, a.n_kv, a.head_dim, a.k_out_row_stride, a.k_out_head_stride)))
     return kv_fail(DT_ERR_INVALID_ARG, "%s: rows of q_out or k_out overlap", who);

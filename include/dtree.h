@@ -560,6 +560,8 @@ dt_status dt_prompt_attention(const dt_prompt_attention_args* args, void* stream
  *   dt_linear          the output head, logits in fp32 (dt_accept_walk's input)
  *   dt_token_logprobs  log probabilities of given tokens
  * Activations and weights are bf16, sums fp32, one rounding at the end.
+ * Addresses are aligned to their elements where nothing more is asked for
+ * (refused otherwise).
  * ------------------------------------------------------------------------ */
 
 /* Activations of dt_linear. */
@@ -576,8 +578,9 @@ dt_status dt_prompt_attention(const dt_prompt_attention_args* args, void* stream
  * x [rows, inner], weight and gate [outer, inner], bias and gate_bias [outer],
  * residual [rows, outer] are bf16, out [rows, outer] bf16 or fp32.  Row strides
  * are in elements; columns are adjacent.  x, weight and gate must be 16-byte
- * aligned, inner and their row strides multiples of 8; residual and out may be
- * anywhere, and out may be the residual itself (bf16, same address and stride), but
+ * aligned, inner and their row strides multiples of 8, and no stride below
+ * inner (rows that overlap are refused); residual and out may be anywhere.
+ * out may be the residual itself (bf16, same address and stride), but
  * must not overlap another input, nor its rows one another (refused; columns of a
  * tensor that holds an input in others of its columns do not overlap it).  Sums are in fp32,
  * in an order that depends on sizes, types and the device only: the same call
@@ -635,7 +638,7 @@ typedef struct dt_qk_norm_rope_args {
   const void* k; /* or NULL */
   int64_t q_row_stride, q_head_stride;
   int64_t k_row_stride, k_head_stride;
-  const void* q_weight; /* [head_dim] bf16 or NULL: no norm */
+  const void* q_weight; /* [head_dim] bf16, 16-byte aligned, or NULL: no norm */
   const void* k_weight;
   const uint64_t* turns;    /* [rot / 2] device, or NULL: no rotation */
   const int32_t* positions; /* [n_req * slots] or NULL */

@@ -568,10 +568,11 @@ void plan_many(LinearParams& p, int sides) {
       p.n_tiles = (p.outer + outs - 1) / outs;
     }
   }
-  // A CTA's part of a step: 128 tokens and half of the columns.  Two blocks of 64 channels a step while four such stages fit: copies of
-  // 32 KB come in faster than of 16 (512 tokens, 4096 to 2560, 96 columns 16.9 us, by one block 18.2; 2080 tokens, 160 columns 33.7 and 35.4).
+  // A CTA's part of a step: 128 tokens and half of the columns.  Two blocks of 64 channels a step while four such stages fit (up to 160
+  // columns, for outputs in 32 bits 128): copies of 32 KB come in faster than of 16 (512 tokens, 4096 to 2560, 96 columns 17.1 us, by one block
+  // 18.3; in 32 bits 19.6 and 21.8; 2080 tokens, 160 columns 32.4 and 33.1), three stages are too few (in 32 bits 43.8 us, by one block 41.3).
   const uint32_t block = 16384 + p.bn * 64;
-  p.per = p.inner % 128 == 0 && p.bn <= 160 ? 2 : 1;
+  p.per = p.inner % 128 == 0 && wide_ring(p.out_fp32) / (2 * block) >= 4 ? 2 : 1;
   p.k_steps = (p.k_blocks + p.per - 1) / p.per;
   p.stage_bytes = p.per * block;
   p.stages = static_cast<int>(wide_ring(p.out_fp32) / p.stage_bytes);

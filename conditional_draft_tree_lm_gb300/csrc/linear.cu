@@ -630,6 +630,10 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (p.rows <= kTokensMost) return kv_launched(who, launch_linear_token(a, p, st));
   const int sides = a.gate ? 2 : 1;
+  // From here on pairs of CTAs, which split nothing.  us by clusters or persistent CTAs and by pairs: 4096 to 2560 13.8 and 14.4 at 224 tokens,
+  // 15.3 and 14.5 at 256, 14.1 and 16.6 at 272, 18.0 and 16.9 at 512; 2560 to 6144 15.0 and 13.6, 16.3 and 13.8, 16.1 and 15.8, 22.8 and 16.4; to
+  // 10240 20.0 and 17.2, 21.0 and 17.4, 26.5 and 23.8, 33.5 and 25.0; but 10240 to 2560 19.7 and 28.6, 21.9 and 28.7, 22.8 and 33.9, 30.0 and 34.4:
+  // the sides meet between 160 and 600 tokens, earlier where rows of weight are many and later where channels are.
   const bool many = p.rows > 256;
   const uintptr_t res = reinterpret_cast<uintptr_t>(a.residual);
   const int64_t at_once = many ? 16 / static_cast<int64_t>(bytes) : 4;  // outputs written together

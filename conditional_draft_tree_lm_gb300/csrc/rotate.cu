@@ -10,9 +10,12 @@
 // Angles: a position times turns[i], in 64-bit integers, wraps by whole turns; the upper 32 bits are what is left of a
 // turn, and exact for any position (fp32 has lost a radian at position 2^24).
 //
-// Bound by instructions and memory alike where there are many rows: 32k rows of 32 + 8 heads of 128 124 us, 5.4 TB/s (one row a
-// CTA 159 us, with 326 instructions a warp in 67 % of the issue slots; four rows 127 us; persistent CTAs with the next row ahead
-// 149 us; without norms 116 us), by the latency of one pass where there are few: 32 rows 2.1 us.
+// Squares are summed in fp32; a head for which they leave it (channels of 2^63 and more, or of 2^-45 and less where eps is as small)
+// is taken once more by a power of two, so that any finite head has its norm.  The check costs 3 % (32k rows 124.3 us without).
+//
+// Bound by instructions and memory alike where there are many rows: 32k rows of 32 + 8 heads of 128 127 us, 5.3 TB/s (before that check one
+// row a CTA 159 us, with 326 instructions a warp in 67 % of the issue slots; four rows 127 us; persistent CTAs with the next row ahead
+// 149 us); without norms 116 us; by the latency of one pass where there are few: 32 rows 2.3 us.
 #include "kv_flash.cuh"
 
 namespace dt {
@@ -46,6 +49,21 @@ DT_DEVINL uint4 pack8(const uint64_t* v) {
     w[i] = pack_p(lo, hi);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Of a head's channels, in all of its lanes.
+template <int G>
+DT_DEVINL float sum_squares(const uint64_t (&v)[8], int tid) {
+  uint64_t sum2 = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum2 = fma2(v[i], v[i], sum2);
+  float sum, other;
+  f32x2_parts(sum2, sum, other);
+  sum += other;
+  const uint32_t lanes = ((1u << G) - 1u) << (tid & 31 & ~(G - 1));
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(lanes, sum, o);
+  return sum;
 }
 
 template <int G, bool INTERLEAVED, int ROWS>
@@ -107,16 +125,17 @@ __global__ void __launch_bounds__(kRotateThreads, ROWS == 1 ? 3 : 2) k_rotate(co
     unpack8(x[r][0], v);
     unpack8(x[r][1], v + 4);
     if (weight) {  // (the same for all lanes of a head)
-      uint64_t sum2 = 0;
+      float mean = fmaf(sum_squares<G>(v, tid), p.one_over, a.eps);
+      // Squares that leave fp32 (a mean below 2^-90, infinite or NaN): the head by a power of two larger or smaller.
+      constexpr uint32_t kLeast = (127 - 90) << 23, kInfinite = 255u << 23;
+      if (__float_as_uint(mean) - kLeast >= kInfinite - kLeast) {
+        const float unit = mean > 1.0f ? 0x1p-70f : 0x1p75f;
+        const uint64_t unit2 = f32x2(unit, unit);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum2 = fma2(v[i], v[i], sum2);
-      float sum, other;
-      f32x2_parts(sum2, sum, other);
-      sum += other;
-      const uint32_t lanes = ((1u << G) - 1u) << (tid & 31 & ~(G - 1));
-#pragma unroll
-      for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(lanes, sum, o);
-      const float scale = rsqrtf(fmaf(sum, p.one_over, a.eps));
+        for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], unit2);
+        mean = fmaf(sum_squares<G>(v, tid), p.one_over, a.eps * unit * unit);
+      }
+      const float scale = rsqrtf(mean);
       const uint64_t scale2 = f32x2(scale, scale);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = mul2(mul2(v[i], scale2), w[i]);

@@ -1,8 +1,8 @@
 """One attention layer of a target model served with drafted trees.
 
-Prompts are read (``kv_plan``, ``prompt_attention``, ``kv_append``), then every round drafts a tree
+Prompts are read (``kv_plan``, ``linear``, ``qk_norm_rope``, ``prompt_attention``, ``kv_append``), then every round drafts a tree
 (``DraftTreeBuilder``), scores all its slots in one pass over the 8-bit cache under the ancestor-only mask
-(``cache_attention``), walks the tree against the target's logits, and appends the keys and values of the accepted
+(the same projections, with a slot's position its request's length and its depth, and ``cache_attention``), walks the tree against the target's logits, and appends the keys and values of the accepted
 path only (``kv_plan`` with the walk's path, ``kv_append`` with its source rows).  No length leaves the GPU: the plan,
 the append and the attention read what the walk has written.
 
@@ -21,10 +21,11 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 
 class TargetLayer:
-    """Embedding, one layer of grouped-head attention, output head: bf16, random."""
+    """Embedding, one layer of grouped-head attention with norms and rotation of its heads, output head: bf16, random."""
 
     def __init__(self, vocab, width, heads, kv_heads, head_dim, gen):
         import torch
+        from conditional_draft_tree_lm_gb300 import Rotary
 
         def normal(*shape, scale):
             return (torch.randn(*shape, generator=gen, device="cuda") * scale).to(torch.bfloat16)
@@ -32,15 +33,23 @@ class TargetLayer:
         self.emb = normal(vocab, width, scale=1.0)
         self.qkv = normal((heads + 2 * kv_heads) * head_dim, width, scale=width ** -0.5)
         self.out = normal(vocab, heads * head_dim, scale=(heads * head_dim) ** -0.5)
+        self.q_norm, self.k_norm = 1 + normal(head_dim, scale=0.1), 1 + normal(head_dim, scale=0.1)
+        self.rotary = Rotary(head_dim, theta=1e6)
 
-    def project(self, tokens):
-        """q, k, v of tokens: slices of one product, used strided as they are."""
-        x = self.emb[tokens.long()] @ self.qkv.T
+    def project(self, tokens, positions=None, base=None, status=None):
+        """q, k, v of tokens: slices of one product, q and k normed and turned in place.  A token stands at its place among
+        the tokens, or at positions, which are counted from base."""
+        from conditional_draft_tree_lm_gb300 import linear, qk_norm_rope
+        x = linear(self.emb[tokens.long()], self.qkv, status=status)
         x = x.view(*tokens.shape, self.heads + 2 * self.kv_heads, self.head_dim)
-        return x[..., :self.heads, :], x[..., self.heads:-self.kv_heads, :], x[..., -self.kv_heads:, :]
+        q, k, v = x[..., :self.heads, :], x[..., self.heads:-self.kv_heads, :], x[..., -self.kv_heads:, :]
+        qk_norm_rope(q, k, positions=positions, base=base, rotary=self.rotary, q_weight=self.q_norm, k_weight=self.k_norm, q_out=q, k_out=k)
+        return q, k, v
 
-    def logits(self, attended):
-        return (attended.flatten(-2) @ self.out.T).float()
+    def logits(self, attended, status=None):
+        import torch
+        from conditional_draft_tree_lm_gb300 import linear
+        return linear(attended.flatten(-2), self.out, out_dtype=torch.float32, status=status)
 
 
 class Server:
@@ -82,19 +91,20 @@ class Server:
         import torch
         from conditional_draft_tree_lm_gb300 import kv_append, prompt_attention
         tokens = torch.cat(prompts)
-        q, k, v = self.target.project(tokens)
-        slots, _ = self.plan(tokens.numel(), delta=torch.tensor([p.numel() for p in prompts], dtype=torch.int32, device="cuda"))
+        positions = torch.empty(tokens.numel(), dtype=torch.int32, device="cuda")
+        slots, _ = self.plan(tokens.numel(), delta=torch.tensor([p.numel() for p in prompts], dtype=torch.int32, device="cuda"), positions=positions)
+        q, k, v = self.target.project(tokens, positions, status=self.status)
         attended = prompt_attention(q, k, v, self.row_start, status=self.status)
         kv_append(self.cache, k, v, slots, status=self.status)
-        return self.target.logits(attended[(self.row_start[1:] - 1).long()])
+        return self.target.logits(attended[(self.row_start[1:] - 1).long()], self.status)
 
     def score_tree(self, tree):
         """Target logits [n_req, slots, V] of every tree slot, and the slots' keys and values."""
         from conditional_draft_tree_lm_gb300 import cache_attention
-        q, k, v = self.target.project(tree["tok"])
+        q, k, v = self.target.project(tree["tok"], tree["depth"], self.length[0], self.status)
         attended = cache_attention(self.cache, q, self.table, self.length[0], k_new=k, v_new=v, mask=tree["mask"],
                                    workspace=self.work, status=self.status)
-        return self.target.logits(attended), k, v
+        return self.target.logits(attended, self.status), k, v
 
     def commit(self, walk, k, v):
         """Root and accepted slots into the cache."""

@@ -2,15 +2,17 @@
 
 Binding of ``dt_linear``, ``dt_qk_norm_rope`` and ``dt_token_logprobs`` of
 ``include/dtree.h``, which states formulas, layouts and errors.  A layer, between
-whose calls those of ``kvcache`` stand::
+whose calls those of ``kvcache`` stand, and with norm() for the norms of the hidden states, which
+are the caller's (torch's ``rms_norm``, say)::
 
-    qkv = linear(x, w_qkv)                                # [rows, heads + 2 kv heads, head_dim], sliced
+    qkv = linear(norm(x), w_qkv)                          # [rows, heads + 2 kv heads, head_dim], sliced
     q, k = qk_norm_rope(q, k, positions=..., rotary=...)  # norms and rotation
     ...                                                   # prompt_attention, kv_append, cache_attention
     x = linear(attended, w_out, residual=x)
-    h = linear(x, w_up, gate=w_gate, activation="silu")
+    y = norm(x)
+    h = linear(y, w_up, gate=w_gate, activation="silu")
     x = linear(h, w_down, residual=x)
-    logits = linear(x, head, out_dtype=torch.float32)     # accept_walk's input
+    logits = linear(norm(x), head, out_dtype=torch.float32)  # accept_walk's input
     found = token_logprobs(logits, tokens, top=5)
 
 As for the cache's calls, nothing here computes: tensors become pointers, a refused

@@ -556,6 +556,8 @@ dt_status dt_prompt_attention(const dt_prompt_attention_args* args, void* stream
  *   (attention, append: above)
  *   dt_linear          back to the residual stream, which is added
  *   dt_linear          the gated feed-forward width; then back, added again
+ * (the norms of the hidden states before the projections, the feed-forward width
+ * and the head are the caller's)
  * and behind the last layer
  *   dt_linear          the output head, logits in fp32 (dt_accept_walk's input)
  *   dt_token_logprobs  log probabilities of given tokens

@@ -19,10 +19,10 @@
 // beside each other by k_few.  Outputs in bf16 (half a step is 4e-3) have one accumulator over all channels.
 //
 // Bound by streaming the weights where they are many: 65 tokens' logits (2560 to 151936, fp32) 129 us, 6.2 TB/s; gated 32 tokens
-// (2560 to 2 x 10240) 21 us, 5.0 TB/s, a quarter of it before the first products and behind the last.  By that latency where
-// they are few: 65 tokens, 4096 to 2560 10.1 us, of which the copies take 2.  Tokens by the hundred: by the operands that every SM
+// (2560 to 2 x 10240) 21 us, 5.1 TB/s, a quarter of it before the first products and behind the last.  By that latency where
+// they are few: 65 tokens, 4096 to 2560 9.8 us, of which the copies take 2.  Tokens by the hundred: by the operands that every SM
 // brings and by the sums of a split, which come over distributed shared memory at 18 bytes a clock (bulk copies are no faster): 200
-// tokens, 2560 to 6144 14.3 us, 256, 4096 to 4096 16.5.
+// tokens, 2560 to 6144 14.6 us, 256, 4096 to 4096 16.3.
 #include "linear.cuh"
 #include "cluster.cuh"
 #include "kv_flash.cuh"
@@ -538,7 +538,7 @@ int clusters_beside(int size) {
 
 // Clusters of as many CTAs as leave all of them beside each other, with four blocks of 64 or more each.  A CTA has an SM with all its
 // shared memory: two an SM, in clusters twice as large, were ahead up to 4 tokens only (2560 to 6144 9.2 us, one 9.5; 16 tokens the same;
-// 65 tokens, 4096 to 2560 13.0, one 10.1).
+// 65 tokens, 4096 to 2560 13.0, one 9.8).
 // False where there are too few accumulators for outputs in 32 bits.
 bool plan_few(LinearParams& p, int sides, int64_t tiles) {
   p.tile_outs = 128;
@@ -633,7 +633,7 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
   // From here on pairs of CTAs, which split nothing.  us by clusters or persistent CTAs and by pairs: 4096 to 2560 13.8 and 14.4 at 224 tokens,
   // 15.3 and 14.5 at 256, 14.1 and 16.6 at 272, 18.0 and 16.9 at 512; 2560 to 6144 15.0 and 13.6, 16.3 and 13.8, 16.1 and 15.8, 22.8 and 16.4; to
   // 10240 20.0 and 17.2, 21.0 and 17.4, 26.5 and 23.8, 33.5 and 25.0; but 10240 to 2560 19.7 and 28.6, 21.9 and 28.7, 22.8 and 33.9, 30.0 and 34.4:
-  // the sides meet between 160 and 600 tokens, earlier where rows of weight are many and later where channels are.
+  // the sides meet below 160 tokens where rows of weight are many (160 gated to 2 x 10240 34.8 and 31.9) and above 512 where channels are.
   const bool many = p.rows > 256;
   const uintptr_t res = reinterpret_cast<uintptr_t>(a.residual);
   const int64_t at_once = many ? 16 / static_cast<int64_t>(bytes) : 4;  // outputs written together
@@ -647,8 +647,8 @@ extern "C" dt_status dt_linear(const dt_linear_args* args, void* stream) {
     plan_tokens(p, sides);
     const int64_t tiles = static_cast<int64_t>((a.outer + 127) / 128) * p.m_tiles;
     if (tiles > (1 << 29)) return kv_fail(DT_ERR_SHAPE, "%s: more than 2^29 tiles", who);
-    // Clusters where tiles leave half of the SMs without one.  us by clusters and by persistent CTAs: 65 tokens, 2560 to 6144 10.7 and 12.1,
-    // to 8192 12.1 and 12.6, to 9728 13.4 and 13.4; 200 tokens 14.4 and 17.7, 15.7 and 18.3, 18.0 and 18.9.
+    // Clusters where tiles leave half of the SMs without one.  us by clusters and by persistent CTAs: 65 tokens, 2560 to 6144 10.8 and 12.1,
+    // to 8192 12.1 and 12.6, to 9728 13.4 and 13.4; 200 tokens 14.6 and 17.7, 15.7 and 18.3, 18.0 and 18.9.
     stream_tiles = tiles >= kSms / 2 || !plan_few(p, sides, tiles);
     if (stream_tiles) plan_stream(p, sides, tiles);
   }

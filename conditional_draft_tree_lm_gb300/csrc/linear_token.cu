@@ -8,7 +8,9 @@
 // tensor-core kernels for few tokens, one token: 2560 to 6144 7.2, 8.0, 9.6; 4096 to 2560 7.9, 5.6, 8.1; 10240 to 2560 16.7, 10.6, 12.9;
 // 2560 to 2 x 10240 18.6, 19.2, 20.7; two tokens: 8.0, 9.5, 9.5; 8.5, 5.9, 8.1; 17.6, 10.8, 13.0; 20.7, 22.5, 21.0; with three, products and
 // the tokens' reads take over: 2560 to 6144 11.4, 10.4, 9.2.
-// Bound by streaming the weights once; no tensor memory, barrier or cluster stands before the first byte.
+// Bound by the latency of that stream: a warp asks for its next pieces when it has used the ones before, three times one after the other
+// for 2560 channels, so that one token streams 4.3 TB/s to 6144 outputs and 5.6 to 2 x 10240; no tensor memory, barrier or cluster stands
+// before the first byte.
 #include "linear.cuh"
 #include "kv_flash.cuh"
 

@@ -10,11 +10,12 @@
 // group of 32 columns each.
 // Outputs in 32 bits: an accumulator takes 512 channels (linear.cu says why), and the epilogue's warps hold a tile's sums, 128 a
 // thread, in registers that the other warps give up.  Every change of accumulator costs about 500 clocks: 4096 tokens, 2560 to
-// 10240 149 us, in bf16 117 us (by single CTAs, which stage twice as much, 220 us).
-// Bound by the tensor cores where tiles are whole: 8192 tokens gated, 2560 to 2 x 10240 443 us, 1.94 PFLOP/s; 4096 to 4096 145 us.  Else by
-// operands, of which a narrower tile brings as many for fewer products, and by rounds of tiles that do not come out even: 2080
-// tokens, 4096 to 2560 34 us, 1.3 PFLOP/s, two rounds of 144 tiles of 256 x 160 over 76 pairs, 113 GB/s into an SM (copies alone reach
-// 137; tokens and weights by a warp each the same times).
+// 10240 152 us, in bf16 119 us (by single CTAs, which stage twice as much, 220 us).
+// Bound by the tensor cores where tiles are whole: 8192 tokens gated, 2560 to 2 x 10240 432 us in a burst at the full clock (2070 MHz; 1.99
+// PFLOP/s, a library's product of the same operands 2.10), 507 us call after call, where the power limit lowers the clock; 4096 to 4096 141 us.
+// Else by operands, of which a narrower tile brings as many for fewer products, and by whole tiles: 2080 tokens, 4096 to 2560 34 us, 1.3
+// PFLOP/s, 144 tiles of 256 x 160 over 76 pairs, two a pair but for eight, so that an SM takes 113 GB/s (copies alone reach
+// 137; tokens and weights by a warp each the same times), and the last 32 tokens cost as much as 256.
 // Both CTAs hold all of their SM's tensor memory while they wait for one another: with 220 KB of shared memory no CTA
 // that holds any can stand beside them, so that nobody waits in a circle.
 #include "cluster.cuh"
